@@ -15,6 +15,8 @@ sections "Guarantees", "Ascend NPU backend", "Dtypes"):
   det_gemm_da(dC[M,N], B[K,N])                 -> dA[M,K] = dC B^T
   det_gemm_db(A[M,K], dC[M,N])                 -> dB[K,N] = A^T dC
   det_gemm_db_transposed(A[M,K], dC[M,N])      -> dB^T[N,K]
+The operators around them (routing, dispatch and combine, 8-bit products,
+embedding) are in _ops.py and exported here as well.
 Matrices are row-major with a leading dimension (``t.stride(0)``) and unit
 column stride; row-slices of bigger tensors are accepted as they are.
 """
@@ -128,7 +130,7 @@ def _stream_handle(stream) -> int:
     return int(torch.cuda.current_stream().cuda_stream)
 
 
-_ELEM_SIZE = {torch.bfloat16: 2, torch.float32: 4}
+_ELEM_SIZE = {torch.bfloat16: 2, torch.float32: 4, torch.float8_e4m3fn: 1}
 
 
 def _name(name: str, index: int) -> str:
@@ -417,8 +419,11 @@ def det_rmsnorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, out=None, s
 
 
 def det_gemm_check(stream=None) -> int:
-    """Synchronise the stream and return (and clear) the device status code."""
-    return int(lib().det_gemm_check(_stream_handle(stream)))
+    """Synchronise the stream and return (and clear) the device status code,
+    of det_gemm's launches and of the operators' (det_ops_check)."""
+    status = int(lib().det_gemm_check(_stream_handle(stream)))
+    ops = det_ops_check(stream)
+    return status if status != OK else ops
 
 
 def det_gemm_tree_schedule(num_leaves: int) -> list[int]:
@@ -470,3 +475,10 @@ __all__ = [
     "det_rmsnorm",
     "det_gemm_fwd_grouped",
 ]
+
+# The mixture-of-experts operators (include/det_ops.h) share this module's
+# library, checks and errors.
+from ._ops import *                                   # noqa: E402,F401,F403
+from ._ops import __all__ as _ops_all                 # noqa: E402
+
+__all__ += _ops_all

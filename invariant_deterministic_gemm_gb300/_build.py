@@ -1,7 +1,7 @@
 """Builds libdet_gemm.so in-tree with nvcc for sm_103a (no GPU needed).
 
-Each .cu file under csrc/ is compiled in parallel to an object under
-``_build/`` and the objects are linked into ``libdet_gemm.so`` next to this
+Each .cu file under csrc/ (det_gemm) and csrc_ops/ (the mixture-of-experts
+operators) is compiled in parallel to an object under ``_build/`` and the objects are linked into ``libdet_gemm.so`` next to this
 file. The CUDA runtime is linked statically, so the library has no load-time
 dependency on libcuda (the driver is reached at run time).
 """
@@ -16,6 +16,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_OPS = os.path.join(PKG, "csrc_ops")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdet_gemm.so")
@@ -31,12 +32,12 @@ def nvcc() -> str:
 
 
 def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+    return sorted(os.path.join(d, f) for d in (CSRC, CSRC_OPS) for f in os.listdir(d) if f.endswith(".cu"))
 
 
 def headers() -> list[str]:
-    hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    return hs + [os.path.join(INCLUDE, "det_gemm.h")]
+    hs = [os.path.join(d, f) for d in (CSRC, CSRC_OPS) for f in os.listdir(d) if f.endswith((".h", ".cuh"))]
+    return hs + [os.path.join(INCLUDE, f) for f in ("det_gemm.h", "det_ops.h")]
 
 
 def _stale(target: str, deps: list[str]) -> bool:
@@ -48,7 +49,7 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 def _compile(src: str, verbose: bool, ptxas_info: bool) -> tuple[str, str]:
     obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
+    cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-I", CSRC_OPS, "-c", src, "-o", obj]
     if ptxas_info:
         cmd[1:1] = ["-Xptxas", "-v"]
     if verbose:
