@@ -10,28 +10,35 @@
 // enter: an element's bits depend on its row of A and its row of B only.
 //
 // The tensor core cannot apply FP32 scales, so every block's accumulator
-// leaves TMEM and is added in registers. For a 128 x 256 tile the four MMAs
-// take 512 cycles at the dense e4m3 rate, the TMEM reads 256 and the
-// multiply-adds 256 on other pipes, so the tensor core stays the bound as
-// long as the reads overlap the next block's MMAs: two accumulators of 256
-// columns fill TMEM and alternate.
+// leaves TMEM and is added in registers. For a 128 x 192 tile the four MMAs
+// take about 390 cycles (98 each); what has to fit beside them is the TMEM
+// read, whose latency (about 200 cycles) is the long part, and 192
+// multiply-adds a row, done two at a time (fma.f32x2).
 //
-// Plain tile (384 threads, one CTA per SM, persistent over tiles):
-//   warps 0-7  epilogue: TMEM lane quadrant w % 4 (32 rows), column half w / 4;
-//              a thread keeps BN / 2 sums of one row in registers
-//   warp 8     copies A and B blocks in with TMA (ring of 4 stages)
-//   warp 9     issues the MMAs
-//   warp 10    allocates and frees TMEM
-// A block of a stage is 128 bytes of contraction for 128 rows of A and BN of
-// B, in 128-byte swizzle. Why 256 columns: a 128 x 128 tile reads 32 KB from
-// L2 for 256 MMA cycles, 128 B a cycle and SM; 128 x 256 reads 96.
+// Plain tile (BN / 64 epilogue warps per quadrant and four service warps,
+// one CTA per SM, persistent over tiles):
+//   epilogue   warp w: TMEM lane quadrant w % 4 (32 rows), columns
+//              64 (w / 4).. of the tile; a thread keeps 64 sums of one row
+//   service 0  copies A and B blocks in with TMA
+//   service 1, 2  issue the MMAs of alternate blocks, each from one thread:
+//              a block's waits, four MMAs and two commits take one thread
+//              about 700 cycles, the MMAs themselves 390
+//   service 3  allocates and frees TMEM
+// Both accumulators of 192 columns alternate. 64 columns a thread let one
+// wait cover a whole block's TMEM read; with eight warps of 128 columns (a
+// 128 x 256 tile) a thread's four waits for TMEM were the bound, 1190 cycles
+// a block where the MMAs take 520.
 //
 // Transposed tile (few rows: decode): the weight is the MMA's row side, its
 // 32, 64 or 128 rows are TMEM lanes, and the tokens its 16 to 64 columns.
-// The launch is bound by reading the weight once; a CTA keeps up to 96 KB of
-// copies in flight and two CTAs share an SM. A tile of 32 or 64 weight rows
-// still issues 128-row MMAs: the other lanes multiply whatever the following
-// shared memory holds and are never read.
+// The launch is bound by reading the weight once, and a tile walks its
+// blocks one after the other, so what a block costs each role counts: a
+// stage holds two blocks (one wait, one release), two threads issue the MMAs
+// of alternate stages, a warp of its own brings the scales' products, and the epilogue
+// takes two blocks a turn where its registers allow. Up to 96 KB of copies
+// are in flight a CTA and two CTAs share an SM (192 KB and one for 64 tokens). A tile of 32 or 64 weight
+// rows still issues 128-row MMAs: the other lanes multiply whatever the
+// following shared memory holds and are never read.
 //
 // Weight gradient: both operands are scaled per row of theirs, so the
 // columns' scales go through shared memory and each element takes one more
@@ -51,6 +58,7 @@ namespace deto {
 
 using detg::elect_one;
 using detg::mbar_arrive_expect_tx;
+using detg::mbar_arrive;
 using detg::mbar_arrive_if;
 using detg::mbar_init;
 using detg::mma_commit;
@@ -65,7 +73,7 @@ using detg::tmem_ld16;
 using detg::tmem_ld32;
 using detg::tmem_wait_ld;
 using detg::wait_bounded;
-using detg::warp_wait;
+using detg::mbar_wait_inline;
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
@@ -102,9 +110,88 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint32_t a_smem, uint32_t 
     for (int k = 0; k < 4; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, idesc, k != 0);
 }
 
+// Two FP32 operations at once, each rounded to nearest like the scalar one.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// sum += v * scale for four columns, the scales read from shared memory. One volatile block: apart, the compiler loads a
+// whole block's scales ahead of their use and spills.
+__device__ __forceinline__ void add4(uint64_t &sum0, uint64_t &sum1, uint64_t v0, uint64_t v1, uint32_t at)
+{
+    asm volatile(
+        "{\n\t.reg .b64 s0, s1;\n\t"
+        "ld.shared.v2.b64 {s0, s1}, [%4];\n\t"
+        "fma.rn.f32x2 %0, %2, s0, %0;\n\t"
+        "fma.rn.f32x2 %1, %3, s1, %1;\n\t}"
+        : "+l"(sum0), "+l"(sum1)
+        : "l"(v0), "l"(v1), "r"(at)
+        : "memory");
+}
+// 16 TMEM lanes x 64 columns: r[4 j + 2 h + e] is lane (thread / 4 + 8 h),
+// column 8 j + 2 (thread % 4) + e. A thread then has few distinct columns
+// (16 of 64) and a few rows, so few distinct scales.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float lds1(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t lds2(uint32_t at)
+{
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// One float into shared memory behind the thread's back; zero when !in.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A CTA's shared state besides the operand ring.
 struct Fp8Shared {
-    uint64_t full[16], empty[16], accf[4], acce[4], drain, never;
+    uint64_t full[16], empty[16], accf[8], acce[8], drain[2], never;
     uint32_t tmem;
     int abort_flag;
     int first[kMaxExperts + 1];      // first work unit of each group
@@ -212,6 +299,22 @@ __device__ __forceinline__ void store_cols8(const Fp8Params &p, long long at, in
     else store8(static_cast<uint16_t *>(p.out) + at, c, p.cols, pack8(f));
 }
 
+// Two neighbouring columns, c even.
+template <bool F32>
+__device__ __forceinline__ void store_cols2(const Fp8Params &p, long long at, int c, float lo, float hi)
+{
+    if constexpr (F32) {
+        float *o = static_cast<float *>(p.out) + at + c;
+        if (c + 1 < p.cols) *reinterpret_cast<float2 *>(o) = make_float2(lo, hi);
+        else if (c < p.cols) *o = lo;
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(p.out) + at + c;
+        const uint32_t v = pack_bf16(lo, hi);
+        if (c + 1 < p.cols) *reinterpret_cast<uint32_t *>(o) = v;
+        else if (c < p.cols) *o = static_cast<uint16_t>(v);
+    }
+}
+
 // Rows of the output that no group owns become zero (grouped launches).
 template <bool F32>
 __device__ __forceinline__ void zero_unowned(const Fp8Params &p, int thread, int threads)
@@ -230,21 +333,28 @@ __device__ __forceinline__ void zero_unowned(const Fp8Params &p, int thread, int
 template <int BN>
 struct PlainCfg {
     static constexpr int BM = 128;
-    static constexpr int EPI_WARPS = 8;
-    static constexpr int THREADS = 384;
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int COLS = 64;                  // columns of a thread
+    static constexpr int EPI_WARPS = BN / COLS * 4;
+    static constexpr int THREADS = 32 * (EPI_WARPS + 4);
+    static constexpr int STAGES = BN == 192 ? 5 : 6;
     static constexpr int A_STAGE = BM * kBlock, B_STAGE = BN * kBlock;
-    static constexpr int NACC = BN == 256 ? 2 : 4;
-    static constexpr int COLS = BN / 2;              // columns of a thread
+    static constexpr int NACC = BN == 192 ? 2 : 4;
     static constexpr int OFF_B = STAGES * A_STAGE;
-    static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;       // [EPI_WARPS][2][COLS] floats
-    static constexpr int OFF_SHARED = OFF_SCALE + EPI_WARPS * 2 * COLS * 4;
+    // Scales are copied kAhead blocks before they are used (an L2 read takes
+    // about as long as two blocks): for each epilogue warp, its rows' and
+    // columns' scales of kAhead blocks.
+    static constexpr int kAhead = 4, SLOT = 32 + COLS;
+    static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;       // [EPI_WARPS][kAhead][SLOT] floats
+    static constexpr int OFF_SHARED = OFF_SCALE + EPI_WARPS * kAhead * SLOT * 4;
     static constexpr int BYTES = OFF_SHARED + static_cast<int>(sizeof(Fp8Shared));
     static constexpr int SMEM = BYTES + 1024;
-    // 65536 registers: 168 a thread at launch; the four service warps keep 40, the epilogue warps take 232.
-    static constexpr int LAUNCH_REGS = 168;
-    static constexpr int SERVICE_REGS = 40, EPI_REGS = 232;
-    static_assert(SERVICE_REGS * 128 + EPI_REGS * 256 <= LAUNCH_REGS * THREADS, "register split");
+    // Registers: a thread's sums, its TMEM words and addresses take about
+    // 160. 384 threads have that (168); 512 are launched with 128 and the
+    // service warps hand theirs over.
+    static constexpr bool SPLIT = THREADS > 384;
+    static constexpr int LAUNCH_REGS = (65536 / THREADS) & ~7;
+    static constexpr int SERVICE_REGS = 24, EPI_REGS = 160;
+    static_assert(!SPLIT || SERVICE_REGS * 128 + EPI_REGS * 32 * EPI_WARPS <= LAUNCH_REGS * THREADS, "register split");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(NACC * BN <= 512, "TMEM");
 };
@@ -253,84 +363,104 @@ template <int KIND, bool F32, int BN>
 __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S, float *scale_smem, int warp, int lane)
 {
     using C = PlainCfg<BN>;
-    const int q = warp & 3, half = warp >> 2;
-    const uint32_t t0 = S.tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::COLS;
-    float *sc = scale_smem + warp * 2 * C::COLS;
+    const int q = warp & 3, part = warp >> 2;
+    const uint32_t t0 = S.tmem + (static_cast<uint32_t>(q * 32) << 16) + part * C::COLS;
+    const uint32_t ring = smem_u32(scale_smem + warp * C::kAhead * C::SLOT);
     const int units = S.first[p.groups];
+    const uint32_t abort_s = smem_u32(&S.abort_flag);
     int acc = 0;
     uint32_t phase = 0;
-    int flip = 0;
-    volatile int *abort_flag = &S.abort_flag;
+    bool ok = true;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const Unit w = unit_of<KIND>(p, S, u, C::BM, BN);
         const int row = w.row0 + q * 32 + lane;
-        const int col = w.col0 + half * C::COLS;
+        const int col = w.col0 + part * C::COLS;
         const bool live = row < w.rows_end;
-        const float *sa = p.sa + row * p.sa_row + w.kblk0 * p.sa_blk;
-        // The thread's column scales: one for all its columns (a weight's
-        // tile), or its lane's share of the warp's columns.
+        // Scales: the row's own; and one for all the columns (a weight's
+        // tile; a lane holds the next 32 blocks') or one for each column.
+        const float *sa = live ? p.sa + row * p.sa_row + w.kblk0 * p.sa_blk : p.sa;
         const float *sb;
-        constexpr int SB = KIND == kFp8Rows ? 1 : C::COLS / 32;
-        float sbv[SB], sav = 0.0f;
-        bool cl[SB];
+        bool in0, in1 = false;
+        float tile_scale = 0.0f;
         if constexpr (KIND == kFp8Rows) {
-            sb = p.sb + w.group * p.sb_grp + static_cast<long long>(col / kBlock) * p.sb_row;
-            cl[0] = col < p.cols;
+            in0 = col < p.cols;
+            sb = in0 ? p.sb + w.group * p.sb_grp + static_cast<long long>(col / kBlock) * p.sb_row : p.sb;
+            tile_scale = in0 && lane < w.nblk ? __ldg(sb + lane * p.sb_blk) : 0.0f;
         } else {
-            sb = p.sb + w.kblk0 * p.sb_blk + static_cast<long long>(col + lane) * p.sb_row;
-#pragma unroll
-            for (int i = 0; i < SB; ++i) cl[i] = col + lane + 32 * i < p.cols;
+            in0 = col + lane < p.cols;
+            in1 = col + lane + 32 < p.cols;
+            sb = p.sb + (in0 ? w.kblk0 * p.sb_blk + static_cast<long long>(col + lane) * p.sb_row : 0);
         }
-        auto load_scales = [&](int b) {
-            sav = live ? __ldg(sa + b * p.sa_blk) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < SB; ++i) sbv[i] = cl[i] ? __ldg(sb + b * p.sb_blk + 32 * i * p.sb_row) : 0.0f;
-        };
-        float sum[C::COLS];
-#pragma unroll
-        for (int i = 0; i < C::COLS; ++i) sum[i] = 0.0f;
-        if (w.nblk > 0) load_scales(0);
-        for (int b = 0; b < w.nblk; ++b) {
-            float rs = sav;
-            const float4 *cs = reinterpret_cast<const float4 *>(sc + flip * C::COLS);
-            if constexpr (KIND == kFp8Rows) {
-                rs = sav * sbv[0];
-            } else {
-#pragma unroll
-                for (int i = 0; i < SB; ++i) sc[flip * C::COLS + lane + 32 * i] = sbv[i];
-                __syncwarp();
-                flip ^= 1;
-            }
-            if (b + 1 < w.nblk) load_scales(b + 1);
-            if (!warp_wait(smem_u32(&S.accf[acc]), phase, abort_flag, p.status, p.timeout_ns)) return;
-            tc_fence_after();
-            const uint32_t t = t0 + acc * BN;
-            uint32_t v[2][32];
-            tmem_ld32(t, v[0]);
-#pragma unroll
-            for (int h = 0; h < C::COLS / 32; ++h) {
-                tmem_wait_ld();
-                reg_fence(v[h & 1]);
-                if (h + 1 < C::COLS / 32) {
-                    tmem_ld32(t + 32 * (h + 1), v[(h + 1) & 1]);
-                } else {
-                    tc_fence_before();
-                    __syncwarp();
-                    mbar_arrive_if(smem_u32(&S.acce[acc]), lane == 0);
+        auto fetch = [&](int b) {
+            if (b < w.nblk) {
+                const uint32_t slot = ring + (b % C::kAhead) * (C::SLOT * 4) + lane * 4;
+                copy_async4(slot, sa + (live ? b * p.sa_blk : 0), live);
+                if constexpr (KIND == kFp8Wgrad) {
+                    copy_async4(slot + 128, sb + (in0 ? b * p.sb_blk : 0), in0);
+                    copy_async4(slot + 256, sb + (in1 ? b * p.sb_blk + 32 * p.sb_row : 0), in1);
                 }
+            }
+            copy_commit();
+        };
+        uint64_t sum[C::COLS / 2];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    float s[4] = {rs, rs, rs, rs};
-                    if constexpr (KIND == kFp8Wgrad) {
-                        const float4 c4 = cs[(32 * h + i) / 4];
-                        s[0] = rs * c4.x;
-                        s[1] = rs * c4.y;
-                        s[2] = rs * c4.z;
-                        s[3] = rs * c4.w;
-                    }
+        for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0;
+        __syncwarp();                // the last tile's scales have been read
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sum[32 * h + i + e] = fmaf(__uint_as_float(v[h & 1][i + e]), s[e], sum[32 * h + i + e]);
+        for (int b = 0; b < C::kAhead - 1; ++b) fetch(b);
+        for (int b = 0; b < w.nblk; ++b) {
+            copy_wait<C::kAhead - 2>();
+            __syncwarp();            // every lane's copies; and slot b - 1 is free
+            fetch(b + C::kAhead - 1);
+            const uint32_t slot = ring + (b % C::kAhead) * (C::SLOT * 4);
+            const uint32_t t = t0 + acc * BN;
+            auto arrived = [&]() {
+                ok &= mbar_wait_inline(smem_u32(&S.accf[acc]), phase, abort_s, p.status, p.timeout_ns) != 0;
+                tc_fence_after();
+            };
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_if(smem_u32(&S.acce[acc]), lane == 0);
+            };
+            if constexpr (KIND == kFp8Rows) {
+                float rs = lds1(slot + lane * 4);
+                if (b > 0 && (b & 31) == 0) tile_scale = in0 && b + lane < w.nblk ? __ldg(sb + (b + lane) * p.sb_blk) : 0.0f;
+                rs *= __shfl_sync(kFull, tile_scale, b & 31);
+                const uint64_t r2 = pair(rs, rs);
+                arrived();
+                uint32_t v0[32], v1[32];
+                tmem_ld32(t, v0);
+                tmem_ld32(t + 32, v1);
+                tmem_wait_ld();
+                reg_fence(v0);
+                reg_fence(v1);
+                release();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[i] = fma2(pair(v0[2 * i], v0[2 * i + 1]), r2, sum[i]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[16 + i] = fma2(pair(v1[2 * i], v1[2 * i + 1]), r2, sum[16 + i]);
+            } else {
+                // sum[16 g + 2 j + h]: row lane / 4 + 16 g + 8 h, columns 8 j + 2 (lane % 4) + {0, 1}
+                uint64_t cs[8], rs[4];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cs[j] = lds2(slot + 128 + (8 * j + 2 * (lane & 3)) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float r = lds1(slot + (8 * i + (lane >> 2)) * 4);
+                    rs[i] = pair(r, r);
+                }
+                arrived();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t v[32];
+                    tmem_ld_16x64(t + (static_cast<uint32_t>(16 * g) << 16), v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+                    if (g == 1) release();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[16 * g + i] = fma2(pair(v[2 * i], v[2 * i + 1]), mul2(rs[2 * g + (i & 1)], cs[i / 2]), sum[16 * g + i]);
                 }
             }
             if (++acc == C::NACC) {
@@ -338,48 +468,54 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
                 phase ^= 1u;
             }
         }
-        if (live) {
-            const long long at = row * p.ldo + (KIND == kFp8Wgrad ? w.group * p.og : 0);
+        if (!ok) return;             // a wait of this tile failed: the launch is aborting
+        if constexpr (KIND == kFp8Rows) {
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < C::COLS; i += 8) {
-                float f[8];
+                for (int i = 0; i < C::COLS; i += 8) {
+                    float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = sum[i + e];
-                if (col + i < p.cols) store_cols8<F32>(p, at, col + i, f);
+                    for (int e = 0; e < 8; e += 2) unpair(sum[(i + e) / 2], f[e], f[e + 1]);
+                    if (col + i < p.cols) store_cols8<F32>(p, row * p.ldo, col + i, f);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int r = w.row0 + q * 32 + (lane >> 2) + 16 * (i >> 4) + 8 * (i & 1);
+                const int c = col + 8 * ((i >> 1) & 7) + 2 * (lane & 3);
+                float lo, hi;
+                unpair(sum[i], lo, hi);
+                if (r < w.rows_end) store_cols2<F32>(p, r * p.ldo + w.group * p.og, c, lo, hi);
             }
         }
     }
     if constexpr (KIND == kFp8Rows) zero_unowned<F32>(p, warp * 32 + lane, C::EPI_WARPS * 32);
 }
 
+// One thread: the whole loop of TMA copies.
 template <int KIND, int BN>
 __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uint32_t base)
 {
     using C = PlainCfg<BN>;
-    const bool leader = elect_one();
     const int units = S.first[p.groups];
     volatile int *abort_flag = &S.abort_flag;
     const uint32_t tx = static_cast<uint32_t>(p.a_box + p.b_box) * kBlock;
     int s = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
-    bool ok = true;
-    if (p.force_timeout)
-        ok = __all_sync(kFull, wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true));
+    bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit w = unit_of<KIND>(p, S, u, C::BM, BN);
         for (int b = 0; b < w.nblk; ++b) {
-            if (!warp_wait(smem_u32(&S.empty[s]), round ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+            if (!wait_bounded(smem_u32(&S.empty[s]), round ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
                 ok = false;
                 break;
             }
-            if (leader) {
-                const uint32_t full = smem_u32(&S.full[s]);
-                mbar_arrive_expect_tx(full, tx);
-                const int k = (w.kblk0 + b) * kBlock;
-                tma_load_2d(base + s * C::A_STAGE, &p.tmap_a, full, k, w.row0);
-                tma_load_3d(base + C::OFF_B + s * C::B_STAGE, &p.tmap_b, full, k, w.col0, KIND == kFp8Rows ? w.group : 0);
-            }
-            __syncwarp();
+            const uint32_t full = smem_u32(&S.full[s]);
+            mbar_arrive_expect_tx(full, tx);
+            const int k = (w.kblk0 + b) * kBlock;
+            tma_load_2d(base + s * C::A_STAGE, &p.tmap_a, full, k, w.row0);
+            tma_load_3d(base + C::OFF_B + s * C::B_STAGE, &p.tmap_b, full, k, w.col0, KIND == kFp8Rows ? w.group : 0);
             loaded |= 1u << s;
             parity = (parity & ~(1u << s)) | (round << s);
             if (++s == C::STAGES) {
@@ -395,52 +531,54 @@ __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uin
     }
 }
 
+// One thread of each of the two issuing warps: issuer i takes the blocks g
+// of the CTA's sequence with g % 2 == i.
 template <int KIND, int BN>
-__device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, uint32_t base)
+__device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, uint32_t base, int issuer)
 {
     using C = PlainCfg<BN>;
     constexpr uint32_t IDESC = idesc_e4m3(C::BM, BN);
-    const bool leader = elect_one();
     const int units = S.first[p.groups];
     volatile int *abort_flag = &S.abort_flag;
-    int s = 0, acc = 0;
+    const uint32_t tmem = S.tmem;
+    int s = issuer, acc = issuer;        // of this issuer's next block
     uint32_t round = 0, phase = 0;
+    int b = issuer;                      // its position in the current tile
     bool ok = true, issued = false;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int nblk = unit_of<KIND>(p, S, u, C::BM, BN).nblk;
-        for (int b = 0; b < nblk; ++b) {
-            if (!warp_wait(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns) ||
-                !warp_wait(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns)) {
+        for (; b < nblk; b += 2) {
+            if (!wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true) ||
+                !wait_bounded(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            if (leader) {
-                mma_block(S.tmem + acc * BN, base + s * C::A_STAGE, base + C::OFF_B + s * C::B_STAGE, IDESC);
-                mma_commit(smem_u32(&S.empty[s]));
-                mma_commit(smem_u32(&S.accf[acc]));
-            }
-            __syncwarp();
+            mma_block(tmem + acc * BN, base + s * C::A_STAGE, base + C::OFF_B + s * C::B_STAGE, IDESC);
+            mma_commit(smem_u32(&S.accf[acc]));
+            mma_commit(smem_u32(&S.empty[s]));
             issued = true;
-            if (++s == C::STAGES) {
-                s = 0;
+            s += 2;
+            if (s >= C::STAGES) {
+                s -= C::STAGES;
                 round ^= 1u;
             }
-            if (++acc == C::NACC) {
-                acc = 0;
+            acc += 2;
+            if (acc >= C::NACC) {
+                acc -= C::NACC;
                 phase ^= 1u;
             }
         }
+        b -= nblk;
     }
     if (!ok && issued) {
-        if (leader) mma_commit(smem_u32(&S.drain));
-        __syncwarp();
-        wait_bounded(smem_u32(&S.drain), 0, abort_flag, p.status, p.timeout_ns, false);
+        mma_commit(smem_u32(&S.drain[issuer]));
+        wait_bounded(smem_u32(&S.drain[issuer]), 0, abort_flag, p.status, p.timeout_ns, false);
     }
 }
 
 template <int KIND, bool F32, int BN>
-__global__ void __launch_bounds__(384, 1) fp8_plain_kernel(const __grid_constant__ Fp8Params p)
+__global__ void __launch_bounds__(PlainCfg<BN>::THREADS, 1) fp8_plain_kernel(const __grid_constant__ Fp8Params p)
 {
     using C = PlainCfg<BN>;
     extern __shared__ uint8_t fp8_smem[];
@@ -460,16 +598,17 @@ __global__ void __launch_bounds__(384, 1) fp8_plain_kernel(const __grid_constant
             mbar_init(smem_u32(&S.accf[a]), 1);
             mbar_init(smem_u32(&S.acce[a]), C::EPI_WARPS);
         }
-        mbar_init(smem_u32(&S.drain), 1);
+        mbar_init(smem_u32(&S.drain[0]), 1);
+        mbar_init(smem_u32(&S.drain[1]), 1);
         mbar_init(smem_u32(&S.never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) setup_groups<KIND>(p, S, C::BM, lane);
-    if (warp == 8 && lane == 0) {
+    if (warp == C::EPI_WARPS && lane == 0) {
         tmap_prefetch(&p.tmap_a);
         tmap_prefetch(&p.tmap_b);
     }
-    if (warp == 10) {
+    if (warp == C::EPI_WARPS + 3) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -478,18 +617,19 @@ __global__ void __launch_bounds__(384, 1) fp8_plain_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (warp < C::EPI_WARPS) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
+        if constexpr (C::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
         plain_epilogue<KIND, F32, BN>(p, S, scale_smem, warp, lane);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::SERVICE_REGS));
-        if (warp == 8) plain_copy<KIND, BN>(p, S, base);
-        else if (warp == 9) plain_issue<KIND, BN>(p, S, base);
+        if constexpr (C::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::SERVICE_REGS));
+        if (warp == C::EPI_WARPS && elect_one()) plain_copy<KIND, BN>(p, S, base);
+        else if ((warp == C::EPI_WARPS + 1 || warp == C::EPI_WARPS + 2) && elect_one())
+            plain_issue<KIND, BN>(p, S, base, warp - C::EPI_WARPS - 1);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 10)
+    if (warp == C::EPI_WARPS + 3)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
 }
 
@@ -498,105 +638,122 @@ __global__ void __launch_bounds__(384, 1) fp8_plain_kernel(const __grid_constant
 template <int NT>
 struct SwapCfg {
     static constexpr int THREADS = 256;
-    static constexpr int NACC = 4;
-    static constexpr int TMEM_COLS = NACC * NT < 32 ? 32 : NACC * NT;
-    static constexpr int B_STAGE = NT * kBlock;
+    static constexpr int NACC = NT == 64 ? 4 : 8;    // accumulators, and slots of scales
+    static constexpr int TMEM_COLS = NACC * NT;
+    static constexpr int PER_STAGE = 2;              // blocks of a stage
+    static constexpr int PER_TURN = NT == 64 ? 1 : 2;    // blocks the epilogue takes at once
     static constexpr int MAX_STAGES = 16;
-    static constexpr int RING = 96 * 1024;           // bytes of the operand ring
-    static constexpr int OFF_SCALE = RING;           // [4 warps][2][NT] floats
-    static constexpr int OFF_SHARED = OFF_SCALE + 4 * 2 * NT * 4;
+    // 64 columns of sums leave registers for one CTA an SM only.
+    static constexpr int CTAS = NT == 64 ? 1 : 2;
+    static constexpr int RING = (CTAS == 1 ? 192 : 96) * 1024;       // bytes of the operand ring
+    static constexpr int OFF_SCALE = RING;           // [NACC][NT] floats
+    static constexpr int OFF_SHARED = OFF_SCALE + NACC * NT * 4;
     static constexpr int BYTES = OFF_SHARED + static_cast<int>(sizeof(Fp8Shared));
     static constexpr int SMEM = BYTES + 1024;
-    static_assert(2 * SMEM <= 232448, "two CTAs share an SM");
-    static_assert(TMEM_COLS * 2 <= 512, "two CTAs share an SM's TMEM");
+    static_assert(CTAS * SMEM <= 232448, "the CTAs of an SM share its memory");
+    static_assert(TMEM_COLS * CTAS <= 512, "the CTAs of an SM share its TMEM");
     __host__ __device__ static int stages(int tile_rows)
     {
-        // The ring's weight part comes first and a 128-row MMA reads up to
-        // 16 KB from its slot's start: that stays inside the allocation.
-        const int n = (RING - (128 - tile_rows) * kBlock) / (tile_rows * kBlock + B_STAGE);
+        // The ring's weight part comes first and a 128-row MMA reads 16 KB
+        // from its block's start: that stays inside the ring.
+        const int n = (RING - (128 - tile_rows) * kBlock) / (PER_STAGE * (tile_rows + NT) * kBlock);
         return n < MAX_STAGES ? n : MAX_STAGES;
     }
 };
 
 template <bool F32, int NT>
-__device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, float *scale_smem, int tile_rows, int warp,
-                                              int lane)
+__device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, const float *scale_smem, int tile_rows,
+                                              int warp, int lane)
 {
     using C = SwapCfg<NT>;
-    constexpr int SL = NT < 32 ? 1 : NT / 32;        // token scales of a lane
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    float *sc = scale_smem + warp * 2 * NT;
     const int units = S.first[p.groups];
-    volatile int *abort_flag = &S.abort_flag;
+    const uint32_t abort_s = smem_u32(&S.abort_flag);
     int acc = 0;
     uint32_t phase = 0;
-    int flip = 0;
+    bool ok = true;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
-        const int n = w.col0 + warp * 32 + lane;     // this lane's output column (a weight row)
-        const float *sw = p.sb + w.group * p.sb_grp + static_cast<long long>(w.col0 / kBlock) * p.sb_row;
-        float tv[SL], wv = 0.0f;
-        auto load_scales = [&](int b) {
-            wv = __ldg(sw + b * p.sb_blk);
+        uint64_t sum[NT / 2];
 #pragma unroll
-            for (int i = 0; i < SL; ++i) {
-                const int r = w.row0 + 32 * i + lane;
-                tv[i] = (32 * i + lane < NT && r < w.rows_end) ? __ldg(p.sa + r * p.sa_row + b * p.sa_blk) : 0.0f;
+        for (int i = 0; i < NT / 2; ++i) sum[i] = 0;
+        auto arrived = [&](int a, uint32_t ph) {
+            ok &= mbar_wait_inline(smem_u32(&S.accf[a]), ph, abort_s, p.status, p.timeout_ns) != 0;
+        };
+        // Adds N columns of a block (words v, scales c) to sum[at..].
+        auto add = [&](const uint32_t *v, uint32_t c, int at, int n) {
+#pragma unroll
+            for (int i = 0; i < n; i += 4) {
+                add4(sum[(at + i) / 2], sum[(at + i) / 2 + 1], pair(v[i], v[i + 1]), pair(v[i + 2], v[i + 3]), c + 4 * i);
             }
         };
-        float sum[NT];
+        auto scales = [&](int a) { return smem_u32(scale_smem + a * NT); };
+        auto release = [&](int a) { mbar_arrive_if(smem_u32(&S.acce[a]), lane == 0); };
+        auto next = [&](int &a, uint32_t &ph) {
+            if (++a == C::NACC) {
+                a = 0;
+                ph ^= 1u;
+            }
+        };
+        for (int b = 0; b < w.nblk; b += C::PER_TURN) {
+            const int a0 = acc;
+            arrived(a0, phase);
+            next(acc, phase);
+            if constexpr (NT == 64) {
+                tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < NT; ++i) sum[i] = 0.0f;
-        if (w.nblk > 0) load_scales(0);
-        for (int b = 0; b < w.nblk; ++b) {
-            float *cs = sc + flip * NT;
-#pragma unroll
-            for (int i = 0; i < SL; ++i)
-                if (32 * i + lane < NT) cs[32 * i + lane] = tv[i] * wv;
-            __syncwarp();
-            flip ^= 1;
-            if (b + 1 < w.nblk) load_scales(b + 1);
-            if (!warp_wait(smem_u32(&S.accf[acc]), phase, abort_flag, p.status, p.timeout_ns)) return;
-            tc_fence_after();
-            const uint32_t t = t0 + acc * NT;
-            if constexpr (NT == 16) {
-                uint32_t v[16];
-                tmem_ld16(t, v);
-                tmem_wait_ld();
-                reg_fence16(v);
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_if(smem_u32(&S.acce[acc]), lane == 0);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sum[i] = fmaf(__uint_as_float(v[i]), cs[i], sum[i]);
-            } else {
-#pragma unroll
-                for (int h = 0; h < NT / 32; ++h) {
+                for (int h = 0; h < 2; ++h) {
                     uint32_t v[32];
-                    tmem_ld32(t + 32 * h, v);
+                    tmem_ld32(t0 + a0 * NT + 32 * h, v);
                     tmem_wait_ld();
                     reg_fence(v);
-                    if (h + 1 == NT / 32) {
-                        tc_fence_before();
-                        __syncwarp();
-                        mbar_arrive_if(smem_u32(&S.acce[acc]), lane == 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[32 * h + i] = fmaf(__uint_as_float(v[i]), cs[32 * h + i], sum[32 * h + i]);
+                    add(v, scales(a0) + 128 * h, 32 * h, 32);
                 }
-            }
-            if (++acc == C::NACC) {
-                acc = 0;
-                phase ^= 1u;
+                tc_fence_before();
+                __syncwarp();
+                release(a0);
+            } else {
+                const bool two = b + 1 < w.nblk;
+                const int a1 = acc;
+                if (two) {
+                    arrived(a1, phase);
+                    next(acc, phase);
+                }
+                tc_fence_after();
+                uint32_t v0[NT], v1[NT];
+                if constexpr (NT == 16) {
+                    tmem_ld16(t0 + a0 * NT, v0);
+                    if (two) tmem_ld16(t0 + a1 * NT, v1);
+                    tmem_wait_ld();
+                    reg_fence16(v0);
+                    reg_fence16(v1);
+                } else {
+                    tmem_ld32(t0 + a0 * NT, v0);
+                    if (two) tmem_ld32(t0 + a1 * NT, v1);
+                    tmem_wait_ld();
+                    reg_fence(v0);
+                    reg_fence(v1);
+                }
+                add(v0, scales(a0), 0, NT);
+                if (two) add(v1, scales(a1), 0, NT);
+                tc_fence_before();
+                __syncwarp();
+                release(a0);
+                if (two) release(a1);
             }
         }
+        if (!ok) return;             // a wait of this tile failed: the launch is aborting
+        const int n = w.col0 + warp * 32 + lane;     // this lane's output column (a weight row)
         if (n < p.cols && warp * 32 < tile_rows) {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const long long r = w.row0 + i;
+                float lo, hi;
+                unpair(sum[i / 2], lo, hi);
+                const float v = (i & 1) ? hi : lo;
                 if (r < w.rows_end) {
-                    if constexpr (F32) static_cast<float *>(p.out)[r * p.ldo + n] = sum[i];
-                    else static_cast<__nv_bfloat16 *>(p.out)[r * p.ldo + n] = __float2bfloat16_rn(sum[i]);
+                    if constexpr (F32) static_cast<float *>(p.out)[r * p.ldo + n] = v;
+                    else static_cast<__nv_bfloat16 *>(p.out)[r * p.ldo + n] = __float2bfloat16_rn(v);
                 }
             }
         }
@@ -604,8 +761,165 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
     zero_unowned<F32>(p, warp * 32 + lane, 128);
 }
 
+// One warp: the products of a block's scales, token by token, into the slot
+// of the block's accumulator. The loads of the next kAhead blocks are under
+// way while the last ones are handed out.
+template <int NT>
+__device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, float *scale_smem, int tile_rows, int lane)
+{
+    using C = SwapCfg<NT>;
+    constexpr int SL = NT < 32 ? 1 : NT / 32;        // tokens of a lane
+    constexpr int kAhead = 8;
+    const int units = S.first[p.groups];
+    const uint32_t abort_s = smem_u32(&S.abort_flag);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
+        const float *sw = p.sb + w.group * p.sb_grp + static_cast<long long>(w.col0 / kBlock) * p.sb_row;
+        float t[kAhead][SL], wv[kAhead];
+        auto load = [&](int b0) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const bool in = b0 + j < w.nblk;
+                wv[j] = in ? __ldg(sw + (b0 + j) * p.sb_blk) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < SL; ++i) {
+                    const int r = w.row0 + 32 * i + lane;
+                    t[j][i] = (in && 32 * i + lane < NT && r < w.rows_end) ? __ldg(p.sa + r * p.sa_row + (b0 + j) * p.sa_blk) : 0.0f;
+                }
+            }
+        };
+        load(0);
+        for (int b0 = 0; b0 < w.nblk; b0 += kAhead) {
+            float c[kAhead][SL];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int i = 0; i < SL; ++i) c[j][i] = t[j][i] * wv[j];
+            load(b0 + kAhead);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (b0 + j >= w.nblk) break;
+                if (!__all_sync(kFull, mbar_wait_inline(smem_u32(&S.acce[slot]), phase ^ 1u, abort_s, p.status, p.timeout_ns) != 0))
+                    return;
+#pragma unroll
+                for (int i = 0; i < SL; ++i)
+                    if (32 * i + lane < NT) scale_smem[slot * NT + 32 * i + lane] = c[j][i];
+                __syncwarp();
+                mbar_arrive_if(smem_u32(&S.accf[slot]), lane == 0);
+                if (++slot == C::NACC) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    }
+}
+
+// One thread: the copies. tmap_b is the weight (b_box rows), tmap_a the
+// tokens (a_box rows).
+template <int NT>
+__device__ __forceinline__ void swap_copy(const Fp8Params &p, Fp8Shared &S, uint32_t base, int tile_rows)
+{
+    using C = SwapCfg<NT>;
+    const int stages = C::stages(tile_rows);
+    const uint32_t w_blk = static_cast<uint32_t>(tile_rows) * kBlock;
+    const uint32_t base_t = base + stages * C::PER_STAGE * w_blk;
+    const uint32_t tx = static_cast<uint32_t>(p.a_box + p.b_box) * kBlock;
+    const int units = S.first[p.groups];
+    volatile int *abort_flag = &S.abort_flag;
+    int s = 0;
+    uint32_t round = 0, loaded = 0, parity = 0;
+    bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
+        for (int b = 0; b < w.nblk; b += C::PER_STAGE) {
+            if (!wait_bounded(smem_u32(&S.empty[s]), round ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
+                ok = false;
+                break;
+            }
+            const uint32_t full = smem_u32(&S.full[s]);
+            const int n = min(C::PER_STAGE, w.nblk - b);
+            mbar_arrive_expect_tx(full, tx * n);
+            for (int j = 0; j < n; ++j) {
+                const int at = s * C::PER_STAGE + j;
+                tma_load_3d(base + at * w_blk, &p.tmap_b, full, (b + j) * kBlock, w.col0, w.group);
+                tma_load_2d(base_t + at * NT * kBlock, &p.tmap_a, full, (b + j) * kBlock, w.row0);
+            }
+            loaded |= 1u << s;
+            parity = (parity & ~(1u << s)) | (round << s);
+            if (++s == stages) {
+                s = 0;
+                round ^= 1u;
+            }
+        }
+    }
+    if (!ok) {
+        for (int i = 0; i < stages; ++i)
+            if (loaded & (1u << i))
+                wait_bounded(smem_u32(&S.full[i]), (parity >> i) & 1u, abort_flag, p.status, p.timeout_ns, false);
+    }
+}
+
+// One thread of each of the two issuing warps: issuer i takes the stages g
+// of the CTA's sequence with g % 2 == i.
+template <int NT>
+__device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uint32_t base, int tile_rows, int issuer)
+{
+    using C = SwapCfg<NT>;
+    constexpr uint32_t IDESC = idesc_e4m3(128, NT);
+    const int stages = C::stages(tile_rows);
+    const uint32_t w_blk = static_cast<uint32_t>(tile_rows) * kBlock;
+    const uint32_t base_t = base + stages * C::PER_STAGE * w_blk;
+    const int units = S.first[p.groups];
+    volatile int *abort_flag = &S.abort_flag;
+    const uint32_t tmem = S.tmem;
+    int s = 0, acc = 0, turn = 0;        // every stage is counted, its own are issued
+    uint32_t round = 0, phase = 0;
+    bool ok = true, issued = false;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const int nblk = unit_of<kFp8Rows>(p, S, u, NT, tile_rows).nblk;
+        for (int b = 0; ok && b < nblk; b += C::PER_STAGE) {
+            const int n = min(C::PER_STAGE, nblk - b);
+            const bool mine = turn == issuer;
+            if (mine && !wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true)) {
+                ok = false;
+                break;
+            }
+            for (int j = 0; j < n; ++j) {
+                if (mine) {
+                    if (!wait_bounded(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int at = s * C::PER_STAGE + j;
+                    mma_block(tmem + acc * NT, base + at * w_blk, base_t + at * NT * kBlock, IDESC);
+                    mma_commit(smem_u32(&S.accf[acc]));
+                    issued = true;
+                }
+                if (++acc == C::NACC) {
+                    acc = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (mine && ok) mma_commit(smem_u32(&S.empty[s]));
+            turn ^= 1;
+            if (++s == stages) {
+                s = 0;
+                round ^= 1u;
+            }
+        }
+    }
+    if (!ok && issued) {
+        mma_commit(smem_u32(&S.drain[issuer]));
+        wait_bounded(smem_u32(&S.drain[issuer]), 0, abort_flag, p.status, p.timeout_ns, false);
+    }
+}
+
 template <bool F32, int NT>
-__global__ void __launch_bounds__(256, 2) fp8_swap_kernel(const __grid_constant__ Fp8Params p, const int tile_rows)
+__global__ void __launch_bounds__(256, SwapCfg<NT>::CTAS) fp8_swap_kernel(const __grid_constant__ Fp8Params p, const int tile_rows)
 {
     using C = SwapCfg<NT>;
     extern __shared__ uint8_t fp8_smem[];
@@ -615,20 +929,18 @@ __global__ void __launch_bounds__(256, 2) fp8_swap_kernel(const __grid_constant_
     Fp8Shared &S = *reinterpret_cast<Fp8Shared *>(smem + C::OFF_SHARED);
     float *scale_smem = reinterpret_cast<float *>(smem + C::OFF_SCALE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int stages = C::stages(tile_rows);
-    const uint32_t w_stage = static_cast<uint32_t>(tile_rows) * kBlock;
-    const uint32_t base_t = base + stages * w_stage;         // token slots
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        for (int s = 0; s < stages; ++s) {
+        for (int s = 0; s < C::MAX_STAGES; ++s) {
             mbar_init(smem_u32(&S.full[s]), 1);
             mbar_init(smem_u32(&S.empty[s]), 1);
         }
         for (int a = 0; a < C::NACC; ++a) {
-            mbar_init(smem_u32(&S.accf[a]), 1);
+            mbar_init(smem_u32(&S.accf[a]), 2);      // the MMAs' commit and the scales
             mbar_init(smem_u32(&S.acce[a]), 4);
         }
-        mbar_init(smem_u32(&S.drain), 1);
+        mbar_init(smem_u32(&S.drain[0]), 1);
+        mbar_init(smem_u32(&S.drain[1]), 1);
         mbar_init(smem_u32(&S.never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -637,7 +949,7 @@ __global__ void __launch_bounds__(256, 2) fp8_swap_kernel(const __grid_constant_
         tmap_prefetch(&p.tmap_a);
         tmap_prefetch(&p.tmap_b);
     }
-    if (warp == 6) {
+    if (warp == 7) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)),
                      "r"(C::TMEM_COLS)
                      : "memory");
@@ -646,89 +958,15 @@ __global__ void __launch_bounds__(256, 2) fp8_swap_kernel(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int units = S.first[p.groups];
-    volatile int *abort_flag = &S.abort_flag;
-    if (warp < 4) {
-        swap_epilogue<F32, NT>(p, S, scale_smem, tile_rows, warp, lane);
-    } else if (warp == 4) {
-        const bool leader = elect_one();
-        // tmap_b is the weight (b_box rows of it), tmap_a the tokens (a_box)
-        const uint32_t tx = static_cast<uint32_t>(p.a_box + p.b_box) * kBlock;
-        int s = 0;
-        uint32_t round = 0, loaded = 0, parity = 0;
-        bool ok = true;
-        if (p.force_timeout)
-            ok = __all_sync(kFull, wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true));
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
-            for (int b = 0; b < w.nblk; ++b) {
-                if (!warp_wait(smem_u32(&S.empty[s]), round ^ 1u, abort_flag, p.status, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                if (leader) {
-                    const uint32_t full = smem_u32(&S.full[s]);
-                    mbar_arrive_expect_tx(full, tx);
-                    tma_load_3d(base + s * w_stage, &p.tmap_b, full, b * kBlock, w.col0, w.group);
-                    tma_load_2d(base_t + s * C::B_STAGE, &p.tmap_a, full, b * kBlock, w.row0);
-                }
-                __syncwarp();
-                loaded |= 1u << s;
-                parity = (parity & ~(1u << s)) | (round << s);
-                if (++s == stages) {
-                    s = 0;
-                    round ^= 1u;
-                }
-            }
-        }
-        if (!ok) {
-            for (int i = 0; i < stages; ++i)
-                if (loaded & (1u << i))
-                    wait_bounded(smem_u32(&S.full[i]), (parity >> i) & 1u, abort_flag, p.status, p.timeout_ns, false);
-        }
-    } else if (warp == 5) {
-        const bool leader = elect_one();
-        constexpr uint32_t IDESC = idesc_e4m3(128, NT);
-        int s = 0, acc = 0;
-        uint32_t round = 0, phase = 0;
-        bool ok = true, issued = false;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const int nblk = unit_of<kFp8Rows>(p, S, u, NT, tile_rows).nblk;
-            for (int b = 0; b < nblk; ++b) {
-                if (!warp_wait(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns) ||
-                    !warp_wait(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (leader) {
-                    mma_block(S.tmem + acc * NT, base + s * w_stage, base_t + s * C::B_STAGE, IDESC);
-                    mma_commit(smem_u32(&S.empty[s]));
-                    mma_commit(smem_u32(&S.accf[acc]));
-                }
-                __syncwarp();
-                issued = true;
-                if (++s == stages) {
-                    s = 0;
-                    round ^= 1u;
-                }
-                if (++acc == C::NACC) {
-                    acc = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (!ok && issued) {
-            if (leader) mma_commit(smem_u32(&S.drain));
-            __syncwarp();
-            wait_bounded(smem_u32(&S.drain), 0, abort_flag, p.status, p.timeout_ns, false);
-        }
-    }
+    if (warp < 4) swap_epilogue<F32, NT>(p, S, scale_smem, tile_rows, warp, lane);
+    else if (warp == 4 && elect_one()) swap_copy<NT>(p, S, base, tile_rows);
+    else if ((warp == 5 || warp == 6) && elect_one()) swap_issue<NT>(p, S, base, tile_rows, warp - 5);
+    else if (warp == 7) swap_scales<NT>(p, S, scale_smem, tile_rows, lane);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 6)
+    if (warp == 7)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(C::TMEM_COLS) : "memory");
 }
 
@@ -757,7 +995,7 @@ cudaError_t run_plain(const Fp8Params &p, int sms, cudaStream_t s)
         cudaError_t x = cudaFuncGetAttributes(&at, fn);
         if (x != cudaSuccess) return x;
         // setmaxnreg shares out exactly the registers of the launch.
-        if (at.numRegs != C::LAUNCH_REGS) return cudaErrorInvalidDeviceFunction;
+        if (C::SPLIT && at.numRegs != C::LAUNCH_REGS) return cudaErrorInvalidDeviceFunction;
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
@@ -774,7 +1012,7 @@ cudaError_t run_swap(const Fp8Params &p, int tile_rows, int sms, cudaStream_t s)
     const cudaError_t e = once_per_device(
         done, [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
     if (e != cudaSuccess) return e;
-    fn<<<2 * sms, C::THREADS, C::SMEM, s>>>(p, tile_rows);
+    fn<<<C::CTAS * sms, C::THREADS, C::SMEM, s>>>(p, tile_rows);
     return cudaGetLastError();
 }
 

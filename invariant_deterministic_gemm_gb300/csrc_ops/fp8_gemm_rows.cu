@@ -16,7 +16,7 @@ cudaError_t launch_fp8(const Fp8Params &p, const Fp8Plan &plan, int sms, cudaStr
         return f ? run_swap<true, 64>(p, plan.tile_n, sms, s) : run_swap<false, 64>(p, plan.tile_n, sms, s);
     }
     if (plan.tile_n == 128) return f ? run_plain<kFp8Rows, true, 128>(p, sms, s) : run_plain<kFp8Rows, false, 128>(p, sms, s);
-    return f ? run_plain<kFp8Rows, true, 256>(p, sms, s) : run_plain<kFp8Rows, false, 256>(p, sms, s);
+    return f ? run_plain<kFp8Rows, true, 192>(p, sms, s) : run_plain<kFp8Rows, false, 192>(p, sms, s);
 }
 
 }  // namespace deto
