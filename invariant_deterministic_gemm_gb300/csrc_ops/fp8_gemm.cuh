@@ -299,19 +299,89 @@ __device__ __forceinline__ void store_cols8(const Fp8Params &p, long long at, in
     else store8(static_cast<uint16_t *>(p.out) + at, c, p.cols, pack8(f));
 }
 
-// Two neighbouring columns, c even.
+// Sixteen bytes of the output at element `at`, column c, clipped to the columns.
 template <bool F32>
-__device__ __forceinline__ void store_cols2(const Fp8Params &p, long long at, int c, float lo, float hi)
+__device__ __forceinline__ void store_chunk(const Fp8Params &p, long long at, int c, const uint32_t (&v)[4])
 {
-    if constexpr (F32) {
-        float *o = static_cast<float *>(p.out) + at + c;
-        if (c + 1 < p.cols) *reinterpret_cast<float2 *>(o) = make_float2(lo, hi);
-        else if (c < p.cols) *o = lo;
-    } else {
-        uint16_t *o = static_cast<uint16_t *>(p.out) + at + c;
-        const uint32_t v = pack_bf16(lo, hi);
-        if (c + 1 < p.cols) *reinterpret_cast<uint32_t *>(o) = v;
-        else if (c < p.cols) *o = static_cast<uint16_t>(v);
+    constexpr int N = F32 ? 4 : 8;
+    if (c + N <= p.cols) {
+        if constexpr (F32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (c + e >= p.cols) break;
+        if constexpr (F32) static_cast<uint32_t *>(p.out)[at + e] = v[e];
+        else static_cast<uint16_t *>(p.out)[at + e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+    }
+}
+
+// 32 rows x 64 bytes of the output from one warp: lane l's row as 16 words.
+// Through `buf` (2 KB of shared memory, 16-byte chunks swizzled by row), so
+// that a store instruction writes 64 contiguous bytes of eight rows.
+template <bool F32>
+__device__ __forceinline__ void store_rows64(const Fp8Params &p, uint32_t buf, const uint32_t (&w)[16], int row0, int rows_end,
+                                             long long base, int col, int lane)
+{
+    constexpr int EPW = F32 ? 1 : 2;                 // elements a word
+    __syncwarp();                                    // the last use of buf is over
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16),
+                     "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), k = lane & 3;
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(buf + r * 64 + ((k ^ (r >> 1)) & 3) * 16)
+                     : "memory");
+        const int c = col + k * 4 * EPW;
+        if (row0 + r < rows_end) store_chunk<F32>(p, base + (row0 + r) * p.ldo + c, c, v);
+    }
+}
+
+// The same for sums in the fragment layout (sum[16 g + 2 j + h]: row lane / 4
+// + 16 g + 8 h, columns 8 j + 2 (lane % 4) + {0, 1}), 64 bytes of columns at a
+// time: words are put where store_rows64 would have put them.
+template <bool F32>
+__device__ __forceinline__ void store_fragment(const Fp8Params &p, uint32_t buf, const uint64_t (&sum)[32], int row0, int rows_end,
+                                               long long base, int col, int lane)
+{
+    constexpr int J = F32 ? 2 : 4;                   // groups of 8 columns in 64 bytes
+    constexpr int EPW = F32 ? 1 : 2;
+#pragma unroll
+    for (int j0 = 0; j0 < 8; j0 += J) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {            // row lane / 4 + 8 i
+                const int r = (lane >> 2) + 8 * i;
+                const uint64_t v = sum[16 * (i >> 1) + 2 * (j0 + j) + (i & 1)];
+                float lo, hi;
+                unpair(v, lo, hi);
+                const int word = F32 ? 8 * j + 2 * (lane & 3) : 4 * j + (lane & 3);
+                const uint32_t at = buf + r * 64 + (((word >> 2) ^ (r >> 1)) & 3) * 16 + (word & 3) * 4;
+                if constexpr (F32) asm volatile("st.shared.b64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+                else asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16(lo, hi)) : "memory");
+            }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), k = lane & 3;
+            const int c = col + 8 * j0 + k * 4 * EPW;
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(buf + r * 64 + ((k ^ (r >> 1)) & 3) * 16)
+                         : "memory");
+            if (row0 + r < rows_end) store_chunk<F32>(p, base + (row0 + r) * p.ldo + c, c, v);
+        }
     }
 }
 
@@ -336,7 +406,7 @@ struct PlainCfg {
     static constexpr int COLS = 64;                  // columns of a thread
     static constexpr int EPI_WARPS = BN / COLS * 4;
     static constexpr int THREADS = 32 * (EPI_WARPS + 4);
-    static constexpr int STAGES = BN == 192 ? 5 : 6;
+    static constexpr int STAGES = BN == 192 ? 4 : 6;
     static constexpr int A_STAGE = BM * kBlock, B_STAGE = BN * kBlock;
     static constexpr int NACC = BN == 192 ? 2 : 4;
     static constexpr int OFF_B = STAGES * A_STAGE;
@@ -345,7 +415,12 @@ struct PlainCfg {
     // columns' scales of kAhead blocks.
     static constexpr int kAhead = 4, SLOT = 32 + COLS;
     static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;       // [EPI_WARPS][kAhead][SLOT] floats
-    static constexpr int OFF_SHARED = OFF_SCALE + EPI_WARPS * kAhead * SLOT * 4;
+    // A finished tile goes out through shared memory, 64 bytes of 32 rows a
+    // time and warp: written straight from the registers, every store
+    // touches 32 lines and a 192-wide tile takes 3000 cycles to leave.
+    static constexpr int OUT = 32 * 64;
+    static constexpr int OFF_OUT = OFF_SCALE + EPI_WARPS * kAhead * SLOT * 4;
+    static constexpr int OFF_SHARED = OFF_OUT + EPI_WARPS * OUT;
     static constexpr int BYTES = OFF_SHARED + static_cast<int>(sizeof(Fp8Shared));
     static constexpr int SMEM = BYTES + 1024;
     // Registers: a thread's sums, its TMEM words and addresses take about
@@ -366,22 +441,38 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
     const int q = warp & 3, part = warp >> 2;
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(q * 32) << 16) + part * C::COLS;
     const uint32_t ring = smem_u32(scale_smem + warp * C::kAhead * C::SLOT);
+    const uint32_t out = smem_u32(scale_smem) + (C::OFF_OUT - C::OFF_SCALE) + warp * C::OUT;
     const int units = S.first[p.groups];
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int acc = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        const Unit w = unit_of<KIND>(p, S, u, C::BM, BN);
-        const int row = w.row0 + q * 32 + lane;
-        const int col = w.col0 + part * C::COLS;
-        const bool live = row < w.rows_end;
-        // Scales: the row's own; and one for all the columns (a weight's
-        // tile; a lane holds the next 32 blocks') or one for each column.
-        const float *sa = live ? p.sa + row * p.sa_row + w.kblk0 * p.sa_blk : p.sa;
-        const float *sb;
-        bool in0, in1 = false;
-        float tile_scale = 0.0f;
+    // The current tile, and where its scales are: the row's own; and one for
+    // all the columns (a weight's tile; a lane holds the next 32 blocks') or
+    // one for each column.
+    Unit w{};
+    const float *sa = p.sa, *sb = p.sb;
+    bool live = false, in0 = false, in1 = false;
+    float tile_scale = 0.0f;
+    auto fetch = [&](int b) {        // block b's scales, on their way into its slot
+        if (b < w.nblk) {
+            const uint32_t slot = ring + (b % C::kAhead) * (C::SLOT * 4) + lane * 4;
+            copy_async4(slot, sa, live);
+            if (live) sa += p.sa_blk;
+            if constexpr (KIND == kFp8Wgrad) {
+                copy_async4(slot + 128, sb, in0);
+                copy_async4(slot + 256, sb + (in1 ? 32 * p.sb_row : 0), in1);
+                if (in0) sb += p.sb_blk;
+            }
+        }
+        copy_commit();
+    };
+    auto begin = [&](int u) {
+        if (u >= units) return;
+        w = unit_of<KIND>(p, S, u, C::BM, BN);
+        const int row = w.row0 + q * 32 + lane, col = w.col0 + part * C::COLS;
+        live = row < w.rows_end;
+        sa = live ? p.sa + row * p.sa_row + w.kblk0 * p.sa_blk : p.sa;
         if constexpr (KIND == kFp8Rows) {
             in0 = col < p.cols;
             sb = in0 ? p.sb + w.group * p.sb_grp + static_cast<long long>(col / kBlock) * p.sb_row : p.sb;
@@ -391,23 +482,15 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
             in1 = col + lane + 32 < p.cols;
             sb = p.sb + (in0 ? w.kblk0 * p.sb_blk + static_cast<long long>(col + lane) * p.sb_row : 0);
         }
-        auto fetch = [&](int b) {
-            if (b < w.nblk) {
-                const uint32_t slot = ring + (b % C::kAhead) * (C::SLOT * 4) + lane * 4;
-                copy_async4(slot, sa + (live ? b * p.sa_blk : 0), live);
-                if constexpr (KIND == kFp8Wgrad) {
-                    copy_async4(slot + 128, sb + (in0 ? b * p.sb_blk : 0), in0);
-                    copy_async4(slot + 256, sb + (in1 ? b * p.sb_blk + 32 * p.sb_row : 0), in1);
-                }
-            }
-            copy_commit();
-        };
-        uint64_t sum[C::COLS / 2];
-#pragma unroll
-        for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0;
         __syncwarp();                // the last tile's scales have been read
 #pragma unroll
         for (int b = 0; b < C::kAhead - 1; ++b) fetch(b);
+    };
+    begin(blockIdx.x);
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        uint64_t sum[C::COLS / 2];
+#pragma unroll
+        for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0;
         for (int b = 0; b < w.nblk; ++b) {
             copy_wait<C::kAhead - 2>();
             __syncwarp();            // every lane's copies; and slot b - 1 is free
@@ -469,25 +552,30 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
             }
         }
         if (!ok) return;             // a wait of this tile failed: the launch is aborting
+        // The next tile's first scales are under way while this one is stored.
+        const Unit done = w;
+        begin(u + gridDim.x);
+        const int row0 = done.row0 + q * 32, col = done.col0 + part * C::COLS;
         if constexpr (KIND == kFp8Rows) {
-            if (live) {
+            constexpr int N = F32 ? 16 : 32;         // columns of 64 bytes
 #pragma unroll
-                for (int i = 0; i < C::COLS; i += 8) {
-                    float f[8];
+            for (int i = 0; i < C::COLS; i += N) {
+                uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) unpair(sum[(i + e) / 2], f[e], f[e + 1]);
-                    if (col + i < p.cols) store_cols8<F32>(p, row * p.ldo, col + i, f);
+                for (int e = 0; e < 16; ++e) {
+                    float lo, hi;
+                    if constexpr (F32) {
+                        unpair(sum[(i + e) / 2], lo, hi);
+                        o[e] = __float_as_uint((e & 1) ? hi : lo);
+                    } else {
+                        unpair(sum[i / 2 + e], lo, hi);
+                        o[e] = pack_bf16(lo, hi);
+                    }
                 }
+                if (col + i < p.cols) store_rows64<F32>(p, out, o, row0, done.rows_end, 0, col + i, lane);
             }
         } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int r = w.row0 + q * 32 + (lane >> 2) + 16 * (i >> 4) + 8 * (i & 1);
-                const int c = col + 8 * ((i >> 1) & 7) + 2 * (lane & 3);
-                float lo, hi;
-                unpair(sum[i], lo, hi);
-                if (r < w.rows_end) store_cols2<F32>(p, r * p.ldo + w.group * p.og, c, lo, hi);
-            }
+            store_fragment<F32>(p, out, sum, row0, done.rows_end, done.group * p.og, col, lane);
         }
     }
     if constexpr (KIND == kFp8Rows) zero_unowned<F32>(p, warp * 32 + lane, C::EPI_WARPS * 32);
