@@ -297,9 +297,9 @@ def det_fp8_quantize_cols(x, offsets=None, *, stream=None):
     nb = _blocks_for(M, offsets)
     with _on(stream):
         q = torch.empty((K, nb * BLOCK), dtype=_E4M3, device=x.device)
-        s = torch.empty((nb, K), dtype=_F32, device=x.device)
+        s = _new(nb, K, _F32, x.device)
     _run("det_fp8_quantize_cols", p, o, q.data_ptr(), s.data_ptr(), M, K, 0 if offsets is None else offsets.shape[0] - 1,
-         nb, ld, nb * BLOCK, max(K, 1), _dg._stream_handle(stream))
+         nb, ld, nb * BLOCK, max(s.stride(0), 4), _dg._stream_handle(stream))
     return q, s
 
 
@@ -405,8 +405,11 @@ def det_fp8_gemm_wgrad(Yt, y_scale, Xt, x_scale, offsets=None, *, out_dtype=_F32
     if L2 != L or L % BLOCK:
         raise ValueError("Yt and Xt must have the same whole number of blocks: %d vs %d columns" % (L, L2))
     nb = L // BLOCK
-    sy = _flat(y_scale, "y_scale", _F32, (nb, N))
-    sx = _flat(x_scale, "x_scale", _F32, (nb, K))
+    sy, ldsy = _mat(y_scale, "y_scale", _F32)
+    sx, ldsx = _mat(x_scale, "x_scale", _F32)
+    if tuple(y_scale.shape) != (nb, N) or tuple(x_scale.shape) != (nb, K):
+        raise ValueError("y_scale and x_scale must have shapes %s and %s, got %s and %s"
+                         % ((nb, N), (nb, K), tuple(y_scale.shape), tuple(x_scale.shape)))
     G = 1
     off = None
     M = L
@@ -423,7 +426,7 @@ def det_fp8_gemm_wgrad(Yt, y_scale, Xt, x_scale, offsets=None, *, out_dtype=_F32
     with _on(stream):
         dW = _new(N, K, out_dtype, Yt.device, None if offsets is None else G) if out is None else _given(out, shape)
     d, _, _, _, ldd, gd = _mats(dW[None] if offsets is None else dW, "out", out_dtype)
-    _run("det_fp8_gemm_wgrad", y, sy, x, sx, off, d, f32, G, M, N, K, nb, max(ldy, 16), N, max(ldx, 16), K, ldd, gd,
+    _run("det_fp8_gemm_wgrad", y, sy, x, sx, off, d, f32, G, M, N, K, nb, max(ldy, 16), max(ldsy, 4), max(ldx, 16), max(ldsx, 4), ldd, gd,
          _dg._stream_handle(stream))
     return dW
 

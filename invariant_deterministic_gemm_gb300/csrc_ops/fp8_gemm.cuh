@@ -177,10 +177,11 @@ __device__ __forceinline__ uint64_t lds2(uint32_t at)
     return v;
 }
 
-// One float into shared memory behind the thread's back; zero when !in.
-__device__ __forceinline__ void copy_async4(uint32_t dst, const float *src, bool in)
+// Sixteen bytes into shared memory behind the thread's back, the first
+// `bytes` of them from src, zeros after.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const float *src, int bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -410,9 +411,9 @@ struct PlainCfg {
     static constexpr int A_STAGE = BM * kBlock, B_STAGE = BN * kBlock;
     static constexpr int NACC = BN == 192 ? 2 : 4;
     static constexpr int OFF_B = STAGES * A_STAGE;
-    // Scales are copied kAhead blocks before they are used (an L2 read takes
-    // about as long as two blocks): for each epilogue warp, its rows' and
-    // columns' scales of kAhead blocks.
+    // Scales are read kAhead blocks before they are used (an L2 read takes
+    // about as long as two blocks): into registers, or, for the weight
+    // gradient, into a ring of each epilogue warp's rows' and columns' scales.
     static constexpr int kAhead = 4, SLOT = 32 + COLS;
     static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;       // [EPI_WARPS][kAhead][SLOT] floats
     // A finished tile goes out through shared memory, 64 bytes of 32 rows a
@@ -447,74 +448,79 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
     int acc = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // The current tile, and where its scales are: the row's own; and one for
-    // all the columns (a weight's tile; a lane holds the next 32 blocks') or
-    // one for each column.
+    // The current tile and where its scales are.
     Unit w{};
     const float *sa = p.sa, *sb = p.sb;
-    bool live = false, in0 = false, in1 = false;
-    float tile_scale = 0.0f;
-    auto fetch = [&](int b) {        // block b's scales, on their way into its slot
-        if (b < w.nblk) {
-            const uint32_t slot = ring + (b % C::kAhead) * (C::SLOT * 4) + lane * 4;
-            copy_async4(slot, sa, live);
-            if (live) sa += p.sa_blk;
-            if constexpr (KIND == kFp8Wgrad) {
-                copy_async4(slot + 128, sb, in0);
-                copy_async4(slot + 256, sb + (in1 ? 32 * p.sb_row : 0), in1);
-                if (in0) sb += p.sb_blk;
-            }
-        }
+    // A weight's product: the row's scale and the weight tile's (one for all
+    // the thread's columns), of the next kAhead blocks.
+    float ra[C::kAhead], rb[C::kAhead];
+    bool live = false, in0 = false;
+    // Weight gradient: lanes 0-7 copy the scales of the warp's rows, lanes
+    // 8-23 those of its columns, four each; `sa` is the lane's next address.
+    int bytes = 0;
+    long long step = 0;
+    auto load = [&](int b, int j) {
+        const bool more = b < w.nblk;
+        ra[j] = more && live ? __ldg(sa) : 0.0f;
+        rb[j] = more && in0 ? __ldg(sb) : 0.0f;
+        sa += p.sa_blk;
+        sb += p.sb_blk;
+    };
+    auto fetch = [&](int b) {
+        if (b < w.nblk && lane < 24) copy_async16(ring + (b % C::kAhead) * (C::SLOT * 4) + lane * 16, sa, bytes);
+        sa += step;
         copy_commit();
     };
     auto begin = [&](int u) {
         if (u >= units) return;
         w = unit_of<KIND>(p, S, u, C::BM, BN);
-        const int row = w.row0 + q * 32 + lane, col = w.col0 + part * C::COLS;
-        live = row < w.rows_end;
-        sa = live ? p.sa + row * p.sa_row + w.kblk0 * p.sa_blk : p.sa;
+        const int row0 = w.row0 + q * 32, col = w.col0 + part * C::COLS;
         if constexpr (KIND == kFp8Rows) {
+            live = row0 + lane < w.rows_end;
             in0 = col < p.cols;
-            sb = in0 ? p.sb + w.group * p.sb_grp + static_cast<long long>(col / kBlock) * p.sb_row : p.sb;
-            tile_scale = in0 && lane < w.nblk ? __ldg(sb + lane * p.sb_blk) : 0.0f;
-        } else {
-            in0 = col + lane < p.cols;
-            in1 = col + lane + 32 < p.cols;
-            sb = p.sb + (in0 ? w.kblk0 * p.sb_blk + static_cast<long long>(col + lane) * p.sb_row : 0);
-        }
-        __syncwarp();                // the last tile's scales have been read
+            sa = p.sa + (live ? (row0 + lane) * p.sa_row : 0);
+            sb = p.sb + (in0 ? w.group * p.sb_grp + static_cast<long long>(col / kBlock) * p.sb_row : 0);
 #pragma unroll
-        for (int b = 0; b < C::kAhead - 1; ++b) fetch(b);
+            for (int j = 0; j < C::kAhead; ++j) load(j, j);
+        } else {
+            const bool rows = lane < 8;
+            const int at = rows ? row0 + lane * 4 : col + (lane - 8) * 4;
+            bytes = min(max((rows ? w.rows_end : p.cols) - at, 0), 4) * 4;
+            step = bytes ? (rows ? p.sa_blk : p.sb_blk) : 0;
+            sa = (rows ? p.sa : p.sb) + (bytes ? at + w.kblk0 * step : 0);
+            __syncwarp();            // the last tile's scales have been read
+#pragma unroll
+            for (int b = 0; b < C::kAhead - 1; ++b) fetch(b);
+        }
     };
-    begin(blockIdx.x);
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    begin(static_cast<int>(blockIdx.x));
+    for (int u = static_cast<int>(blockIdx.x); u < units; u += static_cast<int>(gridDim.x)) {
         uint64_t sum[C::COLS / 2];
 #pragma unroll
         for (int i = 0; i < C::COLS / 2; ++i) sum[i] = 0;
-        for (int b = 0; b < w.nblk; ++b) {
-            copy_wait<C::kAhead - 2>();
-            __syncwarp();            // every lane's copies; and slot b - 1 is free
-            fetch(b + C::kAhead - 1);
-            const uint32_t slot = ring + (b % C::kAhead) * (C::SLOT * 4);
-            const uint32_t t = t0 + acc * BN;
-            auto arrived = [&]() {
-                ok &= mbar_wait_inline(smem_u32(&S.accf[acc]), phase, abort_s, p.status, p.timeout_ns) != 0;
-                tc_fence_after();
-            };
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_if(smem_u32(&S.acce[acc]), lane == 0);
-            };
+        // Waits for the next block's accumulator; hands it back when its words are in registers.
+        auto arrived = [&]() {
+            ok &= mbar_wait_inline(smem_u32(&S.accf[acc]), phase, abort_s, p.status, p.timeout_ns) != 0;
+            tc_fence_after();
+        };
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(smem_u32(&S.acce[acc]), lane == 0);
+            if (++acc == C::NACC) {
+                acc = 0;
+                phase ^= 1u;
+            }
+        };
+        auto block = [&](int b, int j) {
             if constexpr (KIND == kFp8Rows) {
-                float rs = lds1(slot + lane * 4);
-                if (b > 0 && (b & 31) == 0) tile_scale = in0 && b + lane < w.nblk ? __ldg(sb + (b + lane) * p.sb_blk) : 0.0f;
-                rs *= __shfl_sync(kFull, tile_scale, b & 31);
+                const float rs = ra[j] * rb[j];
                 const uint64_t r2 = pair(rs, rs);
+                load(b + C::kAhead, j);
                 arrived();
                 uint32_t v0[32], v1[32];
-                tmem_ld32(t, v0);
-                tmem_ld32(t + 32, v1);
+                tmem_ld32(t0 + acc * BN, v0);
+                tmem_ld32(t0 + acc * BN + 32, v1);
                 tmem_wait_ld();
                 reg_fence(v0);
                 reg_fence(v1);
@@ -524,16 +530,21 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum[16 + i] = fma2(pair(v1[2 * i], v1[2 * i + 1]), r2, sum[16 + i]);
             } else {
-                // sum[16 g + 2 j + h]: row lane / 4 + 16 g + 8 h, columns 8 j + 2 (lane % 4) + {0, 1}
+                // sum[16 g + 2 i + h]: row lane / 4 + 16 g + 8 h, columns 8 i + 2 (lane % 4) + {0, 1}
+                copy_wait<C::kAhead - 2>();
+                __syncwarp();        // every lane's copies of b are here, and every lane has read slot b - 1
+                fetch(b + C::kAhead - 1);
+                const uint32_t slot = ring + j * (C::SLOT * 4);
                 uint64_t cs[8], rs[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) cs[j] = lds2(slot + 128 + (8 * j + 2 * (lane & 3)) * 4);
+                for (int i = 0; i < 8; ++i) cs[i] = lds2(slot + 128 + (8 * i + 2 * (lane & 3)) * 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float r = lds1(slot + (8 * i + (lane >> 2)) * 4);
                     rs[i] = pair(r, r);
                 }
                 arrived();
+                const uint32_t t = t0 + acc * BN;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     uint32_t v[32];
@@ -546,15 +557,18 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
                         sum[16 * g + i] = fma2(pair(v[2 * i], v[2 * i + 1]), mul2(rs[2 * g + (i & 1)], cs[i / 2]), sum[16 * g + i]);
                 }
             }
-            if (++acc == C::NACC) {
-                acc = 0;
-                phase ^= 1u;
+        };
+        for (int b = 0; b < w.nblk; b += C::kAhead) {
+#pragma unroll
+            for (int j = 0; j < C::kAhead; ++j) {
+                if (b + j >= w.nblk) break;
+                block(b + j, j);
             }
         }
         if (!ok) return;             // a wait of this tile failed: the launch is aborting
         // The next tile's first scales are under way while this one is stored.
         const Unit done = w;
-        begin(u + gridDim.x);
+        begin(u + static_cast<int>(gridDim.x));
         const int row0 = done.row0 + q * 32, col = done.col0 + part * C::COLS;
         if constexpr (KIND == kFp8Rows) {
             constexpr int N = F32 ? 16 : 32;         // columns of 64 bytes

@@ -615,8 +615,8 @@ det_gemm_status det_fp8_gemm_wgrad(const uint8_t *Yt, const float *sy, const uin
     const Arr out{dW, N, K, lddw, es, 16, G, gdw};
     det_gemm_status s;
     if (M > 0)
-        s = check_all({mat8(Yt, N, blocks * kBlock, ldyt), Arr{sy, blocks, N, ldsy, 4, 4},
-                       mat8(Xt, K, blocks * kBlock, ldxt), Arr{sx, blocks, K, ldsx, 4, 4},
+        s = check_all({mat8(Yt, N, blocks * kBlock, ldyt), Arr{sy, blocks, N, ldsy, 4, 16},
+                       mat8(Xt, K, blocks * kBlock, ldxt), Arr{sx, blocks, K, ldsx, 4, 16},
                        vec4(offsets, offsets ? G + 1 : 0)}, {out});
     else
         s = check(out);
