@@ -32,10 +32,10 @@
 // Transposed tile (few rows: decode): the weight is the MMA's row side, its
 // 32, 64 or 128 rows are TMEM lanes, and the tokens its 16 to 64 columns.
 // The launch is bound by reading the weight once, and a tile walks its
-// blocks one after the other, so what a block costs each role counts: a
-// stage holds two blocks (one wait, one release), two threads issue the MMAs
-// of alternate stages, a warp of its own brings the scales' products, and the epilogue
-// takes two blocks a turn where its registers allow. Up to 96 KB of copies
+// blocks one after the other, so what a block costs each role counts: copies
+// come two blocks a stage, accumulators go round four blocks at a time (one
+// wait, commit and release for the four), two threads issue the MMAs of
+// alternate fours, and a warp of its own brings the scales' products. Up to 96 KB of copies
 // are in flight a CTA and two CTAs share an SM (192 KB and one for 64 tokens). A tile of 32 or 64 weight
 // rows still issues 128-row MMAs: the other lanes multiply whatever the
 // following shared memory holds and are never read.
@@ -740,16 +740,16 @@ __global__ void __launch_bounds__(PlainCfg<BN>::THREADS, 1) fp8_plain_kernel(con
 template <int NT>
 struct SwapCfg {
     static constexpr int THREADS = 256;
-    static constexpr int NACC = NT == 64 ? 4 : 8;    // accumulators, and slots of scales
-    static constexpr int TMEM_COLS = NACC * NT;
-    static constexpr int PER_STAGE = 2;              // blocks of a stage
-    static constexpr int PER_TURN = NT == 64 ? 1 : 2;    // blocks the epilogue takes at once
+    static constexpr int PER_STAGE = 2;              // blocks of a ring stage
+    static constexpr int PER_SLOT = 4;               // blocks of an accumulator slot: two stages
+    static constexpr int SLOTS = NT == 16 ? 4 : 2;
+    static constexpr int TMEM_COLS = SLOTS * PER_SLOT * NT;
     static constexpr int MAX_STAGES = 16;
     // 64 columns of sums leave registers for one CTA an SM only.
     static constexpr int CTAS = NT == 64 ? 1 : 2;
     static constexpr int RING = (CTAS == 1 ? 192 : 96) * 1024;       // bytes of the operand ring
-    static constexpr int OFF_SCALE = RING;           // [NACC][NT] floats
-    static constexpr int OFF_SHARED = OFF_SCALE + NACC * NT * 4;
+    static constexpr int OFF_SCALE = RING;           // [SLOTS][PER_SLOT][NT] floats
+    static constexpr int OFF_SHARED = OFF_SCALE + SLOTS * PER_SLOT * NT * 4;
     static constexpr int BYTES = OFF_SHARED + static_cast<int>(sizeof(Fp8Shared));
     static constexpr int SMEM = BYTES + 1024;
     static_assert(CTAS * SMEM <= 232448, "the CTAs of an SM share its memory");
@@ -771,7 +771,7 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int units = S.first[p.groups];
     const uint32_t abort_s = smem_u32(&S.abort_flag);
-    int acc = 0;
+    int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -779,69 +779,54 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
         uint64_t sum[NT / 2];
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) sum[i] = 0;
-        auto arrived = [&](int a, uint32_t ph) {
-            ok &= mbar_wait_inline(smem_u32(&S.accf[a]), ph, abort_s, p.status, p.timeout_ns) != 0;
-        };
-        // Adds N columns of a block (words v, scales c) to sum[at..].
-        auto add = [&](const uint32_t *v, uint32_t c, int at, int n) {
+        for (int b = 0; b < w.nblk; b += C::PER_SLOT) {
+            ok &= mbar_wait_inline(smem_u32(&S.accf[slot]), phase, abort_s, p.status, p.timeout_ns) != 0;
+            tc_fence_after();
+            const uint32_t t = t0 + slot * C::PER_SLOT * NT;
+            const float *sc = scale_smem + slot * C::PER_SLOT * NT;
+            if constexpr (NT == 16) {
+                // All four blocks at once (a block past the contraction's end
+                // has words of an earlier turn and is left out).
+                uint32_t v[4][16];
 #pragma unroll
-            for (int i = 0; i < n; i += 4) {
-                add4(sum[(at + i) / 2], sum[(at + i) / 2 + 1], pair(v[i], v[i + 1]), pair(v[i + 2], v[i + 3]), c + 4 * i);
-            }
-        };
-        auto scales = [&](int a) { return smem_u32(scale_smem + a * NT); };
-        auto release = [&](int a) { mbar_arrive_if(smem_u32(&S.acce[a]), lane == 0); };
-        auto next = [&](int &a, uint32_t &ph) {
-            if (++a == C::NACC) {
-                a = 0;
-                ph ^= 1u;
-            }
-        };
-        for (int b = 0; b < w.nblk; b += C::PER_TURN) {
-            const int a0 = acc;
-            arrived(a0, phase);
-            next(acc, phase);
-            if constexpr (NT == 64) {
-                tc_fence_after();
+                for (int j = 0; j < 4; ++j) tmem_ld16(t + j * NT, v[j]);
+                tmem_wait_ld();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
-                    tmem_ld32(t0 + a0 * NT + 32 * h, v);
-                    tmem_wait_ld();
-                    reg_fence(v);
-                    add(v, scales(a0) + 128 * h, 32 * h, 32);
+                for (int j = 0; j < 4; ++j) reg_fence16(v[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (b + j >= w.nblk) break;
+                    const ulonglong2 *c = reinterpret_cast<const ulonglong2 *>(sc + j * NT);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const ulonglong2 s = c[i];
+                        sum[2 * i] = fma2(pair(v[j][4 * i], v[j][4 * i + 1]), s.x, sum[2 * i]);
+                        sum[2 * i + 1] = fma2(pair(v[j][4 * i + 2], v[j][4 * i + 3]), s.y, sum[2 * i + 1]);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                release(a0);
             } else {
-                const bool two = b + 1 < w.nblk;
-                const int a1 = acc;
-                if (two) {
-                    arrived(a1, phase);
-                    next(acc, phase);
+#pragma unroll 1
+                for (int j = 0; j < C::PER_SLOT; ++j) {
+                    if (b + j >= w.nblk) break;
+#pragma unroll
+                    for (int h = 0; h < NT / 32; ++h) {
+                        uint32_t v[32];
+                        tmem_ld32(t + j * NT + 32 * h, v);
+                        tmem_wait_ld();
+                        reg_fence(v);
+                        const uint32_t c = smem_u32(sc + j * NT + 32 * h);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            add4(sum[16 * h + i / 2], sum[16 * h + i / 2 + 1], pair(v[i], v[i + 1]), pair(v[i + 2], v[i + 3]), c + 4 * i);
+                    }
                 }
-                tc_fence_after();
-                uint32_t v0[NT], v1[NT];
-                if constexpr (NT == 16) {
-                    tmem_ld16(t0 + a0 * NT, v0);
-                    if (two) tmem_ld16(t0 + a1 * NT, v1);
-                    tmem_wait_ld();
-                    reg_fence16(v0);
-                    reg_fence16(v1);
-                } else {
-                    tmem_ld32(t0 + a0 * NT, v0);
-                    if (two) tmem_ld32(t0 + a1 * NT, v1);
-                    tmem_wait_ld();
-                    reg_fence(v0);
-                    reg_fence(v1);
-                }
-                add(v0, scales(a0), 0, NT);
-                if (two) add(v1, scales(a1), 0, NT);
-                tc_fence_before();
-                __syncwarp();
-                release(a0);
-                if (two) release(a1);
+            }
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(smem_u32(&S.acce[slot]), lane == 0);
+            if (++slot == C::SLOTS) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
         if (!ok) return;             // a wait of this tile failed: the launch is aborting
@@ -863,15 +848,13 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
     zero_unowned<F32>(p, warp * 32 + lane, 128);
 }
 
-// One warp: the products of a block's scales, token by token, into the slot
-// of the block's accumulator. The loads of the next kAhead blocks are under
-// way while the last ones are handed out.
+// One warp: the products of the scales, token by token, of a slot's blocks.
+// The loads of the next slot are under way while one is handed out.
 template <int NT>
 __device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, float *scale_smem, int tile_rows, int lane)
 {
     using C = SwapCfg<NT>;
     constexpr int SL = NT < 32 ? 1 : NT / 32;        // tokens of a lane
-    constexpr int kAhead = 8;
     const int units = S.first[p.groups];
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int slot = 0;
@@ -879,10 +862,10 @@ __device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, fl
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
         const float *sw = p.sb + w.group * p.sb_grp + static_cast<long long>(w.col0 / kBlock) * p.sb_row;
-        float t[kAhead][SL], wv[kAhead];
+        float t[C::PER_SLOT][SL], wv[C::PER_SLOT];
         auto load = [&](int b0) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < C::PER_SLOT; ++j) {
                 const bool in = b0 + j < w.nblk;
                 wv[j] = in ? __ldg(sw + (b0 + j) * p.sb_blk) : 0.0f;
 #pragma unroll
@@ -893,27 +876,25 @@ __device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, fl
             }
         };
         load(0);
-        for (int b0 = 0; b0 < w.nblk; b0 += kAhead) {
-            float c[kAhead][SL];
+        for (int b0 = 0; b0 < w.nblk; b0 += C::PER_SLOT) {
+            float c[C::PER_SLOT][SL];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
+            for (int j = 0; j < C::PER_SLOT; ++j)
 #pragma unroll
                 for (int i = 0; i < SL; ++i) c[j][i] = t[j][i] * wv[j];
-            load(b0 + kAhead);
+            load(b0 + C::PER_SLOT);
+            if (!__all_sync(kFull, mbar_wait_inline(smem_u32(&S.acce[slot]), phase ^ 1u, abort_s, p.status, p.timeout_ns) != 0))
+                return;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                if (b0 + j >= w.nblk) break;
-                if (!__all_sync(kFull, mbar_wait_inline(smem_u32(&S.acce[slot]), phase ^ 1u, abort_s, p.status, p.timeout_ns) != 0))
-                    return;
+            for (int j = 0; j < C::PER_SLOT; ++j)
 #pragma unroll
                 for (int i = 0; i < SL; ++i)
-                    if (32 * i + lane < NT) scale_smem[slot * NT + 32 * i + lane] = c[j][i];
-                __syncwarp();
-                mbar_arrive_if(smem_u32(&S.accf[slot]), lane == 0);
-                if (++slot == C::NACC) {
-                    slot = 0;
-                    phase ^= 1u;
-                }
+                    if (32 * i + lane < NT) scale_smem[(slot * C::PER_SLOT + j) * NT + 32 * i + lane] = c[j][i];
+            __syncwarp();
+            mbar_arrive_if(smem_u32(&S.accf[slot]), lane == 0);
+            if (++slot == C::SLOTS) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
     }
@@ -964,8 +945,8 @@ __device__ __forceinline__ void swap_copy(const Fp8Params &p, Fp8Shared &S, uint
     }
 }
 
-// One thread of each of the two issuing warps: issuer i takes the stages g
-// of the CTA's sequence with g % 2 == i.
+// One thread of each of the two issuing warps: issuer i takes the slots g of
+// the CTA's sequence with g % 2 == i.
 template <int NT>
 __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uint32_t base, int tile_rows, int issuer)
 {
@@ -977,40 +958,42 @@ __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uin
     const int units = S.first[p.groups];
     volatile int *abort_flag = &S.abort_flag;
     const uint32_t tmem = S.tmem;
-    int s = 0, acc = 0, turn = 0;        // every stage is counted, its own are issued
+    int s = 0, slot = 0;                 // all of them are counted, its own are issued
     uint32_t round = 0, phase = 0;
-    bool ok = true, issued = false;
+    bool ok = true, issued = false, mine = issuer == 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int nblk = unit_of<kFp8Rows>(p, S, u, NT, tile_rows).nblk;
-        for (int b = 0; ok && b < nblk; b += C::PER_STAGE) {
-            const int n = min(C::PER_STAGE, nblk - b);
-            const bool mine = turn == issuer;
-            if (mine && !wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true)) {
+        for (int b = 0; ok && b < nblk; b += C::PER_SLOT) {
+            if (mine && !wait_bounded(smem_u32(&S.acce[slot]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
                 ok = false;
                 break;
             }
-            for (int j = 0; j < n; ++j) {
+            for (int h = 0; h < C::PER_SLOT && b + h < nblk; h += C::PER_STAGE) {
                 if (mine) {
-                    if (!wait_bounded(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
+                    if (!wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int at = s * C::PER_STAGE + j;
-                    mma_block(tmem + acc * NT, base + at * w_blk, base_t + at * NT * kBlock, IDESC);
-                    mma_commit(smem_u32(&S.accf[acc]));
+#pragma unroll
+                    for (int j = 0; j < C::PER_STAGE; ++j) {
+                        if (b + h + j >= nblk) break;
+                        const int at = s * C::PER_STAGE + j;
+                        mma_block(tmem + (slot * C::PER_SLOT + h + j) * NT, base + at * w_blk, base_t + at * NT * kBlock, IDESC);
+                    }
+                    mma_commit(smem_u32(&S.empty[s]));
                     issued = true;
                 }
-                if (++acc == C::NACC) {
-                    acc = 0;
-                    phase ^= 1u;
+                if (++s == stages) {
+                    s = 0;
+                    round ^= 1u;
                 }
             }
-            if (mine && ok) mma_commit(smem_u32(&S.empty[s]));
-            turn ^= 1;
-            if (++s == stages) {
-                s = 0;
-                round ^= 1u;
+            if (mine && ok) mma_commit(smem_u32(&S.accf[slot]));
+            mine = !mine;
+            if (++slot == C::SLOTS) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
     }
@@ -1037,7 +1020,7 @@ __global__ void __launch_bounds__(256, SwapCfg<NT>::CTAS) fp8_swap_kernel(const 
             mbar_init(smem_u32(&S.full[s]), 1);
             mbar_init(smem_u32(&S.empty[s]), 1);
         }
-        for (int a = 0; a < C::NACC; ++a) {
+        for (int a = 0; a < C::SLOTS; ++a) {
             mbar_init(smem_u32(&S.accf[a]), 2);      // the MMAs' commit and the scales
             mbar_init(smem_u32(&S.acce[a]), 4);
         }

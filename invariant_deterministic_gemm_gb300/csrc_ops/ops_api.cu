@@ -224,9 +224,12 @@ Fp8Plan plan_rows(int64_t rows, int64_t cols, int64_t groups, bool grouped, int 
     if (per <= 64) {
         pl.swap = true;
         pl.tile_m = per <= (grouped ? 8 : 16) ? 16 : per <= (grouped ? 16 : 32) ? 32 : 64;
-        const int64_t used = grouped ? std::min(rows, groups) : 1;
-        pl.tile_n = 128;
-        while (pl.tile_n > 32 && used * up(cols, pl.tile_n) < 2 * sms) pl.tile_n /= 2;
+        // The narrowest weight tile whose units all run at once: a tile walks
+        // the contraction block by block at the same pace whatever its width,
+        // so a second round costs as much as the first.
+        const int64_t used = grouped ? std::min(rows, groups) : 1, room = (pl.tile_m == 64 ? 1 : 2) * sms;
+        pl.tile_n = 32;
+        while (pl.tile_n < 128 && used * up(cols, pl.tile_n) > room) pl.tile_n *= 2;
         return pl;
     }
     pl.tile_n = plain_width(up(rows, 128) + (grouped ? groups / 2 : 0), cols, sms);
