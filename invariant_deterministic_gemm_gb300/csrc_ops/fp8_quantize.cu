@@ -6,11 +6,13 @@
 //
 // The quotient decides a rounding, so it is formed exactly enough to never
 // decide it wrongly: t = 448 x is exact in FP32 (11 significant bits), and
-// y0 = t * (1 / amax) is corrected once by its residual t - y0 * amax, which
-// one fused multiply-add forms exactly (Newton's correction of a quotient).
-// y is then exact whenever the quotient has few bits, which every e4m3
-// midpoint has; and a quotient of two BF16 values that is not a midpoint is
-// at least 2^-20 of its size away from one, far more than y's error.
+// y0 = t * r, r = 1 / amax within a unit in the last place, is corrected once
+// by its residual t - y0 * amax, which one fused multiply-add forms exactly
+// (Newton's correction of a quotient). y is then exact whenever the quotient
+// has few bits, which every e4m3 midpoint has; and a quotient of two BF16
+// values that is not a midpoint is at least 2^-20 of its size away from one,
+// far more than y's error. Two elements at a time (f32x2 operations). The
+// scale amax / 448 is corrected the same way and is correctly rounded.
 //
 // Bytes bound these kernels: the input is read once (BF16) and one byte an
 // element is written.
@@ -24,15 +26,59 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float block_scale(float amax)     // amax already floored; inf or NaN: NaN
 {
-    return amax < __int_as_float(0x7f800000) ? __fdiv_rn(amax, kE4M3Max) : __int_as_float(0x7fc00000);
+    if (!(amax < __int_as_float(0x7f800000))) return __int_as_float(0x7fc00000);
+    constexpr float r = 1.0f / kE4M3Max;
+    const float y = amax * r;
+    return fmaf(fmaf(-y, kE4M3Max, amax), r, y);
 }
 
-// x * 448 / amax for one element (r = 1 / amax; 0 when amax is not finite).
-__device__ __forceinline__ float quotient(float x, float amax, float r)
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
 {
-    const float t = x * kE4M3Max;
-    const float y = t * r;
-    return fmaf(fmaf(-y, amax, t), r, y);
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// What a block's elements are divided by: amax (floored, and at most 2^100)
+// and its reciprocal; `down` is what the elements are multiplied by first.
+struct Divisor {
+    float amax, r, down;
+    bool fine;
+};
+__device__ __forceinline__ Divisor divisor(float amax)
+{
+    Divisor d;
+    d.fine = amax < __int_as_float(0x7f800000);
+    // Near the top of the range, where 448 x would overflow, by 2^-40 first.
+    const bool large = amax > 1.2676506e30f;
+    d.down = large ? 448.0f * 9.094947e-13f : 448.0f;
+    d.amax = large ? amax * 9.094947e-13f : amax;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d.r) : "f"(d.amax));
+    return d;
+}
+
+// Two elements' quotients. a: (amax, amax'), r: reciprocals, s: factors.
+__device__ __forceinline__ uint64_t quotient2(uint64_t x, uint64_t neg_a, uint64_t r, uint64_t s)
+{
+    const uint64_t t = mul2(x, s);
+    const uint64_t y = mul2(t, r);
+    return fma2(fma2(y, neg_a, t), r, y);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
@@ -42,27 +88,32 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return d;
 }
 
-// |x| ordered as an integer (NaN above infinity), so that a maximum keeps NaN.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// The larger magnitudes of two pairs of BF16 values, as bit patterns: NaN is
+// above infinity, so a maximum keeps it.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+__device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
 
-__device__ __forceinline__ float floor_amax(uint32_t bits)
+// A BF16 bit pattern (magnitude) as a floored FP32 maximum.
+__device__ __forceinline__ float floor_amax(uint32_t bf16_bits)
 {
-    const uint32_t lo = __float_as_uint(kAmaxMin);
-    return __uint_as_float(bits < lo ? lo : bits);
+    const uint32_t lo = __float_as_uint(kAmaxMin), b = bf16_bits << 16;
+    return __uint_as_float(b < lo ? lo : b);
 }
 
-// Eight elements of one block -> eight e4m3 bytes.
-__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float amax)   // amax floored
+// Eight elements of one block (BF16 pairs) -> eight e4m3 bytes.
+__device__ __forceinline__ uint2 quantize8(const uint4 &v, const Divisor &d)
 {
-    if (!(amax < __int_as_float(0x7f800000))) return make_uint2(0, 0);
-    // Blocks near the top of the range are divided by 2^40 first, where 448 x would overflow.
-    const float down = amax > 1.2676506e30f ? 9.094947e-13f : 1.0f;
-    amax *= down;
-    const float r = __frcp_rn(amax);
-    float y[8];
+    if (!d.fine) return make_uint2(0, 0);
+    const uint64_t na = pair(-d.amax, -d.amax), r = pair(d.r, d.r), s = pair(d.down, d.down);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = quotient(f[i] * down, amax, r);
-    return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpair(quotient2(pair(bf_lo(w[i]), bf_hi(w[i])), na, r, s), lo, hi);
+        q[i] = e4m3x2(lo, hi);
+    }
+    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
 __device__ __forceinline__ void store_q8(uint8_t *row, int c, int cols, const uint2 &v)
@@ -78,9 +129,9 @@ __device__ __forceinline__ void store_q8(uint8_t *row, int c, int cols, const ui
 }
 
 // ---- along rows: 16 lanes own a block of 128 columns, 8 columns each; a
-// warp takes kUnroll pairs of blocks of one row.
+// warp takes kUnroll pairs of blocks of one row, all loads in flight at once.
 constexpr int kRowThreads = 128;
-constexpr int kUnroll = 2;
+constexpr int kUnroll = 4;
 constexpr int kWarpCols = 256 * kUnroll;
 
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p, int col_parts)
@@ -89,7 +140,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantP
     const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
     const long long m = w / col_parts;
     if (m >= p.n) return;
-    const int c0 = static_cast<int>(w % col_parts) * kWarpCols + lane * 8;
+    const int c0 = static_cast<int>(w - m * col_parts) * kWarpCols + lane * 8;
     const uint16_t *src = nullptr;
     if (p.rows) {
         const int f = __ldg(p.rows + m);
@@ -103,111 +154,125 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantP
         v[u] = make_uint4(0, 0, 0, 0);
         if (src && c0 + u * 256 < p.cols) v[u] = load8(src, c0 + u * 256, p.cols);
     }
+    uint8_t *q = p.q + m * p.ldq;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int c = c0 + u * 256;
-        float f[8];
-        unpack8(v[u], f);
-        uint32_t a = 0;
+        if (c - lane * 8 >= p.cols) break;           // the whole warp
+        uint32_t a = max2(max2(abs2(v[u].x), abs2(v[u].y)), max2(abs2(v[u].z), abs2(v[u].w)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a = max(a, abs_bits(f[i]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(kAll, a, o));
-        const float amax = floor_amax(a);
+        for (int o = 8; o > 0; o >>= 1) a = max2(a, __shfl_xor_sync(kAll, a, o));
+        const float amax = floor_amax(max(a & 0xFFFFu, a >> 16));
         if (c >= p.cols) continue;
-        store_q8(p.q + m * p.ldq, c, p.cols, quantize8(f, amax));
+        store_q8(q, c, p.cols, quantize8(v[u], divisor(amax)));
         if ((lane & 15) == 0) p.s[(c / kBlock) * p.lds + m] = block_scale(amax);
     }
 }
 
 // ---- along columns (the contraction is the token dimension): a CTA owns a
-// block of 128 rows and 64 columns. It reads 128 bytes of each row, keeps
-// the tile in shared memory, and writes 128 bytes for each column: out row
-// = column, out column = the block's place. With group bounds a block holds
-// rows of one group only, and the rows past the group's end are zeros.
+// block of 128 rows and 64 columns. A warp reads 16 of the rows, a lane two
+// neighbouring columns of each (whole lines), so a lane ends up with 16
+// consecutive bytes of either column's output; they go out through shared
+// memory as 128 bytes a column. With group bounds a block holds rows of one
+// group only, and the rows past the group's end are zeros.
 constexpr int kColThreads = 256;
 constexpr int kColTile = 64;
+constexpr int kPitch = kBlock + 16;  // bytes between columns in shared memory: 16-byte accesses without conflicts
 
 __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantParams p, int col_tiles)
 {
-    __shared__ float tile[kBlock][kColTile + 1];
-    __shared__ int sb[kMaxExperts + 1];
-    __shared__ uint32_t part[4][kColTile];
+    __shared__ __align__(16) uint8_t out[kColTile * kPitch];
+    __shared__ uint32_t part[kColThreads / 32][32];
     const int blk = blockIdx.x / col_tiles;
-    const int c0 = (blockIdx.x % col_tiles) * kColTile;
+    const int c0 = (blockIdx.x - blk * col_tiles) * kColTile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int r0, r1;
     if (p.offsets) {
-        // First block of each group, by one warp (a running sum over the groups).
-        if (threadIdx.x < 32) {
-            int run = 0;
-            for (int g0 = 0; g0 < p.groups; g0 += 32) {
-                const int g = g0 + threadIdx.x;
-                int nb = 0;
-                if (g < p.groups) {
-                    const int lo = min(max(p.offsets[g], 0), p.n), hi = min(max(p.offsets[g + 1], lo), p.n);
-                    nb = (hi - lo + kBlock - 1) / kBlock;
-                }
-                int v = nb;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int u = __shfl_up_sync(kAll, v, o);
-                    if (static_cast<int>(threadIdx.x) >= o) v += u;
-                }
-                if (g < p.groups) sb[g] = run + v - nb;
-                run += __shfl_sync(kAll, v, 31);
+        // The group this block belongs to: a running sum of the groups'
+        // blocks, 32 groups a step, by every warp for itself.
+        int run = 0;
+        r0 = r1 = -1;
+        for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            const int g = g0 + lane;
+            int lo = 0, hi = 0;
+            if (g < p.groups) {
+                lo = min(max(__ldg(p.offsets + g), 0), p.n);
+                hi = min(max(__ldg(p.offsets + g + 1), lo), p.n);
             }
-            if (threadIdx.x == 0) sb[p.groups] = run;
+            const int nb = (hi - lo + kBlock - 1) / kBlock;
+            int v = nb;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kAll, v, o);
+                if (lane >= o) v += u;
+            }
+            const int first = run + v - nb;
+            const unsigned who = __ballot_sync(kAll, blk >= first && blk < first + nb);
+            if (who) {
+                const int at = __ffs(static_cast<int>(who)) - 1;
+                const int l = __shfl_sync(kAll, lo, at), h = __shfl_sync(kAll, hi, at), f = __shfl_sync(kAll, first, at);
+                r0 = l + (blk - f) * kBlock;
+                r1 = min(h, r0 + kBlock);
+                break;
+            }
+            run += __shfl_sync(kAll, v, 31);
         }
-        __syncthreads();
-        if (blk >= sb[p.groups]) return;
-        int a = 0, b = p.groups;                     // last group whose first block is <= blk
-        while (b - a > 1) {
-            const int mid = (a + b) / 2;
-            if (sb[mid] <= blk) a = mid;
-            else b = mid;
-        }
-        const int lo = min(max(p.offsets[a], 0), p.n), hi = min(max(p.offsets[a + 1], lo), p.n);
-        r0 = lo + (blk - sb[a]) * kBlock;
-        r1 = min(hi, r0 + kBlock);
+        if (r0 < 0) return;          // past the last group's blocks (the whole CTA)
     } else {
         r0 = blk * kBlock;
         r1 = min(p.n, r0 + kBlock);
     }
+    const int c = c0 + 2 * lane;
+    uint32_t v[16];
     {
-        // 8 threads a row, 32 rows at a time
-        const int c = c0 + (threadIdx.x & 7) * 8;
-        for (int r = threadIdx.x >> 3; r < kBlock; r += kColThreads / 8) {
-            float f[8] = {};
-            if (r0 + r < r1 && c < p.cols) unpack8(load8(p.x + (r0 + r) * p.ldx, c, p.cols), f);
+        const uint16_t *x = p.x + (r0 + warp * 16) * p.ldx + c;
+        const int rows = r1 - r0 - warp * 16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tile[r][(threadIdx.x & 7) * 8 + i] = f[i];
+        for (int i = 0; i < 16; ++i) {
+            v[i] = 0;
+            if (i < rows) {
+                if (c + 1 < p.cols) v[i] = __ldg(reinterpret_cast<const uint32_t *>(x + i * p.ldx));
+                else if (c < p.cols) v[i] = __ldg(x + i * p.ldx);
+            }
         }
     }
-    __syncthreads();
-    // Thread: column col, quarter qr of the rows (32 of them).
-    const int col = threadIdx.x & 63, qr = threadIdx.x >> 6;
     uint32_t a = 0;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) a = max(a, abs_bits(tile[qr * 32 + r][col]));
-    part[qr][col] = a;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a = max2(a, abs2(v[i]));
+    part[warp][lane] = a;
     __syncthreads();
-    a = max(max(part[0][col], part[1][col]), max(part[2][col], part[3][col]));
-    if (c0 + col >= p.cols) return;
-    const float amax = floor_amax(a);
-    uint8_t *dst = p.q + static_cast<long long>(c0 + col) * p.ldq + static_cast<long long>(blk) * kBlock + qr * 32;
-    uint32_t w[8];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        float f[8];
+    for (int w = 0; w < kColThreads / 32; ++w) a = max2(a, part[w][lane]);
+    const float a0 = floor_amax(a & 0xFFFFu), a1 = floor_amax(a >> 16);
+    const Divisor d0 = divisor(a0), d1 = divisor(a1);
+    const uint64_t na = pair(-d0.amax, -d1.amax), r = pair(d0.r, d1.r), s = pair(d0.down, d1.down);
+    uint32_t q0[4], q1[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = tile[qr * 32 + b * 8 + i][col];
-        const uint2 q = quantize8(f, amax);
-        w[2 * b] = q.x;
-        w[2 * b + 1] = q.y;
+    for (int i = 0; i < 4; ++i) {
+        float y0[4], y1[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = v[4 * i + e];
+            unpair(quotient2(pair(bf_lo(w), bf_hi(w)), na, r, s), y0[e], y1[e]);
+        }
+        q0[i] = d0.fine ? e4m3x2(y0[0], y0[1]) | (e4m3x2(y0[2], y0[3]) << 16) : 0;
+        q1[i] = d1.fine ? e4m3x2(y1[0], y1[1]) | (e4m3x2(y1[2], y1[3]) << 16) : 0;
     }
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
-    if (qr == 0) p.s[blk * p.lds + c0 + col] = block_scale(amax);
+    *reinterpret_cast<uint4 *>(out + (2 * lane) * kPitch + warp * 16) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+    *reinterpret_cast<uint4 *>(out + (2 * lane + 1) * kPitch + warp * 16) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    if (warp == 0) {
+        float *sc = p.s + blk * p.lds + c;
+        if (c < p.cols) sc[0] = block_scale(a0);
+        if (c + 1 < p.cols) sc[1] = block_scale(a1);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int col = i * 32 + (threadIdx.x >> 3), k = threadIdx.x & 7;
+        if (c0 + col < p.cols)
+            *reinterpret_cast<uint4 *>(p.q + static_cast<long long>(c0 + col) * p.ldq + static_cast<long long>(blk) * kBlock + k * 16) =
+                *reinterpret_cast<const uint4 *>(out + col * kPitch + k * 16);
+    }
 }
 
 // ---- 128 x 128 tiles (weights), written as they lie, transposed, or both.
@@ -229,24 +294,20 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const Quan
         const int r = rt * kBlock + i * 16 + (threadIdx.x >> 4);
         v[i] = make_uint4(0, 0, 0, 0);
         if (r < p.n && c < p.cols) v[i] = load8(x + r * p.ldx, c, p.cols);
-        float f[8];
-        unpack8(v[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a = max(a, abs_bits(f[e]));
+        a = max2(a, max2(max2(abs2(v[i].x), abs2(v[i].y)), max2(abs2(v[i].z), abs2(v[i].w))));
     }
-    a = __reduce_max_sync(kAll, a);
+    a = __reduce_max_sync(kAll, max(a & 0xFFFFu, a >> 16));
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = a;
     __syncthreads();
     a = 0;
 #pragma unroll
     for (int w = 0; w < kTileThreads / 32; ++w) a = max(a, wmax[w]);
     const float amax = floor_amax(a);
+    const Divisor d = divisor(amax);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int rl = i * 16 + (threadIdx.x >> 4), r = rt * kBlock + rl;
-        float f[8];
-        unpack8(v[i], f);
-        const uint2 q = quantize8(f, amax);
+        const uint2 q = quantize8(v[i], d);
         if (p.q && r < p.n && c < p.cols) store_q8(p.q + g * p.qg + r * p.ldq, c, p.cols, q);
         uint32_t *t = reinterpret_cast<uint32_t *>(&tq[rl][(threadIdx.x & 15) * 8]);
         t[0] = q.x;

@@ -16,9 +16,12 @@
 // Which expert is chosen is a discrete question, so FP32 rounding must not
 // decide it. Choices are compared in FP32, where each carries an error of a
 // few units in the last place; when two neighbours of the chosen order (or
-// the last kept and the first dropped group) are closer than kNear times
-// their size, the warp repeats the choice in FP64. Neighbours with equal
-// logits and equal bias are exact ties and need no repeat.
+// the last kept and the first dropped group) are closer than FP32's
+// error bound, the warp repeats the choice in FP64. Neighbours with equal
+// logits and equal bias are exact ties and need no repeat. On 8192 tokens of
+// 256 experts with random logits about one row in a thousand repeats (at
+// 4e-6 for both scores, one in a hundred, and the FP64 units then took most
+// of the launch's 45 us).
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -26,7 +29,11 @@ namespace deto {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr float kNear = 4e-6f;       // > the FP32 errors of two scores and their sums (below 40 * 2^-24 of their size)
+// Bounds of the FP32 errors of two choices, relative to their scores' and
+// biases' sizes. A sigmoid: one unit of expf, an addition, a division and the
+// bias, below 8 * 2^-24 for both; a softmax adds its sum's rounding, common
+// to all choices of a row but not to their biases, below 40 * 2^-24.
+constexpr float kNearSigmoid = 6e-7f, kNearSoftmax = 4e-6f;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -115,7 +122,8 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const F *v
         const F size2 = (val < 0 ? -val : val) + (next < 0 ? -next : next);
         // A value is at most the sum of two choices, each of a score of at
         // most 1 and a bias; the bias can cancel the score, hence the 1.
-        if (!(d > static_cast<F>(kNear) * (p.bias ? size2 + static_cast<F>(1) : size2))) near = true;
+        const F bound = static_cast<F>(p.sigmoid ? kNearSigmoid : kNearSoftmax);
+        if (!(d > bound * (p.bias ? size2 + static_cast<F>(1) : size2))) near = true;
     }
     const uint32_t lanes = __ballot_sync(kAll, kept);
     near = __any_sync(kAll, near);
@@ -265,8 +273,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 
     // The k largest keys in order; with a bias one more, to see how close
     // the first that lost came.
-    int mine = -1;
-    uint32_t my_key = 0;
+    int mine = -1, lost = -1;
+    uint32_t my_key = 0, lost_key = 0;
     const int take = p.bias ? p.k + 1 : p.k;
     for (int j = 0; j < take; ++j) {
         uint32_t best = 0;
@@ -283,24 +291,33 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (i * 32 + lane == e) key[i] = 0;
-        if (p.bias) {
-            // rank j is compared with rank j - 1
-            const uint32_t pk = __shfl_sync(kAll, my_key, (j + 31) & 31);
-            const int pe = __shfl_sync(kAll, mine, (j + 31) & 31);
-            if (j > 0) {
-                const float hi = __uint_as_float((pk & 0x80000000u) ? pk & 0x7FFFFFFFu : ~pk);
-                const float lo = __uint_as_float((m & 0x80000000u) ? m & 0x7FFFFFFFu : ~m);
-                const float bh = p.bias[pe], bl = p.bias[e];
-                const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
-                if (!(hi - lo > kNear * size) &&
-                    !(bh == bl && logit_at<FP32>(p, t, pe) == logit_at<FP32>(p, t, e)))
-                    near = true;
-            }
+        if (j == p.k) {
+            lost = e;
+            lost_key = m;
         }
         if (j < p.k && lane == j) {
             mine = e;
             my_key = m;
         }
+    }
+    if (p.bias) {
+        // Each choice against the next one (the last against the best that lost).
+        int ne = __shfl_down_sync(kAll, mine, 1);
+        uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
+        if (lane == p.k - 1) {
+            ne = lost;
+            nk = lost_key;
+        }
+        if (lane < p.k && mine >= 0 && ne >= 0) {
+            const float hi = __uint_as_float((my_key & 0x80000000u) ? my_key & 0x7FFFFFFFu : ~my_key);
+            const float lo = __uint_as_float((nk & 0x80000000u) ? nk & 0x7FFFFFFFu : ~nk);
+            const float bh = p.bias[mine], bl = p.bias[ne];
+            const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
+            if (!(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
+                !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne)))
+                near = true;
+        }
+        near = __any_sync(kAll, near);
     }
     if (near) mine = choose_fp64<FP32>(p, t, lane, top, vd);
 
