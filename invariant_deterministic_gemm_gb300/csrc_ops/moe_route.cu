@@ -17,11 +17,14 @@
 // decide it. Choices are compared in FP32, where each carries an error of a
 // few units in the last place; when two neighbours of the chosen order (or
 // the last kept and the first dropped group) are closer than FP32's
-// error bound, the warp repeats the choice in FP64. Neighbours with equal
+// error bound, the warp decides again: the few candidates near the last
+// choice in FP64, one a lane, when only their order is in doubt; every expert
+// with pairs of FP32 values (about 43 bits), or in FP64 where a score is too
+// small for those, when a group is. Neighbours with equal
 // logits and equal bias are exact ties and need no repeat. On 8192 tokens of
-// 256 experts with random logits about one row in a thousand repeats (at
-// 4e-6 for both scores, one in a hundred, and the FP64 units then took most
-// of the launch's 45 us).
+// 256 experts with random logits about one row in a thousand decides
+// again; with FP64 for every expert of those, whose units are few, they took
+// 25 of the launch's 45 us.
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -30,8 +33,8 @@ namespace {
 
 constexpr int kWarps = 8;
 // Bounds of the FP32 errors of two choices, relative to their scores' and
-// biases' sizes. A sigmoid: one unit of expf, an addition, a division and the
-// bias, below 8 * 2^-24 for both; a softmax adds its sum's rounding, common
+// biases' sizes. A sigmoid: one unit of expf, an addition, a reciprocal of one
+// unit and the bias, below 8 * 2^-24; a softmax adds its sum's rounding, common
 // to all choices of a row but not to their biases, below 40 * 2^-24.
 constexpr float kNearSigmoid = 6e-7f, kNearSoftmax = 4e-6f;
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -62,6 +65,14 @@ __device__ __forceinline__ F warp_sum(F v)
 
 __device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
 
+// The same within one more unit, for the choice (a reciprocal of one unit's error).
+__device__ __forceinline__ float sigmoid_choice(float l)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-l)));
+    return r;
+}
+
 // Order-preserving map of a float; 0 is left for "not a candidate".
 __device__ __forceinline__ uint32_t order_key(float c)
 {
@@ -77,13 +88,117 @@ __device__ __forceinline__ int lanes_per_group(int groups)
     return l;
 }
 
+// ---- pairs of FP32 values: hi + lo, |lo| at most half a unit of hi (the sums
+// and products of Dekker and Knuth, each operation rounded on its own).
+struct Df {
+    float hi, lo;
+};
+__device__ __forceinline__ Df quick_sum(float a, float b)    // |a| >= |b|
+{
+    const float s = __fadd_rn(a, b);
+    return Df{s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Df two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    return Df{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ Df operator+(const Df &a, const Df &b)
+{
+    Df s = two_sum(a.hi, b.hi);
+    const Df t = two_sum(a.lo, b.lo);
+    s = quick_sum(s.hi, __fadd_rn(s.lo, t.hi));
+    return quick_sum(s.hi, __fadd_rn(s.lo, t.lo));
+}
+__device__ __forceinline__ Df operator*(const Df &a, const Df &b)
+{
+    const float p = __fmul_rn(a.hi, b.hi);
+    const float e = __fmaf_rn(a.hi, b.hi, -p);
+    return quick_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, e)));
+}
+// Quotient by three corrected steps; no branches, so that independent ones overlap.
+__device__ __forceinline__ Df operator/(const Df &a, const Df &b)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b.hi));
+    const float q1 = __fmul_rn(a.hi, r);
+    Df d = a + Df{-q1, 0.0f} * b;
+    const float q2 = __fmul_rn(d.hi, r);
+    d = d + Df{-q2, 0.0f} * b;
+    return quick_sum(q1, q2) + Df{__fmul_rn(d.hi, r), 0.0f};
+}
+__device__ __forceinline__ bool operator>(const Df &a, const Df &b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ bool operator<(const Df &a, const Df &b) { return b > a; }
+__device__ __forceinline__ bool operator==(const Df &a, const Df &b) { return a.hi == b.hi && a.lo == b.lo; }
+
+constexpr Df split(double v)
+{
+    return Df{static_cast<float>(v), static_cast<float>(v - static_cast<double>(static_cast<float>(v)))};
+}
+
+// exp of x in [-60, 60]: x = n ln 2 + r, |r| <= 0.347, and the exponential
+// series of r up to r^12 / 12! (the next term is below 2^-52), its first terms
+// in pairs and those below 2^-23 in FP32. Relative error about 2^-44.
+__device__ __forceinline__ Df exp_df(const Df &x)
+{
+    constexpr Df ln2 = split(0.69314718055994530942);
+    const float n = rintf(x.hi * 1.44269504f);
+    const Df r = x + Df{-n, 0.0f} * ln2;
+    const float t = r.hi;
+    float high = 1.0f / 479001600.0f;
+    high = __fmaf_rn(high, t, 1.0f / 39916800.0f);
+    high = __fmaf_rn(high, t, 1.0f / 3628800.0f);
+    high = __fmaf_rn(high, t, 1.0f / 362880.0f);
+    high = __fmaf_rn(high, t, 1.0f / 40320.0f);
+    high = __fmaf_rn(high, t, 1.0f / 5040.0f);
+    constexpr Df c6 = split(1.0 / 720.0), c5 = split(1.0 / 120.0), c4 = split(1.0 / 24.0), c3 = split(1.0 / 6.0);
+    Df e = Df{high, 0.0f} * r + c6;
+    e = e * r + c5;
+    e = e * r + c4;
+    e = e * r + c3;
+    e = e * r + Df{0.5f, 0.0f};
+    e = e * r + Df{1.0f, 0.0f};
+    e = e * r + Df{1.0f, 0.0f};
+    const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);
+    return Df{e.hi * scale, e.lo * scale};
+}
+
+// The value types the choice runs in.
+template <typename F>
+struct Num;
+template <>
+struct Num<float> {
+    static __device__ __forceinline__ float of(float v) { return v; }
+    static __device__ __forceinline__ float shfl(float v, int l) { return __shfl_sync(kAll, v, l); }
+    static __device__ __forceinline__ float shfl_xor(float v, int o) { return __shfl_xor_sync(kAll, v, o); }
+};
+template <>
+struct Num<double> {
+    static __device__ __forceinline__ double of(float v) { return v; }
+    static __device__ __forceinline__ double shfl(double v, int l) { return __shfl_sync(kAll, v, l); }
+    static __device__ __forceinline__ double shfl_xor(double v, int o) { return __shfl_xor_sync(kAll, v, o); }
+    static __device__ __forceinline__ double expd(float a, float b) { return exp(static_cast<double>(a) - static_cast<double>(b)); }
+};
+template <>
+struct Num<Df> {
+    static __device__ __forceinline__ Df of(float v) { return Df{v, 0.0f}; }
+    static __device__ __forceinline__ Df shfl(Df v, int l) { return Df{__shfl_sync(kAll, v.hi, l), __shfl_sync(kAll, v.lo, l)}; }
+    static __device__ __forceinline__ Df shfl_xor(Df v, int o)
+    {
+        return Df{__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)};
+    }
+    static __device__ __forceinline__ Df expd(float a, float b) { return exp_df(two_sum(a, -b)); }     // exp(a - b)
+};
+
 // Best groups of a token: v[e] are the experts' values in shared memory
-// (-inf: masked). Returns a bit mask of the kept groups; `near` is set when
-// the border between kept and dropped groups is closer than rounding error.
+// (-inf: masked). Returns a bit mask of the kept groups; `near` (FP32 only) is
+// set when the border between kept and dropped groups is closer than rounding
+// error.
 template <typename F>
 __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const F *v, int lane, bool &near)
 {
-    const F ninf = static_cast<F>(neg_inf());
+    using N = Num<F>;
+    const F ninf = N::of(neg_inf());
     const int size = p.experts / p.groups;
     const int lpg = lanes_per_group(p.groups);
     const int g = lane / lpg, sub = lane % lpg;
@@ -100,7 +215,7 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const F *v
         }
     }
     for (int o = 1; o < lpg; o <<= 1) {
-        const F a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        const F a2 = N::shfl_xor(a, o), b2 = N::shfl_xor(b, o);
         const F lo = a < a2 ? a : a2;
         a = a < a2 ? a2 : a;
         b = b < b2 ? b2 : b;
@@ -111,57 +226,60 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const F *v
     int rank = 0;
     F next = ninf;                                    // best value ranked below this group
     for (int h = 0; h < p.groups; ++h) {
-        const F o = __shfl_sync(kAll, val, h * lpg);
+        const F o = N::shfl(val, h * lpg);
         const bool before = o > val || (o == val && h < g);
         rank += before ? 1 : 0;
         if (!before && h != g && o > next) next = o;
     }
     const bool kept = g < p.groups && sub == 0 && rank < p.top_groups && val > ninf;
-    if (kept && rank == p.top_groups - 1 && next > ninf) {
-        const F d = val - next;
-        const F size2 = (val < 0 ? -val : val) + (next < 0 ? -next : next);
-        // A value is at most the sum of two choices, each of a score of at
-        // most 1 and a bias; the bias can cancel the score, hence the 1.
-        const F bound = static_cast<F>(p.sigmoid ? kNearSigmoid : kNearSoftmax);
-        if (!(d > bound * (p.bias ? size2 + static_cast<F>(1) : size2))) near = true;
+    if constexpr (sizeof(F) == 4) {
+        if (kept && rank == p.top_groups - 1 && next > ninf) {
+            // A value is at most the sum of two choices, each of a score of
+            // at most 1 and a bias; the bias can cancel the score, hence the 1.
+            const float size2 = fabsf(val) + fabsf(next) + (p.bias ? 1.0f : 0.0f);
+            if (!(val - next > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size2)) near = true;
+        }
+        near = __any_sync(kAll, near);
     }
     const uint32_t lanes = __ballot_sync(kAll, kept);
-    near = __any_sync(kAll, near);
     uint32_t mask = 0;
     for (int h = 0; h < p.groups; ++h) mask |= ((lanes >> (h * lpg)) & 1u) << h;
     return mask;
 }
 
-// The choice in FP64, for the few rows FP32 cannot decide. Returns the
-// chosen expert of rank `lane` (-1: none).
-template <bool FP32>
-__device__ __noinline__ int choose_fp64(const RouteParams &p, int t, int lane, float top, double *v)
+// The choice with values of type F, for the few rows FP32 cannot decide.
+// Returns the chosen expert of rank `lane` (-1: none).
+template <bool FP32, typename F>
+__device__ __noinline__ int choose_again(const RouteParams &p, int t, int lane, float top, F *v)
 {
-    const double ninf = static_cast<double>(neg_inf());
-    double sum = 1.0;
+    using N = Num<F>;
+    const F ninf = N::of(neg_inf()), one = N::of(1.0f);
+    const bool sig = p.sigmoid;
+    F sum = one;
     if (!p.sigmoid) {
-        sum = 0.0;
+        sum = N::of(0.0f);
         for (int e = lane; e < p.experts; e += 32) {
             const float l = logit_at<FP32>(p, t, e);
-            if (l > neg_inf()) sum += exp(static_cast<double>(l) - static_cast<double>(top));
+            if (l > neg_inf()) sum = sum + N::expd(l, top);
         }
-        sum = warp_sum(sum);
+        for (int o = 16; o > 0; o >>= 1) sum = sum + N::shfl_xor(sum, o);
     }
-    for (int e = lane; e < p.experts; e += 32) {
-        const float l = logit_at<FP32>(p, t, e);
-        double c = ninf;
-        if (l > neg_inf()) {
-            c = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
-                          : exp(static_cast<double>(l) - static_cast<double>(top)) / sum;
-            if (p.bias) c += static_cast<double>(p.bias[e]);
-            if (!(c > ninf)) c = ninf;
-        }
-        v[e] = c;
+    // Four experts of a lane at a time: one chain of these operations waits
+    // for itself most of the time, and this warp is the launch's last.
+#pragma unroll 4
+    for (int e0 = 0; e0 < p.experts; e0 += 32) {
+        const int e = min(e0 + lane, p.experts - 1);
+        const float l = logit_at<FP32>(p, t, e), bias = p.bias ? p.bias[e] : 0.0f;
+        const bool in = l > neg_inf() && bias > neg_inf();
+        const F x = N::expd(sig ? 0.0f : in ? l : top, sig ? (in ? l : 0.0f) : top);
+        F c = (sig ? one : x) / (sig ? one + x : sum);
+        if (p.bias) c = c + N::of(bias);
+        if (e0 + lane < p.experts) v[e] = in ? c : ninf;
     }
     __syncwarp();
     if (p.groups > 1) {
         bool near = false;
-        const uint32_t kept = keep_groups<double>(p, v, lane, near);
+        const uint32_t kept = keep_groups<F>(p, v, lane, near);
         const int size = p.experts / p.groups;
         __syncwarp();
         for (int e = lane; e < p.experts; e += 32)
@@ -170,12 +288,12 @@ __device__ __noinline__ int choose_fp64(const RouteParams &p, int t, int lane, f
     }
     if (!p.bias) {                   // without a bias the logits give the order
         for (int e = lane; e < p.experts; e += 32)
-            if (v[e] > ninf) v[e] = static_cast<double>(logit_at<FP32>(p, t, e));
+            if (v[e] > ninf) v[e] = N::of(logit_at<FP32>(p, t, e));
         __syncwarp();
     }
     int mine = -1;
     for (int j = 0; j < p.k; ++j) {
-        double best = ninf;
+        F best = ninf;
         int at = p.experts;
         for (int e = lane; e < p.experts; e += 32)
             if (v[e] > best) {
@@ -184,7 +302,7 @@ __device__ __noinline__ int choose_fp64(const RouteParams &p, int t, int lane, f
             }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const double b2 = __shfl_xor_sync(kAll, best, o);
+            const F b2 = N::shfl_xor(best, o);
             const int a2 = __shfl_xor_sync(kAll, at, o);
             if (b2 > best || (b2 == best && a2 < at)) {
                 best = b2;
@@ -199,15 +317,45 @@ __device__ __noinline__ int choose_fp64(const RouteParams &p, int t, int lane, f
     return mine;
 }
 
+// The order of a few candidates in FP64, one for each of the first `count`
+// lanes (list[lane].y). Leaves the chosen in list[0 .. min(count, k)).y.
+template <bool FP32>
+__device__ __noinline__ void order_candidates(const RouteParams &p, int t, int lane, float top, uint2 *list, int count)
+{
+    double sum = 1.0;
+    if (!p.sigmoid) {
+        sum = 0.0;
+        for (int e = lane; e < p.experts; e += 32) {
+            const float l = logit_at<FP32>(p, t, e);
+            if (l > neg_inf()) sum += exp(static_cast<double>(l) - static_cast<double>(top));
+        }
+        sum = warp_sum(sum);
+    }
+    const int e = static_cast<int>(list[min(lane, count - 1)].y);
+    const double l = static_cast<double>(logit_at<FP32>(p, t, e));
+    const double c = (p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - static_cast<double>(top)) / sum) + static_cast<double>(p.bias[e]);
+    int rank = 0;
+    for (int o = 0; o < count; ++o) {
+        const double d = __shfl_sync(kAll, c, o);
+        const int f = __shfl_sync(kAll, e, o);
+        rank += (d > c || (d == c && f < e)) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < count) list[rank].y = static_cast<uint32_t>(e);
+    __syncwarp();
+}
+
 // Shared memory per warp: `experts` doubles, used as floats for the group
 // values and as doubles by the FP64 repeat.
 template <bool FP32, int PER>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 {
     extern __shared__ double route_smem[];
+    __shared__ uint2 gather_smem[kWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kWarps + warp;
     if (t >= p.tokens) return;
+    uint2 *gathered = gather_smem[warp];
     double *vd = route_smem + warp * p.experts;
     float *vf = reinterpret_cast<float *>(vd);
 
@@ -241,7 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             const int e = i * 32 + lane;
             c[i] = neg_inf();
             if (l[i] > neg_inf()) {
-                c[i] = p.sigmoid ? sigmoid(l[i]) : __fdiv_rn(expf(l[i] - top), total);
+                c[i] = p.sigmoid ? sigmoid_choice(l[i]) : __fdiv_rn(expf(l[i] - top), total);
                 if (p.bias) c[i] += p.bias[e];
                 if (!(c[i] > neg_inf())) {
                     c[i] = neg_inf();
@@ -271,35 +419,95 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
         for (int i = 0; i < PER; ++i) key[i] = l[i] > neg_inf() ? order_key(l[i]) : 0u;
     }
 
-    // The k largest keys in order; with a bias one more, to see how close
-    // the first that lost came.
+    // The k largest keys in order; with a bias one more, to see how close the
+    // first that lost came. The take-th largest of the lanes' own maxima
+    // bounds the take-th largest of all from below; the few keys that reach
+    // it are gathered, one for each lane, and each counts those before it.
+    // (One warp-wide maximum after the other over all keys took 60
+    // instructions a choice.)
     int mine = -1, lost = -1;
     uint32_t my_key = 0, lost_key = 0;
     const int take = p.bias ? p.k + 1 : p.k;
-    for (int j = 0; j < take; ++j) {
-        uint32_t best = 0;
-        int at = 0;
+    bool emptied = false;            // the keys have been used up
+    uint32_t own = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i * 32 + lane;
+    for (int i = 0; i < PER; ++i) own = max(own, key[i]);
+    uint32_t bound = 1;
+    {
+        uint32_t left = own;
+        for (int j = 0; j < take; ++j) {
+            const uint32_t m = __reduce_max_sync(kAll, left);
+            if (m == 0) {
+                bound = 1;
+                break;
             }
-        const uint32_t m = __reduce_max_sync(kAll, best);
-        if (m == 0) break;
-        const int e = static_cast<int>(__reduce_min_sync(kAll, best == m ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (i * 32 + lane == e) key[i] = 0;
-        if (j == p.k) {
-            lost = e;
-            lost_key = m;
-        }
-        if (j < p.k && lane == j) {
-            mine = e;
-            my_key = m;
+            bound = m;
+            if (left == m) left = 0;                  // equal maxima go together: the bound only gets lower
         }
     }
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = key[i] >= bound;
+        const unsigned who = __ballot_sync(kAll, in);
+        const int at = count + __popc(who & ((1u << lane) - 1u));
+        if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+        count += __popc(who);
+    }
+    __syncwarp();
+    if (count <= 32) {
+        const uint2 c = lane < count ? gathered[lane] : make_uint2(0, 0);
+        __syncwarp();
+        int rank = 0;
+        for (int o = 0; o < count; ++o) {
+            const uint2 d = gathered[o];
+            rank += (d.x > c.x || (d.x == c.x && d.y < c.y)) ? 1 : 0;
+        }
+        __syncwarp();
+        if (lane < count && rank < 32) gathered[rank] = c;
+        __syncwarp();
+        const int n = min(count, p.k);
+        if (lane < n) {
+            my_key = gathered[lane].x;
+            mine = static_cast<int>(gathered[lane].y);
+        }
+        if (p.bias && count > p.k) {
+            if (p.k < 32) {
+                lost_key = gathered[p.k].x;
+                lost = static_cast<int>(gathered[p.k].y);
+            } else {
+                near = true;                          // 32 choices leave no lane for the one that lost
+            }
+        }
+    } else {
+        // Many keys reach the bound (ties, or many choices): one after the other.
+        emptied = true;
+        for (int j = 0; j < take; ++j) {
+            uint32_t best = 0;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = i * 32 + lane;
+                }
+            const uint32_t m = __reduce_max_sync(kAll, best);
+            if (m == 0) break;
+            const int e = static_cast<int>(__reduce_min_sync(kAll, best == m ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i * 32 + lane == e) key[i] = 0;
+            if (j == p.k) {
+                lost = e;
+                lost_key = m;
+            }
+            if (j < p.k && lane == j) {
+                mine = e;
+                my_key = m;
+            }
+        }
+    }
+    bool close = false;              // two neighbours of the choice's order cannot be told apart
     if (p.bias) {
         // Each choice against the next one (the last against the best that lost).
         int ne = __shfl_down_sync(kAll, mine, 1);
@@ -315,11 +523,48 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
             if (!(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
                 !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne)))
-                near = true;
+                close = true;
         }
-        near = __any_sync(kAll, near);
+        close = __any_sync(kAll, close);
     }
-    if (near) mine = choose_fp64<FP32>(p, t, lane, top, vd);
+    if (close && !near && !emptied) {
+        // The groups stand; whatever may lie above the last choice is put in
+        // order again: c >= the last choice less both errors (a score is at
+        // most 1, so the other's bias is at most 1 + |c| in size).
+        const int last = __shfl_sync(kAll, mine, p.k - 1);
+        uint32_t bound2 = 1;
+        if (last >= 0) {
+            const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
+            const float c = __uint_as_float((lk & 0x80000000u) ? lk & 0x7FFFFFFFu : ~lk);
+            bound2 = order_key(c - (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (fabsf(p.bias[last]) + 3.0f * fabsf(c) + 2.0f));
+        }
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool in = key[i] >= bound2 && key[i] != 0;
+            const unsigned who = __ballot_sync(kAll, in);
+            const int at = n + __popc(who & ((1u << lane) - 1u));
+            if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+            n += __popc(who);
+        }
+        __syncwarp();
+        if (n <= 32) {
+            order_candidates<FP32>(p, t, lane, top, gathered, n);
+            mine = lane < min(n, p.k) ? static_cast<int>(gathered[lane].y) : -1;
+            close = false;
+        }
+    }
+    near = near || close;
+    if (near) {
+        // exp's arguments: -l, or l - top. Pairs of FP32 values hold what exp
+        // gives between -60 and 60.
+        bool far = false;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (l[i] > neg_inf()) far |= !(fabsf(p.sigmoid ? l[i] : l[i] - top) < 60.0f);
+        if (__any_sync(kAll, far)) mine = choose_again<FP32, double>(p, t, lane, top, vd);
+        else mine = choose_again<FP32, Df>(p, t, lane, top, reinterpret_cast<Df *>(vd));
+    }
 
     // Weights, FP32: lane j holds choice j.
     const float lj = mine >= 0 ? logit_at<FP32>(p, t, mine) : neg_inf();
