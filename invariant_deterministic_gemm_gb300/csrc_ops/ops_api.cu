@@ -278,6 +278,8 @@ det_gemm_status fp8_rows(const uint8_t *A, const float *sa, const uint8_t *W, co
     return enqueue(x, p, plan_rows(M, N, G, grouped, d->sms), d, stream);
 }
 
+constexpr int64_t kZeroBeside = 64 << 20;    // bytes of the dense gradient zeroed while the tokens are sorted
+
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct GradSpace {
@@ -702,6 +704,13 @@ det_gemm_status det_embedding_grad(const det_gemm_bf16 *dy, const void *tokens, 
         p.ibuf[i] = reinterpret_cast<int32_t *>(w + g.idx[i]);
     }
     p.head = reinterpret_cast<int32_t *>(w + g.head);
+    if (!accumulate) {
+        p.zero = dtable;
+        p.zero_rows = std::min<int64_t>(V, kZeroBeside / (H * ds));
+        p.zero_cols = H * ds;
+        p.zero_pitch = ldd * ds;
+    }
+    p.sms = d->sms;
     p.seen = w + g.seen;
     p.skip_key = static_cast<int>(padding_idx);
     p.status = d->word;
@@ -724,6 +733,7 @@ det_gemm_status det_embedding_grad(const det_gemm_bf16 *dy, const void *tokens, 
     q.order = p.ibuf[(p.passes - 1) & 1];
     q.head = p.head;
     q.seen = p.seen;
+    q.zero_from = static_cast<int>(accumulate ? V : p.zero_rows);
     q.partials = reinterpret_cast<float *>(w + g.partials);
     q.ldp = g.ldp;
     e = launch_embedding_grad(q, cs(stream));

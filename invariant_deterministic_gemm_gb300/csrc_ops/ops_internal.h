@@ -42,7 +42,10 @@ struct SortParams {
     // runs: sorted keys and their original indexes, each position's run head, and which keys occur
     int32_t *kbuf[2], *ibuf[2];      // [n] each; the last pass leaves its result in buffer (passes - 1) & 1
     int32_t *head;
-    uint8_t *seen;                   // [range]
+    uint8_t *seen;                   // [range], rounded up to 16
+    void *zero;                      // rows to zero meanwhile: zero_rows of zero_cols bytes, zero_pitch bytes apart
+    long long zero_rows, zero_cols, zero_pitch;
+    int sms;
     int skip_key;                    // a key treated as out of range (or -1)
     int *status;
     int flag_bad;                    // report keys outside [0, range)
@@ -92,6 +95,7 @@ struct EmbedGradParams {
     int accumulate, fp32;
     const int32_t *keys, *order, *head;
     const uint8_t *seen;
+    int zero_from;                   // rows from here on that never occur are zeroed
     float *partials;                 // [2 * ceil(n / 32), cols rounded up to 8]
     long long ldp;
 };
