@@ -3,7 +3,9 @@
 Each .cu file under csrc/ (det_gemm) and csrc_ops/ (the mixture-of-experts
 operators) is compiled in parallel to an object under ``_build/`` and the objects are linked into ``libdet_gemm.so`` next to this
 file. The CUDA runtime is linked statically, so the library has no load-time
-dependency on libcuda (the driver is reached at run time).
+dependency on libcuda (the driver is reached at run time). The native half of
+_ops.py (binding/) is built beside it as a Python extension against the
+installed PyTorch.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC_OPS = os.path.join(PKG, "csrc_ops")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdet_gemm.so")
+BINDING = os.path.join(PKG, "binding", "ops_native.cpp")
+NATIVE = os.path.join(PKG, "_ops_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -60,29 +65,59 @@ def _compile(src: str, verbose: bool, ptxas_info: bool) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile (if stale) and link libdet_gemm.so; returns its path."""
-    srcs = sources()
-    deps = srcs + headers()
-    if not force and not ptxas_info and not _stale(LIB, deps):
-        return LIB
-    os.makedirs(OBJDIR, exist_ok=True)
-    logs = []
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
-        futs = [ex.submit(_compile, s, verbose, ptxas_info) for s in srcs]
-        objs = []
-        for f in futs:
-            o, log = f.result()
-            objs.append(o)
-            logs.append(log)
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc(), "-shared", *ARCH, "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
+def _compile_binding(verbose: bool) -> str:
+    """Compile the Python extension's object (g++, against PyTorch's headers)."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJDIR, "ops_native.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE, "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"], "-c", BINDING, "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed for %s:\n%s\n%s" % (cmd[0], BINDING, r.stdout, r.stderr))
+    return obj
+
+
+def _link(cmd: list[str], target: str, verbose: bool) -> None:
+    """Run a link command whose output goes to a temporary name, then put it in place."""
+    tmp = target + ".tmp.%d" % os.getpid()
+    cmd = [tmp if c is None else c for c in cmd]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB)
+    os.replace(tmp, target)
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile (if stale) and link libdet_gemm.so and the binding; returns the library's path."""
+    srcs = sources()
+    stale = force or ptxas_info or _stale(LIB, srcs + headers())
+    native = force or stale or _stale(NATIVE, [BINDING, os.path.join(INCLUDE, "det_ops.h"), os.path.join(INCLUDE, "det_gemm.h")])
+    if not stale and not native:
+        return LIB
+    os.makedirs(OBJDIR, exist_ok=True)
+    logs, objs = [], []
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding, verbose) if native else None
+        for f in [ex.submit(_compile, s, verbose, ptxas_info) for s in srcs] if stale else []:
+            o, log = f.result()
+            objs.append(o)
+            logs.append(log)
+        if stale:
+            _link([nvcc(), "-shared", *ARCH, "-o", None, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"], LIB, verbose)
+        if native:
+            import torch
+            tl = os.path.join(os.path.dirname(torch.__file__), "lib")
+            _link([os.environ.get("CXX", "g++"), "-shared", "-o", None, binding.result(), "-L", PKG, "-l:libdet_gemm.so",
+                   "-L", tl, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ltorch",
+                   "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + tl], NATIVE, verbose)
     if ptxas_info:
         sys.stdout.write("".join(logs))
     return LIB
