@@ -136,31 +136,50 @@ constexpr Df split(double v)
     return Df{static_cast<float>(v), static_cast<float>(v - static_cast<double>(static_cast<float>(v)))};
 }
 
-// exp of x in [-60, 60]: x = n ln 2 + r, |r| <= 0.347, and the exponential
-// series of r up to r^12 / 12! (the next term is below 2^-52), its first terms
-// in pairs and those below 2^-23 in FP32. Relative error about 2^-44.
-__device__ __forceinline__ Df exp_df(const Df &x)
+// exp of N values in [-60, 60]: x = n ln 2 + r, |r| <= 0.347, and the
+// exponential series of r up to r^12 / 12! (the next term is below 2^-52), its
+// first terms in pairs and those below 2^-23 in FP32. Relative error about
+// 2^-43. The N values go side by side, so that one's operations fill another's
+// latency, and the terms are a loop, so that the code stays small.
+__constant__ float g_series[6] = {1.0f / 479001600.0f, 1.0f / 39916800.0f, 1.0f / 3628800.0f, 1.0f / 362880.0f, 1.0f / 40320.0f,
+                                  1.0f / 5040.0f};
+__constant__ Df g_terms[7] = {split(1.0 / 720.0), split(1.0 / 120.0), split(1.0 / 24.0), split(1.0 / 6.0), Df{0.5f, 0.0f},
+                              Df{1.0f, 0.0f}, Df{1.0f, 0.0f}};
+
+template <int N>
+__device__ __forceinline__ void exp_all(Df (&x)[N])
 {
     constexpr Df ln2 = split(0.69314718055994530942);
-    const float n = rintf(x.hi * 1.44269504f);
-    const Df r = x + Df{-n, 0.0f} * ln2;
-    const float t = r.hi;
-    float high = 1.0f / 479001600.0f;
-    high = __fmaf_rn(high, t, 1.0f / 39916800.0f);
-    high = __fmaf_rn(high, t, 1.0f / 3628800.0f);
-    high = __fmaf_rn(high, t, 1.0f / 362880.0f);
-    high = __fmaf_rn(high, t, 1.0f / 40320.0f);
-    high = __fmaf_rn(high, t, 1.0f / 5040.0f);
-    constexpr Df c6 = split(1.0 / 720.0), c5 = split(1.0 / 120.0), c4 = split(1.0 / 24.0), c3 = split(1.0 / 6.0);
-    Df e = Df{high, 0.0f} * r + c6;
-    e = e * r + c5;
-    e = e * r + c4;
-    e = e * r + c3;
-    e = e * r + Df{0.5f, 0.0f};
-    e = e * r + Df{1.0f, 0.0f};
-    e = e * r + Df{1.0f, 0.0f};
-    const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);
-    return Df{e.hi * scale, e.lo * scale};
+    float n[N];
+    Df r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        n[i] = rintf(x[i].hi * 1.44269504f);
+        r[i] = x[i] + Df{-n[i], 0.0f} * ln2;
+        x[i] = Df{g_series[0], 0.0f};
+    }
+#pragma unroll 1
+    for (int k = 1; k < 6; ++k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i].hi = __fmaf_rn(x[i].hi, r[i].hi, g_series[k]);
+    }
+#pragma unroll 1
+    for (int k = 0; k < 7; ++k) {
+        const Df c = g_terms[k];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = x[i] * r[i] + c;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float scale = __int_as_float((static_cast<int>(n[i]) + 127) << 23);
+        x[i] = Df{x[i].hi * scale, x[i].lo * scale};
+    }
+}
+template <int N>
+__device__ __forceinline__ void exp_all(double (&x)[N])
+{
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) x[i] = exp(x[i]);
 }
 
 // The value types the choice runs in.
@@ -177,7 +196,7 @@ struct Num<double> {
     static __device__ __forceinline__ double of(float v) { return v; }
     static __device__ __forceinline__ double shfl(double v, int l) { return __shfl_sync(kAll, v, l); }
     static __device__ __forceinline__ double shfl_xor(double v, int o) { return __shfl_xor_sync(kAll, v, o); }
-    static __device__ __forceinline__ double expd(float a, float b) { return exp(static_cast<double>(a) - static_cast<double>(b)); }
+    static __device__ __forceinline__ double diff(float a, float b) { return static_cast<double>(a) - static_cast<double>(b); }
 };
 template <>
 struct Num<Df> {
@@ -187,7 +206,7 @@ struct Num<Df> {
     {
         return Df{__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)};
     }
-    static __device__ __forceinline__ Df expd(float a, float b) { return exp_df(two_sum(a, -b)); }     // exp(a - b)
+    static __device__ __forceinline__ Df diff(float a, float b) { return two_sum(a, -b); }
 };
 
 // Best groups of a token: v[e] are the experts' values in shared memory
@@ -250,31 +269,48 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const F *v
 // The choice with values of type F, for the few rows FP32 cannot decide.
 // Returns the chosen expert of rank `lane` (-1: none).
 template <bool FP32, typename F>
-__device__ __noinline__ int choose_again(const RouteParams &p, int t, int lane, float top, F *v)
+__device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lane, float top, F *v)
 {
     using N = Num<F>;
     const F ninf = N::of(neg_inf()), one = N::of(1.0f);
     const bool sig = p.sigmoid;
-    F sum = one;
-    if (!p.sigmoid) {
-        sum = N::of(0.0f);
-        for (int e = lane; e < p.experts; e += 32) {
-            const float l = logit_at<FP32>(p, t, e);
-            if (l > neg_inf()) sum = sum + N::expd(l, top);
+    constexpr int B = 4;             // experts of a lane side by side
+    F sum = N::of(0.0f);
+    // First the exponentials (exp(-l), or exp(l - top) and their sum), then the choices.
+#pragma unroll 1
+    for (int e0 = 0; e0 < p.experts; e0 += 32 * B) {
+        F x[B];
+        bool in[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int e = e0 + 32 * i + lane;
+            const float l = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
+            in[i] = l > neg_inf();
+            x[i] = N::diff(sig ? 0.0f : in[i] ? l : top, sig ? (in[i] ? l : 0.0f) : top);
         }
-        for (int o = 16; o > 0; o >>= 1) sum = sum + N::shfl_xor(sum, o);
+        exp_all(x);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int e = e0 + 32 * i + lane;
+            if (e < p.experts) v[e] = in[i] ? x[i] : ninf;
+            if (in[i]) sum = sum + x[i];
+        }
     }
-    // Four experts of a lane at a time: one chain of these operations waits
-    // for itself most of the time, and this warp is the launch's last.
-#pragma unroll 4
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-        const int e = min(e0 + lane, p.experts - 1);
-        const float l = logit_at<FP32>(p, t, e), bias = p.bias ? p.bias[e] : 0.0f;
-        const bool in = l > neg_inf() && bias > neg_inf();
-        const F x = N::expd(sig ? 0.0f : in ? l : top, sig ? (in ? l : 0.0f) : top);
-        F c = (sig ? one : x) / (sig ? one + x : sum);
-        if (p.bias) c = c + N::of(bias);
-        if (e0 + lane < p.experts) v[e] = in ? c : ninf;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) sum = sum + N::shfl_xor(sum, o);
+#pragma unroll 1
+    for (int e0 = 0; e0 < p.experts; e0 += 32 * B) {
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int e = e0 + 32 * i + lane;
+            if (e >= p.experts) continue;
+            const F x = v[e];
+            const float bias = p.bias ? p.bias[e] : 0.0f;
+            const bool in = x > ninf && bias > neg_inf();
+            F c = (sig ? one : x) / (sig ? one + x : sum);
+            if (p.bias) c = c + N::of(bias);
+            v[e] = in ? c : ninf;
+        }
     }
     __syncwarp();
     if (p.groups > 1) {
@@ -292,6 +328,7 @@ __device__ __noinline__ int choose_again(const RouteParams &p, int t, int lane, 
         __syncwarp();
     }
     int mine = -1;
+#pragma unroll 1
     for (int j = 0; j < p.k; ++j) {
         F best = ninf;
         int at = p.experts;
@@ -320,7 +357,7 @@ __device__ __noinline__ int choose_again(const RouteParams &p, int t, int lane, 
 // The order of a few candidates in FP64, one for each of the first `count`
 // lanes (list[lane].y). Leaves the chosen in list[0 .. min(count, k)).y.
 template <bool FP32>
-__device__ __noinline__ void order_candidates(const RouteParams &p, int t, int lane, float top, uint2 *list, int count)
+__device__ __forceinline__ void order_candidates(const RouteParams &p, int t, int lane, float top, uint2 *list, int count)
 {
     double sum = 1.0;
     if (!p.sigmoid) {
@@ -348,7 +385,7 @@ __device__ __noinline__ void order_candidates(const RouteParams &p, int t, int l
 // Shared memory per warp: `experts` doubles, used as floats for the group
 // values and as doubles by the FP64 repeat.
 template <bool FP32, int PER>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p)
 {
     extern __shared__ double route_smem[];
     __shared__ uint2 gather_smem[kWarps][32];

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p, 
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        if (r0 + i < p.n) store8(p.dst + (r0 + i) * p.ldd, c, p.cols, v[i]);
+        if (r0 + i < p.n) store8_streaming(p.dst + (r0 + i) * p.ldd, c, p.cols, v[i]);
 }
 
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p, int col_blocks)
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const CombineP
                     dot = fmaf(a[e], b[e], dot);
                     o[e] = w * a[e];
                 }
-                store8(dys, c, p.cols, pack8(o));
+                store8_streaming(dys, c, p.cols, pack8(o));
             }
         }
 #pragma unroll

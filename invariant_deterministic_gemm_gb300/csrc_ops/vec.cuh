@@ -56,6 +56,13 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int cols, const uin
         if (c + i < cols) row[c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
 }
 
+// store8 for rows that this launch does not read again: they leave L2 first.
+__device__ __forceinline__ void store8_streaming(uint16_t *row, int c, int cols, const uint4 &v)
+{
+    if (c + 8 <= cols) __stcs(reinterpret_cast<uint4 *>(row + c), v);
+    else store8(row, c, cols, v);
+}
+
 __device__ __forceinline__ void store8f(float *row, int c, int cols, const float (&f)[8])
 {
     if (c + 8 <= cols) {
