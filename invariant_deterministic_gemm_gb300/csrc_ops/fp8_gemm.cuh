@@ -190,6 +190,12 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The launch in front of this one may be a quantiser, which lets this one set
+// itself up (barriers, TMEM, the groups' tiles) while it ends; any other kernel
+// does not. Its whole grid has to be done before an operand or a scale is read
+// and before the output is written. The group bounds cannot be its work.
+__device__ __forceinline__ void wait_for_quantiser() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A CTA's shared state besides the operand ring.
 struct Fp8Shared {
     uint64_t full[16], empty[16], accf[8], acce[8], drain[2], never;
@@ -319,30 +325,35 @@ __device__ __forceinline__ void store_chunk(const Fp8Params &p, long long at, in
 }
 
 // 32 rows x 64 bytes of the output from one warp: lane l's row as 16 words.
-// Through `buf` (2 KB of shared memory, 16-byte chunks swizzled by row), so
-// that a store instruction writes 64 contiguous bytes of eight rows.
+// Through `buf` (16 rows at a time, 16-byte chunks swizzled by row), so that a
+// store instruction writes 64 contiguous bytes of eight rows.
 template <bool F32>
 __device__ __forceinline__ void store_rows64(const Fp8Params &p, uint32_t buf, const uint32_t (&w)[16], int row0, int rows_end,
                                              long long base, int col, int lane)
 {
     constexpr int EPW = F32 ? 1 : 2;                 // elements a word
-    __syncwarp();                                    // the last use of buf is over
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16),
-                     "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
-                     : "memory");
-    __syncwarp();
+    for (int h = 0; h < 2; ++h) {
+        __syncwarp();                                // the last use of buf is over
+        if ((lane >> 4) == h) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), k = lane & 3;
-        uint32_t v[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                     : "r"(buf + r * 64 + ((k ^ (r >> 1)) & 3) * 16)
-                     : "memory");
-        const int c = col + k * 4 * EPW;
-        if (row0 + r < rows_end) store_chunk<F32>(p, base + (row0 + r) * p.ldo + c, c, v);
+            for (int k = 0; k < 4; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (lane & 15) * 64 + ((k ^ (lane >> 1)) & 3) * 16),
+                             "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                             : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * i + (lane >> 2), k = lane & 3;
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(buf + r * 64 + ((k ^ (r >> 1)) & 3) * 16)
+                         : "memory");
+            const int c = col + k * 4 * EPW, row = row0 + 16 * h + r;
+            if (row < rows_end) store_chunk<F32>(p, base + row * p.ldo + c, c, v);
+        }
     }
 }
 
@@ -401,13 +412,13 @@ __device__ __forceinline__ void zero_unowned(const Fp8Params &p, int thread, int
 
 // ------------------------------------------------------------- plain tile
 
-template <int BN>
+template <int KIND, int BN>
 struct PlainCfg {
     static constexpr int BM = 128;
     static constexpr int COLS = 64;                  // columns of a thread
     static constexpr int EPI_WARPS = BN / COLS * 4;
     static constexpr int THREADS = 32 * (EPI_WARPS + 4);
-    static constexpr int STAGES = BN == 192 ? 4 : 6;
+    static constexpr int STAGES = BN == 128 ? 6 : KIND == kFp8Rows ? 5 : 4;
     static constexpr int A_STAGE = BM * kBlock, B_STAGE = BN * kBlock;
     static constexpr int NACC = BN == 192 ? 2 : 4;
     static constexpr int OFF_B = STAGES * A_STAGE;
@@ -416,11 +427,14 @@ struct PlainCfg {
     // gradient, into a ring of each epilogue warp's rows' and columns' scales.
     static constexpr int kAhead = 4, SLOT = 32 + COLS;
     static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;       // [EPI_WARPS][kAhead][SLOT] floats
-    // A finished tile goes out through shared memory, 64 bytes of 32 rows a
-    // time and warp: written straight from the registers, every store
-    // touches 32 lines and a 192-wide tile takes 3000 cycles to leave.
-    static constexpr int OUT = 32 * 64;
-    static constexpr int OFF_OUT = OFF_SCALE + EPI_WARPS * kAhead * SLOT * 4;
+    // A finished tile goes out through shared memory, 64 bytes of OUT_ROWS rows
+    // a time and warp: written straight from the registers, every store
+    // touches 32 lines and a 192-wide tile takes 3000 cycles to leave. (Half
+    // the rows a time leaves room for a fifth stage where the scales need no
+    // ring: 356 -> 319 ns a block.)
+    static constexpr int OUT_ROWS = KIND == kFp8Rows ? 16 : 32;
+    static constexpr int OUT = OUT_ROWS * 64;
+    static constexpr int OFF_OUT = OFF_SCALE + (KIND == kFp8Wgrad ? EPI_WARPS * kAhead * SLOT * 4 : 0);
     static constexpr int OFF_SHARED = OFF_OUT + EPI_WARPS * OUT;
     static constexpr int BYTES = OFF_SHARED + static_cast<int>(sizeof(Fp8Shared));
     static constexpr int SMEM = BYTES + 1024;
@@ -438,12 +452,13 @@ struct PlainCfg {
 template <int KIND, bool F32, int BN>
 __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S, float *scale_smem, int warp, int lane)
 {
-    using C = PlainCfg<BN>;
+    using C = PlainCfg<KIND, BN>;
     const int q = warp & 3, part = warp >> 2;
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(q * 32) << 16) + part * C::COLS;
     const uint32_t ring = smem_u32(scale_smem + warp * C::kAhead * C::SLOT);
     const uint32_t out = smem_u32(scale_smem) + (C::OFF_OUT - C::OFF_SCALE) + warp * C::OUT;
     const int units = S.first[p.groups];
+    wait_for_quantiser();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int acc = 0;
     uint32_t phase = 0;
@@ -599,13 +614,14 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
 template <int KIND, int BN>
 __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uint32_t base)
 {
-    using C = PlainCfg<BN>;
+    using C = PlainCfg<KIND, BN>;
     const int units = S.first[p.groups];
     volatile int *abort_flag = &S.abort_flag;
     const uint32_t tx = static_cast<uint32_t>(p.a_box + p.b_box) * kBlock;
     int s = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
     bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
+    wait_for_quantiser();
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit w = unit_of<KIND>(p, S, u, C::BM, BN);
         for (int b = 0; b < w.nblk; ++b) {
@@ -638,7 +654,7 @@ __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uin
 template <int KIND, int BN>
 __device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, uint32_t base, int issuer)
 {
-    using C = PlainCfg<BN>;
+    using C = PlainCfg<KIND, BN>;
     constexpr uint32_t IDESC = idesc_e4m3(C::BM, BN);
     const int units = S.first[p.groups];
     volatile int *abort_flag = &S.abort_flag;
@@ -648,7 +664,7 @@ __device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, ui
     int b = issuer;                      // its position in the current tile
     bool ok = true, issued = false;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const int nblk = unit_of<KIND>(p, S, u, C::BM, BN).nblk;
+        const int nblk = KIND == kFp8Rows || !p.offsets ? p.max_blocks : unit_of<KIND>(p, S, u, C::BM, BN).nblk;
         for (; b < nblk; b += 2) {
             if (!wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true) ||
                 !wait_bounded(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
@@ -680,9 +696,9 @@ __device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, ui
 }
 
 template <int KIND, bool F32, int BN>
-__global__ void __launch_bounds__(PlainCfg<BN>::THREADS, 1) fp8_plain_kernel(const __grid_constant__ Fp8Params p)
+__global__ void __launch_bounds__(PlainCfg<KIND, BN>::THREADS, 1) fp8_plain_kernel(const __grid_constant__ Fp8Params p)
 {
-    using C = PlainCfg<BN>;
+    using C = PlainCfg<KIND, BN>;
     extern __shared__ uint8_t fp8_smem[];
     const uint32_t raw = smem_u32(fp8_smem);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -770,6 +786,7 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
     using C = SwapCfg<NT>;
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int units = S.first[p.groups];
+    wait_for_quantiser();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int slot = 0;
     uint32_t phase = 0;
@@ -856,6 +873,7 @@ __device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, fl
     using C = SwapCfg<NT>;
     constexpr int SL = NT < 32 ? 1 : NT / 32;        // tokens of a lane
     const int units = S.first[p.groups];
+    wait_for_quantiser();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int slot = 0;
     uint32_t phase = 0;
@@ -915,6 +933,7 @@ __device__ __forceinline__ void swap_copy(const Fp8Params &p, Fp8Shared &S, uint
     int s = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
     bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
+    wait_for_quantiser();
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
         for (int b = 0; b < w.nblk; b += C::PER_STAGE) {
@@ -962,7 +981,7 @@ __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uin
     uint32_t round = 0, phase = 0;
     bool ok = true, issued = false, mine = issuer == 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const int nblk = unit_of<kFp8Rows>(p, S, u, NT, tile_rows).nblk;
+        const int nblk = p.max_blocks;
         for (int b = 0; ok && b < nblk; b += C::PER_SLOT) {
             if (mine && !wait_bounded(smem_u32(&S.acce[slot]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
                 ok = false;
@@ -1069,10 +1088,29 @@ cudaError_t once_per_device(std::atomic<uint64_t> &done, F set_up)
     return e;
 }
 
+// A launch that may begin while the one in front of it ends, if that one
+// allows it (griddepcontrol).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*fn)(P...), int grid, int threads, int smem, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 template <int KIND, bool F32, int BN>
 cudaError_t run_plain(const Fp8Params &p, int sms, cudaStream_t s)
 {
-    using C = PlainCfg<BN>;
+    using C = PlainCfg<KIND, BN>;
     auto fn = fp8_plain_kernel<KIND, F32, BN>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = once_per_device(done, [&] {
@@ -1084,8 +1122,7 @@ cudaError_t run_plain(const Fp8Params &p, int sms, cudaStream_t s)
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    fn<<<sms, C::THREADS, C::SMEM, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(fn, sms, C::THREADS, C::SMEM, s, p);
 }
 
 template <bool F32, int NT>
@@ -1097,8 +1134,7 @@ cudaError_t run_swap(const Fp8Params &p, int tile_rows, int sms, cudaStream_t s)
     const cudaError_t e = once_per_device(
         done, [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
     if (e != cudaSuccess) return e;
-    fn<<<C::CTAS * sms, C::THREADS, C::SMEM, s>>>(p, tile_rows);
-    return cudaGetLastError();
+    return launch_early(fn, C::CTAS * sms, C::THREADS, C::SMEM, s, p, tile_rows);
 }
 
 }  // namespace deto

@@ -136,6 +136,9 @@ constexpr int kWarpCols = 256 * kUnroll;
 
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p, int col_parts)
 {
+    // A product behind this launch may set itself up already; it waits for
+    // this grid's end before it touches any operand.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
     const long long m = w / col_parts;
