@@ -243,6 +243,7 @@ det_gemm_status fp8_rows(const uint8_t *A, const float *sa, const uint8_t *W, co
 {
     if (!ok_size(M) || !ok_size(N) || !ok_size(K) || G < 0 || G > DET_MOE_MAX_EXPERTS) return DET_GEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return DET_GEMM_OK;
+    if (!launchable((up(M, 16) + G) * up(N, 32))) return DET_GEMM_ERR_INVALID_ARG;    // more tiles than are counted
     const int es = out_fp32 ? 4 : 2;
     const Arr out{C, M, N, ldc, es, 16};
     const int64_t nb = up(K, kBlock);

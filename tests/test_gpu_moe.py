@@ -107,6 +107,27 @@ def test_route_rows_do_not_depend_on_the_batch_or_the_pitch():
     ok()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_experts_masked_by_the_types_lowest_value(score, dtype):
+    """A finite mask: the expert is a candidate, with score 0."""
+    x = logits_of(40, 64, dtype, 21)
+    g = torch.Generator().manual_seed(2)
+    x[torch.rand((40, 64), generator=g) < 0.5] = torch.finfo(dtype).min
+    x[3] = torch.finfo(dtype).min
+    x[4, 2:] = torch.finfo(dtype).min
+    x[5, 1:] = -150.0                                          # scores far below FP32's range next to a large one
+    x[5, 7] = -149.0
+    bias = (torch.rand(64, generator=g) - 0.5) * 0.2
+    for kw in ({}, dict(bias=bias), dict(n_groups=8, top_groups=3), dict(n_groups=8, top_groups=3, bias=bias)):
+        b = kw.get("bias")
+        w, ids = dg.det_moe_route(x.cuda(), 6, score=score, **dict(kw, bias=None if b is None else b.cuda()))
+        ok()
+        rw, rids = ref.route(ref.f64(x), 6, score=score, **dict(kw, bias=None if b is None else ref.f64(b)))
+        assert np.array_equal(ids.cpu().numpy(), rids), kw
+        assert (np.abs(ref.f64(w) - rw) <= np.abs(rw) * (2 * 300 + 64) * 2.0 ** -24 + 1e-37).all()
+
+
 def test_route_of_no_tokens():
     w, ids = dg.det_moe_route(torch.zeros(0, 8).cuda(), 2)
     assert w.shape == (0, 2) and ids.shape == (0, 2)
