@@ -15,23 +15,31 @@
 //
 // Which expert is chosen is a discrete question, so FP32 rounding must not
 // decide it. Choices are compared in FP32, where each carries an error of a
-// few units in the last place; when two neighbours of the chosen order (or
-// the last kept and the first dropped group) are closer than FP32's
-// error bound, the warp decides again: the few candidates near the last
-// choice in FP64, one a lane, when only their order is in doubt; every expert
-// with pairs of FP32 values (about 43 bits), or in FP64 where a score is too
-// small for those, when a group is. Neighbours with equal
-// logits and equal bias are exact ties and need no repeat. On 8192 tokens of
-// 256 experts with random logits about one row in a thousand decides
-// again; with FP64 for every expert of those, whose units are few, they took
-// 25 of the launch's 45 us.
+// few units in the last place; when two neighbours of the chosen order, or the
+// last kept and the first dropped group, are closer than FP32's error bound,
+// the warp decides again: the few candidates near the last choice in FP64, one
+// a lane; the groups whose place is open with pairs of FP32 values (about 43
+// bits), or in FP64 where a score is too small for those; and every expert so
+// where many candidates are close. Neighbours with equal logits and equal
+// bias are exact ties and need no repeat. On 8192 tokens of 256 experts with
+// random logits about one row in a thousand decides again. The launch takes
+// as long as its last row: repeating all experts' choices for a border of
+// groups took 23.6 us in the mean over random inputs, the open groups alone
+// 18.8.
+//
+// On those 8192 x 256 FP32 logits the kernel takes 6.2 us by the logits alone,
+// 10.9 with sigmoid scores and a bias, 16.3 with eight groups besides, where
+// the bytes would take 1.3: instructions bound it, about 1400 a warp, mostly
+// integer and comparisons. Four warps a block keep 40 on an SM to the end.
+#pragma once
+
 #include "ops_internal.h"
 #include "vec.cuh"
 
 namespace deto {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 // Bounds of the FP32 errors of two choices, relative to their scores' and
 // biases' sizes. A sigmoid: one unit of expf, an addition, a reciprocal of one
 // unit and the bias, below 8 * 2^-24; a softmax adds its sum's rounding, common
@@ -76,17 +84,13 @@ __device__ __forceinline__ float sigmoid_choice(float l)
 // Order-preserving map of a float; 0 is left for "not a candidate".
 __device__ __forceinline__ uint32_t order_key(float c)
 {
-    const uint32_t u = __float_as_uint(c + 0.0f);     // -0 -> +0
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const int u = __float_as_int(c + 0.0f);           // -0 -> +0
+    return static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int>(0x80000000u)));
 }
 
-// The lanes that look after group `lane / lanes_per_group`.
-__device__ __forceinline__ int lanes_per_group(int groups)
-{
-    int l = 1;
-    while (l * 2 * groups <= 32) l *= 2;
-    return l;
-}
+// Group g is looked after by the lanes from g << lane_shift on; a set of
+// groups is a mask of those first lanes.
+__device__ __forceinline__ int lane_shift(int groups) { return __clz(groups - 1) - 27; }
 
 // ---- pairs of FP32 values: hi + lo, |lo| at most half a unit of hi (the sums
 // and products of Dekker and Knuth, each operation rounded on its own).
@@ -206,70 +210,185 @@ struct Num<Df> {
     {
         return Df{__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)};
     }
-    static __device__ __forceinline__ Df diff(float a, float b) { return two_sum(a, -b); }
+    // Beyond what exp_all takes lie experts that a bias masks alone: their share of a sum is nothing.
+    static __device__ __forceinline__ Df diff(float a, float b)
+    {
+        const Df d = two_sum(a, -b);
+        return fabsf(d.hi) < 60.0f ? d : Df{d.hi > 0.0f ? 60.0f : -60.0f, 0.0f};
+    }
 };
 
-// Best groups of a token: v[e] are the experts' values in shared memory
-// (-inf: masked). Returns a bit mask of the kept groups; `near` (FP32 only) is
-// set when the border between kept and dropped groups is closer than rounding
-// error.
-template <typename F>
-__device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const F *v, int lane, bool &near)
+// The group of expert e, for e and experts up to 512: e / size by a product
+// (size * (2^18 / size + 1) is above 2^18 by at most size, and e * size < 2^18).
+__device__ __forceinline__ int group_of(const RouteParams &p, int e) { return (e * p.group_mul) >> 18; }
+__device__ __forceinline__ bool in_groups(const RouteParams &p, uint32_t kept, int e)
+{
+    return (kept >> (group_of(p, e) << lane_shift(p.groups))) & 1u;
+}
+
+// The sum over the row of exp(l - top), in type F.
+template <bool FP32, typename F>
+__device__ __forceinline__ F exp_sum(const RouteParams &p, int t, int lane, float top)
 {
     using N = Num<F>;
-    const F ninf = N::of(neg_inf());
+    constexpr int B = 4;             // experts of a lane side by side
+    F sum = N::of(0.0f);
+#pragma unroll 1
+    for (int e0 = 0; e0 < p.experts; e0 += 32 * B) {
+        F x[B];
+        bool in[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int e = e0 + 32 * i + lane;
+            const float l = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
+            in[i] = l > neg_inf();
+            x[i] = N::diff(in[i] ? l : top, top);
+        }
+        exp_all(x);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (in[i]) sum = sum + x[i];
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) sum = sum + N::shfl_xor(sum, o);
+    return sum;
+}
+
+// Of the groups in `doubt`, the `slots` best, with values of type F; two
+// groups at a time, 32 experts of each at a time. Returns their mask.
+template <bool FP32, typename F>
+__device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, int lane, float top, uint32_t doubt, int slots)
+{
+    using N = Num<F>;
+    const F ninf = N::of(neg_inf()), one = N::of(1.0f);
     const int size = p.experts / p.groups;
-    const int lpg = lanes_per_group(p.groups);
-    const int g = lane / lpg, sub = lane % lpg;
-    F a = ninf, b = ninf;                             // best, second best
-    if (g < p.groups) {
-        for (int x = sub; x < size; x += lpg) {
-            const F c = v[g * size + x];
-            if (c > a) {
-                b = a;
-                a = c;
-            } else if (c > b) {
-                b = c;
+    const int shift = lane_shift(p.groups);
+    const F sum = p.sigmoid ? one : exp_sum<FP32, F>(p, t, lane, top);
+    F val = ninf;                    // in a group's first lane: its value
+#pragma unroll 1
+    for (uint32_t left = doubt; left;) {
+        int g[2];
+        g[0] = __ffs(left) - 1;
+        left &= left - 1;
+        g[1] = left ? __ffs(left) - 1 : g[0];
+        left &= left - 1;
+        F a[2] = {ninf, ninf}, b[2] = {ninf, ninf};   // best, second best
+#pragma unroll 1
+        for (int x0 = 0; x0 < size; x0 += 32) {
+            F c[2];
+            float bias[2];
+            bool in[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int x = x0 + lane, e = (g[i] >> shift) * size + x;
+                const float l = x < size ? logit_at<FP32>(p, t, e) : neg_inf();
+                bias[i] = p.bias && x < size ? p.bias[e] : 0.0f;
+                in[i] = l > neg_inf() && bias[i] > neg_inf();
+                c[i] = N::diff(p.sigmoid ? 0.0f : in[i] ? l : top, p.sigmoid ? (in[i] ? l : 0.0f) : top);
             }
+            exp_all(c);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                c[i] = (p.sigmoid ? one : c[i]) / (p.sigmoid ? one + c[i] : sum);
+                if (p.bias) c[i] = c[i] + N::of(in[i] ? bias[i] : 0.0f);
+                if (!in[i]) c[i] = ninf;
+                const F lo = c[i] > a[i] ? a[i] : c[i];
+                a[i] = c[i] > a[i] ? c[i] : a[i];
+                b[i] = lo > b[i] ? lo : b[i];
+            }
+        }
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const F a2 = N::shfl_xor(a[i], o), b2 = N::shfl_xor(b[i], o);
+                const F lo = a2 > a[i] ? a[i] : a2;
+                a[i] = a2 > a[i] ? a2 : a[i];
+                b[i] = b2 > b[i] ? b2 : b[i];
+                b[i] = lo > b[i] ? lo : b[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (lane == g[i]) val = p.group_best == 2 && b[i] > ninf ? a[i] + b[i] : a[i];
+    }
+    int rank = 0;
+    for (int h = 0; h < p.groups; ++h) {
+        const F o = N::shfl(val, h << shift);
+        rank += (o > val || (o == val && h << shift < lane)) ? 1 : 0;
+    }
+    return __ballot_sync(kAll, ((doubt >> lane) & 1u) && rank < slots);
+}
+
+// Best groups of a token: v[e] are the experts' choices in shared memory
+// (-inf: masked). Returns the mask of the kept groups. When FP32 cannot tell
+// the last kept group from the first dropped one, `doubt` are the groups whose
+// place is open and `slots` how many of them stay; the mask then holds the
+// certain ones alone.
+__device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const float *v, int lane, uint32_t &doubt, int &slots)
+{
+    const int size = p.experts / p.groups;
+    const int shift = lane_shift(p.groups), lpg = 1 << shift;
+    const int g = lane >> shift, sub = lane & (lpg - 1);
+    float a = neg_inf(), b = neg_inf();               // best, second best
+    if (g < p.groups) {
+        // Each group begins elsewhere in its row: sizes of 32 keep to different banks.
+        int x = sub + g * lpg;
+        while (x >= size) x -= size;
+#pragma unroll 4
+        for (int i = sub; i < size; i += lpg) {
+            const float c = v[g * size + x];
+            b = fmaxf(b, fminf(a, c));
+            a = fmaxf(a, c);
+            x += lpg;
+            if (x >= size) x -= size;
         }
     }
     for (int o = 1; o < lpg; o <<= 1) {
-        const F a2 = N::shfl_xor(a, o), b2 = N::shfl_xor(b, o);
-        const F lo = a < a2 ? a : a2;
-        a = a < a2 ? a2 : a;
-        b = b < b2 ? b2 : b;
-        b = b < lo ? lo : b;
+        const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+        a = fmaxf(a, a2);
     }
-    F val = a;
-    if (p.group_best == 2 && b > ninf) val = a + b;
+    float val = a, amount = fabsf(a);
+    if (p.group_best == 2 && b > neg_inf()) {
+        val = a + b;
+        amount += fabsf(b);
+    }
     int rank = 0;
-    F next = ninf;                                    // best value ranked below this group
+    float next = neg_inf();                           // best value ranked below this group
+#pragma unroll 4
     for (int h = 0; h < p.groups; ++h) {
-        const F o = N::shfl(val, h * lpg);
+        const float o = __shfl_sync(kAll, val, h << shift);
         const bool before = o > val || (o == val && h < g);
         rank += before ? 1 : 0;
-        if (!before && h != g && o > next) next = o;
+        if (!before && h != g) next = fmaxf(next, o);
     }
-    const bool kept = g < p.groups && sub == 0 && rank < p.top_groups && val > ninf;
-    if constexpr (sizeof(F) == 4) {
-        if (kept && rank == p.top_groups - 1 && next > ninf) {
-            // A value is at most the sum of two choices, each of a score of
-            // at most 1 and a bias; the bias can cancel the score, hence the 1.
-            const float size2 = fabsf(val) + fabsf(next) + (p.bias ? 1.0f : 0.0f);
-            if (!(val - next > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size2)) near = true;
+    const bool leader = g < p.groups && sub == 0 && val > neg_inf();
+    const bool kept = leader && rank < p.top_groups;
+    // A value's FP32 error: that of its scores, which are at most 1 each (a
+    // bias can cancel them, so the value does not tell their size), and of its
+    // one or two additions; scores below 1e-20 only absolutely.
+    const float err = (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (amount + (p.bias ? 1.0f : 0.0f)) + 1e-25f;
+    const uint32_t last = __ballot_sync(kAll, kept && rank == p.top_groups - 1);
+    const uint32_t first = __ballot_sync(kAll, leader && rank == p.top_groups);
+    uint32_t lanes = __ballot_sync(kAll, kept);
+    if (last && first) {
+        const int il = __ffs(last) - 1, jf = __ffs(first) - 1;
+        const float low = __shfl_sync(kAll, val - err, il), high = __shfl_sync(kAll, val + err, jf);
+        if (!(low > high)) {
+            const uint32_t open = __ballot_sync(kAll, leader && !(val - err > high) && !(val + err < low));
+            lanes &= ~open;
+            slots = p.top_groups - __popc(lanes);
+            doubt = open;
         }
-        near = __any_sync(kAll, near);
     }
-    const uint32_t lanes = __ballot_sync(kAll, kept);
-    uint32_t mask = 0;
-    for (int h = 0; h < p.groups; ++h) mask |= ((lanes >> (h * lpg)) & 1u) << h;
-    return mask;
+    return lanes;
 }
 
 // The choice with values of type F, for the few rows FP32 cannot decide.
 // Returns the chosen expert of rank `lane` (-1: none).
 template <bool FP32, typename F>
-__device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lane, float top, F *v)
+__device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lane, float top, uint32_t kept, F *v)
 {
     using N = Num<F>;
     const F ninf = N::of(neg_inf()), one = N::of(1.0f);
@@ -306,22 +425,13 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
             if (e >= p.experts) continue;
             const F x = v[e];
             const float bias = p.bias ? p.bias[e] : 0.0f;
-            const bool in = x > ninf && bias > neg_inf();
+            const bool in = x > ninf && bias > neg_inf() && (p.groups == 1 || in_groups(p, kept, e));
             F c = (sig ? one : x) / (sig ? one + x : sum);
             if (p.bias) c = c + N::of(bias);
             v[e] = in ? c : ninf;
         }
     }
     __syncwarp();
-    if (p.groups > 1) {
-        bool near = false;
-        const uint32_t kept = keep_groups<F>(p, v, lane, near);
-        const int size = p.experts / p.groups;
-        __syncwarp();
-        for (int e = lane; e < p.experts; e += 32)
-            if (!((kept >> (e / size)) & 1u)) v[e] = ninf;
-        __syncwarp();
-    }
     if (!p.bias) {                   // without a bias the logits give the order
         for (int e = lane; e < p.experts; e += 32)
             if (v[e] > ninf) v[e] = N::of(logit_at<FP32>(p, t, e));
@@ -382,10 +492,25 @@ __device__ __forceinline__ void order_candidates(const RouteParams &p, int t, in
     __syncwarp();
 }
 
+// Pairs of FP32 values hold what exp gives between -60 and 60: whether an
+// argument of the row, -l or l - top, lies elsewhere.
+template <int PER>
+__device__ __forceinline__ bool far_logits(const RouteParams &p, const float (&l)[PER], float top)
+{
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (l[i] > neg_inf()) far |= !(fabsf(p.sigmoid ? l[i] : l[i] - top) < 60.0f);
+    return __any_sync(kAll, far);
+}
+
 // Shared memory per warp: `experts` doubles, used as floats for the group
 // values and as doubles by the FP64 repeat.
-template <bool FP32, int PER>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p)
+// MODE: what the choice needs besides the logits. The repeats' registers are
+// held down to the common path's, which then has 40 warps on an SM.
+enum { kLogits, kBias, kGroups };    // kGroups: with or without a bias
+template <bool FP32, int PER, int MODE>
+__global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(const __grid_constant__ RouteParams p)
 {
     extern __shared__ double route_smem[];
     __shared__ uint2 gather_smem[kWarps][32];
@@ -409,7 +534,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     top = warp_max(top);
 
     // Scores are needed for the choice only with a bias or groups.
-    const bool scored = p.bias != nullptr || p.groups > 1;
+    constexpr bool scored = MODE != kLogits;
+    const bool biased = MODE == kBias || (MODE == kGroups && p.bias != nullptr);
     uint32_t key[PER];
     float total = 1.0f;
     if (!p.sigmoid && (scored || !p.renorm)) {
@@ -419,7 +545,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         total = warp_sum(s);
     }
     bool near = false;
-    if (scored) {
+    uint32_t kept = kAll;
+    if constexpr (scored) {
         float c[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -427,29 +554,33 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             c[i] = neg_inf();
             if (l[i] > neg_inf()) {
                 c[i] = p.sigmoid ? sigmoid_choice(l[i]) : __fdiv_rn(expf(l[i] - top), total);
-                if (p.bias) c[i] += p.bias[e];
+                if (biased) c[i] += p.bias[e];
                 if (!(c[i] > neg_inf())) {
                     c[i] = neg_inf();
                     l[i] = neg_inf();
                 }
             }
         }
-        uint32_t kept = kAll;
-        const int size = p.experts / p.groups;
-        if (p.groups > 1) {
+        if constexpr (MODE == kGroups) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = i * 32 + lane;
                 if (e < p.experts) vf[e] = c[i];
             }
             __syncwarp();
-            kept = keep_groups<float>(p, vf, lane, near);
+            uint32_t doubt = 0;
+            int slots = 0;
+            kept = keep_groups(p, vf, lane, doubt, slots);
+            if (doubt)
+                kept |= far_logits(p, l, top) ? settle_groups<FP32, double>(p, t, lane, top, doubt, slots)
+                                              : settle_groups<FP32, Df>(p, t, lane, top, doubt, slots);
+            __syncwarp();
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = i * 32 + lane;
-            const bool ok = l[i] > neg_inf() && (p.groups == 1 || ((kept >> (e / size)) & 1u));
-            key[i] = ok ? order_key(p.bias ? c[i] : l[i]) : 0u;
+            const bool ok = l[i] > neg_inf() && (MODE != kGroups || in_groups(p, kept, e));
+            key[i] = ok ? order_key(biased ? c[i] : l[i]) : 0u;
         }
     } else {
 #pragma unroll
@@ -464,7 +595,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     // instructions a choice.)
     int mine = -1, lost = -1;
     uint32_t my_key = 0, lost_key = 0;
-    const int take = p.bias ? p.k + 1 : p.k;
+    const int take = biased ? p.k + 1 : p.k;
     bool emptied = false;            // the keys have been used up
     uint32_t own = 0;
 #pragma unroll
@@ -508,7 +639,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             my_key = gathered[lane].x;
             mine = static_cast<int>(gathered[lane].y);
         }
-        if (p.bias && count > p.k) {
+        if (biased && count > p.k) {
             if (p.k < 32) {
                 lost_key = gathered[p.k].x;
                 lost = static_cast<int>(gathered[p.k].y);
@@ -544,63 +675,59 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             }
         }
     }
-    bool close = false;              // two neighbours of the choice's order cannot be told apart
-    if (p.bias) {
-        // Each choice against the next one (the last against the best that lost).
-        int ne = __shfl_down_sync(kAll, mine, 1);
-        uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
-        if (lane == p.k - 1) {
-            ne = lost;
-            nk = lost_key;
+    if constexpr (scored) {
+        bool close = false;              // two neighbours of the choice's order cannot be told apart
+        if (biased) {
+            // Each choice against the next one (the last against the best that lost).
+            int ne = __shfl_down_sync(kAll, mine, 1);
+            uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
+            if (lane == p.k - 1) {
+                ne = lost;
+                nk = lost_key;
+            }
+            if (lane < p.k && mine >= 0 && ne >= 0) {
+                const float hi = __uint_as_float((my_key & 0x80000000u) ? my_key & 0x7FFFFFFFu : ~my_key);
+                const float lo = __uint_as_float((nk & 0x80000000u) ? nk & 0x7FFFFFFFu : ~nk);
+                const float bh = p.bias[mine], bl = p.bias[ne];
+                const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
+                if (!(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
+                    !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne)))
+                    close = true;
+            }
+            close = __any_sync(kAll, close);
         }
-        if (lane < p.k && mine >= 0 && ne >= 0) {
-            const float hi = __uint_as_float((my_key & 0x80000000u) ? my_key & 0x7FFFFFFFu : ~my_key);
-            const float lo = __uint_as_float((nk & 0x80000000u) ? nk & 0x7FFFFFFFu : ~nk);
-            const float bh = p.bias[mine], bl = p.bias[ne];
-            const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
-            if (!(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
-                !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne)))
-                close = true;
-        }
-        close = __any_sync(kAll, close);
-    }
-    if (close && !near && !emptied) {
-        // The groups stand; whatever may lie above the last choice is put in
-        // order again: c >= the last choice less both errors (a score is at
-        // most 1, so the other's bias is at most 1 + |c| in size).
-        const int last = __shfl_sync(kAll, mine, p.k - 1);
-        uint32_t bound2 = 1;
-        if (last >= 0) {
-            const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
-            const float c = __uint_as_float((lk & 0x80000000u) ? lk & 0x7FFFFFFFu : ~lk);
-            bound2 = order_key(c - (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (fabsf(p.bias[last]) + 3.0f * fabsf(c) + 2.0f));
-        }
-        int n = 0;
+        if (close && !near && !emptied) {
+            // The groups stand; whatever may lie above the last choice is put in
+            // order again: c >= the last choice less both errors (a score is at
+            // most 1, so the other's bias is at most 1 + |c| in size).
+            const int last = __shfl_sync(kAll, mine, p.k - 1);
+            uint32_t bound2 = 1;
+            if (last >= 0) {
+                const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
+                const float c = __uint_as_float((lk & 0x80000000u) ? lk & 0x7FFFFFFFu : ~lk);
+                bound2 = order_key(c - (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (fabsf(p.bias[last]) + 3.0f * fabsf(c) + 2.0f));
+            }
+            int n = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const bool in = key[i] >= bound2 && key[i] != 0;
-            const unsigned who = __ballot_sync(kAll, in);
-            const int at = n + __popc(who & ((1u << lane) - 1u));
-            if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
-            n += __popc(who);
+            for (int i = 0; i < PER; ++i) {
+                const bool in = key[i] >= bound2 && key[i] != 0;
+                const unsigned who = __ballot_sync(kAll, in);
+                const int at = n + __popc(who & ((1u << lane) - 1u));
+                if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+                n += __popc(who);
+            }
+            __syncwarp();
+            if (n <= 32) {
+                order_candidates<FP32>(p, t, lane, top, gathered, n);
+                mine = lane < min(n, p.k) ? static_cast<int>(gathered[lane].y) : -1;
+                close = false;
+            }
         }
-        __syncwarp();
-        if (n <= 32) {
-            order_candidates<FP32>(p, t, lane, top, gathered, n);
-            mine = lane < min(n, p.k) ? static_cast<int>(gathered[lane].y) : -1;
-            close = false;
+        near = near || close;
+        if (near) {
+            if (far_logits(p, l, top)) mine = choose_again<FP32, double>(p, t, lane, top, kept, vd);
+            else mine = choose_again<FP32, Df>(p, t, lane, top, kept, reinterpret_cast<Df *>(vd));
         }
-    }
-    near = near || close;
-    if (near) {
-        // exp's arguments: -l, or l - top. Pairs of FP32 values hold what exp
-        // gives between -60 and 60.
-        bool far = false;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (l[i] > neg_inf()) far |= !(fabsf(p.sigmoid ? l[i] : l[i] - top) < 60.0f);
-        if (__any_sync(kAll, far)) mine = choose_again<FP32, double>(p, t, lane, top, vd);
-        else mine = choose_again<FP32, Df>(p, t, lane, top, reinterpret_cast<Df *>(vd));
     }
 
     // Weights, FP32: lane j holds choice j.
@@ -714,8 +841,10 @@ cudaError_t go(const RouteParams &p, bool bwd, cudaStream_t s)
     if (bwd) {
         route_bwd_kernel<FP32, PER><<<blocks, kWarps * 32, kWarps * PER * 32 * 4, s>>>(p);
     } else {
-        const bool scored = p.bias != nullptr || p.groups > 1;
-        route_kernel<FP32, PER><<<blocks, kWarps * 32, scored ? kWarps * p.experts * 8 : 0, s>>>(p);
+        const int smem = kWarps * p.experts * 8;
+        if (p.groups > 1) route_kernel<FP32, PER, kGroups><<<blocks, kWarps * 32, smem, s>>>(p);
+        else if (p.bias) route_kernel<FP32, PER, kBias><<<blocks, kWarps * 32, smem, s>>>(p);
+        else route_kernel<FP32, PER, kLogits><<<blocks, kWarps * 32, 0, s>>>(p);
     }
     return cudaGetLastError();
 }
@@ -731,15 +860,4 @@ cudaError_t pick(const RouteParams &p, bool bwd, cudaStream_t s)
 }
 
 }  // namespace
-
-cudaError_t launch_route(const RouteParams &p, bool fp32, cudaStream_t s)
-{
-    return fp32 ? pick<true>(p, false, s) : pick<false>(p, false, s);
-}
-
-cudaError_t launch_route_bwd(const RouteParams &p, bool fp32, cudaStream_t s)
-{
-    return fp32 ? pick<true>(p, true, s) : pick<false>(p, true, s);
-}
-
 }  // namespace deto

@@ -343,11 +343,12 @@ det_gemm_status det_moe_route(const void *logits, int logits_fp32, const float *
     p.k = top_k;
     p.groups = n_groups;
     p.top_groups = top_groups;
+    p.group_mul = (1 << 18) / (static_cast<int>(E) / n_groups) + 1;
     p.group_best = group_best;
     p.renorm = renormalize != 0;
     p.sigmoid = score;
     p.scale = scale;
-    const cudaError_t e = launch_route(p, logits_fp32 != 0, cs(stream));
+    const cudaError_t e = logits_fp32 ? launch_route_f32(p, cs(stream)) : launch_route_bf16(p, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "route launch");
 }
 
@@ -379,7 +380,7 @@ det_gemm_status det_moe_route_bwd(const float *dweights, const void *logits, int
     p.renorm = renormalize != 0;
     p.sigmoid = score;
     p.scale = scale;
-    const cudaError_t e = launch_route_bwd(p, logits_fp32 != 0, cs(stream));
+    const cudaError_t e = logits_fp32 ? launch_route_bwd_f32(p, cs(stream)) : launch_route_bwd_bf16(p, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "route gradient launch");
 }
 

@@ -26,10 +26,13 @@ struct RouteParams {
     void *dlogits;                   // backward: [T, E]
     long long ldl, ldd;
     int tokens, experts, k, groups, top_groups, group_best, renorm, sigmoid;
+    int group_mul;                   // floor(2^18 / experts of a group) + 1
     float scale;
 };
-cudaError_t launch_route(const RouteParams &p, bool fp32, cudaStream_t s);
-cudaError_t launch_route_bwd(const RouteParams &p, bool fp32, cudaStream_t s);
+cudaError_t launch_route_f32(const RouteParams &p, cudaStream_t s);
+cudaError_t launch_route_bf16(const RouteParams &p, cudaStream_t s);
+cudaError_t launch_route_bwd_f32(const RouteParams &p, cudaStream_t s);
+cudaError_t launch_route_bwd_bf16(const RouteParams &p, cudaStream_t s);
 
 // ---- stable sort by key (one cluster), rows to experts and back
 struct SortParams {

@@ -128,6 +128,48 @@ def test_experts_masked_by_the_types_lowest_value(score, dtype):
         assert (np.abs(ref.f64(w) - rw) <= np.abs(rw) * (2 * 300 + 64) * 2.0 ** -24 + 1e-37).all()
 
 
+def test_a_masked_expert_far_away_does_not_move_a_close_choice():
+    """Scores 1.5e-8 apart against biases 1e-8 the other way: FP32 cannot tell,
+    and an expert that only its bias masks lies beyond the others' range."""
+    E, k = 64, 8
+    x = (-1e-6 * torch.arange(E, dtype=torch.float64)).float()[None].repeat(3, 1)
+    bias = (1e-8 * torch.arange(E, dtype=torch.float64)).float()
+    x[:, 40], x[2, 40] = -100.0, -3e38
+    bias[40] = -float("inf")
+    for kw in ({}, dict(n_groups=8, top_groups=3), dict(n_groups=2, top_groups=1)):
+        w, ids = dg.det_moe_route(x.cuda(), k, bias=bias.cuda(), **kw)
+        ok()
+        rw, rids = ref.route(ref.f64(x), k, bias=ref.f64(bias), **kw)
+        assert np.array_equal(ids.cpu().numpy(), rids), kw
+
+
+@pytest.mark.parametrize("E,groups,top,best", [(64, 8, 3, 2), (512, 32, 5, 1), (12, 6, 2, 2), (30, 2, 1, 2), (256, 8, 4, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_too_close_for_32_bits(E, groups, top, best, score):
+    """Rows whose groups hold the same values in other places, shifted by a few
+    units of the last place, exact ties among them; with and without a bias."""
+    g = torch.Generator().manual_seed(E + groups)
+    T, size = 64, E // groups
+    base = torch.randn((T, 1, size), generator=g).expand(T, groups, size).clone()
+    for t in range(T):
+        for h in range(groups):
+            base[t, h] = base[t, h, torch.randperm(size, generator=g)]
+    x = base.reshape(T, E).contiguous()
+    steps = torch.randint(-2, 3, (T, E), generator=g).float() * (torch.arange(T)[:, None] % 3).float()
+    x = x + steps * 2.0 ** -23 * x.abs()
+    bias = (torch.randint(-2, 3, (E,), generator=g) * 1e-8).float()
+    for b in (None, bias):
+        kw = dict(n_groups=groups, top_groups=top, group_best=best)
+        w, ids = dg.det_moe_route(x.cuda(), 3, score=score, bias=None if b is None else b.cuda(), **kw)
+        ok()
+        rw, rids = ref.route(ref.f64(x), 3, score=score, bias=None if b is None else ref.f64(b), **kw)
+        same = (ids.cpu().numpy() == rids).all(1)
+        if b is None:                # values 2^-23 apart or equal: in 64 bits no sum of two lies between
+            assert same.all(), np.nonzero(~same)
+        else:                        # one step of 1e-8 and 2^-24 apart may lie within 2^-43 of one another
+            assert same.mean() >= 0.95, np.nonzero(~same)
+
+
 def test_route_of_no_tokens():
     w, ids = dg.det_moe_route(torch.zeros(0, 8).cuda(), 2)
     assert w.shape == (0, 2) and ids.shape == (0, 2)
