@@ -177,19 +177,6 @@ __device__ __forceinline__ uint64_t lds2(uint32_t at)
     return v;
 }
 
-// Sixteen bytes into shared memory behind the thread's back, the first
-// `bytes` of them from src, zeros after.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const float *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // The launch in front of this one may be a quantiser, which lets this one set
 // itself up (barriers, TMEM, the groups' tiles) while it ends; any other kernel
 // does not. Its whole grid has to be done before an operand or a scale is read
@@ -198,11 +185,10 @@ __device__ __forceinline__ void wait_for_quantiser() { asm volatile("griddepcont
 
 // A CTA's shared state besides the operand ring.
 struct Fp8Shared {
-    uint64_t full[16], empty[16], accf[8], acce[8], drain[2], never;
+    uint64_t full[16], empty[16], accf[8], acce[8], scale[12], drain[2], never;
     uint32_t tmem;
     int abort_flag;
-    int first[kMaxExperts + 1];      // first work unit of each group
-    int blk0[kMaxExperts + 1];       // weight gradient: first contraction block of each group
+    int first[kMaxExperts + 1];      // first work unit of each group; weight gradient: first contraction block
 };
 
 struct Unit {
@@ -211,7 +197,7 @@ struct Unit {
 
 __device__ __forceinline__ int group_lo(const Fp8Params &p, int limit, int g) { return min(max(p.offsets[g], 0), limit); }
 
-// Fills first[] (and blk0[]) from the group bounds; one warp, then a barrier.
+// Fills first[] from the group bounds; one warp, then a barrier.
 // Bounds that decrease or leave [0, limit] are clamped and reported.
 template <int KIND>
 __device__ __forceinline__ void setup_groups(const Fp8Params &p, Fp8Shared &S, int tile_rows, int lane)
@@ -219,44 +205,31 @@ __device__ __forceinline__ void setup_groups(const Fp8Params &p, Fp8Shared &S, i
     if (!p.offsets) {
         if (lane == 0) {
             S.first[0] = 0;
-            S.first[1] = p.m_tiles * p.n_tiles;
-            S.blk0[0] = 0;
-            S.blk0[1] = (p.kc + kBlock - 1) / kBlock;
+            S.first[1] = KIND == kFp8Rows ? p.m_tiles * p.n_tiles : (p.kc + kBlock - 1) / kBlock;
         }
         return;
     }
     const int limit = KIND == kFp8Rows ? p.rows : p.kc;
-    int units = 0, blocks = 0;
+    int units = 0;
     bool bad = false;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
         const int g = g0 + lane;
-        int u = 0, b = 0;
+        int u = 0;
         if (g < p.groups) {
             const int lo = group_lo(p, limit, g), hi = max(lo, group_lo(p, limit, g + 1));
             bad |= p.offsets[g] != lo || p.offsets[g + 1] != hi;
-            b = (hi - lo + kBlock - 1) / kBlock;
-            u = KIND == kFp8Rows ? (hi - lo + tile_rows - 1) / tile_rows * p.n_tiles : p.m_tiles * p.n_tiles;
+            u = KIND == kFp8Rows ? (hi - lo + tile_rows - 1) / tile_rows * p.n_tiles : (hi - lo + kBlock - 1) / kBlock;
         }
-        int us = u, bs = b;
+        int us = u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(kFull, us, o), y = __shfl_up_sync(kFull, bs, o);
-            if (lane >= o) {
-                us += x;
-                bs += y;
-            }
+            const int x = __shfl_up_sync(kFull, us, o);
+            if (lane >= o) us += x;
         }
-        if (g < p.groups) {
-            S.first[g] = units + us - u;
-            S.blk0[g] = blocks + bs - b;
-        }
+        if (g < p.groups) S.first[g] = units + us - u;
         units += __shfl_sync(kFull, us, 31);
-        blocks += __shfl_sync(kFull, bs, 31);
     }
-    if (lane == 0) {
-        S.first[p.groups] = units;
-        S.blk0[p.groups] = blocks;
-    }
+    if (lane == 0) S.first[p.groups] = units;
     if (bad) atomicExch(p.status, kStatusInvalid);
 }
 
@@ -267,18 +240,23 @@ __device__ __forceinline__ Unit unit_of(const Fp8Params &p, const Fp8Shared &S, 
 {
     constexpr int kSpan = 16;
     int g = 0;
-    if (p.offsets) {
-        int a = 0, b = p.groups;
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (S.first[mid] <= u) a = mid;
-            else b = mid;
+    if (KIND == kFp8Wgrad) {
+        g = u / (p.m_tiles * p.n_tiles);
+        u -= g * (p.m_tiles * p.n_tiles);
+    } else {
+        if (p.offsets) {
+            int a = 0, b = p.groups;
+            while (b - a > 1) {
+                const int mid = (a + b) >> 1;
+                if (S.first[mid] <= u) a = mid;
+                else b = mid;
+            }
+            g = a;
         }
-        g = a;
+        u -= S.first[g];
     }
     Unit r;
     r.group = g;
-    u -= S.first[g];
     int lo = 0, hi = p.rows, mt = p.m_tiles;
     if (KIND == kFp8Rows && p.offsets) {
         lo = group_lo(p, p.rows, g);
@@ -293,10 +271,16 @@ __device__ __forceinline__ Unit unit_of(const Fp8Params &p, const Fp8Shared &S, 
     r.row0 = lo + (m0 + (w - n * mw)) * tile_rows;
     r.rows_end = hi;
     r.col0 = n * tile_cols;
-    r.kblk0 = KIND == kFp8Rows ? 0 : S.blk0[g];
+    r.kblk0 = KIND == kFp8Rows ? 0 : S.first[g];
     // Never past the operands, whatever the bounds say (bounds that go down can claim rows twice).
-    r.nblk = KIND == kFp8Rows ? p.max_blocks : max(0, min(S.blk0[g + 1], p.max_blocks) - r.kblk0);
+    r.nblk = KIND == kFp8Rows ? p.max_blocks : max(0, min(S.first[g + 1], p.max_blocks) - r.kblk0);
     return r;
+}
+
+template <int KIND>
+__device__ __forceinline__ int unit_count(const Fp8Params &p, const Fp8Shared &S)
+{
+    return KIND == kFp8Rows ? S.first[p.groups] : p.groups * p.m_tiles * p.n_tiles;
 }
 
 template <bool F32>
@@ -367,14 +351,15 @@ __device__ __forceinline__ void store_fragment(const Fp8Params &p, uint32_t buf,
     constexpr int J = F32 ? 2 : 4;                   // groups of 8 columns in 64 bytes
     constexpr int EPW = F32 ? 1 : 2;
 #pragma unroll
-    for (int j0 = 0; j0 < 8; j0 += J) {
+    for (int x = 0; x < 16 / J; ++x) {
+        const int g = x & 1, j0 = (x >> 1) * J;
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {            // row lane / 4 + 8 i
-                const int r = (lane >> 2) + 8 * i;
-                const uint64_t v = sum[16 * (i >> 1) + 2 * (j0 + j) + (i & 1)];
+            for (int h = 0; h < 2; ++h) {
+                const int r = (lane >> 2) + 8 * h;
+                const uint64_t v = sum[16 * g + 2 * (j0 + j) + h];
                 float lo, hi;
                 unpair(v, lo, hi);
                 const int word = F32 ? 8 * j + 2 * (lane & 3) : 4 * j + (lane & 3);
@@ -384,15 +369,15 @@ __device__ __forceinline__ void store_fragment(const Fp8Params &p, uint32_t buf,
             }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2), k = lane & 3;
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * i + (lane >> 2), k = lane & 3, row = row0 + 16 * g + r;
             const int c = col + 8 * j0 + k * 4 * EPW;
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "r"(buf + r * 64 + ((k ^ (r >> 1)) & 3) * 16)
                          : "memory");
-            if (row0 + r < rows_end) store_chunk<F32>(p, base + (row0 + r) * p.ldo + c, c, v);
+            if (row < rows_end) store_chunk<F32>(p, base + row * p.ldo + c, c, v);
         }
     }
 }
@@ -418,23 +403,26 @@ struct PlainCfg {
     static constexpr int COLS = 64;                  // columns of a thread
     static constexpr int EPI_WARPS = BN / COLS * 4;
     static constexpr int THREADS = 32 * (EPI_WARPS + 4);
-    static constexpr int STAGES = BN == 128 ? 6 : KIND == kFp8Rows ? 5 : 4;
+    static constexpr int STAGES = BN == 128 ? 6 : 5;
     static constexpr int A_STAGE = BM * kBlock, B_STAGE = BN * kBlock;
     static constexpr int NACC = BN == 192 ? 2 : 4;
     static constexpr int OFF_B = STAGES * A_STAGE;
-    // Scales are read kAhead blocks before they are used (an L2 read takes
-    // about as long as two blocks): into registers, or, for the weight
-    // gradient, into a ring of each epilogue warp's rows' and columns' scales.
-    static constexpr int kAhead = 4, SLOT = 32 + COLS;
-    static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;       // [EPI_WARPS][kAhead][SLOT] floats
+    // Scales. A weight's product reads a row's and a weight tile's into
+    // registers, kAhead blocks before they are used (an L2 read takes about as
+    // long as two blocks). The weight gradient's come with the operands'
+    // copies, the tile's rows' and then its columns', into a ring of slots of
+    // their own: a block's copies begin when the MMAs STAGES blocks before it
+    // are done, so when the epilogue has let go of the block STAGES + NACC
+    // before it, and so has read the scales of the one before that.
+    static constexpr int kAhead = 2, SLOTS = STAGES + NACC + 1, SLOT = (BM + BN) * 4;
+    static constexpr int OFF_SCALE = OFF_B + STAGES * B_STAGE;
     // A finished tile goes out through shared memory, 64 bytes of OUT_ROWS rows
     // a time and warp: written straight from the registers, every store
-    // touches 32 lines and a 192-wide tile takes 3000 cycles to leave. (Half
-    // the rows a time leaves room for a fifth stage where the scales need no
-    // ring: 356 -> 319 ns a block.)
-    static constexpr int OUT_ROWS = KIND == kFp8Rows ? 16 : 32;
+    // touches 32 lines and a 192-wide tile takes 3000 cycles to leave. (32
+    // rows a time leave no room for a fifth stage: 356 instead of 315 ns a block.)
+    static constexpr int OUT_ROWS = 16;
     static constexpr int OUT = OUT_ROWS * 64;
-    static constexpr int OFF_OUT = OFF_SCALE + (KIND == kFp8Wgrad ? EPI_WARPS * kAhead * SLOT * 4 : 0);
+    static constexpr int OFF_OUT = OFF_SCALE + (KIND == kFp8Wgrad ? SLOTS * SLOT : 0);
     static constexpr int OFF_SHARED = OFF_OUT + EPI_WARPS * OUT;
     static constexpr int BYTES = OFF_SHARED + static_cast<int>(sizeof(Fp8Shared));
     static constexpr int SMEM = BYTES + 1024;
@@ -450,14 +438,13 @@ struct PlainCfg {
 };
 
 template <int KIND, bool F32, int BN>
-__device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S, float *scale_smem, int warp, int lane)
+__device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S, uint32_t base, int warp, int lane)
 {
     using C = PlainCfg<KIND, BN>;
     const int q = warp & 3, part = warp >> 2;
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(q * 32) << 16) + part * C::COLS;
-    const uint32_t ring = smem_u32(scale_smem + warp * C::kAhead * C::SLOT);
-    const uint32_t out = smem_u32(scale_smem) + (C::OFF_OUT - C::OFF_SCALE) + warp * C::OUT;
-    const int units = S.first[p.groups];
+    const uint32_t out = base + C::OFF_OUT + warp * C::OUT;
+    const int units = unit_count<KIND>(p, S);
     wait_for_quantiser();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int acc = 0;
@@ -470,10 +457,12 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
     // the thread's columns), of the next kAhead blocks.
     float ra[C::kAhead], rb[C::kAhead];
     bool live = false, in0 = false;
-    // Weight gradient: lanes 0-7 copy the scales of the warp's rows, lanes
-    // 8-23 those of its columns, four each; `sa` is the lane's next address.
-    int bytes = 0;
-    long long step = 0;
+    // Weight gradient: the slot of the next block's scales, and where in one
+    // the thread's rows' and (as far on) its columns' begin.
+    int slot = 0;
+    uint32_t slot_phase = 0;
+    const uint32_t scales = base + C::OFF_SCALE + q * 128 + (lane >> 2) * 4;
+    const uint32_t to_cols = C::BM * 4 - q * 128 - (lane >> 2) * 4 + part * (C::COLS * 4) + (lane & 3) * 8;
     auto load = [&](int b, int j) {
         const bool more = b < w.nblk;
         ra[j] = more && live ? __ldg(sa) : 0.0f;
@@ -481,31 +470,17 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
         sa += p.sa_blk;
         sb += p.sb_blk;
     };
-    auto fetch = [&](int b) {
-        if (b < w.nblk && lane < 24) copy_async16(ring + (b % C::kAhead) * (C::SLOT * 4) + lane * 16, sa, bytes);
-        sa += step;
-        copy_commit();
-    };
     auto begin = [&](int u) {
         if (u >= units) return;
         w = unit_of<KIND>(p, S, u, C::BM, BN);
-        const int row0 = w.row0 + q * 32, col = w.col0 + part * C::COLS;
         if constexpr (KIND == kFp8Rows) {
+            const int row0 = w.row0 + q * 32, col = w.col0 + part * C::COLS;
             live = row0 + lane < w.rows_end;
             in0 = col < p.cols;
             sa = p.sa + (live ? (row0 + lane) * p.sa_row : 0);
             sb = p.sb + (in0 ? w.group * p.sb_grp + static_cast<long long>(col / kBlock) * p.sb_row : 0);
 #pragma unroll
             for (int j = 0; j < C::kAhead; ++j) load(j, j);
-        } else {
-            const bool rows = lane < 8;
-            const int at = rows ? row0 + lane * 4 : col + (lane - 8) * 4;
-            bytes = min(max((rows ? w.rows_end : p.cols) - at, 0), 4) * 4;
-            step = bytes ? (rows ? p.sa_blk : p.sb_blk) : 0;
-            sa = (rows ? p.sa : p.sb) + (bytes ? at + w.kblk0 * step : 0);
-            __syncwarp();            // the last tile's scales have been read
-#pragma unroll
-            for (int b = 0; b < C::kAhead - 1; ++b) fetch(b);
         }
     };
     begin(static_cast<int>(blockIdx.x));
@@ -545,40 +520,62 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum[16 + i] = fma2(pair(v1[2 * i], v1[2 * i + 1]), r2, sum[16 + i]);
             } else {
-                // sum[16 g + 2 i + h]: row lane / 4 + 16 g + 8 h, columns 8 i + 2 (lane % 4) + {0, 1}
-                copy_wait<C::kAhead - 2>();
-                __syncwarp();        // every lane's copies of b are here, and every lane has read slot b - 1
-                fetch(b + C::kAhead - 1);
-                const uint32_t slot = ring + j * (C::SLOT * 4);
-                uint64_t cs[8], rs[4];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) cs[i] = lds2(slot + 128 + (8 * i + 2 * (lane & 3)) * 4);
+                // sum[16 g + 2 i + h]: row lane / 4 + 16 g + 8 h, columns 8 i + 2 (lane % 4) + {0, 1}.
+                // The accumulator goes back before the scales are looked at.
+                arrived();
+                uint32_t v[2][32];
+                tmem_ld_16x64(t0 + acc * BN, v[0]);
+                tmem_ld_16x64(t0 + acc * BN + (16u << 16), v[1]);
+                tmem_wait_ld();
+                reg_fence(v[0]);
+                reg_fence(v[1]);
+                release();
+                ok &= mbar_wait_inline(smem_u32(&S.scale[slot]), slot_phase, abort_s, p.status, p.timeout_ns) != 0;
+                const uint32_t at = scales + slot * C::SLOT;
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    slot_phase ^= 1u;
+                }
+                uint64_t rs[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float r = lds1(slot + (8 * i + (lane >> 2)) * 4);
+                    const float r = lds1(at + i * 32);
                     rs[i] = pair(r, r);
                 }
-                arrived();
-                const uint32_t t = t0 + acc * BN;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t v[32];
-                    tmem_ld_16x64(t + (static_cast<uint32_t>(16 * g) << 16), v);
-                    tmem_wait_ld();
-                    reg_fence(v);
-                    if (g == 1) release();
+                for (int i0 = 0; i0 < 8; i0 += 4) {
+                    uint64_t cs[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[16 * g + i] = fma2(pair(v[2 * i], v[2 * i + 1]), mul2(rs[2 * g + (i & 1)], cs[i / 2]), sum[16 * g + i]);
+                    for (int i = 0; i < 4; ++i) cs[i] = lds2(at + to_cols + (i0 + i) * 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int e = 2 * (i0 + i) + (x & 1);    // of row group x / 2
+                            sum[16 * (x >> 1) + e] =
+                                fma2(pair(v[x >> 1][2 * e], v[x >> 1][2 * e + 1]), mul2(rs[x], cs[i]), sum[16 * (x >> 1) + e]);
+                        }
                 }
             }
         };
-        for (int b = 0; b < w.nblk; b += C::kAhead) {
+        if constexpr (KIND == kFp8Rows) {
+            // Whole rounds of the scales' registers, then the rest: with a test after
+            // every block the compiler moves the sums about at each (333 instead of
+            // 315 ns a block).
+            int b = 0;
+#pragma unroll 1
+            for (; b + C::kAhead <= w.nblk; b += C::kAhead) {
 #pragma unroll
-            for (int j = 0; j < C::kAhead; ++j) {
+                for (int j = 0; j < C::kAhead; ++j) block(b + j, j);
+            }
+#pragma unroll
+            for (int j = 0; j < C::kAhead - 1; ++j) {
                 if (b + j >= w.nblk) break;
                 block(b + j, j);
             }
+        } else {
+#pragma unroll 2
+            for (int b = 0; b < w.nblk; ++b) block(b, 0);
         }
         if (!ok) return;             // a wait of this tile failed: the launch is aborting
         // The next tile's first scales are under way while this one is stored.
@@ -615,11 +612,13 @@ template <int KIND, int BN>
 __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uint32_t base)
 {
     using C = PlainCfg<KIND, BN>;
-    const int units = S.first[p.groups];
+    const int units = unit_count<KIND>(p, S);
     volatile int *abort_flag = &S.abort_flag;
     const uint32_t tx = static_cast<uint32_t>(p.a_box + p.b_box) * kBlock;
     int s = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
+    int slot = 0;                        // of the weight gradient's scales
+    uint32_t slot_round = 0, slot_loaded = 0, slot_parity = 0;
     bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
     wait_for_quantiser();
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
@@ -632,6 +631,18 @@ __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uin
             const uint32_t full = smem_u32(&S.full[s]);
             mbar_arrive_expect_tx(full, tx);
             const int k = (w.kblk0 + b) * kBlock;
+            if constexpr (KIND == kFp8Wgrad) {
+                const uint32_t bar = smem_u32(&S.scale[slot]), at = base + C::OFF_SCALE + slot * C::SLOT;
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.sa_box + p.sb_box) * 4);
+                tma_load_2d(at, &p.tmap_sa, bar, w.row0, w.kblk0 + b);
+                tma_load_2d(at + C::BM * 4, &p.tmap_sb, bar, w.col0, w.kblk0 + b);
+                slot_loaded |= 1u << slot;
+                slot_parity = (slot_parity & ~(1u << slot)) | (slot_round << slot);
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    slot_round ^= 1u;
+                }
+            }
             tma_load_2d(base + s * C::A_STAGE, &p.tmap_a, full, k, w.row0);
             tma_load_3d(base + C::OFF_B + s * C::B_STAGE, &p.tmap_b, full, k, w.col0, KIND == kFp8Rows ? w.group : 0);
             loaded |= 1u << s;
@@ -646,6 +657,9 @@ __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uin
         for (int i = 0; i < C::STAGES; ++i)
             if (loaded & (1u << i))
                 wait_bounded(smem_u32(&S.full[i]), (parity >> i) & 1u, abort_flag, p.status, p.timeout_ns, false);
+        for (int i = 0; KIND == kFp8Wgrad && i < C::SLOTS; ++i)
+            if (slot_loaded & (1u << i))
+                wait_bounded(smem_u32(&S.scale[i]), (slot_parity >> i) & 1u, abort_flag, p.status, p.timeout_ns, false);
     }
 }
 
@@ -656,7 +670,7 @@ __device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, ui
 {
     using C = PlainCfg<KIND, BN>;
     constexpr uint32_t IDESC = idesc_e4m3(C::BM, BN);
-    const int units = S.first[p.groups];
+    const int units = unit_count<KIND>(p, S);
     volatile int *abort_flag = &S.abort_flag;
     const uint32_t tmem = S.tmem;
     int s = issuer, acc = issuer;        // of this issuer's next block
@@ -704,7 +718,6 @@ __global__ void __launch_bounds__(PlainCfg<KIND, BN>::THREADS, 1) fp8_plain_kern
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = fp8_smem + (base - raw);
     Fp8Shared &S = *reinterpret_cast<Fp8Shared *>(smem + C::OFF_SHARED);
-    float *scale_smem = reinterpret_cast<float *>(smem + C::OFF_SCALE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
@@ -716,6 +729,7 @@ __global__ void __launch_bounds__(PlainCfg<KIND, BN>::THREADS, 1) fp8_plain_kern
             mbar_init(smem_u32(&S.accf[a]), 1);
             mbar_init(smem_u32(&S.acce[a]), C::EPI_WARPS);
         }
+        for (int i = 0; KIND == kFp8Wgrad && i < C::SLOTS; ++i) mbar_init(smem_u32(&S.scale[i]), 1);
         mbar_init(smem_u32(&S.drain[0]), 1);
         mbar_init(smem_u32(&S.drain[1]), 1);
         mbar_init(smem_u32(&S.never), 1);
@@ -736,7 +750,7 @@ __global__ void __launch_bounds__(PlainCfg<KIND, BN>::THREADS, 1) fp8_plain_kern
     tc_fence_after();
     if (warp < C::EPI_WARPS) {
         if constexpr (C::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
-        plain_epilogue<KIND, F32, BN>(p, S, scale_smem, warp, lane);
+        plain_epilogue<KIND, F32, BN>(p, S, base, warp, lane);
     } else {
         if constexpr (C::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::SERVICE_REGS));
         if (warp == C::EPI_WARPS && elect_one()) plain_copy<KIND, BN>(p, S, base);

@@ -160,6 +160,17 @@ bool encode(CUtensorMap *m, int rank, const void *p, int64_t k, int64_t rows, in
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [blocks, n] scales -> map with boxes of `box` scales of one block.
+bool encode_scales(CUtensorMap *m, const float *p, int64_t n, int64_t blocks, int64_t ld, int box)
+{
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(blocks)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 4};
+    cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), 1}, es[2] = {1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(p), dims, strides, boxes, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Rows of a copied box: the operand's own when it has fewer than the tile
 // (a box mostly outside its tensor is slow to copy).
 int box_rows(int64_t rows, int tile) { return rows >= tile ? tile : static_cast<int>(std::max<int64_t>(16, up(rows, 8) * 8)); }
@@ -174,6 +185,7 @@ struct Fp8Args {
     int out_fp32;
     int64_t groups, rows, cols, kc;      // kc: the contraction's length as stored
     int64_t lda, ldb, gb, ldo, go;
+    int64_t ldsa = 0, ldsb = 0;          // weight gradient: pitches of the scales
 };
 
 det_gemm_status enqueue(const Fp8Args &x, Fp8Params &p, const Fp8Plan &plan, Device *d, det_gemm_stream stream)
@@ -181,8 +193,12 @@ det_gemm_status enqueue(const Fp8Args &x, Fp8Params &p, const Fp8Plan &plan, Dev
     const bool rows_kind = plan.kind == kFp8Rows;
     p.a_box = (rows_kind && x.offsets) ? plan.tile_m : box_rows(x.rows, plan.tile_m);
     p.b_box = box_rows(x.cols, plan.tile_n);
+    p.sa_box = p.a_box;
+    p.sb_box = p.b_box;
     if (!encode(&p.tmap_a, 2, x.a, x.kc, x.rows, x.lda, 1, 0, p.a_box) ||
-        !encode(&p.tmap_b, 3, x.b, x.kc, x.cols, x.ldb, rows_kind ? x.groups : 1, x.gb, p.b_box)) {
+        !encode(&p.tmap_b, 3, x.b, x.kc, x.cols, x.ldb, rows_kind ? x.groups : 1, x.gb, p.b_box) ||
+        (!rows_kind && (!encode_scales(&p.tmap_sa, x.sa, x.rows, p.max_blocks, x.ldsa, p.sa_box) ||
+                        !encode_scales(&p.tmap_sb, x.sb, x.cols, p.max_blocks, x.ldsb, p.sb_box)))) {
         detg::record_detail("tensor map");
         return DET_GEMM_ERR_LAUNCH;
     }
@@ -638,13 +654,10 @@ det_gemm_status det_fp8_gemm_wgrad(const uint8_t *Yt, const float *sy, const uin
         }
         return DET_GEMM_OK;
     }
-    const Fp8Args x{Yt, sy, Xt, sx, offsets, dW, out_fp32, G, N, K, blocks * kBlock, ldyt, ldxt, 0, lddw, gdw};
+    const Fp8Args x{Yt, sy, Xt, sx, offsets, dW, out_fp32, G, N, K, blocks * kBlock, ldyt, ldxt, 0, lddw, gdw,
+                    ldsy, ldsx};
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
-    p.sa_row = 1;
-    p.sa_blk = ldsy;
-    p.sb_row = 1;
-    p.sb_blk = ldsx;
     p.kc = static_cast<int>(M);
     p.max_blocks = static_cast<int>(blocks);
     const Fp8Plan plan{kFp8Wgrad, false, 128, plain_width(G * up(N, 128), K, d->sms)};

@@ -126,6 +126,7 @@ cudaError_t launch_quantize_tiles(const QuantParams &p, cudaStream_t s);
 struct Fp8Params {
     CUtensorMap tmap_a;              // [rows, contraction]
     CUtensorMap tmap_b;              // [cols, contraction] (x experts)
+    CUtensorMap tmap_sa, tmap_sb;    // weight gradient: the scales, [blocks, rows] and [blocks, cols]
     const float *sa, *sb;
     long long sa_row, sa_blk;        // scale of row r, block b: sa[r * sa_row + b * sa_blk]
     long long sb_row, sb_blk, sb_grp;
@@ -137,6 +138,7 @@ struct Fp8Params {
     int n_tiles, m_tiles;            // column tiles; row tiles when there are no offsets
     int out_fp32;
     int a_box, b_box;                // rows of the copied boxes
+    int sa_box, sb_box;              // scales of the copied boxes
     int *status;
     unsigned long long timeout_ns;
     int force_timeout;
