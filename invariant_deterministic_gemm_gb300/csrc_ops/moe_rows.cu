@@ -6,7 +6,11 @@
 // there are no atomics and a token's bits do not depend on the batch.
 //
 // Bytes bound all three: each row is read and written once, 16 bytes a
-// thread, several rows' loads in flight per thread.
+// thread, several rows' loads in flight per thread. 8192 tokens of six experts
+// each, rows of 4096: gather 90 us (5.2 TB/s), combine 78 us (6.0), backward
+// 135 us (6.4); a copy of this card reaches 6.8. The gather's rows leave by
+// streaming stores, so that the six uses of a token's row find it in L2 (98 us
+// without).
 #include "ops_internal.h"
 #include "vec.cuh"
 

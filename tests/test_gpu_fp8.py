@@ -160,6 +160,62 @@ def test_product_of_quantised_tensors(M, N, K):
         assert (np.abs(ref.f64(C) - want) <= tol).all()
 
 
+@pytest.mark.parametrize("K", [100, 640, 1416, 2688])
+@pytest.mark.parametrize("M,N", [(5, 3000), (5, 12000), (5, 20000), (20, 3000), (20, 12000), (20, 20000), (50, 3000), (50, 8000), (50, 12000)])
+def test_few_rows_on_every_weight_tile(M, N, K):
+    """Weight tiles of 32, 64 and 128 rows beside 16, 32 and 64 tokens, with
+    odd and even numbers of blocks, more than one tile for some CTAs."""
+    qa, sa = exact_operand(M, K, M)
+    qw, _ = exact_operand(N, K, N + 1)
+    g = torch.Generator().manual_seed(3)
+    sw = torch.pow(2.0, torch.randint(-2, 3, ((N + 127) // 128, (K + 127) // 128), generator=g).float())
+    A, W = ref.e4m3_tensor(qa).cuda()[:, :K], ref.e4m3_tensor(qw).cuda()[:, :K]
+    want = torch.from_numpy(ref.dequantize(qa, sa.numpy())) @ torch.from_numpy(ref.dequantize_tiles(qw, sw.numpy())).T
+    for _ in range(3):
+        C = dg.det_fp8_gemm(A, sa.cuda(), W, sw.cuda(), out_dtype=torch.float32)
+        ok()
+        assert torch.equal(C.cpu(), want.float())
+
+
+@pytest.mark.parametrize("T,E,N,K", [(4, 16, 2048, 1400), (132, 16, 2048, 4096), (132, 16, 1000, 640), (250, 16, 2048, 1400), (900, 16, 1500, 900),
+                                     (60, 64, 700, 1400)])
+def test_few_rows_for_each_of_many_experts(T, E, N, K):
+    x = real(T, K, 1)
+    w = torch.zeros(E, N, (K + 7) // 8 * 8, dtype=torch.bfloat16, device="cuda")[:, :, :K]
+    for e in range(E):
+        w[e] = rows_of(N, K, 10 + e, 0.02)
+    q, s = dg.det_fp8_quantize_rows(x)
+    wq, ws = dg.det_fp8_quantize_tiles(w)
+    g = torch.Generator().manual_seed(T)
+    cuts = torch.sort(torch.randint(0, T + 1, (E - 1,), generator=g))[0]
+    bounds = [0] + cuts.tolist() + [T]
+    off = torch.tensor(bounds, dtype=torch.int32).cuda()
+    a, b = ref.dequantize(*ref.quantize(ref.f64(x))), None
+    for _ in range(3):
+        C = dg.det_fp8_gemm_grouped(q, s, wq, ws, off, out_dtype=torch.float32)
+        ok()
+        for e, (lo, hi) in enumerate(zip(bounds[:-1], bounds[1:])):
+            if hi > lo:
+                b = ref.dequantize_tiles(*ref.quantize_tiles(ref.f64(w[e])))
+                want = a[lo:hi] @ b.T
+                tol = ref.product_tolerance(np.abs(a[lo:hi]) @ np.abs(b).T, (K + 127) // 128, torch.float32, want)
+                assert (np.abs(ref.f64(C[lo:hi]) - want) <= tol).all(), e
+
+
+def test_bounds_made_by_the_launch_in_front_are_read_after_it():
+    """Group bounds from the kernel directly before the product."""
+    x = real(300, 256, 1)
+    w = torch.stack([rows_of(200, 256, 10 + g, 0.02).contiguous() for g in range(4)])
+    q, s = dg.det_fp8_quantize_rows(x)
+    wq, ws = dg.det_fp8_quantize_tiles(w)
+    counts = torch.tensor([0, 7, 130, 0, 163], device="cuda")
+    want = dg.det_fp8_gemm_grouped(q, s, wq, ws, torch.tensor([0, 7, 137, 137, 300], dtype=torch.int32).cuda())
+    for _ in range(20):
+        off = torch.cumsum(counts, 0, dtype=torch.int32)
+        assert torch.equal(dg.det_fp8_gemm_grouped(q, s, wq, ws, off), want)
+    ok()
+
+
 def test_an_empty_contraction_is_zero():
     q = torch.zeros(5, 16, device="cuda").to(torch.float8_e4m3fn)[:, :0]
     w = torch.zeros(24, 16, device="cuda").to(torch.float8_e4m3fn)[:, :0]
