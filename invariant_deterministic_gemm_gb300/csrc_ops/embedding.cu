@@ -19,6 +19,7 @@
 // tokens, a BF16 gradient of 151936 x 4096: 207 us, the lookup 21 us (6.4 TB/s);
 // 333 tokens, an FP32 gradient of 32003 x 1000: 30 us, of which the sort's
 // latency is about a third.
+#include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -32,13 +33,14 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const EmbedParams p, int col_blocks)
 {
+    begin();
     const int cb = blockIdx.x % col_blocks;
     const long long t = blockIdx.x / col_blocks;
     const int c = cb * kCols + threadIdx.x * 8;
     if (c >= p.cols) return;
     long long v;
-    if (p.tokens64) v = __ldg(static_cast<const long long *>(p.tokens) + t);
-    else v = __ldg(static_cast<const int *>(p.tokens) + t);
+    if (p.tokens64) v = static_cast<const long long *>(p.tokens)[t];
+    else v = static_cast<const int *>(p.tokens)[t];
     if (v < 0 || v >= p.vocab) {
         if (threadIdx.x == 0 && cb == 0) atomicExch(p.status, kStatusInvalid);
         store8(p.out + t * p.ldo, c, p.cols, make_uint4(0, 0, 0, 0));
@@ -81,6 +83,7 @@ constexpr int kZeroRows = 8;
 
 __global__ void __launch_bounds__(kThreads) grad_kernel(const EmbedGradParams p, int col_blocks)
 {
+    begin();
     const long long chunk_blocks = static_cast<long long>(p.n) * col_blocks;
     const int cb = blockIdx.x % col_blocks;
     const int c = cb * kCols + threadIdx.x * 8;
@@ -97,16 +100,16 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const EmbedGradParams p,
         return;
     }
     const int i = static_cast<int>(blockIdx.x / col_blocks);
-    const int head = __ldg(p.head + i);
+    const int head = p.head[i];
     if ((i - head) % kChunk != 0) return;
-    const int key = __ldg(p.keys + i);
+    const int key = p.keys[i];
     if (key >= p.vocab) return;                      // not a token
     // The chunk's length: how many of the next 32 positions hold this key.
     const int lane = threadIdx.x & 31;
-    const bool same = i + lane < p.n && __ldg(p.keys + i + lane) == key;
+    const bool same = i + lane < p.n && p.keys[i + lane] == key;
     const int len = __popc(__ballot_sync(kAll, same));       // the keys are sorted: a prefix
-    const bool more = i + kChunk < p.n && __ldg(p.keys + i + kChunk) == key;
-    const int src = i + lane < p.n ? __ldg(p.order + i + lane) : 0;
+    const bool more = i + kChunk < p.n && p.keys[i + kChunk] == key;
+    const int src = i + lane < p.n ? p.order[i + lane] : 0;
     const bool in = c < p.cols;
     float acc[8] = {};
     for (int r0 = 0; r0 < len; r0 += 4) {
@@ -144,24 +147,25 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const EmbedGradParams p,
 // positions).
 __global__ void __launch_bounds__(kThreads) fold_kernel(const EmbedGradParams p, int col_blocks)
 {
+    begin();
     const int cb = blockIdx.x % col_blocks;
     const int i0 = static_cast<int>(blockIdx.x / col_blocks) * kChunk;
     const int lane = threadIdx.x & 31;
     const int i = i0 + lane;
     bool starts = false;
-    if (i + kChunk < p.n && __ldg(p.head + i) == i) {
-        const int k = __ldg(p.keys + i);
-        starts = k < p.vocab && __ldg(p.keys + i + kChunk) == k;
+    if (i + kChunk < p.n && p.head[i] == i) {
+        const int k = p.keys[i];
+        starts = k < p.vocab && p.keys[i + kChunk] == k;
     }
     const unsigned who = __ballot_sync(kAll, starts);
     if (who == 0) return;
     const int head = i0 + __ffs(static_cast<int>(who)) - 1;
-    const int key = __ldg(p.keys + head);
+    const int key = p.keys[head];
     // The run's chunks after the first: 32 positions 32 apart at a time.
     int chunks = 0;
     for (;;) {
         const long long x = head + static_cast<long long>(chunks + lane + 1) * kChunk;
-        const unsigned same = __ballot_sync(kAll, x < p.n && __ldg(p.keys + x) == key);
+        const unsigned same = __ballot_sync(kAll, x < p.n && p.keys[x] == key);
         const int add = __popc(same);                // the keys are sorted: a prefix
         chunks += add;
         if (add < 32) break;
@@ -200,8 +204,7 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const EmbedGradParams p,
 cudaError_t launch_embedding(const EmbedParams &p, cudaStream_t s)
 {
     const int cb = (p.cols + kCols - 1) / kCols;
-    lookup_kernel<<<static_cast<unsigned>(static_cast<long long>(cb) * p.n), kThreads, 0, s>>>(p, cb);
-    return cudaGetLastError();
+    return launch_early(lookup_kernel, static_cast<long long>(cb) * p.n, kThreads, 0, 1, s, p, cb);
 }
 
 cudaError_t launch_embedding_grad(const EmbedGradParams &p, cudaStream_t s)
@@ -209,11 +212,9 @@ cudaError_t launch_embedding_grad(const EmbedGradParams &p, cudaStream_t s)
     const int cb = (p.cols + kCols - 1) / kCols;
     const long long blocks = static_cast<long long>(cb) * (p.n + (p.vocab - p.zero_from + kZeroRows - 1) / kZeroRows);
     if (blocks == 0) return cudaSuccess;
-    grad_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p, cb);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(grad_kernel, blocks, kThreads, 0, 1, s, p, cb);
     if (e != cudaSuccess || p.n <= kChunk) return e;
-    fold_kernel<<<static_cast<unsigned>(static_cast<long long>(cb) * ((p.n + kChunk - 1) / kChunk)), kThreads, 0, s>>>(p, cb);
-    return cudaGetLastError();
+    return launch_early(fold_kernel, static_cast<long long>(cb) * ((p.n + kChunk - 1) / kChunk), kThreads, 0, 1, s, p, cb);
 }
 
 }  // namespace deto

@@ -49,6 +49,7 @@
 #pragma once
 
 #include "det_gemm_kernel.cuh"
+#include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -177,12 +178,6 @@ __device__ __forceinline__ uint64_t lds2(uint32_t at)
     return v;
 }
 
-// The launch in front of this one may be a quantiser, which lets this one set
-// itself up (barriers, TMEM, the groups' tiles) while it ends; any other kernel
-// need not. Its whole grid has to be done before an operand, a scale or a group
-// bound is read and before the output is written.
-__device__ __forceinline__ void wait_for_quantiser() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // A CTA's shared state besides the operand ring.
 struct Fp8Shared {
     uint64_t full[16], empty[16], accf[8], acce[8], scale[12], drain[2], never;
@@ -209,7 +204,7 @@ __device__ __forceinline__ void setup_groups(const Fp8Params &p, Fp8Shared &S, i
         }
         return;
     }
-    wait_for_quantiser();
+    wait_for_last();
     const int limit = KIND == kFp8Rows ? p.rows : p.kc;
     int units = 0;
     bool bad = false;
@@ -447,7 +442,7 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(q * 32) << 16) + part * C::COLS;
     const uint32_t out = base + C::OFF_OUT + warp * C::OUT;
     const int units = unit_count<KIND>(p, S);
-    wait_for_quantiser();
+    wait_for_last();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int acc = 0;
     uint32_t phase = 0;
@@ -467,8 +462,8 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
     const uint32_t to_cols = C::BM * 4 - q * 128 - (lane >> 2) * 4 + part * (C::COLS * 4) + (lane & 3) * 8;
     auto load = [&](int b, int j) {
         const bool more = b < w.nblk;
-        ra[j] = more && live ? __ldg(sa) : 0.0f;
-        rb[j] = more && in0 ? __ldg(sb) : 0.0f;
+        ra[j] = more && live ? *sa : 0.0f;
+        rb[j] = more && in0 ? *sb : 0.0f;
         sa += p.sa_blk;
         sb += p.sb_blk;
     };
@@ -621,8 +616,8 @@ __device__ __forceinline__ void plain_copy(const Fp8Params &p, Fp8Shared &S, uin
     uint32_t round = 0, loaded = 0, parity = 0;
     int slot = 0;                        // of the weight gradient's scales
     uint32_t slot_round = 0, slot_loaded = 0, slot_parity = 0;
+    wait_for_last();
     bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
-    wait_for_quantiser();
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit w = unit_of<KIND>(p, S, u, C::BM, BN);
         for (int b = 0; b < w.nblk; ++b) {
@@ -679,6 +674,7 @@ __device__ __forceinline__ void plain_issue(const Fp8Params &p, Fp8Shared &S, ui
     uint32_t round = 0, phase = 0;
     int b = issuer;                      // its position in the current tile
     bool ok = true, issued = false;
+    wait_for_last();                     // the bounded waits' time begins after it
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int nblk = KIND == kFp8Rows || !p.offsets ? p.max_blocks : unit_of<KIND>(p, S, u, C::BM, BN).nblk;
         for (; b < nblk; b += 2) {
@@ -720,6 +716,7 @@ template <int KIND, bool F32, int BN>
 __global__ void __launch_bounds__(PlainCfg<KIND, BN>::THREADS, 1) fp8_plain_kernel(const __grid_constant__ Fp8Params p)
 {
     using C = PlainCfg<KIND, BN>;
+    // Barriers, TMEM and, without group bounds, the tiles are set up before the wait for the launch in front.
     extern __shared__ uint8_t fp8_smem[];
     const uint32_t raw = smem_u32(fp8_smem);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -809,7 +806,7 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
     using C = SwapCfg<NT>;
     const uint32_t t0 = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int units = S.first[p.groups];
-    wait_for_quantiser();
+    wait_for_last();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int slot = 0;
     uint32_t phase = 0;
@@ -896,7 +893,7 @@ __device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, fl
     using C = SwapCfg<NT>;
     constexpr int SL = NT < 32 ? 1 : NT / 32;        // tokens of a lane
     const int units = S.first[p.groups];
-    wait_for_quantiser();
+    wait_for_last();
     const uint32_t abort_s = smem_u32(&S.abort_flag);
     int slot = 0;
     uint32_t phase = 0;
@@ -908,11 +905,11 @@ __device__ __forceinline__ void swap_scales(const Fp8Params &p, Fp8Shared &S, fl
 #pragma unroll
             for (int j = 0; j < C::PER_SLOT; ++j) {
                 const bool in = b0 + j < w.nblk;
-                wv[j] = in ? __ldg(sw + (b0 + j) * p.sb_blk) : 0.0f;
+                wv[j] = in ? sw[(b0 + j) * p.sb_blk] : 0.0f;
 #pragma unroll
                 for (int i = 0; i < SL; ++i) {
                     const int r = w.row0 + 32 * i + lane;
-                    t[j][i] = (in && 32 * i + lane < NT && r < w.rows_end) ? __ldg(p.sa + r * p.sa_row + (b0 + j) * p.sa_blk) : 0.0f;
+                    t[j][i] = (in && 32 * i + lane < NT && r < w.rows_end) ? p.sa[r * p.sa_row + (b0 + j) * p.sa_blk] : 0.0f;
                 }
             }
         };
@@ -955,8 +952,8 @@ __device__ __forceinline__ void swap_copy(const Fp8Params &p, Fp8Shared &S, uint
     volatile int *abort_flag = &S.abort_flag;
     int s = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
+    wait_for_last();
     bool ok = !p.force_timeout || wait_bounded(smem_u32(&S.never), 0, abort_flag, p.status, p.timeout_ns, true);
-    wait_for_quantiser();
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit w = unit_of<kFp8Rows>(p, S, u, NT, tile_rows);
         for (int b = 0; b < w.nblk; b += C::PER_STAGE) {
@@ -1003,6 +1000,7 @@ __device__ __forceinline__ void swap_issue(const Fp8Params &p, Fp8Shared &S, uin
     int s = 0, slot = 0;                 // all stages are counted, its own are issued
     uint32_t round = 0, phase = 0;
     bool ok = true, issued = false;
+    wait_for_last();                     // the bounded waits' time begins after it
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const int nblk = p.max_blocks;
         for (int b = 0; b < nblk; b += C::PER_SLOT) {
@@ -1049,6 +1047,7 @@ template <bool F32, int NT>
 __global__ void __launch_bounds__(256, SwapCfg<NT>::CTAS) fp8_swap_kernel(const __grid_constant__ Fp8Params p, const int tile_rows)
 {
     using C = SwapCfg<NT>;
+    // Barriers, TMEM and, without group bounds, the tiles are set up before the wait for the launch in front.
     extern __shared__ uint8_t fp8_smem[];
     const uint32_t raw = smem_u32(fp8_smem);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -1111,25 +1110,6 @@ cudaError_t once_per_device(std::atomic<uint64_t> &done, F set_up)
     return e;
 }
 
-// A launch that may begin while the one in front of it ends, if that one
-// allows it (griddepcontrol).
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*fn)(P...), int grid, int threads, int smem, cudaStream_t s, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
-    return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
 template <int KIND, bool F32, int BN>
 cudaError_t run_plain(const Fp8Params &p, int sms, cudaStream_t s)
 {
@@ -1145,7 +1125,7 @@ cudaError_t run_plain(const Fp8Params &p, int sms, cudaStream_t s)
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    return launch_early(fn, sms, C::THREADS, C::SMEM, s, p);
+    return launch_early(fn, sms, C::THREADS, C::SMEM, 1, s, p);
 }
 
 template <bool F32, int NT>
@@ -1157,7 +1137,7 @@ cudaError_t run_swap(const Fp8Params &p, int tile_rows, int sms, cudaStream_t s)
     const cudaError_t e = once_per_device(
         done, [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
     if (e != cudaSuccess) return e;
-    return launch_early(fn, C::CTAS * sms, C::THREADS, C::SMEM, s, p, tile_rows);
+    return launch_early(fn, C::CTAS * sms, C::THREADS, C::SMEM, 1, s, p, tile_rows);
 }
 
 }  // namespace deto

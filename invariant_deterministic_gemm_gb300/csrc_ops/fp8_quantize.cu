@@ -18,6 +18,7 @@
 // element is written. [8192, 14336] along rows 61 us (5.8 TB/s), along columns
 // 79 us (4.5: its lines of 128 output bytes are scattered); [8192, 4096] 20
 // and 24 us.
+#include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -138,9 +139,7 @@ constexpr int kWarpCols = 256 * kUnroll;
 
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p, int col_parts)
 {
-    // A product behind this launch may set itself up already; it waits for
-    // this grid's end before it touches any operand.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin();
     const int lane = threadIdx.x & 31;
     const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
     const long long m = w / col_parts;
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantP
     const int c0 = static_cast<int>(w - m * col_parts) * kWarpCols + lane * 8;
     const uint16_t *src = nullptr;
     if (p.rows) {
-        const int f = __ldg(p.rows + m);
+        const int f = p.rows[m];
         if (f >= 0 && f / p.k < p.src_rows) src = p.x + (f / p.k) * p.ldx;
     } else {
         src = p.x + m * p.ldx;
@@ -186,6 +185,7 @@ constexpr int kPitch = kBlock + 16;  // bytes between columns in shared memory: 
 
 __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantParams p, int col_tiles)
 {
+    begin();
     __shared__ __align__(16) uint8_t out[kColTile * kPitch];
     __shared__ uint32_t part[kColThreads / 32][32];
     const int blk = blockIdx.x / col_tiles;
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
             const int g = g0 + lane;
             int lo = 0, hi = 0;
             if (g < p.groups) {
-                lo = min(max(__ldg(p.offsets + g), 0), p.n);
-                hi = min(max(__ldg(p.offsets + g + 1), lo), p.n);
+                lo = min(max(p.offsets[g], 0), p.n);
+                hi = min(max(p.offsets[g + 1], lo), p.n);
             }
             const int nb = (hi - lo + kBlock - 1) / kBlock;
             int v = nb;
@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
         for (int i = 0; i < 16; ++i) {
             v[i] = 0;
             if (i < rows) {
-                if (c + 1 < p.cols) v[i] = __ldg(reinterpret_cast<const uint32_t *>(x + i * p.ldx));
-                else if (c < p.cols) v[i] = __ldg(x + i * p.ldx);
+                if (c + 1 < p.cols) v[i] = *reinterpret_cast<const uint32_t *>(x + i * p.ldx);
+                else if (c < p.cols) v[i] = x[i * p.ldx];
             }
         }
     }
@@ -285,6 +285,7 @@ constexpr int kTileThreads = 256;
 
 __global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const QuantParams p, int row_tiles, int col_tiles)
 {
+    begin();
     __shared__ uint8_t tq[kBlock][kBlock + 4];
     __shared__ uint32_t wmax[kTileThreads / 32];
     const int ct = blockIdx.x % col_tiles;
@@ -351,24 +352,21 @@ cudaError_t launch_quantize_rows(const QuantParams &p, cudaStream_t s)
     const int parts = (p.cols + kWarpCols - 1) / kWarpCols;
     const long long warps = static_cast<long long>(parts) * p.n;
     const long long blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    quantize_rows_kernel<<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(p, parts);
-    return cudaGetLastError();
+    return launch_early(quantize_rows_kernel, blocks, kRowThreads, 0, 1, s, p, parts);
 }
 
 cudaError_t launch_quantize_cols(const QuantParams &p, cudaStream_t s)
 {
     const int ct = (p.cols + kColTile - 1) / kColTile;
     const long long blocks = static_cast<long long>(ct) * p.max_blocks;
-    quantize_cols_kernel<<<static_cast<unsigned>(blocks), kColThreads, 0, s>>>(p, ct);
-    return cudaGetLastError();
+    return launch_early(quantize_cols_kernel, blocks, kColThreads, 0, 1, s, p, ct);
 }
 
 cudaError_t launch_quantize_tiles(const QuantParams &p, cudaStream_t s)
 {
     const int rt = (p.n + kBlock - 1) / kBlock, ct = (p.cols + kBlock - 1) / kBlock;
     const long long blocks = static_cast<long long>(rt) * ct * p.groups;
-    quantize_tiles_kernel<<<static_cast<unsigned>(blocks), kTileThreads, 0, s>>>(p, rt, ct);
-    return cudaGetLastError();
+    return launch_early(quantize_tiles_kernel, blocks, kTileThreads, 0, 1, s, p, rt, ct);
 }
 
 }  // namespace deto

@@ -33,6 +33,7 @@
 // integer and comparisons. Four warps a block keep 40 on an SM to the end.
 #pragma once
 
+#include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -512,6 +513,7 @@ enum { kLogits, kBias, kGroups };    // kGroups: with or without a bias
 template <bool FP32, int PER, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(const __grid_constant__ RouteParams p)
 {
+    begin();
     extern __shared__ double route_smem[];
     __shared__ uint2 gather_smem[kWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -761,6 +763,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
 template <bool FP32, int PER>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParams p)
 {
+    begin();
     extern __shared__ double route_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kWarps + warp;
@@ -838,15 +841,11 @@ template <bool FP32, int PER>
 cudaError_t go(const RouteParams &p, bool bwd, cudaStream_t s)
 {
     const int blocks = (p.tokens + kWarps - 1) / kWarps;
-    if (bwd) {
-        route_bwd_kernel<FP32, PER><<<blocks, kWarps * 32, kWarps * PER * 32 * 4, s>>>(p);
-    } else {
-        const int smem = kWarps * p.experts * 8;
-        if (p.groups > 1) route_kernel<FP32, PER, kGroups><<<blocks, kWarps * 32, smem, s>>>(p);
-        else if (p.bias) route_kernel<FP32, PER, kBias><<<blocks, kWarps * 32, smem, s>>>(p);
-        else route_kernel<FP32, PER, kLogits><<<blocks, kWarps * 32, 0, s>>>(p);
-    }
-    return cudaGetLastError();
+    if (bwd) return launch_early(route_bwd_kernel<FP32, PER>, blocks, kWarps * 32, kWarps * PER * 32 * 4, 1, s, p);
+    const int smem = kWarps * p.experts * 8;
+    if (p.groups > 1) return launch_early(route_kernel<FP32, PER, kGroups>, blocks, kWarps * 32, smem, 1, s, p);
+    if (p.bias) return launch_early(route_kernel<FP32, PER, kBias>, blocks, kWarps * 32, smem, 1, s, p);
+    return launch_early(route_kernel<FP32, PER, kLogits>, blocks, kWarps * 32, 0, 1, s, p);
 }
 
 template <bool FP32>

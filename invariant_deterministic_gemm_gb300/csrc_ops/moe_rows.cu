@@ -11,6 +11,7 @@
 // 135 us (6.4); a copy of this card reaches 6.8. The gather's rows leave by
 // streaming stores, so that the six uses of a token's row find it in L2 (98 us
 // without).
+#include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
 
@@ -24,6 +25,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p, int col_blocks)
 {
+    begin();
     const int cb = blockIdx.x % col_blocks;
     const long long r0 = static_cast<long long>(blockIdx.x / col_blocks) * kRows;
     const int c = cb * kCols + threadIdx.x * 8;
@@ -33,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p, 
     for (int i = 0; i < kRows; ++i) {
         v[i] = make_uint4(0, 0, 0, 0);
         if (r0 + i < p.n) {
-            const int f = __ldg(p.rows + r0 + i);
+            const int f = p.rows[r0 + i];
             if (f >= 0 && f / p.k < p.src_rows) v[i] = load8(p.src + (f / p.k) * p.lds, c, p.cols);
         }
     }
@@ -44,6 +46,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p, 
 
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p, int col_blocks)
 {
+    begin();
     const int cb = blockIdx.x % col_blocks;
     const long long t = blockIdx.x / col_blocks;
     const int c = cb * kCols + threadIdx.x * 8;
@@ -57,10 +60,10 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
             v[i] = make_uint4(0, 0, 0, 0);
             w[i] = 0.0f;
             if (j0 + i < p.k) {
-                const int r = __ldg(p.slots + t * p.k + j0 + i);
+                const int r = p.slots[t * p.k + j0 + i];
                 if (r >= 0 && r < p.rows_n) {
                     v[i] = load8(p.ys + r * p.ldys, c, p.cols);
-                    w[i] = p.weights ? __ldg(p.weights + t * p.k + j0 + i) : 1.0f;
+                    w[i] = p.weights ? p.weights[t * p.k + j0 + i] : 1.0f;
                 }
             }
         }
@@ -83,14 +86,15 @@ constexpr int kBwdThreads = 256;
 
 __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const CombineParams p)
 {
+    begin();
     __shared__ float part[kBwdThreads / 32][kMaxTopK];
     const long long t = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *dy = p.dy + t * p.lddy;
     for (int j = 0; j < p.k; ++j) {
-        const int r = __ldg(p.slots + t * p.k + j);
+        const int r = p.slots[t * p.k + j];
         const bool in = r >= 0 && r < p.rows_n;
-        const float w = in ? __ldg(p.weights + t * p.k + j) : 0.0f;
+        const float w = in ? p.weights[t * p.k + j] : 0.0f;
         float dot = 0.0f;
         if (in) {
             const uint16_t *ys = p.ys + r * p.ldys;
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kBwdThreads) combine_bwd_kernel(const CombineP
         if (lane == 0) part[warp][j] = dot;
         // Rows no token owns (after the last expert's) get zero gradients.
         const long long tail = t * p.k + j;
-        if (__ldg(p.rows + tail) < 0) {
+        if (p.rows[tail] < 0) {
             for (int c = threadIdx.x * 8; c < p.cols; c += kBwdThreads * 8)
                 store8(p.dys + tail * p.lddys, c, p.cols, make_uint4(0, 0, 0, 0));
         }
@@ -131,21 +135,18 @@ cudaError_t launch_gather(const GatherParams &p, cudaStream_t s)
 {
     const int cb = (p.cols + kCols - 1) / kCols;
     const long long blocks = static_cast<long long>(cb) * ((p.n + kRows - 1) / kRows);
-    gather_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p, cb);
-    return cudaGetLastError();
+    return launch_early(gather_kernel, blocks, kThreads, 0, 1, s, p, cb);
 }
 
 cudaError_t launch_combine(const CombineParams &p, cudaStream_t s)
 {
     const int cb = (p.cols + kCols - 1) / kCols;
-    combine_kernel<<<static_cast<unsigned>(static_cast<long long>(cb) * p.tokens), kThreads, 0, s>>>(p, cb);
-    return cudaGetLastError();
+    return launch_early(combine_kernel, static_cast<long long>(cb) * p.tokens, kThreads, 0, 1, s, p, cb);
 }
 
 cudaError_t launch_combine_bwd(const CombineParams &p, cudaStream_t s)
 {
-    combine_bwd_kernel<<<p.tokens, kBwdThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(combine_bwd_kernel, p.tokens, kBwdThreads, 0, 1, s, p);
 }
 
 }  // namespace deto

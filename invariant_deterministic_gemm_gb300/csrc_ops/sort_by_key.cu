@@ -28,6 +28,7 @@
 //
 // The first rows of the gradient's dense output are zeroed by the launch's
 // other clusters meanwhile.
+#include "launch.cuh"
 #include "ops_internal.h"
 
 #include <cooperative_groups.h>
@@ -56,8 +57,8 @@ struct Smem {
 __device__ __forceinline__ int key_at(const SortParams &p, int i)
 {
     long long k;
-    if (p.keys64) k = __ldg(static_cast<const long long *>(p.keys) + i);
-    else k = __ldg(static_cast<const int *>(p.keys) + i);
+    if (p.keys64) k = static_cast<const long long *>(p.keys)[i];
+    else k = static_cast<const int *>(p.keys)[i];
     if (k < 0 || k >= p.range) {
         if (p.flag_bad) atomicExch(p.status, kStatusInvalid);
         return p.range;
@@ -107,6 +108,7 @@ __device__ __forceinline__ void zero_rows(const SortParams &p, int block, int bl
 template <bool RUNS>
 __global__ void __launch_bounds__(kThreads) sort_kernel(const SortParams p)
 {
+    begin();
     extern __shared__ uint32_t hist[];               // [kWarps][bins]
     __shared__ Smem sm;
     cg::cluster_group cluster = cg::this_cluster();
@@ -286,19 +288,7 @@ cudaError_t launch_sort(const SortParams &p, bool runs, cudaStream_t s)
     if (e != cudaSuccess) return e;
     // Zeroing: whole clusters beside the sorting one, about two CTAs an SM.
     const int zero = runs && p.zero_rows > 0 ? static_cast<int>((std::min<long long>(2 * p.sms, (p.zero_rows + kWarps - 1) / kWarps) + C - 1) / C * C) : 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C + zero);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = C;
-    at.val.clusterDim.y = 1;
-    at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, p);
+    return launch_early(fn, C + zero, kThreads, smem, C, s, p);
 }
 
 }  // namespace deto

@@ -36,7 +36,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 // the row starts on a 16-byte boundary.
 __device__ __forceinline__ uint4 load8(const uint16_t *row, int c, int cols)
 {
-    if (c + 8 <= cols) return __ldg(reinterpret_cast<const uint4 *>(row + c));
+    if (c + 8 <= cols) return *reinterpret_cast<const uint4 *>(row + c);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
