@@ -45,7 +45,7 @@ extern "C" {
  * scores (without the bias), divided by their sum when renormalize != 0 (a
  * sigmoid's sum plus 1e-20), times scale. An expert whose logit is -inf or
  * NaN is masked; a choice that is left over is id -1 with weight 0.
- * Which experts win is decided in FP64 wherever FP32 could not tell.
+ * Which experts win is decided with 43 bits or more wherever FP32 cannot tell.
  * weights [T,top_k] FP32 and ids [T,top_k] are contiguous.
  */
 det_gemm_status det_moe_route(const void *logits, int logits_fp32, const float *bias, float *weights, int32_t *ids,

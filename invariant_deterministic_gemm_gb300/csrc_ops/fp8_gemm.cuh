@@ -977,6 +977,7 @@ __device__ __forceinline__ void swap_copy(const Fp8Params &p, Fp8Shared &S, uint
             }
         }
     }
+    let_next_begin();                    // the last copies are under way
     if (!ok) {
         for (int i = 0; i < stages; ++i)
             if (loaded & (1u << i))
