@@ -14,10 +14,13 @@
 // far more than y's error. Two elements at a time (f32x2 operations). The
 // scale amax / 448 is corrected the same way and is correctly rounded.
 //
-// Bytes bound these kernels: the input is read once (BF16) and one byte an
-// element is written. [8192, 14336] along rows 61 us (5.8 TB/s), along columns
-// 79 us (4.5: its lines of 128 output bytes are scattered); [8192, 4096] 20
-// and 24 us.
+// The input is read once (BF16) and one byte an element is written, and what
+// is done to an element in between counts about as much as its bytes: a warp's
+// instructions are kept few (a lane has 16 elements of a block along rows, 32
+// of two columns along columns; tests for edges only in tiles that have one).
+// [8192, 14336] along rows 52.6 us (6.7 TB/s; 61 us with eight elements a lane and
+// a 64-bit division a warp), along columns 65 us (5.4 TB/s; 78 us with tests at
+// every load); [8192, 4096] 16 and 20 us.
 #include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
@@ -84,17 +87,32 @@ __device__ __forceinline__ uint64_t quotient2(uint64_t x, uint64_t neg_a, uint64
     return fma2(fma2(y, neg_a, t), r, y);
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+// Four values to four bytes, in one block so that the second conversion
+// merges into the first one's register.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 {
-    uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-    return d;
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return w;
 }
 
-// The larger magnitudes of two pairs of BF16 values, as bit patterns: NaN is
-// above infinity, so a maximum keeps it.
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-__device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
+// The larger magnitudes of two pairs of BF16 values; a NaN stays one.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b32 x, y;\n\t"
+        "abs.bf16x2 x, %1;\n\t"
+        "abs.bf16x2 y, %2;\n\t"
+        "max.NaN.bf16x2 %0, x, y;\n\t}"
+        : "=r"(d)
+        : "r"(a), "r"(b));
+    return d;
+}
 
 // A BF16 bit pattern (magnitude) as a floored FP32 maximum.
 __device__ __forceinline__ float floor_amax(uint32_t bf16_bits)
@@ -109,14 +127,10 @@ __device__ __forceinline__ uint2 quantize8(const uint4 &v, const Divisor &d)
     if (!d.fine) return make_uint2(0, 0);
     const uint64_t na = pair(-d.amax, -d.amax), r = pair(d.r, d.r), s = pair(d.down, d.down);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t q[4];
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        unpair(quotient2(pair(bf_lo(w[i]), bf_hi(w[i])), na, r, s), lo, hi);
-        q[i] = e4m3x2(lo, hi);
-    }
-    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    for (int i = 0; i < 4; ++i) unpair(quotient2(pair(bf_lo(w[i]), bf_hi(w[i])), na, r, s), f[2 * i], f[2 * i + 1]);
+    return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
 __device__ __forceinline__ void store_q8(uint8_t *row, int c, int cols, const uint2 &v)
@@ -131,20 +145,25 @@ __device__ __forceinline__ void store_q8(uint8_t *row, int c, int cols, const ui
         if (c + i < cols) row[c + i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
 }
 
-// ---- along rows: 16 lanes own a block of 128 columns, 8 columns each; a
-// warp takes kUnroll pairs of blocks of one row, all loads in flight at once.
+// ---- along rows: 8 lanes own a block of 128 columns, 8 columns of either half
+// each (whole lines an access); a warp takes kUnroll times four blocks of one
+// row, all loads in flight at once.
 constexpr int kRowThreads = 128;
-constexpr int kUnroll = 4;
-constexpr int kWarpCols = 256 * kUnroll;
+constexpr int kUnroll = 2;
+constexpr int kStepCols = 4 * kBlock;
+constexpr int kWarpCols = kStepCols * kUnroll;
 
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p, int col_parts)
 {
     begin();
     const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const long long m = w / col_parts;
-    if (m >= p.n) return;
-    const int c0 = static_cast<int>(w - m * col_parts) * kWarpCols + lane * 8;
+    // (rows x parts stay below 2^32: the rows are below 2^31, and a part more is a kilobyte of input)
+    const unsigned w = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const unsigned row = w / static_cast<unsigned>(col_parts);
+    if (row >= static_cast<unsigned>(p.n)) return;
+    const long long m = row;
+    const int w0 = static_cast<int>(w - row * col_parts) * kWarpCols;
+    const int c0 = w0 + (lane >> 3) * kBlock + (lane & 7) * 8;
     const uint16_t *src = nullptr;
     if (p.rows) {
         const int f = p.rows[m];
@@ -152,25 +171,34 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantP
     } else {
         src = p.x + m * p.ldx;
     }
-    uint4 v[kUnroll];
+    uint4 v[kUnroll][2];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (src && c0 + u * 256 < p.cols) v[u] = load8(src, c0 + u * 256, p.cols);
-    }
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + u * kStepCols + h * (kBlock / 2);
+            v[u][h] = make_uint4(0, 0, 0, 0);
+            if (src && c < p.cols) v[u][h] = load8(src, c, p.cols);
+        }
     uint8_t *q = p.q + m * p.ldq;
+    float own = 0.0f;                                // maximum of the block whose scale this lane writes
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        const int c = c0 + u * 256;
-        if (c - lane * 8 >= p.cols) break;           // the whole warp
-        uint32_t a = max2(max2(abs2(v[u].x), abs2(v[u].y)), max2(abs2(v[u].z), abs2(v[u].w)));
+        if (w0 + u * kStepCols >= p.cols) break;     // the whole warp
+        const int c = c0 + u * kStepCols;
+        uint32_t a = max2(max2(max2(v[u][0].x, v[u][0].y), max2(v[u][0].z, v[u][0].w)),
+                          max2(max2(v[u][1].x, v[u][1].y), max2(v[u][1].z, v[u][1].w)));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = max2(a, __shfl_xor_sync(kAll, a, o));
+        for (int o = 4; o > 0; o >>= 1) a = max2(a, __shfl_xor_sync(kAll, a, o));
         const float amax = floor_amax(max(a & 0xFFFFu, a >> 16));
+        if ((lane & 7) == u) own = amax;
         if (c >= p.cols) continue;
-        store_q8(q, c, p.cols, quantize8(v[u], divisor(amax)));
-        if ((lane & 15) == 0) p.s[(c / kBlock) * p.lds + m] = block_scale(amax);
+        const Divisor d = divisor(amax);
+        store_q8(q, c, p.cols, quantize8(v[u][0], d));
+        if (c + kBlock / 2 < p.cols) store_q8(q, c + kBlock / 2, p.cols, quantize8(v[u][1], d));
     }
+    const int b = w0 / kBlock + (lane & 7) * (kStepCols / kBlock) + (lane >> 3);
+    if ((lane & 7) < kUnroll && b * kBlock < p.cols) p.s[b * p.lds + m] = block_scale(own);
 }
 
 // ---- along columns (the contraction is the token dimension): a CTA owns a
@@ -232,22 +260,27 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
     {
         const uint16_t *x = p.x + (r0 + warp * 16) * p.ldx + c;
         const int rows = r1 - r0 - warp * 16;
+        if (rows >= 16 && c0 + kColTile <= p.cols) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] = 0;
-            if (i < rows) {
-                if (c + 1 < p.cols) v[i] = *reinterpret_cast<const uint32_t *>(x + i * p.ldx);
-                else if (c < p.cols) v[i] = x[i * p.ldx];
+            for (int i = 0; i < 16; ++i) v[i] = *reinterpret_cast<const uint32_t *>(x + i * p.ldx);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[i] = 0;
+                if (i < rows) {
+                    if (c + 1 < p.cols) v[i] = *reinterpret_cast<const uint32_t *>(x + i * p.ldx);
+                    else if (c < p.cols) v[i] = x[i * p.ldx];
+                }
             }
         }
     }
     uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a = max2(a, abs2(v[i]));
+    for (int i = 0; i < 16; ++i) a = __vmaxu2(a, v[i] & 0x7FFF7FFFu);
     part[warp][lane] = a;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kColThreads / 32; ++w) a = max2(a, part[w][lane]);
+    for (int w = 0; w < kColThreads / 32; ++w) a = __vmaxu2(a, part[w][lane]);
     const float a0 = floor_amax(a & 0xFFFFu), a1 = floor_amax(a >> 16);
     const Divisor d0 = divisor(a0), d1 = divisor(a1);
     const uint64_t na = pair(-d0.amax, -d1.amax), r = pair(d0.r, d1.r), s = pair(d0.down, d1.down);
@@ -260,8 +293,8 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
             const uint32_t w = v[4 * i + e];
             unpair(quotient2(pair(bf_lo(w), bf_hi(w)), na, r, s), y0[e], y1[e]);
         }
-        q0[i] = d0.fine ? e4m3x2(y0[0], y0[1]) | (e4m3x2(y0[2], y0[3]) << 16) : 0;
-        q1[i] = d1.fine ? e4m3x2(y1[0], y1[1]) | (e4m3x2(y1[2], y1[3]) << 16) : 0;
+        q0[i] = d0.fine ? e4m3x4(y0[0], y0[1], y0[2], y0[3]) : 0;
+        q1[i] = d1.fine ? e4m3x4(y1[0], y1[1], y1[2], y1[3]) : 0;
     }
     *reinterpret_cast<uint4 *>(out + (2 * lane) * kPitch + warp * 16) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
     *reinterpret_cast<uint4 *>(out + (2 * lane + 1) * kPitch + warp * 16) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
@@ -300,7 +333,7 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const Quan
         const int r = rt * kBlock + i * 16 + (threadIdx.x >> 4);
         v[i] = make_uint4(0, 0, 0, 0);
         if (r < p.n && c < p.cols) v[i] = load8(x + r * p.ldx, c, p.cols);
-        a = max2(a, max2(max2(abs2(v[i].x), abs2(v[i].y)), max2(abs2(v[i].z), abs2(v[i].w))));
+        a = max2(a, max2(max2(v[i].x, v[i].y), max2(v[i].z, v[i].w)));
     }
     a = __reduce_max_sync(kAll, max(a & 0xFFFFu, a >> 16));
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = a;
