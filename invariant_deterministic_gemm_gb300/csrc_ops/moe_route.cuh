@@ -27,10 +27,14 @@
 // groups took 23.6 us in the mean over random inputs, the open groups alone
 // 18.8.
 //
-// On those 8192 x 256 FP32 logits the kernel takes 6.2 us by the logits alone,
-// 10.9 with sigmoid scores and a bias, 16.3 with eight groups besides, where
-// the bytes would take 1.3: instructions bound it, about 1400 a warp, mostly
-// integer and comparisons. Four warps a block keep 40 on an SM to the end.
+// On those 8192 x 256 FP32 logits the kernel takes 5.8 us by the logits alone,
+// 9.9 with sigmoid scores and a bias, 14.4 with eight groups besides, where
+// the bytes would take 1.3: instructions bound it, mostly integer and
+// comparisons. A lane holds neighbouring experts, so that it loads 16 bytes at a
+// time and a group's best choices are found in registers (every 32nd expert, and
+// groups through shared memory: 6.2, 10.9 and 16.3 us). Four warps a block
+// and 48 registers keep 40 warps on an SM to the end; 48 warps with 40 registers
+// spill and take 15.6.
 #pragma once
 
 #include "launch.cuh"
@@ -55,6 +59,38 @@ __device__ __forceinline__ float logit_at(const RouteParams &p, int t, int e)
 {
     if constexpr (FP32) return static_cast<const float *>(p.logits)[t * p.ldl + e];
     else return bf_at(static_cast<const uint16_t *>(p.logits) + t * p.ldl + e);
+}
+
+// A lane's PER neighbours from src[lane * PER] on, -inf past `experts`; in
+// 16-byte loads where the row is full and aligned.
+template <typename T, int PER>
+__device__ __forceinline__ void load_own(const T *src, int experts, int lane, float (&v)[PER])
+{
+    constexpr int bytes = PER * static_cast<int>(sizeof(T)), N = bytes < 16 ? bytes : 16;   // of one load
+    const T *own = src + lane * PER;
+    if (N >= 4 && experts == 32 * PER && (reinterpret_cast<uintptr_t>(src) & (N - 1)) == 0) {
+        alignas(16) uint32_t w[bytes / 4 > 0 ? bytes / 4 : 1];
+#pragma unroll
+        for (int i = 0; i < bytes / N; ++i) {
+            if constexpr (N == 16) *reinterpret_cast<uint4 *>(w + 4 * i) = reinterpret_cast<const uint4 *>(own)[i];
+            else if constexpr (N == 8) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(own);
+            else w[0] = *reinterpret_cast<const uint32_t *>(own);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+            else v[i] = (i & 1) ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            v[i] = neg_inf();
+            if (lane * PER + i < experts) {
+                if constexpr (sizeof(T) == 4) v[i] = own[i];
+                else v[i] = bf_at(own + i);
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -321,17 +357,12 @@ __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, i
     return __ballot_sync(kAll, ((doubt >> lane) & 1u) && rank < slots);
 }
 
-// Best groups of a token: v[e] are the experts' choices in shared memory
-// (-inf: masked). Returns the mask of the kept groups. When FP32 cannot tell
-// the last kept group from the first dropped one, `doubt` are the groups whose
-// place is open and `slots` how many of them stay; the mask then holds the
-// certain ones alone.
-__device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const float *v, int lane, uint32_t &doubt, int &slots)
+// A lane's two best choices of its group, from the choices in shared memory: a lane takes every (1 << shift)-th of its group.
+__device__ __forceinline__ void scan_group(const RouteParams &p, const float *v, int lane, float &a, float &b)
 {
     const int size = p.experts / p.groups;
     const int shift = lane_shift(p.groups), lpg = 1 << shift;
     const int g = lane >> shift, sub = lane & (lpg - 1);
-    float a = neg_inf(), b = neg_inf();               // best, second best
     if (g < p.groups) {
         // Each group begins elsewhere in its row: sizes of 32 keep to different banks.
         int x = sub + g * lpg;
@@ -345,6 +376,17 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, const floa
             if (x >= size) x -= size;
         }
     }
+}
+
+// Best groups of a token from the two best choices that each lane holds of its
+// group's (a, b; -inf: none). Returns the mask of the kept groups. When FP32 cannot tell
+// the last kept group from the first dropped one, `doubt` are the groups whose
+// place is open and `slots` how many of them stay; the mask then holds the
+// certain ones alone.
+__device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, float b, int lane, uint32_t &doubt, int &slots)
+{
+    const int shift = lane_shift(p.groups), lpg = 1 << shift;
+    const int g = lane >> shift, sub = lane & (lpg - 1);
     for (int o = 1; o < lpg; o <<= 1) {
         const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
         b = fmaxf(fmaxf(b, b2), fminf(a, a2));
@@ -523,15 +565,15 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
     double *vd = route_smem + warp * p.experts;
     float *vf = reinterpret_cast<float *>(vd);
 
+    // Lane `lane` holds experts lane * PER and on.
     float l[PER];
     float top = neg_inf();
+    if constexpr (FP32) load_own(static_cast<const float *>(p.logits) + t * p.ldl, p.experts, lane, l);
+    else load_own(static_cast<const uint16_t *>(p.logits) + t * p.ldl, p.experts, lane, l);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        float x = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
-        if (!(x > neg_inf())) x = neg_inf();          // NaN: masked
-        l[i] = x;
-        top = fmaxf(top, x);
+        if (!(l[i] > neg_inf())) l[i] = neg_inf();    // NaN: masked
+        top = fmaxf(top, l[i]);
     }
     top = warp_max(top);
 
@@ -549,39 +591,51 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
     bool near = false;
     uint32_t kept = kAll;
     if constexpr (scored) {
-        float c[PER];
+        float c[PER], bias[PER];
+        if (biased) load_own(p.bias, p.experts, lane, bias);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = i * 32 + lane;
             c[i] = neg_inf();
             if (l[i] > neg_inf()) {
                 c[i] = p.sigmoid ? sigmoid_choice(l[i]) : __fdiv_rn(expf(l[i] - top), total);
-                if (biased) c[i] += p.bias[e];
+                if (biased) c[i] += bias[i];
                 if (!(c[i] > neg_inf())) {
                     c[i] = neg_inf();
                     l[i] = neg_inf();
                 }
             }
         }
+        // A lane's experts are all of one group, and the group's lanes next to one another: no need of shared memory.
+        bool whole = true, stays = true;
         if constexpr (MODE == kGroups) {
+            const int shift = lane_shift(p.groups);
+            whole = p.experts == (PER << shift) * p.groups;
+            float a = neg_inf(), b = neg_inf();       // best, second best
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = i * 32 + lane;
-                if (e < p.experts) vf[e] = c[i];
+                for (int i = 0; i < PER; ++i) {
+                    b = fmaxf(b, fminf(a, c[i]));
+                    a = fmaxf(a, c[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (lane * PER + i < p.experts) vf[lane * PER + i] = c[i];
+                __syncwarp();
+                scan_group(p, vf, lane, a, b);
+                __syncwarp();
             }
-            __syncwarp();
             uint32_t doubt = 0;
             int slots = 0;
-            kept = keep_groups(p, vf, lane, doubt, slots);
+            kept = keep_groups(p, a, b, lane, doubt, slots);
             if (doubt)
                 kept |= far_logits(p, l, top) ? settle_groups<FP32, double>(p, t, lane, top, doubt, slots)
                                               : settle_groups<FP32, Df>(p, t, lane, top, doubt, slots);
-            __syncwarp();
+            stays = (kept >> (lane >> shift << shift)) & 1u;
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = i * 32 + lane;
-            const bool ok = l[i] > neg_inf() && (MODE != kGroups || in_groups(p, kept, e));
+            const bool ok = l[i] > neg_inf() && (whole ? stays : in_groups(p, kept, lane * PER + i));
             key[i] = ok ? order_key(biased ? c[i] : l[i]) : 0u;
         }
     } else {
@@ -621,7 +675,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
         const bool in = key[i] >= bound;
         const unsigned who = __ballot_sync(kAll, in);
         const int at = count + __popc(who & ((1u << lane) - 1u));
-        if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+        if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(lane * PER + i));
         count += __popc(who);
     }
     __syncwarp();
@@ -659,14 +713,14 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             for (int i = 0; i < PER; ++i)
                 if (key[i] > best) {
                     best = key[i];
-                    at = i * 32 + lane;
+                    at = lane * PER + i;
                 }
             const uint32_t m = __reduce_max_sync(kAll, best);
             if (m == 0) break;
             const int e = static_cast<int>(__reduce_min_sync(kAll, best == m ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (i * 32 + lane == e) key[i] = 0;
+                if (lane * PER + i == e) key[i] = 0;
             if (j == p.k) {
                 lost = e;
                 lost_key = m;
@@ -715,7 +769,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 const bool in = key[i] >= bound2 && key[i] != 0;
                 const unsigned who = __ballot_sync(kAll, in);
                 const int at = n + __popc(who & ((1u << lane) - 1u));
-                if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+                if (in && at < 32) gathered[at] = make_uint2(key[i], static_cast<uint32_t>(lane * PER + i));
                 n += __popc(who);
             }
             __syncwarp();
