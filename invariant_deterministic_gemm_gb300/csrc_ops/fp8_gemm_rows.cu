@@ -4,11 +4,11 @@
 
 namespace deto {
 
-cudaError_t launch_fp8_wgrad(const Fp8Params &p, const Fp8Plan &plan, int sms, cudaStream_t s);
+cudaError_t launch_fp8_wgrad(const Fp8Params &p, int sms, cudaStream_t s);
 
 cudaError_t launch_fp8(const Fp8Params &p, const Fp8Plan &plan, int sms, cudaStream_t s)
 {
-    if (plan.kind == kFp8Wgrad) return launch_fp8_wgrad(p, plan, sms, s);
+    if (plan.kind == kFp8Wgrad) return launch_fp8_wgrad(p, sms, s);
     const bool f = p.out_fp32 != 0;
     if (plan.swap) {
         if (plan.tile_m == 16) return f ? run_swap<true, 16>(p, plan.tile_n, sms, s) : run_swap<false, 16>(p, plan.tile_n, sms, s);

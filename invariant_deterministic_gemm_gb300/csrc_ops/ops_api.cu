@@ -221,9 +221,10 @@ det_gemm_status enqueue(const Fp8Args &x, Fp8Params &p, const Fp8Plan &plan, Dev
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "8-bit product launch");
 }
 
-// Width of the plain tile: 192 columns, or 128 where the last round of one
-// tile per SM would leave too many idle. A block of a 128-wide tile takes
-// 0.72 of the time of one of a 192-wide tile.
+// Width of a weight's product's plain tile: 192 columns, or 128 where the last
+// round of one tile per SM would leave too many idle. A 128-wide tile takes
+// 0.69 (its blocks, 217 of 313 ns) to 1 (its end, 2 us) of a 192-wide one's
+// time; 0.75 with 32 blocks, 0.71 with 112.
 int plain_width(int64_t row_tiles, int64_t cols, int sms)
 {
     const int64_t wide = up(row_tiles * up(cols, 192), sms) * 100, narrow = up(row_tiles * up(cols, 128), sms) * 72;
@@ -660,7 +661,11 @@ det_gemm_status det_fp8_gemm_wgrad(const uint8_t *Yt, const float *sy, const uin
     std::memset(&p, 0, sizeof p);
     p.kc = static_cast<int>(M);
     p.max_blocks = static_cast<int>(blocks);
-    const Fp8Plan plan{kFp8Wgrad, false, 128, plain_width(G * up(N, 128), K, d->sms)};
+    // Always the wide tile: a block takes an epilogue warp 395 ns whether the
+    // tile has eight or twelve of them ([2432, 3648] from 8192 tokens: four rounds
+    // of 128 columns 112 us, three of 192 columns 90; where one round is enough,
+    // [1000, 1000] from 4096, 17.7 and 18.6).
+    const Fp8Plan plan{kFp8Wgrad, false, 128, 192};
     return enqueue(x, p, plan, d, stream);
 }
 
