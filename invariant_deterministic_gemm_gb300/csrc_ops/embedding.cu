@@ -5,20 +5,20 @@
 // of a token in ascending t, in chunks of 32 summed from +0, and the chunks
 // in ascending order. A row's bits depend on its own occurrences alone.
 //
-// The stable sort (sort_by_key.cu) brings a token's occurrences together;
-// one block of threads then owns each chunk. The dense output's rows that
-// never occur are zeroed beside that, and its first 64 MB beside the sort,
-// which leaves the memory idle otherwise (all of it there: 250 us for a
-// gradient of 1.2 GB; none of it: 218). Tokens that occur more than 32 times (a few
-// stand in every twentieth position of a text) leave their chunks' sums in a
-// workspace, and a second launch adds them up; with one owner per run
-// instead, the most frequent token alone would be a serial walk over
+// The stable sort (sort_by_key.cu) brings a token's occurrences together; one
+// block of threads then owns each chunk. The dense output's rows that never
+// occur are zeroed beside that, and its first 128 MB beside the sort, which
+// leaves the memory idle otherwise (a gradient of 1.2 GB: 200 us; with 64 MB
+// there 205, 256 MB 204, all of it 250, nothing 218). Tokens that occur more
+// than 32 times (a few stand in every twentieth position of a text) leave their
+// chunks' sums in a workspace, and a second launch adds them up; with one owner
+// per run instead, the most frequent token alone would be a serial walk over
 // thousands of rows.
 //
 // Bytes bound it: dy is read once and the dense gradient written once. 8192
-// tokens, a BF16 gradient of 151936 x 4096: 207 us, the lookup 21 us (6.4 TB/s);
-// 333 tokens, an FP32 gradient of 32003 x 1000: 30 us, of which the sort's
-// latency is about a third.
+// tokens, a BF16 gradient of 151936 x 4096: 200 us, the lookup 20 us (6.6 TB/s);
+// 333 tokens, an FP32 gradient of 32003 x 1000: 27 us, of which 14 stay without
+// zeros to write (the latency of the sort, the sums and their joining).
 #include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"

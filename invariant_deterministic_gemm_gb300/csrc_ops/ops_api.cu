@@ -296,7 +296,7 @@ det_gemm_status fp8_rows(const uint8_t *A, const float *sa, const uint8_t *W, co
     return enqueue(x, p, plan_rows(M, N, G, grouped, d->sms), d, stream);
 }
 
-constexpr int64_t kZeroBeside = 64 << 20;    // bytes of the dense gradient zeroed while the tokens are sorted
+constexpr int64_t kZeroBeside = 128 << 20;    // bytes of the dense gradient zeroed while the tokens are sorted
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
