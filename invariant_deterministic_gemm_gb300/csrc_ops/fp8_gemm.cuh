@@ -63,8 +63,6 @@
 #include "ops_internal.h"
 #include "vec.cuh"
 
-#include <atomic>
-
 namespace deto {
 
 using detg::elect_one;
@@ -1104,20 +1102,6 @@ __global__ void __launch_bounds__(256, SwapCfg<NT>::CTAS) fp8_swap_kernel(const 
     tc_fence_after();
     if (warp == 7)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(C::TMEM_COLS) : "memory");
-}
-
-// Runs `set_up` once per device for one kernel instance (its state in `done`).
-template <typename F>
-cudaError_t once_per_device(std::atomic<uint64_t> &done, F set_up)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = set_up();
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
 }
 
 template <int KIND, bool F32, int BN>

@@ -17,6 +17,9 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 namespace deto {
 
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -33,6 +36,20 @@ __device__ __forceinline__ void begin()
 {
     if (gridDim.x <= kFewBlocks) let_next_begin();
     wait_for_last();
+}
+
+// Runs `set_up` once per device for one kernel instance (its state in `done`).
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> &done, F set_up)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = set_up();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // cluster: CTAs of a cluster (1: none).

@@ -44,6 +44,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int kMaxBins = 1 << 10;
+static_assert((1 << kDigitBits) <= kMaxExperts + 1, "the larger histogram is the experts'");
 constexpr int kBatch = 8;            // steps of 32 items whose keys are loaded at once
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
@@ -284,7 +285,11 @@ cudaError_t launch_sort(const SortParams &p, bool runs, cudaStream_t s)
     int C = 1;
     while (C < 8 && static_cast<long long>(C) * kThreads * 2 < p.n) C *= 2;
     auto fn = runs ? sort_kernel<true> : sort_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<uint64_t> done[2];
+    const cudaError_t e = once_per_device(done[runs], [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(sizeof(uint32_t)) * kWarps * (kMaxExperts + 1));
+    });
     if (e != cudaSuccess) return e;
     // Zeroing: whole clusters beside the sorting one, about two CTAs an SM.
     const int zero = runs && p.zero_rows > 0 ? static_cast<int>((std::min<long long>(2 * p.sms, (p.zero_rows + kWarps - 1) / kWarps) + C - 1) / C * C) : 0;
