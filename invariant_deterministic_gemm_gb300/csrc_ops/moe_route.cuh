@@ -53,6 +53,7 @@ constexpr float kNearSigmoid = 6e-7f, kNearSoftmax = 4e-6f;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float pos_inf() { return __int_as_float(0x7f800000); }
 
 template <bool FP32>
 __device__ __forceinline__ float logit_at(const RouteParams &p, int t, int e)
@@ -507,8 +508,8 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
     return mine;
 }
 
-// The order of a few candidates in FP64, one for each of the first `count`
-// lanes (list[lane].y). Leaves the chosen in list[0 .. min(count, k)).y.
+// The order of a few candidates (one at least) in FP64, one for each of the first
+// `count` lanes (list[lane].y). Leaves the chosen in list[0 .. min(count, k)).y.
 template <bool FP32>
 __device__ __forceinline__ void order_candidates(const RouteParams &p, int t, int lane, float top, uint2 *list, int count)
 {
@@ -746,7 +747,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 const float lo = __uint_as_float((nk & 0x80000000u) ? nk & 0x7FFFFFFFu : ~nk);
                 const float bh = p.bias[mine], bl = p.bias[ne];
                 const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
-                if (!(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
+                // (a choice of +inf is above every finite one and ties exactly with its like)
+                if (hi < pos_inf() && !(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
                     !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne)))
                     close = true;
             }
@@ -755,7 +757,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
         if (close && !near && !emptied) {
             // The groups stand; whatever may lie above the last choice is put in
             // order again: c >= the last choice less both errors (a score is at
-            // most 1, so the other's bias is at most 1 + |c| in size).
+            // most 1, so the other's bias is at most 1 + |c| in size). The last
+            // choice is finite: it is no larger than one whose neighbour was close.
             const int last = __shfl_sync(kAll, mine, p.k - 1);
             uint32_t bound2 = 1;
             if (last >= 0) {
@@ -773,7 +776,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 n += __popc(who);
             }
             __syncwarp();
-            if (n <= 32) {
+            if (n > 0 && n <= 32) {
                 order_candidates<FP32>(p, t, lane, top, gathered, n);
                 mine = lane < min(n, p.k) ? static_cast<int>(gathered[lane].y) : -1;
                 close = false;
