@@ -15,8 +15,9 @@
 //
 // Which expert is chosen is a discrete question, so FP32 rounding must not
 // decide it. Choices are compared in FP32, where each carries an error of a
-// few units in the last place; when two neighbours of the chosen order, or the
-// last kept and the first dropped group, are closer than FP32's error bound,
+// few units in the last place; when two neighbours of the chosen order, the last
+// choice and any that lost (a large bias means a large error: not only the next
+// one), or the last kept and the first dropped group, are closer than FP32's error bound,
 // the warp decides again: the few candidates near the last choice in FP64, one
 // a lane; the groups whose place is open with pairs of FP32 values (about 43
 // bits), or in FP64 where a score is too small for those; and every expert so
@@ -124,6 +125,11 @@ __device__ __forceinline__ uint32_t order_key(float c)
 {
     const int u = __float_as_int(c + 0.0f);           // -0 -> +0
     return static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int>(0x80000000u)));
+}
+
+__device__ __forceinline__ float key_value(uint32_t key)
+{
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
 // Group g is looked after by the lanes from g << lane_shift on; a set of
@@ -733,26 +739,43 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
         }
     }
     if constexpr (scored) {
-        bool close = false;              // two neighbours of the choice's order cannot be told apart
+        bool close = false;              // two choices whose order matters cannot be told apart
         if (biased) {
             // Each choice against the next one (the last against the best that lost).
+            const float rel = p.sigmoid ? kNearSigmoid : kNearSoftmax;
             int ne = __shfl_down_sync(kAll, mine, 1);
             uint32_t nk = __shfl_down_sync(kAll, my_key, 1);
             if (lane == p.k - 1) {
                 ne = lost;
                 nk = lost_key;
             }
+            bool open = false;
             if (lane < p.k && mine >= 0 && ne >= 0) {
-                const float hi = __uint_as_float((my_key & 0x80000000u) ? my_key & 0x7FFFFFFFu : ~my_key);
-                const float lo = __uint_as_float((nk & 0x80000000u) ? nk & 0x7FFFFFFFu : ~nk);
+                const float hi = key_value(my_key), lo = key_value(nk);
                 const float bh = p.bias[mine], bl = p.bias[ne];
-                const float size = fabsf(bh) + fabsf(hi) + fabsf(bl) + fabsf(lo);   // >= the scores too
+                const float own = fabsf(bh) + fabsf(hi);              // >= the score too
                 // (a choice of +inf is above every finite one and ties exactly with its like)
-                if (hi < pos_inf() && !(hi - lo > (p.sigmoid ? kNearSigmoid : kNearSoftmax) * size) &&
-                    !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne)))
-                    close = true;
+                close = hi < pos_inf() && !(hi - lo > rel * (own + fabsf(bl) + fabsf(lo))) &&
+                        !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne));
+                // Farther back may lie one with a larger error (its bias is at most
+                // 1 + |c| in size), or one behind exact ties of the last choice.
+                open = lane == p.k - 1 && hi < pos_inf() && !(hi - lo > rel * (own + 2.0f * fabsf(lo) + 1.0f));
             }
             close = __any_sync(kAll, close);
+            if (!close && __any_sync(kAll, open)) {
+                const int last = __shfl_sync(kAll, mine, p.k - 1);
+                const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
+                const float c = key_value(lk), b = p.bias[last], x = logit_at<FP32>(p, t, last);
+                const float low = c - rel * (fabsf(b) + fabsf(c));
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int e = lane * PER + i;
+                    if (key[i] == 0 || key[i] > lk || (key[i] == lk && e <= last)) continue;   // not one that lost
+                    const float ce = key_value(key[i]), be = p.bias[e];
+                    if (!(ce + rel * (fabsf(be) + fabsf(ce)) < low) && !(be == b && l[i] == x)) close = true;
+                }
+                close = __any_sync(kAll, close);
+            }
         }
         if (close && !near && !emptied) {
             // The groups stand; whatever may lie above the last choice is put in
@@ -763,7 +786,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             uint32_t bound2 = 1;
             if (last >= 0) {
                 const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
-                const float c = __uint_as_float((lk & 0x80000000u) ? lk & 0x7FFFFFFFu : ~lk);
+                const float c = key_value(lk);
                 bound2 = order_key(c - (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (fabsf(p.bias[last]) + 3.0f * fabsf(c) + 2.0f));
             }
             int n = 0;

@@ -41,3 +41,45 @@ def test_every_bias_infinite():
     for k in (1, 6, 32):
         check_route(x, k, bias)
         check_route(x, k, bias, score="sigmoid")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("offset", [0.0, 0.25])
+def test_a_larger_logit_behind_exact_ties(offset, score, dtype):
+    """Ten equal logits and a later one above them by one to three units in the
+    last place: FP32 may give all of them one choice."""
+    T, E = 200, 64
+    g = torch.Generator().manual_seed(5)
+    base = (torch.randn((T, 1), generator=g) * 2).to(dtype).float()
+    x = base - 8.0 - torch.rand((T, E), generator=g)
+    x[:, :10] = base
+    step = torch.finfo(dtype).eps * 2.0 ** torch.floor(torch.log2(base.abs()))
+    x[:, 40:41] = base + torch.randint(1, 4, (T, 1), generator=g) * step
+    x = x.to(dtype)
+    bias = torch.full((E,), offset)
+    for k in (1, 2, 5, 10, 11):
+        check_route(x, k, bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_choice_with_a_large_bias_among_small_scores(score):
+    """Scores of 1e-7 to 1e-6 that FP32 tells apart, and one of about a half
+    whose bias leaves it among them, off by several of their distances in FP32."""
+    T, E = 60, 64
+    g = torch.Generator().manual_seed(9)
+    for t in range(T):
+        s = 1e-7 + 9e-7 * torch.rand(E, generator=g, dtype=torch.float64)
+        s[10] = 0.3 + 0.4 * float(torch.rand(1, generator=g))
+        if score == "softmax":
+            s[11] = 1.0 - float(s[10]) - float(s[12:].sum()) - float(s[:10].sum())
+            x = torch.log(s)
+        else:
+            x = torch.log(s / (1.0 - s))
+        x = x.float()[None]
+        true = torch.softmax(x.double(), 1)[0] if score == "softmax" else torch.sigmoid(x.double())[0]
+        bias = torch.zeros(E)
+        bias[10] = (5e-7 - true[10]).float()
+        bias[11] = -INF
+        for k in (4, 16, 28):
+            check_route(x, k, bias, score=score)
