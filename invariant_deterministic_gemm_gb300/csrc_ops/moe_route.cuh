@@ -262,6 +262,14 @@ struct Num<Df> {
     }
 };
 
+// A score and its expert's bias. An infinite bias is the choice itself: beside an
+// infinity the low part of a pair would be NaN.
+template <typename F>
+__device__ __forceinline__ F with_bias(const F &score, float bias)
+{
+    return bias < pos_inf() ? score + Num<F>::of(bias) : Num<F>::of(bias);
+}
+
 // The group of expert e, for e and experts up to 512: e / size by a product
 // (size * (2^18 / size + 1) is above 2^18 by at most size, and e * size < 2^18).
 __device__ __forceinline__ int group_of(const RouteParams &p, int e) { return (e * p.group_mul) >> 18; }
@@ -304,7 +312,7 @@ template <bool FP32, typename F>
 __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, int lane, float top, uint32_t doubt, int slots)
 {
     using N = Num<F>;
-    const F ninf = N::of(neg_inf()), one = N::of(1.0f);
+    const F ninf = N::of(neg_inf()), pinf = N::of(pos_inf()), one = N::of(1.0f);
     const int size = p.experts / p.groups;
     const int shift = lane_shift(p.groups);
     const F sum = p.sigmoid ? one : exp_sum<FP32, F>(p, t, lane, top);
@@ -334,7 +342,7 @@ __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, i
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 c[i] = (p.sigmoid ? one : c[i]) / (p.sigmoid ? one + c[i] : sum);
-                if (p.bias) c[i] = c[i] + N::of(in[i] ? bias[i] : 0.0f);
+                if (p.bias) c[i] = with_bias(c[i], in[i] ? bias[i] : 0.0f);
                 if (!in[i]) c[i] = ninf;
                 const F lo = c[i] > a[i] ? a[i] : c[i];
                 a[i] = c[i] > a[i] ? c[i] : a[i];
@@ -354,7 +362,7 @@ __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, i
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (lane == g[i]) val = p.group_best == 2 && b[i] > ninf ? a[i] + b[i] : a[i];
+            if (lane == g[i]) val = p.group_best == 2 && b[i] > ninf && a[i] < pinf ? a[i] + b[i] : a[i];
     }
     int rank = 0;
     for (int h = 0; h < p.groups; ++h) {
@@ -417,8 +425,9 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, f
     const bool kept = leader && rank < p.top_groups;
     // A value's FP32 error: that of its scores, which are at most 1 each (a
     // bias can cancel them, so the value does not tell their size), and of its
-    // one or two additions; scores below 1e-20 only absolutely.
-    const float err = (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (amount + (p.bias ? 1.0f : 0.0f)) + 1e-25f;
+    // one or two additions; scores below 1e-20 only absolutely. A value of +inf
+    // (from a bias) is exact.
+    const float err = val < pos_inf() ? (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (amount + (p.bias ? 1.0f : 0.0f)) + 1e-25f : 0.0f;
     const uint32_t last = __ballot_sync(kAll, kept && rank == p.top_groups - 1);
     const uint32_t first = __ballot_sync(kAll, leader && rank == p.top_groups);
     uint32_t lanes = __ballot_sync(kAll, kept);
@@ -477,7 +486,7 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
             const float bias = p.bias ? p.bias[e] : 0.0f;
             const bool in = x > ninf && bias > neg_inf() && (p.groups == 1 || in_groups(p, kept, e));
             F c = (sig ? one : x) / (sig ? one + x : sum);
-            if (p.bias) c = c + N::of(bias);
+            if (p.bias) c = with_bias(c, bias);
             v[e] = in ? c : ninf;
         }
     }

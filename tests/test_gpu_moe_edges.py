@@ -83,3 +83,32 @@ def test_a_choice_with_a_large_bias_among_small_scores(score):
         bias[11] = -INF
         for k in (4, 16, 28):
             check_route(x, k, bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_close_choices_below_an_infinite_bias(score):
+    x = logits_of(40, 64, torch.float32, 7)
+    s = torch.softmax(x.double(), 1) if score == "softmax" else torch.sigmoid(x.double())
+    bias = (0.5 - s[0]).float()                                # row 0: every other choice is 0.5 up to rounding
+    bias[[50, 9]] = INF
+    for k in (1, 2, 3, 8):
+        check_route(x, k, bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,best,forced", [(64, 8, 2, [5]), (64, 8, 2, [5, 60, 61, 17]), (64, 8, 1, [40, 41, 42]), (60, 5, 2, [59]),
+                                                  (512, 32, 2, [100, 200, 300, 301]), (30, 2, 2, [0, 29])])
+def test_groups_of_an_expert_with_an_infinite_bias(E, groups, best, forced, score):
+    """Their groups come first, ties of groups to the lower index, whether or
+    not the other groups are too close for FP32."""
+    g = torch.Generator().manual_seed(E + groups)
+    x = logits_of(40, E, torch.float32, E)
+    near = logits_of(1, E // groups, torch.float32, 4)[0].repeat(groups)[None].repeat(20, 1)
+    near = near + torch.randint(-2, 3, near.shape, generator=g).float() * 2.0 ** -23 * near.abs()
+    x = torch.cat([x, near])
+    x[1, forced] = -INF
+    bias = torch.zeros(E)
+    bias[forced] = INF
+    for top in {1, max(1, groups // 2), groups - 1, groups}:
+        for k in (1, 3):
+            check_route(x, k, bias, score=score, n_groups=groups, top_groups=top, group_best=best)
