@@ -7,7 +7,9 @@
 //   choices and only the best groups' experts stay; the k largest choices
 //   win, ties to the lower index; w = score[ids], over their sum when
 //   renormalised, times `scale`. An expert whose logit is -inf or NaN is
-//   masked; choices that are left over are -1 with weight 0.
+//   masked; choices that are left over are -1 with weight 0. A logit of +inf
+//   is chosen as the largest finite one would be; the softmax of its row, and
+//   so the row's weights, are NaN.
 //
 // One warp owns a token, so a row's result is a function of that row alone:
 // the logits are read once, and everything else lives in registers. Bytes
@@ -61,6 +63,16 @@ __device__ __forceinline__ float logit_at(const RouteParams &p, int t, int e)
 {
     if constexpr (FP32) return static_cast<const float *>(p.logits)[t * p.ldl + e];
     else return bf_at(static_cast<const uint16_t *>(p.logits) + t * p.ldl + e);
+}
+
+// The same for the choice, where +inf counts as the largest finite value: so its
+// distance to the row's maximum is a number.
+constexpr float kLargest = 3.402823466e38f;
+template <bool FP32>
+__device__ __forceinline__ float choice_logit(const RouteParams &p, int t, int e)
+{
+    const float v = logit_at<FP32>(p, t, e);
+    return v > kLargest ? kLargest : v;              // a NaN stays one
 }
 
 // A lane's PER neighbours from src[lane * PER] on, -inf past `experts`; in
@@ -292,7 +304,7 @@ __device__ __forceinline__ F exp_sum(const RouteParams &p, int t, int lane, floa
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int e = e0 + 32 * i + lane;
-            const float l = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
+            const float l = e < p.experts ? choice_logit<FP32>(p, t, e) : neg_inf();
             in[i] = l > neg_inf();
             x[i] = N::diff(in[i] ? l : top, top);
         }
@@ -333,7 +345,7 @@ __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, i
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int x = x0 + lane, e = (g[i] >> shift) * size + x;
-                const float l = x < size ? logit_at<FP32>(p, t, e) : neg_inf();
+                const float l = x < size ? choice_logit<FP32>(p, t, e) : neg_inf();
                 bias[i] = p.bias && x < size ? p.bias[e] : 0.0f;
                 in[i] = l > neg_inf() && bias[i] > neg_inf();
                 c[i] = N::diff(p.sigmoid ? 0.0f : in[i] ? l : top, p.sigmoid ? (in[i] ? l : 0.0f) : top);
@@ -462,7 +474,7 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int e = e0 + 32 * i + lane;
-            const float l = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
+            const float l = e < p.experts ? choice_logit<FP32>(p, t, e) : neg_inf();
             in[i] = l > neg_inf();
             x[i] = N::diff(sig ? 0.0f : in[i] ? l : top, sig ? (in[i] ? l : 0.0f) : top);
         }
@@ -493,7 +505,7 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
     __syncwarp();
     if (!p.bias) {                   // without a bias the logits give the order
         for (int e = lane; e < p.experts; e += 32)
-            if (v[e] > ninf) v[e] = N::of(logit_at<FP32>(p, t, e));
+            if (v[e] > ninf) v[e] = N::of(choice_logit<FP32>(p, t, e));
         __syncwarp();
     }
     int mine = -1;
@@ -532,13 +544,13 @@ __device__ __forceinline__ void order_candidates(const RouteParams &p, int t, in
     if (!p.sigmoid) {
         sum = 0.0;
         for (int e = lane; e < p.experts; e += 32) {
-            const float l = logit_at<FP32>(p, t, e);
+            const float l = choice_logit<FP32>(p, t, e);
             if (l > neg_inf()) sum += exp(static_cast<double>(l) - static_cast<double>(top));
         }
         sum = warp_sum(sum);
     }
     const int e = static_cast<int>(list[min(lane, count - 1)].y);
-    const double l = static_cast<double>(logit_at<FP32>(p, t, e));
+    const double l = static_cast<double>(choice_logit<FP32>(p, t, e));
     const double c = (p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - static_cast<double>(top)) / sum) + static_cast<double>(p.bias[e]);
     int rank = 0;
     for (int o = 0; o < count; ++o) {
@@ -592,6 +604,12 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
         top = fmaxf(top, l[i]);
     }
     top = warp_max(top);
+    const bool overflowed = top == pos_inf();
+    if (overflowed) {
+        top = kLargest;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) l[i] = fminf(l[i], kLargest);
+    }
 
     // Scores are needed for the choice only with a bias or groups.
     constexpr bool scored = MODE != kLogits;
@@ -765,7 +783,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 const float own = fabsf(bh) + fabsf(hi);              // >= the score too
                 // (a choice of +inf is above every finite one and ties exactly with its like)
                 close = hi < pos_inf() && !(hi - lo > rel * (own + fabsf(bl) + fabsf(lo))) &&
-                        !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne));
+                        !(bh == bl && choice_logit<FP32>(p, t, mine) == choice_logit<FP32>(p, t, ne));
                 // Farther back may lie one with a larger error (its bias is at most
                 // 1 + |c| in size), or one behind exact ties of the last choice.
                 open = lane == p.k - 1 && hi < pos_inf() && !(hi - lo > rel * (own + 2.0f * fabsf(lo) + 1.0f));
@@ -774,7 +792,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             if (!close && __any_sync(kAll, open)) {
                 const int last = __shfl_sync(kAll, mine, p.k - 1);
                 const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
-                const float c = key_value(lk), b = p.bias[last], x = logit_at<FP32>(p, t, last);
+                const float c = key_value(lk), b = p.bias[last], x = choice_logit<FP32>(p, t, last);
                 const float low = c - rel * (fabsf(b) + fabsf(c));
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
@@ -822,7 +840,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
     }
 
     // Weights, FP32: lane j holds choice j.
-    const float lj = mine >= 0 ? logit_at<FP32>(p, t, mine) : neg_inf();
+    const float lj = mine >= 0 ? choice_logit<FP32>(p, t, mine) : neg_inf();
     float w = 0.0f;
     if (p.sigmoid) {
         if (mine >= 0) w = sigmoid(lj);
@@ -836,6 +854,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
     } else if (mine >= 0) {
         w = __fdiv_rn(expf(lj - top), total);
     }
+    if (overflowed && !p.sigmoid) w = __int_as_float(0x7fc00000);     // inf - inf: the row has no softmax
     if (lane < p.k) {
         p.ids[static_cast<long long>(t) * p.k + lane] = mine;
         p.weights[static_cast<long long>(t) * p.k + lane] = mine >= 0 ? w * p.scale : 0.0f;

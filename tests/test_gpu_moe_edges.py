@@ -112,3 +112,39 @@ def test_groups_of_an_expert_with_an_infinite_bias(E, groups, best, forced, scor
     for top in {1, max(1, groups // 2), groups - 1, groups}:
         for k in (1, 3):
             check_route(x, k, bias, score=score, n_groups=groups, top_groups=top, group_best=best)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("groups", [1, 8])
+@pytest.mark.parametrize("biased", [False, True])
+def test_logits_of_plus_infinity(biased, groups, renormalize, score, dtype):
+    """Chosen like the largest finite value; a softmax over one is NaN, and its
+    weights say so in every mode; other rows and sigmoids are as ever."""
+    T, E, k = 24, 64, 5
+    x = logits_of(T, E, dtype, 31)
+    x[0, 7] = INF
+    x[1, [3, 50, 51]] = INF
+    x[2] = INF
+    x[3, 9] = INF
+    x[3, 10:] = -INF
+    x[4, 20] = INF
+    x[4, 21] = float("nan")
+    x[5, 30] = INF
+    x[5, :30] = torch.finfo(dtype).min
+    x[6, 40] = INF                                             # an expert that its bias masks
+    bias = (torch.rand(E, generator=torch.Generator().manual_seed(2)) - 0.5) * 0.2
+    if biased:
+        bias[40] = -INF
+    kw = dict(score=score, renormalize=renormalize, n_groups=groups, top_groups=max(1, groups // 2))
+    w, ids = dg.det_moe_route(x.cuda(), k, bias=bias.cuda() if biased else None, **kw)
+    ok()
+    large = ref.f64(x)
+    large[large == INF] = np.finfo(np.float32).max
+    rw, rids = ref.route(large, k, bias=ref.f64(bias) if biased else None, **kw)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    w = ref.f64(w)
+    inf = (ref.f64(x) == INF).any(1) if score == "softmax" else np.zeros(T, dtype=bool)
+    assert np.isnan(w[inf][rids[inf] >= 0]).all() and not w[inf][rids[inf] < 0].any()
+    assert (np.abs(w - rw)[~inf] <= np.abs(rw[~inf]) * (2 * 20 + 64) * 2.0 ** -24 + 1e-37).all()
