@@ -254,6 +254,7 @@ struct Num<float> {
 template <>
 struct Num<double> {
     static __device__ __forceinline__ double of(float v) { return v; }
+    static __device__ __forceinline__ double half(double v) { return 0.5 * v; }
     static __device__ __forceinline__ double shfl(double v, int l) { return __shfl_sync(kAll, v, l); }
     static __device__ __forceinline__ double shfl_xor(double v, int o) { return __shfl_xor_sync(kAll, v, o); }
     static __device__ __forceinline__ double diff(float a, float b) { return static_cast<double>(a) - static_cast<double>(b); }
@@ -261,6 +262,7 @@ struct Num<double> {
 template <>
 struct Num<Df> {
     static __device__ __forceinline__ Df of(float v) { return Df{v, 0.0f}; }
+    static __device__ __forceinline__ Df half(Df v) { return Df{0.5f * v.hi, 0.5f * v.lo}; }
     static __device__ __forceinline__ Df shfl(Df v, int l) { return Df{__shfl_sync(kAll, v.hi, l), __shfl_sync(kAll, v.lo, l)}; }
     static __device__ __forceinline__ Df shfl_xor(Df v, int o)
     {
@@ -374,7 +376,10 @@ __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, i
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (lane == g[i]) val = p.group_best == 2 && b[i] > ninf && a[i] < pinf ? a[i] + b[i] : a[i];
+            if (lane == g[i]) {
+                val = N::half(a[i]);                  // as in keep_groups
+                if (p.group_best == 2 && b[i] > ninf && a[i] < pinf) val = val + N::half(b[i]);
+            }
     }
     int rank = 0;
     for (int h = 0; h < p.groups; ++h) {
@@ -419,10 +424,11 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, f
         b = fmaxf(fmaxf(b, b2), fminf(a, a2));
         a = fmaxf(a, a2);
     }
-    float val = a, amount = fabsf(a);
+    // Half of the group's value: two of the largest finite biases have a sum then.
+    float val = 0.5f * a, amount = fabsf(val);
     if (p.group_best == 2 && b > neg_inf()) {
-        val = a + b;
-        amount += fabsf(b);
+        val += 0.5f * b;
+        amount += 0.5f * fabsf(b);
     }
     int rank = 0;
     float next = neg_inf();                           // best value ranked below this group

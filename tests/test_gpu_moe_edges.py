@@ -148,3 +148,17 @@ def test_logits_of_plus_infinity(biased, groups, renormalize, score, dtype):
     inf = (ref.f64(x) == INF).any(1) if score == "softmax" else np.zeros(T, dtype=bool)
     assert np.isnan(w[inf][rids[inf] >= 0]).all() and not w[inf][rids[inf] < 0].any()
     assert (np.abs(w - rw)[~inf] <= np.abs(rw[~inf]) * (2 * 20 + 64) * 2.0 ** -24 + 1e-37).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("low,groups,top,k", [([1], 2, 2, 10), ([0], 2, 2, 12), ([1, 2], 3, 2, 12), ([0, 1, 2, 3], 4, 2, 9), ([5, 6], 8, 7, 32)])
+def test_groups_whose_biases_are_the_lowest_finite_value(low, groups, top, k, score, dtype):
+    """Their values are below FP32's range, and they are groups all the same."""
+    E, size = groups * 8, 8
+    x = logits_of(20, E, dtype, 8 + groups)
+    bias = torch.zeros(E)
+    for h in low:                                              # equal logits: exact ties, to the lower index
+        bias[h * size:(h + 1) * size] = torch.finfo(torch.float32).min
+        x[:, h * size:(h + 1) * size] = 0.5
+    check_route(x, k, bias, score=score, n_groups=groups, top_groups=top)
