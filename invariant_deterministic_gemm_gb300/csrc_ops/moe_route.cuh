@@ -19,7 +19,7 @@
 // decide it. Choices are compared in FP32, where each carries an error of a
 // few units in the last place; when two neighbours of the chosen order, the last
 // choice and any that lost (a large bias means a large error: not only the next
-// one), or the last kept and the first dropped group, are closer than FP32's error bound,
+// one), or a kept and a dropped group, are closer than FP32's error bound,
 // the warp decides again: the few candidates near the last choice in FP64, one
 // a lane; the groups whose place is open with pairs of FP32 values (about 43
 // bits), or in FP64 where a score is too small for those; and every expert so
@@ -412,9 +412,9 @@ __device__ __forceinline__ void scan_group(const RouteParams &p, const float *v,
 
 // Best groups of a token from the two best choices that each lane holds of its
 // group's (a, b; -inf: none). Returns the mask of the kept groups. When FP32 cannot tell
-// the last kept group from the first dropped one, `doubt` are the groups whose
-// place is open and `slots` how many of them stay; the mask then holds the
-// certain ones alone.
+// every kept group from every dropped one, `doubt` are the groups whose place is
+// open and `slots` how many of them stay; the mask then holds the certain ones
+// alone.
 __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, float b, int lane, uint32_t &doubt, int &slots)
 {
     const int shift = lane_shift(p.groups), lpg = 1 << shift;
@@ -431,13 +431,10 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, f
         amount += 0.5f * fabsf(b);
     }
     int rank = 0;
-    float next = neg_inf();                           // best value ranked below this group
 #pragma unroll 4
     for (int h = 0; h < p.groups; ++h) {
         const float o = __shfl_sync(kAll, val, h << shift);
-        const bool before = o > val || (o == val && h < g);
-        rank += before ? 1 : 0;
-        if (!before && h != g) next = fmaxf(next, o);
+        rank += (o > val || (o == val && h < g)) ? 1 : 0;
     }
     const bool leader = g < p.groups && sub == 0 && val > neg_inf();
     const bool kept = leader && rank < p.top_groups;
@@ -446,18 +443,16 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, f
     // one or two additions; scores below 1e-20 only absolutely. A value of +inf
     // (from a bias) is exact.
     const float err = val < pos_inf() ? (p.sigmoid ? kNearSigmoid : kNearSoftmax) * (amount + (p.bias ? 1.0f : 0.0f)) + 1e-25f : 0.0f;
-    const uint32_t last = __ballot_sync(kAll, kept && rank == p.top_groups - 1);
-    const uint32_t first = __ballot_sync(kAll, leader && rank == p.top_groups);
+    // Every kept group against every dropped one: errors go with the size of a
+    // group's choices, which its value, a sum, does not tell.
+    const uint32_t low = __reduce_min_sync(kAll, kept ? order_key(val - err) : 0xFFFFFFFFu);
+    const uint32_t high = __reduce_max_sync(kAll, leader && !kept ? order_key(val + err) : 0u);
     uint32_t lanes = __ballot_sync(kAll, kept);
-    if (last && first) {
-        const int il = __ffs(last) - 1, jf = __ffs(first) - 1;
-        const float low = __shfl_sync(kAll, val - err, il), high = __shfl_sync(kAll, val + err, jf);
-        if (!(low > high)) {
-            const uint32_t open = __ballot_sync(kAll, leader && !(val - err > high) && !(val + err < low));
-            lanes &= ~open;
-            slots = p.top_groups - __popc(lanes);
-            doubt = open;
-        }
+    if (low <= high) {
+        const uint32_t open = __ballot_sync(kAll, leader && order_key(val - err) <= high && order_key(val + err) >= low);
+        lanes &= ~open;
+        slots = p.top_groups - __popc(lanes);
+        doubt = open;
     }
     return lanes;
 }

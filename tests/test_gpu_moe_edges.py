@@ -162,3 +162,29 @@ def test_groups_whose_biases_are_the_lowest_finite_value(low, groups, top, k, sc
         bias[h * size:(h + 1) * size] = torch.finfo(torch.float32).min
         x[:, h * size:(h + 1) * size] = 0.5
     check_route(x, k, bias, score=score, n_groups=groups, top_groups=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("large", [64.0, 1024.0])
+def test_a_group_whose_large_biases_cancel(large, score):
+    """Groups of two whose values FP32 tells apart, and one with biases of both
+    signs, whose value is as small and whose error is not: wherever it comes
+    among them, the kept groups are those of 64 bits."""
+    T, G = 60, 8
+    g = torch.Generator().manual_seed(int(large))
+    for t in range(T):
+        value = 0.1 + 2e-5 * torch.randperm(G, generator=g).double()
+        first = value * (0.3 + 0.4 * torch.rand(G, generator=g, dtype=torch.float64))
+        s = torch.stack([first, value - first], 1)
+        h = t % (G - 1)
+        bias = torch.zeros(G, 2)
+        bias[h] = torch.tensor([large, -large])
+        if score == "softmax":                                 # the last group takes what is left, and no part
+            s[-1] = (1.0 - s[:-1].sum()) / 2
+            bias[-1] = -INF
+            x = torch.log(s)
+        else:
+            x = torch.log(s / (1.0 - s))
+        x = x.reshape(1, 2 * G).float()
+        for top in range(1, G - 1):
+            check_route(x, 2, bias.reshape(-1), score=score, n_groups=G, top_groups=top)
