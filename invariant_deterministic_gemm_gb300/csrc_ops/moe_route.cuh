@@ -246,12 +246,6 @@ __device__ __forceinline__ void exp_all(double (&x)[N])
 template <typename F>
 struct Num;
 template <>
-struct Num<float> {
-    static __device__ __forceinline__ float of(float v) { return v; }
-    static __device__ __forceinline__ float shfl(float v, int l) { return __shfl_sync(kAll, v, l); }
-    static __device__ __forceinline__ float shfl_xor(float v, int o) { return __shfl_xor_sync(kAll, v, o); }
-};
-template <>
 struct Num<double> {
     static __device__ __forceinline__ double of(float v) { return v; }
     static __device__ __forceinline__ double half(double v) { return 0.5 * v; }
@@ -457,7 +451,8 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams &p, float a, f
     return lanes;
 }
 
-// The choice with values of type F, for the few rows FP32 cannot decide.
+// The choice with values of type F, for the few rows FP32 cannot decide (with a
+// bias: without one the logits give the order).
 // Returns the chosen expert of rank `lane` (-1: none).
 template <bool FP32, typename F>
 __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lane, float top, uint32_t kept, F *v)
@@ -496,19 +491,13 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
             const int e = e0 + 32 * i + lane;
             if (e >= p.experts) continue;
             const F x = v[e];
-            const float bias = p.bias ? p.bias[e] : 0.0f;
+            const float bias = p.bias[e];
             const bool in = x > ninf && bias > neg_inf() && (p.groups == 1 || in_groups(p, kept, e));
-            F c = (sig ? one : x) / (sig ? one + x : sum);
-            if (p.bias) c = with_bias(c, bias);
-            v[e] = in ? c : ninf;
+            const F c = (sig ? one : x) / (sig ? one + x : sum);
+            v[e] = in ? with_bias(c, bias) : ninf;
         }
     }
     __syncwarp();
-    if (!p.bias) {                   // without a bias the logits give the order
-        for (int e = lane; e < p.experts; e += 32)
-            if (v[e] > ninf) v[e] = N::of(choice_logit<FP32>(p, t, e));
-        __syncwarp();
-    }
     int mine = -1;
 #pragma unroll 1
     for (int j = 0; j < p.k; ++j) {
@@ -623,7 +612,6 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
         for (int i = 0; i < PER; ++i) s += l[i] > neg_inf() ? expf(l[i] - top) : 0.0f;
         total = warp_sum(s);
     }
-    bool near = false;
     uint32_t kept = kAll;
     if constexpr (scored) {
         float c[PER], bias[PER];
@@ -731,12 +719,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             mine = static_cast<int>(gathered[lane].y);
         }
         if (biased && count > p.k) {
-            if (p.k < 32) {
-                lost_key = gathered[p.k].x;
-                lost = static_cast<int>(gathered[p.k].y);
-            } else {
-                near = true;                          // 32 choices leave no lane for the one that lost
-            }
+            lost_key = gathered[p.k].x;
+            lost = static_cast<int>(gathered[p.k].y);
         }
     } else {
         // Many keys reach the bound (ties, or many choices): one after the other.
@@ -805,7 +789,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 close = __any_sync(kAll, close);
             }
         }
-        if (close && !near && !emptied) {
+        if (close && !emptied) {
             // The groups stand; whatever may lie above the last choice is put in
             // order again: c >= the last choice less both errors (a score is at
             // most 1, so the other's bias is at most 1 + |c| in size). The last
@@ -833,8 +817,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 close = false;
             }
         }
-        near = near || close;
-        if (near) {
+        if (close) {
             if (far_logits(p, l, top)) mine = choose_again<FP32, double>(p, t, lane, top, kept, vd);
             else mine = choose_again<FP32, Df>(p, t, lane, top, kept, reinterpret_cast<Df *>(vd));
         }
