@@ -319,7 +319,7 @@ constexpr int kTileThreads = 256;
 __global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const QuantParams p, int row_tiles, int col_tiles)
 {
     begin();
-    __shared__ uint8_t tq[kBlock][kBlock + 4];
+    __shared__ __align__(4) uint8_t tq[kBlock][kBlock + 4];      // (also stored to four bytes at a time)
     __shared__ uint32_t wmax[kTileThreads / 32];
     const int ct = blockIdx.x % col_tiles;
     const int rt = blockIdx.x / col_tiles % row_tiles;
