@@ -111,7 +111,8 @@ det_gemm_status det_fp8_quantize_rows(const det_gemm_bf16 *x, const int32_t *row
  * [G+1]) each group's rows form their own blocks, one group after the other;
  * the blocks that exist number at most ceil(M/128) + G, which is what
  * max_blocks, the room in qt and s, has to be at least (max_blocks =
- * ceil(M/128) without offsets).
+ * ceil(M/128) without offsets). Blocks that no group has are left alone, or
+ * become zero where the bounds are reported.
  */
 det_gemm_status det_fp8_quantize_cols(const det_gemm_bf16 *x, const int32_t *offsets, uint8_t *qt, float *s, int64_t M,
                                       int64_t K, int64_t G, int64_t max_blocks, int64_t ldx, int64_t ldqt, int64_t lds,

@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
         // The group this block belongs to: a running sum of the groups'
         // blocks, 32 groups a step, by every warp for itself.
         int run = 0;
+        bool bad = false;
         r0 = r1 = -1;
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
             const int g = g0 + lane;
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
             if (g < p.groups) {
                 lo = min(max(p.offsets[g], 0), p.n);
                 hi = min(max(p.offsets[g + 1], lo), p.n);
+                bad |= p.offsets[g] != lo || p.offsets[g + 1] != hi;
             }
             const int nb = (hi - lo + kBlock - 1) / kBlock;
             int v = nb;
@@ -250,7 +252,21 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
             }
             run += __shfl_sync(kAll, v, 31);
         }
-        if (r0 < 0) return;          // past the last group's blocks (the whole CTA)
+        if (r0 < 0) {
+            // Past the last group's blocks (the whole CTA): it has seen all bounds, and
+            // there is always one. Where bounds made no sense a product may count
+            // a block here that no group filled: it finds zeros.
+            if (!__any_sync(kAll, bad)) return;
+            if (threadIdx.x == 0) atomicExch(p.status, kStatusInvalid);
+            for (int i = threadIdx.x; i < kColTile * (kBlock / 16); i += kColThreads) {
+                const int col = c0 + i / (kBlock / 16);
+                if (col < p.cols)
+                    *reinterpret_cast<uint4 *>(p.q + col * p.ldq + static_cast<long long>(blk) * kBlock + i % (kBlock / 16) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            if (threadIdx.x < kColTile && c0 + static_cast<int>(threadIdx.x) < p.cols) p.s[blk * p.lds + c0 + threadIdx.x] = 0.0f;
+            return;
+        }
     } else {
         r0 = blk * kBlock;
         r1 = min(p.n, r0 + kBlock);

@@ -561,6 +561,7 @@ det_gemm_status det_fp8_quantize_cols(const det_gemm_bf16 *x, const int32_t *off
     p.cols = static_cast<int>(K);
     p.groups = static_cast<int>(G);
     p.max_blocks = static_cast<int>(blocks);
+    p.status = d->word;
     const cudaError_t e = launch_quantize_cols(p, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "column quantiser launch");
 }

@@ -1,0 +1,44 @@
+"""Group bounds that make no sense, on the GPU: every operator that reads them
+reports them, and none computes with memory that nobody wrote."""
+import pytest
+import torch
+
+import invariant_deterministic_gemm_gb300 as dg
+from test_gpu_moe import rows_of
+
+pytestmark = pytest.mark.gpu
+
+
+def bounds_of(b):
+    return torch.tensor(b, dtype=torch.int32).cuda()
+
+
+def poison():
+    """What the next allocations get holds e4m3 and FP32 NaNs."""
+    torch.cuda.empty_cache()
+    keep = [torch.full((1 << 19,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    keep += [torch.full((1 << 23,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del keep
+
+
+def weight_gradient(dy, x, bounds):
+    poison()
+    off = bounds_of(bounds)
+    yt, sy = dg.det_fp8_quantize_cols(dy, off)
+    xt, sx = dg.det_fp8_quantize_cols(x, off)
+    seen = dg.det_gemm_check()
+    dW = dg.det_fp8_gemm_wgrad(yt, sy, xt, sx, off)
+    dg.det_gemm_check()
+    return seen, dW
+
+
+@pytest.mark.parametrize("M,bad,same", [(100, [0, 100, 128], [0, 100, 100]), (200, [0, 130, 250], [0, 130, 200]), (100, [0, 101, 110, 120], [0, 100, 100, 100]),
+                                        (129, [-5, 129, 1000], [0, 129, 129]), (300, [0] * 40 + [300, 1 << 30], [0] * 40 + [300, 300])])
+def test_bounds_that_leave_the_matrix(M, bad, same):
+    dy, x = rows_of(M, 136, 1, 1e-2), rows_of(M, 200, 2)
+    seen, got = weight_gradient(dy, x, bad)
+    assert seen == 1
+    seen, want = weight_gradient(dy, x, same)
+    assert seen == 0
+    assert torch.equal(got, want)
