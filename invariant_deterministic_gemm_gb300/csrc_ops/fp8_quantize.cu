@@ -21,6 +21,7 @@
 // [8192, 14336] along rows 52.6 us (6.7 TB/s; 61 us with eight elements a lane and
 // a 64-bit division a warp), along columns 65 us (5.4 TB/s; 78 us with tests at
 // every load); [8192, 4096] 16 and 20 us.
+#include "group_bounds.cuh"
 #include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
@@ -229,10 +230,14 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
             const int g = g0 + lane;
             int lo = 0, hi = 0;
-            if (g < p.groups) {
-                lo = min(max(p.offsets[g], 0), p.n);
-                hi = min(max(p.offsets[g + 1], lo), p.n);
-                bad |= p.offsets[g] != lo || p.offsets[g + 1] != hi;
+            for (;;) {               // a second time where the bounds turn out to make no sense
+                if (g < p.groups) {
+                    lo = group_bound(p.offsets, p.n, g, bad);
+                    hi = group_bound(p.offsets, p.n, g + 1, bad);
+                }
+                if (bad) break;
+                bad = __any_sync(kAll, g < p.groups && (p.offsets[g] != lo || p.offsets[g + 1] != hi || hi < lo));
+                if (!bad) break;
             }
             const int nb = (hi - lo + kBlock - 1) / kBlock;
             int v = nb;
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
             // Past the last group's blocks (the whole CTA): it has seen all bounds, and
             // there is always one. Where bounds made no sense a product may count
             // a block here that no group filled: it finds zeros.
-            if (!__any_sync(kAll, bad)) return;
+            if (!bad) return;
             if (threadIdx.x == 0) atomicExch(p.status, kStatusInvalid);
             for (int i = threadIdx.x; i < kColTile * (kBlock / 16); i += kColThreads) {
                 const int col = c0 + i / (kBlock / 16);
