@@ -1,9 +1,10 @@
 """Mixture-of-experts operators (include/det_ops.h) for PyTorch tensors.
 
 Argument marshalling only, in the manner of the det_gemm binding: every
-function takes CUDA tensors, checks their types and layouts, allocates what
-is not given with PyTorch (on the stream the work runs on) and calls the C
-function of the same name. The marshalling itself is native code
+function takes CUDA tensors of the current device (of `stream`'s, where one is
+given), checks their types and layouts, allocates what is not given with
+PyTorch (on the stream the work runs on) and calls the C function of the same
+name. The marshalling itself is native code
 (binding/ops_native.cpp), because a decode-sized call is bound by it. There is
 no fallback.
 

@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
@@ -97,6 +98,26 @@ float real(PyObject *o, const char *name)
         raise(PyExc_TypeError, "%s must be a number", name);
     }
     return static_cast<float>(v);
+}
+
+// The CUDA tensors among a call's arguments lie on the device that the work is
+// enqueued on, the current one: a kernel would follow another device's addresses,
+// in no order with that device's streams.
+void on_current_device(PyObject *const *a, Py_ssize_t n)
+{
+    const Tensor *first = nullptr;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(a[i])) continue;
+        const Tensor &t = THPVariable_Unpack(a[i]);
+        if (!t.is_cuda()) continue;
+        if (!first) first = &t;
+        else if (t.device() != first->device())
+            raise(PyExc_ValueError, "the tensors lie on different devices: %s and %s", first->device().str().c_str(),
+                  t.device().str().c_str());
+    }
+    if (first && first->device().index() != c10::cuda::current_device())
+        raise(PyExc_ValueError, "the tensors lie on %s, the current device is cuda:%d", first->device().str().c_str(),
+              static_cast<int>(c10::cuda::current_device()));
 }
 
 // `stack` row-major matrices; a plain matrix is a stack of one.
@@ -553,6 +574,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
         return nullptr;
     }
     try {
+        on_current_device(args, n);
         return F(args);
     } catch (const Raised &) {
         return nullptr;
