@@ -93,6 +93,8 @@ def lib() -> ctypes.CDLL:
         L.det_rmsnorm.restype = ctypes.c_int
         L.det_gemm_check.argtypes = [p]
         L.det_gemm_check.restype = ctypes.c_int
+        L.det_ops_check.argtypes = [p]
+        L.det_ops_check.restype = ctypes.c_int
         L.det_gemm_status_string.argtypes = [ctypes.c_int]
         L.det_gemm_status_string.restype = ctypes.c_char_p
         L.det_gemm_last_error_detail.argtypes = []

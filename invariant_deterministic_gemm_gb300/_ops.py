@@ -66,9 +66,12 @@ def _fp32(out_dtype):
 
 
 def _on(stream, fn, *args):
-    """fn(*args) with its work and its allocations on the given stream."""
+    """fn(*args) with its work and its allocations on the given stream: a
+    torch.cuda.Stream, or any object whose cuda_stream is a stream's handle."""
     if stream is None:
         return fn(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
     with torch.cuda.stream(stream):
         return fn(*args)
 
@@ -175,7 +178,7 @@ def det_embedding_grad(dy, tokens, vocab, scale=1.0, *, padding_idx=None, out_dt
 
 def det_ops_check(stream=None) -> int:
     """Synchronise the stream and return (and clear) these operators' device status."""
-    return _on(stream, _native.ops_check)
+    return int(_dg.lib().det_ops_check(_dg._stream_handle(stream)))
 
 
 def det_ops_debug_force_timeout(enable: bool) -> None:

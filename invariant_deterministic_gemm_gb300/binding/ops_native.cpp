@@ -556,8 +556,6 @@ PyObject *embedding_grad(Argv a)
     return wrap(out);
 }
 
-PyObject *ops_check(Argv) { return PyLong_FromLong(det_ops_check(stream())); }
-
 PyObject *force_timeout(Argv a)
 {
     det_ops_debug_force_timeout(PyObject_IsTrue(a[0]));
@@ -603,7 +601,6 @@ PyMethodDef g_methods[] = {
     method<gemm_wgrad, 7>("gemm_wgrad"),
     method<embedding, 4>("embedding"),
     method<embedding_grad, 8>("embedding_grad"),
-    method<ops_check, 0>("ops_check"),
     method<force_timeout, 1>("force_timeout"),
     {nullptr, nullptr, 0, nullptr},
 };

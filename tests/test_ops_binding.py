@@ -1,5 +1,10 @@
 """The native binding's checks that need no GPU: tensors that claim to lie on
-one (PyTorch's fake tensors) are refused before their memory is asked for."""
+one (PyTorch's fake tensors) are refused before their memory is asked for. And
+what of det_gemm's binding does not depend on it."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -40,3 +45,39 @@ def test_tensors_of_different_devices_are_refused(dg):
             with pytest.raises(ValueError, match="different devices: cuda:[01] and cuda:[01]"):
                 call()
                 pytest.fail("call %d was not refused" % i)
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+class Named:
+    """An object that names a stream, as any library may have them."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def test_the_check_takes_any_object_that_names_a_stream(dg):
+    status = dg.det_gemm_check(Named(0))
+    assert isinstance(status, int)
+    assert (status == 0) == torch.cuda.is_available()
+
+
+def test_the_check_needs_no_native_binding(dg):
+    code = ("import sys; sys.modules['invariant_deterministic_gemm_gb300._ops_native'] = None\n"
+            "import invariant_deterministic_gemm_gb300 as dg\n"
+            "class Named: cuda_stream = 0\n"
+            "assert isinstance(dg.det_gemm_check(Named()), int)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.gpu
+def test_operators_run_on_any_object_that_names_a_stream(dg):
+    side = torch.cuda.Stream()
+    x = torch.randn(100, 16, device="cuda")
+    want = dg.det_moe_route(x, 2)
+    torch.cuda.synchronize()
+    got = dg.det_moe_route(x, 2, stream=Named(side.cuda_stream))
+    assert dg.det_gemm_check(Named(side.cuda_stream)) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
