@@ -1,11 +1,13 @@
 """Builds libdet_gemm.so in-tree with nvcc for sm_103a (no GPU needed).
 
 Each .cu file under csrc/ (det_gemm) and csrc_ops/ (the mixture-of-experts
-operators) is compiled in parallel to an object under ``_build/`` and the objects are linked into ``libdet_gemm.so`` next to this
-file. The CUDA runtime is linked statically, so the library has no load-time
-dependency on libcuda (the driver is reached at run time). The native half of
-_ops.py (binding/) is built beside it as a Python extension against the
-installed PyTorch.
+operators) is compiled in parallel to an object under ``_build/`` and the
+objects are linked into ``libdet_gemm.so`` next to this file. The CUDA runtime
+is linked statically, so the library has no load-time dependency on libcuda
+(the driver is reached at run time). The native half of _ops.py (binding/) is
+built beside it as a Python extension against the installed PyTorch; where
+there is no C++ compiler or a header is missing, the library is built alone and
+the operators' Python functions say so when they are called.
 """
 from __future__ import annotations
 
@@ -65,13 +67,33 @@ def _compile(src: str, verbose: bool, ptxas_info: bool) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _binding_lacks() -> str:
+    """What the binding cannot be built without and is not there ('' if nothing)."""
+    if shutil.which(_cxx()) is None:
+        return "the C++ compiler %s" % _cxx()
+    for h in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+              os.path.join(_torch_dir(), "include", "torch", "csrc", "Exceptions.h")):
+        if not os.path.exists(h):
+            return h
+    return ""
+
+
 def _compile_binding(verbose: bool) -> str:
     """Compile the Python extension's object (g++, against PyTorch's headers)."""
     import torch
-    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = os.path.join(_torch_dir(), "include")
     obj = os.path.join(OBJDIR, "ops_native.o")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+    cmd = [_cxx(), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE, "-I", inc,
            "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
            "-I", sysconfig.get_paths()["include"], "-c", BINDING, "-o", obj]
@@ -96,10 +118,14 @@ def _link(cmd: list[str], target: str, verbose: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile (if stale) and link libdet_gemm.so and the binding; returns the library's path."""
+    """Compile (if stale) and link libdet_gemm.so and, where it can be built, the
+    binding; returns the library's path."""
     srcs = sources()
     stale = force or ptxas_info or _stale(LIB, srcs + headers())
     native = force or stale or _stale(NATIVE, [BINDING, os.path.join(INCLUDE, "det_ops.h"), os.path.join(INCLUDE, "det_gemm.h")])
+    if native and _binding_lacks():
+        print("the operators' Python binding is not built: no %s" % _binding_lacks(), file=sys.stderr)
+        native = False
     if not stale and not native:
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
@@ -113,9 +139,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if stale:
             _link([nvcc(), "-shared", *ARCH, "-o", None, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"], LIB, verbose)
         if native:
-            import torch
-            tl = os.path.join(os.path.dirname(torch.__file__), "lib")
-            _link([os.environ.get("CXX", "g++"), "-shared", "-o", None, binding.result(), "-L", PKG, "-l:libdet_gemm.so",
+            tl = os.path.join(_torch_dir(), "lib")
+            _link([_cxx(), "-shared", "-o", None, binding.result(), "-L", PKG, "-l:libdet_gemm.so",
                    "-L", tl, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ltorch",
                    "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + tl], NATIVE, verbose)
     if ptxas_info:

@@ -43,7 +43,11 @@ class _Unloaded:
     def __getattr__(self, name):
         global _native
         _dg.lib()                                     # raises if nothing was built
-        from . import _ops_native
+        try:
+            from . import _ops_native
+        except ImportError as e:
+            raise ImportError("the operators' native binding is not built or does not load (%s); _build.build() needs a C++ "
+                              "compiler and PyTorch's and Python's headers for it" % e) from e
         _native = _ops_native
         return getattr(_native, name)
 
