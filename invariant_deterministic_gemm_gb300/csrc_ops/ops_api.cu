@@ -92,10 +92,15 @@ struct Arr {
     bool empty() const { return rows <= 0 || cols <= 0 || mats <= 0; }
 };
 
+// More bytes than there are addresses; what is below fits 64-bit arithmetic.
+constexpr double kMaxBytes = 1ull << 57;
+
 det_gemm_status check(const Arr &a)
 {
     if (a.empty()) return DET_GEMM_OK;
     if (!a.p || a.ld < a.cols || a.ld > (int64_t{1} << 36)) return DET_GEMM_ERR_INVALID_ARG;
+    if ((static_cast<double>(a.mats - 1) * a.gap + static_cast<double>(a.rows - 1) * a.ld + a.cols) * a.es > kMaxBytes)
+        return DET_GEMM_ERR_INVALID_ARG;
     if (a.mats > 1 && (a.gap < (a.rows - 1) * a.ld + a.cols || a.gap > (int64_t{1} << 40))) return DET_GEMM_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(a.p) % a.align != 0 || a.ld * a.es % a.align != 0) return DET_GEMM_ERR_ALIGNMENT;
     if (a.mats > 1 && a.gap * a.es % a.align != 0) return DET_GEMM_ERR_ALIGNMENT;
@@ -266,7 +271,9 @@ det_gemm_status fp8_rows(const uint8_t *A, const float *sa, const uint8_t *W, co
     const int64_t nb = up(K, kBlock);
     det_gemm_status s;
     if (K > 0 && G > 0) {
-        if (!sa || !sb || sa_row < 0 || sa_blk < 0 || sb_row < nb) return DET_GEMM_ERR_INVALID_ARG;
+        if (!sa || !sb || sa_row < 0 || sa_blk < 0 || sb_row < nb ||
+            (static_cast<double>(M - 1) * sa_row + static_cast<double>(nb - 1) * sa_blk) * 4 > kMaxBytes)
+            return DET_GEMM_ERR_INVALID_ARG;
         if (grouped && !offsets) return DET_GEMM_ERR_INVALID_ARG;
         const Arr as{sa, 1, (M - 1) * sa_row + (nb - 1) * sa_blk + 1, int64_t{1} << 36, 4, 4};
         const Arr bs{sb, up(N, kBlock), nb, sb_row, 4, 4, G, gsb};
