@@ -90,6 +90,13 @@ int small(PyObject *o, const char *name)
     return static_cast<int>(std::clamp<int64_t>(integer(o, name), INT32_MIN, INT32_MAX));
 }
 
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
+}
+
 float real(PyObject *o, const char *name)
 {
     const double v = PyFloat_AsDouble(o);
@@ -294,7 +301,7 @@ PyObject *route(Argv a)
     const Tensor w = empty({l.T, std::max(k, 0)}, kF32, l.device), ids = empty({l.T, std::max(k, 0)}, kI32, l.device);
     check(det_moe_route(l.p, l.fp32, bias, ptr<float>(w), ptr<int32_t>(ids), l.T, l.E, l.ld, k, small(a[2], "score"),
                         small(a[4], "n_groups"), small(a[5], "top_groups"), small(a[6], "group_best"),
-                        PyObject_IsTrue(a[7]), real(a[8], "scale"), stream()),
+                        truth(a[7]), real(a[8], "scale"), stream()),
           "det_moe_route");
     return wrap(w, ids);
 }
@@ -310,7 +317,7 @@ PyObject *route_bwd(Argv a)
     const float *dw = static_cast<float *>(flat(a[0], "dweights", kF32, {l.T, k}));
     const Tensor d = empty({l.T, l.E}, l.dtype, l.device);
     check(det_moe_route_bwd(dw, l.p, l.fp32, ptr<int32_t>(ids), ptr(d), l.T, l.E, l.ld, l.E, k, small(a[3], "score"),
-                            PyObject_IsTrue(a[4]), real(a[5], "scale"), stream()),
+                            truth(a[4]), real(a[5], "scale"), stream()),
           "det_moe_route_bwd");
     return wrap(d);
 }
@@ -422,7 +429,7 @@ PyObject *quantize_tiles(Argv a)
 {
     const Tensor &t = tensor(a[0], "w");
     if (t.dim() != 2 && t.dim() != 3) raise(PyExc_ValueError, "w must be a 2-D or 3-D tensor");
-    const bool stack = t.dim() == 3, flip = PyObject_IsTrue(a[1]);
+    const bool stack = t.dim() == 3, flip = truth(a[1]);
     const Mat w = matrix(a[0], "w", kBF16, stack);
     const int64_t rt = blocks_of(w.rows), ct = blocks_of(w.cols), mats = stack ? w.mats : -1;
     const Tensor q = flip ? empty_mat(w.cols, w.rows, kE4M3, t.device(), mats) : empty_mat(w.rows, w.cols, kE4M3, t.device(), mats);
@@ -537,7 +544,7 @@ PyObject *embedding_grad(Argv a)
         raise(PyExc_ValueError, "dy and tokens disagree on the tokens: %lld vs %lld", static_cast<long long>(dy.rows),
               static_cast<long long>(t.n));
     const int64_t V = integer(a[2], "vocab");
-    const bool accumulate = PyObject_IsTrue(a[7]);
+    const bool accumulate = truth(a[7]);
     if (accumulate && a[6] == Py_None) raise(PyExc_ValueError, "accumulate needs out");
     int64_t pad = -1;
     if (a[4] != Py_None) {
@@ -558,7 +565,7 @@ PyObject *embedding_grad(Argv a)
 
 PyObject *force_timeout(Argv a)
 {
-    det_ops_debug_force_timeout(PyObject_IsTrue(a[0]));
+    det_ops_debug_force_timeout(truth(a[0]));
     Py_RETURN_NONE;
 }
 

@@ -81,3 +81,11 @@ def test_operators_run_on_any_object_that_names_a_stream(dg):
     got = dg.det_moe_route(x, 2, stream=Named(side.cuda_stream))
     assert dg.det_gemm_check(Named(side.cuda_stream)) == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_an_argument_without_a_truth_value_is_refused(dg):
+    both = torch.tensor([True, False])
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        dg.det_ops_debug_force_timeout(both)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        dg.det_fp8_quantize_tiles(torch.zeros(16, 16, dtype=torch.bfloat16), transposed=both)
