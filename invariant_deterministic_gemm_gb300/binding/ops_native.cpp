@@ -298,7 +298,8 @@ PyObject *route(Argv a)
     const Logits l = logits(a[0]);
     const int k = small(a[1], "top_k");
     const float *bias = static_cast<float *>(flat_or_null(a[3], "bias", kF32, {l.E}));
-    const Tensor w = empty({l.T, std::max(k, 0)}, kF32, l.device), ids = empty({l.T, std::max(k, 0)}, kI32, l.device);
+    const int64_t room = std::clamp(k, 0, DET_MOE_MAX_TOP_K);          // the library refuses any other
+    const Tensor w = empty({l.T, room}, kF32, l.device), ids = empty({l.T, room}, kI32, l.device);
     check(det_moe_route(l.p, l.fp32, bias, ptr<float>(w), ptr<int32_t>(ids), l.T, l.E, l.ld, k, small(a[2], "score"),
                         small(a[4], "n_groups"), small(a[5], "top_groups"), small(a[6], "group_best"),
                         truth(a[7]), real(a[8], "scale"), stream()),
@@ -326,7 +327,7 @@ PyObject *dispatch(Argv a)
 {
     const Tensor &ids = index(a[0], "ids", 2);
     const int64_t E = integer(a[1], "num_experts"), T = ids.size(0), k = ids.size(1);
-    const Tensor off = empty({std::max<int64_t>(E, -1) + 1}, kI32, ids.device()), rows = empty({T * k}, kI32, ids.device()),
+    const Tensor off = empty({std::clamp<int64_t>(E, -1, DET_MOE_MAX_EXPERTS) + 1}, kI32, ids.device()), rows = empty({T * k}, kI32, ids.device()),
                  slots = empty({T, k}, kI32, ids.device());
     check(det_moe_dispatch(ptr<int32_t>(ids), ptr<int32_t>(off), ptr<int32_t>(rows), ptr<int32_t>(slots), T, E,
                            static_cast<int>(std::min<int64_t>(k, INT32_MAX)), stream()),

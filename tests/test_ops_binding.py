@@ -89,3 +89,17 @@ def test_an_argument_without_a_truth_value_is_refused(dg):
         dg.det_ops_debug_force_timeout(both)
     with pytest.raises(RuntimeError, match="ambiguous"):
         dg.det_fp8_quantize_tiles(torch.zeros(16, 16, dtype=torch.bfloat16), transposed=both)
+
+
+@pytest.mark.gpu
+def test_what_the_library_refuses_is_not_allocated_first(dg):
+    x = torch.zeros(4096, 64, device="cuda")
+    ids = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for call in (lambda: dg.det_moe_route(x, 1 << 24), lambda: dg.det_moe_route(x, 33), lambda: dg.det_moe_route(x, -3),
+                 lambda: dg.det_moe_dispatch(ids, 1 << 40), lambda: dg.det_moe_dispatch(ids, 513), lambda: dg.det_moe_dispatch(ids, -9)):
+        with pytest.raises(dg.DetGemmError, match="INVALID_ARG"):
+            call()
+    assert torch.cuda.max_memory_allocated() - before < 4 << 20
