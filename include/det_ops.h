@@ -144,8 +144,8 @@ det_gemm_status det_fp8_gemm(const uint8_t *A, const float *sa, const uint8_t *W
 /*
  * The same per expert: rows [offsets[g], offsets[g+1]) of A with W_g (gw
  * elements apart, scales gsb apart). offsets (int32 [G+1]) is read on the
- * device; a bound below the ones before it counts as the largest of them.
- * Rows of C outside every group become zero.
+ * device. Rows of C outside every group become zero; all of them, where the
+ * bounds go down somewhere.
  */
 det_gemm_status det_fp8_gemm_grouped(const uint8_t *A, const float *sa, const uint8_t *W, const float *sb,
                                      const int32_t *offsets, void *C, int out_fp32, int64_t G, int64_t M, int64_t N,

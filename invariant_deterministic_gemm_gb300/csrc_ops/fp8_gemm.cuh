@@ -59,7 +59,6 @@
 #pragma once
 
 #include "det_gemm_kernel.cuh"
-#include "group_bounds.cuh"
 #include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
@@ -191,7 +190,6 @@ struct Fp8Shared {
     uint64_t full[16], empty[16], accf[8], acce[8], scale[12], drain[2], never;
     uint32_t tmem;
     int abort_flag;
-    int bad;                         // the group bounds make no sense
     int first[kMaxExperts + 1];      // first work unit of each group; weight gradient: first contraction block
 };
 
@@ -199,14 +197,18 @@ struct Unit {
     int group, row0, rows_end, col0, kblk0, nblk;    // rows_end: first row past the group
 };
 
+__device__ __forceinline__ int group_lo(const Fp8Params &p, int limit, int g) { return min(max(p.offsets[g], 0), limit); }
+
 // Fills first[] from the group bounds; one warp, then a barrier.
-// Bounds that decrease or leave [0, limit] are brought in order and reported.
+// Bounds that leave [0, limit] are clamped and reported. Rows' bounds that go down
+// are reported and leave no work, so that no row has two owners and the units
+// are never more than the host has counted: the outputs become zeros. (Weight
+// gradients have an output a group and blocks that are counted for any bounds.)
 template <int KIND>
 __device__ __forceinline__ void setup_groups(const Fp8Params &p, Fp8Shared &S, int tile_rows, int lane)
 {
     if (!p.offsets) {
         if (lane == 0) {
-            S.bad = 0;
             S.first[0] = 0;
             S.first[1] = KIND == kFp8Rows ? p.m_tiles * p.n_tiles : (p.kc + kBlock - 1) / kBlock;
         }
@@ -214,35 +216,32 @@ __device__ __forceinline__ void setup_groups(const Fp8Params &p, Fp8Shared &S, i
     }
     wait_for_last();
     const int limit = KIND == kFp8Rows ? p.rows : p.kc;
-    bool bad = false;
-    for (;;) {                       // a second time where the bounds turn out to make no sense
-        int units = 0;
-        bool wrong = false;
-        for (int g0 = 0; g0 < p.groups; g0 += 32) {
-            const int g = g0 + lane;
-            int u = 0;
-            if (g < p.groups) {
-                const int lo = group_bound(p.offsets, limit, g, bad), hi = group_bound(p.offsets, limit, g + 1, bad);
-                wrong |= p.offsets[g] != lo || p.offsets[g + 1] != hi || hi < lo;
-                u = KIND == kFp8Rows ? (hi - lo + tile_rows - 1) / tile_rows * p.n_tiles : (hi - lo + kBlock - 1) / kBlock;
-            }
-            int us = u;
+    int units = 0;
+    bool bad = false, down = false;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+        const int g = g0 + lane;
+        int u = 0;
+        if (g < p.groups) {
+            const int lo = group_lo(p, limit, g), hi = max(lo, group_lo(p, limit, g + 1));
+            bad |= p.offsets[g] != lo || p.offsets[g + 1] != hi;
+            if constexpr (KIND == kFp8Rows) down |= p.offsets[g + 1] < p.offsets[g];
+            u = KIND == kFp8Rows ? (hi - lo + tile_rows - 1) / tile_rows * p.n_tiles : (hi - lo + kBlock - 1) / kBlock;
+        }
+        int us = u;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(kFull, us, o);
-                if (lane >= o) us += x;
-            }
-            if (g < p.groups) S.first[g] = units + us - u;
-            units += __shfl_sync(kFull, us, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, us, o);
+            if (lane >= o) us += x;
         }
-        if (lane == 0) {
-            S.first[p.groups] = units;
-            S.bad = bad;
-        }
-        if (bad || !__any_sync(kFull, wrong)) break;
-        bad = true;
+        if (g < p.groups) S.first[g] = units + us - u;
+        units += __shfl_sync(kFull, us, 31);
     }
-    if (bad && lane == 0) atomicExch(p.status, kStatusInvalid);
+    if (lane == 0) S.first[p.groups] = units;
+    if (KIND == kFp8Rows && __any_sync(kFull, down)) {
+        __syncwarp();
+        for (int g = lane; g <= p.groups; g += 32) S.first[g] = 0;
+    }
+    if (bad) atomicExch(p.status, kStatusInvalid);
 }
 
 // Work unit u: row tiles vary fastest, sixteen at a time, so that the CTAs
@@ -271,8 +270,8 @@ __device__ __forceinline__ Unit unit_of(const Fp8Params &p, const Fp8Shared &S, 
     r.group = g;
     int lo = 0, hi = p.rows, mt = p.m_tiles;
     if (KIND == kFp8Rows && p.offsets) {
-        lo = group_bound(p.offsets, p.rows, g, S.bad);
-        hi = group_bound(p.offsets, p.rows, g + 1, S.bad);
+        lo = group_lo(p, p.rows, g);
+        hi = max(lo, group_lo(p, p.rows, g + 1));
         mt = (hi - lo + tile_rows - 1) / tile_rows;
     }
     const int span = kSpan * p.n_tiles;
@@ -394,12 +393,13 @@ __device__ __forceinline__ void store_fragment(const Fp8Params &p, uint32_t buf,
     }
 }
 
-// Rows of the output that no group owns become zero (grouped launches).
+// Rows of the output that no group owns become zero (grouped launches): those in
+// front of the first group and behind the last, or all.
 template <bool F32>
-__device__ __forceinline__ void zero_unowned(const Fp8Params &p, const Fp8Shared &S, int thread, int threads)
+__device__ __forceinline__ void zero_unowned(const Fp8Params &p, int units, int thread, int threads)
 {
     if (!p.offsets) return;
-    const int lo = group_bound(p.offsets, p.rows, 0, S.bad), hi = group_bound(p.offsets, p.rows, p.groups, S.bad);
+    const int lo = group_lo(p, p.rows, 0), hi = units ? max(lo, group_lo(p, p.rows, p.groups)) : lo;
     const float z[8] = {};
     for (int i = blockIdx.x; i < lo + p.rows - hi; i += gridDim.x) {
         const long long r = i < lo ? i : hi + (i - lo);
@@ -617,7 +617,7 @@ __device__ __forceinline__ void plain_epilogue(const Fp8Params &p, Fp8Shared &S,
             store_fragment<F32>(p, out, sum, row0, done.rows_end, done.group * p.og, col, lane);
         }
     }
-    if constexpr (KIND == kFp8Rows) zero_unowned<F32>(p, S, warp * 32 + lane, C::EPI_WARPS * 32);
+    if constexpr (KIND == kFp8Rows) zero_unowned<F32>(p, units, warp * 32 + lane, C::EPI_WARPS * 32);
 }
 
 // One thread: the whole loop of TMA copies.
@@ -898,7 +898,7 @@ __device__ __forceinline__ void swap_epilogue(const Fp8Params &p, Fp8Shared &S, 
             }
         }
     }
-    zero_unowned<F32>(p, S, warp * 32 + lane, 128);
+    zero_unowned<F32>(p, units, warp * 32 + lane, 128);
 }
 
 // One warp: the products of the scales, token by token, of a slot's blocks.

@@ -21,7 +21,6 @@
 // [8192, 14336] along rows 52.6 us (6.7 TB/s; 61 us with eight elements a lane and
 // a 64-bit division a warp), along columns 65 us (5.4 TB/s; 78 us with tests at
 // every load); [8192, 4096] 16 and 20 us.
-#include "group_bounds.cuh"
 #include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"
@@ -230,14 +229,10 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
             const int g = g0 + lane;
             int lo = 0, hi = 0;
-            for (;;) {               // a second time where the bounds turn out to make no sense
-                if (g < p.groups) {
-                    lo = group_bound(p.offsets, p.n, g, bad);
-                    hi = group_bound(p.offsets, p.n, g + 1, bad);
-                }
-                if (bad) break;
-                bad = __any_sync(kAll, g < p.groups && (p.offsets[g] != lo || p.offsets[g + 1] != hi || hi < lo));
-                if (!bad) break;
+            if (g < p.groups) {
+                lo = min(max(p.offsets[g], 0), p.n);
+                hi = min(max(p.offsets[g + 1], lo), p.n);
+                bad |= p.offsets[g] != lo || p.offsets[g + 1] != hi;
             }
             const int nb = (hi - lo + kBlock - 1) / kBlock;
             int v = nb;
@@ -247,7 +242,7 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
                 if (lane >= o) v += u;
             }
             const int first = run + v - nb;
-            const unsigned who = __ballot_sync(kAll, blk >= first && blk < first + nb);
+            const unsigned who = __ballot_sync(kAll, blk >= first && blk < first + nb && blk + 1 < p.max_blocks);
             if (who) {
                 const int at = __ffs(static_cast<int>(who)) - 1;
                 const int l = __shfl_sync(kAll, lo, at), h = __shfl_sync(kAll, hi, at), f = __shfl_sync(kAll, first, at);
@@ -258,10 +253,11 @@ __global__ void __launch_bounds__(kColThreads) quantize_cols_kernel(const QuantP
             run += __shfl_sync(kAll, v, 31);
         }
         if (r0 < 0) {
-            // Past the last group's blocks (the whole CTA): it has seen all bounds, and
-            // there is always one. Where bounds made no sense a product may count
-            // a block here that no group filled: it finds zeros.
-            if (!bad) return;
+            // Past the last group's blocks (the whole CTA), as the last block always is
+            // for bounds in order: it has seen all of them. Where bounds made no
+            // sense a product may count a block here that no group filled: it finds
+            // zeros.
+            if (!__any_sync(kAll, bad)) return;
             if (threadIdx.x == 0) atomicExch(p.status, kStatusInvalid);
             for (int i = threadIdx.x; i < kColTile * (kBlock / 16); i += kColThreads) {
                 const int col = c0 + i / (kBlock / 16);

@@ -638,7 +638,7 @@ det_gemm_status det_fp8_gemm_wgrad(const uint8_t *Yt, const float *sy, const uin
                                    int64_t ldsx, int64_t lddw, int64_t gdw, det_gemm_stream stream)
 {
     if (!ok_size(M) || !ok_size(N) || !ok_size(K) || G < 0 || G > DET_MOE_MAX_EXPERTS || (!offsets && G != 1) ||
-        max_blocks < up(M, kBlock) + (offsets ? G : 0) || !ok_size(max_blocks * kBlock))
+        max_blocks < up(M, kBlock) + (offsets ? G : 0) || !ok_size(max_blocks * kBlock) || !launchable(G * (up(M, kBlock) + 1)))
         return DET_GEMM_ERR_INVALID_ARG;
     if (N == 0 || K == 0 || G == 0) return DET_GEMM_OK;
     if (!launchable(up(N, 128) * up(K, 128) * G)) return DET_GEMM_ERR_INVALID_ARG;

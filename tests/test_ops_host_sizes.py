@@ -20,3 +20,10 @@ def test_rows_beyond_the_addresses(fn):
     tiles = fn("det_fp8_quantize_tiles")
     assert tiles(P, Q, R, None, None, 1 << 30, 64, 64, 64, 1 << 40, 64, 4096, 64, 4096, None) == INVALID
     assert tiles(P, Q, R, None, None, 1 << 30, 64, 64, 64, 4096, 64, 1 << 40, 64, 4096, None) == INVALID
+
+
+def test_blocks_of_any_bounds_are_counted(fn):
+    wgrad = fn("det_fp8_gemm_wgrad")
+    M, nb = 1 << 30, (1 << 23) + 512
+    ld = nb * 128
+    assert wgrad(P, Q, R, S, W, 2 * W, 0, 512, M, 16, 16, nb, ld, 16, ld, 16, 16, 256, None) == INVALID
