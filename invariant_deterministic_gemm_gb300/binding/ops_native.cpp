@@ -110,11 +110,15 @@ float real(PyObject *o, const char *name)
 // The CUDA tensors among a call's arguments lie on the device that the work is
 // enqueued on, the current one: a kernel would follow another device's addresses,
 // in no order with that device's streams.
+thread_local c10::DeviceIndex g_device = 0;      // the current device of this call
+
 void on_current_device(PyObject *const *a, Py_ssize_t n)
 {
     const Tensor *first = nullptr;
     for (Py_ssize_t i = 0; i < n; ++i) {
-        if (!THPVariable_Check(a[i])) continue;
+        // (asking of a plain number whether it is a tensor takes a tenth of a microsecond)
+        PyTypeObject *type = Py_TYPE(a[i]);
+        if (type == &PyLong_Type || type == &PyBool_Type || type == &PyFloat_Type || a[i] == Py_None || !THPVariable_Check(a[i])) continue;
         const Tensor &t = THPVariable_Unpack(a[i]);
         if (!t.is_cuda()) continue;
         if (!first) first = &t;
@@ -122,9 +126,11 @@ void on_current_device(PyObject *const *a, Py_ssize_t n)
             raise(PyExc_ValueError, "the tensors lie on different devices: %s and %s", first->device().str().c_str(),
                   t.device().str().c_str());
     }
-    if (first && first->device().index() != c10::cuda::current_device())
+    if (!first) return;
+    g_device = c10::cuda::current_device();
+    if (first->device().index() != g_device)
         raise(PyExc_ValueError, "the tensors lie on %s, the current device is cuda:%d", first->device().str().c_str(),
-              static_cast<int>(c10::cuda::current_device()));
+              static_cast<int>(g_device));
 }
 
 // `stack` row-major matrices; a plain matrix is a stack of one.
@@ -251,7 +257,7 @@ ScalarType out_type(PyObject *out, PyObject *fp32)
     return t;
 }
 
-det_gemm_stream stream() { return reinterpret_cast<det_gemm_stream>(c10::cuda::getCurrentCUDAStream().stream()); }
+det_gemm_stream stream() { return reinterpret_cast<det_gemm_stream>(c10::cuda::getCurrentCUDAStream(g_device).stream()); }
 
 // Raises DetGemmError for a status that is not OK.
 void check(det_gemm_status st, const char *name)
