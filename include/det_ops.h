@@ -45,8 +45,8 @@ extern "C" {
  * scores (without the bias), divided by their sum when renormalize != 0 (a
  * sigmoid's sum plus 1e-20), times scale. An expert whose logit is -inf or
  * NaN, or whose bias is, is masked; a choice that is left over is id -1 with
- * weight 0. A logit of +inf is chosen as the largest finite FP32 value would
- * be, and the softmax weights of its row are NaN. A bias of +inf puts its
+ * weight 0. A logit of +inf is chosen like the largest finite FP32 value (no
+ * smaller one goes before it), and the softmax weights of its row are NaN. A bias of +inf puts its
  * expert, and its group, first.
  * Which experts win is decided with 43 bits or more wherever FP32 cannot tell.
  * weights [T,top_k] FP32 and ids [T,top_k] are contiguous.

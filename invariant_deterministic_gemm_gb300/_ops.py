@@ -90,7 +90,7 @@ def det_moe_route(logits, top_k, *, score="softmax", bias=None, n_groups=1, top_
     Returns weights [T, top_k] FP32 and ids [T, top_k] int32, best first, ties
     to the lower index. Experts with a logit (or bias) of -inf or NaN are
     masked; a choice left over has id -1 and weight 0. A logit of +inf is
-    chosen as the largest finite FP32 value, and makes its row's softmax
+    chosen like the largest finite FP32 value, and makes its row's softmax
     weights NaN; a bias of +inf puts its expert first."""
     return _on(stream, _native.route, logits, top_k, _score(score), bias, n_groups, top_groups, group_best, renormalize, scale)
 

@@ -8,8 +8,8 @@
 //   win, ties to the lower index; w = score[ids], over their sum when
 //   renormalised, times `scale`. An expert whose logit is -inf or NaN is
 //   masked; choices that are left over are -1 with weight 0. A logit of +inf
-//   is chosen as the largest finite one would be; the softmax of its row, and
-//   so the row's weights, are NaN.
+//   is chosen like the largest finite one; the softmax of its row, and so the
+//   row's weights, are NaN.
 //
 // One warp owns a token, so a row's result is a function of that row alone:
 // the logits are read once, and everything else lives in registers. Bytes
@@ -65,15 +65,7 @@ __device__ __forceinline__ float logit_at(const RouteParams &p, int t, int e)
     else return bf_at(static_cast<const uint16_t *>(p.logits) + t * p.ldl + e);
 }
 
-// The same for the choice, where +inf counts as the largest finite value: so its
-// distance to the row's maximum is a number.
-constexpr float kLargest = 3.402823466e38f;
-template <bool FP32>
-__device__ __forceinline__ float choice_logit(const RouteParams &p, int t, int e)
-{
-    const float v = logit_at<FP32>(p, t, e);
-    return v > kLargest ? kLargest : v;              // a NaN stays one
-}
+constexpr float kLargest = 3.402823466e38f;         // what +inf counts as in the choice
 
 // A lane's PER neighbours from src[lane * PER] on, -inf past `experts`; in
 // 16-byte loads where the row is full and aligned.
@@ -262,12 +254,7 @@ struct Num<Df> {
     {
         return Df{__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)};
     }
-    // Beyond what exp_all takes lie experts that a bias masks alone: their share of a sum is nothing.
-    static __device__ __forceinline__ Df diff(float a, float b)
-    {
-        const Df d = two_sum(a, -b);
-        return fabsf(d.hi) < 60.0f ? d : Df{d.hi > 0.0f ? 60.0f : -60.0f, 0.0f};
-    }
+    static __device__ __forceinline__ Df diff(float a, float b) { return two_sum(a, -b); }
 };
 
 // A score and its expert's bias. An infinite bias is the choice itself: beside an
@@ -300,9 +287,9 @@ __device__ __forceinline__ F exp_sum(const RouteParams &p, int t, int lane, floa
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int e = e0 + 32 * i + lane;
-            const float l = e < p.experts ? choice_logit<FP32>(p, t, e) : neg_inf();
+            const float l = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
             in[i] = l > neg_inf();
-            x[i] = N::diff(in[i] ? l : top, top);
+            x[i] = N::diff(in[i] ? fminf(l, kLargest) : top, top);
         }
         exp_all(x);
 #pragma unroll
@@ -341,10 +328,10 @@ __device__ __forceinline__ uint32_t settle_groups(const RouteParams &p, int t, i
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int x = x0 + lane, e = (g[i] >> shift) * size + x;
-                const float l = x < size ? choice_logit<FP32>(p, t, e) : neg_inf();
+                const float l = x < size ? logit_at<FP32>(p, t, e) : neg_inf();
                 bias[i] = p.bias && x < size ? p.bias[e] : 0.0f;
                 in[i] = l > neg_inf() && bias[i] > neg_inf();
-                c[i] = N::diff(p.sigmoid ? 0.0f : in[i] ? l : top, p.sigmoid ? (in[i] ? l : 0.0f) : top);
+                c[i] = N::diff(p.sigmoid ? 0.0f : in[i] ? fminf(l, kLargest) : top, p.sigmoid ? (in[i] ? l : 0.0f) : top);
             }
             exp_all(c);
 #pragma unroll
@@ -470,9 +457,9 @@ __device__ __forceinline__ int choose_again(const RouteParams &p, int t, int lan
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int e = e0 + 32 * i + lane;
-            const float l = e < p.experts ? choice_logit<FP32>(p, t, e) : neg_inf();
+            const float l = e < p.experts ? logit_at<FP32>(p, t, e) : neg_inf();
             in[i] = l > neg_inf();
-            x[i] = N::diff(sig ? 0.0f : in[i] ? l : top, sig ? (in[i] ? l : 0.0f) : top);
+            x[i] = N::diff(sig ? 0.0f : in[i] ? fminf(l, kLargest) : top, sig ? (in[i] ? l : 0.0f) : top);
         }
         exp_all(x);
 #pragma unroll
@@ -534,13 +521,13 @@ __device__ __forceinline__ void order_candidates(const RouteParams &p, int t, in
     if (!p.sigmoid) {
         sum = 0.0;
         for (int e = lane; e < p.experts; e += 32) {
-            const float l = choice_logit<FP32>(p, t, e);
-            if (l > neg_inf()) sum += exp(static_cast<double>(l) - static_cast<double>(top));
+            const float l = logit_at<FP32>(p, t, e);
+            if (l > neg_inf()) sum += exp(static_cast<double>(fminf(l, kLargest)) - static_cast<double>(top));
         }
         sum = warp_sum(sum);
     }
     const int e = static_cast<int>(list[min(lane, count - 1)].y);
-    const double l = static_cast<double>(choice_logit<FP32>(p, t, e));
+    const double l = static_cast<double>(fminf(logit_at<FP32>(p, t, e), kLargest));
     const double c = (p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - static_cast<double>(top)) / sum) + static_cast<double>(p.bias[e]);
     int rank = 0;
     for (int o = 0; o < count; ++o) {
@@ -554,14 +541,16 @@ __device__ __forceinline__ void order_candidates(const RouteParams &p, int t, in
 }
 
 // Pairs of FP32 values hold what exp gives between -60 and 60: whether an
-// argument of the row, -l or l - top, lies elsewhere.
-template <int PER>
-__device__ __forceinline__ bool far_logits(const RouteParams &p, const float (&l)[PER], float top)
+// argument of the row, -l or l - top, lies elsewhere. (Read again: the repeats
+// are few, and their registers are the common path's.)
+template <bool FP32>
+__device__ __forceinline__ bool far_logits(const RouteParams &p, int t, int lane, float top)
 {
     bool far = false;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (l[i] > neg_inf()) far |= !(fabsf(p.sigmoid ? l[i] : l[i] - top) < 60.0f);
+    for (int e = lane; e < p.experts; e += 32) {
+        const float l = logit_at<FP32>(p, t, e);
+        if (l > neg_inf()) far |= !(fabsf(p.sigmoid ? l : fminf(l, kLargest) - top) < 60.0f);
+    }
     return __any_sync(kAll, far);
 }
 
@@ -594,15 +583,15 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
         top = fmaxf(top, l[i]);
     }
     top = warp_max(top);
-    const bool overflowed = top == pos_inf();
+
+    // Scores are needed for the choice only with a bias or groups.
+    constexpr bool scored = MODE != kLogits;
+    const bool overflowed = scored && top == pos_inf();
     if (overflowed) {
         top = kLargest;
 #pragma unroll
         for (int i = 0; i < PER; ++i) l[i] = fminf(l[i], kLargest);
     }
-
-    // Scores are needed for the choice only with a bias or groups.
-    constexpr bool scored = MODE != kLogits;
     const bool biased = MODE == kBias || (MODE == kGroups && p.bias != nullptr);
     uint32_t key[PER];
     float total = 1.0f;
@@ -652,7 +641,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             int slots = 0;
             kept = keep_groups(p, a, b, lane, doubt, slots);
             if (doubt)
-                kept |= far_logits(p, l, top) ? settle_groups<FP32, double>(p, t, lane, top, doubt, slots)
+                kept |= far_logits<FP32>(p, t, lane, top) ? settle_groups<FP32, double>(p, t, lane, top, doubt, slots)
                                               : settle_groups<FP32, Df>(p, t, lane, top, doubt, slots);
             stays = (kept >> (lane >> shift << shift)) & 1u;
         }
@@ -768,7 +757,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 const float own = fabsf(bh) + fabsf(hi);              // >= the score too
                 // (a choice of +inf is above every finite one and ties exactly with its like)
                 close = hi < pos_inf() && !(hi - lo > rel * (own + fabsf(bl) + fabsf(lo))) &&
-                        !(bh == bl && choice_logit<FP32>(p, t, mine) == choice_logit<FP32>(p, t, ne));
+                        !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne));
                 // Farther back may lie one with a larger error (its bias is at most
                 // 1 + |c| in size), or one behind exact ties of the last choice.
                 open = lane == p.k - 1 && hi < pos_inf() && !(hi - lo > rel * (own + 2.0f * fabsf(lo) + 1.0f));
@@ -777,14 +766,14 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             if (!close && __any_sync(kAll, open)) {
                 const int last = __shfl_sync(kAll, mine, p.k - 1);
                 const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
-                const float c = key_value(lk), b = p.bias[last], x = choice_logit<FP32>(p, t, last);
+                const float c = key_value(lk), b = p.bias[last], x = fminf(logit_at<FP32>(p, t, last), kLargest);
                 const float low = c - rel * (fabsf(b) + fabsf(c));
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int e = lane * PER + i;
                     if (key[i] == 0 || key[i] > lk || (key[i] == lk && e <= last)) continue;   // not one that lost
                     const float ce = key_value(key[i]), be = p.bias[e];
-                    if (!(ce + rel * (fabsf(be) + fabsf(ce)) < low) && !(be == b && l[i] == x)) close = true;
+                    if (!(ce + rel * (fabsf(be) + fabsf(ce)) < low) && !(be == b && fminf(logit_at<FP32>(p, t, e), kLargest) == x)) close = true;
                 }
                 close = __any_sync(kAll, close);
             }
@@ -818,13 +807,13 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
             }
         }
         if (close) {
-            if (far_logits(p, l, top)) mine = choose_again<FP32, double>(p, t, lane, top, kept, vd);
+            if (far_logits<FP32>(p, t, lane, top)) mine = choose_again<FP32, double>(p, t, lane, top, kept, vd);
             else mine = choose_again<FP32, Df>(p, t, lane, top, kept, reinterpret_cast<Df *>(vd));
         }
     }
 
     // Weights, FP32: lane j holds choice j.
-    const float lj = mine >= 0 ? choice_logit<FP32>(p, t, mine) : neg_inf();
+    const float lj = mine >= 0 ? logit_at<FP32>(p, t, mine) : neg_inf();
     float w = 0.0f;
     if (p.sigmoid) {
         if (mine >= 0) w = sigmoid(lj);
@@ -838,7 +827,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
     } else if (mine >= 0) {
         w = __fdiv_rn(expf(lj - top), total);
     }
-    if (overflowed && !p.sigmoid) w = __int_as_float(0x7fc00000);     // inf - inf: the row has no softmax
+    if (overflowed && !p.sigmoid) w = __int_as_float(0x7fc00000);     // inf - inf: the row has no softmax (by the logits alone w is one already)
     if (lane < p.k) {
         p.ids[static_cast<long long>(t) * p.k + lane] = mine;
         p.weights[static_cast<long long>(t) * p.k + lane] = mine >= 0 ? w * p.scale : 0.0f;
