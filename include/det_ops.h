@@ -18,7 +18,10 @@
  * inputs (DET_GEMM_ERR_INVALID_ARG). What only the device can see (a token
  * outside the vocabulary, group bounds that decrease or leave the matrix, a
  * bounded wait that expired) is made harmless there, set in a status word
- * and reported by det_ops_check().
+ * and reported by det_ops_check(). Not reported, because dropped pairs are
+ * ordinary: an expert id outside [0, E), and a pair or row index outside its
+ * range, count as -1. Sizes are below 2^31 - 4096, a vocabulary below 2^27 - 1
+ * for its gradient.
  */
 #ifndef DET_OPS_H
 #define DET_OPS_H

@@ -50,9 +50,10 @@
 // [8192, 4096] x [14336, 4096] takes 385 us (2.50 PFLOP/s), its weight gradient 498
 // us. A block of a 128 x 192 tile takes 315 ns (weight gradient 395); 285 without
 // the epilogue's reads and sums, 262 with operands from few lines of L2 too.
-// The MMAs alone are 196, and power is at its limit: what is left is small
-// beside its price. A tile's end adds 2 us, half of it stores that all CTAs
-// issue at once.
+// The MMAs alone are 196. What holds the 262 is not known: 40 KB a block and SM
+// in them are 156 bytes a ns, and the 128 x 128 tile's 32 KB in 217 ns are 151, so
+// it may be what an SM takes in. A tile's end adds 2 us, half of it stores that
+// all CTAs issue at once: a third of a tile of 14 blocks.
 //
 // Waits are bounded as in det_gemm's kernels (a timeout sets the status
 // word, every role leaves, copies and MMAs in flight are drained).

@@ -20,7 +20,12 @@
 // of two columns along columns; tests for edges only in tiles that have one).
 // [8192, 14336] along rows 52.6 us (6.7 TB/s; 61 us with eight elements a lane and
 // a 64-bit division a warp), along columns 65 us (5.4 TB/s; 78 us with tests at
-// every load); [8192, 4096] 16 and 20 us.
+// every load); [8192, 4096] 16 and 20 us. Gathered, 49152 rows of 4096 from 8192:
+// 85 us, where the gather alone takes 89. Weight tiles, [14336, 4096]: 44 us (4.0
+// TB/s), transposed 51 (3.4), where the bytes would take 26: a CTA loads its 32 KB,
+// waits for the tile's maximum and stores, and five CTAs an SM (48 registers) are
+// few to have loads under way meanwhile: warps wait for memory, and half of the
+// issue slots are empty.
 #include "launch.cuh"
 #include "ops_internal.h"
 #include "vec.cuh"

@@ -30,14 +30,17 @@
 // groups took 23.6 us in the mean over random inputs, the open groups alone
 // 18.8.
 //
-// On those 8192 x 256 FP32 logits the kernel takes 5.8 us by the logits alone,
-// 9.9 with sigmoid scores and a bias, 14.4 with eight groups besides, where
-// the bytes would take 1.3: instructions bound it, mostly integer and
-// comparisons. A lane holds neighbouring experts, so that it loads 16 bytes at a
-// time and a group's best choices are found in registers (every 32nd expert, and
-// groups through shared memory: 6.2, 10.9 and 16.3 us). Four warps a block
-// and 48 registers keep 40 warps on an SM to the end; 48 warps with 40 registers
-// spill and take 15.6.
+// On those 8192 x 256 FP32 logits the kernel takes 5.6 us by the logits alone,
+// 10.3 with sigmoid scores and a bias, 14.4 with eight groups besides, where the
+// bytes would take 1.3: instructions bound it, mostly integer and comparisons.
+// With groups a token takes 1270 of them; on 262144 tokens (330 us, 1.26 ns each)
+// 81 % of the issue slots are used. 8192 tokens at that pace are 10.3 us: the
+// rest is the start and the end, 2048 blocks on an SM's ten places being 1.35
+// rounds (58 % of the slots). A lane holds neighbouring experts, so that it loads
+// 16 bytes at a time and a group's best choices are found in registers (every
+// 32nd expert, and groups through shared memory, cost 0.4, 1.0 and 1.9 us more).
+// Four warps a block and 48 registers keep 40 warps on an SM to the end; 48 warps
+// with 40 registers spill and take 1.2 us more.
 #pragma once
 
 #include "launch.cuh"
@@ -168,7 +171,9 @@ __device__ __forceinline__ Df operator*(const Df &a, const Df &b)
     const float e = __fmaf_rn(a.hi, b.hi, -p);
     return quick_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, e)));
 }
-// Quotient by three corrected steps; no branches, so that independent ones overlap.
+// Quotient by long division: each of three steps takes the quotient of the leading
+// parts as the next digit and its product from the remainder, which stays a pair.
+// No branches, so that independent ones overlap.
 __device__ __forceinline__ Df operator/(const Df &a, const Df &b)
 {
     float r;

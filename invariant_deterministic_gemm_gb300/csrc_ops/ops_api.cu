@@ -227,9 +227,12 @@ det_gemm_status enqueue(const Fp8Args &x, Fp8Params &p, const Fp8Plan &plan, Dev
 }
 
 // Width of a weight's product's plain tile: 192 columns, or 128 where the last
-// round of one tile per SM would leave too many idle. A 128-wide tile takes
-// 0.69 (its blocks, 217 of 313 ns) to 1 (its end, 2 us) of a 192-wide one's
-// time; 0.75 with 32 blocks, 0.71 with 112.
+// round of one tile per SM would leave too many idle. Four rounds of 128-wide
+// tiles take 0.72 of four of 192-wide ones' time with 112 blocks (122 and 170 us)
+// and with 32 (36.0, 49.7), 0.74 with 14 and with 8, 0.76 with 4, 0.80 with 1 (9.4,
+// 11.7); one round 0.69 with 112, 0.75 with 32, 0.80 with 14, 0.90 with 1. Nothing
+// measured is chosen more than 2 % too slow for the one factor ([8192, 4096] from
+// 1024: 128 wide 45.7 us, 192 wide 46.5).
 int plain_width(int64_t row_tiles, int64_t cols, int sms)
 {
     const int64_t wide = up(row_tiles * up(cols, 192), sms) * 100, narrow = up(row_tiles * up(cols, 128), sms) * 72;
@@ -238,7 +241,19 @@ int plain_width(int64_t row_tiles, int64_t cols, int sms)
 
 // The tile of a product with a weight. Both tiles give the same bits; the
 // choice is about time. Few rows (per expert): the transposed tile, which
-// reads a weight once for up to 64 rows; otherwise the plain one.
+// reads a weight once for up to 64 rows; otherwise the plain one. With weights
+// from HBM (us, transposed of 16, 32 and 64 tokens, then plain):
+//   [12288, 4096]  16 rows 12.0 15.3 13.3 13.1    64 rows 21 23 14.0 13.4
+//   [4096, 14336]  16 rows 18.4 21.6 22.6 27.8    64 rows 42 32 23.5 28.6
+//   [14336, 1024]  16 rows 6.5 7.2 7.9 6.6        64 rows 9.4 9.5 8.4 6.9
+//   16 x [2048, 4096], as many rows an expert:    16 rows 25.4 25.8 27.1 33.4
+//     64 rows 46 31 29.6 30.6, 65 rows 53 38 38 30.6
+//   the same, uneven: 16 rows 31 25.9 27.4 33.4; 64 rows 45 39 33 30.3
+//   the same, all but one row each on one expert: 16 rows 32 32.7 27 33.7;
+//     64 rows 54 41 41 35
+// From 65 rows on the plain tile is the faster one everywhere. Up to 64 it is in
+// short contractions and where few experts have most rows (by up to a third: 8 x
+// [1792, 4096] at 64 uneven rows 22.2 and 14.8), which the host cannot see.
 Fp8Plan plan_rows(int64_t rows, int64_t cols, int64_t groups, bool grouped, int sms)
 {
     Fp8Plan pl{kFp8Rows, false, 128, 192};
