@@ -122,9 +122,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     binding; returns the library's path."""
     srcs = sources()
     stale = force or ptxas_info or _stale(LIB, srcs + headers())
-    native = force or stale or _stale(NATIVE, [BINDING, os.path.join(INCLUDE, "det_ops.h"), os.path.join(INCLUDE, "det_gemm.h")])
+    declared = [BINDING, os.path.join(INCLUDE, "det_ops.h"), os.path.join(INCLUDE, "det_gemm.h")]
+    native = force or stale or _stale(NATIVE, declared)
     if native and _binding_lacks():
         print("the operators' Python binding is not built: no %s" % _binding_lacks(), file=sys.stderr)
+        if os.path.exists(NATIVE) and _stale(NATIVE, declared):
+            os.remove(NATIVE)                         # made for other declarations than the library's
         native = False
     if not stale and not native:
         return LIB

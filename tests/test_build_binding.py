@@ -38,6 +38,18 @@ def test_no_python_headers(small, monkeypatch, capfd):
     assert "Python.h" in capfd.readouterr().err
 
 
+def test_a_binding_of_older_declarations_is_not_left_behind(small, monkeypatch):
+    old = small / "native.so"
+    old.write_text("")
+    os.utime(old, (1, 1))
+    monkeypatch.setenv("CXX", str(small / "no-such-compiler"))
+    _build.build()
+    assert not old.exists()
+    old.write_text("")                                        # newer than what it declares: it stays
+    _build.build(force=True)
+    assert old.exists()
+
+
 def test_a_call_without_the_binding_says_so():
     code = ("import sys; sys.modules['invariant_deterministic_gemm_gb300._ops_native'] = None\n"
             "import torch, invariant_deterministic_gemm_gb300 as dg\n"
