@@ -54,8 +54,10 @@ constexpr int kWarps = 4;
 // Bounds of the FP32 errors of two choices, relative to their scores' and
 // biases' sizes. A sigmoid: one unit of expf, an addition, a reciprocal of one
 // unit and the bias, below 8 * 2^-24; a softmax adds its sum's rounding, common
-// to all choices of a row but not to their biases, below 40 * 2^-24.
-constexpr float kNearSigmoid = 6e-7f, kNearSoftmax = 4e-6f;
+// to all choices of a row but not to their biases, and its argument's, 64 * 2^-24
+// of a score whose logit is up to 128 below the row's largest: below 92 * 2^-24.
+// Scores below FP32's normal numbers are off by units of 2^-149 besides.
+constexpr float kNearSigmoid = 6e-7f, kNearSoftmax = 5.5e-6f, kNearTiny = 1e-44f;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 const float bh = p.bias[mine], bl = p.bias[ne];
                 const float own = fabsf(bh) + fabsf(hi);              // >= the score too
                 // (a choice of +inf is above every finite one and ties exactly with its like)
-                close = hi < pos_inf() && !(hi - lo > rel * (own + fabsf(bl) + fabsf(lo))) &&
+                close = hi < pos_inf() && !(hi - lo > rel * (own + fabsf(bl) + fabsf(lo)) + kNearTiny) &&
                         !(bh == bl && logit_at<FP32>(p, t, mine) == logit_at<FP32>(p, t, ne));
                 // Farther back may lie one with a larger error (its bias is at most
                 // 1 + |c| in size), or one behind exact ties of the last choice.
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 10 : 6) route_kernel(c
                 const int last = __shfl_sync(kAll, mine, p.k - 1);
                 const uint32_t lk = __shfl_sync(kAll, my_key, p.k - 1);
                 const float c = key_value(lk), b = p.bias[last], x = fminf(logit_at<FP32>(p, t, last), kLargest);
-                const float low = c - rel * (fabsf(b) + fabsf(c));
+                const float low = c - rel * (fabsf(b) + fabsf(c)) - kNearTiny;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int e = lane * PER + i;

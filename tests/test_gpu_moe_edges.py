@@ -188,3 +188,19 @@ def test_a_group_whose_large_biases_cancel(large, score):
         x = x.reshape(1, 2 * G).float()
         for top in range(1, G - 1):
             check_route(x, 2, bias.reshape(-1), score=score, n_groups=G, top_groups=top)
+
+
+@pytest.mark.parametrize("far", [60.0, 85.0, 95.0, 102.0])
+@pytest.mark.parametrize("shift", [0.0, 0.37])
+def test_scores_far_below_the_rows_largest(far, shift):
+    """Choices among softmax scores of 1e-26 to below FP32's normal numbers, whose
+    logits are a few units in the last place apart: the argument's rounding alone
+    is as large. Biases of zero leave the logits' order."""
+    T, E = 100, 64
+    g = torch.Generator().manual_seed(int(far))
+    x = torch.full((T, E), -far) - torch.randint(0, 200, (T, E), generator=g).float() * 2.0 ** -17
+    x[:, 5] = 0.0
+    x = x + shift * torch.rand((T, 1), generator=g)
+    for k in (2, 8, 20):
+        check_route(x, k, torch.zeros(E))
+        check_route(x, k, torch.zeros(E), n_groups=4, top_groups=2)
