@@ -16,7 +16,8 @@ sections "Guarantees", "Ascend NPU backend", "Dtypes"):
   det_gemm_db(A[M,K], dC[M,N])                 -> dB[K,N] = A^T dC
   det_gemm_db_transposed(A[M,K], dC[M,N])      -> dB^T[N,K]
 The operators around them (routing, dispatch and combine, 8-bit products,
-embedding) are in _ops.py and exported here as well.
+embedding) are in _ops.py, attention (rotary positions, paged cache, one new
+token, packed sequences with gradients) is in _attn.py; both are exported here.
 Matrices are row-major with a leading dimension (``t.stride(0)``) and unit
 column stride; row-slices of bigger tensors are accepted as they are.
 """
@@ -478,9 +479,11 @@ __all__ = [
     "det_gemm_fwd_grouped",
 ]
 
-# The mixture-of-experts operators (include/det_ops.h) share this module's
-# library, checks and errors.
+# The mixture-of-experts (include/det_ops.h) and attention operators
+# (include/det_attn.h) share this module's library, checks and errors.
 from ._ops import *                                   # noqa: E402,F401,F403
 from ._ops import __all__ as _ops_all                 # noqa: E402
+from ._attn import *                                  # noqa: E402,F401,F403
+from ._attn import __all__ as _attn_all               # noqa: E402
 
-__all__ += _ops_all
+__all__ += _ops_all + _attn_all

@@ -1,11 +1,11 @@
 """Builds libdet_gemm.so in-tree with nvcc for sm_103a (no GPU needed).
 
 Each .cu file under csrc/ (det_gemm) and csrc_ops/ (the mixture-of-experts
-operators) is compiled in parallel to an object under ``_build/`` and the
+and attention operators) is compiled in parallel to an object under ``_build/`` and the
 objects are linked into ``libdet_gemm.so`` next to this file. The CUDA runtime
 is linked statically, so the library has no load-time dependency on libcuda
-(the driver is reached at run time). The native half of _ops.py (binding/) is
-built beside it as a Python extension against the installed PyTorch; where
+(the driver is reached at run time). The native half of _ops.py and _attn.py
+(binding/) is built beside it as a Python extension against the installed PyTorch; where
 there is no C++ compiler or a header is missing, the library is built alone and
 the operators' Python functions say so when they are called.
 """
@@ -44,7 +44,7 @@ def sources() -> list[str]:
 
 def headers() -> list[str]:
     hs = [os.path.join(d, f) for d in (CSRC, CSRC_OPS) for f in os.listdir(d) if f.endswith((".h", ".cuh"))]
-    return hs + [os.path.join(INCLUDE, f) for f in ("det_gemm.h", "det_ops.h")]
+    return hs + [os.path.join(INCLUDE, f) for f in ("det_gemm.h", "det_ops.h", "det_attn.h")]
 
 
 def _stale(target: str, deps: list[str]) -> bool:
@@ -122,7 +122,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     binding; returns the library's path."""
     srcs = sources()
     stale = force or ptxas_info or _stale(LIB, srcs + headers())
-    declared = [BINDING, os.path.join(INCLUDE, "det_ops.h"), os.path.join(INCLUDE, "det_gemm.h")]
+    declared = [BINDING] + [os.path.join(INCLUDE, f) for f in ("det_ops.h", "det_attn.h", "det_gemm.h")]
     native = force or stale or _stale(NATIVE, declared)
     if native and _binding_lacks():
         print("the operators' Python binding is not built: no %s" % _binding_lacks(), file=sys.stderr)

@@ -1,8 +1,8 @@
-// The native half of _ops.py: argument marshalling of the mixture-of-experts
-// operators. Each function reads its tensors' types, shapes, strides and
-// pointers, allocates the outputs with PyTorch's allocator and calls the C
-// function of det_ops.h on the current stream; all arithmetic is the
-// library's. A decode-sized call is bound by this work: through ctypes it
+// The native half of _ops.py and _attn.py: argument marshalling of the
+// mixture-of-experts and attention operators. Each function reads its tensors'
+// types, shapes, strides and pointers, allocates the outputs with PyTorch's
+// allocator and calls the C function of det_ops.h or det_attn.h on the current
+// stream; all arithmetic is the library's. A decode-sized call is bound by this work: through ctypes it
 // took 11 to 18 us of host time, most of it Python attribute look-ups and
 // argument conversions.
 #include <torch/csrc/Exceptions.h>
@@ -13,10 +13,12 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <string>
 
+#include "det_attn.h"
 #include "det_ops.h"
 
 namespace {
@@ -570,6 +572,205 @@ PyObject *embedding_grad(Argv a)
     return wrap(out);
 }
 
+// ---- attention
+
+// [tokens, heads, D] with any strides but D's.
+struct Rows {
+    bf16 *p;
+    int64_t T, H, D, t, h;
+};
+
+Rows rows_of(const Tensor &t, const char *name)
+{
+    if (t.dim() != 3) raise(PyExc_ValueError, "%s must be 3-D, got shape %s", name, shape_of(t).c_str());
+    if (t.size(2) > 1 && t.stride(2) != 1) raise(PyExc_ValueError, "%s must have unit stride in its last dimension", name);
+    return Rows{static_cast<bf16 *>(t.data_ptr()), t.size(0), t.size(1), t.size(2), t.stride(0), t.stride(1)};
+}
+Rows rows(PyObject *o, const char *name) { return rows_of(cuda_tensor(o, name, kBF16), name); }
+
+// The output given as `o`, or a new one.
+Tensor rows_out(PyObject *o, int64_t T, int64_t H, int64_t D, at::Device device)
+{
+    if (o == Py_None) return empty({T, H, D}, kBF16, device);
+    const Tensor &t = cuda_tensor(o, "out", kBF16);
+    if (t.dim() != 3 || t.size(0) != T || t.size(1) != H || t.size(2) != D)
+        raise(PyExc_ValueError, "out has shape %s, which is not the result's", shape_of(t).c_str());
+    return t;
+}
+
+void same(const Rows &a, const char *an, const Rows &b, const char *bn, bool tokens, bool heads)
+{
+    if (a.D != b.D || (tokens && a.T != b.T) || (heads && a.H != b.H))
+        raise(PyExc_ValueError, "%s and %s disagree: (%lld, %lld, %lld) vs (%lld, %lld, %lld)", an, bn, static_cast<long long>(a.T),
+              static_cast<long long>(a.H), static_cast<long long>(a.D), static_cast<long long>(b.T), static_cast<long long>(b.H),
+              static_cast<long long>(b.D));
+}
+
+// cos and sin [P, rot / 2].
+struct Turn {
+    const float *c, *s;
+    int64_t P, rot, ld;
+};
+Turn turn_of(PyObject *co, PyObject *si)
+{
+    const Tensor &c = cuda_tensor(co, "cos", kF32), &s = cuda_tensor(si, "sin", kF32);
+    if (c.dim() != 2 || s.sizes() != c.sizes() || s.strides() != c.strides() || (c.size(1) > 1 && c.stride(1) != 1))
+        raise(PyExc_ValueError, "cos and sin must be 2-D, of one shape and layout, with unit column stride");
+    return Turn{ptr<float>(c), ptr<float>(s), c.size(0), 2 * c.size(1), c.size(0) > 1 ? c.stride(0) : std::max<int64_t>(c.size(1), 1)};
+}
+
+struct Pages {
+    bf16 *p;
+    int64_t pages, size, heads, D, sp, ss, sh;
+};
+Pages pages_of(PyObject *o, const char *name)
+{
+    const Tensor &t = cuda_tensor(o, name, kBF16);
+    if (t.dim() != 4) raise(PyExc_ValueError, "%s must be 4-D, got shape %s", name, shape_of(t).c_str());
+    if (t.size(3) > 1 && t.stride(3) != 1) raise(PyExc_ValueError, "%s must have unit stride in its last dimension", name);
+    return Pages{static_cast<bf16 *>(t.data_ptr()), t.size(0), t.size(1), t.size(2), t.size(3), t.stride(0), t.stride(1), t.stride(2)};
+}
+void same(const Pages &k, const Pages &v)
+{
+    if (k.pages != v.pages || k.size != v.size || k.heads != v.heads || k.D != v.D)
+        raise(PyExc_ValueError, "k_cache and v_cache must have one shape");
+}
+
+float scale_of(PyObject *o, int64_t D) { return o == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(std::max<int64_t>(D, 1)))) : real(o, "scale"); }
+int64_t window_of(PyObject *o)
+{
+    if (o == Py_None) return 0;
+    const int64_t w = integer(o, "window");
+    if (w < 1) raise(PyExc_ValueError, "window must be at least 1 (None: no window)");
+    return w;
+}
+
+PyObject *rope(Argv a)
+{
+    const Rows x = rows(a[0], "x");
+    const Turn c = turn_of(a[1], a[2]);
+    const int32_t *pos = static_cast<int32_t *>(flat(a[3], "positions", kI32, {x.T}));
+    const Tensor out = rows_out(a[6], x.T, x.H, x.D, THPVariable_Unpack(a[0]).device());
+    const Rows y = rows_of(out, "out");
+    check(det_rope(x.p, c.c, c.s, pos, y.p, x.T, x.H, x.D, c.rot, c.P, truth(a[4]), truth(a[5]), x.t, x.h, c.ld, y.t, y.h, stream()),
+          "det_rope");
+    return wrap(out);
+}
+
+PyObject *kv_append(Argv a)
+{
+    const Rows k = rows(a[1], "k"), v = rows(a[2], "v");
+    same(k, "k", v, "v", true, true);
+    const Turn c = turn_of(a[3], a[4]);
+    const int32_t *pos = static_cast<int32_t *>(flat(a[5], "positions", kI32, {k.T})),
+                  *slots = static_cast<int32_t *>(flat(a[6], "slots", kI32, {k.T}));
+    const Pages kc = pages_of(a[7], "k_cache"), vc = pages_of(a[8], "v_cache");
+    same(kc, vc);
+    if (kc.heads != k.H || kc.D != k.D)
+        raise(PyExc_ValueError, "k and k_cache disagree on the heads: (%lld, %lld) vs (%lld, %lld)", static_cast<long long>(k.H),
+              static_cast<long long>(k.D), static_cast<long long>(kc.heads), static_cast<long long>(kc.D));
+    Rows q{}, y{};
+    Tensor out;
+    if (a[0] != Py_None) {
+        q = rows(a[0], "q");
+        same(q, "q", k, "k", true, false);
+        out = rows_out(a[10], q.T, q.H, q.D, THPVariable_Unpack(a[0]).device());
+        y = rows_of(out, "out");
+    } else if (a[10] != Py_None) {
+        raise(PyExc_ValueError, "out needs q");
+    }
+    check(det_kv_append(q.p, k.p, v.p, c.c, c.s, pos, slots, y.p, kc.p, vc.p, k.T, q.H, k.H, k.D, c.rot, c.P, kc.pages, kc.size,
+                        truth(a[9]), q.t, q.h, k.t, k.h, v.t, v.h, c.ld, y.t, y.h, kc.sp, kc.ss, kc.sh, vc.sp, vc.ss, vc.sh,
+                        stream()),
+          "det_kv_append");
+    if (a[0] == Py_None) Py_RETURN_NONE;
+    return wrap(out);
+}
+
+PyObject *attn_decode(Argv a)
+{
+    const Rows q = rows(a[0], "q");
+    const Pages kc = pages_of(a[1], "k_cache"), vc = pages_of(a[2], "v_cache");
+    same(kc, vc);
+    if (kc.D != q.D) raise(PyExc_ValueError, "q and k_cache disagree on the head's columns: %lld vs %lld", static_cast<long long>(q.D), static_cast<long long>(kc.D));
+    const Tensor &table = cuda_tensor(a[3], "table", kI32);
+    if (table.dim() != 2 || table.size(0) != q.T) raise(PyExc_ValueError, "table must have a row for each query, got shape %s", shape_of(table).c_str());
+    const int64_t most = table.size(1);
+    if (most > 1 && table.stride(1) != 1) raise(PyExc_ValueError, "table must be row-major with unit column stride");
+    const int32_t *lengths = static_cast<int32_t *>(flat(a[4], "lengths", kI32, {q.T}));
+    const at::Device dev = THPVariable_Unpack(a[0]).device();
+    const int64_t tokens = kc.size > 0 && most <= INT32_MAX / kc.size ? most * kc.size : 0;     // the library refuses more
+    const int64_t size = std::max<int64_t>(det_attn_decode_workspace(q.T, q.H, q.D, tokens), 256);
+    const Tensor ws = empty({size}, ScalarType::Byte, dev);
+    const Tensor out = rows_out(a[8], q.T, q.H, q.D, dev);
+    const Rows y = rows_of(out, "out");
+    check(det_attn_decode(q.p, kc.p, vc.p, ptr<int32_t>(table), lengths, y.p, q.T, q.H, kc.heads, q.D, kc.pages, kc.size, most,
+                          scale_of(a[5], q.D), window_of(a[6]), integer(a[7], "sinks"), q.t, q.h, kc.sp, kc.ss, kc.sh, vc.sp, vc.ss,
+                          vc.sh, q.T > 1 ? table.stride(0) : std::max<int64_t>(most, 1), y.t, y.h, ptr(ws), size, stream()),
+          "det_attn_decode");
+    return wrap(out);
+}
+
+// The bounds of packed sequences: queries' and keys', either may be None.
+struct Packed {
+    const int32_t *q, *k;
+    int64_t N;
+};
+Packed packed(PyObject *qb, PyObject *kb, int64_t T, int64_t S)
+{
+    if (qb == Py_None) {
+        if (kb != Py_None) raise(PyExc_ValueError, "k_bounds needs bounds");
+        return Packed{nullptr, nullptr, 1};
+    }
+    const Tensor &q = index(qb, "bounds", 1);
+    if (q.size(0) < 1) raise(PyExc_ValueError, "bounds must have an element more than there are sequences");
+    Packed r{ptr<int32_t>(q), nullptr, q.size(0) - 1};
+    if (kb != Py_None) r.k = static_cast<int32_t *>(flat(kb, "k_bounds", kI32, q.sizes()));
+    else if (T != S) raise(PyExc_ValueError, "q and k have %lld and %lld rows: k_bounds is needed", static_cast<long long>(T), static_cast<long long>(S));
+    return r;
+}
+
+PyObject *attn(Argv a)
+{
+    const Rows q = rows(a[0], "q"), k = rows(a[1], "k"), v = rows(a[2], "v");
+    same(q, "q", k, "k", false, false);
+    same(k, "k", v, "v", true, true);
+    const Packed b = packed(a[3], a[4], q.T, k.T);
+    const at::Device dev = THPVariable_Unpack(a[0]).device();
+    const Tensor out = rows_out(a[8], q.T, q.H, q.D, dev), lse = empty({q.H, q.T}, kF32, dev);
+    const Rows y = rows_of(out, "out");
+    check(det_attn(q.p, k.p, v.p, b.q, b.k, y.p, ptr<float>(lse), b.N, q.T, k.T, q.H, k.H, q.D, scale_of(a[5], q.D), window_of(a[6]),
+                   integer(a[7], "sinks"), q.t, q.h, k.t, k.h, v.t, v.h, y.t, y.h, stream()),
+          "det_attn");
+    return wrap(out, lse);
+}
+
+PyObject *attn_bwd(Argv a)
+{
+    const Rows d = rows(a[0], "dout"), q = rows(a[1], "q"), k = rows(a[2], "k"), v = rows(a[3], "v"), y = rows(a[4], "out");
+    same(q, "q", k, "k", false, false);
+    same(k, "k", v, "v", true, true);
+    same(d, "dout", q, "q", true, true);
+    same(y, "out", q, "q", true, true);
+    const float *lse = static_cast<float *>(flat(a[5], "lse", kF32, {q.H, q.T}));
+    const Packed b = packed(a[6], a[7], q.T, k.T);
+    const at::Device dev = THPVariable_Unpack(a[0]).device();
+    const int64_t size = std::max<int64_t>(det_attn_bwd_workspace(b.N, q.T, k.T, q.H, k.H, q.D), 256);
+    const Tensor ws = empty({size}, ScalarType::Byte, dev);
+    const Tensor dq = empty({q.T, q.H, q.D}, kBF16, dev), dk = empty({k.T, k.H, k.D}, kBF16, dev), dv = empty({k.T, k.H, k.D}, kBF16, dev);
+    const int64_t qt = q.H * q.D, kt = k.H * k.D;
+    check(det_attn_bwd(d.p, q.p, k.p, v.p, y.p, lse, b.q, b.k, ptr<bf16>(dq), ptr<bf16>(dk), ptr<bf16>(dv), b.N, q.T, k.T, q.H, k.H, q.D,
+                       scale_of(a[8], q.D), window_of(a[9]), integer(a[10], "sinks"), d.t, d.h, q.t, q.h, k.t, k.h, v.t, v.h, y.t, y.h,
+                       qt, q.D, kt, k.D, kt, k.D, ptr(ws), size, stream()),
+          "det_attn_bwd");
+    PyObject *r = PyTuple_New(3);
+    if (!r) throw Raised{};
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(dq));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(dk));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(dv));
+    return r;
+}
+
 PyObject *force_timeout(Argv a)
 {
     det_ops_debug_force_timeout(truth(a[0]));
@@ -615,6 +816,11 @@ PyMethodDef g_methods[] = {
     method<gemm_wgrad, 7>("gemm_wgrad"),
     method<embedding, 4>("embedding"),
     method<embedding_grad, 8>("embedding_grad"),
+    method<rope, 7>("rope"),
+    method<kv_append, 11>("kv_append"),
+    method<attn_decode, 9>("attn_decode"),
+    method<attn, 9>("attn"),
+    method<attn_bwd, 11>("attn_bwd"),
     method<force_timeout, 1>("force_timeout"),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -2,16 +2,14 @@
 // choice of tile, launches.
 #include "det_ops.h"
 #include "det_gemm_internal.h"
+#include "ops_host.h"
 #include "ops_internal.h"
-
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <initializer_list>
 #include <mutex>
 
 namespace deto {
@@ -21,19 +19,13 @@ __device__ int g_ops_status[4];
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t{1} << 31) - 4096;
 constexpr int kMaxDevices = 64;
-
-struct Device {
-    bool init = false;
-    det_gemm_status status = DET_GEMM_OK;
-    int sms = 0;
-    int *word = nullptr;
-};
 std::mutex g_mu;
 Device g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::atomic<int> g_force_timeout{0};
+
+}  // namespace
 
 det_gemm_status fail(det_gemm_status st, cudaError_t e, const char *where)
 {
@@ -80,69 +72,7 @@ det_gemm_status device(Device **out)
     return DET_GEMM_OK;
 }
 
-// A strided array: `rows` rows of `cols` elements, pitch `ld`, element size
-// `es`, in `mats` matrices `gap` elements apart. `align`: the base's and the
-// pitch's alignment in bytes.
-struct Arr {
-    const void *p;
-    int64_t rows, cols, ld;
-    int es, align;
-    int64_t mats = 1, gap = 0;
-    int64_t bytes() const { return ((mats - 1) * gap + (rows - 1) * ld + cols) * es; }
-    bool empty() const { return rows <= 0 || cols <= 0 || mats <= 0; }
-};
-
-// More bytes than there are addresses; what is below fits 64-bit arithmetic.
-constexpr double kMaxBytes = 1ull << 57;
-
-det_gemm_status check(const Arr &a)
-{
-    if (a.empty()) return DET_GEMM_OK;
-    if (!a.p || a.ld < a.cols || a.ld > (int64_t{1} << 36)) return DET_GEMM_ERR_INVALID_ARG;
-    if ((static_cast<double>(a.mats - 1) * a.gap + static_cast<double>(a.rows - 1) * a.ld + a.cols) * a.es > kMaxBytes)
-        return DET_GEMM_ERR_INVALID_ARG;
-    if (a.mats > 1 && (a.gap < (a.rows - 1) * a.ld + a.cols || a.gap > (int64_t{1} << 40))) return DET_GEMM_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(a.p) % a.align != 0 || a.ld * a.es % a.align != 0) return DET_GEMM_ERR_ALIGNMENT;
-    if (a.mats > 1 && a.gap * a.es % a.align != 0) return DET_GEMM_ERR_ALIGNMENT;
-    return DET_GEMM_OK;
-}
-
-bool overlap(const Arr &a, const Arr &b)
-{
-    if (a.empty() || b.empty() || !a.p || !b.p) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + static_cast<uintptr_t>(b.bytes()) && y < x + static_cast<uintptr_t>(a.bytes());
-}
-
-// All arrays well formed, and no output overlapping an input or another output.
-det_gemm_status check_all(std::initializer_list<Arr> in, std::initializer_list<Arr> out)
-{
-    for (const Arr &a : in) {
-        const det_gemm_status s = check(a);
-        if (s != DET_GEMM_OK) return s;
-    }
-    for (const Arr *o = out.begin(); o != out.end(); ++o) {
-        const det_gemm_status s = check(*o);
-        if (s != DET_GEMM_OK) return s;
-        for (const Arr &a : in)
-            if (overlap(*o, a)) return DET_GEMM_ERR_INVALID_ARG;
-        for (const Arr *b = out.begin(); b != o; ++b)
-            if (overlap(*o, *b)) return DET_GEMM_ERR_INVALID_ARG;
-    }
-    return DET_GEMM_OK;
-}
-
-Arr bf16(const void *p, int64_t r, int64_t c, int64_t ld) { return Arr{p, r, c, ld, 2, 16}; }
-Arr vec4(const void *p, int64_t n) { return Arr{p, 1, n, n, 4, 4}; }
-Arr mat8(const void *p, int64_t r, int64_t c, int64_t ld, int64_t mats = 1, int64_t gap = 0)
-{
-    return Arr{p, r, c, ld, 1, 16, mats, gap};
-}
-
-bool ok_size(int64_t v) { return v >= 0 && v <= kMaxRows; }
-bool launchable(int64_t blocks) { return blocks <= (int64_t{1} << 31) - 1; }
-cudaStream_t cs(det_gemm_stream s) { return reinterpret_cast<cudaStream_t>(s); }
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return g_encode; }
 
 unsigned long long timeout_ns()
 {
@@ -151,6 +81,10 @@ unsigned long long timeout_ns()
     long long ms = s ? std::atoll(s) : 1000;
     return static_cast<unsigned long long>(ms < 1 ? 1 : ms) * 1000000ull;
 }
+
+bool timeout_forced() { return g_force_timeout.load() != 0; }
+
+namespace {
 
 // [mats] x [rows, k] e4m3 matrix -> map with boxes of 128 contraction bytes x box_rows.
 bool encode(CUtensorMap *m, int rank, const void *p, int64_t k, int64_t rows, int64_t ld, int64_t mats, int64_t gap,
