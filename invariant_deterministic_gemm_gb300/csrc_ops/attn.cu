@@ -59,48 +59,6 @@ __device__ __forceinline__ void take(float *dst, const uint16_t *row, int D, int
     for (int c = lane; c < D; c += 32) dst[c] = bf_at(row + c);
 }
 
-__global__ void __launch_bounds__(32 * kWarps) attn_fwd_rows(const AttnParams p)
-{
-    begin();
-    __shared__ float qs[kWarps][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y, g = h / p.G;
-    const int t = blockIdx.x * kWarps + warp;
-    if (p.qb && t == 0 && h == 0) {
-        bool bad = false;
-        for (int n = lane; n < p.N; n += 32) {
-            const Seq s = seq_at(p, n);
-            bad |= s.q0 != p.qb[n] || s.q1 != p.qb[n + 1] || s.k0 != p.kb[n] || s.k1 != p.kb[n + 1];
-        }
-        if (bad) atomicExch(p.status, kStatusInvalid);
-    }
-    if (t >= p.T) return;
-    const Seq s = seq_at(p, p.qb ? seq_of(p.qb, p.N, t) : 0);
-    const int pos = t >= s.q0 && t < s.q1 ? s.position(t) : -1;
-    take(qs[warp], p.q.row(t, h), p.D, lane);
-    __syncwarp();
-    float m = -INFINITY, l = 0.0f, o[4] = {};
-    for (int j0 = 0; j0 <= pos; j0 += 32) {
-        const int j = j0 + lane;
-        const bool vis = sees(p, pos, j);
-        if (!__any_sync(kFull, vis)) continue;
-        const float x = vis ? p.scale * dot(qs[warp], p.k.row(s.k0 + j, g), p.D) : -INFINITY;
-        const float top = fmaxf(m, warp_max(x));
-        const float old = m == -INFINITY ? 0.0f : expf(m - top);
-        const float e = vis ? expf(x - top) : 0.0f;
-        l = l * old + warp_sum(e);
-        for (float &v : o) v *= old;
-        m = top;
-        unsigned live = __ballot_sync(kFull, vis);
-        for (; live; live &= live - 1) {
-            const int i = __ffs(live) - 1;
-            add(o, __shfl_sync(kFull, e, i), p.v.row(s.k0 + j0 + i, g), p.D, lane);
-        }
-    }
-    for (float &v : o) v = m == -INFINITY ? 0.0f : v / l;
-    put(p.out.row(t, h), o, p.D, lane);
-    if (lane == 0) p.lse[static_cast<long long>(h) * p.T + t] = m == -INFINITY ? -INFINITY : m + logf(l);
-}
-
 __global__ void __launch_bounds__(32 * kWarps) attn_delta(const AttnParams p)
 {
     begin();
@@ -226,12 +184,6 @@ __global__ void __launch_bounds__(32 * kWarps) attn_decode_rows(const DecodePara
 dim3 grid(int rows, int y) { return dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps), static_cast<unsigned>(y)); }
 
 }  // namespace
-
-cudaError_t launch_attn(const AttnParams &p, int, cudaStream_t s)
-{
-    attn_fwd_rows<<<grid(p.T, p.H), 32 * kWarps, 0, s>>>(p);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_attn_bwd(const AttnParams &p, int, cudaStream_t s)
 {

@@ -1,6 +1,7 @@
 // C entry points of include/det_attn.h: argument checks and launches.
 #include "det_attn.h"
 #include "attn_internal.h"
+#include "det_gemm_internal.h"
 #include "ops_host.h"
 
 #include <algorithm>
@@ -103,6 +104,24 @@ bool ok_heads(int64_t H, int64_t KV, int64_t D)
 bool ok_mask(float scale, int64_t window, int64_t sinks) { return scale > 0.0f && std::isfinite(scale) && window >= 0 && sinks >= 0; }
 int window_of(int64_t w) { return w == 0 || w > kMaxRows ? kNoWindow : static_cast<int>(w); }
 int sinks_of(int64_t s) { return static_cast<int>(std::min(s, kMaxRows)); }
+
+// Heads as (column, head, token), copied in boxes of 64 columns of one head and 128 tokens.
+bool encode(CUtensorMap *m, const void *p, int64_t T, int64_t H, int64_t D, int64_t t, int64_t h)
+{
+    std::memset(m, 0, sizeof *m);
+    if (T == 0) return true;                   // nothing will be copied
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(H > 1 ? h : D) * 2, static_cast<cuuint64_t>(T > 1 ? t : H * D) * 2};
+    cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+det_gemm_status no_map()
+{
+    detg::record_detail("tensor map");
+    return DET_GEMM_ERR_LAUNCH;
+}
 
 bool ok_turn(int64_t D, int64_t rot, int64_t P)
 {
@@ -257,7 +276,7 @@ static det_gemm_status ok_attn(const int32_t *q_bounds, const int32_t *k_bounds,
     if (!q_bounds && (k_bounds || N != 1)) return DET_GEMM_ERR_INVALID_ARG;
     if (q_bounds && !k_bounds && T != S) return DET_GEMM_ERR_INVALID_ARG;
     // Tiles and rows are counted in 32 bits.
-    if (!ok_size(T + S + 256 * (N + 1))) return DET_GEMM_ERR_INVALID_ARG;
+    if (!ok_size(T + S + 256 * (N + 1)) || !launchable((T / 256 + N + 1) * H)) return DET_GEMM_ERR_INVALID_ARG;
     return DET_GEMM_OK;
 }
 
@@ -279,6 +298,8 @@ static AttnParams attn_params(const int32_t *q_bounds, const int32_t *k_bounds, 
     p.window = window_of(window);
     p.sinks = sinks_of(sinks);
     p.status = d->word;
+    p.timeout_ns = timeout_ns();
+    p.force_timeout = timeout_forced();
     return p;
 }
 
@@ -303,7 +324,9 @@ det_gemm_status det_attn(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const d
     p.v = on(v, vt, vh);
     p.out = on(out, ot, oh);
     p.lse = lse;
-    const cudaError_t e = launch_attn(p, d->sms, cs(stream));
+    AttnMaps maps;
+    if (!encode(&maps.q, q, T, H, D, qt, qh) || !encode(&maps.k, k, S, KV, D, kt, kh) || !encode(&maps.v, v, S, KV, D, vt, vh)) return no_map();
+    const cudaError_t e = launch_attn(p, maps, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "attention launch");
 }
 

@@ -47,8 +47,14 @@ struct AttnParams {
     float scale;
     int window, sinks;
     int *status;
+    unsigned long long timeout_ns;
+    int force_timeout;
 };
-cudaError_t launch_attn(const AttnParams &p, int sms, cudaStream_t s);
+// Heads [T, H, D] as (column, head, token), boxes of 64 columns of 128 tokens.
+struct AttnMaps {
+    CUtensorMap q, k, v, dout;
+};
+cudaError_t launch_attn(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
 cudaError_t launch_attn_bwd(const AttnParams &p, int sms, cudaStream_t s);
 
 struct DecodeParams {

@@ -1,0 +1,197 @@
+// What the tensor-core attention kernels share: tiles of 128 rows in shared
+// memory and TMEM, which key blocks a range of queries sees, bounded waits.
+//
+// A tile is 128 rows (tokens of one head) of DH = 64 or 128 columns, in halves
+// of 64 columns of 128 bytes a row (TMA's 128-byte swizzle). As it lies it is a
+// K-major operand of a product over the columns (scores) and an MN-major
+// operand of a product over the rows (values, gradients): nothing is transposed.
+// Columns past D are zeros, written by TMA.
+#pragma once
+
+#include "attn_internal.h"
+#include "det_gemm_kernel.cuh"
+#include "launch.cuh"
+#include "ops_internal.h"
+#include "vec.cuh"
+
+namespace deto {
+
+using detg::elect_one;
+using detg::idesc_bf16;
+using detg::mbar_arrive;
+using detg::mbar_arrive_expect_tx;
+using detg::mbar_init;
+using detg::mma_bf16;
+using detg::mma_commit;
+using detg::reg_fence;
+using detg::sdesc;
+using detg::smem_u32;
+using detg::tc_fence_after;
+using detg::tc_fence_before;
+using detg::tmap_prefetch;
+using detg::tmem_ld32;
+using detg::tmem_st32;
+using detg::tmem_wait_ld;
+using detg::tmem_wait_st;
+
+constexpr int kTile = 128;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr unsigned kWarp = 0xFFFFFFFFu;
+
+// ---- waits
+
+struct Waits {
+    volatile int *abort_flag;
+    int *status;
+    unsigned long long timeout_ns;
+    __device__ bool one(uint32_t bar, uint32_t parity) const { return detg::wait_bounded(bar, parity, abort_flag, status, timeout_ns, true); }
+    __device__ bool drain(uint32_t bar, uint32_t parity) const { return detg::wait_bounded(bar, parity, abort_flag, status, timeout_ns, false); }
+    __device__ bool warp(uint32_t bar, uint32_t parity) const { return detg::warp_wait(bar, parity, abort_flag, status, timeout_ns); }
+};
+
+// ---- tensor maps and copies
+
+// Heads [T, H, D] as (column, head, token); a box is 64 columns of `rows` tokens of one head.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int head, int token)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(col), "r"(head), "r"(token)
+        : "memory");
+}
+template <int DH>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar, int head, int token)
+{
+#pragma unroll
+    for (int h = 0; h < DH / 64; ++h) load_rows(dst + h * kTile * 128, map, bar, h * 64, head, token);
+}
+
+// ---- products
+
+// A in TMEM (128 lanes, two BF16 of consecutive contraction elements a column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// d[128, 128] = A B^T over the columns of two tiles, `steps` of 16 columns.
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int steps)
+{
+    const uint64_t da = sdesc(a, 16u, 1024u), db = sdesc(b, 16u, 1024u);
+    constexpr uint32_t idesc = idesc_bf16(kTile, kTile, 0, 0);
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t at = (k >> 2) * (kTile * 128 / 16) + (k & 3) * 2;      // 16-byte units
+        mma_bf16(d, da + at, db + at, idesc, k != 0);
+    }
+}
+
+// d[128, D] (+)= A (TMEM, 128 x 128) times a tile's rows; n: D rounded up to 16.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint32_t b, int n, bool accumulate)
+{
+    const uint64_t db = sdesc(b, kTile * 128u, 1024u);
+    const uint32_t idesc = idesc_bf16(kTile, n, 0, 1);
+#pragma unroll
+    for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a_tmem + k * 8, db + k * (2048 / 16), idesc, accumulate || k != 0);
+}
+
+// ---- arithmetic
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---- which keys a range of positions sees
+
+// Queries at positions [lo, hi] of one sequence (lo may be negative: those see nothing).
+struct Positions {
+    int lo, hi;
+};
+
+// Blocks of 128 keys that any of them sees: [0, ns) and from w0 on, n together, ascending.
+struct Blocks {
+    int ns, w0, n;
+    __device__ int at(int i) const { return i < ns ? i : w0 + i - ns; }
+};
+__device__ __forceinline__ Blocks blocks_of(const AttnParams &p, Positions q)
+{
+    if (q.hi < 0) return Blocks{0, 0, 0};
+    Blocks b;
+    b.w0 = max(0, max(q.lo, 0) - p.window + 1) / kTile;
+    b.ns = min((p.sinks + kTile - 1) / kTile, b.w0);
+    b.n = b.ns + q.hi / kTile - b.w0 + 1;
+    return b;
+}
+// Some of the queries sees some key of block b.
+__device__ __forceinline__ bool sees_any(const AttnParams &p, Positions q, int b)
+{
+    const int a = b * kTile;
+    return a <= q.hi && (max(q.lo, 0) - (a + kTile - 1) < p.window || a < p.sinks);
+}
+// Every one of them sees every key of it.
+__device__ __forceinline__ bool sees_all(const AttnParams &p, Positions q, int b)
+{
+    const int a = b * kTile;
+    return a + kTile - 1 <= q.lo && (q.hi - a < p.window || a + kTile - 1 < p.sinks);
+}
+
+// ---- tiles of packed rows
+//
+// Sequence n's tiles of `rows` rows have the numbers from bounds[n] / rows + n on:
+// no two sequences share one, whatever their lengths, and nothing has to be
+// summed up first. Numbers that no tile has are skipped.
+__host__ __device__ constexpr int tile_slots(int rows_total, int sequences, int rows) { return rows_total / rows + (sequences > 1 ? sequences : 1); }
+
+__device__ __forceinline__ int clamped(const int32_t *bounds, int n, int limit) { return min(max(bounds[n], 0), limit); }
+
+// The sequence of tile number x, and how many of its tiles come before (x's tile may be past its end).
+__device__ __forceinline__ int tile_sequence(const int32_t *bounds, int N, int limit, int rows, int x, int &tile)
+{
+    if (!bounds) {
+        tile = x;
+        return 0;
+    }
+    int a = 0, b = N;
+    while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (clamped(bounds, mid, limit) / rows + mid <= x) a = mid;
+        else b = mid;
+    }
+    tile = x - (clamped(bounds, a, limit) / rows + a);
+    return a;
+}
+
+}  // namespace deto
