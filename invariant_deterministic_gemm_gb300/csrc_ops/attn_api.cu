@@ -276,7 +276,7 @@ static det_gemm_status ok_attn(const int32_t *q_bounds, const int32_t *k_bounds,
     if (!q_bounds && (k_bounds || N != 1)) return DET_GEMM_ERR_INVALID_ARG;
     if (q_bounds && !k_bounds && T != S) return DET_GEMM_ERR_INVALID_ARG;
     // Tiles and rows are counted in 32 bits.
-    if (!ok_size(T + S + 256 * (N + 1)) || !launchable((T / 256 + N + 1) * H)) return DET_GEMM_ERR_INVALID_ARG;
+    if (!ok_size(T + S + 256 * (N + 1)) || !launchable((T / 128 + N + 1) * H) || !launchable((S / 128 + N + 1) * KV)) return DET_GEMM_ERR_INVALID_ARG;
     return DET_GEMM_OK;
 }
 
@@ -369,7 +369,11 @@ det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, 
     p.dq = on(dq, dqt, dqh);
     p.dk = on(dk, dkt, dkh);
     p.dv = on(dv, dvt, dvh);
-    const cudaError_t e = launch_attn_bwd(p, d->sms, cs(stream));
+    AttnMaps maps;
+    if (!encode(&maps.q, q, T, H, D, qt, qh) || !encode(&maps.k, k, S, KV, D, kt, kh) || !encode(&maps.v, v, S, KV, D, vt, vh) ||
+        !encode(&maps.dout, dout, T, H, D, dot, doh))
+        return no_map();
+    const cudaError_t e = launch_attn_bwd(p, maps, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "attention gradient launch");
 }
 

@@ -1,0 +1,871 @@
+// Gradients of packed attention.
+//
+//   P_ij = 2^(s_ij - lse_i log2(e)), s_ij = scale log2(e) q_i.k_j
+//   delta_i = dout_i.out_i, dS_ij = P_ij (dout_i.v_j - delta_i)
+//   dv_j = sum_i P_ij dout_i, dk_j = scale sum_i dS_ij q_i, dq_i = scale sum_j dS_ij k_j
+//
+// Two launches, each of which writes its outputs once, in a fixed order of
+// sums: no atomics. The first takes 128 queries of a head and walks the keys
+// that they see (three products a block: scores, dout v^T, dq), and writes delta
+// for the second, which takes 128 keys of a KV head and walks the queries that
+// see them, all heads that share it (four products: both transposed score
+// matrices, dv, dk). The scores are made twice: seven products where five would
+// do with dq added up by atomics, whose order changes bits.
+//
+// In both, a row is a TMEM lane; two warpgroups take half of a block's columns
+// each. P and dS go back to TMEM in the place of the scores they came from,
+// rounded to BF16 (as the tensor core wants it beside BF16 operands), and are
+// the left operand of the next product from there; dS is made of the unrounded P.
+//   warps 0-3, 4-7   P and dS of a block's first and last 64 columns
+//   warp 8           copies (TMA)
+//   warp 9           issues the products from one thread
+//   warp 10          second launch: lse and delta of the queries, into shared memory
+//   warp 10, 11      rows that no sequence owns
+// What is masked does not reach the results: masked elements are replaced, and
+// in blocks that are seen in part, rows of the right operands that are not
+// finite are taken out and added to those that see them afterwards.
+#include "attn_tile.cuh"
+
+#include <atomic>
+#include <cmath>
+
+namespace deto {
+namespace {
+
+constexpr int kThreads = 384, kLaunchRegs = 168, kMathRegs = 208, kServiceRegs = 88;
+static_assert(kMathRegs * 256 + kServiceRegs * 128 <= kLaunchRegs * kThreads, "register split");
+constexpr uint32_t kGap = 32;        // columns between the halves of P (or dS): 32 of 64
+
+// ---- what both do
+
+// P of 32 columns: 2^(s c + l) for the row's (or, PER_COLUMN, each column's) l; masked elements zero.
+__device__ __forceinline__ void exp_block(uint32_t (&s)[32], uint64_t c2, uint64_t l2)
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float lo, hi;
+        unpair(fma2(pair(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, l2), lo, hi);
+        s[2 * j] = __float_as_uint(exp2_fast(lo));
+        s[2 * j + 1] = __float_as_uint(exp2_fast(hi));
+    }
+}
+__device__ __forceinline__ void lds4(uint32_t at, uint64_t &a, uint64_t &b) { asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at)); }
+
+__device__ __forceinline__ uint32_t pack_words(uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); }
+
+// 32 FP32 words as 16 of BF16, into TMEM.
+__device__ __forceinline__ void put16(uint32_t at, const uint32_t (&v)[32])
+{
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_words(v[2 * j], v[2 * j + 1]);
+    detg::tmem_st16(at, w);
+}
+
+// Stores a warp's 32 rows of [128, D] sums in TMEM (times f) as BF16, through shared memory (its rows of a tile's place) in
+// whole lines. Columns of 16-byte chunks [c0, c1) of the row.
+template <int DH>
+__device__ __forceinline__ void store_sums(uint32_t tmem, uint32_t tile, int warp, int lane, int x0, int x1, float f, bool some)
+{
+    const int row = warp * 32 + lane;
+#pragma unroll 1
+    for (int x = x0; x < x1; ++x) {
+        uint32_t o[32];
+        if (some) {
+            tmem_ld32(tmem + 32 * x, o);
+            tmem_wait_ld();
+            reg_fence(o);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = some ? pack_bf16(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f) : 0u;
+            const int chunk = 4 * x + q;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) * 16)),
+                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                         : "memory");
+        }
+    }
+    __syncwarp();
+}
+// Rows [warp * 32, + 32) below `rows`, `chunks` chunks each from chunk c0 on.
+template <int CH>
+__device__ __forceinline__ void copy_rows_out(const Heads &out, long long token, int head, uint32_t tile, int warp, int lane, int c0, int rows, int D)
+{
+    constexpr int RW = 32 / CH;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += RW) {
+        const int r = warp * 32 + r0 + lane / CH, chunk = c0 + lane % CH;
+        uint4 y;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                     : "r"(tile + (chunk >> 3) * (kTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) * 16))
+                     : "memory");
+        if (r < rows && chunk * 8 < D) *reinterpret_cast<uint4 *>(out.row(token + r, head) + chunk * 8) = y;
+    }
+}
+
+// Rows of one axis that no sequence owns become zero in the arrays given.
+__device__ void zero_outside(const int32_t *bounds, int N, int limit, int heads, int D, const Heads &a, const Heads *b, int thread, int threads)
+{
+    if (!bounds) return;
+    const int lo = N > 0 ? clamped(bounds, 0, limit) : 0, hi = N > 0 ? max(lo, clamped(bounds, N, limit)) : 0;
+    const long long rows = static_cast<long long>(lo + limit - hi) * heads;
+    for (long long i = blockIdx.x; i < rows; i += gridDim.x) {
+        const int r = static_cast<int>(i / heads), h = static_cast<int>(i % heads), t = r < lo ? r : hi + r - lo;
+        for (int c = thread * 8; c < D; c += threads * 8) {
+            *reinterpret_cast<uint4 *>(a.row(t, h) + c) = make_uint4(0, 0, 0, 0);
+            if (b) *reinterpret_cast<uint4 *>(b->row(t, h) + c) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// ------------------------------------------------------------ queries: dq
+
+template <int DH>
+struct QCfg {
+    static constexpr int TILE = kTile * DH * 2;
+    static constexpr int SLOTS = DH == 128 ? 5 : 8;
+    static constexpr int OFF_RING = 2 * TILE;        // query rows and dout's first
+    static constexpr int OFF_DELTA = OFF_RING + SLOTS * TILE;       // [2][128] floats
+    static constexpr int OFF_SHARED = OFF_DELTA + 1024;
+    static constexpr int SMEM = OFF_SHARED + 384 + 1024;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct QWork {
+    Seq s;
+    int head, kv, row0, rows;
+    Positions pos;
+    Blocks blocks;
+};
+struct QShared {
+    uint64_t q_full, full[8], empty[8], scores[2], dp, read, ds, done, drain, never;
+    uint32_t tmem;
+    int abort_flag, poison, some;
+    QWork work;
+};
+static_assert(sizeof(QShared) <= 384, "shared state");
+
+__device__ __forceinline__ bool find_queries(const AttnParams &p, int unit, int slots, QWork &w)
+{
+    if (p.qb && p.N == 0) return false;
+    w.head = unit % p.H;
+    w.kv = w.head / p.G;
+    int tile;
+    const int n = tile_sequence(p.qb, p.N, p.T, kTile, slots - 1 - unit / p.H, tile);
+    w.s = seq_at(p, n);
+    const long long row0 = w.s.q0 + static_cast<long long>(kTile) * tile;
+    if (row0 >= w.s.q1) return false;
+    w.row0 = static_cast<int>(row0);
+    w.rows = min(kTile, w.s.q1 - w.row0);
+    const int first = w.s.position(w.row0);
+    w.pos = Positions{first, first + w.rows - 1};
+    w.blocks = blocks_of(p, w.pos);
+    return true;
+}
+
+template <int DH>
+__device__ void q_copy(const AttnParams &p, const AttnMaps &maps, QShared &S, uint32_t base, const Waits &wait)
+{
+    using C = QCfg<DH>;
+    const QWork w = S.work;
+    if (w.blocks.n == 0 || (p.force_timeout && !wait.one(smem_u32(&S.never), 0))) return;
+    mbar_arrive_expect_tx(smem_u32(&S.q_full), 2 * C::TILE);
+    load_tile<DH>(base, &maps.q, smem_u32(&S.q_full), w.head, w.row0);
+    load_tile<DH>(base + C::TILE, &maps.dout, smem_u32(&S.q_full), w.head, w.row0);
+    int slot = 0;
+    uint32_t round = 0, loaded = 0, parity = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < 2 * w.blocks.n; ++i) {
+        if (!wait.one(smem_u32(&S.empty[slot]), round ^ 1u)) {
+            ok = false;
+            break;
+        }
+        const uint32_t bar = smem_u32(&S.full[slot]);
+        mbar_arrive_expect_tx(bar, C::TILE);
+        load_tile<DH>(base + C::OFF_RING + slot * C::TILE, (i & 1) ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i >> 1) * kTile);
+        loaded |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | (round << slot);
+        if (++slot == C::SLOTS) {
+            slot = 0;
+            round ^= 1u;
+        }
+    }
+    if (!ok || *wait.abort_flag) {
+        wait.drain(smem_u32(&S.q_full), 0);
+        for (int i = 0; i < C::SLOTS; ++i)
+            if (loaded & (1u << i)) wait.drain(smem_u32(&S.full[i]), (parity >> i) & 1u);
+    }
+}
+
+// TMEM: scores of even and odd blocks, dout v^T, dq. dS takes the scores' place, so the next dout v^T can be made as soon as
+// the last has been read, and the next but one's scores once dq has taken dS.
+template <int DH>
+__device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Waits &wait)
+{
+    using C = QCfg<DH>;
+    const QWork w = S.work;
+    const uint32_t ring = base + C::OFF_RING, tm = S.tmem;
+    const int steps = (p.D + 15) / 16, n = w.blocks.n;
+    bool ok = n == 0 || wait.one(smem_u32(&S.q_full), 0), issued = false;
+    auto arrived = [&](int seq) {
+        ok = ok && wait.one(smem_u32(&S.full[seq % C::SLOTS]), (seq / C::SLOTS) & 1);
+        return ok;
+    };
+    auto scores = [&](int i) {
+        if (!arrived(2 * i)) return;
+        tc_fence_after();
+        mma_scores(tm + (i & 1) * kTile, base, ring + 2 * i % C::SLOTS * C::TILE, steps);
+        mma_commit(smem_u32(&S.scores[i & 1]));
+        issued = true;
+    };
+    auto dp = [&](int i) {
+        if (!arrived(2 * i + 1)) return;
+        tc_fence_after();
+        mma_scores(tm + 2 * kTile, base + C::TILE, ring + (2 * i + 1) % C::SLOTS * C::TILE, steps);
+        mma_commit(smem_u32(&S.dp));
+        mma_commit(smem_u32(&S.empty[(2 * i + 1) % C::SLOTS]));
+        issued = true;
+    };
+    if (ok && n > 0) scores(0);
+    if (ok && n > 0) dp(0);
+    if (ok && n > 1) scores(1);
+    for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n) {
+            ok = wait.one(smem_u32(&S.read), i & 1);
+            if (ok) dp(i + 1);
+        }
+        ok = ok && wait.one(smem_u32(&S.ds), i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tm + 3 * kTile, tm + (i & 1) * kTile, ring + 2 * i % C::SLOTS * C::TILE, steps * 16, i > 0, kGap);
+        mma_commit(smem_u32(&S.empty[2 * i % C::SLOTS]));
+        if (i + 2 < n) scores(i + 2);
+    }
+    if (ok) {
+        mma_commit(smem_u32(&S.done));
+    } else if (issued) {
+        mma_commit(smem_u32(&S.drain));
+        wait.drain(smem_u32(&S.drain), 0);
+    }
+}
+
+// Adds the keys' values that make_finite took out to the queries that see them.
+__device__ __noinline__ void q_add_taken(const AttnParams &p, const QWork &w, uint32_t out, int position, int c0, int c1)
+{
+    for (int c = c0; c < c1; c += 8) {
+        uint32_t o[8];
+        detg::tmem_ld8(out + c, o);
+        tmem_wait_ld();
+        detg::reg_fence8(o);
+        for (int i = 0; i < w.blocks.n; ++i) {
+            const int b = w.blocks.at(i);
+            if (sees_all(p, w.pos, b)) continue;
+            for (int j = b * kTile; j < (b + 1) * kTile && j <= position; ++j) {
+                if (!sees(p, position, j)) continue;
+                float f[8];
+                unpack8(load8(p.k.row(w.s.k0 + j, w.kv), c, p.D), f);
+                for (int e = 0; e < 8; ++e)
+                    if (!isfinite(f[e])) o[e] = __float_as_uint(__uint_as_float(o[e]) + f[e]);
+            }
+        }
+        __syncwarp();
+        detg::tmem_st8(out + c, o);
+        tmem_wait_st();
+    }
+}
+
+template <int DH>
+__device__ void q_math(const AttnParams &p, QShared &S, uint32_t base, const Waits &wait, int half, int warp, int lane)
+{
+    using C = QCfg<DH>;
+    const QWork &w = S.work;
+    const int row = warp * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tm = S.tmem + lanes;
+    const bool live = row < w.rows;
+    const int position = live ? w.pos.lo + row : -1;
+    const long long at = static_cast<long long>(w.head) * p.T + w.row0 + row;
+    // delta: a half of the row's columns each, joined in shared memory, the first half first.
+    float part = 0.0f;
+    if (live) {
+        const uint16_t *a = p.dout.row(w.row0 + row, w.head), *b = p.out.row(w.row0 + row, w.head);
+        uint4 x[DH / 16], y[DH / 16];
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i) {
+            const int c = half * (DH / 2) + 8 * i;
+            if (c < p.D) {
+                x[i] = *reinterpret_cast<const uint4 *>(a + c);
+                y[i] = *reinterpret_cast<const uint4 *>(b + c);
+            } else {
+                x[i] = y[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i) {
+            float f[8], g[8];
+            unpack8(x[i], f);
+            unpack8(y[i], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part = fmaf(f[e], g[e], part);
+        }
+    }
+    float *deltas = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&S) - 1024);
+    deltas[half * kTile + row] = part;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float delta = deltas[row] + deltas[kTile + row];
+    const float lse = live ? p.lse[at] : 0.0f;
+    if (live && half == 0) p.delta[at] = delta;
+    const float c = p.scale * kLog2e, off = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    const uint64_t c2 = pair(c, c), l2 = pair(off, off), d2 = pair(-delta, -delta);
+    bool ok = true;
+    const int n = w.blocks.n;
+    for (int i = 0; i < n; ++i) {
+        const int b = w.blocks.at(i);
+        const bool full = sees_all(p, w.pos, b);
+        const uint32_t ts = tm + (i & 1) * kTile + half * 64;
+        ok = wait.warp(smem_u32(&S.scores[i & 1]), (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[2][32];
+        tmem_ld32(ts, s[0]);
+        tmem_ld32(ts + 32, s[1]);
+        tmem_wait_ld();
+        reg_fence(s[0]);
+        reg_fence(s[1]);
+        exp_block(s[0], c2, l2);
+        exp_block(s[1], c2, l2);
+        const int a = b * kTile + half * 64, last = position - a, first = first_seen(p, position, a), sink = p.sinks - a;
+        if (!full) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k > last || (k < first && k >= sink)) s[k >> 5][k & 31] = 0u;
+        }
+        ok = wait.warp(smem_u32(&S.dp), i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (!full) {
+            // Both score matrices of the block have been made: its keys may be changed for the last product. The other
+            // half's threads wait for the same, and dq for both.
+            const int r = half * 64 + (row & 63);
+            if (row < 64 && make_finite<DH>(base + C::OFF_RING + 2 * i % C::SLOTS * C::TILE, r, min(kTile, w.s.keys() - b * kTile))) S.poison = 1;
+            __syncwarp();
+        }
+        uint32_t d[2][32];
+        tmem_ld32(tm + 2 * kTile + half * 64, d[0]);
+        tmem_ld32(tm + 2 * kTile + half * 64 + 32, d[1]);
+        tmem_wait_ld();
+        reg_fence(d[0]);
+        reg_fence(d[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.read));
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float lo, hi;
+                unpair(mul2(add2(pair(__uint_as_float(d[x][2 * j]), __uint_as_float(d[x][2 * j + 1])), d2),
+                            pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1]))), lo, hi);
+                d[x][2 * j] = __float_as_uint(lo);
+                d[x][2 * j + 1] = __float_as_uint(hi);
+            }
+        if (!full) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k > last || (k < first && k >= sink)) d[k >> 5][k & 31] = 0u;
+        }
+        put16(ts, d[0]);
+        put16(ts + 16, d[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.ds));
+    }
+    if (ok) ok = wait.warp(smem_u32(&S.done), 0);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t out = tm + 3 * kTile;
+    if (n > 0 && *reinterpret_cast<volatile int *>(&S.poison)) q_add_taken(p, w, out, position, half * (DH / 2), (half + 1) * (DH / 2));
+    // Half of the columns each, through the query tile's place.
+    store_sums<DH>(out, base, warp, lane, half * (DH / 64), (half + 1) * (DH / 64), p.scale, n > 0);
+    copy_rows_out<DH / 16>(p.dq, w.row0, w.head, base, warp, lane, half * (DH / 16), w.rows, p.D);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps maps, const int slots)
+{
+    using C = QCfg<DH>;
+    extern __shared__ uint8_t attn_smem[];
+    const uint32_t raw = smem_u32(attn_smem), base = (raw + 1023u) & ~1023u;
+    QShared &S = *reinterpret_cast<QShared *>(attn_smem + (base - raw) + C::OFF_SHARED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        S.abort_flag = 0;
+        S.poison = 0;
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(smem_u32(&S.full[i]), 1);
+            mbar_init(smem_u32(&S.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&S.q_full), 1);
+        mbar_init(smem_u32(&S.scores[0]), 1);
+        mbar_init(smem_u32(&S.scores[1]), 1);
+        mbar_init(smem_u32(&S.dp), 1);
+        mbar_init(smem_u32(&S.read), 8);
+        mbar_init(smem_u32(&S.ds), 8);
+        mbar_init(smem_u32(&S.done), 1);
+        mbar_init(smem_u32(&S.drain), 1);
+        mbar_init(smem_u32(&S.never), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8 && lane == 0 && p.T > 0 && p.S > 0) {
+        tmap_prefetch(&maps.q);
+        tmap_prefetch(&maps.k);
+        tmap_prefetch(&maps.v);
+        tmap_prefetch(&maps.dout);
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    begin();
+    if (threadIdx.x == 32) {
+        QWork w;
+        S.some = find_queries(p, blockIdx.x, slots, w);
+        if (S.some) S.work = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Waits wait{&S.abort_flag, p.status, p.timeout_ns};
+    const bool some = S.some;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
+        if (some) q_math<DH>(p, S, base, wait, warp >> 2, warp & 3, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kServiceRegs));
+        if (some && warp == 8 && elect_one()) q_copy<DH>(p, maps, S, base, wait);
+        else if (some && warp == 9 && elect_one()) q_issue<DH>(p, S, base, wait);
+        __syncwarp();
+        if (warp >= 10) zero_outside(p.qb, p.N, p.T, p.H, p.D, p.dq, nullptr, threadIdx.x - 320, 64);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
+}
+
+// ------------------------------------------------------- keys: dk and dv
+
+template <int DH>
+struct KCfg {
+    static constexpr int TILE = kTile * DH * 2;
+    static constexpr int STAGES = 2;                 // of query rows and of dout
+    static constexpr int OFF_Q = 2 * TILE;           // after keys and values
+    static constexpr int OFF_D = OFF_Q + STAGES * TILE;
+    static constexpr int OFF_VEC = OFF_D + STAGES * TILE;           // [STAGES][2][128] floats: -lse log2(e), -delta
+    static constexpr int OFF_SHARED = OFF_VEC + STAGES * 1024;
+    static constexpr int SMEM = OFF_SHARED + 384 + 1024;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct KWork {
+    Seq s;
+    int kv, key0, rows;              // first key's place in the sequence; keys of the tile
+    int first, n;                    // first block of 128 queries; iterations: blocks times heads
+};
+struct KShared {
+    uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, drain, never;
+    uint32_t tmem;
+    int abort_flag, poison, some;
+    KWork work;
+};
+static_assert(sizeof(KShared) <= 384, "shared state");
+
+// The queries [lo, hi] of the sequence that see some of the tile's keys.
+__device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, KWork &w)
+{
+    if (p.kb && p.N == 0) return false;
+    w.kv = unit % p.KV;
+    int tile;
+    const int n = tile_sequence(p.kb, p.N, p.S, kTile, unit / p.KV, tile);
+    w.s = seq_at(p, n);
+    const long long key0 = static_cast<long long>(kTile) * tile;
+    if (key0 >= w.s.keys()) return false;
+    w.key0 = static_cast<int>(key0);
+    w.rows = min(kTile, w.s.keys() - w.key0);
+    const int shift = w.s.keys() - w.s.queries();                    // position of query 0
+    const long long lo = max(0, w.key0 - shift);
+    long long hi = w.s.queries() - 1;
+    if (w.key0 >= p.sinks) hi = min(hi, static_cast<long long>(w.key0) + w.rows - 1 + p.window - 1 - shift);
+    w.first = static_cast<int>(lo / kTile);
+    w.n = hi >= lo ? static_cast<int>(hi / kTile - lo / kTile + 1) * p.G : 0;
+    return true;
+}
+// Every query of block qb sees every key of the tile.
+__device__ __forceinline__ bool seen_by_all(const AttnParams &p, const KWork &w, int qb)
+{
+    const int r = qb * kTile, pos = r + w.s.keys() - w.s.queries();
+    return pos >= w.key0 + kTile - 1 && r + kTile <= w.s.queries() && (pos + kTile - 1 - w.key0 < p.window || w.key0 + kTile - 1 < p.sinks);
+}
+
+template <int DH>
+__device__ void k_copy(const AttnParams &p, const AttnMaps &maps, KShared &S, uint32_t base, const Waits &wait)
+{
+    using C = KCfg<DH>;
+    const KWork w = S.work;
+    if (w.n == 0 || (p.force_timeout && !wait.one(smem_u32(&S.never), 0))) return;
+    mbar_arrive_expect_tx(smem_u32(&S.kv_full), 2 * C::TILE);
+    load_tile<DH>(base, &maps.k, smem_u32(&S.kv_full), w.kv, w.s.k0 + w.key0);
+    load_tile<DH>(base + C::TILE, &maps.v, smem_u32(&S.kv_full), w.kv, w.s.k0 + w.key0);
+    int q_last[2] = {-1, -1}, d_last[2] = {-1, -1};                  // parity of each stage's last load
+    bool ok = true;
+    for (int i = 0; i < w.n; ++i) {
+        const int st = i & 1, phase = (i >> 1) & 1, row = w.s.q0 + (w.first + i / p.G) * kTile, head = w.kv * p.G + i % p.G;
+        ok = wait.one(smem_u32(&S.q_empty[st]), phase ^ 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(smem_u32(&S.q_full[st]), C::TILE);
+        load_tile<DH>(base + C::OFF_Q + st * C::TILE, &maps.q, smem_u32(&S.q_full[st]), head, row);
+        q_last[st] = phase;
+        ok = wait.one(smem_u32(&S.d_empty[st]), phase ^ 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(smem_u32(&S.d_full[st]), C::TILE);
+        load_tile<DH>(base + C::OFF_D + st * C::TILE, &maps.dout, smem_u32(&S.d_full[st]), head, row);
+        d_last[st] = phase;
+    }
+    if (!ok || *wait.abort_flag) {
+        wait.drain(smem_u32(&S.kv_full), 0);
+        for (int st = 0; st < 2; ++st) {
+            if (q_last[st] >= 0) wait.drain(smem_u32(&S.q_full[st]), q_last[st]);
+            if (d_last[st] >= 0) wait.drain(smem_u32(&S.d_full[st]), d_last[st]);
+        }
+    }
+}
+
+// One warp: -lse log2(e) and -delta of each iteration's queries. A row that saw nothing gets -infinity: P is zero.
+template <int DH>
+__device__ void k_vectors(const AttnParams &p, KShared &S, uint8_t *smem, const Waits &wait, int lane)
+{
+    using C = KCfg<DH>;
+    const KWork &w = S.work;
+    for (int i = 0; i < w.n; ++i) {
+        const int st = i & 1, r0 = (w.first + i / p.G) * kTile;
+        const long long at = static_cast<long long>(w.kv * p.G + i % p.G) * p.T + w.s.q0 + r0;
+        float l[4], d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = lane + 32 * e;
+            const bool live = r0 + r < w.s.queries();
+            l[e] = live ? p.lse[at + r] : 0.0f;
+            d[e] = live ? p.delta[at + r] : 0.0f;
+        }
+        if (!wait.warp(smem_u32(&S.v_empty[st]), ((i >> 1) & 1) ^ 1)) return;
+        float *v = reinterpret_cast<float *>(smem + C::OFF_VEC + st * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[lane + 32 * e] = l[e] == -INFINITY ? -INFINITY : -l[e] * kLog2e;
+            v[kTile + lane + 32 * e] = -d[e];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.v_full[st]));
+    }
+}
+
+// TMEM: transposed scores (keys are the lanes), their gradients, dv, dk: all of it. While P of a block is made, the last
+// block's dk and the next gradient of the scores are; while dS is, dv and the next scores.
+template <int DH>
+__device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Waits &wait)
+{
+    using C = KCfg<DH>;
+    const KWork w = S.work;
+    const uint32_t tm = S.tmem;
+    const int steps = (p.D + 15) / 16;
+    bool ok = w.n == 0 || wait.one(smem_u32(&S.kv_full), 0), issued = false;
+    auto scores = [&](int i) {
+        ok = ok && wait.one(smem_u32(&S.q_full[i & 1]), (i >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        mma_scores(tm, base, base + C::OFF_Q + (i & 1) * C::TILE, steps);
+        mma_commit(smem_u32(&S.scores));
+        issued = true;
+    };
+    auto dp = [&](int i) {
+        ok = ok && wait.one(smem_u32(&S.d_full[i & 1]), (i >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        mma_scores(tm + kTile, base + C::TILE, base + C::OFF_D + (i & 1) * C::TILE, steps);
+        mma_commit(smem_u32(&S.dp));
+        issued = true;
+    };
+    if (w.n > 0) scores(0);
+    if (w.n > 0) dp(0);
+    for (int i = 0; ok && i < w.n; ++i) {
+        ok = wait.one(smem_u32(&S.probs), i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tm + 2 * kTile, tm, base + C::OFF_D + (i & 1) * C::TILE, steps * 16, i > 0, kGap);
+        mma_commit(smem_u32(&S.d_empty[i & 1]));
+        if (i + 1 < w.n) scores(i + 1);
+        ok = ok && wait.one(smem_u32(&S.ds), i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tm + 3 * kTile, tm + kTile, base + C::OFF_Q + (i & 1) * C::TILE, steps * 16, i > 0, kGap);
+        mma_commit(smem_u32(&S.q_empty[i & 1]));
+        if (i + 1 < w.n) dp(i + 1);
+    }
+    if (ok) {
+        mma_commit(smem_u32(&S.done));
+    } else if (issued) {
+        mma_commit(smem_u32(&S.drain));
+        wait.drain(smem_u32(&S.drain), 0);
+    }
+}
+
+// Adds what make_finite took out of the queries' rows (x: q or dout) to the keys that they see. key: place in the sequence, or -1.
+__device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, const Heads &x, uint32_t out, int key, int c0, int c1)
+{
+    for (int c = c0; c < c1; c += 8) {
+        uint32_t o[8];
+        detg::tmem_ld8(out + c, o);
+        tmem_wait_ld();
+        detg::reg_fence8(o);
+        for (int i = 0; i < w.n && key >= 0; ++i) {
+            const int qb = w.first + i / p.G;
+            if (seen_by_all(p, w, qb)) continue;
+            for (int r = qb * kTile; r < min((qb + 1) * kTile, w.s.queries()); ++r) {
+                if (!sees(p, r + w.s.keys() - w.s.queries(), key)) continue;
+                float f[8];
+                unpack8(load8(x.row(w.s.q0 + r, w.kv * p.G + i % p.G), c, p.D), f);
+                for (int e = 0; e < 8; ++e)
+                    if (!isfinite(f[e])) o[e] = __float_as_uint(__uint_as_float(o[e]) + f[e]);
+            }
+        }
+        __syncwarp();
+        detg::tmem_st8(out + c, o);
+        tmem_wait_st();
+    }
+}
+
+template <int DH>
+__device__ void k_math(const AttnParams &p, KShared &S, uint32_t base, const Waits &wait, int half, int warp, int lane)
+{
+    using C = KCfg<DH>;
+    const KWork &w = S.work;
+    const int row = warp * 32 + lane;
+    const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int key = row < w.rows ? w.key0 + row : -1;
+    const float c = p.scale * kLog2e;
+    const uint64_t c2 = pair(c, c);
+    bool ok = true;
+    const int n = w.n;
+    for (int i = 0; i < n; ++i) {
+        const int st = i & 1, qb = w.first + i / p.G;
+        const bool full = seen_by_all(p, w, qb);
+        const uint32_t vec = base + C::OFF_VEC + st * 1024 + half * 256;
+        // Queries of this thread's columns that see the key: [first, last], or up to `end` for one of the first keys.
+        const int shift = w.s.keys() - w.s.queries() + qb * kTile + half * 64, first = key < 0 ? 64 : key - shift;
+        const int end = w.s.queries() - qb * kTile - half * 64 - 1;
+        const int last = key < p.sinks ? end : static_cast<int>(min(static_cast<long long>(end), static_cast<long long>(first) + p.window - 1));
+        ok = wait.warp(smem_u32(&S.v_full[st]), (i >> 1) & 1) && wait.warp(smem_u32(&S.scores), i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[2][32];
+        tmem_ld32(tm + half * 64, s[0]);
+        tmem_ld32(tm + half * 64 + 32, s[1]);
+        tmem_wait_ld();
+        reg_fence(s[0]);
+        reg_fence(s[1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                uint64_t l0, l1;
+                lds4(vec + x * 128 + j * 8, l0, l1);
+                float a0, a1, b0, b1;
+                unpair(fma2(pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1])), c2, l0), a0, a1);
+                unpair(fma2(pair(__uint_as_float(s[x][2 * j + 2]), __uint_as_float(s[x][2 * j + 3])), c2, l1), b0, b1);
+                s[x][2 * j] = __float_as_uint(exp2_fast(a0));
+                s[x][2 * j + 1] = __float_as_uint(exp2_fast(a1));
+                s[x][2 * j + 2] = __float_as_uint(exp2_fast(b0));
+                s[x][2 * j + 3] = __float_as_uint(exp2_fast(b1));
+            }
+        if (!full) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k < first || k > last) s[k >> 5][k & 31] = 0u;
+            // Both score matrices have been made: the queries' rows may be changed for the last two products.
+            ok = wait.warp(smem_u32(&S.dp), i & 1);
+            if (!ok) break;
+            const int live = w.s.queries() - qb * kTile;
+            if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, live)) S.poison = 1;
+            __syncwarp();
+        }
+        put16(tm + half * 64, s[0]);
+        put16(tm + half * 64 + 16, s[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.probs));
+        ok = wait.warp(smem_u32(&S.dp), i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t d[2][32];
+        tmem_ld32(tm + kTile + half * 64, d[0]);
+        tmem_ld32(tm + kTile + half * 64 + 32, d[1]);
+        tmem_wait_ld();
+        reg_fence(d[0]);
+        reg_fence(d[1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                uint64_t d0, d1;
+                lds4(vec + 512 + x * 128 + j * 8, d0, d1);
+                float a0, a1, b0, b1;
+                unpair(mul2(add2(pair(__uint_as_float(d[x][2 * j]), __uint_as_float(d[x][2 * j + 1])), d0),
+                            pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1]))), a0, a1);
+                unpair(mul2(add2(pair(__uint_as_float(d[x][2 * j + 2]), __uint_as_float(d[x][2 * j + 3])), d1),
+                            pair(__uint_as_float(s[x][2 * j + 2]), __uint_as_float(s[x][2 * j + 3]))), b0, b1);
+                d[x][2 * j] = __float_as_uint(a0);
+                d[x][2 * j + 1] = __float_as_uint(a1);
+                d[x][2 * j + 2] = __float_as_uint(b0);
+                d[x][2 * j + 3] = __float_as_uint(b1);
+            }
+        if (!full) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                if (k < first || k > last) d[k >> 5][k & 31] = 0u;
+        }
+        put16(tm + kTile + half * 64, d[0]);
+        put16(tm + kTile + half * 64 + 16, d[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&S.ds));
+            mbar_arrive(smem_u32(&S.v_empty[st]));
+        }
+    }
+    if (ok) ok = wait.warp(smem_u32(&S.done), 0);
+    if (!ok) return;
+    tc_fence_after();
+    // dv through the first warpgroup and the keys' place, dk through the second and the values'.
+    const uint32_t out = tm + (half ? 3 : 2) * kTile, tile = base + half * C::TILE;
+    if (n > 0 && *reinterpret_cast<volatile int *>(&S.poison)) k_add_taken(p, w, half ? p.q : p.dout, out, key, 0, p.D);
+    store_sums<DH>(out, tile, warp, lane, 0, DH / 32, half ? p.scale : 1.0f, n > 0);
+    copy_rows_out<DH / 8>(half ? p.dk : p.dv, static_cast<long long>(w.s.k0) + w.key0, w.kv, tile, warp, lane, 0, w.rows, p.D);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps maps)
+{
+    using C = KCfg<DH>;
+    extern __shared__ uint8_t attn_smem[];
+    const uint32_t raw = smem_u32(attn_smem), base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = attn_smem + (base - raw);
+    KShared &S = *reinterpret_cast<KShared *>(smem + C::OFF_SHARED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        S.abort_flag = 0;
+        S.poison = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&S.q_full[i]), 1);
+            mbar_init(smem_u32(&S.q_empty[i]), 1);
+            mbar_init(smem_u32(&S.d_full[i]), 1);
+            mbar_init(smem_u32(&S.d_empty[i]), 1);
+            mbar_init(smem_u32(&S.v_full[i]), 1);
+            mbar_init(smem_u32(&S.v_empty[i]), 8);
+        }
+        mbar_init(smem_u32(&S.kv_full), 1);
+        mbar_init(smem_u32(&S.scores), 1);
+        mbar_init(smem_u32(&S.dp), 1);
+        mbar_init(smem_u32(&S.probs), 8);
+        mbar_init(smem_u32(&S.ds), 8);
+        mbar_init(smem_u32(&S.done), 1);
+        mbar_init(smem_u32(&S.drain), 1);
+        mbar_init(smem_u32(&S.never), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8 && lane == 0 && p.T > 0 && p.S > 0) {
+        tmap_prefetch(&maps.q);
+        tmap_prefetch(&maps.k);
+        tmap_prefetch(&maps.v);
+        tmap_prefetch(&maps.dout);
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    begin();
+    if (threadIdx.x == 32) {
+        KWork w;
+        S.some = find_keys(p, blockIdx.x, w);
+        if (S.some) S.work = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Waits wait{&S.abort_flag, p.status, p.timeout_ns};
+    const bool some = S.some;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
+        if (some) k_math<DH>(p, S, base, wait, warp >> 2, warp & 3, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kServiceRegs));
+        if (some && warp == 8 && elect_one()) k_copy<DH>(p, maps, S, base, wait);
+        else if (some && warp == 9 && elect_one()) k_issue<DH>(p, S, base, wait);
+        else if (some && warp == 10) k_vectors<DH>(p, S, smem, wait, lane);
+        __syncwarp();
+        if (warp == 11) zero_outside(p.kb, p.N, p.S, p.KV, p.D, p.dk, &p.dv, lane, 32);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
+}
+
+template <typename F>
+cudaError_t set_up(F fn, int smem)
+{
+    cudaFuncAttributes at;
+    const cudaError_t x = cudaFuncGetAttributes(&at, fn);
+    if (x != cudaSuccess) return x;
+    // setmaxnreg shares out exactly the registers of the launch.
+    if (at.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+template <int DH>
+cudaError_t run(const AttnParams &p, const AttnMaps &maps, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [&] {
+        const cudaError_t x = set_up(attn_dq_kernel<DH>, QCfg<DH>::SMEM);
+        return x == cudaSuccess ? set_up(attn_dkv_kernel<DH>, KCfg<DH>::SMEM) : x;
+    });
+    if (e != cudaSuccess) return e;
+    if (p.T > 0) {
+        const int slots = p.qb ? tile_slots(p.T, p.N, kTile) : (p.T + kTile - 1) / kTile;
+        e = launch_early(attn_dq_kernel<DH>, static_cast<long long>(slots) * p.H, kThreads, QCfg<DH>::SMEM, 1, s, p, maps, slots);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.S > 0) {
+        const int slots = p.kb ? tile_slots(p.S, p.N, kTile) : (p.S + kTile - 1) / kTile;
+        e = launch_early(attn_dkv_kernel<DH>, static_cast<long long>(slots) * p.KV, kThreads, KCfg<DH>::SMEM, 1, s, p, maps);
+    }
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd(const AttnParams &p, const AttnMaps &maps, cudaStream_t s)
+{
+    return p.D <= 64 ? run<64>(p, maps, s) : run<128>(p, maps, s);
+}
+
+}  // namespace deto

@@ -221,32 +221,6 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
     }
 }
 
-// Takes what is not finite out of row r of a value tile (if the tile has one), and all of it if the sequence's keys end
-// before. True if something was not finite. The row's eight chunks of 16 bytes are taken in an order of its own, for the banks.
-template <int DH>
-__device__ __noinline__ bool make_finite(uint32_t tile, int r, int live)
-{
-    if (r >= kTile) return false;
-    bool found = false;
-#pragma unroll
-    for (int c = 0; c < DH / 8; ++c) {
-        const uint32_t at = tile + (c >> 3) * (kTile * 128) + r * 128 + ((c ^ r) & 7) * 16;
-        uint32_t x[4], any = 0;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = (x[i] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (x[i] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-            any |= lo | hi;
-            x[i] &= r < live ? ~(lo | hi) : 0u;
-        }
-        if (any != 0 || r >= live)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
-        found |= any != 0 && r < live;
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    return found;
-}
-
 // Adds the values that make_finite took out to the rows that see them.
 __device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, int t, uint32_t out, int position)
 {
@@ -313,7 +287,7 @@ __device__ void softmax_role(const AttnParams &p, Shared &S, uint32_t base, cons
         for (int x = 0; x < 4; ++x) reg_fence(s[x]);
         if (!sees_all(p, w.pos[t], b)) {
             const int a = b * kTile, last = position - a;              // keys [.., last] of the block, from `first` on or below `sink`
-            const int first = position - p.window + 1 - a, sink = p.sinks - a;
+            const int first = first_seen(p, position, a), sink = p.sinks - a;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -471,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         mbar_init(smem_u32(&S.never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && lane == 0 && p.S > 0) {
         tmap_prefetch(&maps.q);
         tmap_prefetch(&maps.k);
         tmap_prefetch(&maps.v);

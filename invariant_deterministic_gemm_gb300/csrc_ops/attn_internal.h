@@ -55,7 +55,7 @@ struct AttnMaps {
     CUtensorMap q, k, v, dout;
 };
 cudaError_t launch_attn(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
-cudaError_t launch_attn_bwd(const AttnParams &p, int sms, cudaStream_t s);
+cudaError_t launch_attn_bwd(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
 
 struct DecodeParams {
     Heads q, out;

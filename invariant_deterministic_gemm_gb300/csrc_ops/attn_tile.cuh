@@ -92,12 +92,39 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, i
 }
 
 // d[128, D] (+)= A (TMEM, 128 x 128) times a tile's rows; n: D rounded up to 16.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint32_t b, int n, bool accumulate)
+// `gap`: columns left out between A's halves (two warpgroups wrote them, each into its own part of the scores).
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint32_t b, int n, bool accumulate, uint32_t gap = 0)
 {
     const uint64_t db = sdesc(b, kTile * 128u, 1024u);
     const uint32_t idesc = idesc_bf16(kTile, n, 0, 1);
 #pragma unroll
-    for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a_tmem + k * 8, db + k * (2048 / 16), idesc, accumulate || k != 0);
+    for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a_tmem + k * 8 + (k >= 4 ? gap : 0), db + k * (2048 / 16), idesc, accumulate || k != 0);
+}
+
+// Takes what is not finite out of row r of a tile (if the tile has one), and all of it if the sequence's rows end
+// before. True if something was not finite. The row's eight chunks of 16 bytes are taken in an order of its own, for the banks.
+template <int DH>
+__device__ __noinline__ bool make_finite(uint32_t tile, int r, int live)
+{
+    if (r >= kTile) return false;
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < DH / 8; ++c) {
+        const uint32_t at = tile + (c >> 3) * (kTile * 128) + r * 128 + ((c ^ r) & 7) * 16;
+        uint32_t x[4], any = 0;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = (x[i] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (x[i] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+            any |= lo | hi;
+            x[i] &= r < live ? ~(lo | hi) : 0u;
+        }
+        if (any != 0 || r >= live)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+        found |= any != 0 && r < live;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return found;
 }
 
 // ---- arithmetic
@@ -166,6 +193,12 @@ __device__ __forceinline__ bool sees_all(const AttnParams &p, Positions q, int b
 {
     const int a = b * kTile;
     return a + kTile - 1 <= q.lo && (q.hi - a < p.window || a + kTile - 1 < p.sinks);
+}
+
+// The first key of a position's window, counted from key a (or below all of them).
+__device__ __forceinline__ int first_seen(const AttnParams &p, int position, int a)
+{
+    return static_cast<int>(max(-1ll, static_cast<long long>(position) - p.window + 1 - a));
 }
 
 // ---- tiles of packed rows
