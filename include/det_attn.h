@@ -84,7 +84,7 @@ det_gemm_status det_kv_append(const det_gemm_bf16 *q, const det_gemm_bf16 *k, co
  * two, a page outside the cache as hidden keys; both are reported. page_size
  * is a multiple of 8, H / KV at most DET_ATTN_MAX_SHARED.
  */
-int64_t det_attn_decode_workspace(int64_t B, int64_t H, int64_t D, int64_t max_tokens);
+int64_t det_attn_decode_workspace(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t max_tokens);
 det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_cache, const det_gemm_bf16 *v_cache,
                                 const int32_t *table, const int32_t *lengths, det_gemm_bf16 *out, int64_t B, int64_t H,
                                 int64_t KV, int64_t D, int64_t pages, int64_t page_size, int64_t max_pages, float scale,

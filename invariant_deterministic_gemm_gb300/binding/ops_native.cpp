@@ -700,7 +700,7 @@ PyObject *attn_decode(Argv a)
     const int32_t *lengths = static_cast<int32_t *>(flat(a[4], "lengths", kI32, {q.T}));
     const at::Device dev = THPVariable_Unpack(a[0]).device();
     const int64_t tokens = kc.size > 0 && most <= INT32_MAX / kc.size ? most * kc.size : 0;     // the library refuses more
-    const int64_t size = std::max<int64_t>(det_attn_decode_workspace(q.T, q.H, q.D, tokens), 256);
+    const int64_t size = std::max<int64_t>(det_attn_decode_workspace(q.T, q.H, kc.heads, q.D, tokens), 256);
     const Tensor ws = empty({size}, ScalarType::Byte, dev);
     const Tensor out = rows_out(a[8], q.T, q.H, q.D, dev);
     const Rows y = rows_of(out, "out");

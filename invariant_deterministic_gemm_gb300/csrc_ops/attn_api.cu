@@ -106,13 +106,13 @@ int window_of(int64_t w) { return w == 0 || w > kMaxRows ? kNoWindow : static_ca
 int sinks_of(int64_t s) { return static_cast<int>(std::min(s, kMaxRows)); }
 
 // Heads as (column, head, token), copied in boxes of 64 columns of one head and 128 tokens.
-bool encode(CUtensorMap *m, const void *p, int64_t T, int64_t H, int64_t D, int64_t t, int64_t h)
+bool encode(CUtensorMap *m, const void *p, int64_t T, int64_t H, int64_t D, int64_t t, int64_t h, int box_heads = 1, int box_tokens = 128)
 {
     std::memset(m, 0, sizeof *m);
     if (T == 0) return true;                   // nothing will be copied
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(H > 1 ? h : D) * 2, static_cast<cuuint64_t>(T > 1 ? t : H * D) * 2};
-    cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)}, es[3] = {1, 1, 1};
     return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -130,6 +130,36 @@ bool ok_turn(int64_t D, int64_t rot, int64_t P)
 
 // Device memory of the backward pass: delta [H, T].
 int64_t bwd_bytes(int64_t T, int64_t H) { return up(std::max<int64_t>(4 * T * H, 1), 256) * 256; }
+
+// Decode: the query heads of a KV head are taken up to 32 at once; device memory of the sequences' unit counts, and of what
+// the CTAs leave in parts.
+constexpr int64_t kMaxCtas = 160, kTokens = 128;
+struct DecodeSpace {
+    int64_t parts, heads, partials, total;
+};
+DecodeSpace decode_space(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t tokens)
+{
+    DecodeSpace s;
+    s.parts = up(H / KV, 32);
+    s.heads = up(H / KV, s.parts);
+    s.partials = up((B + 2) * 8, 256) * 256;
+    s.total = s.partials + up(decode_slots(B * KV * s.parts, tokens, kMaxCtas) * s.heads * (D + 2) * 4, 256) * 256;
+    return s;
+}
+
+// A cache as (column, head, token of a page, page), copied in boxes of 64 columns of one head and `box` tokens of a page.
+bool encode(CUtensorMap *m, const void *p, int64_t pages, int64_t size, int64_t KV, int64_t D, int64_t page, int64_t s, int64_t h, int box)
+{
+    std::memset(m, 0, sizeof *m);
+    if (pages == 0) return true;               // nothing will be copied
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(KV), static_cast<cuuint64_t>(size), static_cast<cuuint64_t>(pages)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(KV > 1 ? h : D) * 2, static_cast<cuuint64_t>(size > 1 ? s : D) * 2,
+                             static_cast<cuuint64_t>(pages > 1 ? page : D) * 2};
+    cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, es[4] = {1, 1, 1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, boxes, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace
 }  // namespace deto
@@ -217,10 +247,10 @@ det_gemm_status det_kv_append(const det_gemm_bf16 *q, const det_gemm_bf16 *k, co
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "append launch");
 }
 
-int64_t det_attn_decode_workspace(int64_t B, int64_t H, int64_t D, int64_t max_tokens)
+int64_t det_attn_decode_workspace(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t max_tokens)
 {
-    if (!ok_size(B) || H < 0 || H > DET_ATTN_MAX_HEADS || D < 0 || D > DET_ATTN_MAX_HEAD_DIM || !ok_size(max_tokens)) return 0;
-    return 256;
+    if (!ok_size(B) || !ok_heads(H, KV, D) || !ok_size(max_tokens)) return 0;
+    return decode_space(B, H, KV, D, max_tokens).total;
 }
 
 det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_cache, const det_gemm_bf16 *v_cache,
@@ -235,7 +265,8 @@ det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_c
         !ok_size(max_pages * page_size) || !ok_mask(scale, window, sinks))
         return DET_GEMM_ERR_INVALID_ARG;
     if (B == 0) return DET_GEMM_OK;
-    const int64_t need = det_attn_decode_workspace(B, H, D, max_pages * page_size);
+    const DecodeSpace space = decode_space(B, H, KV, D, max_pages * page_size);
+    const int64_t need = space.total;
     const Strided kc{k_cache, {pages, page_size, KV}, {kcp, kcs, kch}, D}, vc{v_cache, {pages, page_size, KV}, {vcp, vcs, vch}, D};
     det_gemm_status s = check_all({heads(q, B, H, D, qt, qh), kc, vc}, {Arr{table, B, max_pages, ldt, 4, 4}, vec4(lengths, B)},
                                   {heads(out, B, H, D, ot, oh)}, {bytes(workspace, need)});
@@ -247,8 +278,6 @@ det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_c
     std::memset(&p, 0, sizeof p);
     p.q = on(q, qt, qh);
     p.out = on(out, ot, oh);
-    p.kc = on(k_cache, kcp, kcs, kch);
-    p.vc = on(v_cache, vcp, vcs, vch);
     p.table = table;
     p.lengths = lengths;
     p.ldt = ldt;
@@ -263,8 +292,21 @@ det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_c
     p.scale = scale;
     p.window = window_of(window);
     p.sinks = sinks_of(sinks);
+    p.parts = static_cast<int>(space.parts);
+    p.heads = static_cast<int>(space.heads);
+    p.box = static_cast<int>(std::min<int64_t>(page_size & -page_size, kTokens));
+    p.prefix = static_cast<long long *>(workspace);
+    p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + space.partials);
     p.status = d->word;
-    const cudaError_t e = launch_attn_decode(p, d->sms, cs(stream));
+    p.timeout_ns = timeout_ns();
+    p.force_timeout = timeout_forced();
+    DecodeMaps maps;
+    if (!encode(&maps.q, q, B, H, D, qt, qh, space.heads <= 16 ? 16 : 32, 1) ||
+        !encode(&maps.k, k_cache, pages, page_size, KV, D, kcp, kcs, kch, p.box) ||
+        !encode(&maps.v, v_cache, pages, page_size, KV, D, vcp, vcs, vch, p.box))
+        return no_map();
+    const int64_t most = B * KV * space.parts * up(std::max<int64_t>(max_pages * page_size, 1), kChunk);
+    const cudaError_t e = launch_attn_decode(p, maps, static_cast<int>(std::min({most, static_cast<int64_t>(d->sms), kMaxCtas})), cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "decode attention launch");
 }
 

@@ -1,112 +1,852 @@
-// Attention of packed sequences and its gradients: one warp for each row of
-// the output, 32 keys (or queries) at a time, running maximum and sum.
+// Attention of one new token a sequence over a paged key-value cache.
 //
-//   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - m_i),  lse_i = m_i + log sum_j p_ij
-//   P = exp(scale q.k - lse), dS = P (dout.v - delta), delta_i = dout_i.out_i
-//   dv_j = sum_i P_ij dout_i, dq_i = scale sum_j dS_ij k_j, dk_j = scale sum_i dS_ij q_i
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = scale log2(e) q.k_j,  m = max_j s_j
 //
-// Everything in FP32; a lane holds four columns of the row's sums.
-#include "attn_internal.h"
-#include "launch.cuh"
-#include "ops_internal.h"
-#include "vec.cuh"
+// The launch is bound by reading keys and values once, so they come by TMA
+// through a ring of tiles of 128 tokens (one copy a page and 64 columns), and
+// everything else has to fit beside that. The tokens are the product's wide
+// side: scores [128 tokens, heads] = K Q^T, outputs [D, heads] = V^T P^T, both
+// from the tiles as they lie, so 16 (or 32) query heads that share a KV head
+// cost one pass over its keys and no lane is wasted on a single query.
+//
+// The bits of a sequence do not depend on the batch: its keys are cut in chunks
+// of 256 at fixed places, each with a maximum and a sum of its own, and chunks
+// are joined in a fixed order: four to a block, 16 blocks to a super block, those
+// one after the other. Where the work is cut between CTAs is about time alone:
+// all CTAs take equally long runs of units (chunks, blocks or super blocks, the
+// largest of which there are four for every CTA), and what one CTA does not
+// see whole it leaves as its units' sums for a second launch, which joins them
+// in the same order with the same arithmetic. Which those are is found on the
+// device from the lengths, so a captured launch serves any.
+//
+//   warps 0-3   scores to P (a lane a token), P to shared memory as the next
+//               product's operand; the chunk before is joined meanwhile (a lane a
+//               column of the output)
+//   warp 4      copies
+//   warp 5      issues the products
+//   warp 6      sequences without tokens
+// The sum of P is one more product, with ones in TMEM as its left operand: of
+// the rounded P, which the weights then add up to exactly, and without any
+// exchange between lanes. P is rounded to BF16 beside BF16 values.
+#include "attn_tile.cuh"
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 namespace deto {
 namespace {
 
-constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kWarps = 4;
+constexpr int kThreads = 256;
 
-__device__ __forceinline__ float warp_max(float v)
-{
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
-__device__ __forceinline__ float warp_sum(float v)
-{
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
+template <int DH, int NT>
+struct Cfg {
+    static constexpr int TILE = kTile * DH * 2;
+    static constexpr int SLOTS = DH == 128 ? 6 : 12;
+    static constexpr int BUF = NT == 16 ? 2 : 1;     // of scores, P and a chunk's sums
+    static constexpr int Q_BYTES = NT * DH * 2, P_BYTES = NT * kChunk * 2;
+    // The ring is followed by more than the 16 KB that a tile of 64 columns' product reads past its end (128 lanes, of which
+    // 64 are used).
+    static constexpr int OFF_P = SLOTS * TILE;       // [BUF]
+    static constexpr int OFF_Q = OFF_P + BUF * P_BYTES;             // [2]
+    static constexpr int OFF_SHARED = OFF_Q + 2 * Q_BYTES;
+    static constexpr int SMEM = OFF_SHARED + 1536 + 1024;
+    static_assert(OFF_SHARED - OFF_P >= (DH == 64 ? 16384 : 0), "reads past the ring stay inside");
+    static_assert(SMEM <= 232448, "shared memory");
+    // TMEM columns. A state: sums [NT], l [NT], m [NT].
+    static constexpr int STATE = 3 * NT;
+    static constexpr int T_SCORES = 0;               // [BUF][2 tiles][NT]
+    static constexpr int T_CHUNK = 2 * NT * BUF;     // [BUF] states
+    static constexpr int T_LEVEL = T_CHUNK + BUF * STATE;           // block, super block, all
+    static constexpr int T_ONES = T_LEVEL + 3 * STATE;
+    static_assert(T_ONES + 8 <= 512, "TMEM");
+};
 
-__device__ __forceinline__ float dot(const float *a, const uint16_t *row, int D)
-{
-    float s = 0.0f;
-    for (int c = 0; c < D; c += 8) {
-        float f[8];
-        unpack8(*reinterpret_cast<const uint4 *>(row + c), f);
-        for (int i = 0; i < 8; ++i) s += a[c + i] * f[i];
-    }
-    return s;
-}
+struct Shared {
+    uint64_t full[12], empty[12], q_full[2], q_empty[2], scores[2], probs[2], sums[2], drain, never;
+    uint32_t tmem;
+    int abort_flag;
+    unsigned loaded[16];             // of the chunks under way: which groups of eight tokens have a page
+    alignas(16) float top[2][4][32]; // each warp's maxima of a chunk
+    long long first, last;           // the CTA's units
+    long long scan[8];
+    int start;                       // sequence of the first unit
+    int unit;                        // chunks a unit
+    long long start_units;           // units before it
+    long long total[3];
+};
+static_assert(sizeof(Shared) <= 1536, "shared state");
 
-// sum += w * row, four columns a lane.
-__device__ __forceinline__ void add(float (&sum)[4], float w, const uint16_t *row, int D, int lane)
-{
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < D) sum[i] += w * bf_at(row + lane + 32 * i);
-}
+// ---- the key axis
 
-__device__ __forceinline__ void put(uint16_t *row, const float (&v)[4], int D, int lane)
+__device__ __forceinline__ int tokens_of(const DecodeParams &p, int b)
 {
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < D) row[lane + 32 * i] = static_cast<uint16_t>(pack_bf16(v[i], 0.0f));
-}
-
-__device__ __forceinline__ void take(float *dst, const uint16_t *row, int D, int lane)
-{
-    for (int c = lane; c < D; c += 32) dst[c] = bf_at(row + c);
-}
-
-// One warp for each sequence and head.
-__global__ void __launch_bounds__(32 * kWarps) attn_decode_rows(const DecodeParams p)
-{
-    begin();
-    __shared__ float qs[kWarps][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * kWarps + warp, b = blockIdx.x;
-    if (h >= p.H) return;
-    const int g = h / p.G;
-    take(qs[warp], p.q.row(b, h), p.D, lane);
-    __syncwarp();
     const long long room = static_cast<long long>(p.max_pages) * p.page_size;
-    const int given = p.lengths[b];
-    const int n = given < 0 ? 0 : given > room ? static_cast<int>(room) : given;
-    bool bad = n != given;
-    float m = -INFINITY, l = 0.0f, o[4] = {};
-    for (int j0 = 0; j0 < n; j0 += 32) {
-        const int j = j0 + lane;
-        bool vis = j < n && (n - 1 - j < p.window || j < p.sinks);
-        const int page = vis ? p.table[b * p.ldt + j / p.page_size] : -1;
-        if (vis && (page < 0 || page >= p.pages)) {
-            bad = true;
-            vis = false;
+    const int n = p.lengths[b];
+    return n < 0 ? 0 : n > room ? static_cast<int>(room) : n;
+}
+// The chunks that n tokens' last one sees: [0, ns) and from w0 on.
+struct Chunks {
+    int ns, w0, n;
+    __device__ int at(int i) const { return i < ns ? i : w0 + i - ns; }
+};
+__device__ __forceinline__ Chunks chunks_of(const DecodeParams &p, int n)
+{
+    if (n == 0) return Chunks{0, 0, 0};
+    Chunks c;
+    c.w0 = max(0, n - p.window) / kChunk;
+    c.ns = min((p.sinks + kChunk - 1) / kChunk, c.w0);
+    c.n = c.ns + (n - 1) / kChunk - c.w0 + 1;
+    return c;
+}
+__device__ __forceinline__ bool sees(const DecodeParams &p, int n, int j) { return j < n && (n - 1 - j < p.window || j < p.sinks); }
+// Some, or every, of the tokens [a, a + len) is seen.
+__device__ __forceinline__ bool sees_some(const DecodeParams &p, int n, int a, int len)
+{
+    return a < n && (n - 1 - (a + len - 1) < p.window || a < p.sinks);
+}
+__device__ __forceinline__ bool sees_every(const DecodeParams &p, int n, int a, int len)
+{
+    return a + len <= n && (n - 1 - a < p.window || a + len - 1 < p.sinks);
+}
+
+// A part of one sequence's chunks for one KV head (and part of its query heads), within a CTA's run.
+struct Segment {
+    int b, kv, part, tokens;
+    Chunks chunks;
+    int c0, c1;                      // chunks (of the list) to take
+    long long unit0;                 // number of the list's first unit
+    bool whole;
+};
+
+// Walks a CTA's run, segment by segment; every role walks it by itself.
+struct Walk {
+    const DecodeParams &p;
+    long long at, last, before;      // next unit, the run's end, units before sequence b
+    int b, unit;
+    __device__ Walk(const DecodeParams &p, const Shared &S) : p(p), at(S.first), last(S.last), before(S.start_units), b(S.start), unit(S.unit) {}
+    __device__ bool next(Segment &s)
+    {
+        if (at >= last) return false;
+        int n, units;
+        Chunks c;
+        const int lists = p.KV * p.parts;
+        for (;; ++b) {
+            n = tokens_of(p, b);
+            c = chunks_of(p, n);
+            units = (c.n + unit - 1) / unit;
+            if (at < before + static_cast<long long>(units) * lists) break;
+            before += static_cast<long long>(units) * lists;
         }
-        if (!__any_sync(kFull, vis)) continue;
-        const float x = vis ? p.scale * dot(qs[warp], p.kc.row(page, j % p.page_size, g), p.D) : -INFINITY;
-        const float top = fmaxf(m, warp_max(x));
-        const float old = m == -INFINITY ? 0.0f : expf(m - top);
-        const float e = vis ? expf(x - top) : 0.0f;
-        l = l * old + warp_sum(e);
-        for (float &v : o) v *= old;
-        m = top;
-        unsigned live = __ballot_sync(kFull, vis);
-        for (; live; live &= live - 1) {
-            const int i = __ffs(live) - 1;
-            add(o, __shfl_sync(kFull, e, i), p.vc.row(__shfl_sync(kFull, page, i), (j0 + i) % p.page_size, g), p.D, lane);
+        const long long in = at - before;
+        const int list = static_cast<int>(in / units), u0 = static_cast<int>(in - static_cast<long long>(list) * units);
+        const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + (last - at)));
+        s.b = b;
+        s.kv = list / p.parts;
+        s.part = list % p.parts;
+        s.tokens = n;
+        s.chunks = c;
+        s.c0 = u0 * unit;
+        s.c1 = min(u1 * unit, c.n);
+        s.unit0 = at - u0;
+        s.whole = u0 == 0 && u1 == units;
+        at += u1 - u0;
+        return true;
+    }
+};
+
+// Which of a chunk's two tiles are needed.
+__device__ __forceinline__ unsigned tiles_of(const DecodeParams &p, int n, int chunk)
+{
+    const int a = chunk * kChunk;
+    return (sees_some(p, n, a, kTile) ? 1u : 0u) | (sees_some(p, n, a + kTile, kTile) ? 2u : 0u);
+}
+
+// The CTA's run: how many units there are, of which size, and where its part begins. All threads.
+__device__ void plan(const DecodeParams &p, Shared &S)
+{
+    const int thread = threadIdx.x, warp = thread >> 5, lane = thread & 31;
+    const long long lists = static_cast<long long>(p.KV) * p.parts;
+    long long sum[3] = {0, 0, 0};
+    for (int b = thread; b < p.B; b += kThreads) {
+        const int n = tokens_of(p, b), c = chunks_of(p, n).n;
+        if (blockIdx.x == 0 && n != p.lengths[b]) atomicExch(p.status, kStatusInvalid);
+        sum[0] += c;
+        sum[1] += (c + kBlockChunks - 1) / kBlockChunks;
+        sum[2] += (c + kSuperChunks - 1) / kSuperChunks;
+    }
+    if (thread < 3) S.total[thread] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(kWarp, sum[i], o);
+        if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(&S.total[i]), static_cast<unsigned long long>(sum[i]));
+    }
+    __syncthreads();
+    const long long enough = static_cast<long long>(kUnitsEach) * gridDim.x;
+    const int level = S.total[2] * lists >= enough ? 2 : S.total[1] * lists >= enough ? 1 : 0;
+    const int unit = level == 2 ? kSuperChunks : level == 1 ? kBlockChunks : 1;
+    const long long units = S.total[level] * lists;
+    const long long first = units * blockIdx.x / gridDim.x, last = units * (blockIdx.x + 1) / gridDim.x;
+    if (thread == 0) {
+        S.first = first;
+        S.last = last;
+        S.unit = unit;
+        S.start = 0;
+        S.start_units = 0;
+    }
+    long long carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + thread;
+        const long long mine = b < p.B ? (chunks_of(p, tokens_of(p, b)).n + unit - 1) / unit * lists : 0;
+        long long up = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(kWarp, up, o);
+            if (lane >= o) up += x;
+        }
+        __syncthreads();
+        if (lane == 31) S.scan[warp] = up;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) up += S.scan[w];
+        up += carry;
+        const long long before = up - mine;
+        if (mine > 0 && first >= before && first < up) {
+            S.start = b;
+            S.start_units = before;
+        }
+        if (blockIdx.x == 0 && b < p.B) p.prefix[b] = before;
+        for (int w = 0; w < kThreads / 32; ++w) carry += S.scan[w];
+    }
+    if (blockIdx.x == 0 && thread == 0) {
+        p.prefix[p.B] = units;
+        p.prefix[p.B + 1] = unit;
+    }
+}
+
+// ---- roles
+
+// One warp: queries and tiles. A lane looks up the page of eight tokens; lanes at a box's begin copy it.
+template <int DH, int NT>
+__device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared &S, uint32_t base, const Waits &wait, int lane)
+{
+    using C = Cfg<DH, NT>;
+    Walk walk(p, S);
+    Segment s;
+    int seq = 0, seg = 0, n = 0, queries = 0;
+    bool ok = !p.force_timeout || wait.warp(smem_u32(&S.never), 0), bad = false;
+    const unsigned in_box = p.box >= 128 ? 0xFFFFu : (1u << (p.box / 8)) - 1u;
+    for (; ok && walk.next(s); ++seg) {
+        const uint32_t qb = smem_u32(&S.q_full[seg & 1]);
+        ok = wait.warp(smem_u32(&S.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1);
+        if (!ok) break;
+        ++queries;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(qb, C::Q_BYTES);
+            for (int h = 0; h < DH / 64; ++h)
+                load_rows(base + C::OFF_Q + (seg & 1) * C::Q_BYTES + h * NT * 128, &maps.q, qb, h * 64, s.kv * p.G + s.part * p.heads, s.b);
+        }
+        for (int c = s.c0; ok && c < s.c1; ++c) {
+            const int chunk = s.chunks.at(c);
+            const unsigned tiles = tiles_of(p, s.tokens, chunk);
+            // Pages of both tiles' tokens, eight a lane.
+            const int token = chunk * kChunk + lane * 8;
+            const bool seen = sees_some(p, s.tokens, token, 8);
+            const int page = seen ? p.table[s.b * p.ldt + token / p.page_size] : -1;
+            const bool have = page >= 0 && page < p.pages;
+            bad |= seen && !have;
+            const unsigned got = __ballot_sync(kWarp, have);
+            const int at = token % p.page_size, pg = have ? page : 0;
+            // (The chunk's values are in the ring until its scores have been read, so the copies are at most a ring, 12
+            // chunks, ahead of that.)
+            if (lane == 0) S.loaded[n & 15] = got;
+            ++n;
+            for (int kind = 0; kind < 2; ++kind)
+                for (int t = 0; t < 2; ++t) {
+                    if (!((tiles >> t) & 1u)) continue;
+                    const int slot = seq % C::SLOTS;
+                    ok = ok && wait.warp(smem_u32(&S.empty[slot]), ((seq / C::SLOTS) & 1) ^ 1);
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&S.full[slot]);
+                    const unsigned mine = (got >> (16 * t)) & 0xFFFFu;
+                    // Boxes with a seen token: the first of its groups of eight stands for the box.
+                    const int g = lane & 15;
+                    const bool head = (lane >> 4) == t && ((g * 8) & (p.box - 1)) == 0 && ((mine >> g) & in_box) != 0;
+                    const unsigned boxes = __popc(__ballot_sync(kWarp, head));
+                    if (lane == 0) mbar_arrive_expect_tx(bar, boxes * p.box * (DH / 64) * 128);
+                    __syncwarp();
+                    // The box's page: of any of its groups that are seen (they share it).
+                    const int from = __ffs((mine >> g) & in_box) - 1;
+                    const int box_page = __shfl_sync(kWarp, pg, (16 * t + g + (from < 0 ? 0 : from)) & 31);
+                    if (head) {
+                        for (int h = 0; h < DH / 64; ++h) {
+                            const uint32_t dst = base + slot * C::TILE + h * kTile * 128 + g * 1024;
+                            asm volatile(
+                                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                                " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                                "l"(reinterpret_cast<uint64_t>(kind ? &maps.v : &maps.k)), "r"(bar), "r"(h * 64), "r"(s.kv), "r"(at), "r"(box_page)
+                                : "memory");
+                        }
+                    }
+                    __syncwarp();
+                    ++seq;
+                }
         }
     }
     if (bad) atomicExch(p.status, kStatusInvalid);
-    for (float &v : o) v = m == -INFINITY ? 0.0f : v / l;
-    put(p.out.row(b, h), o, p.D, lane);
+    if (!ok || *wait.abort_flag) {
+        for (int i = max(0, queries - 2); i < queries; ++i) wait.drain(smem_u32(&S.q_full[i & 1]), (i >> 1) & 1);
+        for (int i = max(0, seq - C::SLOTS); i < seq; ++i) wait.drain(smem_u32(&S.full[i % C::SLOTS]), (i / C::SLOTS) & 1);
+    }
+}
+
+// What the issuer keeps of a chunk whose scores have been made.
+struct Ahead {
+    int seq;                         // of its first key tile
+    unsigned tiles;
+    bool last;                       // of its segment
+    int seg;
+};
+
+template <int DH, int NT>
+__device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, const Waits &wait)
+{
+    using C = Cfg<DH, NT>;
+    constexpr uint32_t SC = idesc_bf16(kTile, NT, 0, 0), PV = idesc_bf16(kTile, NT, 1, 0);
+    const uint32_t tm = S.tmem;
+    const int steps = (p.D + 15) / 16;
+    Walk walk(p, S);
+    Segment s;
+    bool ok = true, issued = false, more = walk.next(s);
+    int seq = 0, seg = 0, c = more ? s.c0 : 0, n = 0;                  // n: chunks whose scores were issued
+    auto full = [&](int q) {
+        ok = ok && wait.one(smem_u32(&S.full[q % C::SLOTS]), (q / C::SLOTS) & 1);
+        return ok;
+    };
+    // The scores of the run's next chunk.
+    auto scores = [&](Ahead &a) {
+        if (c == s.c0) ok = ok && wait.one(smem_u32(&S.q_full[seg & 1]), (seg >> 1) & 1);
+        a = Ahead{seq, tiles_of(p, s.tokens, s.chunks.at(c)), c + 1 == s.c1, seg};
+        int q = seq;
+        for (int t = 0; t < 2; ++t) {
+            if (!((a.tiles >> t) & 1u)) continue;
+            if (!full(q)) return;
+            tc_fence_after();
+            const uint64_t k = sdesc(base + q % C::SLOTS * C::TILE, 16u, 1024u), x = sdesc(base + C::OFF_Q + (seg & 1) * C::Q_BYTES, 16u, 1024u);
+            const uint32_t d = tm + C::T_SCORES + ((n & (C::BUF - 1)) * 2 + t) * NT;
+            for (int i = 0; i < steps; ++i)
+                mma_bf16(d, k + (i >> 2) * (kTile * 128 / 16) + (i & 3) * 2, x + (i >> 2) * (NT * 128 / 16) + (i & 3) * 2, SC, i != 0);
+            issued = true;
+            ++q;
+        }
+        mma_commit(smem_u32(&S.scores[n & (C::BUF - 1)]));
+        for (int i = seq; i < q; ++i) mma_commit(smem_u32(&S.empty[i % C::SLOTS]));
+        if (a.last) mma_commit(smem_u32(&S.q_empty[seg & 1]));
+        seq = q + (q - seq);         // past its values
+        ++n;
+        if (++c == s.c1) {
+            more = walk.next(s);
+            ++seg;
+            c = more ? s.c0 : 0;
+        }
+    };
+    // The weighted values of chunk i.
+    auto values = [&](const Ahead &a, int i) {
+        ok = ok && wait.one(smem_u32(&S.probs[i & 1]), (i >> 1) & 1);
+        if (!ok) return;
+        const uint32_t d = tm + C::T_CHUNK + (i & (C::BUF - 1)) * C::STATE;
+        const int tiles = __popc(a.tiles);
+        int q = a.seq + tiles, first = 1;
+        for (int t = 0; t < 2; ++t) {
+            if (!((a.tiles >> t) & 1u)) continue;
+            if (!full(q)) return;
+            tc_fence_after();
+            const uint64_t v = sdesc(base + q % C::SLOTS * C::TILE, kTile * 128u, 1024u);
+            for (int k = 0; k < kTile / 16; ++k) {
+                const int key = t * kTile + k * 16;
+                const uint64_t pr = sdesc(base + C::OFF_P + (i & (C::BUF - 1)) * C::P_BYTES + (key >> 6) * NT * 128, 16u, 1024u) + ((key >> 4) & 3) * 2;
+                mma_bf16(d, v + k * (2048 / 16), pr, PV, !first);
+                mma_ts(d + NT, tm + C::T_ONES, pr, SC, !first);
+                first = 0;
+            }
+            issued = true;
+            ++q;
+        }
+        mma_commit(smem_u32(&S.sums[i & 1]));
+        for (int j = a.seq + tiles; j < q; ++j) mma_commit(smem_u32(&S.empty[j % C::SLOTS]));
+    };
+    Ahead cur{}, next{};
+    bool have = more;
+    if (more) scores(cur);
+    for (int i = 0; ok && have; ++i) {
+        const bool have_next = more;
+        if constexpr (C::BUF == 2) {
+            if (have_next) scores(next);
+            if (ok) values(cur, i);
+        } else {
+            // One buffer of scores: the next are made when P has been.
+            ok = ok && wait.one(smem_u32(&S.probs[i & 1]), (i >> 1) & 1);
+            if (ok && have_next) scores(next);
+            if (ok) values(cur, i);
+        }
+        cur = next;
+        have = have_next;
+    }
+    if (!ok && issued) {
+        mma_commit(smem_u32(&S.drain));
+        wait.drain(smem_u32(&S.drain), 0);
+    }
+}
+
+__device__ __forceinline__ float redux_max(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Whether one of the softmax warps says so; they wait for one another.
+__device__ __forceinline__ bool any_of_four(bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
+// Joins (m, l, o) of two neighbours, the earlier first: each scaled to the larger maximum.
+struct Factors {
+    float a, b, m;
+};
+__device__ __forceinline__ Factors factors(float ma, float mb)
+{
+    const float m = fmaxf(ma, mb), off = m == -INFINITY ? 0.0f : m;
+    return Factors{exp2_fast(ma - off), exp2_fast(mb - off), m};
+}
+__device__ __forceinline__ float join(float a, float b, const Factors &f) { return __fmaf_rn(a, f.a, __fmul_rn(b, f.b)); }
+
+using detg::reg_fence16;
+using detg::tmem_ld16;
+using detg::tmem_st16;
+
+// State `to` (nothing yet with `first`) joined with `from` behind it; TMEM columns of this thread's lane.
+template <int NT>
+__device__ __forceinline__ void join_states(uint32_t to, uint32_t from, bool first)
+{
+#pragma unroll
+    for (int h = 0; h < NT; h += 16) {
+        uint32_t o[16], l[16], m[16];
+        tmem_ld16(from + h, o);
+        tmem_ld16(from + NT + h, l);
+        tmem_ld16(from + 2 * NT + h, m);
+        if (!first) {
+            uint32_t ao[16], al[16], am[16];
+            tmem_ld16(to + h, ao);
+            tmem_ld16(to + NT + h, al);
+            tmem_ld16(to + 2 * NT + h, am);
+            tmem_wait_ld();
+            reg_fence16(o);
+            reg_fence16(l);
+            reg_fence16(m);
+            reg_fence16(ao);
+            reg_fence16(al);
+            reg_fence16(am);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const Factors f = factors(__uint_as_float(am[i]), __uint_as_float(m[i]));
+                o[i] = __float_as_uint(join(__uint_as_float(ao[i]), __uint_as_float(o[i]), f));
+                l[i] = __float_as_uint(join(__uint_as_float(al[i]), __uint_as_float(l[i]), f));
+                m[i] = __float_as_uint(f.m);
+            }
+        } else {
+            tmem_wait_ld();
+            reg_fence16(o);
+            reg_fence16(l);
+            reg_fence16(m);
+        }
+        tmem_st16(to + h, o);
+        tmem_st16(to + NT + h, l);
+        tmem_st16(to + 2 * NT + h, m);
+    }
+    tmem_wait_st();
+}
+
+template <int DH, int NT>
+__device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, const Waits &wait, int warp, int lane)
+{
+    using C = Cfg<DH, NT>;
+    const int row = warp * 32 + lane;                // token of a tile; column of the output
+    const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float c = p.scale * kLog2e;
+    {
+        uint32_t ones[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ones[i] = 0x3F803F80u;
+        detg::tmem_st8(tm + C::T_ONES, ones);        // (the first P's barrier orders it before its use)
+        tmem_wait_st();
+    }
+    Walk walk(p, S);
+    Segment s;
+    bool ok = true;
+    int n = 0, seq = 0;
+    // The chunk whose sums are still to be joined.
+    Segment prev{};
+    int prev_c = -1;
+    // Joins chunk i (the list's c-th of segment g), and writes what is complete.
+    auto finish = [&](const Segment &g, int ch, int i) {
+        ok = ok && wait.warp(smem_u32(&S.sums[i & 1]), (i >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        uint32_t state = tm + C::T_CHUNK + (i & (C::BUF - 1)) * C::STATE;
+        const bool end = ch + 1 == g.c1;
+        // Levels: block, super block, all. A level is closed at its end, or at the segment's.
+        const uint32_t level = tm + C::T_LEVEL;
+        bool closed = true;
+        const int unit = S.unit;
+        int span = 1;
+#pragma unroll 1
+        for (int k = 0; k < 3 && closed; ++k) {
+            if (!g.whole && span >= unit) break;     // larger ones are the second launch's
+            const int next_span = k == 0 ? kBlockChunks : k == 1 ? kSuperChunks : 0x40000000;
+            // The first of its level, and nothing follows: as it is.
+            const bool first = ch / span * span == ch / next_span * next_span;
+            closed = end || (ch + 1) % next_span == 0;
+            if (first && closed) {
+                span = next_span;
+                continue;
+            }
+            join_states<NT>(level + k * C::STATE, state, first);
+            state = level + k * C::STATE;
+            span = next_span;
+        }
+        const bool unit_end = end || (ch + 1) % unit == 0;
+        if (!(g.whole ? end : unit_end)) return;
+        const int head0 = g.kv * p.G + g.part * p.heads, heads = min(p.heads, p.G - g.part * p.heads);
+#pragma unroll
+        for (int h = 0; h < NT; h += 16) {
+            uint32_t o[16], l[16], m[16];
+            tmem_ld16(state + h, o);
+            tmem_ld16(state + NT + h, l);
+            tmem_ld16(state + 2 * NT + h, m);
+            tmem_wait_ld();
+            reg_fence16(o);
+            reg_fence16(l);
+            reg_fence16(m);
+            if (g.whole) {
+#pragma unroll
+                for (int i2 = 0; i2 < 16; ++i2) {
+                    const float sum = __uint_as_float(l[i2]), y = sum == 0.0f ? 0.0f : __uint_as_float(o[i2]) / sum;
+                    if (h + i2 < heads && row < p.D) p.out.row(g.b, head0 + h + i2)[row] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+                }
+            } else {
+                float *part = p.partials + (g.unit0 + ch / unit) * static_cast<long long>(p.heads) * (p.D + 2);
+#pragma unroll
+                for (int i2 = 0; i2 < 16; ++i2) {
+                    if (h + i2 >= heads) continue;
+                    if (row < p.D) part[(h + i2) * p.D + row] = __uint_as_float(o[i2]);
+                    if (row == 0) {
+                        part[p.heads * p.D + h + i2] = __uint_as_float(l[i2]);
+                        part[p.heads * (p.D + 1) + h + i2] = __uint_as_float(m[i2]);
+                    }
+                }
+            }
+        }
+    };
+    while (walk.next(s)) {
+        for (int ch = s.c0; ch < s.c1; ++ch, ++n) {
+            const int chunk = s.chunks.at(ch), token = chunk * kChunk + row;
+            const unsigned tiles = tiles_of(p, s.tokens, chunk);
+            const int count = __popc(tiles);
+            uint32_t x[2][NT];
+            float top[NT];
+            float *shared_top = &S.top[n & 1][0][0];
+            ok = ok && wait.warp(smem_u32(&S.scores[n & (C::BUF - 1)]), (n / C::BUF) & 1);
+            if (ok) {
+                tc_fence_after();
+                const unsigned loaded = S.loaded[n & 15];
+                bool seen[2], edge = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    seen[t] = false;
+                    if ((tiles >> t) & 1u) {
+                        const unsigned have = (loaded >> (16 * t)) & 0xFFFFu;
+                        seen[t] = sees(p, s.tokens, token + t * kTile) && ((have >> (row >> 3)) & 1u);
+                        edge |= have != 0xFFFFu || !sees_every(p, s.tokens, chunk * kChunk + t * kTile, kTile);
+                        const uint32_t at = tm + C::T_SCORES + ((n & (C::BUF - 1)) * 2 + t) * NT;
+                        if constexpr (NT == 16) tmem_ld16(at, x[t]);
+                        else tmem_ld32(at, x[t]);
+                    }
+                }
+                tmem_wait_ld();
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if constexpr (NT == 16) reg_fence16(x[t]);
+                    else reg_fence(x[t]);
+#pragma unroll
+                    for (int h = 0; h < NT; ++h) x[t][h] = __float_as_uint(seen[t] ? __uint_as_float(x[t][h]) * c : -INFINITY);
+                }
+#pragma unroll
+                for (int h = 0; h < NT; ++h) top[h] = redux_max(fmaxf(__uint_as_float(x[0][h]), __uint_as_float(x[1][h])));
+                if (lane == 0) {
+#pragma unroll
+                    for (int h = 0; h < NT; h += 4) *reinterpret_cast<float4 *>(shared_top + warp * 32 + h) = make_float4(top[h], top[h + 1], top[h + 2], top[h + 3]);
+                }
+                // Values of hidden tokens are whatever was there: zeros, for the product.
+                if (edge) {
+                    int v = seq + count;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!((tiles >> t) & 1u)) continue;
+                        ok = ok && wait.warp(smem_u32(&S.full[v % C::SLOTS]), (v / C::SLOTS) & 1);
+                        if (ok && !seen[t]) {
+                            const uint32_t at = base + v % C::SLOTS * C::TILE + row * 128;
+#pragma unroll
+                            for (int h = 0; h < DH / 64; ++h)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + h * kTile * 128 + ((e ^ row) & 7) * 16), "r"(0) : "memory");
+                        }
+                        ++v;
+                    }
+                }
+            }
+            // All four warps leave here together, if one has to: none waits below for another that is gone.
+            if (any_of_four(!ok)) return;
+#pragma unroll
+            for (int h = 0; h < NT; h += 4) {
+                float4 y = *reinterpret_cast<const float4 *>(shared_top + h);
+#pragma unroll
+                for (int w = 1; w < 4; ++w) {
+                    const float4 z = *reinterpret_cast<const float4 *>(shared_top + w * 32 + h);
+                    y = make_float4(fmaxf(y.x, z.x), fmaxf(y.y, z.y), fmaxf(y.z, z.z), fmaxf(y.w, z.w));
+                }
+                top[h] = y.x;
+                top[h + 1] = y.y;
+                top[h + 2] = y.z;
+                top[h + 3] = y.w;
+            }
+            const uint32_t pr = base + C::OFF_P + (n & (C::BUF - 1)) * C::P_BYTES;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!((tiles >> t) & 1u)) continue;
+                const int key = t * kTile + row;
+                const uint32_t at = pr + (key >> 6) * NT * 128 + (key & 7) * 2;
+#pragma unroll
+                for (int h = 0; h < NT; ++h) {
+                    const float y = exp2_fast(__uint_as_float(x[t][h]) - (top[h] == -INFINITY ? 0.0f : top[h]));
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (h >> 3) * 1024 + (h & 7) * 128 + ((((key >> 3) & 7) ^ (h & 7)) * 16)),
+                                 "h"(static_cast<uint16_t>(pack_bf16(y, 0.0f)))
+                                 : "memory");
+                }
+            }
+            // The chunk's maxima beside its sums-to-be.
+            const uint32_t state = tm + C::T_CHUNK + (n & (C::BUF - 1)) * C::STATE + 2 * NT;
+#pragma unroll
+            for (int h = 0; h < NT; h += 16) {
+                uint32_t m[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) m[i] = __float_as_uint(top[h + i]);
+                tmem_st16(state + h, m);
+            }
+            tmem_wait_st();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.probs[n & 1]));
+            seq += 2 * count;
+            if constexpr (C::BUF == 2) {
+                if (prev_c >= 0) finish(prev, prev_c, n - 1);
+                prev = s;
+                prev_c = ch;
+            } else {
+                finish(s, ch, n);
+            }
+        }
+    }
+    if constexpr (C::BUF == 2)
+        if (ok && prev_c >= 0) finish(prev, prev_c, n - 1);
+}
+
+template <int DH, int NT>
+__global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeMaps maps)
+{
+    using C = Cfg<DH, NT>;
+    extern __shared__ uint8_t attn_smem[];
+    const uint32_t raw = smem_u32(attn_smem), base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = attn_smem + (base - raw);
+    Shared &S = *reinterpret_cast<Shared *>(smem + C::OFF_SHARED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        S.abort_flag = 0;
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(smem_u32(&S.full[i]), 1);
+            mbar_init(smem_u32(&S.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&S.q_full[i]), 1);
+            mbar_init(smem_u32(&S.q_empty[i]), 1);
+            mbar_init(smem_u32(&S.scores[i]), 1);
+            mbar_init(smem_u32(&S.probs[i]), 4);
+            mbar_init(smem_u32(&S.sums[i]), 1);
+        }
+        mbar_init(smem_u32(&S.drain), 1);
+        mbar_init(smem_u32(&S.never), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4 && lane == 0) {
+        tmap_prefetch(&maps.q);
+        if (p.pages > 0) {
+            tmap_prefetch(&maps.k);
+            tmap_prefetch(&maps.v);
+        }
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    begin();
+    plan(p, S);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Waits wait{&S.abort_flag, p.status, p.timeout_ns};
+    if (warp < 4) {
+        softmax_role<DH, NT>(p, S, base, wait, warp, lane);
+    } else if (warp == 4) {
+        copy_role<DH, NT>(p, maps, S, base, wait, lane);
+    } else if (warp == 5) {
+        if (elect_one()) issue_role<DH, NT>(p, S, base, wait);
+    } else if (warp == 6) {
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            if (tokens_of(p, b) == 0)
+                for (int i = lane * 8; i < p.H * p.D; i += 256) *reinterpret_cast<uint4 *>(p.out.row(b, i / p.D) + i % p.D) = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
+}
+
+// ------------------------------------------- joining what was cut
+//
+// One block a cut between two CTAs' runs and query head: if it is the first inside a list (a sequence, KV head and part),
+// the list's units are joined: threads of a warpgroup are the columns, warpgroups take super blocks.
+
+constexpr int kJoinGroups = 4;
+
+struct State {
+    float o, l, m;
+};
+__device__ __forceinline__ void join(State &a, const State &b, bool first)
+{
+    if (first) {
+        a = b;
+        return;
+    }
+    const Factors f = factors(a.m, b.m);
+    a.o = join(a.o, b.o, f);
+    a.l = join(a.l, b.l, f);
+    a.m = f.m;
+}
+
+__global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const DecodeParams p, int ctas)
+{
+    begin();
+    __shared__ State at_super[kJoinGroups][128];
+    const long long units = p.prefix[p.B];
+    const int unit = static_cast<int>(p.prefix[p.B + 1]), cut = blockIdx.x + 1, h = blockIdx.y;
+    const long long u = units * cut / ctas;
+    int a = 0, b = p.B;
+    while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (p.prefix[mid] <= u) a = mid;
+        else b = mid;
+    }
+    if (u >= units) return;
+    const long long in = u - p.prefix[a];
+    const int n = static_cast<int>((p.prefix[a + 1] - p.prefix[a]) / (p.KV * p.parts));       // units of a list
+    const int list = static_cast<int>(in / n);
+    const long long lo = p.prefix[a] + static_cast<long long>(list) * n;
+    if (u == lo || units * (cut - 1) / ctas > lo) return;              // at its begin, or not the first cut inside
+    const int kv = list / p.parts, part = list % p.parts, heads = min(p.heads, p.G - part * p.heads);
+    if (h >= heads) return;
+    const int group = threadIdx.x >> 7, d = threadIdx.x & 127, column = min(d, p.D - 1);
+    const long long pitch = static_cast<long long>(p.heads) * (p.D + 2);
+    const float *mine = p.partials + lo * pitch;
+    auto load = [&](int i) {
+        const float *x = mine + i * pitch;
+        return State{x[h * p.D + column], x[p.heads * p.D + h], x[p.heads * (p.D + 1) + h]};
+    };
+    const int per_block = max(1, kBlockChunks / unit), per_super = kSuperChunks / unit, supers = (n + per_super - 1) / per_super;
+    State all{};
+    for (int s0 = 0; s0 < supers; s0 += kJoinGroups) {
+        const int s = s0 + group;
+        if (s < supers) {
+            State super{}, block{};
+            const int end = min(n, (s + 1) * per_super);
+            int i = s * per_super;
+            // Eight loads in flight.
+            while (i < end) {
+                State x[8];
+                const int count = min(8, end - i);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = load(min(i + k, end - 1));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= count) break;
+                    join(block, x[k], (i + k) % per_block == 0);
+                    if ((i + k + 1) % per_block == 0 || i + k + 1 == end) join(super, block, (i + k) / per_block * per_block == s * per_super);
+                }
+                i += count;
+            }
+            at_super[group][d] = super;
+        }
+        __syncthreads();
+        if (group == 0)
+            for (int k = 0; k < kJoinGroups && s0 + k < supers; ++k) join(all, at_super[k][d], s0 + k == 0);
+        __syncthreads();
+    }
+    if (group == 0 && d < p.D) {
+        const float y = all.l == 0.0f ? 0.0f : all.o / all.l;
+        p.out.row(a, kv * p.G + part * p.heads + h)[d] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+    }
+}
+
+template <int DH, int NT>
+cudaError_t run(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStream_t s)
+{
+    using C = Cfg<DH, NT>;
+    auto fn = attn_decode_kernel<DH, NT>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
+    if (e != cudaSuccess) return e;
+    e = launch_early(fn, ctas, kThreads, C::SMEM, 1, s, p, maps);
+    if (e != cudaSuccess || ctas < 2) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(p.heads));
+    cfg.blockDim = dim3(128 * kJoinGroups);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel, p, ctas);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
-cudaError_t launch_attn_decode(const DecodeParams &p, int, cudaStream_t s)
+cudaError_t launch_attn_decode(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStream_t s)
 {
-    attn_decode_rows<<<dim3(p.B, (p.H + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.heads <= 16) return p.D <= 64 ? run<64, 16>(p, maps, ctas, s) : run<128, 16>(p, maps, ctas, s);
+    return p.D <= 64 ? run<64, 32>(p, maps, ctas, s) : run<128, 32>(p, maps, ctas, s);
 }
 
 }  // namespace deto

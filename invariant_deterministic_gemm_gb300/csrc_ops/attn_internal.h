@@ -57,17 +57,44 @@ struct AttnMaps {
 cudaError_t launch_attn(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
 cudaError_t launch_attn_bwd(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
 
+// The key axis of one sequence of a decode step: chunks of 256 keys, four to a block, 16 blocks to a super block. A
+// sequence's result is its super blocks joined in ascending order, each of its blocks, each of its chunks.
+constexpr int kChunk = 256, kBlockChunks = 4, kSuperChunks = 64;
+
 struct DecodeParams {
     Heads q, out;
-    Cache kc, vc;
     const int32_t *table, *lengths;
     long long ldt;
     int B, H, KV, G, D, pages, page_size, max_pages;
+    int parts, heads;                // query heads of a KV head are taken in `parts` of at most `heads`
+    int box;                         // tokens of one copy: a power of two that divides the page
     float scale;
     int window, sinks;
+    long long *prefix;               // [B + 2]: units before each sequence; then chunks a unit
+    float *partials;                 // of each unit: [heads][D] sums, [heads] l, [heads] m
     int *status;
+    unsigned long long timeout_ns;
+    int force_timeout;
 };
-cudaError_t launch_attn_decode(const DecodeParams &p, int sms, cudaStream_t s);
+struct DecodeMaps {
+    CUtensorMap q;                   // (column, head, sequence): boxes of 64 columns of 16 or 32 heads
+    CUtensorMap k, v;                // (column, head, token of a page, page): boxes of 64 columns of `box` tokens
+};
+cudaError_t launch_attn_decode(const DecodeParams &p, const DecodeMaps &maps, int sms, cudaStream_t s);
+
+// Units that a launch of `ctas` may leave in parts: chunks while there are few blocks, blocks while there are few super
+// blocks. At most `tokens` tokens a sequence, `lists` sequences times KV heads.
+constexpr int kUnitsEach = 4;        // units for every CTA that are enough
+inline long long decode_slots(long long lists, long long tokens, long long ctas)
+{
+    const auto least = [](long long a, long long b) { return a < b ? a : b; };
+    const long long chunks = least(lists * ((tokens + kChunk - 1) / kChunk), kUnitsEach * kBlockChunks * ctas);
+    const long long block = kChunk * kBlockChunks, super = kChunk * kSuperChunks;
+    const long long blocks = least(lists * ((tokens + block - 1) / block), kUnitsEach * (kSuperChunks / kBlockChunks) * ctas);
+    const long long supers = lists * ((tokens + super - 1) / super);
+    const long long most = chunks > blocks ? chunks : blocks;
+    return most > supers ? most : supers;
+}
 
 // ---- sequences and what a query sees
 

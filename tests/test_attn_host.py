@@ -56,7 +56,7 @@ DEFAULTS = {
     "det_kv_append": dict(q=A[0], k=A[1], v=A[2], cosine=A[3], sine=A[4], positions=A[5], slots=A[6], q_out=A[7], k_cache=A[8], v_cache=A[9],
                           T=4, H=4, KV=2, D=64, rot=64, P=100, pages=3, page_size=8, interleaved=0, qt=256, qh=64, kt=128, kh=64, vt=128, vh=64,
                           ldt=32, ot=256, oh=64, kcp=1024, kcs=128, kch=64, vcp=1024, vcs=128, vch=64, stream=None),
-    "det_attn_decode_workspace": dict(B=3, H=4, D=64, max_tokens=80),
+    "det_attn_decode_workspace": dict(B=3, H=4, KV=2, D=64, max_tokens=80),
     "det_attn_decode": dict(q=A[0], k_cache=A[1], v_cache=A[2], table=A[3], lengths=A[4], out=A[5], B=3, H=4, KV=2, D=64, pages=20, page_size=16,
                             max_pages=5, scale=0.1, window=0, sinks=0, qt=256, qh=64, kcp=2048, kcs=128, kch=64, vcp=2048, vcs=128, vch=64, ldt=5,
                             ot=256, oh=64, workspace=A[6], workspace_bytes=1 << 30, stream=None),
