@@ -131,8 +131,8 @@ bool ok_turn(int64_t D, int64_t rot, int64_t P)
 // Device memory of the backward pass: delta [H, T].
 int64_t bwd_bytes(int64_t T, int64_t H) { return up(std::max<int64_t>(4 * T * H, 1), 256) * 256; }
 
-// Decode: the query heads of a KV head are taken up to 32 at once; device memory of the sequences' unit counts, and of what
-// the CTAs leave in parts.
+// Decode: the query heads of a KV head are taken up to 32 at once; device memory of the cuts between CTAs, and of what
+// they leave in parts.
 constexpr int64_t kMaxCtas = 160, kTokens = 128;
 struct DecodeSpace {
     int64_t parts, heads, partials, total;
@@ -142,7 +142,7 @@ DecodeSpace decode_space(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t to
     DecodeSpace s;
     s.parts = up(H / KV, 32);
     s.heads = up(H / KV, s.parts);
-    s.partials = up((B + 2) * 8, 256) * 256;
+    s.partials = up(kMaxCtas * static_cast<int64_t>(sizeof(Cut)), 256) * 256;
     s.total = s.partials + up(decode_slots(B * KV * s.parts, tokens, kMaxCtas) * s.heads * (D + 2) * 4, 256) * 256;
     return s;
 }
@@ -295,7 +295,7 @@ det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_c
     p.parts = static_cast<int>(space.parts);
     p.heads = static_cast<int>(space.heads);
     p.box = static_cast<int>(std::min<int64_t>(page_size & -page_size, kTokens));
-    p.prefix = static_cast<long long *>(workspace);
+    p.cuts = static_cast<Cut *>(workspace);
     p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + space.partials);
     p.status = d->word;
     p.timeout_ns = timeout_ns();

@@ -19,15 +19,17 @@
 // in the same order with the same arithmetic. Which those are is found on the
 // device from the lengths, so a captured launch serves any.
 //
-//   warps 0-3   scores to P (a lane a token), P to shared memory as the next
-//               product's operand; the chunk before is joined meanwhile (a lane a
-//               column of the output)
-//   warp 4      copies
-//   warp 5      issues the products
-//   warp 6      sequences without tokens
-// The sum of P is one more product, with ones in TMEM as its left operand: of
-// the rounded P, which the weights then add up to exactly, and without any
-// exchange between lanes. P is rounded to BF16 beside BF16 values.
+//   warps 0-3, 4-7   scores of even and odd chunks to P (a lane a token), P to
+//                    shared memory as the next product's operand
+//   warps 8-11       join the chunks' sums (a lane a column of the output)
+//   warp 12          copies
+//   warp 13          issues the products
+//   warp 14          sequences without tokens
+// A chunk's way through one warpgroup is latency (barriers, TMEM, the maximum
+// over 256 tokens), about as long as its bytes take, so two take turns. The sum
+// of P is one more product, with ones in TMEM as its left operand: of the
+// rounded P, which the weights then add up to exactly, and without any exchange
+// between lanes. P is rounded to BF16 beside BF16 values.
 #include "attn_tile.cuh"
 
 #include <algorithm>
@@ -37,45 +39,48 @@
 namespace deto {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kLaunchRegs = 128;
 
-template <int DH, int NT>
+// HE: query heads that are computed, 4 to 32; the products take at least 16.
+template <int DH, int HE>
 struct Cfg {
+    static constexpr int NT = HE < 16 ? 16 : HE;
     static constexpr int TILE = kTile * DH * 2;
-    static constexpr int SLOTS = DH == 128 ? 6 : 12;
-    static constexpr int BUF = NT == 16 ? 2 : 1;     // of scores, P and a chunk's sums
+    static constexpr int SLOTS = (NT == 16 ? 6 : 5) * (DH == 128 ? 1 : 2);
     static constexpr int Q_BYTES = NT * DH * 2, P_BYTES = NT * kChunk * 2;
     // The ring is followed by more than the 16 KB that a tile of 64 columns' product reads past its end (128 lanes, of which
     // 64 are used).
-    static constexpr int OFF_P = SLOTS * TILE;       // [BUF]
-    static constexpr int OFF_Q = OFF_P + BUF * P_BYTES;             // [2]
+    static constexpr int OFF_P = SLOTS * TILE;       // [2]
+    static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;               // [2]
     static constexpr int OFF_SHARED = OFF_Q + 2 * Q_BYTES;
-    static constexpr int SMEM = OFF_SHARED + 1536 + 1024;
+    static constexpr int SMEM = OFF_SHARED + 3584 + 1024;
     static_assert(OFF_SHARED - OFF_P >= (DH == 64 ? 16384 : 0), "reads past the ring stay inside");
     static_assert(SMEM <= 232448, "shared memory");
-    // TMEM columns. A state: sums [NT], l [NT], m [NT].
-    static constexpr int STATE = 3 * NT;
-    static constexpr int T_SCORES = 0;               // [BUF][2 tiles][NT]
-    static constexpr int T_CHUNK = 2 * NT * BUF;     // [BUF] states
-    static constexpr int T_LEVEL = T_CHUNK + BUF * STATE;           // block, super block, all
-    static constexpr int T_ONES = T_LEVEL + 3 * STATE;
+    // TMEM columns: scores [2][2 tiles][NT], sums of a chunk [2] (values [NT], P [NT]), states of the levels above a block
+    // [2] (values, sum and maximum [HE]), ones.
+    static constexpr int T_SCORES = 0, T_CHUNK = 4 * NT, T_LEVEL = T_CHUNK + 4 * NT, STATE = 3 * HE, T_ONES = T_LEVEL + 2 * STATE;
     static_assert(T_ONES + 8 <= 512, "TMEM");
+    // The joining warps hold two states of up to 96 registers; the service warps hand over what they can do without.
+    static constexpr int JOIN_REGS = HE == 32 ? 208 : 152, SERVICE_REGS = HE == 32 ? 48 : 104;
+    static_assert(JOIN_REGS + SERVICE_REGS <= 2 * kLaunchRegs, "register split");
 };
 
 struct Shared {
-    uint64_t full[12], empty[12], q_full[2], q_empty[2], scores[2], probs[2], sums[2], drain, never;
+    uint64_t full[12], empty[12], q_full[2], q_empty[2], scores[2], probs[2], sums[2], joined[2], drain, never;
     uint32_t tmem;
     int abort_flag;
     unsigned loaded[16];             // of the chunks under way: which groups of eight tokens have a page
-    alignas(16) float top[2][4][32]; // each warp's maxima of a chunk
+    alignas(16) float top[2][2][4][32];   // each warp's maxima of a chunk: of even and odd ones, the last two of each
+    alignas(16) float most[2][32];   // the chunk's
     long long first, last;           // the CTA's units
-    long long scan[8];
+    long long scan[16];
     int start;                       // sequence of the first unit
     int unit;                        // chunks a unit
     long long start_units;           // units before it
     long long total[3];
 };
-static_assert(sizeof(Shared) <= 1536, "shared state");
+static_assert(sizeof(Shared) <= 3584, "shared state");
 
 // ---- the key axis
 
@@ -214,22 +219,28 @@ __device__ void plan(const DecodeParams &p, Shared &S)
             S.start = b;
             S.start_units = before;
         }
-        if (blockIdx.x == 0 && b < p.B) p.prefix[b] = before;
         for (int w = 0; w < kThreads / 32; ++w) carry += S.scan[w];
     }
-    if (blockIdx.x == 0 && thread == 0) {
-        p.prefix[p.B] = units;
-        p.prefix[p.B + 1] = unit;
+    __syncthreads();
+    // The cut at the run's begin, for the second launch: the list that it goes through, if it is the first inside.
+    if (blockIdx.x > 0 && thread == 0) {
+        Cut cut{0, 0, 0, 0, unit};
+        if (first < units) {
+            const int n = (chunks_of(p, tokens_of(p, S.start)).n + unit - 1) / unit;
+            const long long list = (first - S.start_units) / n, lo = S.start_units + list * n;
+            if (first > lo && units * (blockIdx.x - 1) / gridDim.x <= lo) cut = Cut{lo, n, S.start, static_cast<int>(list), unit};
+        }
+        p.cuts[blockIdx.x] = cut;
     }
 }
 
 // ---- roles
 
 // One warp: queries and tiles. A lane looks up the page of eight tokens; lanes at a box's begin copy it.
-template <int DH, int NT>
+template <int DH, int HE>
 __device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared &S, uint32_t base, const Waits &wait, int lane)
 {
-    using C = Cfg<DH, NT>;
+    using C = Cfg<DH, HE>;
     Walk walk(p, S);
     Segment s;
     int seq = 0, seg = 0, n = 0, queries = 0;
@@ -243,7 +254,7 @@ __device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared 
         if (lane == 0) {
             mbar_arrive_expect_tx(qb, C::Q_BYTES);
             for (int h = 0; h < DH / 64; ++h)
-                load_rows(base + C::OFF_Q + (seg & 1) * C::Q_BYTES + h * NT * 128, &maps.q, qb, h * 64, s.kv * p.G + s.part * p.heads, s.b);
+                load_rows(base + C::OFF_Q + (seg & 1) * C::Q_BYTES + h * C::NT * 128, &maps.q, qb, h * 64, s.kv * p.G + s.part * p.heads, s.b);
         }
         for (int c = s.c0; ok && c < s.c1; ++c) {
             const int chunk = s.chunks.at(c);
@@ -307,10 +318,11 @@ struct Ahead {
     int seg;
 };
 
-template <int DH, int NT>
+template <int DH, int HE>
 __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, const Waits &wait)
 {
-    using C = Cfg<DH, NT>;
+    using C = Cfg<DH, HE>;
+    constexpr int NT = C::NT;
     constexpr uint32_t SC = idesc_bf16(kTile, NT, 0, 0), PV = idesc_bf16(kTile, NT, 1, 0);
     const uint32_t tm = S.tmem;
     const int steps = (p.D + 15) / 16;
@@ -332,13 +344,13 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
             if (!full(q)) return;
             tc_fence_after();
             const uint64_t k = sdesc(base + q % C::SLOTS * C::TILE, 16u, 1024u), x = sdesc(base + C::OFF_Q + (seg & 1) * C::Q_BYTES, 16u, 1024u);
-            const uint32_t d = tm + C::T_SCORES + ((n & (C::BUF - 1)) * 2 + t) * NT;
+            const uint32_t d = tm + C::T_SCORES + ((n & 1) * 2 + t) * NT;
             for (int i = 0; i < steps; ++i)
                 mma_bf16(d, k + (i >> 2) * (kTile * 128 / 16) + (i & 3) * 2, x + (i >> 2) * (NT * 128 / 16) + (i & 3) * 2, SC, i != 0);
             issued = true;
             ++q;
         }
-        mma_commit(smem_u32(&S.scores[n & (C::BUF - 1)]));
+        mma_commit(smem_u32(&S.scores[n & 1]));
         for (int i = seq; i < q; ++i) mma_commit(smem_u32(&S.empty[i % C::SLOTS]));
         if (a.last) mma_commit(smem_u32(&S.q_empty[seg & 1]));
         seq = q + (q - seq);         // past its values
@@ -353,7 +365,7 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
     auto values = [&](const Ahead &a, int i) {
         ok = ok && wait.one(smem_u32(&S.probs[i & 1]), (i >> 1) & 1);
         if (!ok) return;
-        const uint32_t d = tm + C::T_CHUNK + (i & (C::BUF - 1)) * C::STATE;
+        const uint32_t d = tm + C::T_CHUNK + (i & 1) * 2 * NT;
         const int tiles = __popc(a.tiles);
         int q = a.seq + tiles, first = 1;
         for (int t = 0; t < 2; ++t) {
@@ -363,7 +375,7 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
             const uint64_t v = sdesc(base + q % C::SLOTS * C::TILE, kTile * 128u, 1024u);
             for (int k = 0; k < kTile / 16; ++k) {
                 const int key = t * kTile + k * 16;
-                const uint64_t pr = sdesc(base + C::OFF_P + (i & (C::BUF - 1)) * C::P_BYTES + (key >> 6) * NT * 128, 16u, 1024u) + ((key >> 4) & 3) * 2;
+                const uint64_t pr = sdesc(base + C::OFF_P + (i & 1) * C::P_BYTES + (key >> 6) * NT * 128, 16u, 1024u) + ((key >> 4) & 3) * 2;
                 mma_bf16(d, v + k * (2048 / 16), pr, PV, !first);
                 mma_ts(d + NT, tm + C::T_ONES, pr, SC, !first);
                 first = 0;
@@ -379,15 +391,8 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
     if (more) scores(cur);
     for (int i = 0; ok && have; ++i) {
         const bool have_next = more;
-        if constexpr (C::BUF == 2) {
-            if (have_next) scores(next);
-            if (ok) values(cur, i);
-        } else {
-            // One buffer of scores: the next are made when P has been.
-            ok = ok && wait.one(smem_u32(&S.probs[i & 1]), (i >> 1) & 1);
-            if (ok && have_next) scores(next);
-            if (ok) values(cur, i);
-        }
+        if (have_next) scores(next);
+        if (ok) values(cur, i);
         cur = next;
         have = have_next;
     }
@@ -404,86 +409,57 @@ __device__ __forceinline__ float redux_max(float v)
     return r;
 }
 
-// Whether one of the softmax warps says so; they wait for one another.
-__device__ __forceinline__ bool any_of_four(bool v)
+// Whether one of a warpgroup's warps says so; they wait for one another (named barrier `id`).
+__device__ __forceinline__ bool any_of_four(bool v, int id)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, 1, 128, q;\n\t"
+        "bar.red.or.pred p, %2, 128, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(v))
+        : "r"(static_cast<uint32_t>(v)), "r"(id)
         : "memory");
     return r != 0;
 }
 
-// Joins (m, l, o) of two neighbours, the earlier first: each scaled to the larger maximum.
-struct Factors {
-    float a, b, m;
-};
-__device__ __forceinline__ Factors factors(float ma, float mb)
+// N TMEM columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void ld(uint32_t at, uint32_t (&r)[N])
 {
-    const float m = fmaxf(ma, mb), off = m == -INFINITY ? 0.0f : m;
-    return Factors{exp2_fast(ma - off), exp2_fast(mb - off), m};
+    if constexpr (N == 4) detg::tmem_ld4(at, r);
+    else if constexpr (N == 8) detg::tmem_ld8(at, r);
+    else if constexpr (N == 16) detg::tmem_ld16(at, r);
+    else tmem_ld32(at, r);
 }
-__device__ __forceinline__ float join(float a, float b, const Factors &f) { return __fmaf_rn(a, f.a, __fmul_rn(b, f.b)); }
-
-using detg::reg_fence16;
-using detg::tmem_ld16;
-using detg::tmem_st16;
-
-// State `to` (nothing yet with `first`) joined with `from` behind it; TMEM columns of this thread's lane.
-template <int NT>
-__device__ __forceinline__ void join_states(uint32_t to, uint32_t from, bool first)
+template <int N>
+__device__ __forceinline__ void st(uint32_t at, const uint32_t (&r)[N])
 {
-#pragma unroll
-    for (int h = 0; h < NT; h += 16) {
-        uint32_t o[16], l[16], m[16];
-        tmem_ld16(from + h, o);
-        tmem_ld16(from + NT + h, l);
-        tmem_ld16(from + 2 * NT + h, m);
-        if (!first) {
-            uint32_t ao[16], al[16], am[16];
-            tmem_ld16(to + h, ao);
-            tmem_ld16(to + NT + h, al);
-            tmem_ld16(to + 2 * NT + h, am);
-            tmem_wait_ld();
-            reg_fence16(o);
-            reg_fence16(l);
-            reg_fence16(m);
-            reg_fence16(ao);
-            reg_fence16(al);
-            reg_fence16(am);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const Factors f = factors(__uint_as_float(am[i]), __uint_as_float(m[i]));
-                o[i] = __float_as_uint(join(__uint_as_float(ao[i]), __uint_as_float(o[i]), f));
-                l[i] = __float_as_uint(join(__uint_as_float(al[i]), __uint_as_float(l[i]), f));
-                m[i] = __float_as_uint(f.m);
-            }
-        } else {
-            tmem_wait_ld();
-            reg_fence16(o);
-            reg_fence16(l);
-            reg_fence16(m);
-        }
-        tmem_st16(to + h, o);
-        tmem_st16(to + NT + h, l);
-        tmem_st16(to + 2 * NT + h, m);
-    }
-    tmem_wait_st();
+    if constexpr (N == 4) detg::tmem_st4(at, r);
+    else if constexpr (N == 8) detg::tmem_st8(at, r);
+    else if constexpr (N == 16) detg::tmem_st16(at, r);
+    else tmem_st32(at, r);
+}
+template <int N>
+__device__ __forceinline__ void fence(uint32_t (&r)[N])
+{
+    if constexpr (N == 4) detg::reg_fence4(r);
+    else if constexpr (N == 8) detg::reg_fence8(r);
+    else if constexpr (N == 16) detg::reg_fence16(r);
+    else reg_fence(r);
 }
 
-template <int DH, int NT>
-__device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, const Waits &wait, int warp, int lane)
+// One of two warpgroups: the chunks n with n % 2 == group.
+template <int DH, int HE>
+__device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, const Waits &wait, int group, int warp, int lane)
 {
-    using C = Cfg<DH, NT>;
-    const int row = warp * 32 + lane;                // token of a tile; column of the output
+    using C = Cfg<DH, HE>;
+    constexpr int NT = C::NT;
+    const int row = warp * 32 + lane;                // token of a tile
     const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float c = p.scale * kLog2e;
-    {
+    if (group == 0) {
         uint32_t ones[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) ones[i] = 0x3F803F80u;
@@ -494,78 +470,18 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
     Segment s;
     bool ok = true;
     int n = 0, seq = 0;
-    // The chunk whose sums are still to be joined.
-    Segment prev{};
-    int prev_c = -1;
-    // Joins chunk i (the list's c-th of segment g), and writes what is complete.
-    auto finish = [&](const Segment &g, int ch, int i) {
-        ok = ok && wait.warp(smem_u32(&S.sums[i & 1]), (i >> 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        uint32_t state = tm + C::T_CHUNK + (i & (C::BUF - 1)) * C::STATE;
-        const bool end = ch + 1 == g.c1;
-        // Levels: block, super block, all. A level is closed at its end, or at the segment's.
-        const uint32_t level = tm + C::T_LEVEL;
-        bool closed = true;
-        const int unit = S.unit;
-        int span = 1;
-#pragma unroll 1
-        for (int k = 0; k < 3 && closed; ++k) {
-            if (!g.whole && span >= unit) break;     // larger ones are the second launch's
-            const int next_span = k == 0 ? kBlockChunks : k == 1 ? kSuperChunks : 0x40000000;
-            // The first of its level, and nothing follows: as it is.
-            const bool first = ch / span * span == ch / next_span * next_span;
-            closed = end || (ch + 1) % next_span == 0;
-            if (first && closed) {
-                span = next_span;
-                continue;
-            }
-            join_states<NT>(level + k * C::STATE, state, first);
-            state = level + k * C::STATE;
-            span = next_span;
-        }
-        const bool unit_end = end || (ch + 1) % unit == 0;
-        if (!(g.whole ? end : unit_end)) return;
-        const int head0 = g.kv * p.G + g.part * p.heads, heads = min(p.heads, p.G - g.part * p.heads);
-#pragma unroll
-        for (int h = 0; h < NT; h += 16) {
-            uint32_t o[16], l[16], m[16];
-            tmem_ld16(state + h, o);
-            tmem_ld16(state + NT + h, l);
-            tmem_ld16(state + 2 * NT + h, m);
-            tmem_wait_ld();
-            reg_fence16(o);
-            reg_fence16(l);
-            reg_fence16(m);
-            if (g.whole) {
-#pragma unroll
-                for (int i2 = 0; i2 < 16; ++i2) {
-                    const float sum = __uint_as_float(l[i2]), y = sum == 0.0f ? 0.0f : __uint_as_float(o[i2]) / sum;
-                    if (h + i2 < heads && row < p.D) p.out.row(g.b, head0 + h + i2)[row] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
-                }
-            } else {
-                float *part = p.partials + (g.unit0 + ch / unit) * static_cast<long long>(p.heads) * (p.D + 2);
-#pragma unroll
-                for (int i2 = 0; i2 < 16; ++i2) {
-                    if (h + i2 >= heads) continue;
-                    if (row < p.D) part[(h + i2) * p.D + row] = __uint_as_float(o[i2]);
-                    if (row == 0) {
-                        part[p.heads * p.D + h + i2] = __uint_as_float(l[i2]);
-                        part[p.heads * (p.D + 1) + h + i2] = __uint_as_float(m[i2]);
-                    }
-                }
-            }
-        }
-    };
     while (walk.next(s)) {
         for (int ch = s.c0; ch < s.c1; ++ch, ++n) {
             const int chunk = s.chunks.at(ch), token = chunk * kChunk + row;
             const unsigned tiles = tiles_of(p, s.tokens, chunk);
-            const int count = __popc(tiles);
-            uint32_t x[2][NT];
-            float top[NT];
-            float *shared_top = &S.top[n & 1][0][0];
-            ok = ok && wait.warp(smem_u32(&S.scores[n & (C::BUF - 1)]), (n / C::BUF) & 1);
+            const int count = __popc(tiles), keys = seq;
+            seq += 2 * count;
+            if ((n & 1) != group) continue;
+            const uint32_t phase = (n >> 1) & 1;
+            uint32_t x[2][HE];
+            float top[HE];
+            float *shared_top = &S.top[group][phase][0][0];
+            ok = ok && wait.warp(smem_u32(&S.scores[group]), phase);
             if (ok) {
                 tc_fence_after();
                 const unsigned loaded = S.loaded[n & 15];
@@ -577,28 +493,25 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                         const unsigned have = (loaded >> (16 * t)) & 0xFFFFu;
                         seen[t] = sees(p, s.tokens, token + t * kTile) && ((have >> (row >> 3)) & 1u);
                         edge |= have != 0xFFFFu || !sees_every(p, s.tokens, chunk * kChunk + t * kTile, kTile);
-                        const uint32_t at = tm + C::T_SCORES + ((n & (C::BUF - 1)) * 2 + t) * NT;
-                        if constexpr (NT == 16) tmem_ld16(at, x[t]);
-                        else tmem_ld32(at, x[t]);
+                        ld<HE>(tm + C::T_SCORES + (group * 2 + t) * NT, x[t]);
                     }
                 }
                 tmem_wait_ld();
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if constexpr (NT == 16) reg_fence16(x[t]);
-                    else reg_fence(x[t]);
+                    fence<HE>(x[t]);
 #pragma unroll
-                    for (int h = 0; h < NT; ++h) x[t][h] = __float_as_uint(seen[t] ? __uint_as_float(x[t][h]) * c : -INFINITY);
+                    for (int h = 0; h < HE; ++h) x[t][h] = __float_as_uint(seen[t] ? __uint_as_float(x[t][h]) * c : -INFINITY);
                 }
 #pragma unroll
-                for (int h = 0; h < NT; ++h) top[h] = redux_max(fmaxf(__uint_as_float(x[0][h]), __uint_as_float(x[1][h])));
+                for (int h = 0; h < HE; ++h) top[h] = redux_max(fmaxf(__uint_as_float(x[0][h]), __uint_as_float(x[1][h])));
                 if (lane == 0) {
 #pragma unroll
-                    for (int h = 0; h < NT; h += 4) *reinterpret_cast<float4 *>(shared_top + warp * 32 + h) = make_float4(top[h], top[h + 1], top[h + 2], top[h + 3]);
+                    for (int h = 0; h < HE; h += 4) *reinterpret_cast<float4 *>(shared_top + warp * 32 + h) = make_float4(top[h], top[h + 1], top[h + 2], top[h + 3]);
                 }
                 // Values of hidden tokens are whatever was there: zeros, for the product.
                 if (edge) {
-                    int v = seq + count;
+                    int v = keys + count;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!((tiles >> t) & 1u)) continue;
@@ -614,68 +527,189 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                         ++v;
                     }
                 }
+                // The chunk two before has been joined: its P, its sums and its maxima make room.
+                ok = ok && wait.warp(smem_u32(&S.joined[group]), phase ^ 1u);
             }
             // All four warps leave here together, if one has to: none waits below for another that is gone.
-            if (any_of_four(!ok)) return;
+            if (any_of_four(!ok, 1 + group)) return;
 #pragma unroll
-            for (int h = 0; h < NT; h += 4) {
+            for (int h = 0; h < HE; h += 4) {
                 float4 y = *reinterpret_cast<const float4 *>(shared_top + h);
 #pragma unroll
                 for (int w = 1; w < 4; ++w) {
                     const float4 z = *reinterpret_cast<const float4 *>(shared_top + w * 32 + h);
                     y = make_float4(fmaxf(y.x, z.x), fmaxf(y.y, z.y), fmaxf(y.z, z.z), fmaxf(y.w, z.w));
                 }
+                if (row == 0) *reinterpret_cast<float4 *>(&S.most[group][h]) = y;
                 top[h] = y.x;
                 top[h + 1] = y.y;
                 top[h + 2] = y.z;
                 top[h + 3] = y.w;
             }
-            const uint32_t pr = base + C::OFF_P + (n & (C::BUF - 1)) * C::P_BYTES;
+            const uint32_t pr = base + C::OFF_P + group * C::P_BYTES;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (!((tiles >> t) & 1u)) continue;
                 const int key = t * kTile + row;
                 const uint32_t at = pr + (key >> 6) * NT * 128 + (key & 7) * 2;
 #pragma unroll
-                for (int h = 0; h < NT; ++h) {
+                for (int h = 0; h < HE; ++h) {
                     const float y = exp2_fast(__uint_as_float(x[t][h]) - (top[h] == -INFINITY ? 0.0f : top[h]));
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (h >> 3) * 1024 + (h & 7) * 128 + ((((key >> 3) & 7) ^ (h & 7)) * 16)),
                                  "h"(static_cast<uint16_t>(pack_bf16(y, 0.0f)))
                                  : "memory");
                 }
             }
-            // The chunk's maxima beside its sums-to-be.
-            const uint32_t state = tm + C::T_CHUNK + (n & (C::BUF - 1)) * C::STATE + 2 * NT;
-#pragma unroll
-            for (int h = 0; h < NT; h += 16) {
-                uint32_t m[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) m[i] = __float_as_uint(top[h + i]);
-                tmem_st16(state + h, m);
-            }
-            tmem_wait_st();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.probs[n & 1]));
-            seq += 2 * count;
-            if constexpr (C::BUF == 2) {
-                if (prev_c >= 0) finish(prev, prev_c, n - 1);
-                prev = s;
-                prev_c = ch;
+            if (lane == 0) mbar_arrive(smem_u32(&S.probs[group]));
+        }
+    }
+}
+
+// Joins (m, l, o) of two neighbours, the earlier first: each scaled to the larger maximum.
+struct Factors {
+    float a, b, m;
+};
+__device__ __forceinline__ Factors factors(float ma, float mb)
+{
+    const float m = fmaxf(ma, mb), off = m == -INFINITY ? 0.0f : m;
+    return Factors{exp2_fast(ma - off), exp2_fast(mb - off), m};
+}
+__device__ __forceinline__ float join(float a, float b, const Factors &f) { return __fmaf_rn(a, f.a, __fmul_rn(b, f.b)); }
+
+// Column `row` of the sums of every head, their l and m.
+template <int HE>
+struct Sums {
+    uint32_t o[HE], l[HE], m[HE];
+    // This, then `next`: into this.
+    __device__ __forceinline__ void join_next(const Sums &next)
+    {
+#pragma unroll
+        for (int i = 0; i < HE; ++i) {
+            const Factors f = factors(__uint_as_float(m[i]), __uint_as_float(next.m[i]));
+            o[i] = __float_as_uint(join(__uint_as_float(o[i]), __uint_as_float(next.o[i]), f));
+            l[i] = __float_as_uint(join(__uint_as_float(l[i]), __uint_as_float(next.l[i]), f));
+            m[i] = __float_as_uint(f.m);
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t at)
+    {
+        ld<HE>(at, o);
+        ld<HE>(at + HE, l);
+        ld<HE>(at + 2 * HE, m);
+        tmem_wait_ld();
+        fence<HE>(o);
+        fence<HE>(l);
+        fence<HE>(m);
+    }
+    __device__ __forceinline__ void store(uint32_t at) const
+    {
+        st<HE>(at, o);
+        st<HE>(at + HE, l);
+        st<HE>(at + 2 * HE, m);
+        tmem_wait_st();
+    }
+};
+
+// One warpgroup: the chunks' sums in order. A block's are kept in registers, those of a super block and of all in TMEM.
+template <int DH, int HE>
+__device__ void join_role(const DecodeParams &p, Shared &S, const Waits &wait, int warp, int lane)
+{
+    using C = Cfg<DH, HE>;
+    constexpr int NT = C::NT;
+    const int row = warp * 32 + lane, unit = S.unit;
+    const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    Walk walk(p, S);
+    Segment s;
+    int n = 0;
+    Sums<HE> sums;
+    while (walk.next(s)) {
+        const int head0 = s.kv * p.G + s.part * p.heads, heads = min(p.heads, p.G - s.part * p.heads);
+        for (int ch = s.c0; ch < s.c1; ++ch, ++n) {
+            if (!wait.warp(smem_u32(&S.sums[n & 1]), (n >> 1) & 1)) return;
+            tc_fence_after();
+            Sums<HE> x;
+            ld<HE>(tm + C::T_CHUNK + (n & 1) * 2 * NT, x.o);
+            ld<HE>(tm + C::T_CHUNK + (n & 1) * 2 * NT + NT, x.l);
+#pragma unroll
+            for (int h = 0; h < HE; h += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(&S.most[n & 1][h]);
+                x.m[h] = __float_as_uint(y.x);
+                x.m[h + 1] = __float_as_uint(y.y);
+                x.m[h + 2] = __float_as_uint(y.z);
+                x.m[h + 3] = __float_as_uint(y.w);
+            }
+            tmem_wait_ld();
+            fence<HE>(x.o);
+            fence<HE>(x.l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.joined[n & 1]));
+            const bool end = ch + 1 == s.c1;
+            // A unit that is one chunk of a list that others have parts of goes as it is; a block begins with its first.
+            if ((unit == 1 && !s.whole) || ch % kBlockChunks == 0) {
+                sums = x;
             } else {
-                finish(s, ch, n);
+                sums.join_next(x);
+            }
+            if (s.whole || unit > kBlockChunks) {
+                // The block is over: into its super block, which is over as well at its end or the list's.
+                if (!end && (ch + 1) % kBlockChunks != 0) continue;
+                const bool super_end = end || (ch + 1) % kSuperChunks == 0;
+                if (ch / kBlockChunks * kBlockChunks != ch / kSuperChunks * kSuperChunks) {
+                    Sums<HE> before;
+                    before.load(tm + C::T_LEVEL);
+                    before.join_next(sums);
+                    sums = before;
+                }
+                if (!super_end) {
+                    sums.store(tm + C::T_LEVEL);
+                    continue;
+                }
+                if (s.whole) {
+                    if (ch >= kSuperChunks) {
+                        Sums<HE> before;
+                        before.load(tm + C::T_LEVEL + C::STATE);
+                        before.join_next(sums);
+                        sums = before;
+                    }
+                    if (!end) {
+                        sums.store(tm + C::T_LEVEL + C::STATE);
+                        continue;
+                    }
+                }
+            } else if (!end && (ch + 1) % unit != 0) {
+                continue;
+            }
+            if (s.whole) {
+#pragma unroll
+                for (int h = 0; h < HE; ++h) {
+                    if (h >= heads) break;
+                    const float l = __uint_as_float(sums.l[h]), y = l == 0.0f ? 0.0f : __fdiv_rn(__uint_as_float(sums.o[h]), l);
+                    if (row < p.D) p.out.row(s.b, head0 + h)[row] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+                }
+            } else {
+                float *part = p.partials + (s.unit0 + ch / unit) * static_cast<long long>(p.heads) * (p.D + 2);
+#pragma unroll
+                for (int h = 0; h < HE; ++h) {
+                    if (h >= heads) break;
+                    if (row < p.D) part[h * p.D + row] = __uint_as_float(sums.o[h]);
+                    if (row == 0) {
+                        part[p.heads * p.D + h] = __uint_as_float(sums.l[h]);
+                        part[p.heads * (p.D + 1) + h] = __uint_as_float(sums.m[h]);
+                    }
+                }
             }
         }
     }
-    if constexpr (C::BUF == 2)
-        if (ok && prev_c >= 0) finish(prev, prev_c, n - 1);
 }
 
-template <int DH, int NT>
+template <int DH, int HE>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeMaps maps)
 {
-    using C = Cfg<DH, NT>;
+    using C = Cfg<DH, HE>;
     extern __shared__ uint8_t attn_smem[];
     const uint32_t raw = smem_u32(attn_smem), base = (raw + 1023u) & ~1023u;
     uint8_t *smem = attn_smem + (base - raw);
@@ -693,52 +727,60 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             mbar_init(smem_u32(&S.scores[i]), 1);
             mbar_init(smem_u32(&S.probs[i]), 4);
             mbar_init(smem_u32(&S.sums[i]), 1);
+            mbar_init(smem_u32(&S.joined[i]), 4);
         }
         mbar_init(smem_u32(&S.drain), 1);
         mbar_init(smem_u32(&S.never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == 12 && lane == 0) {
         tmap_prefetch(&maps.q);
         if (p.pages > 0) {
             tmap_prefetch(&maps.k);
             tmap_prefetch(&maps.v);
         }
     }
-    if (warp == 5) {
+    if (warp == 13) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    begin();
+    wait_for_last();
     plan(p, S);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const Waits wait{&S.abort_flag, p.status, p.timeout_ns};
-    if (warp < 4) {
-        softmax_role<DH, NT>(p, S, base, wait, warp, lane);
-    } else if (warp == 4) {
-        copy_role<DH, NT>(p, maps, S, base, wait, lane);
-    } else if (warp == 5) {
-        if (elect_one()) issue_role<DH, NT>(p, S, base, wait);
-    } else if (warp == 6) {
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-            if (tokens_of(p, b) == 0)
-                for (int i = lane * 8; i < p.H * p.D; i += 256) *reinterpret_cast<uint4 *>(p.out.row(b, i / p.D) + i % p.D) = make_uint4(0, 0, 0, 0);
+    if (warp < 8) {
+        softmax_role<DH, HE>(p, S, base, wait, warp >> 2, warp & 3, lane);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::JOIN_REGS));
+        join_role<DH, HE>(p, S, wait, warp & 3, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::SERVICE_REGS));
+        if (warp == 12) {
+            copy_role<DH, HE>(p, maps, S, base, wait, lane);
+        } else if (warp == 13) {
+            if (elect_one()) issue_role<DH, HE>(p, S, base, wait);
+        } else if (warp == 14) {
+            for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+                if (tokens_of(p, b) == 0)
+                    for (int i = lane * 8; i < p.H * p.D; i += 256) *reinterpret_cast<uint4 *>(p.out.row(b, i / p.D) + i % p.D) = make_uint4(0, 0, 0, 0);
+        }
     }
+    let_next_begin();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
+    if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
 }
 
 // ------------------------------------------- joining what was cut
 //
-// One block a cut between two CTAs' runs and query head: if it is the first inside a list (a sequence, KV head and part),
-// the list's units are joined: threads of a warpgroup are the columns, warpgroups take super blocks.
+// One block a CTA whose run begins inside a list (a sequence, KV head and part), the first of those, and query head: the
+// list's units are joined. Threads of a warpgroup are the columns, warpgroups take super blocks.
 
-constexpr int kJoinGroups = 4;
+constexpr int kJoinGroups = 8;
 
 struct State {
     float o, l, m;
@@ -755,30 +797,18 @@ __device__ __forceinline__ void join(State &a, const State &b, bool first)
     a.m = f.m;
 }
 
-__global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const DecodeParams p, int ctas)
+__global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const DecodeParams p)
 {
-    begin();
+    wait_for_last();
     __shared__ State at_super[kJoinGroups][128];
-    const long long units = p.prefix[p.B];
-    const int unit = static_cast<int>(p.prefix[p.B + 1]), cut = blockIdx.x + 1, h = blockIdx.y;
-    const long long u = units * cut / ctas;
-    int a = 0, b = p.B;
-    while (b - a > 1) {
-        const int mid = (a + b) >> 1;
-        if (p.prefix[mid] <= u) a = mid;
-        else b = mid;
-    }
-    if (u >= units) return;
-    const long long in = u - p.prefix[a];
-    const int n = static_cast<int>((p.prefix[a + 1] - p.prefix[a]) / (p.KV * p.parts));       // units of a list
-    const int list = static_cast<int>(in / n);
-    const long long lo = p.prefix[a] + static_cast<long long>(list) * n;
-    if (u == lo || units * (cut - 1) / ctas > lo) return;              // at its begin, or not the first cut inside
-    const int kv = list / p.parts, part = list % p.parts, heads = min(p.heads, p.G - part * p.heads);
+    const Cut cut = p.cuts[blockIdx.x + 1];
+    const int n = cut.n, unit = cut.unit, h = blockIdx.y;
+    if (n == 0) return;
+    const int kv = cut.list / p.parts, part = cut.list % p.parts, heads = min(p.heads, p.G - part * p.heads);
     if (h >= heads) return;
     const int group = threadIdx.x >> 7, d = threadIdx.x & 127, column = min(d, p.D - 1);
     const long long pitch = static_cast<long long>(p.heads) * (p.D + 2);
-    const float *mine = p.partials + lo * pitch;
+    const float *mine = p.partials + cut.first * pitch;
     auto load = [&](int i) {
         const float *x = mine + i * pitch;
         return State{x[h * p.D + column], x[p.heads * p.D + h], x[p.heads * (p.D + 1) + h]};
@@ -813,18 +843,25 @@ __global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const Deco
         __syncthreads();
     }
     if (group == 0 && d < p.D) {
-        const float y = all.l == 0.0f ? 0.0f : all.o / all.l;
-        p.out.row(a, kv * p.G + part * p.heads + h)[d] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
+        const float y = all.l == 0.0f ? 0.0f : __fdiv_rn(all.o, all.l);
+        p.out.row(cut.b, kv * p.G + part * p.heads + h)[d] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
     }
 }
 
-template <int DH, int NT>
+template <int DH, int HE>
 cudaError_t run(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStream_t s)
 {
-    using C = Cfg<DH, NT>;
-    auto fn = attn_decode_kernel<DH, NT>;
+    using C = Cfg<DH, HE>;
+    auto fn = attn_decode_kernel<DH, HE>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = once_per_device(done, [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
+    cudaError_t e = once_per_device(done, [&] {
+        cudaFuncAttributes a;
+        const cudaError_t x = cudaFuncGetAttributes(&a, fn);
+        if (x != cudaSuccess) return x;
+        // setmaxnreg shares out exactly the registers of the launch.
+        if (a.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
     if (e != cudaSuccess) return e;
     e = launch_early(fn, ctas, kThreads, C::SMEM, 1, s, p, maps);
     if (e != cudaSuccess || ctas < 2) return e;
@@ -837,16 +874,23 @@ cudaError_t run(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStr
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel, p, ctas);
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int DH>
+cudaError_t run(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStream_t s)
+{
+    if (p.heads <= 4) return run<DH, 4>(p, maps, ctas, s);
+    if (p.heads <= 8) return run<DH, 8>(p, maps, ctas, s);
+    return p.heads <= 16 ? run<DH, 16>(p, maps, ctas, s) : run<DH, 32>(p, maps, ctas, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_decode(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStream_t s)
 {
-    if (p.heads <= 16) return p.D <= 64 ? run<64, 16>(p, maps, ctas, s) : run<128, 16>(p, maps, ctas, s);
-    return p.D <= 64 ? run<64, 32>(p, maps, ctas, s) : run<128, 32>(p, maps, ctas, s);
+    return p.D <= 64 ? run<64>(p, maps, ctas, s) : run<128>(p, maps, ctas, s);
 }
 
 }  // namespace deto

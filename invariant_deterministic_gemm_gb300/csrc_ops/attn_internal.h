@@ -61,6 +61,13 @@ cudaError_t launch_attn_bwd(const AttnParams &p, const AttnMaps &maps, cudaStrea
 // sequence's result is its super blocks joined in ascending order, each of its blocks, each of its chunks.
 constexpr int kChunk = 256, kBlockChunks = 4, kSuperChunks = 64;
 
+// Where a CTA's run begins inside a list (a sequence, KV head and part of its query heads), if no CTA before it does: the
+// list's first unit and their number (0: nothing to join), chunks a unit.
+struct Cut {
+    long long first;
+    int n, b, list, unit;
+};
+
 struct DecodeParams {
     Heads q, out;
     const int32_t *table, *lengths;
@@ -70,7 +77,7 @@ struct DecodeParams {
     int box;                         // tokens of one copy: a power of two that divides the page
     float scale;
     int window, sinks;
-    long long *prefix;               // [B + 2]: units before each sequence; then chunks a unit
+    Cut *cuts;                       // of each CTA's begin
     float *partials;                 // of each unit: [heads][D] sums, [heads] l, [heads] m
     int *status;
     unsigned long long timeout_ns;
