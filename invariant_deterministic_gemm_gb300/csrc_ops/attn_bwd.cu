@@ -218,14 +218,14 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
     auto scores = [&](int i) {
         if (!arrived(2 * i)) return;
         tc_fence_after();
-        mma_scores(tm + (i & 1) * kTile, base, ring + 2 * i % C::SLOTS * C::TILE, steps);
+        mma_scores<DH>(tm + (i & 1) * kTile, base, ring + 2 * i % C::SLOTS * C::TILE, steps);
         mma_commit(smem_u32(&S.scores[i & 1]));
         issued = true;
     };
     auto dp = [&](int i) {
         if (!arrived(2 * i + 1)) return;
         tc_fence_after();
-        mma_scores(tm + 2 * kTile, base + C::TILE, ring + (2 * i + 1) % C::SLOTS * C::TILE, steps);
+        mma_scores<DH>(tm + 2 * kTile, base + C::TILE, ring + (2 * i + 1) % C::SLOTS * C::TILE, steps);
         mma_commit(smem_u32(&S.dp));
         mma_commit(smem_u32(&S.empty[(2 * i + 1) % C::SLOTS]));
         issued = true;
@@ -589,7 +589,7 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
         ok = ok && wait.one(smem_u32(&S.q_full[i & 1]), (i >> 1) & 1);
         if (!ok) return;
         tc_fence_after();
-        mma_scores(tm, base, base + C::OFF_Q + (i & 1) * C::TILE, steps);
+        mma_scores<DH>(tm, base, base + C::OFF_Q + (i & 1) * C::TILE, steps);
         mma_commit(smem_u32(&S.scores));
         issued = true;
     };
@@ -597,7 +597,7 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
         ok = ok && wait.one(smem_u32(&S.d_full[i & 1]), (i >> 1) & 1);
         if (!ok) return;
         tc_fence_after();
-        mma_scores(tm + kTile, base + C::TILE, base + C::OFF_D + (i & 1) * C::TILE, steps);
+        mma_scores<DH>(tm + kTile, base + C::TILE, base + C::OFF_D + (i & 1) * C::TILE, steps);
         mma_commit(smem_u32(&S.dp));
         issued = true;
     };

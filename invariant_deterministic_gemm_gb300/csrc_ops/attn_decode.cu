@@ -22,14 +22,13 @@
 //   warps 0-3, 4-7   scores of even and odd chunks to P (a lane a token), P to
 //                    shared memory as the next product's operand
 //   warps 8-11       join the chunks' sums (a lane a column of the output)
-//   warp 12          copies
+//   warps 12, 14     copies of keys and of values
 //   warp 13          issues the products
-//   warp 14          sequences without tokens
+//   warp 15          looks up the pages, some chunks ahead; sequences without tokens
 // A chunk's way through one warpgroup is latency (barriers, TMEM, the maximum
-// over 256 tokens), about as long as its bytes take, so two take turns. The sum
-// of P is one more product, with ones in TMEM as its left operand: of the
-// rounded P, which the weights then add up to exactly, and without any exchange
-// between lanes. P is rounded to BF16 beside BF16 values.
+// over 256 tokens), about as long as its bytes take, so two take turns. P is
+// rounded to BF16 beside BF16 values, and the sum is that of the rounded ones:
+// the weights add up to one.
 #include "attn_tile.cuh"
 
 #include <algorithm>
@@ -41,46 +40,50 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128;
+constexpr int kSums = 2;             // chunks whose sums wait to be joined (four: 78 instead of 74 us for 96 windows of 1024)
 
 // HE: query heads that are computed, 4 to 32; the products take at least 16.
 template <int DH, int HE>
 struct Cfg {
     static constexpr int NT = HE < 16 ? 16 : HE;
     static constexpr int TILE = kTile * DH * 2;
-    static constexpr int SLOTS = (NT == 16 ? 6 : 5) * (DH == 128 ? 1 : 2);
+    // Tiles of keys and of values in rings of their own: keys leave with their scores, values a chunk's softmax later.
+    static constexpr int KEYS = (NT == 16 ? 3 : 2) * (DH == 128 ? 1 : 2), VALUES = 3 * (DH == 128 ? 1 : 2), SLOTS = KEYS + VALUES;
     static constexpr int Q_BYTES = NT * DH * 2, P_BYTES = NT * kChunk * 2;
     // The ring is followed by more than the 16 KB that a tile of 64 columns' product reads past its end (128 lanes, of which
     // 64 are used).
     static constexpr int OFF_P = SLOTS * TILE;       // [2]
     static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;               // [2]
     static constexpr int OFF_SHARED = OFF_Q + 2 * Q_BYTES;
-    static constexpr int SMEM = OFF_SHARED + 3584 + 1024;
+    static constexpr int SMEM = OFF_SHARED + 7168 + 1024;
     static_assert(OFF_SHARED - OFF_P >= (DH == 64 ? 16384 : 0), "reads past the ring stay inside");
     static_assert(SMEM <= 232448, "shared memory");
-    // TMEM columns: scores [2][2 tiles][NT], sums of a chunk [2] (values [NT], P [NT]), states of the levels above a block
-    // [2] (values, sum and maximum [HE]), ones.
-    static constexpr int T_SCORES = 0, T_CHUNK = 4 * NT, T_LEVEL = T_CHUNK + 4 * NT, STATE = 3 * HE, T_ONES = T_LEVEL + 2 * STATE;
-    static_assert(T_ONES + 8 <= 512, "TMEM");
+    // TMEM columns: scores [2][2 tiles][NT], weighted values of a chunk [kSums][NT], states of the levels above a block [2]
+    // (values, sum and maximum [HE]).
+    static constexpr int T_SCORES = 0, T_CHUNK = 4 * NT, T_LEVEL = T_CHUNK + kSums * NT, STATE = 3 * HE;
+    static_assert(T_LEVEL + 2 * STATE <= 512, "TMEM");
     // The joining warps hold two states of up to 96 registers; the service warps hand over what they can do without.
     static constexpr int JOIN_REGS = HE == 32 ? 208 : 152, SERVICE_REGS = HE == 32 ? 48 : 104;
     static_assert(JOIN_REGS + SERVICE_REGS <= 2 * kLaunchRegs, "register split");
 };
 
 struct Shared {
-    uint64_t full[12], empty[12], q_full[2], q_empty[2], scores[2], probs[2], sums[2], joined[2], drain, never;
+    uint64_t full[12], empty[12], q_full[2], q_empty[2], scores[2], probs[2], sums[kSums], joined[kSums], pages_full[8], pages_empty[8], drain, never;
     uint32_t tmem;
     int abort_flag;
-    unsigned loaded[16];             // of the chunks under way: which groups of eight tokens have a page
+    int page[8][32];                 // of the chunks ahead: the page of each eight tokens, -1 for hidden ones
+    unsigned loaded[16];             // which of them have one
     alignas(16) float top[2][2][4][32];   // each warp's maxima of a chunk: of even and odd ones, the last two of each
-    alignas(16) float most[2][32];   // the chunk's
+    alignas(16) float most[kSums][32];   // the chunk's
+    alignas(16) float sum[kSums][4][32]; // each warp's sums of P
     long long first, last;           // the CTA's units
     long long scan[16];
-    int start;                       // sequence of the first unit
+    int start, start_list, start_unit;           // sequence of the first unit, its list, and its place there
     int unit;                        // chunks a unit
-    long long start_units;           // units before it
+    long long start_units, list_unit;            // units before the sequence, and before the list
     long long total[3];
 };
-static_assert(sizeof(Shared) <= 3584, "shared state");
+static_assert(sizeof(Shared) <= 7168, "shared state");
 
 // ---- the key axis
 
@@ -127,35 +130,44 @@ struct Segment {
 // Walks a CTA's run, segment by segment; every role walks it by itself.
 struct Walk {
     const DecodeParams &p;
-    long long at, last, before;      // next unit, the run's end, units before sequence b
-    int b, unit;
-    __device__ Walk(const DecodeParams &p, const Shared &S) : p(p), at(S.first), last(S.last), before(S.start_units), b(S.start), unit(S.unit) {}
+    long long left, unit0;           // units of the run still to come; number of the current list's first unit
+    int b, list, u0, unit, units, tokens;
+    Chunks chunks;
+    __device__ Walk(const DecodeParams &p, const Shared &S)
+        : p(p), left(S.last - S.first), unit0(S.list_unit), b(S.start - 1), list(p.KV * p.parts), u0(S.start_unit), unit(S.unit), units(0), tokens(0), chunks{0, 0, 0}
+    {
+        if (left <= 0) return;
+        sequence();
+        list = S.start_list;
+    }
+    // The next sequence with something to see.
+    __device__ void sequence()
+    {
+        do {
+            tokens = tokens_of(p, ++b);
+            chunks = chunks_of(p, tokens);
+        } while (chunks.n == 0);
+        units = (chunks.n + unit - 1) / unit;
+        list = 0;
+    }
     __device__ bool next(Segment &s)
     {
-        if (at >= last) return false;
-        int n, units;
-        Chunks c;
-        const int lists = p.KV * p.parts;
-        for (;; ++b) {
-            n = tokens_of(p, b);
-            c = chunks_of(p, n);
-            units = (c.n + unit - 1) / unit;
-            if (at < before + static_cast<long long>(units) * lists) break;
-            before += static_cast<long long>(units) * lists;
-        }
-        const long long in = at - before;
-        const int list = static_cast<int>(in / units), u0 = static_cast<int>(in - static_cast<long long>(list) * units);
-        const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + (last - at)));
+        if (left <= 0) return false;
+        if (list == p.KV * p.parts) sequence();
+        const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + left));
         s.b = b;
-        s.kv = list / p.parts;
-        s.part = list % p.parts;
-        s.tokens = n;
-        s.chunks = c;
+        s.kv = p.parts == 1 ? list : list / p.parts;
+        s.part = list - s.kv * p.parts;
+        s.tokens = tokens;
+        s.chunks = chunks;
         s.c0 = u0 * unit;
-        s.c1 = min(u1 * unit, c.n);
-        s.unit0 = at - u0;
+        s.c1 = min(u1 * unit, chunks.n);
+        s.unit0 = unit0;
         s.whole = u0 == 0 && u1 == units;
-        at += u1 - u0;
+        left -= u1 - u0;
+        unit0 += units;
+        u0 = 0;
+        ++list;
         return true;
     }
 };
@@ -222,13 +234,16 @@ __device__ void plan(const DecodeParams &p, Shared &S)
         for (int w = 0; w < kThreads / 32; ++w) carry += S.scan[w];
     }
     __syncthreads();
-    // The cut at the run's begin, for the second launch: the list that it goes through, if it is the first inside.
-    if (blockIdx.x > 0 && thread == 0) {
+    if (thread == 0) {
         Cut cut{0, 0, 0, 0, unit};
         if (first < units) {
             const int n = (chunks_of(p, tokens_of(p, S.start)).n + unit - 1) / unit;
             const long long list = (first - S.start_units) / n, lo = S.start_units + list * n;
-            if (first > lo && units * (blockIdx.x - 1) / gridDim.x <= lo) cut = Cut{lo, n, S.start, static_cast<int>(list), unit};
+            S.start_list = static_cast<int>(list);
+            S.start_unit = static_cast<int>(first - lo);
+            S.list_unit = lo;
+            // The cut at the run's begin, for the second launch: the list that it goes through, if it is the first inside.
+            if (blockIdx.x > 0 && first > lo && units * (blockIdx.x - 1) / gridDim.x <= lo) cut = Cut{lo, n, S.start, static_cast<int>(list), unit};
         }
         p.cuts[blockIdx.x] = cut;
     }
@@ -236,86 +251,125 @@ __device__ void plan(const DecodeParams &p, Shared &S)
 
 // ---- roles
 
-// One warp: queries and tiles. A lane looks up the page of eight tokens; lanes at a box's begin copy it.
+constexpr int kPagesAhead = 8, kLoaded = 16;
+
+// One warp: the page of each eight tokens of a chunk (a lane each), kPagesAhead chunks ahead of the copies.
+__device__ void page_role(const DecodeParams &p, Shared &S, const Waits &wait, int lane)
+{
+    Walk walk(p, S);
+    Segment s;
+    bool bad = false, more = walk.next(s);
+    int c = more ? s.c0 : 0;
+    // Four chunks' look-ups at once: each is a trip to memory that is busy.
+    constexpr int kAtOnce = 4;
+    for (int n = 0; more; n += kAtOnce) {
+        int page[kAtOnce], count = 0;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            page[j] = -2;
+            if (!more) continue;
+            const int token = s.chunks.at(c) * kChunk + lane * 8;
+            if (sees_some(p, s.tokens, token, 8)) page[j] = p.table[s.b * p.ldt + token / p.page_size];
+            ++count;
+            if (++c == s.c1) {
+                more = walk.next(s);
+                c = more ? s.c0 : 0;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (j >= count) break;
+            const int at = n + j;
+            const bool have = page[j] >= 0 && page[j] < p.pages;
+            bad |= page[j] != -2 && !have;
+            const unsigned got = __ballot_sync(kWarp, have);
+            if (!wait.warp(smem_u32(&S.pages_empty[at % kPagesAhead]), ((at / kPagesAhead) & 1) ^ 1)) return;
+            S.page[at % kPagesAhead][lane] = have ? page[j] : -1;
+            // (Read with the scores, when the copies cannot be as far as the chunk kLoaded further on.)
+            if (lane == 0) S.loaded[at % kLoaded] = got;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.pages_full[at % kPagesAhead]));
+        }
+    }
+    if (bad) atomicExch(p.status, kStatusInvalid);
+}
+
+// One warp for the queries and the keys' tiles (kind 0), one for the values' (kind 1): a copy of a page of 16 tokens is 2 KB, and
+// issuing them is work enough for two. A lane is eight tokens (lanes 16-31: their second 64 columns); those at a box's begin
+// copy it.
 template <int DH, int HE>
-__device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared &S, uint32_t base, const Waits &wait, int lane)
+__device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared &S, uint32_t base, const Waits &wait, int kind, int lane)
 {
     using C = Cfg<DH, HE>;
     Walk walk(p, S);
     Segment s;
-    int seq = 0, seg = 0, n = 0, queries = 0;
-    bool ok = !p.force_timeout || wait.warp(smem_u32(&S.never), 0), bad = false;
+    const CUtensorMap *map = kind ? &maps.v : &maps.k;
+    const int g = lane & 15, half = lane >> 4;
     const unsigned in_box = p.box >= 128 ? 0xFFFFu : (1u << (p.box / 8)) - 1u;
-    for (; ok && walk.next(s); ++seg) {
-        const uint32_t qb = smem_u32(&S.q_full[seg & 1]);
-        ok = wait.warp(smem_u32(&S.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1);
-        if (!ok) break;
-        ++queries;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(qb, C::Q_BYTES);
-            for (int h = 0; h < DH / 64; ++h)
-                load_rows(base + C::OFF_Q + (seg & 1) * C::Q_BYTES + h * C::NT * 128, &maps.q, qb, h * 64, s.kv * p.G + s.part * p.heads, s.b);
+    const bool begins_box = ((g * 8) & (p.box - 1)) == 0;
+    const int slots = kind ? C::VALUES : C::KEYS, slot0 = kind ? C::KEYS : 0;
+    int seq = 0, n = 0, queries = 0;
+    unsigned begun = 0, parity = 0;  // slots that this warp has filled, and the phase of the last time
+    bool ok = !p.force_timeout || kind || wait.warp(smem_u32(&S.never), 0);
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+        if (kind == 0) {
+            const uint32_t qb = smem_u32(&S.q_full[seg & 1]);
+            ok = wait.warp(smem_u32(&S.q_empty[seg & 1]), ((seg >> 1) & 1) ^ 1);
+            if (!ok) break;
+            ++queries;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(qb, C::Q_BYTES);
+                for (int h = 0; h < DH / 64; ++h)
+                    load_rows(base + C::OFF_Q + (seg & 1) * C::Q_BYTES + h * C::NT * 128, &maps.q, qb, h * 64, s.kv * p.G + s.part * p.heads, s.b);
+            }
         }
-        for (int c = s.c0; ok && c < s.c1; ++c) {
+        for (int c = s.c0; ok && c < s.c1; ++c, ++n) {
             const int chunk = s.chunks.at(c);
             const unsigned tiles = tiles_of(p, s.tokens, chunk);
-            // Pages of both tiles' tokens, eight a lane.
-            const int token = chunk * kChunk + lane * 8;
-            const bool seen = sees_some(p, s.tokens, token, 8);
-            const int page = seen ? p.table[s.b * p.ldt + token / p.page_size] : -1;
-            const bool have = page >= 0 && page < p.pages;
-            bad |= seen && !have;
-            const unsigned got = __ballot_sync(kWarp, have);
-            const int at = token % p.page_size, pg = have ? page : 0;
-            // (The chunk's values are in the ring until its scores have been read, so the copies are at most a ring, 12
-            // chunks, ahead of that.)
-            if (lane == 0) S.loaded[n & 15] = got;
-            ++n;
-            for (int kind = 0; kind < 2; ++kind)
-                for (int t = 0; t < 2; ++t) {
-                    if (!((tiles >> t) & 1u)) continue;
-                    const int slot = seq % C::SLOTS;
-                    ok = ok && wait.warp(smem_u32(&S.empty[slot]), ((seq / C::SLOTS) & 1) ^ 1);
-                    if (!ok) break;
-                    const uint32_t bar = smem_u32(&S.full[slot]);
-                    const unsigned mine = (got >> (16 * t)) & 0xFFFFu;
-                    // Boxes with a seen token: the first of its groups of eight stands for the box.
-                    const int g = lane & 15;
-                    const bool head = (lane >> 4) == t && ((g * 8) & (p.box - 1)) == 0 && ((mine >> g) & in_box) != 0;
-                    const unsigned boxes = __popc(__ballot_sync(kWarp, head));
-                    if (lane == 0) mbar_arrive_expect_tx(bar, boxes * p.box * (DH / 64) * 128);
-                    __syncwarp();
-                    // The box's page: of any of its groups that are seen (they share it).
-                    const int from = __ffs((mine >> g) & in_box) - 1;
-                    const int box_page = __shfl_sync(kWarp, pg, (16 * t + g + (from < 0 ? 0 : from)) & 31);
-                    if (head) {
-                        for (int h = 0; h < DH / 64; ++h) {
-                            const uint32_t dst = base + slot * C::TILE + h * kTile * 128 + g * 1024;
-                            asm volatile(
-                                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                                " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-                                "l"(reinterpret_cast<uint64_t>(kind ? &maps.v : &maps.k)), "r"(bar), "r"(h * 64), "r"(s.kv), "r"(at), "r"(box_page)
-                                : "memory");
-                        }
-                    }
-                    __syncwarp();
-                    ++seq;
-                }
+            ok = wait.warp(smem_u32(&S.pages_full[n % kPagesAhead]), (n / kPagesAhead) & 1);
+            if (!ok) break;
+            const int page[2] = {S.page[n % kPagesAhead][g], S.page[n % kPagesAhead][16 + g]};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.pages_empty[n % kPagesAhead]));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!((tiles >> t) & 1u)) continue;
+                // Boxes with a token to copy. Its page: of any of its groups (they share it).
+                const unsigned got = __ballot_sync(kWarp, page[t] >= 0) & 0xFFFFu, mine = begins_box ? (got >> g) & in_box : 0;
+                const int box_page = __shfl_sync(kWarp, page[t], mine ? (g + __ffs(mine) - 1) & 15 : g);
+                const unsigned boxes = __popc(__ballot_sync(kWarp, mine != 0) & 0xFFFFu);
+                const int slot = slot0 + seq % slots, token = chunk * kChunk + t * kTile + g * 8;
+                ok = ok && wait.warp(smem_u32(&S.empty[slot]), ((seq / slots) & 1) ^ 1);
+                if (!ok) break;
+                begun |= 1u << slot;
+                parity = (parity & ~(1u << slot)) | ((seq / slots) & 1) << slot;
+                const uint32_t bar = smem_u32(&S.full[slot]);
+                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * p.box * (DH / 64) * 128);
+                __syncwarp();
+                if (mine && half < DH / 64)
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(base + slot * C::TILE + half * kTile * 128 + g * 1024),
+                        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(half * 64), "r"(s.kv), "r"(token % p.page_size), "r"(box_page)
+                        : "memory");
+                __syncwarp();
+                ++seq;
+            }
         }
     }
-    if (bad) atomicExch(p.status, kStatusInvalid);
     if (!ok || *wait.abort_flag) {
+        // Copies in flight are of the last phases that were begun; older ones are over.
         for (int i = max(0, queries - 2); i < queries; ++i) wait.drain(smem_u32(&S.q_full[i & 1]), (i >> 1) & 1);
-        for (int i = max(0, seq - C::SLOTS); i < seq; ++i) wait.drain(smem_u32(&S.full[i % C::SLOTS]), (i / C::SLOTS) & 1);
+        for (int i = 0; i < C::SLOTS; ++i)
+            if ((begun >> i) & 1u) wait.drain(smem_u32(&S.full[i]), (parity >> i) & 1u);
     }
 }
 
-// What the issuer keeps of a chunk whose scores have been made.
+// What the issuer keeps of a chunk whose scores have been made. (Whoever waits for products hands back the tiles that they
+// read: a commit for each would cost the issuing thread about 100 cycles.)
 struct Ahead {
-    int seq;                         // of its first key tile
+    int value;                       // number of its first tile of values
     unsigned tiles;
-    bool last;                       // of its segment
-    int seg;
 };
 
 template <int DH, int HE>
@@ -329,31 +383,31 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
     Walk walk(p, S);
     Segment s;
     bool ok = true, issued = false, more = walk.next(s);
-    int seq = 0, seg = 0, c = more ? s.c0 : 0, n = 0;                  // n: chunks whose scores were issued
-    auto full = [&](int q) {
-        ok = ok && wait.one(smem_u32(&S.full[q % C::SLOTS]), (q / C::SLOTS) & 1);
+    int keys = 0, value = 0, seg = 0, c = more ? s.c0 : 0, n = 0;      // n: chunks whose scores were issued
+    auto full = [&](int slot, int round) {
+        ok = ok && wait.one(smem_u32(&S.full[slot]), round & 1);
         return ok;
     };
     // The scores of the run's next chunk.
     auto scores = [&](Ahead &a) {
         if (c == s.c0) ok = ok && wait.one(smem_u32(&S.q_full[seg & 1]), (seg >> 1) & 1);
-        a = Ahead{seq, tiles_of(p, s.tokens, s.chunks.at(c)), c + 1 == s.c1, seg};
-        int q = seq;
+        a = Ahead{value, tiles_of(p, s.tokens, s.chunks.at(c))};
+        int q = keys;
         for (int t = 0; t < 2; ++t) {
             if (!((a.tiles >> t) & 1u)) continue;
-            if (!full(q)) return;
+            if (!full(q % C::KEYS, q / C::KEYS)) return;
             tc_fence_after();
-            const uint64_t k = sdesc(base + q % C::SLOTS * C::TILE, 16u, 1024u), x = sdesc(base + C::OFF_Q + (seg & 1) * C::Q_BYTES, 16u, 1024u);
+            const uint64_t k = sdesc(base + q % C::KEYS * C::TILE, 16u, 1024u), x = sdesc(base + C::OFF_Q + (seg & 1) * C::Q_BYTES, 16u, 1024u);
             const uint32_t d = tm + C::T_SCORES + ((n & 1) * 2 + t) * NT;
-            for (int i = 0; i < steps; ++i)
-                mma_bf16(d, k + (i >> 2) * (kTile * 128 / 16) + (i & 3) * 2, x + (i >> 2) * (NT * 128 / 16) + (i & 3) * 2, SC, i != 0);
+#pragma unroll
+            for (int i = 0; i < DH / 16; ++i)
+                if (i < steps) mma_bf16(d, k + (i >> 2) * (kTile * 128 / 16) + (i & 3) * 2, x + (i >> 2) * (NT * 128 / 16) + (i & 3) * 2, SC, i != 0);
             issued = true;
             ++q;
         }
         mma_commit(smem_u32(&S.scores[n & 1]));
-        for (int i = seq; i < q; ++i) mma_commit(smem_u32(&S.empty[i % C::SLOTS]));
-        if (a.last) mma_commit(smem_u32(&S.q_empty[seg & 1]));
-        seq = q + (q - seq);         // past its values
+        value += q - keys;
+        keys = q;
         ++n;
         if (++c == s.c1) {
             more = walk.next(s);
@@ -365,26 +419,24 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
     auto values = [&](const Ahead &a, int i) {
         ok = ok && wait.one(smem_u32(&S.probs[i & 1]), (i >> 1) & 1);
         if (!ok) return;
-        const uint32_t d = tm + C::T_CHUNK + (i & 1) * 2 * NT;
-        const int tiles = __popc(a.tiles);
-        int q = a.seq + tiles, first = 1;
+        const uint32_t d = tm + C::T_CHUNK + i % kSums * NT;
+        int q = a.value, first = 1;
         for (int t = 0; t < 2; ++t) {
             if (!((a.tiles >> t) & 1u)) continue;
-            if (!full(q)) return;
+            if (!full(C::KEYS + q % C::VALUES, q / C::VALUES)) return;
             tc_fence_after();
-            const uint64_t v = sdesc(base + q % C::SLOTS * C::TILE, kTile * 128u, 1024u);
+            const uint64_t v = sdesc(base + (C::KEYS + q % C::VALUES) * C::TILE, kTile * 128u, 1024u);
+#pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
                 const int key = t * kTile + k * 16;
                 const uint64_t pr = sdesc(base + C::OFF_P + (i & 1) * C::P_BYTES + (key >> 6) * NT * 128, 16u, 1024u) + ((key >> 4) & 3) * 2;
                 mma_bf16(d, v + k * (2048 / 16), pr, PV, !first);
-                mma_ts(d + NT, tm + C::T_ONES, pr, SC, !first);
                 first = 0;
             }
             issued = true;
             ++q;
         }
-        mma_commit(smem_u32(&S.sums[i & 1]));
-        for (int j = a.seq + tiles; j < q; ++j) mma_commit(smem_u32(&S.empty[j % C::SLOTS]));
+        mma_commit(smem_u32(&S.sums[i % kSums]));
     };
     Ahead cur{}, next{};
     bool have = more;
@@ -450,6 +502,23 @@ __device__ __forceinline__ void fence(uint32_t (&r)[N])
     else reg_fence(r);
 }
 
+// v[0] of lane i: the sum over all lanes of v[i / (32 / N)]. Each step halves the values and doubles the lanes that they are of.
+template <int N>
+__device__ __forceinline__ void sum_lanes(float (&v)[N], int lane)
+{
+#pragma unroll
+    for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+        const bool high = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = high ? v[i] : v[i + n], keep = high ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(kWarp, give, o);
+        }
+    }
+#pragma unroll
+    for (int o = 16 / N; o >= 1; o /= 2) v[0] += __shfl_xor_sync(kWarp, v[0], o);
+}
+
 // One of two warpgroups: the chunks n with n % 2 == group.
 template <int DH, int HE>
 __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, const Waits &wait, int group, int warp, int lane)
@@ -459,23 +528,17 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
     const int row = warp * 32 + lane;                // token of a tile
     const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float c = p.scale * kLog2e;
-    if (group == 0) {
-        uint32_t ones[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ones[i] = 0x3F803F80u;
-        detg::tmem_st8(tm + C::T_ONES, ones);        // (the first P's barrier orders it before its use)
-        tmem_wait_st();
-    }
     Walk walk(p, S);
     Segment s;
     bool ok = true;
-    int n = 0, seq = 0;
-    while (walk.next(s)) {
+    int n = 0, value = 0;
+    for (int seg = 0; walk.next(s); ++seg) {
         for (int ch = s.c0; ch < s.c1; ++ch, ++n) {
             const int chunk = s.chunks.at(ch), token = chunk * kChunk + row;
             const unsigned tiles = tiles_of(p, s.tokens, chunk);
-            const int count = __popc(tiles), keys = seq;
-            seq += 2 * count;
+            int v = value;
+            const int k = value;     // keys' tiles have the values' numbers
+            value += __popc(tiles);
             if ((n & 1) != group) continue;
             const uint32_t phase = (n >> 1) & 1;
             uint32_t x[2][HE];
@@ -483,8 +546,10 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
             float *shared_top = &S.top[group][phase][0][0];
             ok = ok && wait.warp(smem_u32(&S.scores[group]), phase);
             if (ok) {
+                if (warp == 0 && lane < value - k) mbar_arrive(smem_u32(&S.empty[(k + lane) % C::KEYS]));
+                if (warp == 1 && lane == 0 && ch + 1 == s.c1) mbar_arrive(smem_u32(&S.q_empty[seg & 1]));
                 tc_fence_after();
-                const unsigned loaded = S.loaded[n & 15];
+                const unsigned loaded = S.loaded[n % kLoaded];
                 bool seen[2], edge = false;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -509,15 +574,21 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
 #pragma unroll
                     for (int h = 0; h < HE; h += 4) *reinterpret_cast<float4 *>(shared_top + warp * 32 + h) = make_float4(top[h], top[h + 1], top[h + 2], top[h + 3]);
                 }
-                // Values of hidden tokens are whatever was there: zeros, for the product.
+                // The values of the chunk two before have been weighted, and make room for P; the chunk kSums before has been
+                // joined, for the sums.
+                if (n >= 2) ok = ok && wait.warp(smem_u32(&S.sums[(n - 2) % kSums]), ((n - 2) / kSums) & 1);
+                ok = ok && wait.warp(smem_u32(&S.joined[n % kSums]), ((n / kSums) & 1) ^ 1);
+                // Values of hidden tokens are whatever was there: zeros, for the product. What was in these values' slots
+                // before has been used, so that their barriers are in the phase before: it was a chunk's two before or older,
+                // or (a ring of less than two chunks) of the one before, whose sums are awaited.
                 if (edge) {
-                    int v = keys + count;
+                    if (C::VALUES < 4 && n > 0) ok = ok && wait.warp(smem_u32(&S.sums[(n - 1) % kSums]), ((n - 1) / kSums) & 1);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!((tiles >> t) & 1u)) continue;
-                        ok = ok && wait.warp(smem_u32(&S.full[v % C::SLOTS]), (v / C::SLOTS) & 1);
+                        ok = ok && wait.warp(smem_u32(&S.full[C::KEYS + v % C::VALUES]), (v / C::VALUES) & 1);
                         if (ok && !seen[t]) {
-                            const uint32_t at = base + v % C::SLOTS * C::TILE + row * 128;
+                            const uint32_t at = base + (C::KEYS + v % C::VALUES) * C::TILE + row * 128;
 #pragma unroll
                             for (int h = 0; h < DH / 64; ++h)
 #pragma unroll
@@ -527,8 +598,6 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                         ++v;
                     }
                 }
-                // The chunk two before has been joined: its P, its sums and its maxima make room.
-                ok = ok && wait.warp(smem_u32(&S.joined[group]), phase ^ 1u);
             }
             // All four warps leave here together, if one has to: none waits below for another that is gone.
             if (any_of_four(!ok, 1 + group)) return;
@@ -540,7 +609,7 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                     const float4 z = *reinterpret_cast<const float4 *>(shared_top + w * 32 + h);
                     y = make_float4(fmaxf(y.x, z.x), fmaxf(y.y, z.y), fmaxf(y.z, z.z), fmaxf(y.w, z.w));
                 }
-                if (row == 0) *reinterpret_cast<float4 *>(&S.most[group][h]) = y;
+                if (row == 0) *reinterpret_cast<float4 *>(&S.most[n % kSums][h]) = y;
                 top[h] = y.x;
                 top[h + 1] = y.y;
                 top[h + 2] = y.z;
@@ -554,13 +623,21 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                 const uint32_t at = pr + (key >> 6) * NT * 128 + (key & 7) * 2;
 #pragma unroll
                 for (int h = 0; h < HE; ++h) {
-                    const float y = exp2_fast(__uint_as_float(x[t][h]) - (top[h] == -INFINITY ? 0.0f : top[h]));
+                    const uint32_t y = pack_bf16(exp2_fast(__uint_as_float(x[t][h]) - (top[h] == -INFINITY ? 0.0f : top[h])), 0.0f);
+                    x[t][h] = y << 16;
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (h >> 3) * 1024 + (h & 7) * 128 + ((((key >> 3) & 7) ^ (h & 7)) * 16)),
-                                 "h"(static_cast<uint16_t>(pack_bf16(y, 0.0f)))
+                                 "h"(static_cast<uint16_t>(y))
                                  : "memory");
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+            for (int h = 0; h < HE; ++h) {
+                const float a = (tiles & 1u) ? __uint_as_float(x[0][h]) : 0.0f, b = (tiles & 2u) ? __uint_as_float(x[1][h]) : 0.0f;
+                top[h] = a + b;
+            }
+            sum_lanes<HE>(top, lane);
+            if (lane % (32 / HE) == 0) S.sum[n % kSums][warp][lane / (32 / HE)] = top[0];
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.probs[group]));
@@ -578,6 +655,9 @@ __device__ __forceinline__ Factors factors(float ma, float mb)
     return Factors{exp2_fast(ma - off), exp2_fast(mb - off), m};
 }
 __device__ __forceinline__ float join(float a, float b, const Factors &f) { return __fmaf_rn(a, f.a, __fmul_rn(b, f.b)); }
+
+// The output: zero where nothing was seen. (The quotient is off by 2^-22 at most, and rounded to BF16.)
+__device__ __forceinline__ float weighted(float o, float l) { return l == 0.0f ? 0.0f : __fdividef(o, l); }
 
 // Column `row` of the sums of every head, their l and m.
 template <int HE>
@@ -623,30 +703,38 @@ __device__ void join_role(const DecodeParams &p, Shared &S, const Waits &wait, i
     const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     Walk walk(p, S);
     Segment s;
-    int n = 0;
+    int n = 0, value = 0;
     Sums<HE> sums;
     while (walk.next(s)) {
         const int head0 = s.kv * p.G + s.part * p.heads, heads = min(p.heads, p.G - s.part * p.heads);
         for (int ch = s.c0; ch < s.c1; ++ch, ++n) {
-            if (!wait.warp(smem_u32(&S.sums[n & 1]), (n >> 1) & 1)) return;
+            const int at = n % kSums;
+            if (!wait.warp(smem_u32(&S.sums[at]), (n / kSums) & 1)) return;
+            const int count = __popc(tiles_of(p, s.tokens, s.chunks.at(ch)));
+            if (warp == 0 && lane < count) mbar_arrive(smem_u32(&S.empty[C::KEYS + (value + lane) % C::VALUES]));
+            value += count;
             tc_fence_after();
             Sums<HE> x;
-            ld<HE>(tm + C::T_CHUNK + (n & 1) * 2 * NT, x.o);
-            ld<HE>(tm + C::T_CHUNK + (n & 1) * 2 * NT + NT, x.l);
+            ld<HE>(tm + C::T_CHUNK + at * NT, x.o);
 #pragma unroll
             for (int h = 0; h < HE; h += 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(&S.most[n & 1][h]);
+                const float4 y = *reinterpret_cast<const float4 *>(&S.most[at][h]);
                 x.m[h] = __float_as_uint(y.x);
                 x.m[h + 1] = __float_as_uint(y.y);
                 x.m[h + 2] = __float_as_uint(y.z);
                 x.m[h + 3] = __float_as_uint(y.w);
+                const float4 a = *reinterpret_cast<const float4 *>(&S.sum[at][0][h]), b = *reinterpret_cast<const float4 *>(&S.sum[at][1][h]);
+                const float4 c = *reinterpret_cast<const float4 *>(&S.sum[at][2][h]), d = *reinterpret_cast<const float4 *>(&S.sum[at][3][h]);
+                x.l[h] = __float_as_uint((a.x + b.x) + (c.x + d.x));
+                x.l[h + 1] = __float_as_uint((a.y + b.y) + (c.y + d.y));
+                x.l[h + 2] = __float_as_uint((a.z + b.z) + (c.z + d.z));
+                x.l[h + 3] = __float_as_uint((a.w + b.w) + (c.w + d.w));
             }
             tmem_wait_ld();
             fence<HE>(x.o);
-            fence<HE>(x.l);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.joined[n & 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&S.joined[at]));
             const bool end = ch + 1 == s.c1;
             // A unit that is one chunk of a list that others have parts of goes as it is; a block begins with its first.
             if ((unit == 1 && !s.whole) || ch % kBlockChunks == 0) {
@@ -683,25 +771,24 @@ __device__ void join_role(const DecodeParams &p, Shared &S, const Waits &wait, i
             } else if (!end && (ch + 1) % unit != 0) {
                 continue;
             }
-            if (s.whole) {
+            if (s.whole && row < p.D) {
+                uint16_t *out = p.out.row(s.b, head0) + row;
 #pragma unroll
-                for (int h = 0; h < HE; ++h) {
-                    if (h >= heads) break;
-                    const float l = __uint_as_float(sums.l[h]), y = l == 0.0f ? 0.0f : __fdiv_rn(__uint_as_float(sums.o[h]), l);
-                    if (row < p.D) p.out.row(s.b, head0 + h)[row] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
-                }
-            } else {
+                for (int h = 0; h < HE; ++h, out += p.out.h)
+                    if (h < heads) *out = static_cast<uint16_t>(pack_bf16(weighted(__uint_as_float(sums.o[h]), __uint_as_float(sums.l[h])), 0.0f));
+            } else if (row < p.D) {
                 float *part = p.partials + (s.unit0 + ch / unit) * static_cast<long long>(p.heads) * (p.D + 2);
 #pragma unroll
-                for (int h = 0; h < HE; ++h) {
-                    if (h >= heads) break;
-                    if (row < p.D) part[h * p.D + row] = __uint_as_float(sums.o[h]);
-                    if (row == 0) {
-                        part[p.heads * p.D + h] = __uint_as_float(sums.l[h]);
-                        part[p.heads * (p.D + 1) + h] = __uint_as_float(sums.m[h]);
+                for (int h = 0; h < HE; ++h)
+                    if (h < heads) {
+                        part[h * p.D + row] = __uint_as_float(sums.o[h]);
+                        if (row == 0) {
+                            part[p.heads * p.D + h] = __uint_as_float(sums.l[h]);
+                            part[p.heads * (p.D + 1) + h] = __uint_as_float(sums.m[h]);
+                        }
                     }
-                }
             }
+            __syncwarp();
         }
     }
 }
@@ -721,13 +808,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             mbar_init(smem_u32(&S.full[i]), 1);
             mbar_init(smem_u32(&S.empty[i]), 1);
         }
+        for (int i = 0; i < kSums; ++i) {
+            mbar_init(smem_u32(&S.sums[i]), 1);
+            mbar_init(smem_u32(&S.joined[i]), 4);
+        }
+        for (int i = 0; i < kPagesAhead; ++i) {
+            mbar_init(smem_u32(&S.pages_full[i]), 1);
+            mbar_init(smem_u32(&S.pages_empty[i]), 2);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&S.q_full[i]), 1);
             mbar_init(smem_u32(&S.q_empty[i]), 1);
             mbar_init(smem_u32(&S.scores[i]), 1);
             mbar_init(smem_u32(&S.probs[i]), 4);
-            mbar_init(smem_u32(&S.sums[i]), 1);
-            mbar_init(smem_u32(&S.joined[i]), 4);
         }
         mbar_init(smem_u32(&S.drain), 1);
         mbar_init(smem_u32(&S.never), 1);
@@ -757,11 +850,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         join_role<DH, HE>(p, S, wait, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::SERVICE_REGS));
-        if (warp == 12) {
-            copy_role<DH, HE>(p, maps, S, base, wait, lane);
+        if (warp == 12 || warp == 14) {
+            copy_role<DH, HE>(p, maps, S, base, wait, warp == 14, lane);
         } else if (warp == 13) {
             if (elect_one()) issue_role<DH, HE>(p, S, base, wait);
-        } else if (warp == 14) {
+        } else {
+            page_role(p, S, wait, lane);
             for (int b = blockIdx.x; b < p.B; b += gridDim.x)
                 if (tokens_of(p, b) == 0)
                     for (int i = lane * 8; i < p.H * p.D; i += 256) *reinterpret_cast<uint4 *>(p.out.row(b, i / p.D) + i % p.D) = make_uint4(0, 0, 0, 0);
@@ -843,7 +937,7 @@ __global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const Deco
         __syncthreads();
     }
     if (group == 0 && d < p.D) {
-        const float y = all.l == 0.0f ? 0.0f : __fdiv_rn(all.o, all.l);
+        const float y = weighted(all.o, all.l);
         p.out.row(cut.b, kv * p.G + part * p.heads + h)[d] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
     }
 }

@@ -157,7 +157,7 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
         return ok;
     };
     auto scores = [&](int t, uint32_t k) {
-        mma_scores(tm + t * kTile, base + t * C::TILE, ring + k * C::TILE, steps);
+        mma_scores<DH>(tm + t * kTile, base + t * C::TILE, ring + k * C::TILE, steps);
         mma_commit(smem_u32(&S.scores[t]));
         issued = true;
     };
