@@ -49,6 +49,10 @@ struct Cfg {
     static constexpr int TILE = kTile * DH * 2;
     // Tiles of keys and of values in rings of their own: keys leave with their scores, values a chunk's softmax later.
     static constexpr int KEYS = (NT == 16 ? 3 : 2) * (DH == 128 ? 1 : 2), VALUES = 3 * (DH == 128 ? 1 : 2), SLOTS = KEYS + VALUES;
+    // A tile that its products have read goes back to the copies by a commit, at once, or (which spares the issuing thread
+    // about 100 cycles each) by those who wait for the products. Tiles of 64 columns are half as long a wait, in twice as many
+    // slots.
+    static constexpr bool COMMIT = DH == 128;
     static constexpr int Q_BYTES = NT * DH * 2, P_BYTES = NT * kChunk * 2;
     // The ring is followed by more than the 16 KB that a tile of 64 columns' product reads past its end (128 lanes, of which
     // 64 are used).
@@ -365,8 +369,7 @@ __device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared 
     }
 }
 
-// What the issuer keeps of a chunk whose scores have been made. (Whoever waits for products hands back the tiles that they
-// read: a commit for each would cost the issuing thread about 100 cycles.)
+// What the issuer keeps of a chunk whose scores have been made. 
 struct Ahead {
     int value;                       // number of its first tile of values
     unsigned tiles;
@@ -406,6 +409,7 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
             ++q;
         }
         mma_commit(smem_u32(&S.scores[n & 1]));
+        for (int i = keys; C::COMMIT && i < q; ++i) mma_commit(smem_u32(&S.empty[i % C::KEYS]));
         value += q - keys;
         keys = q;
         ++n;
@@ -437,6 +441,7 @@ __device__ void issue_role(const DecodeParams &p, Shared &S, uint32_t base, cons
             ++q;
         }
         mma_commit(smem_u32(&S.sums[i % kSums]));
+        for (int j = a.value; C::COMMIT && j < q; ++j) mma_commit(smem_u32(&S.empty[C::KEYS + j % C::VALUES]));
     };
     Ahead cur{}, next{};
     bool have = more;
@@ -546,7 +551,7 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
             float *shared_top = &S.top[group][phase][0][0];
             ok = ok && wait.warp(smem_u32(&S.scores[group]), phase);
             if (ok) {
-                if (warp == 0 && lane < value - k) mbar_arrive(smem_u32(&S.empty[(k + lane) % C::KEYS]));
+                if (!C::COMMIT && warp == 0 && lane < value - k) mbar_arrive(smem_u32(&S.empty[(k + lane) % C::KEYS]));
                 if (warp == 1 && lane == 0 && ch + 1 == s.c1) mbar_arrive(smem_u32(&S.q_empty[seg & 1]));
                 tc_fence_after();
                 const unsigned loaded = S.loaded[n % kLoaded];
@@ -576,7 +581,7 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                 }
                 // The values of the chunk two before have been weighted, and make room for P; the chunk kSums before has been
                 // joined, for the sums.
-                if (n >= 2) ok = ok && wait.warp(smem_u32(&S.sums[(n - 2) % kSums]), ((n - 2) / kSums) & 1);
+                if (kSums > 2 && n >= 2) ok = ok && wait.warp(smem_u32(&S.sums[(n - 2) % kSums]), ((n - 2) / kSums) & 1);
                 ok = ok && wait.warp(smem_u32(&S.joined[n % kSums]), ((n / kSums) & 1) ^ 1);
                 // Values of hidden tokens are whatever was there: zeros, for the product. What was in these values' slots
                 // before has been used, so that their barriers are in the phase before: it was a chunk's two before or older,
@@ -711,7 +716,7 @@ __device__ void join_role(const DecodeParams &p, Shared &S, const Waits &wait, i
             const int at = n % kSums;
             if (!wait.warp(smem_u32(&S.sums[at]), (n / kSums) & 1)) return;
             const int count = __popc(tiles_of(p, s.tokens, s.chunks.at(ch)));
-            if (warp == 0 && lane < count) mbar_arrive(smem_u32(&S.empty[C::KEYS + (value + lane) % C::VALUES]));
+            if (!C::COMMIT && warp == 0 && lane < count) mbar_arrive(smem_u32(&S.empty[C::KEYS + (value + lane) % C::VALUES]));
             value += count;
             tc_fence_after();
             Sums<HE> x;
