@@ -367,7 +367,9 @@ det_gemm_status det_attn(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const d
     p.out = on(out, ot, oh);
     p.lse = lse;
     AttnMaps maps;
-    if (!encode(&maps.q, q, T, H, D, qt, qh) || !encode(&maps.k, k, S, KV, D, kt, kh) || !encode(&maps.v, v, S, KV, D, vt, vh)) return no_map();
+    if (!encode(&maps.q, q, T, H, D, qt, qh) || !encode(&maps.k, k, S, KV, D, kt, kh) || !encode(&maps.v, v, S, KV, D, vt, vh) ||
+        !encode(&maps.out, out, T, H, D, ot, oh, 1, 32))
+        return no_map();
     const cudaError_t e = launch_attn(p, maps, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "attention launch");
 }
@@ -413,7 +415,8 @@ det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, 
     p.dv = on(dv, dvt, dvh);
     AttnMaps maps;
     if (!encode(&maps.q, q, T, H, D, qt, qh) || !encode(&maps.k, k, S, KV, D, kt, kh) || !encode(&maps.v, v, S, KV, D, vt, vh) ||
-        !encode(&maps.dout, dout, T, H, D, dot, doh))
+        !encode(&maps.dout, dout, T, H, D, dot, doh) || !encode(&maps.out, dq, T, H, D, dqt, dqh, 1, 32) ||
+        !encode(&maps.dk, dk, S, KV, D, dkt, dkh, 1, 32) || !encode(&maps.dv, dv, S, KV, D, dvt, dvh, 1, 32))
         return no_map();
     const cudaError_t e = launch_attn_bwd(p, maps, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "attention gradient launch");

@@ -21,10 +21,11 @@
 // a function of its own query and keys, and blocks begin at fixed places of
 // the sequence: batch, packing and chunks do not enter.
 //
-// What is masked does not reach the output: masked scores are replaced, and in
-// blocks where some row sees only some keys, values that are not finite are
-// taken out before the product (zero times infinity) and added afterwards to
-// the rows that see them.
+// What is masked does not reach the output: masked scores are replaced. A value
+// that is not finite would (zero times infinity), in blocks where some row sees
+// only some keys; then that row's output is not finite. Such a tile is done a
+// second time, with what is not finite taken out of those values before the
+// product and added to the rows that see it afterwards.
 #include "attn_tile.cuh"
 
 #include <atomic>
@@ -34,7 +35,7 @@ namespace deto {
 namespace {
 
 // The softmax warps keep a row's 128 scores in registers; the third warpgroup hands over what it does not need.
-constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 208, kServiceRegs = 88;
+constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 216, kServiceRegs = 72;
 static_assert(kSoftmaxRegs * 256 + kServiceRegs * 128 <= kLaunchRegs * kThreads, "register split");
 constexpr float kSlack = 8.0f;       // how far (log2) a row's maximum may be above what it is scaled by
 
@@ -44,7 +45,7 @@ struct Cfg {
     static constexpr int SLOTS = DH == 128 ? 5 : 8;  // ring of key and value tiles
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_SHARED = OFF_RING + SLOTS * TILE;
-    static constexpr int SMEM = OFF_SHARED + 384 + 1024;
+    static constexpr int SMEM = OFF_SHARED + 512 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -55,57 +56,69 @@ struct Work {
     int rows[2];                     // queries of each tile
     Positions pos[2];
     Blocks blocks;                   // of both tiles
+    Places at[2];
+    // What is done for the tiles `act` (a bit each): all that see something, or those that have to be done again.
+    __device__ bool used(int i, unsigned act) const { return ((act & 1u) && at[0].sees(i)) || ((act & 2u) && at[1].sees(i)); }
+    // Some row of such a tile sees some keys of the block and not all.
+    __device__ bool partly(int i, unsigned act) const
+    {
+        return ((act & 1u) && at[0].sees(i) && !at[0].whole(i)) || ((act & 2u) && at[1].sees(i) && !at[1].whole(i));
+    }
+    __device__ unsigned seeing() const { return (at[0].last() >= 0 ? 1u : 0u) | (at[1].last() >= 0 ? 2u : 0u); }
 };
 
 struct Shared {
-    uint64_t q_full[2], full[8], empty[8], scores[2], probs[2], sane[2], done[2], drain, never;
+    uint64_t q_full[2], full[8], empty[8], scores[2], probs[2], sane[2], done[2], verdict[2], drain, never;
     uint32_t tmem;
     int abort_flag;
-    int poison;                      // some value of a partly masked block is not finite
+    int again[2];                    // the tile has to be done again
+    int taken;                       // some value has been taken out
     int some;                        // there is something to do
     Work work;
 };
-static_assert(sizeof(Shared) <= 384, "shared state");
+static_assert(sizeof(Shared) <= 512, "shared state");
 
 __device__ __forceinline__ bool find_work(const AttnParams &p, int unit, int slots, Work &w)
 {
+    if (p.qb && p.N == 0) return false;
     w.head = unit % p.H;
     w.kv = w.head / p.G;
-    if (p.qb && p.N == 0) return false;
     int tile;
     const int n = tile_sequence(p.qb, p.N, p.T, 2 * kTile, slots - 1 - unit / p.H, tile);
     w.s = seq_at(p, n);
     const long long row0 = w.s.q0 + 2ll * kTile * tile;
     if (row0 >= w.s.q1) return false;
     w.row0 = static_cast<int>(row0);
-    w.pos[0] = w.pos[1] = Positions{0, -1};
     for (int t = 0; t < 2; ++t) {
         w.rows[t] = max(0, min(kTile, w.s.q1 - w.row0 - t * kTile));
         const int first = w.s.position(w.row0 + t * kTile);
-        if (w.rows[t] > 0) w.pos[t] = Positions{first, first + w.rows[t] - 1};
+        w.pos[t] = w.rows[t] > 0 ? Positions{first, first + w.rows[t] - 1} : Positions{0, -1};
     }
     w.blocks = blocks_of(p, Positions{w.pos[0].lo, max(w.pos[0].hi, w.pos[1].hi)});
+    for (int t = 0; t < 2; ++t) w.at[t] = places_of(p, w.pos[t], w.blocks);
     return true;
-}
-
-// Some row sees some key of the block and not all: its values are looked at before the product.
-__device__ __forceinline__ bool partly(const AttnParams &p, const Work &w, int b)
-{
-    return (sees_any(p, w.pos[0], b) && !sees_all(p, w.pos[0], b)) || (sees_any(p, w.pos[1], b) && !sees_all(p, w.pos[1], b));
 }
 
 // ---- roles
 
+// Waits for both tiles' verdicts; which of them are done again.
+__device__ __forceinline__ unsigned done_again(Shared &S, const Waits &wait)
+{
+    for (int t = 0; t < 2; ++t)
+        if (!wait.one(smem_u32(&S.verdict[t]), 0)) return 0;
+    const volatile int *again = S.again;
+    return (again[0] ? 1u : 0u) | (again[1] ? 2u : 0u);
+}
+
 template <int DH>
 __device__ void copy_role(const AttnParams &p, const AttnMaps &maps, Shared &S, uint32_t base, const Waits &wait)
 {
-    const Work w = S.work;
     using C = Cfg<DH>;
+    const Work w = S.work;
     if (p.force_timeout && !wait.one(smem_u32(&S.never), 0)) return;
-    bool tile[2];
+    const unsigned all = w.seeing();
     for (int t = 0; t < 2; ++t) {
-        tile[t] = w.pos[t].hi >= 0 && w.blocks.n > 0;
-        if (!tile[t]) continue;
+        if (!((all >> t) & 1u)) continue;
         mbar_arrive_expect_tx(smem_u32(&S.q_full[t]), C::TILE);
         load_tile<DH>(base + t * C::TILE, &maps.q, smem_u32(&S.q_full[t]), w.head, w.row0 + t * kTile);
     }
@@ -113,25 +126,29 @@ __device__ void copy_role(const AttnParams &p, const AttnMaps &maps, Shared &S, 
     uint32_t round = 0;
     bool ok = true;
     uint32_t loaded = 0, parity = 0;
-    for (int i = 0; ok && i < 2 * w.blocks.n; ++i) {
-        if (!wait.one(smem_u32(&S.empty[slot]), round ^ 1u)) {
-            ok = false;
-            break;
+    auto pass = [&](unsigned act) {
+        for (int i = 0; ok && i < w.blocks.n; ++i) {
+            if (!w.used(i, act)) continue;
+            for (int kind = 0; kind < 2; ++kind) {
+                ok = wait.one(smem_u32(&S.empty[slot]), round ^ 1u);
+                if (!ok) return;
+                const uint32_t bar = smem_u32(&S.full[slot]);
+                mbar_arrive_expect_tx(bar, C::TILE);
+                load_tile<DH>(base + C::OFF_RING + slot * C::TILE, kind ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i) * kTile);
+                loaded |= 1u << slot;
+                parity = (parity & ~(1u << slot)) | (round << slot);
+                if (++slot == C::SLOTS) {
+                    slot = 0;
+                    round ^= 1u;
+                }
+            }
         }
-        const uint32_t bar = smem_u32(&S.full[slot]);
-        mbar_arrive_expect_tx(bar, C::TILE);
-        load_tile<DH>(base + C::OFF_RING + slot * C::TILE, (i & 1) ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i >> 1) * kTile);
-        loaded |= 1u << slot;
-        parity = (parity & ~(1u << slot)) | (round << slot);
-        if (++slot == C::SLOTS) {
-            slot = 0;
-            round ^= 1u;
-        }
-    }
+    };
+    for (int again = 0; again < 2 && ok; ++again) pass(again ? done_again(S, wait) : all);
     // Nothing may land after the CTA's end; when all went well the last blocks' products have waited for them.
     if (!ok || *wait.abort_flag) {
         for (int t = 0; t < 2; ++t)
-            if (tile[t]) wait.drain(smem_u32(&S.q_full[t]), 0);
+            if ((all >> t) & 1u) wait.drain(smem_u32(&S.q_full[t]), 0);
         for (int i = 0; i < C::SLOTS; ++i)
             if (loaded & (1u << i)) wait.drain(smem_u32(&S.full[i]), (parity >> i) & 1u);
     }
@@ -140,13 +157,13 @@ __device__ void copy_role(const AttnParams &p, const AttnMaps &maps, Shared &S, 
 template <int DH>
 __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const Waits &wait)
 {
-    const Work w = S.work;
     using C = Cfg<DH>;
+    const Work w = S.work;
     const uint32_t ring = base + C::OFF_RING, tm = S.tmem;
     const int steps = (p.D + 15) / 16, n = steps * 16;
     int slot = 0;                    // of the next tile in the ring
     uint32_t round = 0, probs = 0, sane = 0;     // phases (a bit a tile)
-    bool ok = true, issued = false, begun[2] = {false, false};
+    bool ok = true, issued = false;
     auto arrive_tile = [&](uint32_t &at) {       // waits for the next tile of the ring
         at = slot;
         ok = ok && wait.one(smem_u32(&S.full[slot]), round);
@@ -156,73 +173,73 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
         }
         return ok;
     };
+    unsigned begun = 0;
     auto scores = [&](int t, uint32_t k) {
+        if (!((begun >> t) & 1u)) {
+            ok = ok && wait.one(smem_u32(&S.q_full[t]), 0);
+            begun |= 1u << t;
+        }
+        if (!ok) return;
+        tc_fence_after();
         mma_scores<DH>(tm + t * kTile, base + t * C::TILE, ring + k * C::TILE, steps);
         mma_commit(smem_u32(&S.scores[t]));
         issued = true;
     };
-    uint32_t k = 0, v = 0;
-    if (w.blocks.n > 0 && arrive_tile(k)) {
-        for (int t = 0; ok && t < 2; ++t) {
-            if (!sees_any(p, w.pos[t], w.blocks.at(0))) continue;
-            ok = wait.one(smem_u32(&S.q_full[t]), 0);
-            if (!ok) break;
-            tc_fence_after();
-            begun[t] = true;
-            scores(t, k);
-        }
-        if (ok) mma_commit(smem_u32(&S.empty[k]));
-    }
-    bool out[2] = {false, false};                // the output has been written
-    for (int i = 0; ok && i < w.blocks.n; ++i) {
-        const int b = w.blocks.at(i), next = i + 1 < w.blocks.n ? w.blocks.at(i + 1) : -1;
-        const bool both = sees_any(p, w.pos[0], b) && sees_any(p, w.pos[1], b);
-        const bool edge = partly(p, w, b);
-        if (!arrive_tile(v)) break;
-        bool have_next = false;
-        for (int t = 0; t < 2; ++t) {
-            if (sees_any(p, w.pos[t], b)) {
-                if (!wait.one(smem_u32(&S.probs[t]), (probs >> t) & 1u)) { ok = false; break; }
-                probs ^= 1u << t;
-                if (both && edge) {              // the other tile's threads have looked at their part of the values
-                    if (!wait.one(smem_u32(&S.sane[1 - t]), (sane >> (1 - t)) & 1u)) { ok = false; break; }
-                    sane ^= 1u << (1 - t);
+    auto pass = [&](unsigned act, bool safe) {
+        const bool on[2] = {(act & 1u) != 0, (act & 2u) != 0};
+        const int last[2] = {on[0] ? w.at[0].last() : -1, on[1] ? w.at[1].last() : -1};
+        bool out[2] = {false, false};            // the output has been written
+        uint32_t k = 0, v = 0;
+        int i = 0;
+        while (i < w.blocks.n && !w.used(i, act)) ++i;
+        if (i == w.blocks.n || !arrive_tile(k)) return;
+        for (int t = 0; t < 2; ++t)
+            if (on[t] && w.at[t].sees(i)) scores(t, k);
+        if (!ok) return;
+        mma_commit(smem_u32(&S.empty[k]));
+        while (i < w.blocks.n) {
+            int next = i + 1;
+            while (next < w.blocks.n && !w.used(next, act)) ++next;
+            const bool more = next < w.blocks.n;
+            const bool check = safe && on[0] && on[1] && w.at[0].sees(i) && w.at[1].sees(i) && w.partly(i, act);
+            if (!arrive_tile(v)) return;
+            bool have_next = false;
+            for (int t = 0; t < 2; ++t) {
+                if (!on[t]) continue;
+                if (w.at[t].sees(i)) {
+                    ok = wait.one(smem_u32(&S.probs[t]), (probs >> t) & 1u);
+                    probs ^= 1u << t;
+                    if (ok && check) {           // the other tile's threads have looked at their part of the values
+                        ok = wait.one(smem_u32(&S.sane[1 - t]), (sane >> (1 - t)) & 1u);
+                        sane ^= 1u << (1 - t);
+                    }
+                    if (!ok) return;
+                    tc_fence_after();
+                    mma_rows(tm + 2 * kTile + t * kTile, tm + t * kTile, ring + v * C::TILE, n, out[t]);
+                    out[t] = issued = true;
+                    if (i == last[t]) mma_commit(smem_u32(&S.done[t]));
                 }
-                tc_fence_after();
-                mma_rows(tm + 2 * kTile + t * kTile, tm + t * kTile, ring + v * C::TILE, n, out[t]);
-                out[t] = issued = true;
-            }
-            if (next >= 0 && sees_any(p, w.pos[t], next)) {
-                if (!have_next) {
-                    if (!arrive_tile(k)) break;
+                if (more && w.at[t].sees(next)) {
+                    if (!have_next && !arrive_tile(k)) return;
                     have_next = true;
+                    scores(t, k);
+                    if (!ok) return;
                 }
-                if (!begun[t]) {
-                    if (!wait.one(smem_u32(&S.q_full[t]), 0)) { ok = false; break; }
-                    begun[t] = true;
-                }
-                tc_fence_after();
-                scores(t, k);
             }
+            mma_commit(smem_u32(&S.empty[v]));
+            if (more) mma_commit(smem_u32(&S.empty[k]));
+            i = next;
         }
-        if (!ok) break;
-        mma_commit(smem_u32(&S.empty[v]));
-        if (next >= 0) {
-            if (!have_next && !arrive_tile(k)) break;        // (a block that neither tile sees does not occur)
-            mma_commit(smem_u32(&S.empty[k]));
-        }
-    }
-    if (ok) {
-        mma_commit(smem_u32(&S.done[0]));
-        mma_commit(smem_u32(&S.done[1]));
-    } else if (issued) {
+    };
+    for (int again = 0; again < 2 && ok; ++again) pass(again ? done_again(S, wait) : w.seeing(), again != 0);
+    if ((!ok || *wait.abort_flag) && issued) {
         mma_commit(smem_u32(&S.drain));
         wait.drain(smem_u32(&S.drain), 0);
     }
 }
 
 // Adds the values that make_finite took out to the rows that see them.
-__device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, int t, uint32_t out, int position)
+__device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, unsigned act, int t, uint32_t out, int position)
 {
     for (int c = 0; c < p.D; c += 8) {
         uint32_t o[8];
@@ -231,7 +248,7 @@ __device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, int t
         detg::reg_fence8(o);
         for (int i = 0; i < w.blocks.n; ++i) {
             const int b = w.blocks.at(i);
-            if (!sees_any(p, w.pos[t], b) || !partly(p, w, b)) continue;
+            if (!w.at[t].sees(i) || !w.partly(i, act)) continue;
             for (int j = b * kTile; j < (b + 1) * kTile && j <= position; ++j) {
                 if (!sees(p, position, j)) continue;
                 const uint4 v = *reinterpret_cast<const uint4 *>(p.v.row(w.s.k0 + j, w.kv) + c);
@@ -248,154 +265,177 @@ __device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, int t
 }
 
 template <int DH>
-__device__ void softmax_role(const AttnParams &p, Shared &S, uint32_t base, const Waits &wait, int t, int warp, int lane)
+__device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &S, uint32_t base, const Waits &wait, int t, int warp, int lane)
 {
-    const Work &w = S.work;
     using C = Cfg<DH>;
+    const Work &w = S.work;
     const int row = warp * 32 + lane;                                  // of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t ts = S.tmem + lanes + t * kTile, to = S.tmem + lanes + 2 * kTile + t * kTile;
-    const int position = row < w.rows[t] ? w.pos[t].lo + row : -1;
+    const int rows = w.rows[t], position = w.pos[t].lo + row;          // (of a row past the tile's: never stored)
+    const int warp_lo = w.pos[t].lo + warp * 32, warp_hi = warp_lo + 31;
+    const Places at = w.at[t];
     const float c = p.scale * kLog2e;
     float m = -INFINITY, l = 0.0f;               // m: what the row is scaled by, log2
-    bool ok = true, out = false;
     uint32_t phase = 0;
-    int v_slot = 1;                              // ring slot of block i's values: 2 i + 1
-    for (int i = 0; ok && i < w.blocks.n; ++i, v_slot = (v_slot + 2) % C::SLOTS) {
-        const int b = w.blocks.at(i);
-        if (!sees_any(p, w.pos[t], b)) continue;
-        ok = wait.warp(smem_u32(&S.scores[t]), phase);
-        if (!ok) break;
-        phase ^= 1u;
-        if (partly(p, w, b)) {
-            // The scores wait for every tile of the ring before block i's values, so that their slot's barrier is in the
-            // phase before: slot (2 i + 1) % SLOTS for the ((2 i + 1) / SLOTS)th time.
-            const bool both = sees_any(p, w.pos[1 - t], b);
-            ok = wait.warp(smem_u32(&S.full[v_slot]), ((2 * i + 1) / C::SLOTS) & 1);
-            if (!ok) break;
-            const int live = min(kTile, w.s.keys() - b * kTile);
-            if (make_finite<DH>(base + C::OFF_RING + v_slot * C::TILE, both ? 2 * row + t : row, live)) S.poison = 1;
-            __syncwarp();
-            if (both && lane == 0) mbar_arrive(smem_u32(&S.sane[t]));
-        }
-        tc_fence_after();
-        uint32_t s[4][32];
+    int tile = 0;                                // of the ring, of the next block's keys
+    // All blocks that the tile sees; `safe`: what is not finite is taken out of values that some rows of `act` do not see.
+    auto pass = [&](unsigned act, bool safe) {
+        bool out = false;
+        m = -INFINITY;
+        l = 0.0f;
+        for (int i = 0; i < w.blocks.n; ++i) {
+            if (!at.sees(i)) {
+                if (w.used(i, act)) tile += 2;
+                continue;
+            }
+            const int v_tile = tile + 1;
+            tile += 2;
+            if (!wait.warp(smem_u32(&S.scores[t]), phase)) return false;
+            phase ^= 1u;
+            if (safe && w.partly(i, act)) {
+                // The scores wait for every tile of the ring before these values, so that their slot's barrier is in the phase before.
+                const bool both = act == 3u && w.at[1 - t].sees(i);
+                const int slot = v_tile % C::SLOTS;
+                if (!wait.warp(smem_u32(&S.full[slot]), (v_tile / C::SLOTS) & 1)) return false;
+                const int live = min(kTile, w.s.keys() - w.blocks.at(i) * kTile);
+                if (make_finite<DH>(base + C::OFF_RING + slot * C::TILE, both ? 2 * row + t : row, live)) S.taken = 1;
+                __syncwarp();
+                if (both && lane == 0) mbar_arrive(smem_u32(&S.sane[t]));
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
+            for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) reg_fence(s[x]);
+            unsigned hidden = 0;                 // 32 keys (a bit each) that no row of the warp sees
+            if (!at.whole(i)) {
+                const int a = w.blocks.at(i) * kTile, last = position - a, first = first_seen(p, position, a), sink = p.sinks - a;
+                const int first_lo = first_seen(p, warp_lo, a), first_hi = first_seen(p, warp_hi, a);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int k = 32 * x;
+                    if (k > warp_hi - a || (k + 31 < first_lo && k >= sink)) {
+                        hidden |= 1u << x;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[x][j] = __float_as_uint(-INFINITY);
+                    } else if (k + 31 > warp_lo - a || (k < first_hi && k + 31 >= sink)) {
+                        const uint32_t seen = seen_bits(k, first, last, sink);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(seen & (1u << j))) s[x][j] = __float_as_uint(-INFINITY);
+                    }
+                }
+            }
+            float top[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                top[x] = __uint_as_float(s[x][0]);
+#pragma unroll
+                for (int j = 1; j < 32; ++j) top[x] = fmaxf(top[x], __uint_as_float(s[x][j]));
+            }
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+            const bool grown = mx > m + kSlack;
+            if (__any_sync(kWarp, grown)) {
+                const float old = grown ? (m == -INFINITY ? 0.0f : exp2_fast(m - mx)) : 1.0f;
+                l *= old;
+                if (grown) m = mx;
+                if (out) {
+                    const uint64_t f = pair(old, old);
+#pragma unroll 1
+                    for (int x = 0; x < DH / 32; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * x, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float lo, hi;
+                            unpair(mul2(pair(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])), f), lo, hi);
+                            o[2 * j] = __float_as_uint(lo);
+                            o[2 * j + 1] = __float_as_uint(hi);
+                        }
+                        tmem_st32(to + 32 * x, o);
+                    }
+                }
+            }
+            const float off = m == -INFINITY ? 0.0f : -m;
+            const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+            uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if ((hidden >> x) & 1u) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[x >> 1][16 * (x & 1) + j] = 0u;
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float lo, hi;
+                    unpair(fma2(pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1])), c2, off2), lo, hi);
+                    lo = exp2_fast(lo);
+                    hi = exp2_fast(hi);
+                    sum[j & 3] = add2(sum[j & 3], pair(lo, hi));
+                    s[x >> 1][16 * (x & 1) + j] = pack_bf16(lo, hi);
+                }
+            }
+            tmem_st32(ts, s[0]);
+            tmem_st32(ts + 32, s[1]);
+            float lo, hi;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
+            l += lo + hi;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.probs[t]));
+            out = true;
+        }
+        return true;
+    };
+    const bool some = at.last() >= 0;            // the tile sees something
+    uint32_t o[DH / 32][32];
+    if (!some && lane == 0) mbar_arrive(smem_u32(&S.verdict[t]));
+    unsigned act = w.seeing();
+    for (int again = 0; some; ++again) {
+        if (!pass(act, again != 0) || !wait.warp(smem_u32(&S.done[t]), again)) return;
+        tc_fence_after();
+        if (again && *reinterpret_cast<volatile int *>(&S.taken)) add_taken(p, w, act, t, to, row < rows ? position : -1);
+#pragma unroll
+        for (int x = 0; x < DH / 32; ++x) tmem_ld32(to + 32 * x, o[x]);
         tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) reg_fence(s[x]);
-        if (!sees_all(p, w.pos[t], b)) {
-            const int a = b * kTile, last = position - a;              // keys [.., last] of the block, from `first` on or below `sink`
-            const int first = first_seen(p, position, a), sink = p.sinks - a;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int k = 32 * x + j;
-                    if (k > last || (k < first && k >= sink)) s[x][j] = __float_as_uint(-INFINITY);
-                }
-        }
-        float top[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            top[x] = __uint_as_float(s[x][0]);
-#pragma unroll
-            for (int j = 1; j < 32; ++j) top[x] = fmaxf(top[x], __uint_as_float(s[x][j]));
-        }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-        const bool grown = mx > m + kSlack;
-        if (__any_sync(kWarp, grown)) {
-            const float old = grown ? (m == -INFINITY ? 0.0f : exp2_fast(m - mx)) : 1.0f;
-            l *= old;
-            if (grown) m = mx;
-            if (out) {
-                const uint64_t f = pair(old, old);
-#pragma unroll 1
-                for (int x = 0; x < DH / 32; ++x) {
-                    uint32_t o[32];
-                    tmem_ld32(to + 32 * x, o);
-                    tmem_wait_ld();
-                    reg_fence(o);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float lo, hi;
-                        unpair(mul2(pair(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])), f), lo, hi);
-                        o[2 * j] = __float_as_uint(lo);
-                        o[2 * j + 1] = __float_as_uint(hi);
-                    }
-                    tmem_st32(to + 32 * x, o);
-                }
-            }
-        }
-        const float off = m == -INFINITY ? 0.0f : -m;
-        const uint64_t c2 = pair(c, c), off2 = pair(off, off);
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float lo, hi;
-                unpair(fma2(pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1])), c2, off2), lo, hi);
-                lo = exp2_fast(lo);
-                hi = exp2_fast(hi);
-                sum[j & 3] = add2(sum[j & 3], pair(lo, hi));
-                s[x >> 1][16 * (x & 1) + j] = pack_bf16(lo, hi);
-            }
-        }
-        tmem_st32(ts, s[0]);
-        tmem_st32(ts + 32, s[1]);
-        float lo, hi;
-        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
-        l += lo + hi;
-        tmem_wait_st();
+        for (int x = 0; x < DH / 32; ++x) reg_fence(o[x]);
+        if (again) break;
+        if (__any_sync(kWarp, row < rows && not_finite(o))) S.again[t] = 1;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&S.probs[t]));
-        out = true;
+        if (lane == 0) mbar_arrive(smem_u32(&S.verdict[t]));
+        if (!wait.warp(smem_u32(&S.verdict[t]), 0)) return;
+        if (!*reinterpret_cast<volatile int *>(&S.again[t])) break;
+        // (The other tile's verdict says which blocks come.)
+        if (!wait.warp(smem_u32(&S.verdict[1 - t]), 0)) return;
+        act = 1u << t | (*reinterpret_cast<volatile int *>(&S.again[1 - t]) ? 2u >> t : 0u);
     }
     // ---- the rows' end
-    if (ok) ok = wait.warp(smem_u32(&S.done[t]), 0);
-    if (!ok) return;
-    tc_fence_after();
-    if (out && *reinterpret_cast<volatile int *>(&S.poison)) add_taken(p, w, t, to, position);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const bool seen = l != 0.0f;
+    const float inv = seen ? 1.0f / l : 0.0f;
     // Through the tile's query rows (its own warp's part; the scores are done with them), so that rows leave in whole lines.
     const uint32_t mine = base + t * C::TILE;
-#pragma unroll 1
-    for (int x = 0; x < DH / 32; ++x) {
-        uint32_t o[32];
-        if (out) {
-            tmem_ld32(to + 32 * x, o);
-            tmem_wait_ld();
-            reg_fence(o);
-        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t y[4];
+    for (int chunk = 0; chunk < DH / 8; ++chunk) {
+        uint32_t y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[e] = seen && out ? pack_bf16(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv) : 0u;
-            const int chunk = 4 * x + q;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) * 16)),
-                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                         : "memory");
-        }
-    }
-    __syncwarp();
-    constexpr int CH = DH / 8, RW = 32 / CH;     // 16-byte chunks of a row; rows of one store instruction
-#pragma unroll 4
-    for (int r0 = 0; r0 < 32; r0 += RW) {
-        const int r = warp * 32 + r0 + lane / CH, chunk = lane % CH;
-        uint4 y;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                     : "r"(mine + (chunk >> 3) * (kTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) * 16))
+        for (int e = 0; e < 4; ++e)
+            y[e] = seen ? pack_bf16(__uint_as_float(o[chunk >> 2][8 * (chunk & 3) + 2 * e]) * inv, __uint_as_float(o[chunk >> 2][8 * (chunk & 3) + 2 * e + 1]) * inv) : 0u;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) * 16)),
+                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                      : "memory");
-        if (r < w.rows[t] && chunk * 8 < p.D) *reinterpret_cast<uint4 *>(p.out.row(w.row0 + t * kTile + r, w.head) + chunk * 8) = y;
     }
-    if (row < w.rows[t]) p.lse[static_cast<long long>(w.head) * p.T + w.row0 + t * kTile + row] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const int token = w.row0 + t * kTile;
+    if (row < rows) p.lse[static_cast<long long>(w.head) * p.T + token + row] = seen ? (m + log2f(l)) * kLn2 : -INFINITY;
+    write_rows<DH>(&maps.out, p.out, mine, w.head, token, warp, lane, rows, p.D);
 }
 
 // Rows that no sequence owns, and the report of bad bounds: the two warps without another task.
@@ -429,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.poison = 0;
+        S.again[0] = S.again[1] = S.taken = 0;
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
             mbar_init(smem_u32(&S.empty[i]), 1);
@@ -440,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             mbar_init(smem_u32(&S.probs[t]), 4);
             mbar_init(smem_u32(&S.sane[t]), 4);
             mbar_init(smem_u32(&S.done[t]), 1);
+            mbar_init(smem_u32(&S.verdict[t]), 4);
         }
         mbar_init(smem_u32(&S.drain), 1);
         mbar_init(smem_u32(&S.never), 1);
@@ -467,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const bool some = S.some;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        if (some) softmax_role<DH>(p, S, base, wait, warp >> 2, warp & 3, lane);
+        if (some) softmax_role<DH>(p, maps, S, base, wait, warp >> 2, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kServiceRegs));
         if (some && warp == 8 && elect_one()) copy_role<DH>(p, maps, S, base, wait);

@@ -67,6 +67,47 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
     for (int h = 0; h < DH / 64; ++h) load_rows(dst + h * kTile * 128, map, bar, h * 64, head, token);
 }
 
+// A warp's 32 rows of a tile (its halves 16 KB apart, as copies leave them) to rows [token, + 32) of an array.
+template <int DH>
+__device__ __forceinline__ void store_rows(const CUtensorMap *map, uint32_t src, int head, int token)
+{
+#pragma unroll
+    for (int h = 0; h < DH / 64; ++h)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                     "r"(src + h * kTile * 128), "r"(h * 64), "r"(head), "r"(token)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The thread's stores have read shared memory.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// A warp's 32 rows of a tile, those below `rows`, to an array: at once where all are, one after the other where the sequence ends.
+template <int DH>
+__device__ __forceinline__ void write_rows(const CUtensorMap *map, const Heads &out, uint32_t tile, int head, int token, int warp, int lane, int rows, int D)
+{
+    if (warp * 32 + 32 <= rows) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            store_rows<DH>(map, tile + warp * 32 * 128, head, token + warp * 32);
+            stores_read();
+        }
+        return;
+    }
+    __syncwarp();
+    constexpr int CH = DH / 8, RW = 32 / CH;     // 16-byte chunks of a row; rows of one store instruction
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += RW) {
+        const int r = warp * 32 + r0 + lane / CH, chunk = lane % CH;
+        uint4 y;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                     : "r"(tile + (chunk >> 3) * (kTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) * 16))
+                     : "memory");
+        if (r < rows && chunk * 8 < D) *reinterpret_cast<uint4 *>(out.row(static_cast<long long>(token) + r, head) + chunk * 8) = y;
+    }
+}
+
 // ---- products
 
 // A in TMEM (128 lanes, two BF16 of consecutive contraction elements a column).
@@ -203,6 +244,54 @@ __device__ __forceinline__ bool sees_all(const AttnParams &p, Positions q, int b
 __device__ __forceinline__ int first_seen(const AttnParams &p, int position, int a)
 {
     return static_cast<int>(max(-1ll, static_cast<long long>(position) - p.window + 1 - a));
+}
+
+// Bits [0, n) of 32.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Of 32 keys from k on: those up to `last` and from `first` on, or below `sink`.
+__device__ __forceinline__ uint32_t seen_bits(int k, int first, int last, int sink)
+{
+    return below(last + 1 - k) & (~below(first - k) | below(sink - k));
+}
+
+// The blocks that a tile of queries sees, as places i in a list of blocks: the first ns (of the first keys) and [s, e]; every one of
+// its queries sees all of the first nf, and of [fs, fe).
+struct Places {
+    int ns, s, e, nf, fs, fe;
+    __device__ bool sees(int i) const { return i < ns || (i >= s && i <= e); }
+    __device__ bool whole(int i) const { return i < nf || (i >= fs && i < fe); }
+    // The last of them (-1: none).
+    __device__ int last() const { return e >= s ? e : ns - 1; }
+};
+__device__ __forceinline__ Places places_of(const AttnParams &p, Positions q, const Blocks &b)
+{
+    if (q.hi < 0) return Places{0, 0, -1, 0, 0, 0};
+    Places r;
+    // (Where the list leaves nothing out, place i is block i, and the first keys' blocks may be inside the window's.)
+    r.ns = min((p.sinks + kTile - 1) / kTile, q.hi / kTile + 1);
+    r.s = b.ns + max(0, max(q.lo, 0) - p.window + 1) / kTile - b.w0;
+    r.e = b.ns + q.hi / kTile - b.w0;
+    r.nf = q.lo < 0 ? 0 : min(p.sinks / kTile, (q.lo + 1) / kTile);
+    r.fs = max(b.ns, b.ns + (max(0, q.hi - p.window + 1) + kTile - 1) / kTile - b.w0);
+    r.fe = q.lo < 0 ? 0 : b.ns + (q.lo + 1) / kTile - b.w0;
+    return r;
+}
+
+// Whether some of the numbers is not finite (their products with zero add up to zero otherwise).
+template <int N>
+__device__ __forceinline__ bool not_finite(const uint32_t (&o)[N][32])
+{
+    uint64_t z0 = 0, z1 = 0;
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            z0 = fma2(pair(__uint_as_float(o[x][j]), __uint_as_float(o[x][j + 1])), 0, z0);
+            z1 = fma2(pair(__uint_as_float(o[x][j + 2]), __uint_as_float(o[x][j + 3])), 0, z1);
+        }
+    float lo, hi;
+    unpair(add2(z0, z1), lo, hi);
+    return !(lo + hi == 0.0f);
 }
 
 // ---- tiles of packed rows
