@@ -21,9 +21,11 @@
 //   warp 9           issues the products from one thread
 //   warp 10          second launch: lse and delta of the queries, into shared memory
 //   warp 10, 11      rows that no sequence owns
-// What is masked does not reach the results: masked elements are replaced, and
-// in blocks that are seen in part, rows of the right operands that are not
-// finite are taken out and added to those that see them afterwards.
+// What is masked does not reach the results: masked elements are replaced. Rows
+// of the right operands that are not finite would (zero times infinity), in
+// blocks that are seen in part; then the result is not finite. Such a tile is
+// done a second time, with what is not finite taken out and added to those that
+// see it afterwards.
 #include "attn_tile.cuh"
 
 #include <atomic>
@@ -62,51 +64,20 @@ __device__ __forceinline__ void put16(uint32_t at, const uint32_t (&v)[32])
     detg::tmem_st16(at, w);
 }
 
-// Stores a warp's 32 rows of [128, D] sums in TMEM (times f) as BF16, through shared memory (its rows of a tile's place) in
-// whole lines. Columns of 16-byte chunks [c0, c1) of the row.
-template <int DH>
-__device__ __forceinline__ void store_sums(uint32_t tmem, uint32_t tile, int warp, int lane, int x0, int x1, float f, bool some)
+// A row's sums (times f) as BF16, 32 columns from 32 x on, into a tile's place.
+__device__ __forceinline__ void put_sums(uint32_t tile, int row, int x, const uint32_t (&o)[32], float f)
 {
-    const int row = warp * 32 + lane;
-#pragma unroll 1
-    for (int x = x0; x < x1; ++x) {
-        uint32_t o[32];
-        if (some) {
-            tmem_ld32(tmem + 32 * x, o);
-            tmem_wait_ld();
-            reg_fence(o);
-        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t y[4];
+    for (int q = 0; q < 4; ++q) {
+        uint32_t y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[e] = some ? pack_bf16(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f) : 0u;
-            const int chunk = 4 * x + q;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) * 16)),
-                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                         : "memory");
-        }
-    }
-    __syncwarp();
-}
-// Rows [warp * 32, + 32) below `rows`, `chunks` chunks each from chunk c0 on.
-template <int CH>
-__device__ __forceinline__ void copy_rows_out(const Heads &out, long long token, int head, uint32_t tile, int warp, int lane, int c0, int rows, int D)
-{
-    constexpr int RW = 32 / CH;
-#pragma unroll 4
-    for (int r0 = 0; r0 < 32; r0 += RW) {
-        const int r = warp * 32 + r0 + lane / CH, chunk = c0 + lane % CH;
-        uint4 y;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                     : "r"(tile + (chunk >> 3) * (kTile * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) * 16))
+        for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f);
+        const int chunk = 4 * x + q;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) * 16)),
+                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                      : "memory");
-        if (r < rows && chunk * 8 < D) *reinterpret_cast<uint4 *>(out.row(token + r, head) + chunk * 8) = y;
     }
 }
-
 // Rows of one axis that no sequence owns become zero in the arrays given.
 __device__ void zero_outside(const int32_t *bounds, int N, int limit, int heads, int D, const Heads &a, const Heads *b, int thread, int threads)
 {
@@ -131,7 +102,7 @@ struct QCfg {
     static constexpr int OFF_RING = 2 * TILE;        // query rows and dout's first
     static constexpr int OFF_DELTA = OFF_RING + SLOTS * TILE;       // [2][128] floats
     static constexpr int OFF_SHARED = OFF_DELTA + 1024;
-    static constexpr int SMEM = OFF_SHARED + 384 + 1024;
+    static constexpr int SMEM = OFF_SHARED + 512 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -140,14 +111,15 @@ struct QWork {
     int head, kv, row0, rows;
     Positions pos;
     Blocks blocks;
+    Places at;
 };
 struct QShared {
-    uint64_t q_full, full[8], empty[8], scores[2], dp, read, ds, done, drain, never;
+    uint64_t q_full, full[8], empty[8], scores[2], dp, read, ds, done, verdict, staged, drain, never;
     uint32_t tmem;
-    int abort_flag, poison, some;
+    int abort_flag, taken, again, some;
     QWork work;
 };
-static_assert(sizeof(QShared) <= 384, "shared state");
+static_assert(sizeof(QShared) <= 512, "shared state");
 
 __device__ __forceinline__ bool find_queries(const AttnParams &p, int unit, int slots, QWork &w)
 {
@@ -164,7 +136,15 @@ __device__ __forceinline__ bool find_queries(const AttnParams &p, int unit, int 
     const int first = w.s.position(w.row0);
     w.pos = Positions{first, first + w.rows - 1};
     w.blocks = blocks_of(p, w.pos);
+    w.at = places_of(p, w.pos, w.blocks);
     return true;
+}
+
+// Waits for the verdict: whether the tile is done again.
+template <typename S>
+__device__ __forceinline__ bool done_again(S &shared, const Waits &wait)
+{
+    return wait.one(smem_u32(&shared.verdict), 0) && *reinterpret_cast<volatile int *>(&shared.again) != 0;
 }
 
 template <int DH>
@@ -179,19 +159,20 @@ __device__ void q_copy(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
     int slot = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
     bool ok = true;
-    for (int i = 0; ok && i < 2 * w.blocks.n; ++i) {
-        if (!wait.one(smem_u32(&S.empty[slot]), round ^ 1u)) {
-            ok = false;
-            break;
-        }
-        const uint32_t bar = smem_u32(&S.full[slot]);
-        mbar_arrive_expect_tx(bar, C::TILE);
-        load_tile<DH>(base + C::OFF_RING + slot * C::TILE, (i & 1) ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i >> 1) * kTile);
-        loaded |= 1u << slot;
-        parity = (parity & ~(1u << slot)) | (round << slot);
-        if (++slot == C::SLOTS) {
-            slot = 0;
-            round ^= 1u;
+    for (int again = 0; ok && again < 2; ++again) {
+        if (again && !done_again(S, wait)) break;
+        for (int i = 0; i < 2 * w.blocks.n; ++i) {
+            ok = wait.one(smem_u32(&S.empty[slot]), round ^ 1u);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&S.full[slot]);
+            mbar_arrive_expect_tx(bar, C::TILE);
+            load_tile<DH>(base + C::OFF_RING + slot * C::TILE, (i & 1) ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i >> 1) * kTile);
+            loaded |= 1u << slot;
+            parity = (parity & ~(1u << slot)) | (round << slot);
+            if (++slot == C::SLOTS) {
+                slot = 0;
+                round ^= 1u;
+            }
         }
     }
     if (!ok || *wait.abort_flag) {
@@ -211,6 +192,7 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
     const uint32_t ring = base + C::OFF_RING, tm = S.tmem;
     const int steps = (p.D + 15) / 16, n = w.blocks.n;
     bool ok = n == 0 || wait.one(smem_u32(&S.q_full), 0), issued = false;
+    // Block i of all passes: its keys are tile 2 i of the ring, its values the next.
     auto arrived = [&](int seq) {
         ok = ok && wait.one(smem_u32(&S.full[seq % C::SLOTS]), (seq / C::SLOTS) & 1);
         return ok;
@@ -230,24 +212,27 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
         mma_commit(smem_u32(&S.empty[(2 * i + 1) % C::SLOTS]));
         issued = true;
     };
-    if (ok && n > 0) scores(0);
-    if (ok && n > 0) dp(0);
-    if (ok && n > 1) scores(1);
-    for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {
-            ok = wait.one(smem_u32(&S.read), i & 1);
-            if (ok) dp(i + 1);
+    for (int begin = 0; ok && n > 0 && begin < 2 * n; begin += n) {
+        if (begin && !done_again(S, wait)) break;
+        const int end = begin + n;
+        scores(begin);
+        if (ok) dp(begin);
+        if (ok && n > 1) scores(begin + 1);
+        for (int i = begin; ok && i < end; ++i) {
+            if (i + 1 < end) {
+                ok = wait.one(smem_u32(&S.read), i & 1);
+                if (ok) dp(i + 1);
+            }
+            ok = ok && wait.one(smem_u32(&S.ds), i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            mma_rows(tm + 3 * kTile, tm + (i & 1) * kTile, ring + 2 * i % C::SLOTS * C::TILE, steps * 16, i > begin, kGap);
+            mma_commit(smem_u32(&S.empty[2 * i % C::SLOTS]));
+            if (i + 2 < end) scores(i + 2);
         }
-        ok = ok && wait.one(smem_u32(&S.ds), i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        mma_rows(tm + 3 * kTile, tm + (i & 1) * kTile, ring + 2 * i % C::SLOTS * C::TILE, steps * 16, i > 0, kGap);
-        mma_commit(smem_u32(&S.empty[2 * i % C::SLOTS]));
-        if (i + 2 < n) scores(i + 2);
+        if (ok) mma_commit(smem_u32(&S.done));
     }
-    if (ok) {
-        mma_commit(smem_u32(&S.done));
-    } else if (issued) {
+    if ((!ok || *wait.abort_flag) && issued) {
         mma_commit(smem_u32(&S.drain));
         wait.drain(smem_u32(&S.drain), 0);
     }
@@ -263,7 +248,7 @@ __device__ __noinline__ void q_add_taken(const AttnParams &p, const QWork &w, ui
         detg::reg_fence8(o);
         for (int i = 0; i < w.blocks.n; ++i) {
             const int b = w.blocks.at(i);
-            if (sees_all(p, w.pos, b)) continue;
+            if (w.at.whole(i)) continue;
             for (int j = b * kTile; j < (b + 1) * kTile && j <= position; ++j) {
                 if (!sees(p, position, j)) continue;
                 float f[8];
@@ -279,7 +264,7 @@ __device__ __noinline__ void q_add_taken(const AttnParams &p, const QWork &w, ui
 }
 
 template <int DH>
-__device__ void q_math(const AttnParams &p, QShared &S, uint32_t base, const Waits &wait, int half, int warp, int lane)
+__device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, uint32_t base, const Waits &wait, int half, int warp, int lane)
 {
     using C = QCfg<DH>;
     const QWork &w = S.work;
@@ -287,7 +272,7 @@ __device__ void q_math(const AttnParams &p, QShared &S, uint32_t base, const Wai
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tm = S.tmem + lanes;
     const bool live = row < w.rows;
-    const int position = live ? w.pos.lo + row : -1;
+    const int position = w.pos.lo + row;             // (of a row past the tile's: never stored)
     const long long at = static_cast<long long>(w.head) * p.T + w.row0 + row;
     // delta: a half of the row's columns each, joined in shared memory, the first half first.
     float part = 0.0f;
@@ -315,84 +300,111 @@ __device__ void q_math(const AttnParams &p, QShared &S, uint32_t base, const Wai
     }
     float *deltas = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&S) - 1024);
     deltas[half * kTile + row] = part;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    asm volatile("bar.sync 1, 256;" ::: "memory");               // (before any wait: nobody has left)
     const float delta = deltas[row] + deltas[kTile + row];
     const float lse = live ? p.lse[at] : 0.0f;
     if (live && half == 0) p.delta[at] = delta;
     const float c = p.scale * kLog2e, off = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
     const uint64_t c2 = pair(c, c), l2 = pair(off, off), d2 = pair(-delta, -delta);
-    bool ok = true;
+    const Places places = w.at;
     const int n = w.blocks.n;
-    for (int i = 0; i < n; ++i) {
-        const int b = w.blocks.at(i);
-        const bool full = sees_all(p, w.pos, b);
-        const uint32_t ts = tm + (i & 1) * kTile + half * 64;
-        ok = wait.warp(smem_u32(&S.scores[i & 1]), (i >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[2][32];
-        tmem_ld32(ts, s[0]);
-        tmem_ld32(ts + 32, s[1]);
-        tmem_wait_ld();
-        reg_fence(s[0]);
-        reg_fence(s[1]);
-        exp_block(s[0], c2, l2);
-        exp_block(s[1], c2, l2);
-        const int a = b * kTile + half * 64, last = position - a, first = first_seen(p, position, a), sink = p.sinks - a;
-        if (!full) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (k > last || (k < first && k >= sink)) s[k >> 5][k & 31] = 0u;
-        }
-        ok = wait.warp(smem_u32(&S.dp), i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (!full) {
-            // Both score matrices of the block have been made: its keys may be changed for the last product. The other
-            // half's threads wait for the same, and dq for both.
-            const int r = half * 64 + (row & 63);
-            if (row < 64 && make_finite<DH>(base + C::OFF_RING + 2 * i % C::SLOTS * C::TILE, r, min(kTile, w.s.keys() - b * kTile))) S.poison = 1;
-            __syncwarp();
-        }
-        uint32_t d[2][32];
-        tmem_ld32(tm + 2 * kTile + half * 64, d[0]);
-        tmem_ld32(tm + 2 * kTile + half * 64 + 32, d[1]);
-        tmem_wait_ld();
-        reg_fence(d[0]);
-        reg_fence(d[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&S.read));
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float lo, hi;
-                unpair(mul2(add2(pair(__uint_as_float(d[x][2 * j]), __uint_as_float(d[x][2 * j + 1])), d2),
-                            pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1]))), lo, hi);
-                d[x][2 * j] = __float_as_uint(lo);
-                d[x][2 * j + 1] = __float_as_uint(hi);
-            }
-        if (!full) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (k > last || (k < first && k >= sink)) d[k >> 5][k & 31] = 0u;
-        }
-        put16(ts, d[0]);
-        put16(ts + 16, d[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&S.ds));
-    }
-    if (ok) ok = wait.warp(smem_u32(&S.done), 0);
-    if (!ok) return;
-    tc_fence_after();
     const uint32_t out = tm + 3 * kTile;
-    if (n > 0 && *reinterpret_cast<volatile int *>(&S.poison)) q_add_taken(p, w, out, position, half * (DH / 2), (half + 1) * (DH / 2));
-    // Half of the columns each, through the query tile's place.
-    store_sums<DH>(out, base, warp, lane, half * (DH / 64), (half + 1) * (DH / 64), p.scale, n > 0);
-    copy_rows_out<DH / 16>(p.dq, w.row0, w.head, base, warp, lane, half * (DH / 16), w.rows, p.D);
+    uint32_t o[DH / 64][32];
+    int j = 0;                       // blocks of all passes
+    for (int again = 0; n > 0; ++again) {
+        for (int i = 0; i < n; ++i, ++j) {
+            const bool full = places.whole(i);
+            const uint32_t ts = tm + (j & 1) * kTile + half * 64;
+            if (!wait.warp(smem_u32(&S.scores[j & 1]), (j >> 1) & 1)) return;
+            tc_fence_after();
+            uint32_t s[2][32];
+            tmem_ld32(ts, s[0]);
+            tmem_ld32(ts + 32, s[1]);
+            tmem_wait_ld();
+            reg_fence(s[0]);
+            reg_fence(s[1]);
+            uint32_t seen[2] = {~0u, ~0u};
+            if (!full) {
+                const int a = w.blocks.at(i) * kTile + half * 64, first = first_seen(p, position, a), sink = p.sinks - a;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) seen[x] = seen_bits(32 * x, first, position - a, sink);
+            }
+            exp_block(s[0], c2, l2);
+            exp_block(s[1], c2, l2);
+            if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
+            tc_fence_after();
+            if (again && !full) {
+                // Both score matrices of the block have been made: its keys may be changed for the last product. The other
+                // half's threads wait for the same, and dq for both.
+                const int keys = w.s.keys() - w.blocks.at(i) * kTile;
+                if (row < 64 && make_finite<DH>(base + C::OFF_RING + 2 * j % C::SLOTS * C::TILE, half * 64 + row, min(kTile, keys))) S.taken = 1;
+                __syncwarp();
+            }
+            uint32_t d[2][32];
+            tmem_ld32(tm + 2 * kTile + half * 64, d[0]);
+            tmem_ld32(tm + 2 * kTile + half * 64 + 32, d[1]);
+            tmem_wait_ld();
+            reg_fence(d[0]);
+            reg_fence(d[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.read));
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float lo, hi;
+                    unpair(mul2(add2(pair(__uint_as_float(d[x][2 * k]), __uint_as_float(d[x][2 * k + 1])), d2),
+                                pair(__uint_as_float(s[x][2 * k]), __uint_as_float(s[x][2 * k + 1]))), lo, hi);
+                    d[x][2 * k] = __float_as_uint(lo);
+                    d[x][2 * k + 1] = __float_as_uint(hi);
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (__any_sync(kWarp, seen[x] != ~0u)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(seen[x] & (1u << k))) d[x][k] = 0u;
+                }
+            put16(ts, d[0]);
+            put16(ts + 16, d[1]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.ds));
+        }
+        if (!wait.warp(smem_u32(&S.done), again)) return;
+        tc_fence_after();
+        if (again && *reinterpret_cast<volatile int *>(&S.taken)) q_add_taken(p, w, out, live ? position : -1, half * (DH / 2), (half + 1) * (DH / 2));
+#pragma unroll
+        for (int x = 0; x < DH / 64; ++x) tmem_ld32(out + half * (DH / 2) + 32 * x, o[x]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < DH / 64; ++x) reg_fence(o[x]);
+        if (again) break;
+        if (__any_sync(kWarp, live && not_finite(o))) S.again = 1;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.verdict));
+        if (!wait.warp(smem_u32(&S.verdict), 0)) return;
+        if (!*reinterpret_cast<volatile int *>(&S.again)) break;
+    }
+    // Half of the columns each, through the query tile's place; a warp's rows leave when both halves are there.
+    if (n == 0) {
+#pragma unroll
+        for (int x = 0; x < DH / 64; ++x)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[x][k] = 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < DH / 64; ++x) put_sums(base, row, half * (DH / 64) + x, o[x], p.scale);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (half) {
+        if (lane == 0) mbar_arrive(smem_u32(&S.staged));
+    } else if (wait.warp(smem_u32(&S.staged), 0)) {
+        write_rows<DH>(&maps.out, p.dq, base, w.head, w.row0, warp, lane, w.rows, p.D);
+    }
 }
 
 template <int DH>
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.poison = 0;
+        S.again = S.taken = 0;
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
             mbar_init(smem_u32(&S.empty[i]), 1);
@@ -417,6 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         mbar_init(smem_u32(&S.read), 8);
         mbar_init(smem_u32(&S.ds), 8);
         mbar_init(smem_u32(&S.done), 1);
+        mbar_init(smem_u32(&S.verdict), 8);
+        mbar_init(smem_u32(&S.staged), 4);
         mbar_init(smem_u32(&S.drain), 1);
         mbar_init(smem_u32(&S.never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     const bool some = S.some;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
-        if (some) q_math<DH>(p, S, base, wait, warp >> 2, warp & 3, lane);
+        if (some) q_math<DH>(p, maps, S, base, wait, warp >> 2, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kServiceRegs));
         if (some && warp == 8 && elect_one()) q_copy<DH>(p, maps, S, base, wait);
@@ -469,7 +483,7 @@ struct KCfg {
     static constexpr int OFF_D = OFF_Q + STAGES * TILE;
     static constexpr int OFF_VEC = OFF_D + STAGES * TILE;           // [STAGES][2][128] floats: -lse log2(e), -delta
     static constexpr int OFF_SHARED = OFF_VEC + STAGES * 1024;
-    static constexpr int SMEM = OFF_SHARED + 384 + 1024;
+    static constexpr int SMEM = OFF_SHARED + 512 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -477,14 +491,15 @@ struct KWork {
     Seq s;
     int kv, key0, rows;              // first key's place in the sequence; keys of the tile
     int first, n;                    // first block of 128 queries; iterations: blocks times heads
+    int f0, f1;                      // the blocks of which every query sees every key of the tile
 };
 struct KShared {
-    uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, drain, never;
+    uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, verdict, drain, never;
     uint32_t tmem;
-    int abort_flag, poison, some;
+    int abort_flag, taken, again, some;
     KWork work;
 };
-static_assert(sizeof(KShared) <= 384, "shared state");
+static_assert(sizeof(KShared) <= 512, "shared state");
 
 // The queries [lo, hi] of the sequence that see some of the tile's keys.
 __device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, KWork &w)
@@ -504,13 +519,12 @@ __device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, KWork &
     if (w.key0 >= p.sinks) hi = min(hi, static_cast<long long>(w.key0) + w.rows - 1 + p.window - 1 - shift);
     w.first = static_cast<int>(lo / kTile);
     w.n = hi >= lo ? static_cast<int>(hi / kTile - lo / kTile + 1) * p.G : 0;
+    const long long f0 = max(0ll, static_cast<long long>(w.key0) + kTile - 1 - shift);
+    long long f1 = w.s.queries();    // whole blocks that begin before
+    if (w.key0 + kTile - 1 >= p.sinks) f1 = min(f1, static_cast<long long>(w.key0) - shift + p.window);
+    w.f0 = static_cast<int>((f0 + kTile - 1) / kTile);
+    w.f1 = w.rows == kTile ? static_cast<int>(max(0ll, f1) / kTile) : 0;
     return true;
-}
-// Every query of block qb sees every key of the tile.
-__device__ __forceinline__ bool seen_by_all(const AttnParams &p, const KWork &w, int qb)
-{
-    const int r = qb * kTile, pos = r + w.s.keys() - w.s.queries();
-    return pos >= w.key0 + kTile - 1 && r + kTile <= w.s.queries() && (pos + kTile - 1 - w.key0 < p.window || w.key0 + kTile - 1 < p.sinks);
 }
 
 template <int DH>
@@ -524,18 +538,26 @@ __device__ void k_copy(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
     load_tile<DH>(base + C::TILE, &maps.v, smem_u32(&S.kv_full), w.kv, w.s.k0 + w.key0);
     int q_last[2] = {-1, -1}, d_last[2] = {-1, -1};                  // parity of each stage's last load
     bool ok = true;
-    for (int i = 0; i < w.n; ++i) {
-        const int st = i & 1, phase = (i >> 1) & 1, row = w.s.q0 + (w.first + i / p.G) * kTile, head = w.kv * p.G + i % p.G;
-        ok = wait.one(smem_u32(&S.q_empty[st]), phase ^ 1);
-        if (!ok) break;
-        mbar_arrive_expect_tx(smem_u32(&S.q_full[st]), C::TILE);
-        load_tile<DH>(base + C::OFF_Q + st * C::TILE, &maps.q, smem_u32(&S.q_full[st]), head, row);
-        q_last[st] = phase;
-        ok = wait.one(smem_u32(&S.d_empty[st]), phase ^ 1);
-        if (!ok) break;
-        mbar_arrive_expect_tx(smem_u32(&S.d_full[st]), C::TILE);
-        load_tile<DH>(base + C::OFF_D + st * C::TILE, &maps.dout, smem_u32(&S.d_full[st]), head, row);
-        d_last[st] = phase;
+    for (int again = 0, j = 0; ok && again < 2; ++again) {
+        if (again && !done_again(S, wait)) break;
+        int row = w.s.q0 + w.first * kTile, h = 0;
+        for (int i = 0; i < w.n; ++i, ++j) {
+            const int st = j & 1, phase = (j >> 1) & 1, head = w.kv * p.G + h;
+            ok = wait.one(smem_u32(&S.q_empty[st]), phase ^ 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(smem_u32(&S.q_full[st]), C::TILE);
+            load_tile<DH>(base + C::OFF_Q + st * C::TILE, &maps.q, smem_u32(&S.q_full[st]), head, row);
+            q_last[st] = phase;
+            ok = wait.one(smem_u32(&S.d_empty[st]), phase ^ 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(smem_u32(&S.d_full[st]), C::TILE);
+            load_tile<DH>(base + C::OFF_D + st * C::TILE, &maps.dout, smem_u32(&S.d_full[st]), head, row);
+            d_last[st] = phase;
+            if (++h == p.G) {
+                h = 0;
+                row += kTile;
+            }
+        }
     }
     if (!ok || *wait.abort_flag) {
         wait.drain(smem_u32(&S.kv_full), 0);
@@ -551,27 +573,35 @@ template <int DH>
 __device__ void k_vectors(const AttnParams &p, KShared &S, uint8_t *smem, const Waits &wait, int lane)
 {
     using C = KCfg<DH>;
-    const KWork &w = S.work;
-    for (int i = 0; i < w.n; ++i) {
-        const int st = i & 1, r0 = (w.first + i / p.G) * kTile;
-        const long long at = static_cast<long long>(w.kv * p.G + i % p.G) * p.T + w.s.q0 + r0;
-        float l[4], d[4];
+    const KWork w = S.work;
+    for (int again = 0, j = 0; again < 2; ++again) {
+        if (again && (w.n == 0 || !__all_sync(kWarp, done_again(S, wait)))) return;
+        int r0 = w.first * kTile, h = 0;
+        for (int i = 0; i < w.n; ++i, ++j) {
+            const int st = j & 1;
+            const long long at = static_cast<long long>(w.kv * p.G + h) * p.T + w.s.q0 + r0;
+            float l[4], d[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = lane + 32 * e;
-            const bool live = r0 + r < w.s.queries();
-            l[e] = live ? p.lse[at + r] : 0.0f;
-            d[e] = live ? p.delta[at + r] : 0.0f;
-        }
-        if (!wait.warp(smem_u32(&S.v_empty[st]), ((i >> 1) & 1) ^ 1)) return;
-        float *v = reinterpret_cast<float *>(smem + C::OFF_VEC + st * 1024);
+            for (int e = 0; e < 4; ++e) {
+                const int r = lane + 32 * e;
+                const bool live = r0 + r < w.s.queries();
+                l[e] = live ? p.lse[at + r] : 0.0f;
+                d[e] = live ? p.delta[at + r] : 0.0f;
+            }
+            if (!wait.warp(smem_u32(&S.v_empty[st]), ((j >> 1) & 1) ^ 1)) return;
+            float *v = reinterpret_cast<float *>(smem + C::OFF_VEC + st * 1024);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[lane + 32 * e] = l[e] == -INFINITY ? -INFINITY : -l[e] * kLog2e;
-            v[kTile + lane + 32 * e] = -d[e];
+            for (int e = 0; e < 4; ++e) {
+                v[lane + 32 * e] = l[e] == -INFINITY ? -INFINITY : -l[e] * kLog2e;
+                v[kTile + lane + 32 * e] = -d[e];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.v_full[st]));
+            if (++h == p.G) {
+                h = 0;
+                r0 += kTile;
+            }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&S.v_full[st]));
     }
 }
 
@@ -601,25 +631,28 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
         mma_commit(smem_u32(&S.dp));
         issued = true;
     };
-    if (w.n > 0) scores(0);
-    if (w.n > 0) dp(0);
-    for (int i = 0; ok && i < w.n; ++i) {
-        ok = wait.one(smem_u32(&S.probs), i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        mma_rows(tm + 2 * kTile, tm, base + C::OFF_D + (i & 1) * C::TILE, steps * 16, i > 0, kGap);
-        mma_commit(smem_u32(&S.d_empty[i & 1]));
-        if (i + 1 < w.n) scores(i + 1);
-        ok = ok && wait.one(smem_u32(&S.ds), i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        mma_rows(tm + 3 * kTile, tm + kTile, base + C::OFF_Q + (i & 1) * C::TILE, steps * 16, i > 0, kGap);
-        mma_commit(smem_u32(&S.q_empty[i & 1]));
-        if (i + 1 < w.n) dp(i + 1);
+    for (int begin = 0; ok && w.n > 0 && begin < 2 * w.n; begin += w.n) {
+        if (begin && !done_again(S, wait)) break;
+        const int end = begin + w.n;
+        scores(begin);
+        if (ok) dp(begin);
+        for (int i = begin; ok && i < end; ++i) {
+            ok = wait.one(smem_u32(&S.probs), i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            mma_rows(tm + 2 * kTile, tm, base + C::OFF_D + (i & 1) * C::TILE, steps * 16, i > begin, kGap);
+            mma_commit(smem_u32(&S.d_empty[i & 1]));
+            if (i + 1 < end) scores(i + 1);
+            ok = ok && wait.one(smem_u32(&S.ds), i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            mma_rows(tm + 3 * kTile, tm + kTile, base + C::OFF_Q + (i & 1) * C::TILE, steps * 16, i > begin, kGap);
+            mma_commit(smem_u32(&S.q_empty[i & 1]));
+            if (i + 1 < end) dp(i + 1);
+        }
+        if (ok) mma_commit(smem_u32(&S.done));
     }
-    if (ok) {
-        mma_commit(smem_u32(&S.done));
-    } else if (issued) {
+    if ((!ok || *wait.abort_flag) && issued) {
         mma_commit(smem_u32(&S.drain));
         wait.drain(smem_u32(&S.drain), 0);
     }
@@ -635,7 +668,7 @@ __device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, co
         detg::reg_fence8(o);
         for (int i = 0; i < w.n && key >= 0; ++i) {
             const int qb = w.first + i / p.G;
-            if (seen_by_all(p, w, qb)) continue;
+            if (qb >= w.f0 && qb < w.f1) continue;
             for (int r = qb * kTile; r < min((qb + 1) * kTile, w.s.queries()); ++r) {
                 if (!sees(p, r + w.s.keys() - w.s.queries(), key)) continue;
                 float f[8];
@@ -651,113 +684,158 @@ __device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, co
 }
 
 template <int DH>
-__device__ void k_math(const AttnParams &p, KShared &S, uint32_t base, const Waits &wait, int half, int warp, int lane)
+__device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, uint32_t base, const Waits &wait, int half, int warp, int lane)
 {
     using C = KCfg<DH>;
     const KWork &w = S.work;
     const int row = warp * 32 + lane;
     const uint32_t tm = S.tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int key = row < w.rows ? w.key0 + row : -1;
+    const bool live = row < w.rows;                  // (rows past the tile's are never stored)
+    const int key = w.key0 + row;
     const float c = p.scale * kLog2e;
     const uint64_t c2 = pair(c, c);
-    bool ok = true;
-    const int n = w.n;
-    for (int i = 0; i < n; ++i) {
-        const int st = i & 1, qb = w.first + i / p.G;
-        const bool full = seen_by_all(p, w, qb);
-        const uint32_t vec = base + C::OFF_VEC + st * 1024 + half * 256;
-        // Queries of this thread's columns that see the key: [first, last], or up to `end` for one of the first keys.
-        const int shift = w.s.keys() - w.s.queries() + qb * kTile + half * 64, first = key < 0 ? 64 : key - shift;
-        const int end = w.s.queries() - qb * kTile - half * 64 - 1;
-        const int last = key < p.sinks ? end : static_cast<int>(min(static_cast<long long>(end), static_cast<long long>(first) + p.window - 1));
-        ok = wait.warp(smem_u32(&S.v_full[st]), (i >> 1) & 1) && wait.warp(smem_u32(&S.scores), i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[2][32];
-        tmem_ld32(tm + half * 64, s[0]);
-        tmem_ld32(tm + half * 64 + 32, s[1]);
-        tmem_wait_ld();
-        reg_fence(s[0]);
-        reg_fence(s[1]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                uint64_t l0, l1;
-                lds4(vec + x * 128 + j * 8, l0, l1);
-                float a0, a1, b0, b1;
-                unpair(fma2(pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1])), c2, l0), a0, a1);
-                unpair(fma2(pair(__uint_as_float(s[x][2 * j + 2]), __uint_as_float(s[x][2 * j + 3])), c2, l1), b0, b1);
-                s[x][2 * j] = __float_as_uint(exp2_fast(a0));
-                s[x][2 * j + 1] = __float_as_uint(exp2_fast(a1));
-                s[x][2 * j + 2] = __float_as_uint(exp2_fast(b0));
-                s[x][2 * j + 3] = __float_as_uint(exp2_fast(b1));
-            }
-        if (!full) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (k < first || k > last) s[k >> 5][k & 31] = 0u;
-            // Both score matrices have been made: the queries' rows may be changed for the last two products.
-            ok = wait.warp(smem_u32(&S.dp), i & 1);
-            if (!ok) break;
-            const int live = w.s.queries() - qb * kTile;
-            if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, live)) S.poison = 1;
-            __syncwarp();
-        }
-        put16(tm + half * 64, s[0]);
-        put16(tm + half * 64 + 16, s[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&S.probs));
-        ok = wait.warp(smem_u32(&S.dp), i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t d[2][32];
-        tmem_ld32(tm + kTile + half * 64, d[0]);
-        tmem_ld32(tm + kTile + half * 64 + 32, d[1]);
-        tmem_wait_ld();
-        reg_fence(d[0]);
-        reg_fence(d[1]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                uint64_t d0, d1;
-                lds4(vec + 512 + x * 128 + j * 8, d0, d1);
-                float a0, a1, b0, b1;
-                unpair(mul2(add2(pair(__uint_as_float(d[x][2 * j]), __uint_as_float(d[x][2 * j + 1])), d0),
-                            pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1]))), a0, a1);
-                unpair(mul2(add2(pair(__uint_as_float(d[x][2 * j + 2]), __uint_as_float(d[x][2 * j + 3])), d1),
-                            pair(__uint_as_float(s[x][2 * j + 2]), __uint_as_float(s[x][2 * j + 3]))), b0, b1);
-                d[x][2 * j] = __float_as_uint(a0);
-                d[x][2 * j + 1] = __float_as_uint(a1);
-                d[x][2 * j + 2] = __float_as_uint(b0);
-                d[x][2 * j + 3] = __float_as_uint(b1);
-            }
-        if (!full) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-                if (k < first || k > last) d[k >> 5][k & 31] = 0u;
-        }
-        put16(tm + kTile + half * 64, d[0]);
-        put16(tm + kTile + half * 64 + 16, d[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(smem_u32(&S.ds));
-            mbar_arrive(smem_u32(&S.v_empty[st]));
-        }
-    }
-    if (ok) ok = wait.warp(smem_u32(&S.done), 0);
-    if (!ok) return;
-    tc_fence_after();
+    const int n = w.n, shift = w.s.keys() - w.s.queries(), f0 = w.f0, f1 = w.f1;
     // dv through the first warpgroup and the keys' place, dk through the second and the values'.
     const uint32_t out = tm + (half ? 3 : 2) * kTile, tile = base + half * C::TILE;
-    if (n > 0 && *reinterpret_cast<volatile int *>(&S.poison)) k_add_taken(p, w, half ? p.q : p.dout, out, key, 0, p.D);
-    store_sums<DH>(out, tile, warp, lane, 0, DH / 32, half ? p.scale : 1.0f, n > 0);
-    copy_rows_out<DH / 8>(half ? p.dk : p.dv, static_cast<long long>(w.s.k0) + w.key0, w.kv, tile, warp, lane, 0, w.rows, p.D);
+    int j = 0;                       // iterations of all passes
+    for (int again = 0; n > 0; ++again) {
+        int qb = w.first, h = 0;
+        for (int i = 0; i < n; ++i, ++j) {
+            const int st = j & 1;
+            const bool full = qb >= f0 && qb < f1;
+            const uint32_t vec = base + C::OFF_VEC + st * 1024 + half * 256;
+            uint32_t seen[2] = {~0u, ~0u};           // of this thread's columns, the queries that see the key
+            if (!full) {
+                // From `first` on, up to `last`: the window's end, or the sequence's for one of the first keys.
+                const int first = key - shift - qb * kTile - half * 64, end = w.s.queries() - qb * kTile - half * 64 - 1;
+                const int last = key < p.sinks ? end : static_cast<int>(min(static_cast<long long>(end), static_cast<long long>(first) + p.window - 1));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) seen[x] = below(last + 1 - 32 * x) & ~below(first - 32 * x);
+            }
+            if (!wait.warp(smem_u32(&S.v_full[st]), (j >> 1) & 1) || !wait.warp(smem_u32(&S.scores), j & 1)) return;
+            tc_fence_after();
+            uint32_t s[2][32];
+            tmem_ld32(tm + half * 64, s[0]);
+            tmem_ld32(tm + half * 64 + 32, s[1]);
+            tmem_wait_ld();
+            reg_fence(s[0]);
+            reg_fence(s[1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    uint64_t l0, l1;
+                    lds4(vec + x * 128 + k * 8, l0, l1);
+                    float a0, a1, b0, b1;
+                    unpair(fma2(pair(__uint_as_float(s[x][2 * k]), __uint_as_float(s[x][2 * k + 1])), c2, l0), a0, a1);
+                    unpair(fma2(pair(__uint_as_float(s[x][2 * k + 2]), __uint_as_float(s[x][2 * k + 3])), c2, l1), b0, b1);
+                    s[x][2 * k] = __float_as_uint(exp2_fast(a0));
+                    s[x][2 * k + 1] = __float_as_uint(exp2_fast(a1));
+                    s[x][2 * k + 2] = __float_as_uint(exp2_fast(b0));
+                    s[x][2 * k + 3] = __float_as_uint(exp2_fast(b1));
+                }
+            bool some[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                some[x] = __any_sync(kWarp, seen[x] != ~0u);
+                if (some[x]) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(seen[x] & (1u << k))) s[x][k] = 0u;
+                }
+            }
+            if (again && !full) {
+                // When both score matrices have been made the queries' rows may be changed for the last two products.
+                if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
+                if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, w.s.queries() - qb * kTile)) S.taken = 1;
+                __syncwarp();
+            }
+            put16(tm + half * 64, s[0]);
+            put16(tm + half * 64 + 16, s[1]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.probs));
+            if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
+            tc_fence_after();
+            uint32_t d[2][32];
+            tmem_ld32(tm + kTile + half * 64, d[0]);
+            tmem_ld32(tm + kTile + half * 64 + 32, d[1]);
+            tmem_wait_ld();
+            reg_fence(d[0]);
+            reg_fence(d[1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    uint64_t d0, d1;
+                    lds4(vec + 512 + x * 128 + k * 8, d0, d1);
+                    float a0, a1, b0, b1;
+                    unpair(mul2(add2(pair(__uint_as_float(d[x][2 * k]), __uint_as_float(d[x][2 * k + 1])), d0),
+                                pair(__uint_as_float(s[x][2 * k]), __uint_as_float(s[x][2 * k + 1]))), a0, a1);
+                    unpair(mul2(add2(pair(__uint_as_float(d[x][2 * k + 2]), __uint_as_float(d[x][2 * k + 3])), d1),
+                                pair(__uint_as_float(s[x][2 * k + 2]), __uint_as_float(s[x][2 * k + 3]))), b0, b1);
+                    d[x][2 * k] = __float_as_uint(a0);
+                    d[x][2 * k + 1] = __float_as_uint(a1);
+                    d[x][2 * k + 2] = __float_as_uint(b0);
+                    d[x][2 * k + 3] = __float_as_uint(b1);
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (some[x]) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(seen[x] & (1u << k))) d[x][k] = 0u;
+                }
+            put16(tm + kTile + half * 64, d[0]);
+            put16(tm + kTile + half * 64 + 16, d[1]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&S.ds));
+                mbar_arrive(smem_u32(&S.v_empty[st]));
+            }
+            if (++h == p.G) {
+                h = 0;
+                ++qb;
+            }
+        }
+        if (!wait.warp(smem_u32(&S.done), again)) return;
+        tc_fence_after();
+        if (again && *reinterpret_cast<volatile int *>(&S.taken)) k_add_taken(p, w, half ? p.q : p.dout, out, live ? key : -1, 0, p.D);
+        bool bad = false;
+#pragma unroll 1
+        for (int x = 0; x < DH / 32; ++x) {
+            uint32_t o[1][32];
+            tmem_ld32(out + 32 * x, o[0]);
+            tmem_wait_ld();
+            reg_fence(o[0]);
+            bad |= not_finite(o);
+            if (again) put_sums(tile, row, x, o[0], half ? p.scale : 1.0f);
+        }
+        if (again) break;
+        if (__any_sync(kWarp, live && bad)) S.again = 1;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.verdict));
+        if (!wait.warp(smem_u32(&S.verdict), 0)) return;
+        if (*reinterpret_cast<volatile int *>(&S.again)) continue;
+#pragma unroll 1
+        for (int x = 0; x < DH / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld32(out + 32 * x, o);
+            tmem_wait_ld();
+            reg_fence(o);
+            put_sums(tile, row, x, o, half ? p.scale : 1.0f);
+        }
+        break;
+    }
+    if (n == 0) {
+        const uint32_t zero[32] = {};
+        for (int x = 0; x < DH / 32; ++x) put_sums(tile, row, x, zero, 0.0f);
+    }
+    write_rows<DH>(half ? &maps.dk : &maps.dv, half ? p.dk : p.dv, tile, w.kv, w.s.k0 + w.key0, warp, lane, w.rows, p.D);
 }
 
 template <int DH>
@@ -771,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.poison = 0;
+        S.again = S.taken = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&S.q_full[i]), 1);
             mbar_init(smem_u32(&S.q_empty[i]), 1);
@@ -786,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         mbar_init(smem_u32(&S.probs), 8);
         mbar_init(smem_u32(&S.ds), 8);
         mbar_init(smem_u32(&S.done), 1);
+        mbar_init(smem_u32(&S.verdict), 8);
         mbar_init(smem_u32(&S.drain), 1);
         mbar_init(smem_u32(&S.never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -813,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const bool some = S.some;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMathRegs));
-        if (some) k_math<DH>(p, S, base, wait, warp >> 2, warp & 3, lane);
+        if (some) k_math<DH>(p, maps, S, base, wait, warp >> 2, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kServiceRegs));
         if (some && warp == 8 && elect_one()) k_copy<DH>(p, maps, S, base, wait);
