@@ -415,7 +415,7 @@ det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, 
     p.dv = on(dv, dvt, dvh);
     AttnMaps maps;
     if (!encode(&maps.q, q, T, H, D, qt, qh) || !encode(&maps.k, k, S, KV, D, kt, kh) || !encode(&maps.v, v, S, KV, D, vt, vh) ||
-        !encode(&maps.dout, dout, T, H, D, dot, doh) || !encode(&maps.out, dq, T, H, D, dqt, dqh, 1, 32) ||
+        !encode(&maps.dout, dout, T, H, D, dot, doh) || !encode(&maps.o, out, T, H, D, ot, oh) || !encode(&maps.out, dq, T, H, D, dqt, dqh, 1, 32) ||
         !encode(&maps.dk, dk, S, KV, D, dkt, dkh, 1, 32) || !encode(&maps.dv, dv, S, KV, D, dvt, dvh, 1, 32))
         return no_map();
     const cudaError_t e = launch_attn_bwd(p, maps, cs(stream));

@@ -114,7 +114,7 @@ struct QWork {
     Places at;
 };
 struct QShared {
-    uint64_t q_full, full[8], empty[8], scores[2], dp, read, ds, done, verdict, staged, drain, never;
+    uint64_t q_full, o_full, o_read, full[8], empty[8], scores[2], dp, read, ds, done, verdict, staged, drain, never;
     uint32_t tmem;
     int abort_flag, taken, again, some;
     QWork work;
@@ -153,16 +153,19 @@ __device__ void q_copy(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
     using C = QCfg<DH>;
     const QWork w = S.work;
     if (w.blocks.n == 0 || (p.force_timeout && !wait.one(smem_u32(&S.never), 0))) return;
-    mbar_arrive_expect_tx(smem_u32(&S.q_full), 2 * C::TILE);
+    // The output's rows, for delta, lie where the ring's last tile will.
+    mbar_arrive_expect_tx(smem_u32(&S.o_full), 2 * C::TILE);
+    load_tile<DH>(base + C::TILE, &maps.dout, smem_u32(&S.o_full), w.head, w.row0);
+    load_tile<DH>(base + C::OFF_RING + (C::SLOTS - 1) * C::TILE, &maps.o, smem_u32(&S.o_full), w.head, w.row0);
+    mbar_arrive_expect_tx(smem_u32(&S.q_full), C::TILE);
     load_tile<DH>(base, &maps.q, smem_u32(&S.q_full), w.head, w.row0);
-    load_tile<DH>(base + C::TILE, &maps.dout, smem_u32(&S.q_full), w.head, w.row0);
     int slot = 0;
     uint32_t round = 0, loaded = 0, parity = 0;
     bool ok = true;
     for (int again = 0; ok && again < 2; ++again) {
         if (again && !done_again(S, wait)) break;
         for (int i = 0; i < 2 * w.blocks.n; ++i) {
-            ok = wait.one(smem_u32(&S.empty[slot]), round ^ 1u);
+            ok = wait.one(smem_u32(&S.empty[slot]), round ^ 1u) && (slot < C::SLOTS - 1 || wait.one(smem_u32(&S.o_read), 0));
             if (!ok) break;
             const uint32_t bar = smem_u32(&S.full[slot]);
             mbar_arrive_expect_tx(bar, C::TILE);
@@ -176,6 +179,7 @@ __device__ void q_copy(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
         }
     }
     if (!ok || *wait.abort_flag) {
+        wait.drain(smem_u32(&S.o_full), 0);
         wait.drain(smem_u32(&S.q_full), 0);
         for (int i = 0; i < C::SLOTS; ++i)
             if (loaded & (1u << i)) wait.drain(smem_u32(&S.full[i]), (parity >> i) & 1u);
@@ -191,7 +195,7 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
     const QWork w = S.work;
     const uint32_t ring = base + C::OFF_RING, tm = S.tmem;
     const int steps = (p.D + 15) / 16, n = w.blocks.n;
-    bool ok = n == 0 || wait.one(smem_u32(&S.q_full), 0), issued = false;
+    bool ok = n == 0 || (wait.one(smem_u32(&S.q_full), 0) && wait.one(smem_u32(&S.o_full), 0)), issued = false;
     // Block i of all passes: its keys are tile 2 i of the ring, its values the next.
     auto arrived = [&](int seq) {
         ok = ok && wait.one(smem_u32(&S.full[seq % C::SLOTS]), (seq / C::SLOTS) & 1);
@@ -274,34 +278,35 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
     const bool live = row < w.rows;
     const int position = w.pos.lo + row;             // (of a row past the tile's: never stored)
     const long long at = static_cast<long long>(w.head) * p.T + w.row0 + row;
-    // delta: a half of the row's columns each, joined in shared memory, the first half first.
-    float part = 0.0f;
-    if (live) {
-        const uint16_t *a = p.dout.row(w.row0 + row, w.head), *b = p.out.row(w.row0 + row, w.head);
-        uint4 x[DH / 16], y[DH / 16];
+    // delta from the copies of dout and out: a half of the row's columns each, joined in shared memory, the first half first.
+    float delta = 0.0f;
+    if (w.blocks.n > 0) {
+        const bool ok = wait.warp(smem_u32(&S.o_full), 0);
+        float part = 0.0f;
+        if (ok) {
 #pragma unroll
-        for (int i = 0; i < DH / 16; ++i) {
-            const int c = half * (DH / 2) + 8 * i;
-            if (c < p.D) {
-                x[i] = *reinterpret_cast<const uint4 *>(a + c);
-                y[i] = *reinterpret_cast<const uint4 *>(b + c);
-            } else {
-                x[i] = y[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < DH / 16; ++i) {
+                const int chunk = half * (DH / 16) + i;
+                const uint32_t of = (chunk >> 3) * (kTile * 128) + row * 128 + ((chunk ^ row) & 7) * 16;
+                uint4 x, y;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(base + C::TILE + of));
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                             : "r"(base + C::OFF_RING + (C::SLOTS - 1) * C::TILE + of));
+                float f[8], g[8];
+                unpack8(x, f);
+                unpack8(y, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part = fmaf(f[e], g[e], part);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.o_read));
         }
-#pragma unroll
-        for (int i = 0; i < DH / 16; ++i) {
-            float f[8], g[8];
-            unpack8(x[i], f);
-            unpack8(y[i], g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) part = fmaf(f[e], g[e], part);
-        }
+        float *deltas = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&S) - 1024);
+        deltas[half * kTile + row] = part;
+        if (any_at(1, 256, !ok)) return;             // (all leave together: nobody is waited for in vain)
+        delta = deltas[row] + deltas[kTile + row];
     }
-    float *deltas = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&S) - 1024);
-    deltas[half * kTile + row] = part;
-    asm volatile("bar.sync 1, 256;" ::: "memory");               // (before any wait: nobody has left)
-    const float delta = deltas[row] + deltas[kTile + row];
     const float lse = live ? p.lse[at] : 0.0f;
     if (live && half == 0) p.delta[at] = delta;
     const float c = p.scale * kLog2e, off = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
@@ -423,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
             mbar_init(smem_u32(&S.empty[i]), 1);
         }
         mbar_init(smem_u32(&S.q_full), 1);
+        mbar_init(smem_u32(&S.o_full), 1);
+        mbar_init(smem_u32(&S.o_read), 8);
         mbar_init(smem_u32(&S.scores[0]), 1);
         mbar_init(smem_u32(&S.scores[1]), 1);
         mbar_init(smem_u32(&S.dp), 1);

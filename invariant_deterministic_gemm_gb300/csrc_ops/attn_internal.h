@@ -50,10 +50,10 @@ struct AttnParams {
     unsigned long long timeout_ns;
     int force_timeout;
 };
-// Heads [T, H, D] as (column, head, token): inputs in boxes of 64 columns of 128 tokens, outputs (out, or dq, dk and dv) in
-// boxes of 32 tokens.
+// Heads [T, H, D] as (column, head, token): inputs (o: the forward pass's output) in boxes of 64 columns of 128 tokens, outputs
+// (out, or dq in its place, dk and dv) in boxes of 32 tokens.
 struct AttnMaps {
-    CUtensorMap q, k, v, dout, out, dk, dv;
+    CUtensorMap q, k, v, dout, o, out, dk, dv;
 };
 cudaError_t launch_attn(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
 cudaError_t launch_attn_bwd(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);

@@ -49,6 +49,21 @@ struct Waits {
     __device__ bool warp(uint32_t bar, uint32_t parity) const { return __all_sync(kWarp, one(bar, parity)); }
 };
 
+// Whether one of the `threads` of named barrier `id` says so; they wait for one another, and none leaves but where all do.
+__device__ __forceinline__ bool any_at(int id, int threads, bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+
 // ---- tensor maps and copies
 
 // Heads [T, H, D] as (column, head, token); a box is 64 columns of `rows` tokens of one head.
