@@ -123,8 +123,11 @@ det_gemm_status no_map()
     return DET_GEMM_ERR_LAUNCH;
 }
 
-bool ok_turn(int64_t D, int64_t rot, int64_t P)
+// (The launch counts blocks of 256 items, at most 128 a head.)
+bool ok_turn(int64_t T, int64_t heads, int64_t D, int64_t rot, int64_t P)
 {
+    if (!launchable(T * heads / 2 + 1)) return false;
+
     return D >= 8 && D <= DET_ATTN_MAX_HEAD_DIM && D % 8 == 0 && rot >= 2 && rot <= D && rot % 2 == 0 && ok_size(P);
 }
 
@@ -172,7 +175,7 @@ det_gemm_status det_rope(const det_gemm_bf16 *x, const float *cosine, const floa
                          det_gemm_bf16 *y, int64_t T, int64_t H, int64_t D, int64_t rot, int64_t P, int interleaved,
                          int inverse, int64_t xt, int64_t xh, int64_t ldt, int64_t yt, int64_t yh, det_gemm_stream stream)
 {
-    if (!ok_size(T) || H < 0 || H > DET_ATTN_MAX_HEADS || !ok_turn(D, rot, P)) return DET_GEMM_ERR_INVALID_ARG;
+    if (!ok_size(T) || H < 0 || H > DET_ATTN_MAX_HEADS || !ok_turn(T, H, D, rot, P)) return DET_GEMM_ERR_INVALID_ARG;
     if (T == 0 || H == 0) return DET_GEMM_OK;
     const Strided in = heads(x, T, H, D, xt, xh), out = heads(y, T, H, D, yt, yh);
     const bool place = x == y && (T == 1 || xt == yt) && (H == 1 || xh == yh);
@@ -196,7 +199,7 @@ det_gemm_status det_rope(const det_gemm_bf16 *x, const float *cosine, const floa
     p.P = static_cast<int>(P);
     p.sign = inverse ? -1.0f : 1.0f;
     p.status = d->word;
-    const cudaError_t e = launch_rope(p, interleaved != 0, d->sms, cs(stream));
+    const cudaError_t e = launch_rope(p, interleaved != 0, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "rotation launch");
 }
 
@@ -208,7 +211,7 @@ det_gemm_status det_kv_append(const det_gemm_bf16 *q, const det_gemm_bf16 *k, co
                               int64_t oh, int64_t kcp, int64_t kcs, int64_t kch, int64_t vcp, int64_t vcs, int64_t vch,
                               det_gemm_stream stream)
 {
-    if (!ok_size(T) || H < 0 || H > DET_ATTN_MAX_HEADS || KV < 1 || KV > DET_ATTN_MAX_HEADS || !ok_turn(D, rot, P) ||
+    if (!ok_size(T) || H < 0 || H > DET_ATTN_MAX_HEADS || KV < 1 || KV > DET_ATTN_MAX_HEADS || !ok_turn(T, H + 2 * KV, D, rot, P) ||
         !ok_size(pages) || page_size < 1 || !ok_size(page_size) || !ok_size(pages * page_size))
         return DET_GEMM_ERR_INVALID_ARG;
     if (T == 0) return DET_GEMM_OK;
@@ -243,7 +246,7 @@ det_gemm_status det_kv_append(const det_gemm_bf16 *q, const det_gemm_bf16 *k, co
     p.page_size = static_cast<int>(page_size);
     p.sign = 1.0f;
     p.status = d->word;
-    const cudaError_t e = launch_rope(p, interleaved != 0, d->sms, cs(stream));
+    const cudaError_t e = launch_rope(p, interleaved != 0, cs(stream));
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "append launch");
 }
 

@@ -36,7 +36,7 @@ struct RopeParams {
     float sign;                      // -1: back
     int *status;
 };
-cudaError_t launch_rope(const RopeParams &p, bool interleaved, int sms, cudaStream_t s);
+cudaError_t launch_rope(const RopeParams &p, bool interleaved, cudaStream_t s);
 
 struct AttnParams {
     Heads q, k, v, out, dout, dq, dk, dv;
