@@ -113,7 +113,8 @@ det_gemm_status det_attn(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const d
  * the query heads that share a KV head. P and dS are rounded to BF16 for
  * their second products. Rows outside every sequence become zero.
  */
-int64_t det_attn_bwd_workspace(int64_t N, int64_t T, int64_t S, int64_t H, int64_t KV, int64_t D);
+int64_t det_attn_bwd_workspace(int64_t N, int64_t T, int64_t S, int64_t H, int64_t KV, int64_t D, int64_t window,
+                               int64_t sinks);
 det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, const det_gemm_bf16 *k,
                              const det_gemm_bf16 *v, const det_gemm_bf16 *out, const float *lse, const int32_t *q_bounds,
                              const int32_t *k_bounds, det_gemm_bf16 *dq, det_gemm_bf16 *dk, det_gemm_bf16 *dv, int64_t N,

@@ -755,12 +755,13 @@ PyObject *attn_bwd(Argv a)
     const float *lse = static_cast<float *>(flat(a[5], "lse", kF32, {q.H, q.T}));
     const Packed b = packed(a[6], a[7], q.T, k.T);
     const at::Device dev = THPVariable_Unpack(a[0]).device();
-    const int64_t size = std::max<int64_t>(det_attn_bwd_workspace(b.N, q.T, k.T, q.H, k.H, q.D), 256);
+    const int64_t window = window_of(a[9]), sinks = integer(a[10], "sinks");
+    const int64_t size = std::max<int64_t>(det_attn_bwd_workspace(b.N, q.T, k.T, q.H, k.H, q.D, window, sinks), 256);
     const Tensor ws = empty({size}, ScalarType::Byte, dev);
     const Tensor dq = empty({q.T, q.H, q.D}, kBF16, dev), dk = empty({k.T, k.H, k.D}, kBF16, dev), dv = empty({k.T, k.H, k.D}, kBF16, dev);
     const int64_t qt = q.H * q.D, kt = k.H * k.D;
     check(det_attn_bwd(d.p, q.p, k.p, v.p, y.p, lse, b.q, b.k, ptr<bf16>(dq), ptr<bf16>(dk), ptr<bf16>(dv), b.N, q.T, k.T, q.H, k.H, q.D,
-                       scale_of(a[8], q.D), window_of(a[9]), integer(a[10], "sinks"), d.t, d.h, q.t, q.h, k.t, k.h, v.t, v.h, y.t, y.h,
+                       scale_of(a[8], q.D), window, sinks, d.t, d.h, q.t, q.h, k.t, k.h, v.t, v.h, y.t, y.h,
                        qt, q.D, kt, k.D, kt, k.D, ptr(ws), size, stream()),
           "det_attn_bwd");
     PyObject *r = PyTuple_New(3);

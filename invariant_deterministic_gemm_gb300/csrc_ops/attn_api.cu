@@ -131,8 +131,15 @@ bool ok_turn(int64_t T, int64_t heads, int64_t D, int64_t rot, int64_t P)
     return D >= 8 && D <= DET_ATTN_MAX_HEAD_DIM && D % 8 == 0 && rot >= 2 && rot <= D && rot % 2 == 0 && ok_size(P);
 }
 
-// Device memory of the backward pass: delta [H, T].
-int64_t bwd_bytes(int64_t T, int64_t H) { return up(std::max<int64_t>(4 * T * H, 1), 256) * 256; }
+// Device memory of the backward pass: delta [H, T], then the first keys' pieces.
+struct BwdSpace {
+    int64_t partials, total;
+};
+BwdSpace bwd_space(int64_t N, int64_t T, int64_t H, int64_t KV, int64_t D, int64_t window, int64_t sinks)
+{
+    const int64_t delta = up(std::max<int64_t>(4 * T * H, 1), 256) * 256;
+    return BwdSpace{delta, delta + piece_slots(T, N, true) * sink_blocks(window, sinks) * KV * 2 * 128 * D * 4};
+}
 
 // Decode: the query heads of a KV head are taken up to 32 at once; device memory of the cuts between CTAs, and of what
 // they leave in parts.
@@ -377,10 +384,10 @@ det_gemm_status det_attn(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const d
     return e == cudaSuccess ? DET_GEMM_OK : fail(DET_GEMM_ERR_LAUNCH, e, "attention launch");
 }
 
-int64_t det_attn_bwd_workspace(int64_t N, int64_t T, int64_t S, int64_t H, int64_t KV, int64_t D)
+int64_t det_attn_bwd_workspace(int64_t N, int64_t T, int64_t S, int64_t H, int64_t KV, int64_t D, int64_t window, int64_t sinks)
 {
-    if (!ok_size(N) || !ok_size(T) || !ok_size(S) || !ok_heads(H, KV, D)) return 0;
-    return bwd_bytes(T, H);
+    if (!ok_size(N) || !ok_size(T) || !ok_size(S) || !ok_heads(H, KV, D) || window < 0 || sinks < 0) return 0;
+    return bwd_space(N, T, H, KV, D, window, sinks).total;
 }
 
 det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, const det_gemm_bf16 *k,
@@ -395,7 +402,9 @@ det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, 
     det_gemm_status s = ok_attn(q_bounds, k_bounds, N, T, S, H, KV, D, scale, window, sinks);
     if (s != DET_GEMM_OK) return s;
     if (T == 0 && S == 0) return DET_GEMM_OK;
-    const int64_t need = det_attn_bwd_workspace(N, T, S, H, KV, D);
+    const BwdSpace space = bwd_space(N, T, H, KV, D, window, sinks);
+    const int64_t need = space.total;
+    if (!launchable((S / 128 + N + 1 + piece_slots(T, N, true) * sink_blocks(window, sinks)) * KV)) return DET_GEMM_ERR_INVALID_ARG;
     if ((s = check_all({heads(dout, T, H, D, dot, doh), heads(q, T, H, D, qt, qh), heads(k, S, KV, D, kt, kh),
                         heads(v, S, KV, D, vt, vh), heads(out, T, H, D, ot, oh)},
                        {vec4(lse, H * T), vec4(q_bounds, q_bounds ? N + 1 : 0), vec4(k_bounds, k_bounds ? N + 1 : 0)},
@@ -413,6 +422,8 @@ det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, 
     p.out = on(out, ot, oh);
     p.lse = const_cast<float *>(lse);
     p.delta = static_cast<float *>(workspace);
+    p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + space.partials);
+    p.sink_blocks = sink_blocks(window, sinks);
     p.dq = on(dq, dqt, dqh);
     p.dk = on(dk, dkt, dkh);
     p.dv = on(dv, dvt, dvh);

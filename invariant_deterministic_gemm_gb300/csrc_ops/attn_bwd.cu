@@ -12,6 +12,9 @@
 // matrices, dv, dk). The scores are made twice: seven products where five would
 // do with dq added up by atomics, whose order changes bits.
 //
+// With a window, the first keys that stay visible are seen by all queries: they are taken in pieces of 512 queries, which a
+// third launch adds up (one CTA would walk every query: 50 us of 85 for three sequences of about 700 with a window of 257).
+//
 // In both, a row is a TMEM lane; two warpgroups take half of a block's columns
 // each. P and dS go back to TMEM in the place of the scores they came from,
 // rounded to BF16 (as the tensor core wants it beside BF16 operands), and are
@@ -499,6 +502,7 @@ struct KWork {
     int kv, key0, rows;              // first key's place in the sequence; keys of the tile
     int first, n;                    // first block of 128 queries; iterations: blocks times heads
     int f0, f1;                      // the blocks of which every query sees every key of the tile
+    int piece;                       // of the first keys' queries, or -1: all that see the tile
 };
 struct KShared {
     uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, verdict, drain, never;
@@ -509,14 +513,27 @@ struct KShared {
 static_assert(sizeof(KShared) <= 512, "shared state");
 
 // The queries [lo, hi] of the sequence that see some of the tile's keys.
-__device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, KWork &w)
+// Of a piece (units below `pieces`): those among kPiece queries.
+__device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, int pieces, KWork &w)
 {
     if (p.kb && p.N == 0) return false;
-    w.kv = unit % p.KV;
-    int tile;
-    const int n = tile_sequence(p.kb, p.N, p.S, kTile, unit / p.KV, tile);
-    w.s = seq_at(p, n);
-    const long long key0 = static_cast<long long>(kTile) * tile;
+    long long key0;
+    int part = 0;
+    w.piece = -1;
+    if (unit < pieces) {
+        w.piece = unit;
+        w.kv = unit % p.KV;
+        key0 = static_cast<long long>(unit / p.KV % p.sink_blocks) * kTile;
+        w.s = seq_at(p, tile_sequence(p.qb, p.N, p.T, kPiece, unit / p.KV / p.sink_blocks, part));
+        if (static_cast<long long>(part) * kPiece >= w.s.queries()) return false;
+    } else {
+        unit -= pieces;
+        w.kv = unit % p.KV;
+        int tile;
+        w.s = seq_at(p, tile_sequence(p.kb, p.N, p.S, kTile, unit / p.KV, tile));
+        key0 = static_cast<long long>(kTile) * tile;
+        if (tile < p.sink_blocks) return false;              // the pieces'
+    }
     if (key0 >= w.s.keys()) return false;
     w.key0 = static_cast<int>(key0);
     w.rows = min(kTile, w.s.keys() - w.key0);
@@ -524,8 +541,14 @@ __device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, KWork &
     const long long lo = max(0, w.key0 - shift);
     long long hi = w.s.queries() - 1;
     if (w.key0 >= p.sinks) hi = min(hi, static_cast<long long>(w.key0) + w.rows - 1 + p.window - 1 - shift);
-    w.first = static_cast<int>(lo / kTile);
-    w.n = hi >= lo ? static_cast<int>(hi / kTile - lo / kTile + 1) * p.G : 0;
+    long long b0 = lo / kTile, b1 = hi >= lo ? hi / kTile : b0 - 1;
+    if (w.piece >= 0) {
+        b0 = max(b0, static_cast<long long>(part) * (kPiece / kTile));
+        b1 = min(b1, static_cast<long long>(part + 1) * (kPiece / kTile) - 1);
+        if (b1 < b0) return false;
+    }
+    w.first = static_cast<int>(b0);
+    w.n = static_cast<int>(b1 - b0 + 1) * p.G;
     const long long f0 = max(0ll, static_cast<long long>(w.key0) + kTile - 1 - shift);
     long long f1 = w.s.queries();    // whole blocks that begin before
     if (w.key0 + kTile - 1 >= p.sinks) f1 = min(f1, static_cast<long long>(w.key0) - shift + p.window);
@@ -704,6 +727,19 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
     const int n = w.n, shift = w.s.keys() - w.s.queries(), f0 = w.f0, f1 = w.f1;
     // dv through the first warpgroup and the keys' place, dk through the second and the values'.
     const uint32_t out = tm + (half ? 3 : 2) * kTile, tile = base + half * C::TILE;
+    // A piece's sums go out as they are.
+    float *part = w.piece < 0 ? nullptr : p.partials + (static_cast<long long>(w.piece) * 2 + half) * kTile * p.D + static_cast<long long>(row) * p.D;
+    auto put = [&](int x, const uint32_t (&o)[32]) {
+        if (!part) {
+            put_sums(tile, row, x, o, half ? p.scale : 1.0f);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+            if (32 * x + k < p.D)
+                *reinterpret_cast<float4 *>(part + 32 * x + k) =
+                    make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+    };
     int j = 0;                       // iterations of all passes
     for (int again = 0; n > 0; ++again) {
         int qb = w.first, h = 0;
@@ -819,7 +855,7 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
             tmem_wait_ld();
             reg_fence(o[0]);
             bad |= not_finite(o);
-            if (again) put_sums(tile, row, x, o[0], half ? p.scale : 1.0f);
+            if (again) put(x, o[0]);
         }
         if (again) break;
         if (__any_sync(kWarp, live && bad)) S.again = 1;
@@ -834,10 +870,11 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
             tmem_ld32(out + 32 * x, o);
             tmem_wait_ld();
             reg_fence(o);
-            put_sums(tile, row, x, o, half ? p.scale : 1.0f);
+            put(x, o);
         }
         break;
     }
+    if (part) return;
     if (n == 0) {
         const uint32_t zero[32] = {};
         for (int x = 0; x < DH / 32; ++x) put_sums(tile, row, x, zero, 0.0f);
@@ -846,7 +883,7 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
 }
 
 template <int DH>
-__global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps maps)
+__global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps maps, const int pieces)
 {
     using C = KCfg<DH>;
     extern __shared__ uint8_t attn_smem[];
@@ -889,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     begin();
     if (threadIdx.x == 32) {
         KWork w;
-        S.some = find_keys(p, blockIdx.x, w);
+        S.some = find_keys(p, blockIdx.x, pieces, w);
         if (S.some) S.work = w;
     }
     tc_fence_before();
@@ -913,6 +950,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
+}
+
+// dk and dv of the first keys from their pieces, in ascending order: a block takes kJoinRows keys of a sequence and KV head.
+constexpr int kJoinRows = 8, kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) attn_pieces_kernel(const AttnParams p)
+{
+    begin();
+    constexpr int GROUPS = kTile / kJoinRows;
+    int id = blockIdx.x;
+    const int r0 = id % GROUPS * kJoinRows;
+    id /= GROUPS;
+    const int kv = id % p.KV, block = id / p.KV % p.sink_blocks, n = id / p.KV / p.sink_blocks;
+    const Seq s = seq_at(p, n);
+    const int key0 = block * kTile + r0, shift = s.keys() - s.queries();
+    // The pieces that hold queries which see the block.
+    const int lo = max(0, block * kTile - shift) / kPiece, hi = (s.queries() + kPiece - 1) / kPiece;
+    const int slot0 = p.qb ? clamped(p.qb, n, p.T) / kPiece + n : 0;
+    const int quads = p.D / 4;
+    for (int i = threadIdx.x; i < 2 * kJoinRows * quads; i += kJoinThreads) {
+        const int c = i % quads * 4, r = i / quads % kJoinRows, which = i / quads / kJoinRows;
+        if (key0 + r >= s.keys()) continue;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int x = lo; x < hi; ++x) {
+            const long long piece = (static_cast<long long>(slot0 + x) * p.sink_blocks + block) * p.KV + kv;
+            const float4 v = *reinterpret_cast<const float4 *>(p.partials + ((piece * 2 + which) * kTile + r0 + r) * p.D + c);
+            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+        }
+        const float f = which ? p.scale : 1.0f;
+        const Heads &out = which ? p.dk : p.dv;
+        *reinterpret_cast<uint2 *>(out.row(static_cast<long long>(s.k0) + key0 + r, kv) + c) = make_uint2(pack_bf16(sum.x * f, sum.y * f), pack_bf16(sum.z * f, sum.w * f));
+    }
 }
 
 template <typename F>
@@ -942,7 +1012,10 @@ cudaError_t run(const AttnParams &p, const AttnMaps &maps, cudaStream_t s)
     }
     if (p.S > 0) {
         const int slots = p.kb ? tile_slots(p.S, p.N, kTile) : (p.S + kTile - 1) / kTile;
-        e = launch_early(attn_dkv_kernel<DH>, static_cast<long long>(slots) * p.KV, kThreads, KCfg<DH>::SMEM, 1, s, p, maps);
+        const int pieces = static_cast<int>(piece_slots(p.T, p.N, p.qb != nullptr)) * p.sink_blocks * p.KV;
+        e = launch_early(attn_dkv_kernel<DH>, pieces + static_cast<long long>(slots) * p.KV, kThreads, KCfg<DH>::SMEM, 1, s, p, maps, pieces);
+        if (e != cudaSuccess || p.sink_blocks == 0 || (p.qb && p.N == 0)) return e;
+        e = launch_early(attn_pieces_kernel, static_cast<long long>(p.qb ? p.N : 1) * p.sink_blocks * p.KV * (kTile / kJoinRows), kJoinThreads, 0, 1, s, p);
     }
     return e;
 }

@@ -42,6 +42,8 @@ struct AttnParams {
     Heads q, k, v, out, dout, dq, dk, dv;
     float *lse;                      // [H, T]
     float *delta;                    // backward: [H, T]
+    float *partials;                 // backward: the first keys' gradients by pieces, [pieces][2: dv, dk][128][D]
+    int sink_blocks;                 // blocks of first keys that are taken in pieces (0: none)
     const int32_t *qb, *kb;          // bounds [N + 1], or null: one sequence
     int N, T, S, H, KV, G, D;
     float scale;
@@ -56,6 +58,11 @@ struct AttnMaps {
     CUtensorMap q, k, v, dout, o, out, dk, dv;
 };
 cudaError_t launch_attn(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
+// With a window the first keys, which stay visible, are seen by all queries and the others by few: their gradients are summed
+// in pieces of so many queries, and the pieces joined. Only where there are at most kPieceSinks of them.
+constexpr int kPiece = 512, kPieceSinks = 512;
+inline int sink_blocks(long long window, long long sinks) { return window > 0 && sinks > 0 && sinks <= kPieceSinks ? static_cast<int>((sinks + 127) / 128) : 0; }
+inline long long piece_slots(long long T, long long N, bool packed) { return packed ? T / kPiece + (N > 1 ? N : 1) : (T + kPiece - 1) / kPiece; }
 cudaError_t launch_attn_bwd(const AttnParams &p, const AttnMaps &maps, cudaStream_t s);
 
 // The key axis of one sequence of a decode step: chunks of 256 keys, four to a block, 16 blocks to a super block. A

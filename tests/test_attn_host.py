@@ -62,7 +62,7 @@ DEFAULTS = {
                             ot=256, oh=64, workspace=A[6], workspace_bytes=1 << 30, stream=None),
     "det_attn": dict(q=A[0], k=A[1], v=A[2], q_bounds=A[3], k_bounds=None, out=A[4], lse=A[5], N=2, T=10, S=10, H=4, KV=2, D=64, scale=0.1,
                      window=0, sinks=0, qt=256, qh=64, kt=128, kh=64, vt=128, vh=64, ot=256, oh=64, stream=None),
-    "det_attn_bwd_workspace": dict(N=2, T=10, S=10, H=4, KV=2, D=64),
+    "det_attn_bwd_workspace": dict(N=2, T=10, S=10, H=4, KV=2, D=64, window=0, sinks=0),
     "det_attn_bwd": dict(dout=A[0], q=A[1], k=A[2], v=A[3], out=A[4], lse=A[5], q_bounds=A[6], k_bounds=None, dq=A[7], dk=A[8], dv=A[9], N=2, T=10,
                          S=10, H=4, KV=2, D=64, scale=0.1, window=0, sinks=0, dot=256, doh=64, qt=256, qh=64, kt=128, kh=64, vt=128, vh=64,
                          ot=256, oh=64, dqt=256, dqh=64, dkt=128, dkh=64, dvt=128, dvh=64, workspace=A[10], workspace_bytes=1 << 30, stream=None),
@@ -114,6 +114,7 @@ def test_empty_and_valid(call):
 def test_workspaces(call):
     assert call("det_attn_decode_workspace") > 0 and call("det_attn_decode_workspace", B=-1) == 0
     assert call("det_attn_bwd_workspace") >= 4 * 10 * 4 and call("det_attn_bwd_workspace", H=3) == 0
+    assert call("det_attn_bwd_workspace", window=100, sinks=4) > call("det_attn_bwd_workspace", window=100) and call("det_attn_bwd_workspace", sinks=-1) == 0
 
 
 def test_exports(dg):
