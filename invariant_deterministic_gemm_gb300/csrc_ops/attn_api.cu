@@ -404,7 +404,9 @@ det_gemm_status det_attn_bwd(const det_gemm_bf16 *dout, const det_gemm_bf16 *q, 
     if (T == 0 && S == 0) return DET_GEMM_OK;
     const BwdSpace space = bwd_space(N, T, H, KV, D, window, sinks);
     const int64_t need = space.total;
-    if (!launchable((S / 128 + N + 1 + piece_slots(T, N, true) * sink_blocks(window, sinks)) * KV)) return DET_GEMM_ERR_INVALID_ARG;
+    if (!launchable((S / 128 + N + 1 + piece_slots(T, N, true) * sink_blocks(window, sinks)) * KV) ||
+        !launchable(N * sink_blocks(window, sinks) * KV * 16))
+        return DET_GEMM_ERR_INVALID_ARG;
     if ((s = check_all({heads(dout, T, H, D, dot, doh), heads(q, T, H, D, qt, qh), heads(k, S, KV, D, kt, kh),
                         heads(v, S, KV, D, vt, vh), heads(out, T, H, D, ot, oh)},
                        {vec4(lse, H * T), vec4(q_bounds, q_bounds ? N + 1 : 0), vec4(k_bounds, k_bounds ? N + 1 : 0)},

@@ -68,7 +68,7 @@ struct Work {
 };
 
 struct Shared {
-    uint64_t q_full[2], full[8], empty[8], scores[2], probs[2], sane[2], done[2], verdict[2], drain, never;
+    uint64_t q_full[2], full[8], empty[8], scores[2], probs[2][2], sane[2], done[2], verdict[2], drain, never;
     uint32_t tmem;
     int abort_flag;
     int again[2];                    // the tile has to be done again
@@ -207,7 +207,8 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
             for (int t = 0; t < 2; ++t) {
                 if (!on[t]) continue;
                 if (w.at[t].sees(i)) {
-                    ok = wait.one(smem_u32(&S.probs[t]), (probs >> t) & 1u);
+                    const uint32_t phase = (probs >> t) & 1u;
+                    ok = wait.one(smem_u32(&S.probs[t][0]), phase);
                     probs ^= 1u << t;
                     if (ok && check) {           // the other tile's threads have looked at their part of the values
                         ok = wait.one(smem_u32(&S.sane[1 - t]), (sane >> (1 - t)) & 1u);
@@ -215,8 +216,12 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
                     }
                     if (!ok) return;
                     tc_fence_after();
-                    mma_rows(tm + 2 * kTile + t * kTile, tm + t * kTile, ring + v * C::TILE, n, out[t]);
+                    mma_rows<64>(tm + 2 * kTile + t * kTile, tm + t * kTile, ring + v * C::TILE, n, out[t]);
                     out[t] = issued = true;
+                    ok = wait.one(smem_u32(&S.probs[t][1]), phase);
+                    if (!ok) return;
+                    tc_fence_after();
+                    mma_rows<64>(tm + 2 * kTile + t * kTile, tm + t * kTile + 32, ring + v * C::TILE + 64 * 128, n, true);
                     if (i == last[t]) mma_commit(smem_u32(&S.done[t]));
                 }
                 if (more && w.at[t].sees(next)) {
@@ -332,9 +337,9 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
             float top[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                top[x] = __uint_as_float(s[x][0]);
+                top[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
 #pragma unroll
-                for (int j = 1; j < 32; ++j) top[x] = fmaxf(top[x], __uint_as_float(s[x][j]));
+                for (int j = 2; j < 32; j += 2) top[x] = max3(top[x], __uint_as_float(s[x][j]), __uint_as_float(s[x][j + 1]));
             }
             const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             const bool grown = mx > m + kSlack;
@@ -364,32 +369,37 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
             const float off = m == -INFINITY ? 0.0f : -m;
             const uint64_t c2 = pair(c, c), off2 = pair(off, off);
             uint64_t sum[4] = {0, 0, 0, 0};
+            // The first half of P goes to its product while the second is made.
+            auto arrive = [&](int half) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.probs[t][half]));
+            };
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 if ((hidden >> x) & 1u) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[x >> 1][16 * (x & 1) + j] = 0u;
-                    continue;
-                }
+                } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float lo, hi;
-                    unpair(fma2(pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1])), c2, off2), lo, hi);
-                    lo = exp2_fast(lo);
-                    hi = exp2_fast(hi);
-                    sum[j & 3] = add2(sum[j & 3], pair(lo, hi));
-                    s[x >> 1][16 * (x & 1) + j] = pack_bf16(lo, hi);
+                    for (int j = 0; j < 16; ++j) {
+                        float lo, hi;
+                        unpair(fma2(pair(__uint_as_float(s[x][2 * j]), __uint_as_float(s[x][2 * j + 1])), c2, off2), lo, hi);
+                        lo = exp2_fast(lo);
+                        hi = exp2_fast(hi);
+                        sum[j & 3] = add2(sum[j & 3], pair(lo, hi));
+                        s[x >> 1][16 * (x & 1) + j] = pack_bf16(lo, hi);
+                    }
                 }
+                if (x == 1) tmem_st32(ts, s[0]);
+                if (x == 2) arrive(0);
+                if (x == 3) tmem_st32(ts + 32, s[1]);
             }
-            tmem_st32(ts, s[0]);
-            tmem_st32(ts + 32, s[1]);
             float lo, hi;
             unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
             l += lo + hi;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.probs[t]));
+            arrive(1);
             out = true;
         }
         return true;
@@ -477,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&S.q_full[t]), 1);
             mbar_init(smem_u32(&S.scores[t]), 1);
-            mbar_init(smem_u32(&S.probs[t]), 4);
+            mbar_init(smem_u32(&S.probs[t][0]), 4);
+            mbar_init(smem_u32(&S.probs[t][1]), 4);
             mbar_init(smem_u32(&S.sane[t]), 4);
             mbar_init(smem_u32(&S.done[t]), 1);
             mbar_init(smem_u32(&S.verdict[t]), 4);

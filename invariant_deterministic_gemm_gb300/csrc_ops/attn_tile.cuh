@@ -152,13 +152,14 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, i
 }
 
 // d[128, D] (+)= A (TMEM, 128 x 128) times a tile's rows; n: D rounded up to 16.
-// `gap`: columns left out between A's halves (two warpgroups wrote them, each into its own part of the scores).
+// `gap`: columns left out between A's halves (two warpgroups wrote them, each into its own part of the scores). K: rows of b.
+template <int K = kTile>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint32_t b, int n, bool accumulate, uint32_t gap = 0)
 {
     const uint64_t db = sdesc(b, kTile * 128u, 1024u);
     const uint32_t idesc = idesc_bf16(kTile, n, 0, 1);
 #pragma unroll
-    for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a_tmem + k * 8 + (k >= 4 ? gap : 0), db + k * (2048 / 16), idesc, accumulate || k != 0);
+    for (int k = 0; k < K / 16; ++k) mma_ts(d, a_tmem + k * 8 + (k >= 4 ? gap : 0), db + k * (2048 / 16), idesc, accumulate || k != 0);
 }
 
 // Takes what is not finite out of row r of a tile (if the tile has one), and all of it if the sequence's rows end
@@ -218,6 +219,13 @@ __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
