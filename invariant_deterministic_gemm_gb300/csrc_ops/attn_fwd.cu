@@ -35,7 +35,7 @@ namespace deto {
 namespace {
 
 // The softmax warps keep a row's 128 scores in registers; the third warpgroup hands over what it does not need.
-constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 216, kServiceRegs = 72;
+constexpr int kThreads = 384, kLaunchRegs = 168, kSoftmaxRegs = 200, kServiceRegs = 104;
 static_assert(kSoftmaxRegs * 256 + kServiceRegs * 128 <= kLaunchRegs * kThreads, "register split");
 constexpr float kSlack = 8.0f;       // how far (log2) a row's maximum may be above what it is scaled by
 
@@ -392,8 +392,7 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
                         s[x >> 1][16 * (x & 1) + j] = pack_bf16(lo, hi);
                     }
                 }
-                if (x == 1) tmem_st32(ts, s[0]);
-                if (x == 2) arrive(0);
+                if (x == 1) { tmem_st32(ts, s[0]); arrive(0); }
                 if (x == 3) tmem_st32(ts + 32, s[1]);
             }
             float lo, hi;
