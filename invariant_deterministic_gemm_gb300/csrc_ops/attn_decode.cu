@@ -81,13 +81,15 @@ struct Shared {
     alignas(16) float most[kSums][32];   // the chunk's
     alignas(16) float sum[kSums][4][32]; // each warp's sums of P
     long long first, last;           // the CTA's units
-    long long scan[16];
+    unsigned scan[16];
     int start, start_list, start_unit;           // sequence of the first unit, its list, and its place there
     int unit;                        // chunks a unit
-    long long start_units, list_unit;            // units before the sequence, and before the list
-    long long total[3];
+    long long list_unit;                         // units before the list
+    long long sums_of[3][16];
 };
 static_assert(sizeof(Shared) <= 7168, "shared state");
+
+__device__ __forceinline__ void prefetch_l2(const void *x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); }
 
 // ---- the key axis
 
@@ -184,72 +186,79 @@ __device__ __forceinline__ unsigned tiles_of(const DecodeParams &p, int n, int c
 }
 
 // The CTA's run: how many units there are, of which size, and where its part begins. All threads.
+__device__ __forceinline__ long long quotient(long long x, unsigned y)
+{
+    return x >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / y);
+}
 __device__ void plan(const DecodeParams &p, Shared &S)
 {
-    const int thread = threadIdx.x, warp = thread >> 5, lane = thread & 31;
-    const long long lists = static_cast<long long>(p.KV) * p.parts;
+    const int thread = threadIdx.x, warp = thread >> 5, lane = thread & 31, warps = min(kThreads / 32, (p.B + 31) / 32);
+    const unsigned lists = p.KV * p.parts, ctas = gridDim.x;
     long long sum[3] = {0, 0, 0};
-    for (int b = thread; b < p.B; b += kThreads) {
-        const int n = tokens_of(p, b), c = chunks_of(p, n).n;
-        if (blockIdx.x == 0 && n != p.lengths[b]) atomicExch(p.status, kStatusInvalid);
-        sum[0] += c;
-        sum[1] += (c + kBlockChunks - 1) / kBlockChunks;
-        sum[2] += (c + kSuperChunks - 1) / kSuperChunks;
+    int first_chunks = 0;            // of sequence `thread`
+    for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + lane;
+        unsigned c = 0;              // less than 2^23: a warp's sum fits
+        if (b < p.B) {
+            const int n = tokens_of(p, b);
+            c = chunks_of(p, n).n;
+            if (blockIdx.x == 0 && n != p.lengths[b]) atomicExch(p.status, kStatusInvalid);
+        }
+        if (b0 == warp * 32) first_chunks = c;
+        sum[0] += __reduce_add_sync(kWarp, c);
+        sum[1] += __reduce_add_sync(kWarp, (c + kBlockChunks - 1) / kBlockChunks);
+        sum[2] += __reduce_add_sync(kWarp, (c + kSuperChunks - 1) / kSuperChunks);
     }
-    if (thread < 3) S.total[thread] = 0;
+    if (warp < warps && lane < 3) S.sums_of[lane][warp] = lane == 0 ? sum[0] : lane == 1 ? sum[1] : sum[2];
     __syncthreads();
+    long long total[3] = {0, 0, 0};
+    for (int w = 0; w < warps; ++w)
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(kWarp, sum[i], o);
-        if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(&S.total[i]), static_cast<unsigned long long>(sum[i]));
-    }
-    __syncthreads();
-    const long long enough = static_cast<long long>(kUnitsEach) * gridDim.x;
-    const int level = S.total[2] * lists >= enough ? 2 : S.total[1] * lists >= enough ? 1 : 0;
+        for (int i = 0; i < 3; ++i) total[i] += S.sums_of[i][w];
+    const long long enough = static_cast<long long>(kUnitsEach) * ctas;
+    const int level = total[2] * lists >= enough ? 2 : total[1] * lists >= enough ? 1 : 0;
     const int unit = level == 2 ? kSuperChunks : level == 1 ? kBlockChunks : 1;
-    const long long units = S.total[level] * lists;
-    const long long first = units * blockIdx.x / gridDim.x, last = units * (blockIdx.x + 1) / gridDim.x;
+    const long long units = (level == 2 ? total[2] : level == 1 ? total[1] : total[0]) * lists;
+    // Run i of the CTAs' is [units * i / ctas, units * (i + 1) / ctas).
+    const long long each = quotient(units, ctas);
+    const unsigned rest = static_cast<unsigned>(units - each * ctas);
+    auto begin = [&](unsigned i) { return each * i + rest * i / ctas; };
+    const long long first = begin(blockIdx.x), last = begin(blockIdx.x + 1);
     if (thread == 0) {
         S.first = first;
         S.last = last;
         S.unit = unit;
         S.start = 0;
-        S.start_units = 0;
+        if (first >= units) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, unit};
     }
     long long carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    for (int b0 = 0; b0 < p.B && carry <= first; b0 += kThreads) {
         const int b = b0 + thread;
-        const long long mine = b < p.B ? (chunks_of(p, tokens_of(p, b)).n + unit - 1) / unit * lists : 0;
-        long long up = mine;
+        const int n = b >= p.B ? 0 : ((b0 ? chunks_of(p, tokens_of(p, b)).n : first_chunks) + unit - 1) / unit;
+        unsigned up = n;
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(kWarp, up, o);
+            const unsigned x = __shfl_up_sync(kWarp, up, o);
             if (lane >= o) up += x;
         }
-        __syncthreads();
+        if (b0) __syncthreads();
         if (lane == 31) S.scan[warp] = up;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) up += S.scan[w];
-        up += carry;
-        const long long before = up - mine;
-        if (mine > 0 && first >= before && first < up) {
-            S.start = b;
-            S.start_units = before;
+        long long before = carry + static_cast<long long>(up - n) * lists;
+        for (int w = 0; w < warps; ++w) {
+            const long long x = static_cast<long long>(S.scan[w]) * lists;
+            if (w < warp) before += x;
+            carry += x;
         }
-        for (int w = 0; w < kThreads / 32; ++w) carry += S.scan[w];
-    }
-    __syncthreads();
-    if (thread == 0) {
-        Cut cut{0, 0, 0, 0, unit};
-        if (first < units) {
-            const int n = (chunks_of(p, tokens_of(p, S.start)).n + unit - 1) / unit;
-            const long long list = (first - S.start_units) / n, lo = S.start_units + list * n;
+        if (first < units && first >= before && first < before + static_cast<long long>(n) * lists) {
+            const long long list = quotient(first - before, n), lo = before + list * n;
+            S.start = b;
             S.start_list = static_cast<int>(list);
             S.start_unit = static_cast<int>(first - lo);
             S.list_unit = lo;
             // The cut at the run's begin, for the second launch: the list that it goes through, if it is the first inside.
-            if (blockIdx.x > 0 && first > lo && units * (blockIdx.x - 1) / gridDim.x <= lo) cut = Cut{lo, n, S.start, static_cast<int>(list), unit};
+            const bool cut = blockIdx.x > 0 && first > lo && begin(blockIdx.x - 1) <= lo;
+            p.cuts[blockIdx.x] = cut ? Cut{lo, n, b, static_cast<int>(list), unit} : Cut{0, 0, 0, 0, unit};
         }
-        p.cuts[blockIdx.x] = cut;
     }
 }
 
@@ -843,6 +852,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     wait_for_last();
+    if (warp == 14) {
+        // The look-ups come after the lengths: the table's lines (of small ones all, else the first) are on their way to L2 by then.
+        const int lines = (p.max_pages + 31) / 32, i = blockIdx.x * 32 + lane;
+        if (lines > 0 && i / lines < p.B) prefetch_l2(p.table + i / lines * p.ldt + i % lines * 32);
+    }
     plan(p, S);
     tc_fence_before();
     __syncthreads();
@@ -899,7 +913,7 @@ __device__ __forceinline__ void join(State &a, const State &b, bool first)
 __global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const DecodeParams p)
 {
     wait_for_last();
-    __shared__ State at_super[kJoinGroups][128];
+    __shared__ State at[kSuperChunks / kBlockChunks][128];
     const Cut cut = p.cuts[blockIdx.x + 1];
     const int n = cut.n, unit = cut.unit, h = blockIdx.y;
     if (n == 0) return;
@@ -914,32 +928,49 @@ __global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const Deco
     };
     const int per_block = max(1, kBlockChunks / unit), per_super = kSuperChunks / unit, supers = (n + per_super - 1) / per_super;
     State all{};
-    for (int s0 = 0; s0 < supers; s0 += kJoinGroups) {
-        const int s = s0 + group;
-        if (s < supers) {
-            State super{}, block{};
-            const int end = min(n, (s + 1) * per_super);
-            int i = s * per_super;
-            // Eight loads in flight.
-            while (i < end) {
-                State x[8];
-                const int count = min(8, end - i);
+    if (supers == 1) {
+        // Warpgroups take its blocks.
+        const int blocks = (n + per_block - 1) / per_block;
+        for (int i = group; i < blocks; i += kJoinGroups) {
+            State x[kBlockChunks], block{};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = load(min(i + k, end - 1));
+            for (int k = 0; k < kBlockChunks; ++k) x[k] = load(min(i * per_block + min(k, per_block - 1), n - 1));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k >= count) break;
-                    join(block, x[k], (i + k) % per_block == 0);
-                    if ((i + k + 1) % per_block == 0 || i + k + 1 == end) join(super, block, (i + k) / per_block * per_block == s * per_super);
-                }
-                i += count;
-            }
-            at_super[group][d] = super;
+            for (int k = 0; k < kBlockChunks; ++k)
+                if (k < per_block && i * per_block + k < n) join(block, x[k], k == 0);
+            at[i][d] = block;
         }
         __syncthreads();
         if (group == 0)
-            for (int k = 0; k < kJoinGroups && s0 + k < supers; ++k) join(all, at_super[k][d], s0 + k == 0);
-        __syncthreads();
+            for (int i = 0; i < blocks; ++i) join(all, at[i][d], i == 0);
+    } else {
+        for (int s0 = 0; s0 < supers; s0 += kJoinGroups) {
+            const int s = s0 + group;
+            if (s < supers) {
+                State super{}, block{};
+                const int end = min(n, (s + 1) * per_super);
+                int i = s * per_super;
+                // Eight loads in flight.
+                while (i < end) {
+                    State x[8];
+                    const int count = min(8, end - i);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = load(min(i + k, end - 1));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= count) break;
+                        join(block, x[k], (i + k) % per_block == 0);
+                        if ((i + k + 1) % per_block == 0 || i + k + 1 == end) join(super, block, (i + k) / per_block * per_block == s * per_super);
+                    }
+                    i += count;
+                }
+                at[group][d] = super;
+            }
+            __syncthreads();
+            if (group == 0)
+                for (int k = 0; k < kJoinGroups && s0 + k < supers; ++k) join(all, at[k][d], s0 + k == 0);
+            __syncthreads();
+        }
     }
     if (group == 0 && d < p.D) {
         const float y = weighted(all.o, all.l);
