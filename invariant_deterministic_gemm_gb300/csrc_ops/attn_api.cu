@@ -157,7 +157,9 @@ DecodeSpace decode_space(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t to
     return s;
 }
 
-// A cache as (column, head, token of a page, page), copied in boxes of 64 columns of one head and `box` tokens of a page.
+// A cache as (column, head, token of a page, page), copied in boxes of 64 columns of one head and `box` tokens of a page. Where
+// a head's row is 128 bytes, no more than that is fetched (256, with the next head's: 69.8 instead of 67.7 us for 96 windows of
+// 1024 in eight heads of 64; rows of 256 bytes by 128: 222 instead of 218 us for 64 contexts up to 8192).
 bool encode(CUtensorMap *m, const void *p, int64_t pages, int64_t size, int64_t KV, int64_t D, int64_t page, int64_t s, int64_t h, int box)
 {
     std::memset(m, 0, sizeof *m);
@@ -167,7 +169,7 @@ bool encode(CUtensorMap *m, const void *p, int64_t pages, int64_t size, int64_t 
                              static_cast<cuuint64_t>(pages > 1 ? page : D) * 2};
     cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, es[4] = {1, 1, 1, 1};
     return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, boxes, es,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, D <= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

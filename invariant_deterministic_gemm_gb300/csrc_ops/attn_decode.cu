@@ -890,8 +890,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
 
 // ------------------------------------------- joining what was cut
 //
-// One block a CTA whose run begins inside a list (a sequence, KV head and part), the first of those, and query head: the
-// list's units are joined. Threads of a warpgroup are the columns, warpgroups take super blocks.
+// For each CTA whose run begins inside a list (a sequence, KV head and part), the first of those: the list's units are joined.
+// Threads of a warpgroup are the columns. Where no list is longer than a super block, a warpgroup is a query head (blocks of
+// the grid: eight heads), or if there is one head a block of the list in turn; else a warpgroup is a super block in turn, and
+// each head has blocks of its own. (With a block of the grid for each head throughout, 96 windows of 1024 took 20 us to join.)
 
 constexpr int kJoinGroups = 8;
 
@@ -910,16 +912,17 @@ __device__ __forceinline__ void join(State &a, const State &b, bool first)
     a.m = f.m;
 }
 
-__global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const DecodeParams p, const bool short_lists)
 {
     wait_for_last();
     __shared__ State at[kSuperChunks / kBlockChunks][128];
     const Cut cut = p.cuts[blockIdx.x + 1];
-    const int n = cut.n, unit = cut.unit, h = blockIdx.y;
+    const int group = threadIdx.x >> 7, d = threadIdx.x & 127, column = min(d, p.D - 1);
+    const bool by_head = short_lists && p.heads > 1;
+    const int n = cut.n, unit = cut.unit, h = by_head ? blockIdx.y * kJoinGroups + group : blockIdx.y;
     if (n == 0) return;
     const int kv = cut.list / p.parts, part = cut.list % p.parts, heads = min(p.heads, p.G - part * p.heads);
-    if (h >= heads) return;
-    const int group = threadIdx.x >> 7, d = threadIdx.x & 127, column = min(d, p.D - 1);
+    if (h >= heads) return;          // (whole blocks, or groups that none waits for)
     const long long pitch = static_cast<long long>(p.heads) * (p.D + 2);
     const float *mine = p.partials + cut.first * pitch;
     auto load = [&](int i) {
@@ -927,9 +930,30 @@ __global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const Deco
         return State{x[h * p.D + column], x[p.heads * p.D + h], x[p.heads * (p.D + 1) + h]};
     };
     const int per_block = max(1, kBlockChunks / unit), per_super = kSuperChunks / unit, supers = (n + per_super - 1) / per_super;
+    // Super block s, eight loads in flight.
+    auto super_block = [&](int s) {
+        State super{}, block{};
+        const int end = min(n, (s + 1) * per_super);
+        int i = s * per_super;
+        while (i < end) {
+            State x[8];
+            const int count = min(8, end - i);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = load(min(i + k, end - 1));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k >= count) break;
+                join(block, x[k], (i + k) % per_block == 0);
+                if ((i + k + 1) % per_block == 0 || i + k + 1 == end) join(super, block, (i + k) / per_block * per_block == s * per_super);
+            }
+            i += count;
+        }
+        return super;
+    };
     State all{};
-    if (supers == 1) {
-        // Warpgroups take its blocks.
+    if (by_head) {
+        all = super_block(0);
+    } else if (short_lists) {
         const int blocks = (n + per_block - 1) / per_block;
         for (int i = group; i < blocks; i += kJoinGroups) {
             State x[kBlockChunks], block{};
@@ -945,34 +969,14 @@ __global__ void __launch_bounds__(128 * kJoinGroups) attn_join_kernel(const Deco
             for (int i = 0; i < blocks; ++i) join(all, at[i][d], i == 0);
     } else {
         for (int s0 = 0; s0 < supers; s0 += kJoinGroups) {
-            const int s = s0 + group;
-            if (s < supers) {
-                State super{}, block{};
-                const int end = min(n, (s + 1) * per_super);
-                int i = s * per_super;
-                // Eight loads in flight.
-                while (i < end) {
-                    State x[8];
-                    const int count = min(8, end - i);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = load(min(i + k, end - 1));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (k >= count) break;
-                        join(block, x[k], (i + k) % per_block == 0);
-                        if ((i + k + 1) % per_block == 0 || i + k + 1 == end) join(super, block, (i + k) / per_block * per_block == s * per_super);
-                    }
-                    i += count;
-                }
-                at[group][d] = super;
-            }
+            if (s0 + group < supers) at[group][d] = super_block(s0 + group);
             __syncthreads();
             if (group == 0)
                 for (int k = 0; k < kJoinGroups && s0 + k < supers; ++k) join(all, at[k][d], s0 + k == 0);
             __syncthreads();
         }
     }
-    if (group == 0 && d < p.D) {
+    if ((by_head || group == 0) && d < p.D) {
         const float y = weighted(all.o, all.l);
         p.out.row(cut.b, kv * p.G + part * p.heads + h)[d] = static_cast<uint16_t>(pack_bf16(y, 0.0f));
     }
@@ -995,8 +999,12 @@ cudaError_t run(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStr
     if (e != cudaSuccess) return e;
     e = launch_early(fn, ctas, kThreads, C::SMEM, 1, s, p, maps);
     if (e != cudaSuccess || ctas < 2) return e;
+    // The chunks of the longest list: the cache's, or its first and the window's.
+    const long long room = (static_cast<long long>(p.max_pages) * p.page_size + kChunk - 1) / kChunk;
+    const long long kept = (static_cast<long long>(p.sinks) + kChunk - 1) / kChunk + (static_cast<long long>(p.window) - 1) / kChunk + 2;
+    const bool short_lists = std::min(room, kept) <= kSuperChunks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(p.heads));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(short_lists ? (p.heads + kJoinGroups - 1) / kJoinGroups : p.heads));
     cfg.blockDim = dim3(128 * kJoinGroups);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1004,7 +1012,7 @@ cudaError_t run(const DecodeParams &p, const DecodeMaps &maps, int ctas, cudaStr
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel, p, short_lists);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
