@@ -140,26 +140,30 @@ struct Walk {
     int b, list, u0, unit, units, tokens;
     Chunks chunks;
     __device__ Walk(const DecodeParams &p, const Shared &S)
-        : p(p), left(S.last - S.first), unit0(S.list_unit), b(S.start - 1), list(p.KV * p.parts), u0(S.start_unit), unit(S.unit), units(0), tokens(0), chunks{0, 0, 0}
+        : p(p), left(S.last - S.first), unit0(S.list_unit), b(S.start - 1), list(S.start_list), u0(S.start_unit), unit(S.unit), units(0), tokens(0), chunks{0, 0, 0}
     {
-        if (left <= 0) return;
-        sequence();
-        list = S.start_list;
+        if (left > 0) sequence();
     }
     // The next sequence with something to see.
     __device__ void sequence()
     {
         do {
-            tokens = tokens_of(p, ++b);
+            if (++b == p.B) {
+                b = 0;
+                ++list;
+            }
+            tokens = tokens_of(p, b);
             chunks = chunks_of(p, tokens);
         } while (chunks.n == 0);
         units = (chunks.n + unit - 1) / unit;
-        list = 0;
     }
     __device__ bool next(Segment &s)
     {
         if (left <= 0) return false;
-        if (list == p.KV * p.parts) sequence();
+        if (u0 == units) {
+            sequence();
+            u0 = 0;
+        }
         const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + left));
         s.b = b;
         s.kv = p.parts == 1 ? list : list / p.parts;
@@ -172,8 +176,7 @@ struct Walk {
         s.whole = u0 == 0 && u1 == units;
         left -= u1 - u0;
         unit0 += units;
-        u0 = 0;
-        ++list;
+        u0 = units;
         return true;
     }
 };
@@ -185,15 +188,17 @@ __device__ __forceinline__ unsigned tiles_of(const DecodeParams &p, int n, int c
     return (sees_some(p, n, a, kTile) ? 1u : 0u) | (sees_some(p, n, a + kTile, kTile) ? 2u : 0u);
 }
 
-// The CTA's run: how many units there are, of which size, and where its part begins. All threads.
-__device__ __forceinline__ long long quotient(long long x, unsigned y)
+__device__ __forceinline__ long long quotient(long long x, long long y)
 {
-    return x >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / y);
+    return (x | y) >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
 }
+// The CTA's run: how many units there are, of which size, and where its part begins. All threads. Units are numbered KV head
+// by KV head, so that CTAs that go through different heads of a sequence, whose rows lie side by side, do it about the same time
+// (sequence by sequence: 218.6 instead of 212.9 us for 64 contexts up to 8192, 266 instead of 258 for two of 262,144).
 __device__ void plan(const DecodeParams &p, Shared &S)
 {
     const int thread = threadIdx.x, warp = thread >> 5, lane = thread & 31, warps = min(kThreads / 32, (p.B + 31) / 32);
-    const unsigned lists = p.KV * p.parts, ctas = gridDim.x;
+    const unsigned heads = p.KV * p.parts, ctas = gridDim.x;
     long long sum[3] = {0, 0, 0};
     int first_chunks = 0;            // of sequence `thread`
     for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) {
@@ -216,23 +221,23 @@ __device__ void plan(const DecodeParams &p, Shared &S)
 #pragma unroll
         for (int i = 0; i < 3; ++i) total[i] += S.sums_of[i][w];
     const long long enough = static_cast<long long>(kUnitsEach) * ctas;
-    const int level = total[2] * lists >= enough ? 2 : total[1] * lists >= enough ? 1 : 0;
+    const int level = total[2] * heads >= enough ? 2 : total[1] * heads >= enough ? 1 : 0;
     const int unit = level == 2 ? kSuperChunks : level == 1 ? kBlockChunks : 1;
-    const long long units = (level == 2 ? total[2] : level == 1 ? total[1] : total[0]) * lists;
+    const long long round = level == 2 ? total[2] : level == 1 ? total[1] : total[0], units = round * heads;
     // Run i of the CTAs' is [units * i / ctas, units * (i + 1) / ctas).
     const long long each = quotient(units, ctas);
     const unsigned rest = static_cast<unsigned>(units - each * ctas);
     auto begin = [&](unsigned i) { return each * i + rest * i / ctas; };
     const long long first = begin(blockIdx.x), last = begin(blockIdx.x + 1);
+    const long long list = first < units ? quotient(first, round) : 0, place = first - list * round;
     if (thread == 0) {
         S.first = first;
         S.last = last;
         S.unit = unit;
-        S.start = 0;
-        if (first >= units) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, unit};
+        if (first == units) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, unit};
     }
     long long carry = 0;
-    for (int b0 = 0; b0 < p.B && carry <= first; b0 += kThreads) {
+    for (int b0 = 0; b0 < p.B && carry <= place; b0 += kThreads) {
         const int b = b0 + thread;
         const int n = b >= p.B ? 0 : ((b0 ? chunks_of(p, tokens_of(p, b)).n : first_chunks) + unit - 1) / unit;
         unsigned up = n;
@@ -243,17 +248,17 @@ __device__ void plan(const DecodeParams &p, Shared &S)
         if (b0) __syncthreads();
         if (lane == 31) S.scan[warp] = up;
         __syncthreads();
-        long long before = carry + static_cast<long long>(up - n) * lists;
+        long long before = carry + up - n;
         for (int w = 0; w < warps; ++w) {
-            const long long x = static_cast<long long>(S.scan[w]) * lists;
+            const unsigned x = S.scan[w];
             if (w < warp) before += x;
             carry += x;
         }
-        if (first < units && first >= before && first < before + static_cast<long long>(n) * lists) {
-            const long long list = quotient(first - before, n), lo = before + list * n;
+        if (first < units && place >= before && place < before + n) {
+            const long long lo = list * round + before;
             S.start = b;
             S.start_list = static_cast<int>(list);
-            S.start_unit = static_cast<int>(first - lo);
+            S.start_unit = static_cast<int>(place - before);
             S.list_unit = lo;
             // The cut at the run's begin, for the second launch: the list that it goes through, if it is the first inside.
             const bool cut = blockIdx.x > 0 && first > lo && begin(blockIdx.x - 1) <= lo;
@@ -880,6 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                     for (int i = lane * 8; i < p.H * p.D; i += 256) *reinterpret_cast<uint4 *>(p.out.row(b, i / p.D) + i % p.D) = make_uint4(0, 0, 0, 0);
         }
     }
+    // (Every CTA: the next launch may be the join, which waits for all of this one at its start in any case.)
     let_next_begin();
     __syncwarp();
     tc_fence_before();
