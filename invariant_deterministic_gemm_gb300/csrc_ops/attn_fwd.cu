@@ -392,7 +392,10 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
                         s[x >> 1][16 * (x & 1) + j] = pack_bf16(lo, hi);
                     }
                 }
-                if (x == 1) { tmem_st32(ts, s[0]); arrive(0); }
+                if (x == 1) {
+                    tmem_st32(ts, s[0]);
+                    arrive(0);
+                }
                 if (x == 3) tmem_st32(ts + 32, s[1]);
             }
             float lo, hi;

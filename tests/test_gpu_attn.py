@@ -286,3 +286,78 @@ def test_empty_calls():
     out, lse = dg.det_attn(q, k[:5], v[:5], none)                      # no sequences: rows of nobody
     assert not out.any() and (lse == -INF).all()
     assert dg.det_gemm_check() == 0
+
+
+# The first keys' gradients are those of every query, in pieces of 512 queries (of up to 512 such keys); beyond that in one.
+@pytest.mark.parametrize("sinks,window,lengths", [(5, 200, (1300, 700)), (130, 100, (1100,)), (600, 64, (1000, 3, 530)), (512, 1, (1025,))])
+def test_first_keys_over_several_pieces_of_queries(sinks, window, lengths):
+    n = sum(lengths)
+    q, k, v = make(n, n, 4, 2, 64, 31)
+    check_all(q, k, v, bounds(*lengths), window=window, sinks=sinks)
+
+
+def test_first_keys_of_chunks_of_queries():
+    q, k, v = make(1200, 2100, 2, 1, 72, 32)
+    check_all(q, k, v, bounds(700, 500), bounds(900, 1200), window=90, sinks=5)
+
+
+@pytest.mark.parametrize("kw", [dict(window=70, sinks=140), dict()])
+def test_the_bits_of_long_sequences_do_not_depend_on_their_batch(kw):
+    lengths = (1300, 40, 1030)
+    n = sum(lengths)
+    q, k, v = make(n, n, 4, 2, 128, 33)
+    dout, b = randn(8, n, 4, 128), bounds(*lengths)
+    out, lse = dg.det_attn(q, k, v, b, **kw)
+    g = dg.det_attn_bwd(dout, q, k, v, out, lse, b, **kw)
+    a = 0
+    for m in lengths:
+        s = slice(a, a + m)
+        o1, l1 = dg.det_attn(q[s], k[s], v[s], **kw)
+        g1 = dg.det_attn_bwd(dout[s], q[s], k[s], v[s], o1, l1, **kw)
+        assert torch.equal(out[s], o1) and torch.equal(lse[:, s], l1)
+        assert all(torch.equal(x[s], y) for x, y in zip(g, g1))
+        a += m
+
+
+def test_two_streams_at_once():
+    sets = [make(900, 900, 8, 2, 128, s) + (randn(s, 900, 8, 128),) for s in (41, 42)]
+    kw = dict(window=200, sinks=3)
+
+    def step(x, stream=None):
+        q, k, v, dout = x
+        out, lse = dg.det_attn(q, k, v, stream=stream, **kw)
+        return (out, lse) + dg.det_attn_bwd(dout, q, k, v, out, lse, stream=stream, **kw)
+
+    want = [step(x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(step(sets[i], s))
+    torch.cuda.synchronize()
+    assert dg.det_gemm_check() == 0
+    for w, g in zip(want, got):
+        for one in g:
+            assert all(torch.equal(x, y) for x, y in zip(w, one))
+
+
+def test_a_timeout_is_reported_and_the_context_stays_usable():
+    q, k, v = make(300, 300, 4, 2, 64, 51)
+    dout = randn(52, 300, 4, 64)
+    kw = dict(window=50, sinks=2)
+    out, lse = dg.det_attn(q, k, v, **kw)
+    g = dg.det_attn_bwd(dout, q, k, v, out, lse, **kw)
+    assert dg.det_gemm_check() == 0
+    dg.det_ops_debug_force_timeout(True)
+    try:
+        dg.det_attn(q, k, v, **kw)
+        assert dg.det_gemm_check() == 6
+        dg.det_attn_bwd(dout, q, k, v, out, lse, **kw)
+        assert dg.det_gemm_check() == 6
+    finally:
+        dg.det_ops_debug_force_timeout(False)
+    o2, l2 = dg.det_attn(q, k, v, **kw)
+    g2 = dg.det_attn_bwd(dout, q, k, v, o2, l2, **kw)
+    assert dg.det_gemm_check() == 0
+    assert torch.equal(out, o2) and torch.equal(lse, l2) and all(torch.equal(x, y) for x, y in zip(g, g2))

@@ -190,3 +190,66 @@ def test_empty():
     assert dg.det_attn_decode(q[:0], kc, vc, table[:0], n[:0]).shape == (0, 4, 64)
     out = dg.det_attn_decode(q, kc[:0], vc[:0], table[:, :0], torch.zeros_like(n))
     assert not out.any() and dg.det_gemm_check() == 0
+
+
+def pages_of(lengths, H, KV, D, page, seed):
+    """Like build(), for long caches: drawn on the device, every page of the table a page of its own."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    held = [-(-n // page) for n in lengths]
+    perm = torch.randperm(sum(held), generator=g, device="cuda").to(I32)
+    table = torch.full((len(lengths), max(held)), -1, dtype=I32, device="cuda")
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = perm[at:at + h]
+        at += h
+    kc, vc = (torch.randn((sum(held), page, KV, D), generator=g, device="cuda", dtype=torch.float32).to(BF16) for _ in range(2))
+    q = torch.randn((len(lengths), H, D), generator=g, device="cuda").to(BF16)
+    return q, kc, vc, table, torch.tensor(lengths, dtype=I32).cuda()
+
+
+# Runs of the CTAs that are cut at any chunk, at every fourth, and at every 64th: the work decides, the bits do not tell.
+@pytest.mark.parametrize("lengths", [[20000, 700], [45000, 41000, 20000, 1], [20000] + [256] * 80 + [17000]])
+@pytest.mark.parametrize("H,KV,D", [(8, 8, 64), (24, 8, 128)])
+def test_the_cuts_between_ctas_do_not_show(lengths, H, KV, D):
+    q, kc, vc, table, n = pages_of(lengths, H, KV, D, 32, 5)
+    out = dg.det_attn_decode(q, kc, vc, table, n)
+    assert dg.det_gemm_check() == 0
+    for b in (0, 1, len(lengths) - 1):
+        one = dg.det_attn_decode(q[b:b + 1], kc, vc, table[b:b + 1], n[b:b + 1].clone())
+        assert torch.equal(one[0], out[b])
+        ids = table[b, :-(-lengths[b] // 32)].long()
+        k, v = (x[ids].flatten(0, 1)[:lengths[b]] for x in (kc, vc))
+        want, _, tol, _ = ref.attention(q[b:b + 1], k, v)
+        ref.assert_within(out[b:b + 1], want, tol, "sequence %d" % b)
+
+
+@pytest.mark.parametrize("H,KV", [(1, 1), (3, 3), (15, 5), (40, 1), (64, 1), (35, 7)])
+@pytest.mark.parametrize("D", [40, 64, 120])
+def test_odd_numbers_of_heads(H, KV, D):
+    check_all([700, 0, 33, 1600], H, KV, D, 16)
+
+
+def test_two_streams_at_once():
+    sets = [pages_of([3000, 500, 9000, 1], 16, 4, 128, 16, s) for s in (1, 2)]
+    want = [dg.det_attn_decode(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[dg.det_attn_decode(*s, stream=st) for s, st in zip(sets, streams)] for _ in range(8)]
+    torch.cuda.synchronize()
+    assert dg.det_gemm_check() == 0
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
+
+
+def test_a_timeout_is_reported_and_the_context_stays_usable():
+    q, kc, vc, table, n, _ = build([700, 30, 2000], 8, 2, 64, 16)
+    want = dg.det_attn_decode(q, kc, vc, table, n)
+    assert dg.det_gemm_check() == 0
+    dg.det_ops_debug_force_timeout(True)
+    try:
+        dg.det_attn_decode(q, kc, vc, table, n)
+        assert dg.det_gemm_check() == 6
+    finally:
+        dg.det_ops_debug_force_timeout(False)
+    assert torch.equal(dg.det_attn_decode(q, kc, vc, table, n), want)
+    assert dg.det_gemm_check() == 0
