@@ -25,6 +25,11 @@
 //   warps 12, 14     copies of keys and of values
 //   warp 13          issues the products
 //   warp 15          looks up the pages, some chunks ahead; sequences without tokens
+// 64 contexts up to 8192 (32 heads of 128 on 8) 211 us, 6.3 TB/s; two of 262,144
+// 257 us; one of 1021 12.8 us, of which three trips to memory in a row (lengths, page
+// table, keys) are half; 96 windows of 1024 in eight heads of 64 67.7 us, where
+// three chunks in flight are what bounds.
+//
 // A chunk's way through one warpgroup is latency (barriers, TMEM, the maximum
 // over 256 tokens), about as long as its bytes take, so two take turns. P is
 // rounded to BF16 beside BF16 values, and the sum is that of the rounded ones:

@@ -11,7 +11,14 @@
 //   warp 8           copies (TMA): both query tiles, then key and value blocks
 //                    through a ring of tiles
 //   warp 9           issues the products from one thread: P V of a tile, then its
-//                    next scores, while the other tile's softmax runs
+//                    next scores, while the other tile's softmax runs (the
+//                    scores land where that P lies: one thread's products run
+//                    in the order of their issue)
+// Bound by a tile's chain: scores 512 cycles, the softmax, P V 512; two chains are
+// what TMEM holds. A block takes both tiles about 3300 cycles, its products 2048.
+// Prompts of 2048 queries over up to 8192 keys (32 heads of 128 on 8) 88.5 us, 0.50
+// of the measured BF16 rate by visible pairs; 16384 tokens, window 1024, 16 heads
+// 181 us. P through shared memory 98 where 94, half blocks 113, two threads a row 136.
 // P is rounded to BF16, as the tensor core wants it beside BF16 values; the sum
 // takes the unrounded ones.
 //

@@ -8,8 +8,8 @@
 // thread takes an item, 16 bytes of a row, or 32 where a pair's columns lie apart
 // (two times 8 or 16), with the pairs' table values; the token, head and place
 // come from its number by multiplications. What keeps bytes under way is threads:
-// two items each take a prompt from 40 to 46 us, four to 52. Appending 8192
-// tokens (32 + 8 + 8 heads of 128): 40 us, 5.2 TB/s; turning 4099 tokens of 12
+// two items each took a prompt from 40 to 46 us, four to 52. Appending 8192
+// tokens (32 + 8 + 8 heads of 128): 36 us, 5.7 TB/s; turning 4099 tokens of 12
 // heads of 80: 4.0 us, 3.9 TB/s.
 #include "attn_internal.h"
 #include "launch.cuh"
