@@ -64,7 +64,9 @@ det_gemm_status det_rope(const det_gemm_bf16 *x, const float *cosine, const floa
  * turned goes to q_out. Slot -1 stores nothing. A slot outside the cache, or a
  * token whose position is outside the tables, stores nothing and is reported.
  * Slots other than -1 are distinct: of a slot that occurs twice the row holds
- * parts of either token. Caches have strides for page, token and head.
+ * parts of either token. Caches have strides for page, token and head, and
+ * may lie between one another (a buffer whose pages, tokens or heads hold
+ * keys and then values).
  */
 det_gemm_status det_kv_append(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const det_gemm_bf16 *v, const float *cosine,
                               const float *sine, const int32_t *positions, const int32_t *slots, det_gemm_bf16 *q_out,

@@ -60,6 +60,29 @@ Range range(const Arr &a)
 }
 bool overlap(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi; }
 
+// Whether two arrays of one shape and layout lie between one another, as keys and values do that share each page, token or head of
+// a buffer: b begins in a place that an axis of a leaves free.
+bool interleaved(const Strided &a, const Strided &b)
+{
+    if (a.D != b.D || !std::equal(a.n, a.n + 3, b.n) || !std::equal(a.stride, a.stride + 3, b.stride)) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    int64_t off = static_cast<int64_t>((x < y ? y - x : x - y) / 2), span = a.D, inner[3];
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int i, int j) { return a.stride[i] < a.stride[j]; });
+    for (int i : order) {
+        inner[i] = span;
+        if (a.n[i] > 1) span += (a.n[i] - 1) * a.stride[i];
+    }
+    for (int k = 2; k >= 0; --k) {
+        const int i = order[k];
+        if (a.n[i] == 1) continue;
+        off %= a.stride[i];
+        if (off + inner[i] > a.stride[i]) return false;
+        if (off >= inner[i]) return true;
+    }
+    return false;
+}
+
 // All arrays well formed, and no output overlapping an input or another output.
 det_gemm_status check_all(std::initializer_list<Strided> in, std::initializer_list<Arr> flat_in, std::initializer_list<Strided> out,
                           std::initializer_list<Arr> flat_out)
@@ -87,7 +110,8 @@ det_gemm_status check_all(std::initializer_list<Strided> in, std::initializer_li
         for (int i = 0; i < ni; ++i)
             if (overlap(outs[o], ins[i])) return DET_GEMM_ERR_INVALID_ARG;
         for (int i = 0; i < o; ++i)
-            if (overlap(outs[o], outs[i])) return DET_GEMM_ERR_INVALID_ARG;
+            if (overlap(outs[o], outs[i]) && !(o < static_cast<int>(out.size()) && interleaved(out.begin()[o], out.begin()[i])))
+                return DET_GEMM_ERR_INVALID_ARG;
     }
     return DET_GEMM_OK;
 }
@@ -127,7 +151,6 @@ det_gemm_status no_map()
 bool ok_turn(int64_t T, int64_t heads, int64_t D, int64_t rot, int64_t P)
 {
     if (!launchable(T * heads / 2 + 1)) return false;
-
     return D >= 8 && D <= DET_ATTN_MAX_HEAD_DIM && D % 8 == 0 && rot >= 2 && rot <= D && rot % 2 == 0 && ok_size(P);
 }
 
@@ -261,7 +284,7 @@ det_gemm_status det_kv_append(const det_gemm_bf16 *q, const det_gemm_bf16 *k, co
 
 int64_t det_attn_decode_workspace(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t max_tokens)
 {
-    if (!ok_size(B) || !ok_heads(H, KV, D) || !ok_size(max_tokens)) return 0;
+    if (!ok_size(B) || !ok_heads(H, KV, D) || !ok_size(B * H) || !ok_size(max_tokens)) return 0;
     return decode_space(B, H, KV, D, max_tokens).total;
 }
 
@@ -272,7 +295,7 @@ det_gemm_status det_attn_decode(const det_gemm_bf16 *q, const det_gemm_bf16 *k_c
                                 int64_t kch, int64_t vcp, int64_t vcs, int64_t vch, int64_t ldt, int64_t ot, int64_t oh,
                                 void *workspace, int64_t workspace_bytes, det_gemm_stream stream)
 {
-    if (!ok_size(B) || !ok_heads(H, KV, D) || H / KV > DET_ATTN_MAX_SHARED || !ok_size(pages) || page_size < 8 ||
+    if (!ok_size(B) || !ok_heads(H, KV, D) || !ok_size(B * H) || H / KV > DET_ATTN_MAX_SHARED || !ok_size(pages) || page_size < 8 ||
         page_size % 8 != 0 || !ok_size(page_size) || !ok_size(pages * page_size) || !ok_size(max_pages) ||
         !ok_size(max_pages * page_size) || !ok_mask(scale, window, sinks))
         return DET_GEMM_ERR_INVALID_ARG;

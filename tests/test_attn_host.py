@@ -153,3 +153,23 @@ def test_tensors_of_different_devices_are_refused(dg):
             with pytest.raises(ValueError, match="different devices: cuda:[01] and cuda:[01]"):
                 f()
                 pytest.fail("call %d was not refused" % n)
+
+
+# Keys and values in one buffer: [pages, 2, size, KV, D], [pages, size, 2, KV, D], [pages, size, KV, 2, D].
+BETWEEN = [(2048, dict(kcp=2048, vcp=2048)), (256, dict(kcp=2048, vcp=2048, kcs=256, vcs=256)),
+           (128, dict(kcp=2048, vcp=2048, kcs=256, vcs=256, kch=128, vch=128))]
+
+
+@pytest.mark.parametrize("at,strides", BETWEEN)
+@pytest.mark.parametrize("first", ["k_cache", "v_cache"])
+def test_caches_that_lie_between_one_another(call, at, strides, first):
+    second = "v_cache" if first == "k_cache" else "k_cache"
+    if not torch.cuda.is_available():
+        assert call("det_kv_append", **{first: A[8], second: A[8] + at}, **strides) == NO_DEVICE
+    for off in (0, at // 2, at + 16, 2 * at + 64):
+        assert call("det_kv_append", **{first: A[8], second: A[8] + off}, **strides) in (INVALID, ALIGN), off
+
+
+def test_rows_times_heads_below_two_to_the_31(call):
+    assert call("det_attn_decode", B=1 << 21, H=1024, KV=1024) == INVALID
+    assert call("det_attn_decode_workspace", B=1 << 21, H=1024, KV=1024) == 0

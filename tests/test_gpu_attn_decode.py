@@ -253,3 +253,22 @@ def test_a_timeout_is_reported_and_the_context_stays_usable():
         dg.det_ops_debug_force_timeout(False)
     assert torch.equal(dg.det_attn_decode(q, kc, vc, table, n), want)
     assert dg.det_gemm_check() == 0
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2, 3, 4), (0, 2, 1, 3, 4), (0, 2, 3, 1, 4)])
+def test_keys_and_values_in_one_buffer(order):
+    """[pages, 2, size, KV, D] with its axes in three orders: appended to and read as two that lie apart."""
+    KV, page, D, n = 2, 16, 64, 90
+    buffer = torch.zeros([(7, 2, page, KV, D)[i] for i in order], dtype=BF16, device="cuda")
+    kv = buffer.permute([order.index(i) for i in range(5)])
+    kc, vc = torch.zeros((7, page, KV, D), dtype=BF16, device="cuda"), torch.zeros((7, page, KV, D), dtype=BF16, device="cuda")
+    q, k, v = randn(1, n, 4, D), randn(2, n, KV, D), randn(3, n, KV, D)
+    angle = torch.randn((n, D // 2), generator=torch.Generator().manual_seed(4)).cuda()
+    pos = torch.arange(n, dtype=I32).cuda()
+    for a, b in ((kv[:, 0], kv[:, 1]), (kc, vc)):
+        dg.det_kv_append(q, k, v, angle.cos(), angle.sin(), pos, pos, a, b)
+    assert torch.equal(kv[:, 0], kc) and torch.equal(kv[:, 1], vc)
+    table, lengths = torch.arange(6, dtype=I32).cuda()[None], torch.tensor([n], dtype=I32).cuda()
+    got = dg.det_attn_decode(q[-1:], kv[:, 0], kv[:, 1], table, lengths)
+    assert dg.det_gemm_check() == 0
+    assert torch.equal(got, dg.det_attn_decode(q[-1:], kc, vc, table, lengths))
