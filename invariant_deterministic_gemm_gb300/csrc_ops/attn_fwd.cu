@@ -331,8 +331,6 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
                     const int k = 32 * x;
                     if (k > warp_hi - a || (k + 31 < first_lo && k >= sink)) {
                         hidden |= 1u << x;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) s[x][j] = __float_as_uint(-INFINITY);
                     } else if (k + 31 > warp_lo - a || (k < first_hi && k + 31 >= sink)) {
                         const uint32_t seen = seen_bits(k, first, last, sink);
 #pragma unroll
@@ -342,11 +340,21 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
                 }
             }
             float top[4];
+            auto largest = [&](int x) {
+                float v = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                top[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
+                for (int j = 2; j < 32; j += 2) v = max3(v, __uint_as_float(s[x][j]), __uint_as_float(s[x][j + 1]));
+                return v;
+            };
+            if (hidden == 0) {                   // (the four go side by side)
 #pragma unroll
-                for (int j = 2; j < 32; j += 2) top[x] = max3(top[x], __uint_as_float(s[x][j]), __uint_as_float(s[x][j + 1]));
+                for (int x = 0; x < 4; ++x) top[x] = largest(x);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    top[x] = -INFINITY;
+                    if (!((hidden >> x) & 1u)) top[x] = largest(x);
+                }
             }
             const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             const bool grown = mx > m + kSlack;
