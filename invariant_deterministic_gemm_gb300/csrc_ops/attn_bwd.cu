@@ -308,12 +308,13 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
 #pragma unroll
                 for (int e = 0; e < 8; ++e) part = fmaf(f[e], g[e], part);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.o_read));
         }
         float *deltas = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&S) - 1024);
         deltas[half * kTile + row] = part;
         if (any_at(1, 256, !ok)) return;             // (all leave together: nobody is waited for in vain)
+        // All sums have been made: the copies' places are free. (Loads come back late while products read shared memory. An arrival of
+        // each warp behind its loads, but ahead of what they are for, let the ring's tile in before them now and then.)
+        if (threadIdx.x == 0) mbar_arrive(smem_u32(&S.o_read));
         delta = deltas[row] + deltas[kTile + row];
     }
     const float lse = live ? p.lse[at] : 0.0f;
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         }
         mbar_init(smem_u32(&S.q_full), 1);
         mbar_init(smem_u32(&S.o_full), 1);
-        mbar_init(smem_u32(&S.o_read), 8);
+        mbar_init(smem_u32(&S.o_read), 1);
         mbar_init(smem_u32(&S.scores[0]), 1);
         mbar_init(smem_u32(&S.scores[1]), 1);
         mbar_init(smem_u32(&S.dp), 1);
