@@ -83,8 +83,10 @@ struct Shared {
     int page[8][32];                 // of the chunks ahead: the page of each eight tokens, -1 for hidden ones
     unsigned loaded[16];             // which of them have one
     alignas(16) float top[2][2][4][32];   // each warp's maxima of a chunk: of even and odd ones, the last two of each
-    alignas(16) float most[kSums][32];   // the chunk's
-    alignas(16) float sum[kSums][4][32]; // each warp's sums of P
+    // The chunk's maxima, and each warp's sums of P: of twice as many chunks as wait to be joined, so that those who write them know
+    // of arrivals behind the use of the last ones, not behind their loads alone.
+    alignas(16) float most[2 * kSums][32];
+    alignas(16) float sum[2 * kSums][4][32];
     long long first, last;           // the CTA's units
     unsigned scan[16];
     int start, start_list, start_unit;           // sequence of the first unit, its list, and its place there
@@ -352,13 +354,14 @@ __device__ void copy_role(const DecodeParams &p, const DecodeMaps &maps, Shared 
             ok = wait.warp(smem_u32(&S.pages_full[n % kPagesAhead]), (n / kPagesAhead) & 1);
             if (!ok) break;
             const int page[2] = {S.page[n % kPagesAhead][g], S.page[n % kPagesAhead][16 + g]};
-            __syncwarp();
+            // Groups with a page, of either tile. (The vote needs the pages, which an arrival behind their loads would not wait for.)
+            const unsigned pages[2] = {__ballot_sync(kWarp, page[0] >= 0) & 0xFFFFu, __ballot_sync(kWarp, page[1] >= 0) & 0xFFFFu};
             if (lane == 0) mbar_arrive(smem_u32(&S.pages_empty[n % kPagesAhead]));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (!((tiles >> t) & 1u)) continue;
                 // Boxes with a token to copy. Its page: of any of its groups (they share it).
-                const unsigned got = __ballot_sync(kWarp, page[t] >= 0) & 0xFFFFu, mine = begins_box ? (got >> g) & in_box : 0;
+                const unsigned mine = begins_box ? (pages[t] >> g) & in_box : 0;
                 const int box_page = __shfl_sync(kWarp, page[t], mine ? (g + __ffs(mine) - 1) & 15 : g);
                 const unsigned boxes = __popc(__ballot_sync(kWarp, mine != 0) & 0xFFFFu);
                 const int slot = slot0 + seq % slots, token = chunk * kChunk + t * kTile + g * 8;
@@ -633,7 +636,7 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                     const float4 z = *reinterpret_cast<const float4 *>(shared_top + w * 32 + h);
                     y = make_float4(fmaxf(y.x, z.x), fmaxf(y.y, z.y), fmaxf(y.z, z.z), fmaxf(y.w, z.w));
                 }
-                if (row == 0) *reinterpret_cast<float4 *>(&S.most[n % kSums][h]) = y;
+                if (row == 0) *reinterpret_cast<float4 *>(&S.most[n % (2 * kSums)][h]) = y;
                 top[h] = y.x;
                 top[h + 1] = y.y;
                 top[h + 2] = y.z;
@@ -661,7 +664,7 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
                 top[h] = a + b;
             }
             sum_lanes<HE>(top, lane);
-            if (lane % (32 / HE) == 0) S.sum[n % kSums][warp][lane / (32 / HE)] = top[0];
+            if (lane % (32 / HE) == 0) S.sum[n % (2 * kSums)][warp][lane / (32 / HE)] = top[0];
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.probs[group]));
@@ -732,7 +735,7 @@ __device__ void join_role(const DecodeParams &p, Shared &S, const Waits &wait, i
     while (walk.next(s)) {
         const int head0 = s.kv * p.G + s.part * p.heads, heads = min(p.heads, p.G - s.part * p.heads);
         for (int ch = s.c0; ch < s.c1; ++ch, ++n) {
-            const int at = n % kSums;
+            const int at = n % kSums, of = n % (2 * kSums);
             if (!wait.warp(smem_u32(&S.sums[at]), (n / kSums) & 1)) return;
             const int count = __popc(tiles_of(p, s.tokens, s.chunks.at(ch)));
             if (!C::COMMIT && warp == 0 && lane < count) mbar_arrive(smem_u32(&S.empty[C::KEYS + (value + lane) % C::VALUES]));
@@ -742,13 +745,13 @@ __device__ void join_role(const DecodeParams &p, Shared &S, const Waits &wait, i
             ld<HE>(tm + C::T_CHUNK + at * NT, x.o);
 #pragma unroll
             for (int h = 0; h < HE; h += 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(&S.most[at][h]);
+                const float4 y = *reinterpret_cast<const float4 *>(&S.most[of][h]);
                 x.m[h] = __float_as_uint(y.x);
                 x.m[h + 1] = __float_as_uint(y.y);
                 x.m[h + 2] = __float_as_uint(y.z);
                 x.m[h + 3] = __float_as_uint(y.w);
-                const float4 a = *reinterpret_cast<const float4 *>(&S.sum[at][0][h]), b = *reinterpret_cast<const float4 *>(&S.sum[at][1][h]);
-                const float4 c = *reinterpret_cast<const float4 *>(&S.sum[at][2][h]), d = *reinterpret_cast<const float4 *>(&S.sum[at][3][h]);
+                const float4 a = *reinterpret_cast<const float4 *>(&S.sum[of][0][h]), b = *reinterpret_cast<const float4 *>(&S.sum[of][1][h]);
+                const float4 c = *reinterpret_cast<const float4 *>(&S.sum[of][2][h]), d = *reinterpret_cast<const float4 *>(&S.sum[of][3][h]);
                 x.l[h] = __float_as_uint((a.x + b.x) + (c.x + d.x));
                 x.l[h + 1] = __float_as_uint((a.y + b.y) + (c.y + d.y));
                 x.l[h + 2] = __float_as_uint((a.z + b.z) + (c.z + d.z));
