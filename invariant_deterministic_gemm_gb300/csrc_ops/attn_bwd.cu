@@ -123,7 +123,7 @@ struct QWork {
     Places at;
 };
 struct QShared {
-    uint64_t q_full, o_full, o_read, full[8], empty[8], scores[2], dp, read, ds, done, verdict, staged, drain, never;
+    uint64_t q_full, o_full, o_read, full[8], empty[8], scores[2], dp, read, ds[2], done, verdict, staged, drain, never;
     uint32_t tmem;
     int abort_flag, taken, again, some;
     QWork work;
@@ -236,7 +236,8 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
                 ok = wait.one(smem_u32(&S.read), i & 1);
                 if (ok) dp(i + 1);
             }
-            ok = ok && wait.one(smem_u32(&S.ds), i & 1);
+            // (dS of the next block may be there before this wait is over: two barriers, so that neither goes two phases on.)
+            ok = ok && wait.one(smem_u32(&S.ds[i & 1]), (i >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             mma_rows(tm + 3 * kTile, tm + (i & 1) * kTile, ring + 2 * i % C::SLOTS * C::TILE, steps * 16, i > begin, kGap);
@@ -386,7 +387,7 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.ds));
+            if (lane == 0) mbar_arrive(smem_u32(&S.ds[j & 1]));
         }
         if (!wait.warp(smem_u32(&S.done), again)) return;
         tc_fence_after();
@@ -444,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         mbar_init(smem_u32(&S.scores[1]), 1);
         mbar_init(smem_u32(&S.dp), 1);
         mbar_init(smem_u32(&S.read), 8);
-        mbar_init(smem_u32(&S.ds), 8);
+        mbar_init(smem_u32(&S.ds[0]), 8);
+        mbar_init(smem_u32(&S.ds[1]), 8);
         mbar_init(smem_u32(&S.done), 1);
         mbar_init(smem_u32(&S.verdict), 8);
         mbar_init(smem_u32(&S.staged), 4);
