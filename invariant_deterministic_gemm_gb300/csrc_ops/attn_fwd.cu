@@ -217,9 +217,11 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
                     const uint32_t phase = (probs >> t) & 1u;
                     ok = wait.one(smem_u32(&S.probs[t][0]), phase);
                     probs ^= 1u << t;
-                    if (ok && check) {           // the other tile's threads have looked at their part of the values
-                        ok = wait.one(smem_u32(&S.sane[1 - t]), (sane >> (1 - t)) & 1u);
-                        sane ^= 1u << (1 - t);
+                    // Both tiles' threads have looked at their part of the values. (The first tile's have if its P is there; awaited
+                    // here all the same, as its next scores could take them on to the next block.)
+                    if (ok && check && t == 0) {
+                        for (int u = 0; u < 2; ++u) ok = ok && wait.one(smem_u32(&S.sane[u]), (sane >> u) & 1u);
+                        sane ^= 3u;
                     }
                     if (!ok) return;
                     tc_fence_after();
