@@ -18,7 +18,7 @@
 // what TMEM holds. A block takes both tiles about 3300 cycles, its products 2048.
 // Prompts of 2048 queries over up to 8192 keys (32 heads of 128 on 8) 88.5 us, 0.50
 // of the measured BF16 rate by visible pairs; 16384 tokens, window 1024, 16 heads
-// 181 us. P through shared memory 98 where 94, half blocks 113, two threads a row 136.
+// 179 us. P through shared memory 98 where 94, half blocks 113, two threads a row 136.
 // P is rounded to BF16, as the tensor core wants it beside BF16 values; the sum
 // takes the unrounded ones.
 //
