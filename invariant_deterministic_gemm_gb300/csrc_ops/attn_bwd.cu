@@ -320,7 +320,8 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
     }
     const float lse = live ? p.lse[at] : 0.0f;
     if (live && half == 0) p.delta[at] = delta;
-    const float c = p.scale * kLog2e, off = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    // (A row that sees nothing has no P. One that sees a single key has no dS: P is one whatever its score.)
+    const float c = p.scale * kLog2e, off = lse == -INFINITY || sees_one(p, position) ? -INFINITY : -lse * kLog2e;
     const uint64_t c2 = pair(c, c), l2 = pair(off, off), d2 = pair(-delta, -delta);
     const Places places = w.at;
     const int n = w.blocks.n;
@@ -808,6 +809,15 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.probs));
+            // A query that sees a single key has no dS: the one at place 0, or every one.
+            if (!full) {
+                const int alone = -shift - qb * kTile - half * 64;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (sees_one(p, 1)) seen[x] = 0u;
+                    else if (key == 0) seen[x] &= below(alone - 32 * x) | ~below(alone + 1 - 32 * x);
+                }
+            }
             if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
             tc_fence_after();
             uint32_t d[2][32];

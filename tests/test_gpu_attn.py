@@ -382,3 +382,27 @@ def test_a_timeout_is_reported_and_the_context_stays_usable():
     g2 = dg.det_attn_bwd(dout, q, k, v, o2, l2, **kw)
     assert dg.det_gemm_check() == 0
     assert torch.equal(out, o2) and torch.equal(lse, l2) and all(torch.equal(x, y) for x, y in zip(g, g2))
+
+
+@pytest.mark.parametrize("lengths,kw", [((1, 1, 1), {}), ((1,), {}), ((300, 1, 70), dict(window=1))])
+def test_queries_that_see_a_single_key_have_no_gradient(lengths, kw):
+    n = sum(lengths)
+    q, k, v = make(n, n, 6, 2, 72, 71)
+    dout, b = randn(9, n, 6, 72), bounds(*lengths)
+    out, lse = dg.det_attn(q, k, v, b, **kw)
+    assert torch.equal(out, v.repeat_interleave(3, 1))
+    dq, dk, dv = dg.det_attn_bwd(dout, q, k, v, out, lse, b, **kw)
+    assert dg.det_gemm_check() == 0
+    assert not dq.any() and not dk.any()
+    want = ref.f64(dout).unflatten(1, (2, 3)).sum(2)
+    ref.assert_within(dv, want, ref.f64(dout).abs().unflatten(1, (2, 3)).sum(2) * (2.0 ** -8 + 2.0 ** -20), "dv")
+
+
+def test_the_first_query_of_a_sequence_has_no_gradient():
+    q, k, v = make(400, 400, 4, 2, 128, 72)
+    b = bounds(200, 200)
+    out, lse = dg.det_attn(q, k, v, b)
+    dout = torch.zeros_like(out)
+    dout[0], dout[200] = randn(1, 4, 128), randn(2, 4, 128)
+    dq, dk, dv = dg.det_attn_bwd(dout, q, k, v, out, lse, b)
+    assert not dq.any() and not dk.any() and dv[0].any() and dv[200].any()
