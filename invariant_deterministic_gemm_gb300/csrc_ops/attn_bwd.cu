@@ -17,7 +17,7 @@
 //
 // Bound by the products and the chain between them: a block of dq takes about 1725
 // cycles (products 1536), of dk and dv 2200 to 2600 (2048); of a packed training
-// pass of 635 us dq is 244, dk and dv 217. Scores of 64 columns at a time, with
+// pass of 638 us dq is 244, dk and dv 217. Scores of 64 columns at a time, with
 // both operands from shared memory, are bound by its 128 bytes a cycle; waits for
 // each product's end cost dk and dv 257 us.
 //
