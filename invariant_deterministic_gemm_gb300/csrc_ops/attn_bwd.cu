@@ -139,7 +139,7 @@ __device__ __forceinline__ bool find_queries(const AttnParams &p, int unit, int 
     const int n = tile_sequence(p.qb, p.N, p.T, kTile, slots - 1 - unit / p.H, tile);
     w.s = seq_at(p, n);
     const long long row0 = w.s.q0 + static_cast<long long>(kTile) * tile;
-    if (row0 >= w.s.q1) return false;
+    if (tile < 0 || row0 >= w.s.q1) return false;
     w.row0 = static_cast<int>(row0);
     w.rows = min(kTile, w.s.q1 - w.row0);
     const int first = w.s.position(w.row0);
@@ -535,14 +535,14 @@ __device__ __forceinline__ bool find_keys(const AttnParams &p, int unit, int pie
         w.kv = unit % p.KV;
         key0 = static_cast<long long>(unit / p.KV % p.sink_blocks) * kTile;
         w.s = seq_at(p, tile_sequence(p.qb, p.N, p.T, kPiece, unit / p.KV / p.sink_blocks, part));
-        if (static_cast<long long>(part) * kPiece >= w.s.queries()) return false;
+        if (part < 0 || static_cast<long long>(part) * kPiece >= w.s.queries()) return false;
     } else {
         unit -= pieces;
         w.kv = unit % p.KV;
         int tile;
         w.s = seq_at(p, tile_sequence(p.kb, p.N, p.S, kTile, unit / p.KV, tile));
         key0 = static_cast<long long>(kTile) * tile;
-        if (tile < p.sink_blocks) return false;              // the pieces'
+        if (tile < 0 || tile < p.sink_blocks) return false;  // (the pieces')
     }
     if (key0 >= w.s.keys()) return false;
     w.key0 = static_cast<int>(key0);

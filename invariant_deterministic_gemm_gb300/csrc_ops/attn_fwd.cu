@@ -94,7 +94,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int unit, int slo
     const int n = tile_sequence(p.qb, p.N, p.T, 2 * kTile, slots - 1 - unit / p.H, tile);
     w.s = seq_at(p, n);
     const long long row0 = w.s.q0 + 2ll * kTile * tile;
-    if (row0 >= w.s.q1) return false;
+    if (tile < 0 || row0 >= w.s.q1) return false;
     w.row0 = static_cast<int>(row0);
     for (int t = 0; t < 2; ++t) {
         w.rows[t] = max(0, min(kTile, w.s.q1 - w.row0 - t * kTile));

@@ -326,7 +326,8 @@ __host__ __device__ constexpr int tile_slots(int rows_total, int sequences, int 
 
 __device__ __forceinline__ int clamped(const int32_t *bounds, int n, int limit) { return min(max(bounds[n], 0), limit); }
 
-// The sequence of tile number x, and how many of its tiles come before (x's tile may be past its end).
+// The sequence of tile number x, and how many of its tiles come before: x's tile may be past its end, and is negative where x is
+// below the first sequence's numbers, whose rows nobody owns.
 __device__ __forceinline__ int tile_sequence(const int32_t *bounds, int N, int limit, int rows, int x, int &tile)
 {
     if (!bounds) {
