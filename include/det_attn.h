@@ -23,7 +23,8 @@
  * position outside the tables, a slot or page outside the cache, a length
  * that the page table does not hold, bounds that go down or leave the
  * array) is made harmless there, set in a status word and reported by
- * det_ops_check(). Sizes are below 2^31 - 4096.
+ * det_ops_check(); a row that two sequences of such bounds hold gets the
+ * results of either. Sizes are below 2^31 - 4096.
  *
  * Visible keys: query i of a sequence of n keys and m queries is at position
  * i + n - m (its last query at its last key) and sees the keys j at or

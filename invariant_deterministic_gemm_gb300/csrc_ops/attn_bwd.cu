@@ -484,7 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
         if (some && warp == 8 && elect_one()) q_copy<DH>(p, maps, S, base, wait);
         else if (some && warp == 9 && elect_one()) q_issue<DH>(p, S, base, wait);
         __syncwarp();
-        if (warp >= 10) zero_outside(p.qb, p.N, p.T, p.H, p.D, p.dq, nullptr, threadIdx.x - 320, 64);
+        if (warp >= 10) {
+            report_bounds(p, threadIdx.x - 320, 64);
+            zero_outside(p.qb, p.N, p.T, p.H, p.D, p.dq, nullptr, threadIdx.x - 320, 64);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -962,7 +965,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
         else if (some && warp == 9 && elect_one()) k_issue<DH>(p, S, base, wait);
         else if (some && warp == 10) k_vectors<DH>(p, S, smem, wait, lane);
         __syncwarp();
-        if (warp == 11) zero_outside(p.kb, p.N, p.S, p.KV, p.D, p.dk, &p.dv, lane, 32);
+        if (warp == 11) {
+            if (p.T == 0) report_bounds(p, lane, 32);        // (else the first launch has)
+            zero_outside(p.kb, p.N, p.S, p.KV, p.D, p.dk, &p.dv, lane, 32);
+        }
     }
     __syncwarp();
     tc_fence_before();

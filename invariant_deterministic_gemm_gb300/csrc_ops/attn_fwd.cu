@@ -471,14 +471,7 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
 __device__ void outside(const AttnParams &p, int thread)
 {
     if (!p.qb) return;
-    if (blockIdx.x == 0) {
-        bool bad = false;
-        for (int n = thread; n < p.N; n += 64) {
-            const Seq s = seq_at(p, n);
-            bad |= s.q0 != p.qb[n] || s.q1 != p.qb[n + 1] || s.k0 != p.kb[n] || s.k1 != p.kb[n + 1];
-        }
-        if (bad) atomicExch(p.status, kStatusInvalid);
-    }
+    report_bounds(p, thread, 64);
     const int lo = p.N > 0 ? clamped(p.qb, 0, p.T) : 0, hi = p.N > 0 ? max(lo, clamped(p.qb, p.N, p.T)) : 0;
     const long long rows = static_cast<long long>(lo + p.T - hi) * p.H;
     for (long long i = blockIdx.x; i < rows; i += gridDim.x) {

@@ -344,4 +344,16 @@ __device__ __forceinline__ int tile_sequence(const int32_t *bounds, int N, int l
     return a;
 }
 
+// Bounds that go down or leave the array, by `threads` threads of the launch's first block.
+__device__ __forceinline__ void report_bounds(const AttnParams &p, int thread, int threads)
+{
+    if (!p.qb || blockIdx.x != 0) return;
+    bool bad = false;
+    for (int n = thread; n < p.N; n += threads) {
+        const Seq s = seq_at(p, n);
+        bad |= s.q0 != p.qb[n] || s.q1 != p.qb[n + 1] || s.k0 != p.kb[n] || s.k1 != p.kb[n + 1];
+    }
+    if (bad) atomicExch(p.status, kStatusInvalid);
+}
+
 }  // namespace deto
