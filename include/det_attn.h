@@ -113,7 +113,10 @@ det_gemm_status det_attn(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const d
  * Gradients of det_attn: dq [T, H, D], dk and dv [S, KV, D] from dout, the
  * inputs, out and lse. With P = exp(scores - lse): dv = P^T dout, dS = P
  * (dout v^T - rowsum(dout out)), dq = scale dS k, dk = scale dS^T q, summed over
- * the query heads that share a KV head. P and dS are rounded to BF16 for
+ * the query heads that share a KV head. out and lse may be those of more keys
+ * than these (results over several ranges of keys, joined). A query that sees
+ * a single key, and whose lse is that key's score, has dS = 0 and not the
+ * rounding of its two terms. P and dS are rounded to BF16 for
  * their second products. Rows outside every sequence become zero.
  */
 int64_t det_attn_bwd_workspace(int64_t N, int64_t T, int64_t S, int64_t H, int64_t KV, int64_t D, int64_t window,

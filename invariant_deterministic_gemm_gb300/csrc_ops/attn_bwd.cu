@@ -62,6 +62,13 @@ __device__ __forceinline__ void exp_block(uint32_t (&s)[32], uint64_t c2, uint64
 }
 __device__ __forceinline__ void lds4(uint32_t at, uint64_t &a, uint64_t &b) { asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at)); }
 
+// A query that sees a single key, whose weight P is one, has no dS whatever the score: dout v^T and delta are two sums of the same
+// numbers in different orders, so its delta is that key's dout v^T, for both launches (the tensor core's sum has the same bits
+// with its operands exchanged). Whether P is one its lse tells, and not its place alone: an lse over more keys than these (of
+// results that were joined) is larger than the score, and P less. P is off by a few steps of 2^-24 times the argument's terms
+// (score, lse: l is -lse log2(e)); 2^-18 is 64 of them, and what is left out that small a part of the two terms of dS.
+__device__ __forceinline__ bool is_one(uint32_t p, float l) { return fabsf(__uint_as_float(p) - 1.0f) <= 0x1p-18f * (1.0f + fabsf(l)); }
+
 __device__ __forceinline__ uint32_t pack_words(uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); }
 
 // 32 FP32 words as 16 of BF16, into TMEM.
@@ -319,9 +326,10 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
         delta = deltas[row] + deltas[kTile + row];
     }
     const float lse = live ? p.lse[at] : 0.0f;
-    if (live && half == 0) p.delta[at] = delta;
-    // (A row that sees nothing has no P. One that sees a single key has no dS: P is one whatever its score.)
-    const float c = p.scale * kLog2e, off = lse == -INFINITY || sees_one(p, position) ? -INFINITY : -lse * kLog2e;
+    // (Of a query that sees a single key: when that key's dout v^T is there.)
+    if (live && half == 0 && !(position >= 0 && sees_one(p, position))) p.delta[at] = delta;
+    // (A row that sees nothing has no P.)
+    const float c = p.scale * kLog2e, off = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
     const uint64_t c2 = pair(c, c), l2 = pair(off, off), d2 = pair(-delta, -delta);
     const Places places = w.at;
     const int n = w.blocks.n;
@@ -366,6 +374,19 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.read));
+            if (!full && __any_sync(kWarp, sees_one(p, position))) {
+                // (The one key is in the half of one of two threads, which writes delta.)
+                float mine = delta;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (sees_one(p, position) && ((seen[x] >> k) & 1u) && is_one(s[x][k], off)) {
+                            mine = __uint_as_float(d[x][k]);
+                            s[x][k] = 0u;
+                        }
+                if (live && !again && sees_one(p, position) && (seen[0] | seen[1]) != 0) p.delta[at] = mine;
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -790,16 +811,13 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
                     s[x][2 * k + 2] = __float_as_uint(exp2_fast(b0));
                     s[x][2 * k + 3] = __float_as_uint(exp2_fast(b1));
                 }
-            bool some[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                some[x] = __any_sync(kWarp, seen[x] != ~0u);
-                if (some[x]) {
+            for (int x = 0; x < 2; ++x)
+                if (__any_sync(kWarp, seen[x] != ~0u)) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (!(seen[x] & (1u << k))) s[x][k] = 0u;
                 }
-            }
             if (again && !full) {
                 // When both score matrices have been made the queries' rows may be changed for the last two products.
                 if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
@@ -812,15 +830,6 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.probs));
-            // A query that sees a single key has no dS: the one at place 0, or every one.
-            if (!full) {
-                const int alone = -shift - qb * kTile - half * 64;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (sees_one(p, 1)) seen[x] = 0u;
-                    else if (key == 0) seen[x] &= below(alone - 32 * x) | ~below(alone + 1 - 32 * x);
-                }
-            }
             if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
             tc_fence_after();
             uint32_t d[2][32];
@@ -847,7 +856,7 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
                 }
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                if (some[x]) {
+                if (__any_sync(kWarp, seen[x] != ~0u)) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (!(seen[x] & (1u << k))) d[x][k] = 0u;

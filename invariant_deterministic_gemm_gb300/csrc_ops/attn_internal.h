@@ -148,7 +148,7 @@ __device__ __forceinline__ bool sees(const AttnParams &p, int position, int j)
 {
     return j <= position && (position - j < p.window || j < p.sinks);
 }
-// A query at `position` (0 or more) sees a single key.
+// A query at `position` (0 or more) sees a single key of these.
 __device__ __forceinline__ bool sees_one(const AttnParams &p, int position) { return position == 0 || (p.window == 1 && p.sinks == 0); }
 
 }  // namespace deto
