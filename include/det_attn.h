@@ -31,7 +31,8 @@
  * before it with position - j < window or j < sinks. window 0: no window.
  * A query that sees no key gives zeros (and lse -inf). Scores are scale q.k;
  * scale is positive and finite. What masked keys and values hold, infinities
- * and NaN included, does not reach the output.
+ * and NaN included, does not reach the output. In det_attn a visible value that
+ * is not finite is added as it is, however small its weight.
  */
 #ifndef DET_ATTN_H
 #define DET_ATTN_H

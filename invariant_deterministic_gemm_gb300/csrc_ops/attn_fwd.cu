@@ -31,8 +31,10 @@
 // What is masked does not reach the output: masked scores are replaced. A value
 // that is not finite would (zero times infinity), in blocks where some row sees
 // only some keys; then that row's output is not finite. Such a tile is done a
-// second time, with what is not finite taken out of those values before the
-// product and added to the rows that see it afterwards.
+// second time, with what is not finite taken out of all values before the
+// product and added to the rows that see it afterwards: as it is, since weights
+// are positive, those too that are zero in FP32 (times infinity they would be NaN
+// in blocks that are seen whole, which depends on where tiles begin).
 #include "attn_tile.cuh"
 
 #include <atomic>
@@ -66,20 +68,16 @@ struct Work {
     Places at[2];
     // What is done for the tiles `act` (a bit each): all that see something, or those that have to be done again.
     __device__ bool used(int i, unsigned act) const { return ((act & 1u) && at[0].sees(i)) || ((act & 2u) && at[1].sees(i)); }
-    // Some row of such a tile sees some keys of the block and not all.
-    __device__ bool partly(int i, unsigned act) const
-    {
-        return ((act & 1u) && at[0].sees(i) && !at[0].whole(i)) || ((act & 2u) && at[1].sees(i) && !at[1].whole(i));
-    }
     __device__ unsigned seeing() const { return (at[0].last() >= 0 ? 1u : 0u) | (at[1].last() >= 0 ? 2u : 0u); }
 };
 
+constexpr int kTakenWords = 16;
 struct Shared {
     uint64_t q_full[2], full[8], empty[8], scores[2], probs[2][2], sane[2], done[2], verdict[2], drain, never;
     uint32_t tmem;
     int abort_flag;
     int again[2];                    // the tile has to be done again
-    int taken;                       // some value has been taken out
+    uint32_t taken[kTakenWords];     // some value has been taken out of the block (a bit each, in turn)
     int some;                        // there is something to do
     Work work;
 };
@@ -208,7 +206,7 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
             int next = i + 1;
             while (next < w.blocks.n && !w.used(next, act)) ++next;
             const bool more = next < w.blocks.n;
-            const bool check = safe && on[0] && on[1] && w.at[0].sees(i) && w.at[1].sees(i) && w.partly(i, act);
+            const bool check = safe && on[0] && on[1] && w.at[0].sees(i) && w.at[1].sees(i);
             if (!arrive_tile(v)) return;
             bool have_next = false;
             for (int t = 0; t < 2; ++t) {
@@ -253,16 +251,21 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
 }
 
 // Adds the values that make_finite took out to the rows that see them.
-__device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, unsigned act, int t, uint32_t out, int position)
+__device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, const uint32_t *taken, int t, uint32_t out, int position)
 {
     for (int c = 0; c < p.D; c += 8) {
         uint32_t o[8];
         detg::tmem_ld8(out + c, o);
         tmem_wait_ld();
         detg::reg_fence8(o);
-        for (int i = 0; i < w.blocks.n; ++i) {
-            const int b = w.blocks.at(i);
-            if (!w.at[t].sees(i) || !w.partly(i, act)) continue;
+        auto all_nan = [&] {         // (nothing changes them any more)
+            bool all = true;
+            for (int e = 0; e < 8; ++e) all &= isnan(__uint_as_float(o[e]));
+            return all;
+        };
+        for (int i = 0; i < w.blocks.n && !all_nan(); ++i) {
+            const int b = w.blocks.at(i), x = i % (32 * kTakenWords);
+            if (!w.at[t].sees(i) || !((taken[x / 32] >> (x % 32)) & 1u)) continue;
             for (int j = b * kTile; j < (b + 1) * kTile && j <= position; ++j) {
                 if (!sees(p, position, j)) continue;
                 const uint4 v = *reinterpret_cast<const uint4 *>(p.v.row(w.s.k0 + j, w.kv) + c);
@@ -293,7 +296,7 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
     float m = -INFINITY, l = 0.0f;               // m: what the row is scaled by, log2
     uint32_t phase = 0;
     int tile = 0;                                // of the ring, of the next block's keys
-    // All blocks that the tile sees; `safe`: what is not finite is taken out of values that some rows of `act` do not see.
+    // All blocks that the tile sees; `safe`: what is not finite is taken out of the values.
     auto pass = [&](unsigned act, bool safe) {
         bool out = false;
         m = -INFINITY;
@@ -307,13 +310,16 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
             tile += 2;
             if (!wait.warp(smem_u32(&S.scores[t]), phase)) return false;
             phase ^= 1u;
-            if (safe && w.partly(i, act)) {
+            if (safe) {
                 // The scores wait for every tile of the ring before these values, so that their slot's barrier is in the phase before.
                 const bool both = act == 3u && w.at[1 - t].sees(i);
                 const int slot = v_tile % C::SLOTS;
                 if (!wait.warp(smem_u32(&S.full[slot]), (v_tile / C::SLOTS) & 1)) return false;
                 const int live = min(kTile, w.s.keys() - w.blocks.at(i) * kTile);
-                if (make_finite<DH>(base + C::OFF_RING + slot * C::TILE, both ? 2 * row + t : row, live)) S.taken = 1;
+                if (make_finite<DH>(base + C::OFF_RING + slot * C::TILE, both ? 2 * row + t : row, live)) {
+                    const int x = i % (32 * kTakenWords);
+                    atomicOr(&S.taken[x / 32], 1u << (x % 32));
+                }
                 __syncwarp();
                 if (both && lane == 0) mbar_arrive(smem_u32(&S.sane[t]));
             }
@@ -430,7 +436,7 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
     for (int again = 0; some; ++again) {
         if (!pass(act, again != 0) || !wait.warp(smem_u32(&S.done[t]), again)) return;
         tc_fence_after();
-        if (again && *reinterpret_cast<volatile int *>(&S.taken)) add_taken(p, w, act, t, to, row < rows ? position : -1);
+        if (again) add_taken(p, w, S.taken, t, to, row < rows ? position : -1);
 #pragma unroll
         for (int x = 0; x < DH / 32; ++x) tmem_ld32(to + 32 * x, o[x]);
         tmem_wait_ld();
@@ -491,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.again[0] = S.again[1] = S.taken = 0;
+        S.again[0] = S.again[1] = 0;
+        for (int i = 0; i < kTakenWords; ++i) S.taken[i] = 0;
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
             mbar_init(smem_u32(&S.empty[i]), 1);
