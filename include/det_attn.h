@@ -32,7 +32,8 @@
  * A query that sees no key gives zeros (and lse -inf). Scores are scale q.k;
  * scale is positive and finite. What masked keys and values hold, infinities
  * and NaN included, does not reach the output. In det_attn a visible value that
- * is not finite is added as it is, however small its weight.
+ * is not finite is added as it is, however small its weight, and in det_attn_bwd
+ * so is such a row of dout.
  */
 #ifndef DET_ATTN_H
 #define DET_ATTN_H

@@ -33,8 +33,11 @@
 // What is masked does not reach the results: masked elements are replaced. Rows
 // of the right operands that are not finite would (zero times infinity), in
 // blocks that are seen in part; then the result is not finite. Such a tile is
-// done a second time, with what is not finite taken out and added to those that
-// see it afterwards.
+// done a second time, with what is not finite taken out, and put back afterwards
+// for those that see it. A gradient of the output (dv) is added as it is: weights
+// are positive, those too that are zero in FP32. Keys (dq) and queries (dk) make
+// NaN: with a score of -infinity P and dS are zero, and zero times infinity is NaN,
+// as it is in blocks that are seen whole; any other such score has made NaN of dS.
 #include "attn_tile.cuh"
 
 #include <atomic>
@@ -45,6 +48,7 @@ namespace {
 
 constexpr int kThreads = 384, kLaunchRegs = 168, kMathRegs = 208, kServiceRegs = 88;
 static_assert(kMathRegs * 256 + kServiceRegs * 128 <= kLaunchRegs * kThreads, "register split");
+constexpr uint32_t kNan = 0x7FFFFFFFu;
 constexpr uint32_t kGap = 32;        // columns between the halves of P (or dS): 32 of 64
 
 // ---- what both do
@@ -259,7 +263,7 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
     }
 }
 
-// Adds the keys' values that make_finite took out to the queries that see them.
+// NaN for the queries that see a key which make_finite has taken something out of.
 __device__ __noinline__ void q_add_taken(const AttnParams &p, const QWork &w, uint32_t out, int position, int c0, int c1)
 {
     for (int c = c0; c < c1; c += 8) {
@@ -275,7 +279,7 @@ __device__ __noinline__ void q_add_taken(const AttnParams &p, const QWork &w, ui
                 float f[8];
                 unpack8(load8(p.k.row(w.s.k0 + j, w.kv), c, p.D), f);
                 for (int e = 0; e < 8; ++e)
-                    if (!isfinite(f[e])) o[e] = __float_as_uint(__uint_as_float(o[e]) + f[e]);
+                    if (!isfinite(f[e])) o[e] = kNan;
             }
         }
         __syncwarp();
@@ -538,10 +542,12 @@ struct KWork {
     int f0, f1;                      // the blocks of which every query sees every key of the tile
     int piece;                       // of the first keys' queries, or -1: all that see the tile
 };
+constexpr int kTakenWords = 16;
 struct KShared {
     uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, verdict, drain, never;
     uint32_t tmem;
-    int abort_flag, taken, again, some;
+    int abort_flag, again, some;
+    uint32_t taken[kTakenWords];     // something has been taken out of the iteration's rows (a bit each, in turn)
     KWork work;
 };
 static_assert(sizeof(KShared) <= 512, "shared state");
@@ -722,23 +728,30 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
     }
 }
 
-// Adds what make_finite took out of the queries' rows (x: q or dout) to the keys that they see. key: place in the sequence, or -1.
-__device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, const Heads &x, uint32_t out, int key, int c0, int c1)
+// What make_finite took out of the queries' rows (x: dout, or q) for the keys that they see: added to dv, NaN in dk. key: place in the
+// sequence, or -1.
+__device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, const uint32_t *taken, bool is_q, uint32_t out, int key)
 {
-    for (int c = c0; c < c1; c += 8) {
+    const Heads &x = is_q ? p.q : p.dout;
+    for (int c = 0; c < p.D; c += 8) {
         uint32_t o[8];
         detg::tmem_ld8(out + c, o);
         tmem_wait_ld();
         detg::reg_fence8(o);
-        for (int i = 0; i < w.n && key >= 0; ++i) {
-            const int qb = w.first + i / p.G;
-            if (qb >= w.f0 && qb < w.f1) continue;
+        auto all_nan = [&] {         // (nothing changes them any more)
+            bool all = true;
+            for (int e = 0; e < 8; ++e) all &= isnan(__uint_as_float(o[e]));
+            return all;
+        };
+        for (int i = 0; i < w.n && key >= 0 && !all_nan(); ++i) {
+            const int qb = w.first + i / p.G, bit = i % (32 * kTakenWords);
+            if (!((taken[bit / 32] >> (bit % 32)) & 1u)) continue;
             for (int r = qb * kTile; r < min((qb + 1) * kTile, w.s.queries()); ++r) {
                 if (!sees(p, r + w.s.keys() - w.s.queries(), key)) continue;
                 float f[8];
                 unpack8(load8(x.row(w.s.q0 + r, w.kv * p.G + i % p.G), c, p.D), f);
                 for (int e = 0; e < 8; ++e)
-                    if (!isfinite(f[e])) o[e] = __float_as_uint(__uint_as_float(o[e]) + f[e]);
+                    if (!isfinite(f[e])) o[e] = is_q ? kNan : __float_as_uint(__uint_as_float(o[e]) + f[e]);
             }
         }
         __syncwarp();
@@ -818,10 +831,13 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
                     for (int k = 0; k < 32; ++k)
                         if (!(seen[x] & (1u << k))) s[x][k] = 0u;
                 }
-            if (again && !full) {
+            if (again) {
                 // When both score matrices have been made the queries' rows may be changed for the last two products.
                 if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
-                if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, w.s.queries() - qb * kTile)) S.taken = 1;
+                if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, w.s.queries() - qb * kTile)) {
+                    const int bit = i % (32 * kTakenWords);
+                    atomicOr(&S.taken[bit / 32], 1u << (bit % 32));
+                }
                 __syncwarp();
             }
             put16(tm + half * 64, s[0]);
@@ -877,7 +893,7 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
         }
         if (!wait.warp(smem_u32(&S.done), again)) return;
         tc_fence_after();
-        if (again && *reinterpret_cast<volatile int *>(&S.taken)) k_add_taken(p, w, half ? p.q : p.dout, out, live ? key : -1, 0, p.D);
+        if (again) k_add_taken(p, w, S.taken, half != 0, out, live ? key : -1);
         bool bad = false;
 #pragma unroll 1
         for (int x = 0; x < DH / 32; ++x) {
@@ -924,7 +940,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.again = S.taken = 0;
+        S.again = 0;
+        for (int i = 0; i < kTakenWords; ++i) S.taken[i] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&S.q_full[i]), 1);
             mbar_init(smem_u32(&S.q_empty[i]), 1);

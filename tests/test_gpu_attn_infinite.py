@@ -71,3 +71,73 @@ def test_values_of_one_sequence_only():
     assert torch.equal(out[:70], clean[:70]) and torch.equal(out[270:], clean[270:])
     assert torch.isnan(out[70:270].float()).all()
     assert dg.det_gemm_check() == 0
+
+
+def gradients(q, k, v, dout, b=None, **kw):
+    out, lse = dg.det_attn(q, k, v, b, **kw)
+    return [x.float() for x in dg.det_attn_bwd(dout, q, k, v, out, lse, b, **kw)]
+
+
+@pytest.mark.parametrize("bad", [INF, -INF])
+@pytest.mark.parametrize("D,kw", [(64, dict()), (128, dict()), (80, dict(window=300, sinks=2)), (64, dict(window=520, sinks=200))])
+def test_infinite_gradients_of_the_output(bad, D, kw):
+    """dv of all keys that the query sees, those too to which it gives a weight of zero in FP32, has them with their sign."""
+    T, at = 700, 40
+    q, k, v = with_a_small_weight(T, D, at)
+    for i in (60, 300, 690):                 # their first keys are seen in blocks of queries that are seen in part, and whole
+        dout = randn(5, T, 4, D)
+        clean = gradients(q, k, v, dout, **kw)
+        dout[i, 1, 5] = bad
+        dq, dk, dv = gradients(q, k, v, dout, **kw)
+        j = torch.arange(T, device="cuda")
+        seen = (j <= i) & ((i - j < kw.get("window", T)) | (j < kw.get("sinks", 0)))
+        assert (dv[seen, 0, 5] == bad).all(), i
+        rest = torch.ones_like(dv, dtype=torch.bool)
+        rest[seen, 0, 5] = False
+        assert torch.equal(dv[rest], clean[2][rest]), i
+        assert torch.equal(dk[:, 1], clean[1][:, 1]) and torch.equal(dk[~seen], clean[1][~seen]), i
+        others = torch.arange(T, device="cuda") != i
+        assert torch.equal(dq[others], clean[0][others]), i
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("D,kw", [(64, dict()), (128, dict()), (80, dict(window=300, sinks=2))])
+def test_keys_and_queries_with_scores_of_minus_infinity(sign, D, kw):
+    """Their P and dS are zero, and zero times infinity is NaN: in that column of dq, for the queries that see the key, and of dk,
+    for the keys that the query sees, in whichever block."""
+    T, at = 700, 140
+    q, k, v = make(T, T, 4, 2, D, 7)
+    dout, j = randn(5, T, 4, D), torch.arange(T, device="cuda")
+    window, sinks = kw.get("window", T), kw.get("sinks", 0)
+    q[:, :, 3], k[:, :, 3] = sign, 0.0
+    clean = gradients(q, k, v, dout, **kw)
+    k[at, 1, 3] = -sign * INF
+    got = gradients(q, k, v, dout, **kw)
+    sees = (j >= at) & (j - at < window)
+    assert torch.isnan(got[0][sees][:, 2:, 3]).all()
+    assert torch.isfinite(got[0][~sees]).all() and torch.isfinite(got[0][:, :2]).all() and torch.isfinite(got[0][..., :3]).all()
+    assert torch.equal(got[0][:, :2], clean[0][:, :2]) and torch.equal(got[0][:at], clean[0][:at])
+    # a query whose scores are all -infinity
+    q, k, v = make(T, T, 4, 2, D, 7)
+    k[:, :, 3] = -sign
+    clean = gradients(q, k, v, dout, **kw)
+    q[at, 2, 3] = sign * INF
+    got = gradients(q, k, v, dout, **kw)
+    seen = (j <= at) & ((at - j < window) | (j < sinks))
+    assert torch.isnan(got[1][seen][:, 1, 3]).all()
+    assert torch.equal(got[1][~seen], clean[1][~seen]) and torch.equal(got[1][:, 0], clean[1][:, 0])
+    assert torch.isfinite(got[1][:, 1, 4:]).all() and torch.isfinite(got[2]).all()
+
+
+def test_gradients_of_a_sequence_between_others():
+    lengths = (70, 200, 90)
+    q, k, v = make(360, 360, 4, 2, 128, 6)
+    b, dout = bounds(*lengths), randn(8, 360, 4, 128)
+    clean = gradients(q, k, v, dout, b)
+    for x in (q, k, v, dout):
+        x[70:270] = NAN
+        x[100:150, :, ::2] = INF
+    got = gradients(q, k, v, dout, b)
+    for x, y in zip(got, clean):
+        assert torch.equal(x[:70], y[:70]) and torch.equal(x[270:], y[270:]) and torch.isnan(x[71:270]).all()
+    assert dg.det_gemm_check() == 0
