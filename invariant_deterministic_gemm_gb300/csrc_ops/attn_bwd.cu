@@ -48,7 +48,6 @@ namespace {
 
 constexpr int kThreads = 384, kLaunchRegs = 168, kMathRegs = 208, kServiceRegs = 88;
 static_assert(kMathRegs * 256 + kServiceRegs * 128 <= kLaunchRegs * kThreads, "register split");
-constexpr uint32_t kNan = 0x7FFFFFFFu;
 constexpr uint32_t kGap = 32;        // columns between the halves of P (or dS): 32 of 64
 
 // ---- what both do
@@ -271,7 +270,7 @@ __device__ __noinline__ void q_add_taken(const AttnParams &p, const QWork &w, ui
         detg::tmem_ld8(out + c, o);
         tmem_wait_ld();
         detg::reg_fence8(o);
-        for (int i = 0; i < w.blocks.n; ++i) {
+        for (int i = 0; i < w.blocks.n && !all_nan(o); ++i) {
             const int b = w.blocks.at(i);
             if (w.at.whole(i)) continue;
             for (int j = b * kTile; j < (b + 1) * kTile && j <= position; ++j) {
@@ -366,7 +365,7 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
                 // Both score matrices of the block have been made: its keys may be changed for the last product. The other
                 // half's threads wait for the same, and dq for both.
                 const int keys = w.s.keys() - w.blocks.at(i) * kTile;
-                if (row < 64 && make_finite<DH>(base + C::OFF_RING + 2 * j % C::SLOTS * C::TILE, half * 64 + row, min(kTile, keys))) S.taken = 1;
+                if (row < 64 && make_finite<DH>(base + C::OFF_RING + 2 * j % C::SLOTS * C::TILE, half * 64 + row, min(kTile, keys), nullptr, nullptr)) S.taken = 1;
                 __syncwarp();
             }
             uint32_t d[2][32];
@@ -542,12 +541,11 @@ struct KWork {
     int f0, f1;                      // the blocks of which every query sees every key of the tile
     int piece;                       // of the first keys' queries, or -1: all that see the tile
 };
-constexpr int kTakenWords = 16;
 struct KShared {
     uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, verdict, drain, never;
     uint32_t tmem;
-    int abort_flag, again, some;
-    uint32_t taken[kTakenWords];     // something has been taken out of the iteration's rows (a bit each, in turn)
+    int abort_flag, taken, again, some;
+    NotFinite whole;                 // what was, of rows of dout that see all of the tile's keys
     KWork work;
 };
 static_assert(sizeof(KShared) <= 512, "shared state");
@@ -728,9 +726,9 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
     }
 }
 
-// What make_finite took out of the queries' rows (x: dout, or q) for the keys that they see: added to dv, NaN in dk. key: place in the
-// sequence, or -1.
-__device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, const uint32_t *taken, bool is_q, uint32_t out, int key)
+// What make_finite took out of the queries' rows (x: dout, or q) for the keys that they see: added to dv, NaN in dk. Row by row in
+// blocks that are seen in part, `whole` for all others. key: place in the sequence, or -1.
+__device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, const NotFinite &whole, bool is_q, uint32_t out, int key)
 {
     const Heads &x = is_q ? p.q : p.dout;
     for (int c = 0; c < p.D; c += 8) {
@@ -738,14 +736,9 @@ __device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, co
         detg::tmem_ld8(out + c, o);
         tmem_wait_ld();
         detg::reg_fence8(o);
-        auto all_nan = [&] {         // (nothing changes them any more)
-            bool all = true;
-            for (int e = 0; e < 8; ++e) all &= isnan(__uint_as_float(o[e]));
-            return all;
-        };
-        for (int i = 0; i < w.n && key >= 0 && !all_nan(); ++i) {
-            const int qb = w.first + i / p.G, bit = i % (32 * kTakenWords);
-            if (!((taken[bit / 32] >> (bit % 32)) & 1u)) continue;
+        for (int i = 0; i < w.n && key >= 0 && !all_nan(o); ++i) {
+            const int qb = w.first + i / p.G;
+            if (qb >= w.f0 && qb < w.f1) continue;
             for (int r = qb * kTile; r < min((qb + 1) * kTile, w.s.queries()); ++r) {
                 if (!sees(p, r + w.s.keys() - w.s.queries(), key)) continue;
                 float f[8];
@@ -754,6 +747,7 @@ __device__ __noinline__ void k_add_taken(const AttnParams &p, const KWork &w, co
                     if (!isfinite(f[e])) o[e] = is_q ? kNan : __float_as_uint(__uint_as_float(o[e]) + f[e]);
             }
         }
+        if (!is_q) whole.add_to(o, c);
         __syncwarp();
         detg::tmem_st8(out + c, o);
         tmem_wait_st();
@@ -831,13 +825,12 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
                     for (int k = 0; k < 32; ++k)
                         if (!(seen[x] & (1u << k))) s[x][k] = 0u;
                 }
-            if (again) {
-                // When both score matrices have been made the queries' rows may be changed for the last two products.
+            if (again && (half || !full)) {
+                // When both score matrices have been made the queries' rows may be changed for the last two products: those of
+                // dout everywhere, of q where the block is seen in part.
                 if (!wait.warp(smem_u32(&S.dp), j & 1)) return;
-                if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, w.s.queries() - qb * kTile)) {
-                    const int bit = i % (32 * kTakenWords);
-                    atomicOr(&S.taken[bit / 32], 1u << (bit % 32));
-                }
+                if (make_finite<DH>(base + (half ? C::OFF_D : C::OFF_Q) + st * C::TILE, row, w.s.queries() - qb * kTile, full ? &S.whole : nullptr, nullptr))
+                    S.taken = 1;
                 __syncwarp();
             }
             put16(tm + half * 64, s[0]);
@@ -893,7 +886,7 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
         }
         if (!wait.warp(smem_u32(&S.done), again)) return;
         tc_fence_after();
-        if (again) k_add_taken(p, w, S.taken, half != 0, out, live ? key : -1);
+        if (again && *reinterpret_cast<volatile int *>(&S.taken)) k_add_taken(p, w, S.whole, half != 0, out, live ? key : -1);
         bool bad = false;
 #pragma unroll 1
         for (int x = 0; x < DH / 32; ++x) {
@@ -940,8 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.again = 0;
-        for (int i = 0; i < kTakenWords; ++i) S.taken[i] = 0;
+        S.again = S.taken = 0;
+        S.whole = NotFinite{};
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&S.q_full[i]), 1);
             mbar_init(smem_u32(&S.q_empty[i]), 1);

@@ -34,7 +34,9 @@
 // second time, with what is not finite taken out of all values before the
 // product and added to the rows that see it afterwards: as it is, since weights
 // are positive, those too that are zero in FP32 (times infinity they would be NaN
-// in blocks that are seen whole, which depends on where tiles begin).
+// in blocks that are seen whole, which depends on where tiles begin). For such
+// blocks columns are noted, the others' keys looked at again: 8192 tokens whose
+// values are all infinite would take 115 ms if every row looked at every key.
 #include "attn_tile.cuh"
 
 #include <atomic>
@@ -54,7 +56,7 @@ struct Cfg {
     static constexpr int SLOTS = DH == 128 ? 5 : 8;  // ring of key and value tiles
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_SHARED = OFF_RING + SLOTS * TILE;
-    static constexpr int SMEM = OFF_SHARED + 512 + 1024;
+    static constexpr int SMEM = OFF_SHARED + 640 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -68,20 +70,22 @@ struct Work {
     Places at[2];
     // What is done for the tiles `act` (a bit each): all that see something, or those that have to be done again.
     __device__ bool used(int i, unsigned act) const { return ((act & 1u) && at[0].sees(i)) || ((act & 2u) && at[1].sees(i)); }
+    // All rows of such a tile see all of the block's keys.
+    __device__ bool whole(int i, int t, unsigned act) const { return ((act >> t) & 1u) && at[t].sees(i) && at[t].whole(i); }
     __device__ unsigned seeing() const { return (at[0].last() >= 0 ? 1u : 0u) | (at[1].last() >= 0 ? 2u : 0u); }
 };
 
-constexpr int kTakenWords = 16;
 struct Shared {
     uint64_t q_full[2], full[8], empty[8], scores[2], probs[2][2], sane[2], done[2], verdict[2], drain, never;
     uint32_t tmem;
     int abort_flag;
     int again[2];                    // the tile has to be done again
-    uint32_t taken[kTakenWords];     // some value has been taken out of the block (a bit each, in turn)
+    int taken;                       // some value has been taken out
+    NotFinite whole[2];              // what was, of the blocks that all of a tile's rows see
     int some;                        // there is something to do
     Work work;
 };
-static_assert(sizeof(Shared) <= 512, "shared state");
+static_assert(sizeof(Shared) <= 640, "shared state");
 
 __device__ __forceinline__ bool find_work(const AttnParams &p, int unit, int slots, Work &w)
 {
@@ -250,22 +254,17 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
     }
 }
 
-// Adds the values that make_finite took out to the rows that see them.
-__device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, const uint32_t *taken, int t, uint32_t out, int position)
+// Adds the values that make_finite took out to the rows that see them: those of blocks that are seen in part key by key.
+__device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, const NotFinite &whole, int t, uint32_t out, int position)
 {
     for (int c = 0; c < p.D; c += 8) {
         uint32_t o[8];
         detg::tmem_ld8(out + c, o);
         tmem_wait_ld();
         detg::reg_fence8(o);
-        auto all_nan = [&] {         // (nothing changes them any more)
-            bool all = true;
-            for (int e = 0; e < 8; ++e) all &= isnan(__uint_as_float(o[e]));
-            return all;
-        };
-        for (int i = 0; i < w.blocks.n && !all_nan(); ++i) {
-            const int b = w.blocks.at(i), x = i % (32 * kTakenWords);
-            if (!w.at[t].sees(i) || !((taken[x / 32] >> (x % 32)) & 1u)) continue;
+        for (int i = 0; i < w.blocks.n && !all_nan(o); ++i) {
+            const int b = w.blocks.at(i);
+            if (!w.at[t].sees(i) || w.at[t].whole(i)) continue;
             for (int j = b * kTile; j < (b + 1) * kTile && j <= position; ++j) {
                 if (!sees(p, position, j)) continue;
                 const uint4 v = *reinterpret_cast<const uint4 *>(p.v.row(w.s.k0 + j, w.kv) + c);
@@ -275,6 +274,7 @@ __device__ __noinline__ void add_taken(const AttnParams &p, const Work &w, const
                     if (!isfinite(f[e])) o[e] = __float_as_uint(__uint_as_float(o[e]) + f[e]);
             }
         }
+        whole.add_to(o, c);
         __syncwarp();
         detg::tmem_st8(out + c, o);
         tmem_wait_st();
@@ -316,10 +316,8 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
                 const int slot = v_tile % C::SLOTS;
                 if (!wait.warp(smem_u32(&S.full[slot]), (v_tile / C::SLOTS) & 1)) return false;
                 const int live = min(kTile, w.s.keys() - w.blocks.at(i) * kTile);
-                if (make_finite<DH>(base + C::OFF_RING + slot * C::TILE, both ? 2 * row + t : row, live)) {
-                    const int x = i % (32 * kTakenWords);
-                    atomicOr(&S.taken[x / 32], 1u << (x % 32));
-                }
+                if (make_finite<DH>(base + C::OFF_RING + slot * C::TILE, both ? 2 * row + t : row, live, w.whole(i, 0, act) ? &S.whole[0] : nullptr, w.whole(i, 1, act) ? &S.whole[1] : nullptr))
+                    S.taken = 1;
                 __syncwarp();
                 if (both && lane == 0) mbar_arrive(smem_u32(&S.sane[t]));
             }
@@ -436,7 +434,7 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
     for (int again = 0; some; ++again) {
         if (!pass(act, again != 0) || !wait.warp(smem_u32(&S.done[t]), again)) return;
         tc_fence_after();
-        if (again) add_taken(p, w, S.taken, t, to, row < rows ? position : -1);
+        if (again && *reinterpret_cast<volatile int *>(&S.taken)) add_taken(p, w, S.whole[t], t, to, row < rows ? position : -1);
 #pragma unroll
         for (int x = 0; x < DH / 32; ++x) tmem_ld32(to + 32 * x, o[x]);
         tmem_wait_ld();
@@ -497,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
-        S.again[0] = S.again[1] = 0;
-        for (int i = 0; i < kTakenWords; ++i) S.taken[i] = 0;
+        S.again[0] = S.again[1] = S.taken = 0;
+        S.whole[0] = S.whole[1] = NotFinite{};
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
             mbar_init(smem_u32(&S.empty[i]), 1);

@@ -37,6 +37,7 @@ using detg::tmem_wait_st;
 constexpr int kTile = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr unsigned kWarp = 0xFFFFFFFFu;
+constexpr uint32_t kNan = 0x7FFFFFFFu;
 
 // ---- waits
 
@@ -162,10 +163,37 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint32_t b
     for (int k = 0; k < K / 16; ++k) mma_ts(d, a_tmem + k * 8 + (k >= 4 ? gap : 0), db + k * (2048 / 16), idesc, accumulate || k != 0);
 }
 
+// Which columns of some rows hold +infinity, -infinity, NaN: a bit a column.
+struct NotFinite {
+    uint32_t bits[3][4];
+    // Adds them to the sums of columns [c, c + 8).
+    __device__ __forceinline__ void add_to(uint32_t (&o)[8], int c) const
+    {
+        const uint32_t plus = bits[0][c >> 5] >> (c & 31), minus = bits[1][c >> 5] >> (c & 31), nan = bits[2][c >> 5] >> (c & 31);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float x = __uint_as_float(o[e]);
+            if ((plus >> e) & 1u) x += INFINITY;
+            if ((minus >> e) & 1u) x -= INFINITY;
+            o[e] = (nan >> e) & 1u ? kNan : __float_as_uint(x);
+        }
+    }
+};
+
+// Sums that nothing changes any more.
+__device__ __forceinline__ bool all_nan(const uint32_t (&o)[8])
+{
+    bool all = true;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) all &= isnan(__uint_as_float(o[e]));
+    return all;
+}
+
 // Takes what is not finite out of row r of a tile (if the tile has one), and all of it if the sequence's rows end
-// before. True if something was not finite. The row's eight chunks of 16 bytes are taken in an order of its own, for the banks.
+// before. True if something was not finite; which columns, in shared memory, is noted in `a` and `b` (either may be null). The row's
+// eight chunks of 16 bytes are taken in an order of its own, for the banks.
 template <int DH>
-__device__ __noinline__ bool make_finite(uint32_t tile, int r, int live)
+__device__ __noinline__ bool make_finite(uint32_t tile, int r, int live, NotFinite *a, NotFinite *b)
 {
     if (r >= kTile) return false;
     bool found = false;
@@ -174,15 +202,25 @@ __device__ __noinline__ bool make_finite(uint32_t tile, int r, int live)
         const uint32_t at = tile + (c >> 3) * (kTile * 128) + r * 128 + ((c ^ r) & 7) * 16;
         uint32_t x[4], any = 0;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+        uint32_t kinds = 0;          // 8 bits each
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t lo = (x[i] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (x[i] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
             any |= lo | hi;
+            if (lo) kinds |= ((x[i] & 0x7Fu) ? 1u << 16 : (x[i] & 0x8000u) ? 1u << 8 : 1u) << (2 * i);
+            if (hi) kinds |= ((x[i] & 0x7F0000u) ? 1u << 16 : (x[i] >> 31) ? 1u << 8 : 1u) << (2 * i + 1);
             x[i] &= r < live ? ~(lo | hi) : 0u;
         }
         if (any != 0 || r >= live)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
-        found |= any != 0 && r < live;
+        if (any != 0 && r < live) {
+            found = true;
+            for (int k = 0; k < 3; ++k) {
+                const uint32_t bits = ((kinds >> (8 * k)) & 0xFFu) << (8 * (c & 3));
+                if (a && bits & ~*const_cast<volatile uint32_t *>(&a->bits[k][c >> 2])) atomicOr(&a->bits[k][c >> 2], bits);
+                if (b && bits & ~*const_cast<volatile uint32_t *>(&b->bits[k][c >> 2])) atomicOr(&b->bits[k][c >> 2], bits);
+            }
+        }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     return found;
