@@ -416,14 +416,14 @@ __device__ void q_math(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
         }
         if (!wait.warp(smem_u32(&S.done), again)) return;
         tc_fence_after();
-        if (again && *reinterpret_cast<volatile int *>(&S.taken)) q_add_taken(p, w, out, live ? position : -1, half * (DH / 2), (half + 1) * (DH / 2));
+        if (again && *reinterpret_cast<volatile int *>(&S.taken)) q_add_taken(p, w, out, live ? position : -1, half * (DH / 2), min((half + 1) * (DH / 2), written(p)));
 #pragma unroll
         for (int x = 0; x < DH / 64; ++x) tmem_ld32(out + half * (DH / 2) + 32 * x, o[x]);
         tmem_wait_ld();
 #pragma unroll
         for (int x = 0; x < DH / 64; ++x) reg_fence(o[x]);
         if (again) break;
-        if (__any_sync(kWarp, live && not_finite(o))) S.again = 1;
+        if (__any_sync(kWarp, live && not_finite(o, written(p) - half * (DH / 2)))) S.again = 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&S.verdict));
@@ -894,7 +894,7 @@ __device__ void k_math(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
             tmem_ld32(out + 32 * x, o[0]);
             tmem_wait_ld();
             reg_fence(o[0]);
-            bad |= not_finite(o);
+            bad |= not_finite(o, written(p) - 32 * x);
             if (again) put(x, o[0]);
         }
         if (again) break;

@@ -441,7 +441,7 @@ __device__ void softmax_role(const AttnParams &p, const AttnMaps &maps, Shared &
 #pragma unroll
         for (int x = 0; x < DH / 32; ++x) reg_fence(o[x]);
         if (again) break;
-        if (__any_sync(kWarp, row < rows && not_finite(o))) S.again[t] = 1;
+        if (__any_sync(kWarp, row < rows && not_finite(o, written(p)))) S.again[t] = 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&S.verdict[t]));

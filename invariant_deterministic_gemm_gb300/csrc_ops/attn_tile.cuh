@@ -338,22 +338,26 @@ __device__ __forceinline__ Places places_of(const AttnParams &p, Positions q, co
     return r;
 }
 
-// Whether some of the numbers is not finite (their products with zero add up to zero otherwise).
+// Whether some of the first n numbers (a multiple of 16) is not finite: their products with zero add up to zero otherwise. (Columns
+// that the products do not write, past D rounded up to 16, hold what another launch left in TMEM.)
 template <int N>
-__device__ __forceinline__ bool not_finite(const uint32_t (&o)[N][32])
+__device__ __forceinline__ bool not_finite(const uint32_t (&o)[N][32], int n)
 {
     uint64_t z0 = 0, z1 = 0;
 #pragma unroll
-    for (int x = 0; x < N; ++x)
+    for (int x = 0; x < 2 * N; ++x)
+        if (16 * x < n)
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            z0 = fma2(pair(__uint_as_float(o[x][j]), __uint_as_float(o[x][j + 1])), 0, z0);
-            z1 = fma2(pair(__uint_as_float(o[x][j + 2]), __uint_as_float(o[x][j + 3])), 0, z1);
-        }
+            for (int j = 16 * (x & 1); j < 16 * (x & 1) + 16; j += 4) {
+                z0 = fma2(pair(__uint_as_float(o[x >> 1][j]), __uint_as_float(o[x >> 1][j + 1])), 0, z0);
+                z1 = fma2(pair(__uint_as_float(o[x >> 1][j + 2]), __uint_as_float(o[x >> 1][j + 3])), 0, z1);
+            }
     float lo, hi;
     unpair(add2(z0, z1), lo, hi);
     return !(lo + hi == 0.0f);
 }
+// Columns that the second products write.
+__device__ __forceinline__ int written(const AttnParams &p) { return (p.D + 15) & ~15; }
 
 // ---- tiles of packed rows
 //
