@@ -136,6 +136,7 @@ struct QShared {
     uint64_t q_full, o_full, o_read, full[8], empty[8], scores[2], dp, read, ds[2], done, verdict, staged, drain, never;
     uint32_t tmem;
     int abort_flag, taken, again, some;
+    InFlight copies;                 // barriers from q_full on
     QWork work;
 };
 static_assert(sizeof(QShared) <= 512, "shared state");
@@ -179,8 +180,10 @@ __device__ void q_copy(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
     mbar_arrive_expect_tx(smem_u32(&S.q_full), C::TILE);
     load_tile<DH>(base, &maps.q, smem_u32(&S.q_full), w.head, w.row0);
     int slot = 0;
-    uint32_t round = 0, loaded = 0, parity = 0;
+    uint32_t round = 0;
     bool ok = true;
+    InFlight copies{3, 0};           // (q_full, o_full)
+    constexpr int RING = offsetof(QShared, full) / 8 - offsetof(QShared, q_full) / 8;
     for (int again = 0; ok && again < 2; ++again) {
         if (again && !done_again(S, wait)) break;
         for (int i = 0; i < 2 * w.blocks.n; ++i) {
@@ -189,20 +192,14 @@ __device__ void q_copy(const AttnParams &p, const AttnMaps &maps, QShared &S, ui
             const uint32_t bar = smem_u32(&S.full[slot]);
             mbar_arrive_expect_tx(bar, C::TILE);
             load_tile<DH>(base + C::OFF_RING + slot * C::TILE, (i & 1) ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i >> 1) * kTile);
-            loaded |= 1u << slot;
-            parity = (parity & ~(1u << slot)) | (round << slot);
+            copies.add(RING + slot, round);
             if (++slot == C::SLOTS) {
                 slot = 0;
                 round ^= 1u;
             }
         }
     }
-    if (!ok || *wait.abort_flag) {
-        wait.drain(smem_u32(&S.o_full), 0);
-        wait.drain(smem_u32(&S.q_full), 0);
-        for (int i = 0; i < C::SLOTS; ++i)
-            if (loaded & (1u << i)) wait.drain(smem_u32(&S.full[i]), (parity >> i) & 1u);
-    }
+    S.copies = copies;
 }
 
 // TMEM: scores of even and odd blocks, dout v^T, dq. dS takes the scores' place, so the next dout v^T can be made as soon as
@@ -214,7 +211,7 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
     const QWork w = S.work;
     const uint32_t ring = base + C::OFF_RING, tm = S.tmem;
     const int steps = (p.D + 15) / 16, n = w.blocks.n;
-    bool ok = n == 0 || (wait.one(smem_u32(&S.q_full), 0) && wait.one(smem_u32(&S.o_full), 0)), issued = false;
+    bool ok = n == 0 || (wait.one(smem_u32(&S.q_full), 0) && wait.one(smem_u32(&S.o_full), 0));
     // Block i of all passes: its keys are tile 2 i of the ring, its values the next.
     auto arrived = [&](int seq) {
         ok = ok && wait.one(smem_u32(&S.full[seq % C::SLOTS]), (seq / C::SLOTS) & 1);
@@ -225,7 +222,6 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
         tc_fence_after();
         mma_scores<DH>(tm + (i & 1) * kTile, base, ring + 2 * i % C::SLOTS * C::TILE, steps);
         mma_commit(smem_u32(&S.scores[i & 1]));
-        issued = true;
     };
     auto dp = [&](int i) {
         if (!arrived(2 * i + 1)) return;
@@ -233,7 +229,6 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
         mma_scores<DH>(tm + 2 * kTile, base + C::TILE, ring + (2 * i + 1) % C::SLOTS * C::TILE, steps);
         mma_commit(smem_u32(&S.dp));
         mma_commit(smem_u32(&S.empty[(2 * i + 1) % C::SLOTS]));
-        issued = true;
     };
     for (int begin = 0; ok && n > 0 && begin < 2 * n; begin += n) {
         if (begin && !done_again(S, wait)) break;
@@ -255,10 +250,6 @@ __device__ void q_issue(const AttnParams &p, QShared &S, uint32_t base, const Wa
             if (i + 2 < end) scores(i + 2);
         }
         if (ok) mma_commit(smem_u32(&S.done));
-    }
-    if ((!ok || *wait.abort_flag) && issued) {
-        mma_commit(smem_u32(&S.drain));
-        wait.drain(smem_u32(&S.drain), 0);
     }
 }
 
@@ -458,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
+        S.copies = InFlight{0, 0};
         S.again = S.taken = 0;
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
@@ -517,6 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*wait.abort_flag) {
+        if (warp == 8 && elect_one()) drain_copies(&S.q_full, S.copies, wait);
+        if (warp == 9 && elect_one()) drain_products(smem_u32(&S.drain), wait);
+        __syncwarp();
+        __syncthreads();
+    }
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
 }
 
@@ -545,6 +543,7 @@ struct KShared {
     uint64_t kv_full, q_full[2], q_empty[2], d_full[2], d_empty[2], v_full[2], v_empty[2], scores, dp, probs, ds, done, verdict, drain, never;
     uint32_t tmem;
     int abort_flag, taken, again, some;
+    InFlight copies;                 // barriers from kv_full on
     NotFinite whole;                 // what was, of rows of dout that see all of the tile's keys
     KWork work;
 };
@@ -604,7 +603,8 @@ __device__ void k_copy(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
     mbar_arrive_expect_tx(smem_u32(&S.kv_full), 2 * C::TILE);
     load_tile<DH>(base, &maps.k, smem_u32(&S.kv_full), w.kv, w.s.k0 + w.key0);
     load_tile<DH>(base + C::TILE, &maps.v, smem_u32(&S.kv_full), w.kv, w.s.k0 + w.key0);
-    int q_last[2] = {-1, -1}, d_last[2] = {-1, -1};                  // parity of each stage's last load
+    InFlight copies{1, 0};           // (kv_full)
+    constexpr int Q = offsetof(KShared, q_full) / 8 - offsetof(KShared, kv_full) / 8, D = offsetof(KShared, d_full) / 8 - offsetof(KShared, kv_full) / 8;
     bool ok = true;
     for (int again = 0, j = 0; ok && again < 2; ++again) {
         if (again && !done_again(S, wait)) break;
@@ -615,25 +615,19 @@ __device__ void k_copy(const AttnParams &p, const AttnMaps &maps, KShared &S, ui
             if (!ok) break;
             mbar_arrive_expect_tx(smem_u32(&S.q_full[st]), C::TILE);
             load_tile<DH>(base + C::OFF_Q + st * C::TILE, &maps.q, smem_u32(&S.q_full[st]), head, row);
-            q_last[st] = phase;
+            copies.add(Q + st, phase);
             ok = wait.one(smem_u32(&S.d_empty[st]), phase ^ 1);
             if (!ok) break;
             mbar_arrive_expect_tx(smem_u32(&S.d_full[st]), C::TILE);
             load_tile<DH>(base + C::OFF_D + st * C::TILE, &maps.dout, smem_u32(&S.d_full[st]), head, row);
-            d_last[st] = phase;
+            copies.add(D + st, phase);
             if (++h == p.G) {
                 h = 0;
                 row += kTile;
             }
         }
     }
-    if (!ok || *wait.abort_flag) {
-        wait.drain(smem_u32(&S.kv_full), 0);
-        for (int st = 0; st < 2; ++st) {
-            if (q_last[st] >= 0) wait.drain(smem_u32(&S.q_full[st]), q_last[st]);
-            if (d_last[st] >= 0) wait.drain(smem_u32(&S.d_full[st]), d_last[st]);
-        }
-    }
+    S.copies = copies;
 }
 
 // One warp: -lse log2(e) and -delta of each iteration's queries. A row that saw nothing gets -infinity: P is zero.
@@ -682,14 +676,13 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
     const KWork w = S.work;
     const uint32_t tm = S.tmem;
     const int steps = (p.D + 15) / 16;
-    bool ok = w.n == 0 || wait.one(smem_u32(&S.kv_full), 0), issued = false;
+    bool ok = w.n == 0 || wait.one(smem_u32(&S.kv_full), 0);
     auto scores = [&](int i) {
         ok = ok && wait.one(smem_u32(&S.q_full[i & 1]), (i >> 1) & 1);
         if (!ok) return;
         tc_fence_after();
         mma_scores<DH>(tm, base, base + C::OFF_Q + (i & 1) * C::TILE, steps);
         mma_commit(smem_u32(&S.scores));
-        issued = true;
     };
     auto dp = [&](int i) {
         ok = ok && wait.one(smem_u32(&S.d_full[i & 1]), (i >> 1) & 1);
@@ -697,7 +690,6 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
         tc_fence_after();
         mma_scores<DH>(tm + kTile, base + C::TILE, base + C::OFF_D + (i & 1) * C::TILE, steps);
         mma_commit(smem_u32(&S.dp));
-        issued = true;
     };
     for (int begin = 0; ok && w.n > 0 && begin < 2 * w.n; begin += w.n) {
         if (begin && !done_again(S, wait)) break;
@@ -719,10 +711,6 @@ __device__ void k_issue(const AttnParams &p, KShared &S, uint32_t base, const Wa
             if (i + 1 < end) dp(i + 1);
         }
         if (ok) mma_commit(smem_u32(&S.done));
-    }
-    if ((!ok || *wait.abort_flag) && issued) {
-        mma_commit(smem_u32(&S.drain));
-        wait.drain(smem_u32(&S.drain), 0);
     }
 }
 
@@ -933,6 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
+        S.copies = InFlight{0, 0};
         S.again = S.taken = 0;
         S.whole = NotFinite{};
         for (int i = 0; i < 2; ++i) {
@@ -993,6 +982,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*wait.abort_flag) {
+        if (warp == 8 && elect_one()) drain_copies(&S.kv_full, S.copies, wait);
+        if (warp == 9 && elect_one()) drain_products(smem_u32(&S.drain), wait);
+        __syncwarp();
+        __syncthreads();
+    }
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
 }
 

@@ -79,6 +79,7 @@ struct Shared {
     uint64_t q_full[2], full[8], empty[8], scores[2], probs[2][2], sane[2], done[2], verdict[2], drain, never;
     uint32_t tmem;
     int abort_flag;
+    InFlight copies;                 // barriers from q_full[0] on
     int again[2];                    // the tile has to be done again
     int taken;                       // some value has been taken out
     NotFinite whole[2];              // what was, of the blocks that all of a tile's rows see
@@ -134,7 +135,7 @@ __device__ void copy_role(const AttnParams &p, const AttnMaps &maps, Shared &S, 
     int slot = 0;
     uint32_t round = 0;
     bool ok = true;
-    uint32_t loaded = 0, parity = 0;
+    InFlight copies{all, 0};
     auto pass = [&](unsigned act) {
         for (int i = 0; ok && i < w.blocks.n; ++i) {
             if (!w.used(i, act)) continue;
@@ -144,8 +145,7 @@ __device__ void copy_role(const AttnParams &p, const AttnMaps &maps, Shared &S, 
                 const uint32_t bar = smem_u32(&S.full[slot]);
                 mbar_arrive_expect_tx(bar, C::TILE);
                 load_tile<DH>(base + C::OFF_RING + slot * C::TILE, kind ? &maps.v : &maps.k, bar, w.kv, w.s.k0 + w.blocks.at(i) * kTile);
-                loaded |= 1u << slot;
-                parity = (parity & ~(1u << slot)) | (round << slot);
+                copies.add(2 + slot, round);
                 if (++slot == C::SLOTS) {
                     slot = 0;
                     round ^= 1u;
@@ -154,13 +154,7 @@ __device__ void copy_role(const AttnParams &p, const AttnMaps &maps, Shared &S, 
         }
     };
     for (int again = 0; again < 2 && ok; ++again) pass(again ? done_again(S, wait) : all);
-    // Nothing may land after the CTA's end; when all went well the last blocks' products have waited for them.
-    if (!ok || *wait.abort_flag) {
-        for (int t = 0; t < 2; ++t)
-            if ((all >> t) & 1u) wait.drain(smem_u32(&S.q_full[t]), 0);
-        for (int i = 0; i < C::SLOTS; ++i)
-            if (loaded & (1u << i)) wait.drain(smem_u32(&S.full[i]), (parity >> i) & 1u);
-    }
+    S.copies = copies;
 }
 
 template <int DH>
@@ -172,7 +166,7 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
     const int steps = (p.D + 15) / 16, n = steps * 16;
     int slot = 0;                    // of the next tile in the ring
     uint32_t round = 0, probs = 0, sane = 0;     // phases (a bit a tile)
-    bool ok = true, issued = false;
+    bool ok = true;
     auto arrive_tile = [&](uint32_t &at) {       // waits for the next tile of the ring
         at = slot;
         ok = ok && wait.one(smem_u32(&S.full[slot]), round);
@@ -192,7 +186,6 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
         tc_fence_after();
         mma_scores<DH>(tm + t * kTile, base + t * C::TILE, ring + k * C::TILE, steps);
         mma_commit(smem_u32(&S.scores[t]));
-        issued = true;
     };
     auto pass = [&](unsigned act, bool safe) {
         const bool on[2] = {(act & 1u) != 0, (act & 2u) != 0};
@@ -228,7 +221,7 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
                     if (!ok) return;
                     tc_fence_after();
                     mma_rows<64>(tm + 2 * kTile + t * kTile, tm + t * kTile, ring + v * C::TILE, n, out[t]);
-                    out[t] = issued = true;
+                    out[t] = true;
                     ok = wait.one(smem_u32(&S.probs[t][1]), phase);
                     if (!ok) return;
                     tc_fence_after();
@@ -248,10 +241,6 @@ __device__ void issue_role(const AttnParams &p, Shared &S, uint32_t base, const 
         }
     };
     for (int again = 0; again < 2 && ok; ++again) pass(again ? done_again(S, wait) : w.seeing(), again != 0);
-    if ((!ok || *wait.abort_flag) && issued) {
-        mma_commit(smem_u32(&S.drain));
-        wait.drain(smem_u32(&S.drain), 0);
-    }
 }
 
 // Adds the values that make_finite took out to the rows that see them: those of blocks that are seen in part key by key.
@@ -495,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         S.abort_flag = 0;
+        S.copies = InFlight{0, 0};
         S.again[0] = S.again[1] = S.taken = 0;
         S.whole[0] = S.whole[1] = NotFinite{};
         for (int i = 0; i < C::SLOTS; ++i) {
@@ -548,6 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*wait.abort_flag) {
+        if (warp == 8 && elect_one()) drain_copies(S.q_full, S.copies, wait);
+        if (warp == 9 && elect_one()) drain_products(smem_u32(&S.drain), wait);
+        __syncwarp();
+        __syncthreads();
+    }
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(512) : "memory");
 }
 

@@ -50,6 +50,29 @@ struct Waits {
     __device__ bool warp(uint32_t bar, uint32_t parity) const { return __all_sync(kWarp, one(bar, parity)); }
 };
 
+// Copies that a role has started: the barriers (a bit each, counted from one of them) of its last ones, and their phases' parities.
+struct InFlight {
+    uint32_t begun, parity;
+    __device__ void add(int i, uint32_t p)
+    {
+        begun |= 1u << i;
+        parity = (parity & ~(1u << i)) | p << i;
+    }
+};
+// The end of a CTA in which a role has given up, once all roles are over: nothing may land, and no product may be under way, when its
+// shared memory and TMEM go back. Whichever role gave up, and when; so not by the roles, which may have ended before.
+static __device__ __noinline__ void drain_copies(const uint64_t *barriers, InFlight f, Waits wait)
+{
+    for (int i = 0; i < 32; ++i)
+        if ((f.begun >> i) & 1u) wait.drain(smem_u32(barriers + i), (f.parity >> i) & 1u);
+}
+// (By the thread that issued the products; a warp's elected thread is always the same.)
+__device__ __forceinline__ void drain_products(uint32_t bar, const Waits &wait)
+{
+    mma_commit(bar);
+    wait.drain(bar, 0);
+}
+
 // Whether one of the `threads` of named barrier `id` says so; they wait for one another, and none leaves but where all do.
 __device__ __forceinline__ bool any_at(int id, int threads, bool v)
 {
