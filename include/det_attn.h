@@ -30,7 +30,7 @@
  * i + n - m (its last query at its last key) and sees the keys j at or
  * before it with position - j < window or j < sinks. window 0: no window.
  * A query that sees no key gives zeros (and lse -inf). Scores are scale q.k;
- * scale is positive and finite. What masked keys and values hold, infinities
+ * scale is positive and at most 2^127. What masked keys and values hold, infinities
  * and NaN included, does not reach the output. In det_attn a visible value that
  * is not finite is added as it is, however small its weight, and in det_attn_bwd
  * so is such a row of dout.

@@ -125,7 +125,11 @@ bool ok_heads(int64_t H, int64_t KV, int64_t D)
 {
     return KV >= 1 && H >= KV && H <= DET_ATTN_MAX_HEADS && H % KV == 0 && D >= 8 && D <= DET_ATTN_MAX_HEAD_DIM && D % 8 == 0;
 }
-bool ok_mask(float scale, int64_t window, int64_t sinks) { return scale > 0.0f && std::isfinite(scale) && window >= 0 && sinks >= 0; }
+// (The kernels' scores are in units of log2: scale times log2(e), which has to be a number too.)
+bool ok_mask(float scale, int64_t window, int64_t sinks)
+{
+    return scale > 0.0f && std::isfinite(scale * 1.4426950408889634f) && window >= 0 && sinks >= 0;
+}
 int window_of(int64_t w) { return w == 0 || w > kMaxRows ? kNoWindow : static_cast<int>(w); }
 int sinks_of(int64_t s) { return static_cast<int>(std::min(s, kMaxRows)); }
 
