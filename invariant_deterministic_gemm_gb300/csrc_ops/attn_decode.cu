@@ -602,9 +602,8 @@ __device__ void softmax_role(const DecodeParams &p, Shared &S, uint32_t base, co
 #pragma unroll
                     for (int h = 0; h < HE; h += 4) *reinterpret_cast<float4 *>(shared_top + warp * 32 + h) = make_float4(top[h], top[h + 1], top[h + 2], top[h + 3]);
                 }
-                // The values of the chunk two before have been weighted, and make room for P; the chunk kSums before has been
-                // joined, for the sums.
-                if (kSums > 2 && n >= 2) ok = ok && wait.warp(smem_u32(&S.sums[(n - 2) % kSums]), ((n - 2) / kSums) & 1);
+                // The chunk two before has been joined: its values have been weighted and make room for P, and its sums for new ones.
+                static_assert(kSums == 2, "P and sums are of the same chunks");
                 ok = ok && wait.warp(smem_u32(&S.joined[n % kSums]), ((n / kSums) & 1) ^ 1);
                 // Values of hidden tokens are whatever was there: zeros, for the product. What was in these values' slots
                 // before has been used, so that their barriers are in the phase before: it was a chunk's two before or older,

@@ -132,18 +132,6 @@ __device__ __forceinline__ Seq seq_at(const AttnParams &p, int n)
     return s;
 }
 
-// The last sequence whose first row (query, or key with of_keys) is at or before row t; its bounds need not hold t.
-__device__ __forceinline__ int seq_of(const int32_t *bounds, int N, int t)
-{
-    int a = 0, b = N;
-    while (b - a > 1) {
-        const int mid = (a + b) >> 1;
-        if (bounds[mid] <= t) a = mid;
-        else b = mid;
-    }
-    return a;
-}
-
 __device__ __forceinline__ bool sees(const AttnParams &p, int position, int j)
 {
     return j <= position && (position - j < p.window || j < p.sinks);

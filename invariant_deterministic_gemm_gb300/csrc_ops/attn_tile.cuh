@@ -311,19 +311,6 @@ __device__ __forceinline__ Blocks blocks_of(const AttnParams &p, Positions q)
     b.n = b.ns + q.hi / kTile - b.w0 + 1;
     return b;
 }
-// Some of the queries sees some key of block b.
-__device__ __forceinline__ bool sees_any(const AttnParams &p, Positions q, int b)
-{
-    const int a = b * kTile;
-    return a <= q.hi && (max(q.lo, 0) - (a + kTile - 1) < p.window || a < p.sinks);
-}
-// Every one of them sees every key of it.
-__device__ __forceinline__ bool sees_all(const AttnParams &p, Positions q, int b)
-{
-    const int a = b * kTile;
-    return a + kTile - 1 <= q.lo && (q.hi - a < p.window || a + kTile - 1 < p.sinks);
-}
-
 // The first key of a position's window, counted from key a (or below all of them).
 __device__ __forceinline__ int first_seen(const AttnParams &p, int position, int a)
 {
