@@ -19,7 +19,7 @@
  * output enqueues nothing; nothing is allocated, and a workspace is device
  * memory of the size that the function of its name gives, 256-byte aligned,
  * used until the enqueued work is done. Outputs must not overlap inputs or
- * each other (DET_GEMM_ERR_INVALID_ARG). What only the device can see (a
+ * each other, by their first and last bytes (DET_GEMM_ERR_INVALID_ARG). What only the device can see (a
  * position outside the tables, a slot or page outside the cache, a length
  * that the page table does not hold, bounds that go down or leave the
  * array) is made harmless there, set in a status word and reported by
