@@ -7,7 +7,9 @@
  * Like the library's products these are deterministic and batch-invariant:
  * a token's output is a function of its own sequence alone, whatever else
  * is in the batch and however a prompt is cut in chunks; every sum has a
- * fixed order and nothing is added with atomics.
+ * fixed order and nothing is added with atomics. That holds for each operator
+ * by itself: det_attn and det_attn_decode sum the same keys in orders of their
+ * own, and the same token has other bits from one than from the other.
  *
  * Conventions: an array of heads is [tokens, heads, D] BF16 with unit stride
  * in D and a stride (in elements) for each other axis, so that views of one
@@ -29,11 +31,18 @@
  * Visible keys: query i of a sequence of n keys and m queries is at position
  * i + n - m (its last query at its last key) and sees the keys j at or
  * before it with position - j < window or j < sinks. window 0: no window.
- * A query that sees no key gives zeros (and lse -inf). Scores are scale q.k;
+ * A query that sees no key, or none whose score is above -infinity, gives
+ * zeros (and lse -inf). Scores are scale q.k;
  * scale is positive and at most 2^127. What masked keys and values hold, infinities
  * and NaN included, does not reach the output. In det_attn a visible value that
  * is not finite is added as it is, however small its weight, and in det_attn_bwd
- * so is such a row of dout.
+ * so is such a row of dout; det_attn_decode multiplies it with its weight in FP32
+ * (NaN where that is zero).
+ *
+ * Precision: sums, maxima, exponentials and lse are FP32. The weights P are
+ * rounded to BF16 for their product with the values, and results once. The
+ * sum that det_attn divides by is that of P before this rounding,
+ * det_attn_decode's that of the rounded ones.
  */
 #ifndef DET_ATTN_H
 #define DET_ATTN_H
@@ -118,8 +127,8 @@ det_gemm_status det_attn(const det_gemm_bf16 *q, const det_gemm_bf16 *k, const d
  * the query heads that share a KV head. out and lse may be those of more keys
  * than these (results over several ranges of keys, joined). A query that sees
  * a single key, and whose lse is that key's score, has dS = 0 and not the
- * rounding of its two terms. P and dS are rounded to BF16 for
- * their second products. Rows outside every sequence become zero.
+ * rounding of its two terms. P and dS are rounded to BF16 for their second
+ * products. Rows outside every sequence become zero.
  */
 int64_t det_attn_bwd_workspace(int64_t N, int64_t T, int64_t S, int64_t H, int64_t KV, int64_t D, int64_t window,
                                int64_t sinks);

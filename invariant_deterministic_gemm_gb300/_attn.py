@@ -40,7 +40,8 @@ def det_attn_decode(q, k_cache, v_cache, table, lengths, *, scale=None, window=N
     lengths[b] tokens of the pages table[b] (int32 [B, max_pages]), the new
     token's own key among them. With a window only the last `window` keys and
     the first `sinks` are seen. scale: 1 / sqrt(D) unless given. A sequence of
-    length 0 gives zeros."""
+    length 0 gives zeros. The same in any batch; det_attn's row of the same
+    token differs by roundings."""
     return _on(stream, _ops._native.attn_decode, q, k_cache, v_cache, table, lengths, scale, window, sinks, out)
 
 
@@ -55,7 +56,9 @@ def det_attn(q, k, v, bounds=None, k_bounds=None, *, scale=None, window=None, si
 
 
 def det_attn_bwd(dout, q, k, v, out, lse, bounds=None, k_bounds=None, *, scale=None, window=None, sinks=0, stream=None):
-    """Gradients dq, dk, dv of det_attn, from its inputs and results."""
+    """Gradients dq, dk, dv of det_attn, from its inputs and results. out and lse
+    may be those of more keys than k and v (results over several ranges of
+    keys, joined): the gradients are then this range's part."""
     return _on(stream, _ops._native.attn_bwd, dout, q, k, v, out, lse, bounds, k_bounds, scale, window, sinks)
 
 

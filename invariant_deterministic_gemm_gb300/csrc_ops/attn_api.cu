@@ -185,7 +185,7 @@ DecodeSpace decode_space(int64_t B, int64_t H, int64_t KV, int64_t D, int64_t to
 }
 
 // A cache as (column, head, token of a page, page), copied in boxes of 64 columns of one head and `box` tokens of a page. Where
-// a head's row is 128 bytes, no more than that is fetched (256, with the next head's: 69.8 instead of 67.7 us for 96 windows of
+// a head's row is 128 bytes, no more than that is fetched (256, with the next head's: 69.8 instead of 67.7 us, then, for 96 windows of
 // 1024 in eight heads of 64; rows of 256 bytes by 128: 222 instead of 218 us for 64 contexts up to 8192).
 bool encode(CUtensorMap *m, const void *p, int64_t pages, int64_t size, int64_t KV, int64_t D, int64_t page, int64_t s, int64_t h, int box)
 {

@@ -15,11 +15,15 @@
 // With a window, the first keys that stay visible are seen by all queries: they are taken in pieces of 512 queries, which a
 // third launch adds up (one CTA would walk every query: 50 us of 85 for three sequences of about 700 with a window of 257).
 //
-// Bound by the products and the chain between them: a block of dq takes about 1725
-// cycles (products 1536), of dk and dv 2200 to 2600 (2048); of a packed training
-// pass of 638 us dq is 244, dk and dv 217. Scores of 64 columns at a time, with
-// both operands from shared memory, are bound by its 128 bytes a cycle; waits for
-// each product's end cost dk and dv 257 us.
+// A block of dq takes 1725 to 2100 cycles (products 1536), of dk and dv 2200 to 2600
+// (2048); of a packed training pass of 638 us dq is 244, dk and dv 217. dk and dv are
+// bound by their blocks. Of dq they are a little more than half: 2080 CTAs of ten
+// blocks each are 13.7 rounds of 152, and each begins (barriers, TMEM, copies of q,
+// dout and out, delta, the first products) and ends (dq out of TMEM, its rows
+// stored) with nothing of the next one under way, since a CTA holds all of TMEM:
+// 7 us a round (a launch of one block a CTA takes 8.1), some 97 us. Scores of 64
+// columns at a time, with both operands from shared memory, are bound by its 128
+// bytes a cycle; waits for each product's end cost dk and dv 257 us.
 //
 // In both, a row is a TMEM lane; two warpgroups take half of a block's columns
 // each. P and dS go back to TMEM in the place of the scores they came from,

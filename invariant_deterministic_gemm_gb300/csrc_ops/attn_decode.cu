@@ -27,8 +27,12 @@
 //   warp 15          looks up the pages, some chunks ahead; sequences without tokens
 // 64 contexts up to 8192 (32 heads of 128 on 8) 211 us, 6.3 TB/s; two of 262,144
 // 257 us; one of 1021 12.8 us, of which three trips to memory in a row (lengths, page
-// table, keys) are half; 96 windows of 1024 in eight heads of 64 67.7 us, where
-// three chunks in flight are what bounds.
+// table, keys) are half; 96 windows of 1024 in eight heads of 64 66.6 us, where
+// three chunks in flight are what bounds. With more than eight query heads to a KV head
+// the softmax warps bound: 16 heads on one take 262 us for the 64 contexts (128 heads
+// on 8), 32 heads 461 (256 on 8), where the bytes take 170. The instances for 17 to 32
+// spill 730 to 870 bytes a thread: the softmax warps hold two tiles' scores and the
+// maxima of 32 heads in 128 registers, as the joining warps need 208.
 //
 // A chunk's way through one warpgroup is latency (barriers, TMEM, the maximum
 // over 256 tokens), about as long as its bytes take, so two take turns. P is
