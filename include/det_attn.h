@@ -20,13 +20,14 @@
  * waiting; argument errors come back before anything is enqueued; an empty
  * output enqueues nothing; nothing is allocated, and a workspace is device
  * memory of the size that the function of its name gives, 256-byte aligned,
- * used until the enqueued work is done. Outputs must not overlap inputs or
- * each other, by their first and last bytes (DET_GEMM_ERR_INVALID_ARG). What only the device can see (a
- * position outside the tables, a slot or page outside the cache, a length
- * that the page table does not hold, bounds that go down or leave the
- * array) is made harmless there, set in a status word and reported by
- * det_ops_check(); a row that two sequences of such bounds hold gets the
- * results of either. Sizes are below 2^31 - 4096.
+ * used until the enqueued work is done, until when inputs (lengths, tables
+ * and bounds among them) stay as they are. Outputs must not overlap inputs or
+ * each other, by their first and last bytes (DET_GEMM_ERR_INVALID_ARG).
+ * What only the device can see (a position outside the tables, a slot or
+ * page outside the cache, a length that the page table does not hold,
+ * bounds that go down or leave the array) is made harmless there, set in a
+ * status word and reported by det_ops_check(); a row that two sequences of
+ * such bounds hold gets the results of either. Sizes are below 2^31 - 4096.
  *
  * Visible keys: query i of a sequence of n keys and m queries is at position
  * i + n - m (its last query at its last key) and sees the keys j at or
