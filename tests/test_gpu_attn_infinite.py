@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+import attn_ref as ref
 import invariant_deterministic_gemm_gb300 as dg
 from test_gpu_attn import bounds, make, randn
 
@@ -140,4 +141,30 @@ def test_gradients_of_a_sequence_between_others():
     got = gradients(q, k, v, dout, b)
     for x, y in zip(got, clean):
         assert torch.equal(x[:70], y[:70]) and torch.equal(x[270:], y[270:]) and torch.isnan(x[71:270]).all()
+    assert dg.det_gemm_check() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_of_minus_infinity_alone_give_zeros(D):
+    """In packed attention and in the decode, as if no key were seen; beside a finite score they weigh nothing."""
+    T, page = 200, 16
+    q, k, v = make(T, T, 4, 2, D, 4)
+    q[:, :, 3], k[:150, :, 3], k[150:, :, 3] = 1.0, -INF, 0.0
+    out, lse = dg.det_attn(q, k, v)
+    assert not out[:150].any() and (lse[:, :150] == -INF).all()
+    want, wl, tol, ltol = ref.attention(q[150:], k[150:], v[150:])
+    ref.assert_within(out[150:], want, tol, "out")
+    ref.assert_within(lse[:, 150:], wl, ltol, "lse")
+    pages = -(-T // page)
+    kc, vc = (torch.zeros((pages, page, 2, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc.view(-1, 2, D)[:T], vc.view(-1, 2, D)[:T] = k, v
+    table = torch.arange(pages, dtype=torch.int32).cuda()[None].expand(3, -1).contiguous()
+    n = torch.tensor([1, 150, T], dtype=torch.int32).cuda()
+    got = dg.det_attn_decode(q[[0, 149, T - 1]], kc, vc, table, n)
+    assert not got[:2].any()
+    ref.assert_within(got[2], want[-1], tol[-1], "decode")
+    # an infinite value of no weight: multiplied with it in the decode
+    vc[0, 0, 0, 5] = INF
+    got = dg.det_attn_decode(q[[T - 1] * 3], kc, vc, table, n)
+    assert torch.isnan(got[2, :2, 5]).all() and int((~torch.isfinite(got[2])).sum()) == 2
     assert dg.det_gemm_check() == 0
